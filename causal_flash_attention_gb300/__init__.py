@@ -29,6 +29,8 @@ __all__ = [
     "DTYPE_CODES", "fa_bwd_noalloc", "NOALLOC_SCRATCH_BYTES", "fa_fwd_kv", "fa_bwd_kv",
     "fa_bwd_kv_workspace_bytes", "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_bytes",
     "decode_forward", "fa_fwd_splitkv_paged", "decode_forward_paged",
+    "fa_fwd_span", "fa_bwd_span", "fa_bwd_span_workspace_bytes", "attention_span_forward",
+    "attention_span_backward", "key_spans",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa.so")
@@ -70,6 +72,12 @@ def lib() -> ctypes.CDLL:
     L.fa_fwd_splitkv_workspace_bytes.restype = sz
     L.fa_fwd_splitkv_paged.argtypes = [vp] * 6 + [i32] * 10 + [f32, i32, i32, vp, sz, vp]
     L.fa_fwd_splitkv_paged.restype = i32
+    L.fa_fwd_span.argtypes = [vp] * 7 + [i32] * 6 + [f32, f32, vp, i32, vp]
+    L.fa_fwd_span.restype = i32
+    L.fa_bwd_span_workspace_bytes.argtypes = [i32] * 6
+    L.fa_bwd_span_workspace_bytes.restype = sz
+    L.fa_bwd_span.argtypes = [vp] * 11 + [i32] * 6 + [f32, f32, vp, i32, vp, sz, vp]
+    L.fa_bwd_span.restype = i32
     L.fa_strerror.argtypes = [i32]
     L.fa_strerror.restype = ctypes.c_char_p
     L.fa_last_device_status.argtypes = [vp, ctypes.POINTER(i32)]
@@ -316,6 +324,180 @@ def attention_backward(q, k, v, out, dout, lse, causal=True, scale=None, workspa
     else:
         fa_bwd_kv(q, k, v, out, dout, lse, dq, dk, dv, workspace, causal, scale, stream)
     return dq, dk, dv
+
+
+# ------------------------------------------------------------- key spans --
+def _check_like(ref, dtype, **named):
+    """Every given tensor on ref's device and contiguous, of `dtype` where one is given, with
+    the given shape: named maps a name to (tensor, shape, dtype or None for `dtype`)."""
+    for name, (t, shape, dt) in named.items():
+        if t is None:
+            continue
+        if t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+        if t.dtype != (dt or dtype):
+            raise ValueError(f"{name} must be {dt or dtype}, not {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _check_cuda(t, name="q"):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _alloc_stream(stream, t):
+    """Where a call on `stream` allocates: that stream's own memory pool, so that the memory's
+    earlier and later users are ordered with the call."""
+    if stream is None:
+        return _NULL_CONTEXT
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=t.device)
+    return torch.cuda.stream(stream)
+
+
+def _span_dims(q, k, v, key_begin, key_end, slopes, **more):
+    _check_cuda(q)
+    B, Hq, Hkv, Sq, Skv, d = _dims_kv(q, k)
+    qs, ks = (B, Hq, Sq, d), (B, Hkv, Skv, d)
+    _check_like(q, q.dtype, q=(q, qs, None), k=(k, ks, None), v=(v, ks, None),
+                key_begin=(key_begin, (B, Sq), torch.int32),
+                key_end=(key_end, (B, Sq), torch.int32), slopes=(slopes, (Hq,), torch.float32),
+                **{n: (t, {"q": qs, "k": ks, "r": qs[:3]}[w], dt)
+                   for n, (t, w, dt) in more.items()})
+    return B, Hq, Hkv, Sq, Skv, d
+
+
+def fa_fwd_span(q, k, v, key_begin, key_end, out, lse, softcap=0.0, slopes=None, scale=None,
+                stream=None):
+    """Call fa_fwd_span: row i of batch b sees keys key_begin[b, i] <= j < key_end[b, i]
+    (int32 [B,Sq]); scores capped by softcap (0: not) and biased by
+    -slopes[h] * |i + Skv - Sq - j| (float32 [Hq], or None)."""
+    B, Hq, Hkv, Sq, Skv, d = _span_dims(q, k, v, key_begin, key_end, slopes,
+                                        out=(out, "q", None), lse=(lse, "r", torch.float32))
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    with _on_device(q):
+        rc = lib().fa_fwd_span(_ptr(q), _ptr(k), _ptr(v), _ptr(key_begin), _ptr(key_end),
+                               _ptr(out), _ptr(lse), B, Hq, Hkv, Sq, Skv, d, scale,
+                               float(softcap), _ptr(slopes), DTYPE_CODES.get(q.dtype, -1),
+                               _stream(stream, q))
+    if rc != 0:
+        raise FAError(rc, "fa_fwd_span")
+
+
+def fa_bwd_span_workspace_bytes(B, Hq, Hkv, Sq, Skv, d) -> int:
+    return int(lib().fa_bwd_span_workspace_bytes(B, Hq, Hkv, Sq, Skv, d))
+
+
+def fa_bwd_span(q, k, v, key_begin, key_end, out, dout, lse, dq, dk, dv, workspace, softcap=0.0,
+                slopes=None, scale=None, stream=None):
+    """Call fa_bwd_span; `workspace` is a device tensor of at least
+    fa_bwd_span_workspace_bytes(...) bytes."""
+    B, Hq, Hkv, Sq, Skv, d = _span_dims(
+        q, k, v, key_begin, key_end, slopes, out=(out, "q", None), dout=(dout, "q", None),
+        lse=(lse, "r", torch.float32), dq=(dq, "q", None), dk=(dk, "k", None), dv=(dv, "k", None))
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    ws_bytes = _workspace_bytes(workspace, q)
+    with _on_device(q):
+        rc = lib().fa_bwd_span(_ptr(q), _ptr(k), _ptr(v), _ptr(key_begin), _ptr(key_end),
+                               _ptr(out), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), B,
+                               Hq, Hkv, Sq, Skv, d, scale, float(softcap), _ptr(slopes),
+                               DTYPE_CODES.get(q.dtype, -1), _ptr(workspace), ws_bytes,
+                               _stream(stream, q))
+    if rc != 0:
+        raise FAError(rc, "fa_bwd_span")
+
+
+def _workspace_bytes(workspace, ref):
+    """Size of a caller's workspace (0 for None), which has to be dense and on ref's device."""
+    if workspace is None:
+        return 0
+    if workspace.device != ref.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {ref.device}")
+    return workspace.numel() * workspace.element_size()
+
+
+def attention_span_forward(q, k, v, key_begin, key_end, softcap=0.0, slopes=None, scale=None,
+                           stream=None):
+    """Allocate out and lse and run fa_fwd_span. Returns (out, lse)."""
+    _check_cuda(q)
+    with _alloc_stream(stream, q):
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    fa_fwd_span(q, k, v, key_begin, key_end, out, lse, softcap, slopes, scale, stream)
+    return out, lse
+
+
+def attention_span_backward(q, k, v, out, dout, lse, key_begin, key_end, softcap=0.0,
+                            slopes=None, scale=None, workspace=None, stream=None):
+    """Allocate dq, dk, dv (and a workspace unless given) and run fa_bwd_span."""
+    _check_cuda(q)
+    B, Hq, Hkv, Sq, Skv, d = _dims_kv(q, k)
+    with _alloc_stream(stream, q):
+        dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, k))
+        if workspace is None:
+            n = fa_bwd_span_workspace_bytes(B, Hq, Hkv, Sq, Skv, d)
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    fa_bwd_span(q, k, v, key_begin, key_end, out, dout, lse, dq, dk, dv, workspace, softcap,
+                slopes, scale, stream)
+    return dq, dk, dv
+
+
+def key_spans(B, Sq, Skv=None, *, causal=True, window=0, doc_lens=None, prefix_lens=None,
+              kv_lens=None, device=None):
+    """(key_begin, key_end), int32 [B, Sq], of the usual masks, combined. Query row i stands at
+    position i + Skv - Sq.
+
+    causal       up to the row's own position
+    window       only the last `window` keys up to the row's position (0: all)
+    doc_lens     lengths of the documents packed along the keys, the same in every sequence
+                 (a list) or one list per sequence: a row sees its own document only, and rows
+                 past the last document see nothing
+    prefix_lens  one number, or one per sequence: the first keys (of the row's document, with
+                 doc_lens) that every row sees although they lie after it
+    kv_lens      one number, or one per sequence: real keys; rows and keys past them are padding
+    """
+    Skv = Sq if Skv is None else Skv
+    pos = torch.arange(Sq, dtype=torch.int64)[None, :].expand(B, Sq) + (Skv - Sq)
+
+    def column(x):
+        t = torch.as_tensor(x, dtype=torch.int64).reshape(-1)
+        if t.numel() not in (1, B):
+            raise ValueError(f"one value or {B} wanted, not {t.numel()}")
+        return t[:, None].expand(B, 1)
+
+    begin, last = torch.zeros(B, Sq, dtype=torch.int64), torch.full((B, Sq), Skv)
+    if doc_lens is not None:
+        rows = list(doc_lens)
+        if not rows or not isinstance(rows[0], (list, tuple)):
+            rows = [rows] * B
+        if len(rows) != B:
+            raise ValueError(f"one list of lengths or {B} wanted, not {len(rows)}")
+        for b, lens in enumerate(rows):
+            if any(n < 0 for n in lens) or sum(lens) > Skv:
+                raise ValueError("documents must have lengths >= 0 and fit into the keys")
+            ends = torch.tensor(list(lens), dtype=torch.int64).cumsum(0)
+            which = torch.searchsorted(ends, pos[b].contiguous(), right=True)
+            edges = torch.cat((torch.zeros(1, dtype=torch.int64), ends, ends[-1:] if lens else
+                               torch.zeros(1, dtype=torch.int64)))
+            begin[b], last[b] = edges[which], edges[which + 1]
+    if kv_lens is not None:
+        n = column(kv_lens)
+        last = torch.where(pos < n, torch.minimum(last, n), torch.zeros_like(last))
+    end = torch.minimum(last, pos + 1) if causal else last
+    first = begin
+    if window:
+        begin = torch.maximum(begin, pos + 1 - int(window))
+    if prefix_lens is not None:
+        if window:
+            raise ValueError("a prefix and a window together are not one range of keys")
+        end = torch.maximum(end, torch.minimum(first + column(prefix_lens), last))
+    empty = end <= begin
+    begin, end = (torch.where(empty, torch.zeros_like(x), x).to(torch.int32).contiguous()
+                  for x in (begin, end))
+    return begin.to(device), end.to(device)
 
 
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024   # FA_NOALLOC_SCRATCH_BYTES in include/fa.h

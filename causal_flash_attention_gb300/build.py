@@ -28,7 +28,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_pair.cu", "fa_bwd.cu", "fa_simt.cu", "fa_noalloc.cu",
            "fa_decode.cu"]
-HEADERS = ["ptx.cuh", "fa_internal.h", "fa_decode.h", os.path.join("..", "..", "include", "fa.h")]
+HEADERS = ["ptx.cuh", "score_mod.cuh", "fa_internal.h", "fa_decode.h", os.path.join("..", "..", "include", "fa.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -180,6 +180,48 @@ SplitPlan split_plan(int B, int Hq, int Hkv, int Sq, int Skv, int d, int n_split
   return sp;
 }
 
+// Arguments the span entry points add.
+struct SpanArgs {
+  const int* key_begin;
+  const int* key_end;
+  const float* slopes;
+  float softcap;
+};
+
+int check_span(const SpanArgs& m) {
+  if (!(std::isfinite(m.softcap) && m.softcap >= 0.f)) return FA_ERR_SCALE;
+  if (!m.key_begin || !m.key_end) return FA_ERR_NULL;
+  if (((reinterpret_cast<uintptr_t>(m.key_begin) | reinterpret_cast<uintptr_t>(m.key_end) |
+        reinterpret_cast<uintptr_t>(m.slopes)) & 3u) != 0)
+    return FA_ERR_ALIGN;
+  return FA_OK;
+}
+
+ScoreMod make_mod(const SpanArgs& m, int Sq, int Skv, float scale) {
+  ScoreMod r;
+  r.key_begin = m.key_begin;
+  r.key_end = m.key_end;
+  r.slopes = m.slopes;
+  r.cap_in = m.softcap > 0.f ? 2.f * kLog2e * scale / m.softcap : 0.f;
+  r.cap_log2 = m.softcap * kLog2e;
+  r.pos_offset = Skv - Sq;
+  return r;
+}
+
+// Extra workspace of the span backward behind ws_layout's.
+struct SpanWs {
+  size_t spans, plan, total;
+};
+
+SpanWs span_ws(const WsLayout& w, int B, int Sq, int Skv) {
+  SpanWs s;
+  s.spans = w.total;
+  s.plan = s.spans + static_cast<size_t>(round_up(round_up(Sq, kTileM) * B * 8, 256));
+  const long long n_kv = (Skv + kTileN - 1) / kTileN;
+  s.total = s.plan + static_cast<size_t>(round_up(n_kv * B * 8, 256));
+  return s;
+}
+
 }  // namespace
 
 int check_bwd_args(const void* q, const void* k, const void* v, const void* out,
@@ -208,6 +250,120 @@ extern "C" void fa_trace_set(void* buf) { g_trace_buf = static_cast<unsigned lon
 #else
 #define FA_TRACE_PTR nullptr
 #endif
+
+namespace {
+
+// Shared body of fa_bwd_kv (mod null) and fa_bwd_span.
+int bwd_impl(const void* q, const void* k, const void* v, const void* out, const void* dout,
+             const float* lse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Sq,
+             int Skv, int d, int causal, float scale, int dtype, void* workspace,
+             size_t workspace_bytes, fa_stream_t stream, const SpanArgs* mod) {
+  int rc = check_bwd_args(q, k, v, out, dout, lse, dq, dk, dv, B, Hq, Hkv, Sq, Skv, d, causal,
+                          scale, dtype);
+  if (rc != FA_OK) return rc;
+  const WsLayout ws = ws_layout(B, Hq, Sq, d);
+  const SpanWs sws = span_ws(ws, B, Sq, Skv);
+  if (!workspace || workspace_bytes < (mod ? sws.total : ws.total)) return FA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_ALIGN;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* wsb = static_cast<uint8_t*>(workspace);
+  const int BH = B * Hq;
+  const int Sq_pad = static_cast<int>(round_up(Sq, kTileM));
+  const int kv_offset = causal ? Skv - Sq : 0;
+
+  float* delta = reinterpret_cast<float*>(wsb + ws.delta);
+  float* lse2 = reinterpret_cast<float*>(wsb + ws.lse2);
+  float* dq_acc = dtype == FA_F32 ? nullptr : reinterpret_cast<float*>(wsb + ws.dq_acc);
+  int* status = status_ptr();
+  if (!status) return FA_ERR_CUDA;
+
+  // Everything that can fail on the host (descriptor encoding, the status
+  // lookup) happens before the first kernel is enqueued.
+  const bool bf16 = dtype == FA_BF16;
+  BwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (dtype != FA_F32 &&
+      (!make_tmap(&p.tm_q, q, BH, Sq, d, bf16) || !make_tmap(&p.tm_k, k, B * Hkv, Skv, d, bf16) ||
+       !make_tmap(&p.tm_v, v, B * Hkv, Skv, d, bf16) ||
+       !make_tmap(&p.tm_do, dout, BH, Sq, d, bf16) ||
+       !make_tmap_acc(&p.tm_dq, dq_acc, BH, Sq_pad, d) ||
+       !make_tmap(&p.tm_dk, dk, B * Hkv, Skv, d, bf16, 32) ||
+       !make_tmap(&p.tm_dv, dv, B * Hkv, Skv, d, bf16, 32)))
+    return FA_ERR_TMA;
+
+  BwdPreParams pre{};
+  pre.out = out;
+  pre.dout = dout;
+  pre.lse = lse;
+  pre.delta = delta;
+  pre.lse2 = lse2;
+  pre.dq_acc = dq_acc;
+  pre.work = dtype == FA_F32 ? nullptr : reinterpret_cast<int*>(wsb + ws.work);
+  pre.BH = BH; pre.Sq = Sq; pre.Sq_pad = Sq_pad; pre.d = d;
+  pre.dtype = dtype;
+  if (mod) {
+    pre.B = B;
+    pre.Skv = Skv;
+    pre.n_kv_tiles = (Skv + kTileN - 1) / kTileN;
+    pre.key_begin = mod->key_begin;
+    pre.key_end = mod->key_end;
+    pre.spans = reinterpret_cast<int2*>(wsb + sws.spans);
+    pre.plan = reinterpret_cast<int2*>(wsb + sws.plan);
+  }
+  if ((mod ? launch_bwd_pre_span(pre, st) : launch_bwd_pre(pre, st)) != cudaSuccess)
+    return FA_ERR_CUDA;
+
+  if (dtype == FA_F32) {
+    SimtParams sp{};
+    sp.q = static_cast<const float*>(q);
+    sp.k = static_cast<const float*>(k);
+    sp.v = static_cast<const float*>(v);
+    sp.dout = static_cast<const float*>(dout);
+    sp.lse = lse;
+    sp.delta = delta;
+    sp.dq = static_cast<float*>(dq);
+    sp.dk = static_cast<float*>(dk);
+    sp.dv = static_cast<float*>(dv);
+    sp.B = B; sp.Hq = Hq; sp.Hkv = Hkv; sp.Sq = Sq; sp.Skv = Skv; sp.kv_offset = kv_offset;
+    sp.d = d;
+    sp.causal = causal != 0;
+    sp.scale = scale;
+    return launch_bwd_simt(sp, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  }
+
+  p.delta = delta;
+  p.lse2 = lse2;
+  p.dq_acc = dq_acc;
+  p.work = reinterpret_cast<int*>(wsb + ws.work);
+  p.dk = dk;
+  p.dv = dv;
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Sq = Sq; p.Skv = Skv; p.Sq_pad = Sq_pad;
+  p.kv_offset = kv_offset;
+  p.causal = causal != 0;
+  p.scale = scale;
+  p.scale_log2 = scale * kLog2e;
+  p.n_kv_tiles = (Skv + kTileN - 1) / kTileN;
+  p.n_q_tiles = (Sq + kTileM - 1) / kTileM;
+  p.trace = FA_TRACE_PTR;
+  p.status = status;
+  if (mod) {
+    p.mod = make_mod(*mod, Sq, Skv, scale);
+    p.spans = pre.spans;
+    p.plan = pre.plan;
+  }
+  if ((mod ? launch_bwd_span(p, d, bf16, st) : launch_bwd_tc(p, d, bf16, st)) != cudaSuccess)
+    return FA_ERR_CUDA;
+
+  DqConvertParams cv;
+  cv.dq_acc = dq_acc;
+  cv.dq = dq;
+  cv.BH = BH; cv.Sq = Sq; cv.Sq_pad = Sq_pad; cv.d = d;
+  cv.scale = scale;
+  cv.dtype = dtype;
+  return launch_dq_convert(cv, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -297,92 +453,8 @@ int fa_bwd_kv(const void* q, const void* k, const void* v, const void* out, cons
               const float* lse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Sq,
               int Skv, int d, int causal, float scale, int dtype, void* workspace,
               size_t workspace_bytes, fa_stream_t stream) {
-  int rc = check_bwd_args(q, k, v, out, dout, lse, dq, dk, dv, B, Hq, Hkv, Sq, Skv, d, causal,
-                          scale, dtype);
-  if (rc != FA_OK) return rc;
-  const WsLayout ws = ws_layout(B, Hq, Sq, d);
-  if (!workspace || workspace_bytes < ws.total) return FA_ERR_WORKSPACE;
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_ALIGN;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  uint8_t* wsb = static_cast<uint8_t*>(workspace);
-  const int BH = B * Hq;
-  const int Sq_pad = static_cast<int>(round_up(Sq, kTileM));
-  const int kv_offset = causal ? Skv - Sq : 0;
-
-  float* delta = reinterpret_cast<float*>(wsb + ws.delta);
-  float* lse2 = reinterpret_cast<float*>(wsb + ws.lse2);
-  float* dq_acc = dtype == FA_F32 ? nullptr : reinterpret_cast<float*>(wsb + ws.dq_acc);
-  int* status = status_ptr();
-  if (!status) return FA_ERR_CUDA;
-
-  // Everything that can fail on the host (descriptor encoding, the status
-  // lookup) happens before the first kernel is enqueued.
-  const bool bf16 = dtype == FA_BF16;
-  BwdParams p;
-  std::memset(&p, 0, sizeof(p));
-  if (dtype != FA_F32 &&
-      (!make_tmap(&p.tm_q, q, BH, Sq, d, bf16) || !make_tmap(&p.tm_k, k, B * Hkv, Skv, d, bf16) ||
-       !make_tmap(&p.tm_v, v, B * Hkv, Skv, d, bf16) ||
-       !make_tmap(&p.tm_do, dout, BH, Sq, d, bf16) ||
-       !make_tmap_acc(&p.tm_dq, dq_acc, BH, Sq_pad, d) ||
-       !make_tmap(&p.tm_dk, dk, B * Hkv, Skv, d, bf16, 32) ||
-       !make_tmap(&p.tm_dv, dv, B * Hkv, Skv, d, bf16, 32)))
-    return FA_ERR_TMA;
-
-  BwdPreParams pre;
-  pre.out = out;
-  pre.dout = dout;
-  pre.lse = lse;
-  pre.delta = delta;
-  pre.lse2 = lse2;
-  pre.dq_acc = dq_acc;
-  pre.work = dtype == FA_F32 ? nullptr : reinterpret_cast<int*>(wsb + ws.work);
-  pre.BH = BH; pre.Sq = Sq; pre.Sq_pad = Sq_pad; pre.d = d;
-  pre.dtype = dtype;
-  if (launch_bwd_pre(pre, st) != cudaSuccess) return FA_ERR_CUDA;
-
-  if (dtype == FA_F32) {
-    SimtParams sp{};
-    sp.q = static_cast<const float*>(q);
-    sp.k = static_cast<const float*>(k);
-    sp.v = static_cast<const float*>(v);
-    sp.dout = static_cast<const float*>(dout);
-    sp.lse = lse;
-    sp.delta = delta;
-    sp.dq = static_cast<float*>(dq);
-    sp.dk = static_cast<float*>(dk);
-    sp.dv = static_cast<float*>(dv);
-    sp.B = B; sp.Hq = Hq; sp.Hkv = Hkv; sp.Sq = Sq; sp.Skv = Skv; sp.kv_offset = kv_offset;
-    sp.d = d;
-    sp.causal = causal != 0;
-    sp.scale = scale;
-    return launch_bwd_simt(sp, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
-  }
-
-  p.delta = delta;
-  p.lse2 = lse2;
-  p.dq_acc = dq_acc;
-  p.work = reinterpret_cast<int*>(wsb + ws.work);
-  p.dk = dk;
-  p.dv = dv;
-  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Sq = Sq; p.Skv = Skv; p.Sq_pad = Sq_pad;
-  p.kv_offset = kv_offset;
-  p.causal = causal != 0;
-  p.scale = scale;
-  p.scale_log2 = scale * kLog2e;
-  p.n_kv_tiles = (Skv + kTileN - 1) / kTileN;
-  p.n_q_tiles = (Sq + kTileM - 1) / kTileM;
-  p.trace = FA_TRACE_PTR;
-  p.status = status;
-  if (launch_bwd_tc(p, d, bf16, st) != cudaSuccess) return FA_ERR_CUDA;
-
-  DqConvertParams cv;
-  cv.dq_acc = dq_acc;
-  cv.dq = dq;
-  cv.BH = BH; cv.Sq = Sq; cv.Sq_pad = Sq_pad; cv.d = d;
-  cv.scale = scale;
-  cv.dtype = dtype;
-  return launch_dq_convert(cv, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return bwd_impl(q, k, v, out, dout, lse, dq, dk, dv, B, Hq, Hkv, Sq, Skv, d, causal, scale,
+                  dtype, workspace, workspace_bytes, stream, nullptr);
 }
 
 int fa_bwd(const void* q, const void* k, const void* v, const void* out, const void* dout,
@@ -503,6 +575,54 @@ int fa_fwd_splitkv_paged(const void* q, const void* k_cache, const void* v_cache
   return splitkv_impl(q, k_cache, v_cache, out, lse, B, Hq, Hkv, Sq, Skv, d, causal, scale, dtype,
                       n_splits, workspace, workspace_bytes, stream, block_table, block_size,
                       max_blocks, num_blocks);
+}
+
+int fa_fwd_span(const void* q, const void* k, const void* v, const int* key_begin,
+                const int* key_end, void* out, float* lse, int B, int Hq, int Hkv, int Sq, int Skv,
+                int d, float scale, float softcap, const float* slopes, int dtype,
+                fa_stream_t stream) {
+  int rc = check_common(B, Hq, Hkv, Sq, Skv, d, 0, scale, dtype);
+  if (rc != FA_OK) return rc;
+  if (dtype == FA_F32) return FA_ERR_DTYPE;   // the span path runs on the tensor cores only
+  const SpanArgs mod{key_begin, key_end, slopes, softcap};
+  if ((rc = check_span(mod)) != FA_OK) return rc;
+  if (!q || !k || !v || !out || !lse) return FA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(lse))
+    return FA_ERR_ALIGN;
+  const bool bf16 = dtype == FA_BF16;
+  FwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (!make_tmap(&p.tm_q, q, B * Hq, Sq, d, bf16) || !make_tmap(&p.tm_k, k, B * Hkv, Skv, d, bf16) ||
+      !make_tmap(&p.tm_v, v, B * Hkv, Skv, d, bf16))
+    return FA_ERR_TMA;
+  p.out = out;
+  p.lse = lse;
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Sq = Sq; p.Skv = Skv;
+  p.scale_log2 = scale * kLog2e;
+  p.mod = make_mod(mod, Sq, Skv, scale);
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  return launch_fwd_span(p, d, bf16, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_bwd_span_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Skv, int d) {
+  if (check_common(B, Hq, Hkv, Sq, Skv, d, 0, 1.f, FA_BF16) != FA_OK) return 0;
+  return span_ws(ws_layout(B, Hq, Sq, d), B, Sq, Skv).total;
+}
+
+int fa_bwd_span(const void* q, const void* k, const void* v, const int* key_begin,
+                const int* key_end, const void* out, const void* dout, const float* lse, void* dq,
+                void* dk, void* dv, int B, int Hq, int Hkv, int Sq, int Skv, int d, float scale,
+                float softcap, const float* slopes, int dtype, void* workspace,
+                size_t workspace_bytes, fa_stream_t stream) {
+  if (dtype == FA_F32) return FA_ERR_DTYPE;
+  const SpanArgs mod{key_begin, key_end, slopes, softcap};
+  int rc = check_common(B, Hq, Hkv, Sq, Skv, d, 0, scale, dtype);
+  if (rc == FA_OK) rc = check_span(mod);
+  if (rc != FA_OK) return rc;
+  return bwd_impl(q, k, v, out, dout, lse, dq, dk, dv, B, Hq, Hkv, Sq, Skv, d, 0, scale, dtype,
+                  workspace, workspace_bytes, stream, &mod);
 }
 
 int fa_last_device_status(fa_stream_t stream, int* status) {

@@ -48,11 +48,22 @@
 // At d = 64, P^T [64,128) and dQ [192,256) have columns of their own instead:
 // S^T(i+1) is issued once the compute warps have read S^T(i), dP^T(i+1)
 // right after dQ(i), and the warps read dQ(i) out after P^T(i+1).
+//
+// Span form (kSpan): query row i sees the keys of its own span. Extra blocks of
+// the pre-pass clamp and pad the spans and find, for every key tile, the first
+// and last query tile with a row whose span reaches into it; an item walks that
+// range. The mask of a warp's 32 key rows against its 64 query columns is formed
+// as one word per column and transposed across the warp, so that each key row
+// holds its own 64 bits; tiles that every span covers skip it. With a cap, dS =
+// P (1 - tanh^2) (dP - D): the product P (1 - tanh^2) is kept, rounded to 16
+// bits as P itself is, in place of P, so it costs no registers. A row that sees
+// nothing has LSE = -inf and takes part with P = 0.
 #include <algorithm>
 #include <type_traits>
 
 #include "fa_internal.h"
 #include "ptx.cuh"
+#include "score_mod.cuh"
 
 namespace fa {
 namespace {
@@ -127,19 +138,75 @@ __device__ __forceinline__ float dot16(const uint4& a, const uint4& b) {
   return s;
 }
 
-template <typename T>
+// Span form: the clamped, padded spans of batch b (written by its first block)
+// and the query-tile range of kPlanTiles key tiles. Each warp takes every 8th
+// query tile and reduces its rows' least begin and greatest end.
+constexpr int kPlanTiles = 8;
+__device__ __forceinline__ void bwd_plan(const BwdPreParams& p) {
+  __shared__ int first[kPlanTiles], last[kPlanTiles];
+  const int per_b = (p.n_kv_tiles + kPlanTiles - 1) / kPlanTiles;
+  const int b = blockIdx.x / per_b, j0 = (blockIdx.x % per_b) * kPlanTiles;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x < kPlanTiles) {
+    first[threadIdx.x] = 0x7fffffff;
+    last[threadIdx.x] = -1;
+  }
+  __syncthreads();
+  const int* begin = p.key_begin + static_cast<size_t>(b) * p.Sq;
+  const int* end = p.key_end + static_cast<size_t>(b) * p.Sq;
+  int2* spans = p.spans + static_cast<size_t>(b) * p.Sq_pad;
+  for (int t = warp; t < p.Sq_pad / kTileM; t += 8) {
+    int lo = 0x7fffffff, hi = 0;
+#pragma unroll
+    for (int u = 0; u < kTileM / 32; ++u) {
+      const int i = t * kTileM + u * 32 + lane;
+      int2 s = make_int2(0, 0);
+      if (i < p.Sq) s = make_int2(max(begin[i], 0), min(end[i], p.Skv));
+      if (s.y <= s.x) s = make_int2(0, 0);
+      else lo = min(lo, s.x);
+      hi = max(hi, s.y);
+      if (j0 == 0) spans[i] = s;
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    const int k0 = (j0 + lane) * kTileN;
+    if (lane < kPlanTiles && hi > k0 && lo < k0 + kTileN) {
+      atomicMin(&first[lane], t);
+      atomicMax(&last[lane], t);
+    }
+  }
+  __syncthreads();
+  const int j = j0 + static_cast<int>(threadIdx.x);
+  if (threadIdx.x < kPlanTiles && j < p.n_kv_tiles) {
+    // a key tile that nothing sees takes one step, with P = 0: its dK and dV
+    // are written as zeros like any other's
+    const int f = first[threadIdx.x], l = last[threadIdx.x];
+    p.plan[static_cast<size_t>(b) * p.n_kv_tiles + j] =
+        l < 0 ? make_int2(0, 1) : make_int2(f, l - f + 1);
+  }
+}
+
+template <typename T, bool kSpan>
 __global__ void __launch_bounds__(256, 8) bwd_pre_kernel(const BwdPreParams p) {
   // the main kernel (launched as this grid's programmatic dependent) may be
   // scheduled now: its prologue overlaps this pass, and it waits for this
   // grid's completion before it reads anything this pass writes
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (kSpan) {
+    if (static_cast<int>(blockIdx.x) < p.n_plan_blocks) {
+      bwd_plan(p);
+      return;
+    }
+  }
+  const unsigned block = blockIdx.x - (kSpan ? p.n_plan_blocks : 0);
+  const unsigned n_blocks = gridDim.x - (kSpan ? p.n_plan_blocks : 0);
   const int lane = threadIdx.x & 31;
   const int U = p.d * static_cast<int>(sizeof(T)) / 16;   // power of two, divides 32
   const int rpw = 32 / U;
   const int sub = lane / U, u = lane % U;
   const long long total = static_cast<long long>(p.BH) * p.Sq_pad;
-  const long long warp0 = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
+  const long long warp0 = (static_cast<long long>(block) * blockDim.x + threadIdx.x) >> 5;
+  const long long nwarps = (static_cast<long long>(n_blocks) * blockDim.x) >> 5;
   for (long long row0 = warp0 * rpw; row0 < total; row0 += nwarps * rpw) {   // warp-uniform
     const long long row = row0 + sub;                                       // bh * Sq_pad + i
     const bool live = row < total;
@@ -155,14 +222,16 @@ __global__ void __launch_bounds__(256, 8) bwd_pre_kernel(const BwdPreParams p) {
     for (int sft = U / 2; sft > 0; sft >>= 1) dsum += __shfl_xor_sync(0xffffffffu, dsum, sft);
     if (live && u == 0) {
       p.delta[row] = (i < p.Sq) ? dsum : 0.f;
-      p.lse2[row] = (i < p.Sq) ? p.lse[static_cast<size_t>(bh) * p.Sq + i] * kLog2eF : INFINITY;
+      float l2 = (i < p.Sq) ? p.lse[static_cast<size_t>(bh) * p.Sq + i] * kLog2eF : INFINITY;
+      if (kSpan && l2 == -INFINITY) l2 = INFINITY;   // sees nothing: P = 0 as on padding rows
+      p.lse2[row] = l2;
     }
     if (p.dq_acc && live) {
       float4* acc = reinterpret_cast<float4*>(p.dq_acc + static_cast<size_t>(row) * p.d);
       for (int e = u; e < p.d / 4; e += U) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
-  if (p.work && blockIdx.x == 0 && threadIdx.x == 0) *p.work = 0;
+  if (p.work && block == 0 && threadIdx.x == 0) *p.work = 0;
 }
 
 // -------------------------------------------------------------- convert --
@@ -200,6 +269,7 @@ struct BwdItem {
   int i_start, n_i, n_iter;
 };
 
+template <bool kSpan>
 __device__ __forceinline__ BwdItem bwd_item(const BwdParams& p, int w) {
   BwdItem it;
   const int BHkv = p.B * p.Hkv;
@@ -209,13 +279,19 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdParams& p, int w) {
   it.g = it.bkv % p.Hkv;
   // causal: the first query tile holding a row at position >= this tile's
   // first key (query row i stands at position i + kv_offset)
-  it.i_start = p.causal ? max(0, it.j * kTileN - p.kv_offset) / kTileM : 0;
-  it.n_i = p.n_q_tiles - it.i_start;
+  if constexpr (kSpan) {
+    const int2 r = p.plan[static_cast<size_t>(it.b) * p.n_kv_tiles + it.j];
+    it.i_start = r.x;
+    it.n_i = r.y;
+  } else {
+    it.i_start = p.causal ? max(0, it.j * kTileN - p.kv_offset) / kTileM : 0;
+    it.n_i = p.n_q_tiles - it.i_start;
+  }
   it.n_iter = (p.Hq / p.Hkv) * it.n_i;
   return it;
 }
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kSpan>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa_bwd_kernel(const __grid_constant__ BwdParams p) {
   using Cfg = BwdCfg<D>;
@@ -358,7 +434,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int k = 0; ok; ++k) {
         BwdItem I{};
         if (w < n_items) {
-          I = bwd_item(p, w);
+          I = bwd_item<kSpan>(p, w);
           if (!(ok = load_step(I, 0))) break;
         }
         if (k > 0) {
@@ -383,7 +459,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!ok) break;
         w = atomicAdd(p.work, 1);
         if (w < n_items) {   // the next item's K_j, V_j into L2 while this item runs
-          const BwdItem J = bwd_item(p, w);
+          const BwdItem J = bwd_item<kSpan>(p, w);
           for (int c = 0; c < Cfg::kChunks; ++c) {
             tma_prefetch_l2_3d(&p.tm_k, c * kChunk, J.j * kTileN, J.bkv);
             tma_prefetch_l2_3d(&p.tm_v, c * kChunk, J.j * kTileN, J.bkv);
@@ -483,7 +559,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (k == 0 && !(ok = mbar_wait(drain, 0, abort_flag, p.status))) break;
 #endif
         tr(9);
-        const int N = bwd_item(p, w).n_iter;
+        const int N = bwd_item<kSpan>(p, w).n_iter;
         if (!(ok = issue_s(g) && issue_dp(g))) break;
         for (int n = 0; n < N; ++n, ++g) {
           const int st = g % NQ;
@@ -644,7 +720,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!ok) break;
       const int w = *item_slot;
       if (w >= n_items) break;
-      const BwdItem I = bwd_item(p, w);
+      const BwdItem I = bwd_item<kSpan>(p, w);
       const int kv = I.j * kTileN + r;
       for (int it = 0; it < I.n_iter; ++it, ++g) {
         const int st = g % NQ;
@@ -666,8 +742,85 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int q0 = i * kTileM + c0;
         const int thr = kv >= p.Skv ? 64 : (p.causal ? min(kv - p.kv_offset - q0, 64) : 0);
         const bool any_mask = __any_sync(0xffffffffu, thr > 0);
-        uint32_t ppk[32];
-        {
+        uint32_t ppk[32];   // P^T, packed (span form with a cap: P^T (1 - tanh^2))
+        if constexpr (kSpan) {
+          // this lane's key row against query columns 2 l (vis0 bit l) and 2 l + 1 (vis1)
+          const int4 sp = reinterpret_cast<const int4*>(
+              p.spans + (static_cast<size_t>(I.b) * p.Sq_pad + q0))[lane];
+          const int k0 = kv - lane;   // this warp's first key
+          const bool partial = __any_sync(
+              0xffffffffu, sp.x > k0 || sp.y < k0 + 32 || sp.z > k0 || sp.w < k0 + 32);
+          uint32_t vis0 = 0xffffffffu, vis1 = 0xffffffffu;
+          if (partial) {
+            vis0 = transpose_bits(span_bits(sp.x, sp.y, k0), lane);
+            vis1 = transpose_bits(span_bits(sp.z, sp.w, k0), lane);
+          }
+          const bool cap = p.mod.cap_in != 0.f;
+          const float cs = cap ? 1.f : c;
+          const float bias =
+              p.mod.slopes ? p.mod.slopes[I.g * (p.Hq / p.Hkv) + it / I.n_i] * (kLog2eF / cs) : 0.f;
+          const float d0 = static_cast<float>(q0 + p.mod.pos_offset - kv);
+          // Two halves of 32 columns, so that the cap's factors fit into
+          // registers. Packed P^T goes over score columns this warp has read
+          // itself, or into the P^T buffer at d = 64: the first half's after the
+          // second half has been read.
+          const uint32_t p_dst = Cfg::kSepQ ? t_p + half * 32 : t_s + half * 96;
+          uint32_t pk[16];
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t raw[32], fac[16];
+            tmem_ld32(t_s + c0 + hh * 32, raw);
+            tmem_wait_ld();
+            if (hh == 1) {
+              if constexpr (Cfg::kSepQ) {
+                tc_fence_before();   // S^T(n+1) may overwrite these scores
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free);
+                if (g > 0)           // dV(n-1) has read the previous P^T
+                  ok = __all_sync(0xffffffffu,
+                                  mbar_wait(dv_done, (g - 1) & 1, abort_flag, p.status));
+                tc_fence_after();
+              }
+              tmem_st16(p_dst, pk);
+            }
+            if (cap) {
+              const float cl = p.mod.cap_log2;
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float r0 = cap_r(__uint_as_float(raw[e]), p.mod.cap_in);
+                const float r1 = cap_r(__uint_as_float(raw[e + 1]), p.mod.cap_in);
+                raw[e] = __float_as_uint(fmaf(-2.f * cl, r0, cl));
+                raw[e + 1] = __float_as_uint(fmaf(-2.f * cl, r1, cl));
+                fac[e / 2] = pack2<false>(4.f * r0 * (1.f - r0), 4.f * r1 * (1.f - r1));
+              }
+            }
+            if (p.mod.slopes) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                raw[e] = __float_as_uint(fmaf(-bias, fabsf(d0 + static_cast<float>(hh * 32 + e)),
+                                              __uint_as_float(raw[e])));
+            }
+            if (partial) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((((e & 1) ? vis1 : vis0) >> (hh * 16 + e / 2)) & 1u))
+                  raw[e] = __float_as_uint(-INFINITY);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 l2 = *reinterpret_cast<const float2*>(l2s + hh * 32 + e);
+              const float p0 = ex2(fmaf(__uint_as_float(raw[e]), cs, -l2.x));
+              const float p1 = ex2(fmaf(__uint_as_float(raw[e + 1]), cs, -l2.y));
+              pk[e / 2] = pack2<kBf16>(p0, p1);
+              ppk[hh * 16 + e / 2] = pk[e / 2];
+              if (cap) {
+                const float2 f = unpack2<false>(fac[e / 2]);
+                ppk[hh * 16 + e / 2] = pack2<kBf16>(p0 * f.x, p1 * f.y);
+              }
+            }
+          }
+          tmem_st16(p_dst + 16, pk);
+        } else {
           uint32_t raw[64];
           tmem_ld32(t_s + c0, *reinterpret_cast<uint32_t(*)[32]>(raw));
           tmem_ld32(t_s + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(raw + 32));
@@ -847,10 +1000,10 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 block, siz
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kSpan = false>
 cudaError_t launch_bwd_impl(const BwdParams& p, cudaStream_t stream) {
   constexpr int smem = BwdCfg<D>::kSmemBytes;
-  auto kernel = fa_bwd_kernel<D, kBf16>;
+  auto kernel = fa_bwd_kernel<D, kBf16, kSpan>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // persistent: one CTA per SM (the shared and tensor memory of one CTA fill
@@ -865,19 +1018,40 @@ cudaError_t launch_bwd_impl(const BwdParams& p, cudaStream_t stream) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-}  // namespace
-
-cudaError_t launch_bwd_pre(const BwdPreParams& p, cudaStream_t stream) {
+unsigned pre_row_blocks(const BwdPreParams& p) {
   // one wave of 8-warp blocks (8 per SM), fewer when the rows run out
   const long long rows = static_cast<long long>(p.BH) * p.Sq_pad;
   const int esize = p.dtype == 0 ? 4 : 2;
   const long long rows_per_block = 8LL * (32 / (p.d * esize / 16));
-  const unsigned grid =
-      static_cast<unsigned>(std::min<long long>((rows + rows_per_block - 1) / rows_per_block, 152LL * 8));
-  if (p.dtype == 0) bwd_pre_kernel<float><<<grid, 256, 0, stream>>>(p);
-  else if (p.dtype == 1) bwd_pre_kernel<__half><<<grid, 256, 0, stream>>>(p);
-  else bwd_pre_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(p);
+  return static_cast<unsigned>(
+      std::min<long long>((rows + rows_per_block - 1) / rows_per_block, 152LL * 8));
+}
+
+}  // namespace
+
+cudaError_t launch_bwd_pre(const BwdPreParams& p, cudaStream_t stream) {
+  const unsigned grid = pre_row_blocks(p);
+  if (p.dtype == 0) bwd_pre_kernel<float, false><<<grid, 256, 0, stream>>>(p);
+  else if (p.dtype == 1) bwd_pre_kernel<__half, false><<<grid, 256, 0, stream>>>(p);
+  else bwd_pre_kernel<__nv_bfloat16, false><<<grid, 256, 0, stream>>>(p);
   return cudaGetLastError();
+}
+
+cudaError_t launch_bwd_pre_span(const BwdPreParams& p0, cudaStream_t stream) {
+  BwdPreParams p = p0;
+  p.n_plan_blocks = p.B * ((p.n_kv_tiles + kPlanTiles - 1) / kPlanTiles);
+  const unsigned grid = pre_row_blocks(p) + static_cast<unsigned>(p.n_plan_blocks);
+  if (p.dtype == 1) bwd_pre_kernel<__half, true><<<grid, 256, 0, stream>>>(p);
+  else bwd_pre_kernel<__nv_bfloat16, true><<<grid, 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_bwd_span(const BwdParams& p, int d, bool bf16, cudaStream_t stream) {
+  if (d == 128)
+    return bf16 ? launch_bwd_impl<128, true, true>(p, stream)
+                : launch_bwd_impl<128, false, true>(p, stream);
+  return bf16 ? launch_bwd_impl<64, true, true>(p, stream)
+              : launch_bwd_impl<64, false, true>(p, stream);
 }
 
 cudaError_t launch_bwd_tc(const BwdParams& p, int d, bool bf16, cudaStream_t stream) {

@@ -45,17 +45,27 @@
 // CTAs overlap each other's softmax, loads, start-up and write-out the same
 // way; the launcher takes it for grids of at least four one-tile CTAs per SM,
 // and for every grid at d = 64.
+//
+// Span form (kSpan, one tile per CTA): row i sees the keys of its own span
+// [key_begin_i, key_end_i) instead of the causal range. The CTA walks the key
+// tiles from the least begin to the greatest end of its 128 rows; a row masks
+// a tile that its span does not cover by a bit mask per 32 keys. Scores may be
+// capped (softcap * tanh(s / softcap)) and biased by distance
+// (-slope_h |i + Skv - Sq - j|) before the mask, in place of S in registers. A
+// row that sees nothing gets out = 0 and LSE = -inf.
 #include <algorithm>
 #include <cstdlib>
 #include <type_traits>
 
 #include "fa_internal.h"
 #include "ptx.cuh"
+#include "score_mod.cuh"
 
 namespace fa {
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2eF = 1.4426950408889634f;
 // A row's reference max only moves when the running max exceeds it by more
 // than this many powers of two; until then p = 2^(x - m_ref) <= 2^8, which
 // fp32 accumulation and 16-bit P both hold without loss of range.
@@ -85,7 +95,9 @@ struct FwdCfg {
   //           s_full[2], p_full[2], pv_done[2], drain, (kSepP) s_free[2]
   static constexpr int kNumBars = 1 + 4 * kStages + 6 + 1 + (kSepP ? 2 : 0);
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem base, abort flag
+  static constexpr int kOffSpan = kOffMisc + 16;            // span form: 4 warps' (begin, end)
   static constexpr int kSmemBytes = kOffMisc + 16 + 1024;   // + alignment slack
+  static constexpr int kSmemBytesSpan = kSmemBytes + 32;
 };
 
 struct FwdBars {
@@ -112,10 +124,12 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, int* s
   }
 }
 
-template <int D, bool kBf16, int T>
+template <int D, bool kBf16, int T, bool kSpan>
 __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
     fa_fwd_kernel(const __grid_constant__ FwdParams p) {
+  static_assert(!kSpan || T == 1, "the span form has one query tile per CTA");
   using Cfg = FwdCfg<D, T>;
+  static_assert(!kSpan || Cfg::kOffSpan % 16 == 0, "read as 16-byte vectors");
   constexpr int NS = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -158,8 +172,25 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
     if (q0 >= p.Sq) n_t[t] = 0;
     else n_t[t] = p.causal ? min(q0 / kTileN + p.kv_tiles_ahead, n_kv_total) : n_kv_total;
   }
-  const int n_load = max(n_t[0], n_t[1]);
-  if (threadIdx.x == 0) {
+  // span form: this softmax thread's row's keys, and the range of key tiles of
+  // the CTA's rows (known after the set-up barrier below)
+  int row_lo = 0, row_hi = 0, tile0 = 0;
+  if constexpr (kSpan) {
+    if (warp >= 2) {
+      const int row = unit * kTileM + (warp & 3) * 32 + lane;
+      if (row < p.Sq) {
+        const size_t at = static_cast<size_t>(b) * p.Sq + row;
+        row_lo = max(p.mod.key_begin[at], 0);
+        row_hi = min(p.mod.key_end[at], p.Skv);
+      }
+      if (row_hi <= row_lo) row_lo = row_hi = 0;   // sees nothing
+      const int lo = __reduce_min_sync(0xffffffffu, row_hi > 0 ? row_lo : 0x7fffffff);
+      const int hi = __reduce_max_sync(0xffffffffu, row_hi);
+      if (lane == 0)
+        *reinterpret_cast<int2*>(smem + Cfg::kOffSpan + (warp & 3) * 8) = make_int2(lo, hi);
+    }
+  }
+  if (!kSpan && threadIdx.x == 0) {
     trace_span(p.trace, 0, clock64());
     trace_span(p.trace, 1, smid());
     trace_span(p.trace, 2, n_t[0] + n_t[1]);
@@ -191,6 +222,14 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (kSpan) {
+    const int4 a = *reinterpret_cast<const int4*>(smem + Cfg::kOffSpan);
+    const int4 c = *reinterpret_cast<const int4*>(smem + Cfg::kOffSpan + 16);
+    const int hi = max(max(a.y, a.w), max(c.y, c.w));
+    tile0 = hi > 0 ? min(min(a.x, a.z), min(c.x, c.z)) / kTileN : 0;
+    n_t[0] = (hi + kTileN - 1) / kTileN - tile0;   // 0 when no row sees a key
+  }
+  const int n_load = max(n_t[0], n_t[1]);
 
   if (warp == 0) {
     // ===================== TMA producer =====================
@@ -217,7 +256,7 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
         mbar_arrive_expect_tx(bars.kf(st), Cfg::kTileBytes);
         for (int c = 0; c < Cfg::kChunks; ++c)
           tma_load_3d(sbase + Cfg::kOffK + st * Cfg::kTileBytes + c * (kTileN * 128), &p.tm_k,
-                      bars.kf(st), c * kChunk, j * kTileN, bkv);
+                      bars.kf(st), c * kChunk, (tile0 + j) * kTileN, bkv);
         if (j >= NS && !mbar_wait(bars.ve(st), (use - 1) & 1, abort_flag, p.status)) {
           ++j;   // the K load of this iteration is in flight
           break;
@@ -225,7 +264,7 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
         mbar_arrive_expect_tx(bars.vf(st), Cfg::kTileBytes);
         for (int c = 0; c < Cfg::kChunks; ++c)
           tma_load_3d(sbase + Cfg::kOffV + st * Cfg::kTileBytes + c * (kTileN * 128), &p.tm_v,
-                      bars.vf(st), c * kChunk, j * kTileN, bkv);
+                      bars.vf(st), c * kChunk, (tile0 + j) * kTileN, bkv);
       }
       if (*abort_flag) {
         // let every copy already issued land before the CTA releases its memory
@@ -333,7 +372,11 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
     const uint32_t s_tmem = tmem + lane_off + t * 128;
     const uint32_t o_tmem = tmem + lane_off + 128 * T + t * 128;
     const uint32_t p_tmem = Cfg::kSepP ? o_tmem + D : s_tmem;
-    const float c = p.scale_log2;
+    // span form with a cap: the capped scores come out in the log2 domain
+    const float c = (kSpan && p.mod.cap_in != 0.f) ? 1.f : p.scale_log2;
+    float bias = 0.f;   // span form: the distance bias per key, in units of 1 / c
+    if constexpr (kSpan)
+      if (p.mod.slopes) bias = p.mod.slopes[hq] * (kLog2eF / c);
 
     Tracer tr(((warp == 2 || warp == 6) && lane == 0) ? p.trace : nullptr, 2 + t);
     unsigned n_rescale = 0;    // steps that rescaled O (trace builds record it)
@@ -361,15 +404,39 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.sfr(t));
       }
-      const int kv0 = j * kTileN;
+      const int kv0 = (tile0 + j) * kTileN;
       // inline mask: causal (key after the query's position) and keys past the
       // sequence end; lim = last visible key of this row (rows past Sq are
       // never stored, so their limit may run past Skv - 1)
-      const int lim = p.causal ? row + p.kv_offset : p.Skv - 1;
-      if (kv0 + kTileN - 1 > lim) {
+      if constexpr (kSpan) {
+        if (p.mod.cap_in != 0.f) {
+          const float cap = p.mod.cap_log2;
 #pragma unroll
-        for (int i = 0; i < kTileN; ++i)
-          if (kv0 + i > lim) s[i] = -INFINITY;
+          for (int i = 0; i < kTileN; ++i)
+            s[i] = fmaf(-2.f * cap, cap_r(s[i], p.mod.cap_in), cap);
+        }
+        if (p.mod.slopes) {
+          const float d0 = static_cast<float>(kv0 - row - p.mod.pos_offset);
+#pragma unroll
+          for (int i = 0; i < kTileN; ++i)
+            s[i] = fmaf(-bias, fabsf(d0 + static_cast<float>(i)), s[i]);
+        }
+        if (kv0 < row_lo || kv0 + kTileN > row_hi) {
+#pragma unroll
+          for (int h = 0; h < kTileN / 32; ++h) {
+            const uint32_t w = span_bits(row_lo, row_hi, kv0 + h * 32);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((w >> i) & 1u)) s[h * 32 + i] = -INFINITY;
+          }
+        }
+      } else {
+        const int lim = p.causal ? row + p.kv_offset : p.Skv - 1;
+        if (kv0 + kTileN - 1 > lim) {
+#pragma unroll
+          for (int i = 0; i < kTileN; ++i)
+            if (kv0 + i > lim) s[i] = -INFINITY;
+        }
       }
       float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
       if constexpr (Cfg::kPaired) {
@@ -474,7 +541,8 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
       if (warp == 2 && lane == 0) trace_span(p.trace, 4, clock64());
       if (ok) {
         tc_fence_after();
-        const float inv_l = 1.f / l;
+        // span form: a row that sees nothing has O = 0, l = 0
+        const float inv_l = (kSpan && !(l > 0.f)) ? 0.f : 1.f / l;
         using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
         Elem* orow = reinterpret_cast<Elem*>(p.out) + (static_cast<size_t>(bh) * p.Sq + row) * D;
 #pragma unroll
@@ -495,7 +563,17 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
           }
         }
         if (row < p.Sq)
-          p.lse[static_cast<size_t>(bh) * p.Sq + row] = (m_ref + __log2f(l)) * kLn2;
+          p.lse[static_cast<size_t>(bh) * p.Sq + row] =
+              (kSpan && !(l > 0.f)) ? -INFINITY : (m_ref + __log2f(l)) * kLn2;
+      }
+    }
+    if constexpr (kSpan) {
+      if (n == 0 && row < p.Sq) {   // no row of the tile sees a key
+        const size_t at = static_cast<size_t>(bh) * p.Sq + row;
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + at * (D * 2));
+#pragma unroll
+        for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0u, 0u, 0u, 0u);
+        p.lse[at] = -INFINITY;
       }
     }
   }
@@ -509,10 +587,10 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
   }
 }
 
-template <int D, bool kBf16, int T>
+template <int D, bool kBf16, int T, bool kSpan = false>
 cudaError_t launch_fwd_impl(const FwdParams& p0, cudaStream_t stream) {
-  constexpr int smem = FwdCfg<D, T>::kSmemBytes;
-  auto kernel = fa_fwd_kernel<D, kBf16, T>;
+  constexpr int smem = kSpan ? FwdCfg<D, T>::kSmemBytesSpan : FwdCfg<D, T>::kSmemBytes;
+  auto kernel = fa_fwd_kernel<D, kBf16, T, kSpan>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   FwdParams p = p0;
@@ -552,6 +630,14 @@ cudaError_t launch_fwd_d(const FwdParams& p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t launch_fwd_span(const FwdParams& p, int d, bool bf16, cudaStream_t stream) {
+  if (d == 128)
+    return bf16 ? launch_fwd_impl<128, true, 1, true>(p, stream)
+                : launch_fwd_impl<128, false, 1, true>(p, stream);
+  return bf16 ? launch_fwd_impl<64, true, 1, true>(p, stream)
+              : launch_fwd_impl<64, false, 1, true>(p, stream);
+}
 
 cudaError_t launch_fwd_tc(const FwdParams& p, int d, bool bf16, cudaStream_t stream) {
   if (d == 128) return bf16 ? launch_fwd_d<128, true>(p, stream) : launch_fwd_d<128, false>(p, stream);

@@ -15,6 +15,18 @@ constexpr int kTileM = 128;
 constexpr int kTileN = 128;
 constexpr int kChunk = 64;
 
+// Score changes of the span entry points: query row i of batch b sees keys
+// key_begin[b][i] <= j < key_end[b][i] (clamped to [0, Skv)); scores are capped
+// to softcap * tanh(s / softcap) and biased by -slope_h * |i + Skv - Sq - j|.
+struct ScoreMod {
+  const int* key_begin;   // [B][Sq]
+  const int* key_end;     // [B][Sq]
+  const float* slopes;    // [Hq], or null: no distance bias
+  float cap_in;           // 2 log2(e) scale / softcap: e^(2 s / softcap) = 2^(cap_in <q, k>); 0: no cap
+  float cap_log2;         // softcap * log2(e)
+  int pos_offset;         // Skv - Sq: query row i stands at position i + pos_offset
+};
+
 // Sequence lengths: Sq query rows, Skv key/value rows (equal for
 // self-attention). Under the causal mask query row i stands at position
 // i + kv_offset, kv_offset = Skv - Sq >= 0 (0 without the mask).
@@ -36,6 +48,8 @@ struct FwdParams {
   // CTA-pair forward (d = 128) only:
   CUtensorMap tm_k_half;   // k as tm_k with a box of 64 rows: each CTA of a pair loads half a tile
   int n_qblocks;           // ceil(Sq / 512): CTA pairs per (batch, query head)
+  // span forward (fa_fwd_span) only
+  ScoreMod mod;
 };
 
 struct BwdPreParams {
@@ -48,6 +62,12 @@ struct BwdPreParams {
   int* work;          // the main kernel's work-item counter, zeroed here (null: none)
   int BH, Sq, Sq_pad, d;
   int dtype;
+  // span backward only (n_plan_blocks blocks more, which write spans and plan):
+  int n_plan_blocks, B, Skv, n_kv_tiles;
+  const int* key_begin;   // [B][Sq]
+  const int* key_end;     // [B][Sq]
+  int2* spans;            // [B][Sq_pad] clamped (begin, end), empty spans as (0, 0)
+  int2* plan;             // [B][n_kv_tiles] (first query tile, number of query tiles)
 };
 
 struct BwdParams {
@@ -72,6 +92,10 @@ struct BwdParams {
   int n_q_tiles;      // ceil(Sq / 128)
   int* status;
   unsigned long long* trace;   // timeline buffer of trace builds (FA_TRACE); else null
+  // span backward only
+  ScoreMod mod;
+  const int2* spans;  // [B][Sq_pad], written by the pre-pass
+  const int2* plan;   // [B][n_kv_tiles], written by the pre-pass
 };
 
 struct DqConvertParams {
@@ -102,9 +126,12 @@ int check_bwd_args(const void* q, const void* k, const void* v, const void* out,
 
 // Launchers; each returns a cudaError_t from the launch.
 cudaError_t launch_fwd_tc(const FwdParams& p, int d, bool bf16, cudaStream_t stream);
+cudaError_t launch_fwd_span(const FwdParams& p, int d, bool bf16, cudaStream_t stream);
 cudaError_t launch_fwd_pair(const FwdParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_bwd_pre(const BwdPreParams& p, cudaStream_t stream);
 cudaError_t launch_bwd_tc(const BwdParams& p, int d, bool bf16, cudaStream_t stream);
+cudaError_t launch_bwd_pre_span(const BwdPreParams& p, cudaStream_t stream);
+cudaError_t launch_bwd_span(const BwdParams& p, int d, bool bf16, cudaStream_t stream);
 cudaError_t launch_dq_convert(const DqConvertParams& p, cudaStream_t stream);
 cudaError_t launch_fwd_simt(const SimtParams& p, cudaStream_t stream);
 cudaError_t launch_bwd_simt(const SimtParams& p, cudaStream_t stream);

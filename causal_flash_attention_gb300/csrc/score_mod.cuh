@@ -1,0 +1,50 @@
+// Score changes of the span entry points, shared by their kernels: key spans
+// as bit masks, the tanh cap and the distance bias.
+#pragma once
+
+#include "fa_internal.h"
+#include "ptx.cuh"
+
+namespace fa {
+
+// Bits [0, x) of a word, for any x.
+__device__ __forceinline__ uint32_t bits_below(int x) {
+  return x <= 0 ? 0u : (x >= 32 ? 0xffffffffu : (1u << x) - 1u);
+}
+
+// Bits of [lo, hi) that fall into the 32 positions from `base`.
+__device__ __forceinline__ uint32_t span_bits(int lo, int hi, int base) {
+  return bits_below(hi - base) & ~bits_below(lo - base);
+}
+
+// Bit matrix transpose across a warp: bit l of lane r's word becomes bit r of
+// lane l's. Five exchanges of ever smaller blocks (the recursive block
+// transpose).
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
+  uint32_t m = 0x0000ffffu;
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, j);
+    x = (lane & j) ? ((x & ~m) | ((y & ~m) >> j)) : ((x & m) | ((y & m) << j));
+    m ^= m << (j >> 1);   // the next, half as wide, low-half mask
+  }
+  return x;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / (1 + e^(2u)) with e^(2u) = 2^(cap_in * s), s the unscaled score: tanh u =
+// 1 - 2r and 1 - tanh^2 u = 4 r (1 - r). Both ends are exact limits (2^x
+// overflows to infinity, r = 0; underflows to 0, r = 1). tanh.approx would take
+// one special-function instruction instead of two, but its relative error of
+// 2^-11 is as large as the rounding of P to 16 bits; this form is off by about
+// 2^-21 of the cap.
+__device__ __forceinline__ float cap_r(float s, float cap_in) {
+  return rcp_approx(1.f + ex2(s * cap_in));
+}
+
+}  // namespace fa

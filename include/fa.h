@@ -206,6 +206,52 @@ int fa_fwd_splitkv_paged(const void* q, const void* k_cache, const void* v_cache
                          size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * Attention in which every query row sees its own contiguous range of keys,
+ * for packed documents, sliding windows, prefixes seen by all, and padding:
+ * row i of batch b sees keys j with
+ *
+ *   max(key_begin[b][i], 0) <= j < min(key_end[b][i], Skv)
+ *
+ * in every head (key_begin, key_end: [B][Sq] int32 in device memory). Spans
+ * need no order among the rows. Scores are
+ *
+ *   s_ij = scale * <Q_i, K_j>                                softcap == 0
+ *   s_ij = softcap * tanh(scale * <Q_i, K_j> / softcap)      softcap > 0
+ *   s_ij -= slopes[h] * |i + Skv - Sq - j|                   slopes != NULL
+ *
+ * (slopes: [Hq] float32; a distance bias on the positions of fa_fwd_kv).
+ * Everything else is as for fa_fwd_kv without the causal mask, whose other
+ * arguments these are; Sq and Skv are unrelated. A row that sees no key gets
+ * out = 0 and lse = -infinity, and contributes nothing to any gradient; a key
+ * that no row sees gets dk = dv = 0. No gradient is formed for slopes.
+ *
+ * Masked positions: a masked probability of 0 still multiplies V (forward) and
+ * dO, Q, K (backward) of the same 128-row tile, so q, k, v, out and dout must
+ * be finite everywhere, padding included.
+ *
+ * FA_BF16 and FA_F16 only (FA_F32 gives FA_ERR_DTYPE). softcap must be finite
+ * and >= 0 (else FA_ERR_SCALE); key_begin, key_end and slopes need 4-byte
+ * alignment. dk and dv have the same bits on every call; dq is summed with
+ * fp32 additions in global memory whose order, and so its last bits, may differ.
+ */
+int fa_fwd_span(const void* q, const void* k, const void* v, const int* key_begin,
+                const int* key_end, void* out, float* lse, int B, int Hq, int Hkv, int Sq,
+                int Skv, int d, float scale, float softcap, const float* slopes, int dtype,
+                fa_stream_t stream);
+
+/* Workspace bytes of fa_bwd_span: fa_bwd_kv_workspace_bytes, then the padded
+ * spans ([B][Sq rounded up to 128] pairs of int32) and the query-tile range of
+ * every key tile ([B][ceil(Skv / 128)] pairs), each region 256-byte aligned.
+ * Returns 0 for invalid sizes. */
+size_t fa_bwd_span_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Skv, int d);
+
+int fa_bwd_span(const void* q, const void* k, const void* v, const int* key_begin,
+                const int* key_end, const void* out, const void* dout, const float* lse,
+                void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Sq, int Skv, int d,
+                float scale, float softcap, const float* slopes, int dtype, void* workspace,
+                size_t workspace_bytes, fa_stream_t stream);
+
+/*
  * Size of the fixed device scratch array behind fa_bwd_noalloc (32 MiB). A
  * call fits when fa_bwd_workspace_bytes(B, Hq, Hkv, S, d) is at most this,
  * e.g. B*Hq = 96 heads at S = 1024, d = 64 (about 25.9 MB). The limit uses
