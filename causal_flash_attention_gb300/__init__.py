@@ -30,7 +30,8 @@ __all__ = [
     "fa_bwd_kv_workspace_bytes", "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_bytes",
     "decode_forward", "fa_fwd_splitkv_paged", "decode_forward_paged",
     "fa_fwd_span", "fa_bwd_span", "fa_bwd_span_workspace_bytes", "attention_span_forward",
-    "attention_span_backward", "key_spans",
+    "attention_span_backward", "key_spans", "fa_fwd_ragged_paged",
+    "fa_fwd_ragged_paged_workspace_bytes", "decode_forward_ragged",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa.so")
@@ -78,6 +79,10 @@ def lib() -> ctypes.CDLL:
     L.fa_bwd_span_workspace_bytes.restype = sz
     L.fa_bwd_span.argtypes = [vp] * 11 + [i32] * 6 + [f32, f32, vp, i32, vp, sz, vp]
     L.fa_bwd_span.restype = i32
+    L.fa_fwd_ragged_paged.argtypes = [vp] * 7 + [i32] * 9 + [f32, f32, vp, i32, vp, sz, vp]
+    L.fa_fwd_ragged_paged.restype = i32
+    L.fa_fwd_ragged_paged_workspace_bytes.argtypes = [i32] * 7
+    L.fa_fwd_ragged_paged_workspace_bytes.restype = sz
     L.fa_strerror.argtypes = [i32]
     L.fa_strerror.restype = ctypes.c_char_p
     L.fa_last_device_status.argtypes = [vp, ctypes.POINTER(i32)]
@@ -498,6 +503,62 @@ def key_spans(B, Sq, Skv=None, *, causal=True, window=0, doc_lens=None, prefix_l
     begin, end = (torch.where(empty, torch.zeros_like(x), x).to(torch.int32).contiguous()
                   for x in (begin, end))
     return begin.to(device), end.to(device)
+
+
+# ------------------------------------------------------ ragged paged cache --
+def _ragged_dims(q, k_cache, v_cache, block_table, seq_lens, **more):
+    _check_cuda(q)
+    if q.dim() != 4 or k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q [B,Hq,Sq,d], caches [num_blocks,Hkv,block_size,d], table [B,max_blocks]")
+    B, Hq, Sq, d = (int(x) for x in q.shape)
+    num_blocks, Hkv, block_size = (int(x) for x in k_cache.shape[:3])
+    max_blocks = int(block_table.shape[1])
+    cache = (num_blocks, Hkv, block_size, d)
+    _check_like(q, q.dtype, q=(q, q.shape, None), k_cache=(k_cache, cache, None), v_cache=(v_cache, cache, None),
+                block_table=(block_table, (B, max_blocks), torch.int32),
+                seq_lens=(seq_lens, (B,), torch.int32), **more)
+    return B, Hq, Hkv, Sq, d, block_size, num_blocks, max_blocks
+
+
+def fa_fwd_ragged_paged_workspace_bytes(B, Hq, Hkv, Sq, d, block_size, max_blocks) -> int:
+    return int(lib().fa_fwd_ragged_paged_workspace_bytes(B, Hq, Hkv, Sq, d, block_size, max_blocks))
+
+
+def fa_fwd_ragged_paged(q, k_cache, v_cache, block_table, seq_lens, out, lse, workspace,
+                        window=0, softcap=0.0, slopes=None, scale=None, stream=None):
+    """Call fa_fwd_ragged_paged: q [B,Hq,Sq,d], the last Sq tokens of each sequence;
+    k_cache/v_cache [num_blocks,Hkv,block_size,d]; block_table int32 [B,max_blocks];
+    seq_lens int32 [B]; `workspace` a device tensor of at least
+    fa_fwd_ragged_paged_workspace_bytes(...) bytes."""
+    B, Hq, Hkv, Sq, d, block_size, num_blocks, max_blocks = _ragged_dims(
+        q, k_cache, v_cache, block_table, seq_lens,
+        out=(out, q.shape, None), lse=(lse, q.shape[:3], torch.float32),
+        slopes=(slopes, (q.shape[1],), torch.float32))
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    with _on_device(q):
+        rc = lib().fa_fwd_ragged_paged(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(out),
+            _ptr(lse), B, Hq, Hkv, Sq, d, block_size, num_blocks, max_blocks, int(window), scale,
+            float(softcap), _ptr(slopes), DTYPE_CODES.get(q.dtype, -1), _ptr(workspace),
+            _workspace_bytes(workspace, q), _stream(stream, q))
+    if rc != 0:
+        raise FAError(rc, "fa_fwd_ragged_paged")
+
+
+def decode_forward_ragged(q, k_cache, v_cache, block_table, seq_lens, window=0, softcap=0.0,
+                          slopes=None, scale=None, stream=None):
+    """Allocate out, lse and the workspace and run fa_fwd_ragged_paged. Returns (out, lse)."""
+    _check_cuda(q)
+    B, Hq, Sq, d = (int(x) for x in q.shape)
+    n = fa_fwd_ragged_paged_workspace_bytes(B, Hq, int(k_cache.shape[1]), Sq, d,
+                                            int(k_cache.shape[2]), int(block_table.shape[1]))
+    with _alloc_stream(stream, q):
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+    fa_fwd_ragged_paged(q, k_cache, v_cache, block_table, seq_lens, out, lse, ws, window, softcap,
+                        slopes, scale, stream)
+    return out, lse
 
 
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024   # FA_NOALLOC_SCRATCH_BYTES in include/fa.h

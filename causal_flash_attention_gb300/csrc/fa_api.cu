@@ -11,6 +11,7 @@
 #include "../../include/fa.h"
 #include "fa_decode.h"
 #include "fa_internal.h"
+#include "fa_ragged.h"
 
 namespace fa {
 
@@ -178,6 +179,35 @@ SplitPlan split_plan(int B, int Hq, int Hkv, int Sq, int Skv, int d, int n_split
     sp.total = sp.part_lse2 + static_cast<size_t>(round_up(rows * 4, 256));
   }
   return sp;
+}
+
+// Plan of fa_fwd_ragged_paged: one wave of CTAs (fewer when the table cannot
+// hold that many key tiles), two partial results a CTA.
+struct RaggedPlan {
+  int n_ctas, R;
+  size_t part_out, part_lse2, prefix, total;
+};
+
+RaggedPlan ragged_plan(int B, int Hq, int Hkv, int Sq, int d, int block_size, int max_blocks) {
+  RaggedPlan rp;
+  const long long tiles = (static_cast<long long>(max_blocks) * block_size + kTileN - 1) / kTileN;
+  const long long bhkv = static_cast<long long>(B) * Hkv;
+  rp.n_ctas = bhkv >= kDecodeWaveCtas ? kDecodeWaveCtas
+                                      : static_cast<int>(std::min<long long>(kDecodeWaveCtas, bhkv * tiles));
+  rp.R = (Hq / Hkv) * Sq;
+  const long long rows = 2LL * rp.n_ctas * rp.R;
+  rp.part_out = 0;
+  rp.part_lse2 = static_cast<size_t>(round_up(rows * d * 4, 256));
+  rp.prefix = rp.part_lse2 + static_cast<size_t>(round_up(rows * 4, 256));
+  rp.total = rp.prefix + static_cast<size_t>(round_up((B + 1LL) * 8, 256));
+  return rp;
+}
+
+// Sizes of a paged cache and of few query rows against it.
+bool paged_sizes_ok(int Hq, int Hkv, int Sq, int block_size, int num_blocks, int max_blocks) {
+  return static_cast<long long>(Hq / Hkv) * Sq <= kDecodeMaxRows && block_size >= 16 &&
+         block_size <= 1024 && (block_size & (block_size - 1)) == 0 && num_blocks >= 1 &&
+         static_cast<long long>(num_blocks) * Hkv <= (1LL << 30) && max_blocks >= 1;
 }
 
 // Arguments the span entry points add.
@@ -623,6 +653,68 @@ int fa_bwd_span(const void* q, const void* k, const void* v, const int* key_begi
   if (rc != FA_OK) return rc;
   return bwd_impl(q, k, v, out, dout, lse, dq, dk, dv, B, Hq, Hkv, Sq, Skv, d, 0, scale, dtype,
                   workspace, workspace_bytes, stream, &mod);
+}
+
+size_t fa_fwd_ragged_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int d, int block_size,
+                                           int max_blocks) {
+  if (check_common(B, Hq, Hkv, Sq, Sq, d, 0, 1.f, FA_BF16) != FA_OK ||
+      !paged_sizes_ok(Hq, Hkv, Sq, block_size, 1, max_blocks))
+    return 0;
+  return ragged_plan(B, Hq, Hkv, Sq, d, block_size, max_blocks).total;
+}
+
+int fa_fwd_ragged_paged(const void* q, const void* k_cache, const void* v_cache,
+                        const int* block_table, const int* seq_lens, void* out, float* lse, int B,
+                        int Hq, int Hkv, int Sq, int d, int block_size, int num_blocks,
+                        int max_blocks, int window, float scale, float softcap,
+                        const float* slopes, int dtype, void* workspace, size_t workspace_bytes,
+                        fa_stream_t stream) {
+  int rc = check_common(B, Hq, Hkv, Sq, Sq, d, 0, scale, dtype);
+  if (rc != FA_OK) return rc;
+  if (dtype == FA_F32) return FA_ERR_DTYPE;   // the paged path runs on the tensor cores only
+  if (!paged_sizes_ok(Hq, Hkv, Sq, block_size, num_blocks, max_blocks) || window < 0)
+    return FA_ERR_SHAPE;
+  if (!(std::isfinite(softcap) && softcap >= 0.f)) return FA_ERR_SCALE;
+  if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !lse) return FA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      !aligned16(lse) ||
+      ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(seq_lens) |
+        reinterpret_cast<uintptr_t>(slopes)) & 3u) != 0)
+    return FA_ERR_ALIGN;
+  const RaggedPlan rp = ragged_plan(B, Hq, Hkv, Sq, d, block_size, max_blocks);
+  if (!workspace || workspace_bytes < rp.total) return FA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_ALIGN;
+  uint8_t* wsb = static_cast<uint8_t*>(workspace);
+  const bool bf16 = dtype == FA_BF16;
+  RaggedParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.box_rows = std::min(block_size, kTileN);
+  if (!make_tmap(&p.tm_k, k_cache, num_blocks * Hkv, block_size, d, bf16, p.box_rows) ||
+      !make_tmap(&p.tm_v, v_cache, num_blocks * Hkv, block_size, d, bf16, p.box_rows))
+    return FA_ERR_TMA;
+  const ScoreMod mod = make_mod(SpanArgs{nullptr, nullptr, slopes, softcap}, 0, 0, scale);
+  p.q = q;
+  p.out = out;
+  p.lse = lse;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.slopes = slopes;
+  p.part_out = reinterpret_cast<float*>(wsb + rp.part_out);
+  p.part_lse2 = reinterpret_cast<float*>(wsb + rp.part_lse2);
+  p.prefix = reinterpret_cast<long long*>(wsb + rp.prefix);
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Sq = Sq;
+  p.G = Hq / Hkv;
+  p.R = rp.R;
+  p.block_size = block_size; p.max_blocks = max_blocks; p.num_blocks = num_blocks;
+  p.window = window;
+  p.scale_log2 = scale * kLog2e;
+  p.cap_in = mod.cap_in;
+  p.cap_log2 = mod.cap_log2;
+  p.n_ctas = rp.n_ctas;
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  return launch_ragged(p, d, bf16, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK : FA_ERR_CUDA;
 }
 
 int fa_last_device_status(fa_stream_t stream, int* status) {

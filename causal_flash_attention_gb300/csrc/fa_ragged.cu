@@ -1,0 +1,657 @@
+// Attention of one or a few new tokens per sequence over a paged key/value
+// cache, for sequences of unequal length known on the device only.
+//
+// Row s of sequence b (length L_b, its new tokens included) stands at position
+// p = L_b - Sq + s and sees keys max(0, p + 1 - window) <= j <= p (window 0: from
+// key 0); scores may be capped and biased by distance as in the span forward.
+// The query packing, the tile pipeline and the merge formula are those of the
+// split-KV forward (fa_decode.cu); the division of the work is not:
+//
+//   - the host knows neither the lengths nor how uneven they are, so the work is
+//     one list of 128-key tiles over all sequences and heads, and each of one
+//     wave of CTAs takes an equal, contiguous share of it, found by a scan over
+//     the lengths at its start. One long sequence among short ones spreads over
+//     the GPU, and a captured graph stays balanced when the lengths change;
+//   - a share is a run of segments, each a key range of one (sequence, key/value
+//     head). Loads run ahead across segments. A segment that holds its whole
+//     range writes out and LSE itself; the others (at most the first and the
+//     last of a share) write a partial result, which the merge kernel joins in
+//     the order of the shares, so results do not depend on scheduling.
+//
+// The kernel is bound by the bytes of K and V (G * Sq <= 128 rows share each
+// tile). Rows of the cache outside a sequence's keys (the tail of its last page,
+// keys before every row's window) are cleared in the V tile before use, so that
+// whatever they hold, NaN included, cannot reach O through a probability of 0.
+//
+// Warp roles and tensor memory: as fa_decode.cu.
+#include <algorithm>
+#include <type_traits>
+
+#include "fa_ragged.h"
+#include "ptx.cuh"
+#include "score_mod.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr float kLn2R = 0.6931471805599453f;
+constexpr float kLog2eR = 1.4426950408889634f;
+constexpr float kRescaleThresholdR = 8.0f;   // same lazy-rescale rule as the forward
+
+template <int D>
+struct RagCfg {
+  static constexpr int kChunks = D / kChunk;
+  static constexpr int kTileBytes = kTileM * D * 2;
+  static constexpr int kStages = 3;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kTileBytes;
+  static constexpr int kOffV = kOffK + kStages * kTileBytes;
+  static constexpr int kOffBar = kOffV + kStages * kTileBytes;
+  // q_ready, k_full[S], k_empty[S], v_full[S], v_empty[S], s_full[2],
+  // p_full[2], pv_done[2], drain
+  static constexpr int kNumBars = 1 + 4 * kStages + 6 + 1;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffScan = kOffMisc + 16;            // 6 warp totals, start (b, prefix)
+  static constexpr int kSmemBytes = kOffScan + 64 + 1024;   // + alignment slack
+};
+
+__device__ __forceinline__ void drain_wait_r(uint32_t bar, uint32_t parity, int* status) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > kDrainLimitCycles) {
+      atomicOr(status, kStatusWaitTimeout);
+      return;
+    }
+  }
+}
+
+// Keys of one sequence that any of its rows sees, and their tiles.
+struct SeqKeys {
+  int len, first;     // keys [first, len)
+  int tile0, n;       // tiles [tile0, tile0 + n)
+};
+
+__device__ __forceinline__ SeqKeys seq_keys(const RaggedParams& p, int b) {
+  SeqKeys s;
+  const long long capacity = static_cast<long long>(p.max_blocks) * p.block_size;
+  s.len = static_cast<int>(
+      min(static_cast<long long>(max(p.seq_lens[b], 0)), min(capacity, 0x7fffff00LL)));
+  s.first = p.window > 0 ? max(0, s.len - p.Sq + 1 - p.window) : 0;
+  s.tile0 = s.first / kTileN;
+  s.n = s.len > 0 ? (s.len + kTileN - 1) / kTileN - s.tile0 : 0;
+  return s;
+}
+
+// Shares of a list of `total` tiles: no more than it has tiles, so that none is
+// empty (the merge reads a part of every share between a head's first and last).
+__device__ __forceinline__ int n_shares(const RaggedParams& p, long long total) {
+  return static_cast<int>(min(static_cast<long long>(p.n_ctas), total));
+}
+__device__ __forceinline__ long long share_begin(long long total, int c, int n) {
+  return total * c / n;
+}
+
+// The segments of one CTA's share, in order; every role walks its own copy.
+struct Segments {
+  long long cur, end, pre;   // list position, end of the share, tiles per head before b
+  int b;
+  SeqKeys keys;
+  // the current segment
+  int kvh, tile0, n;
+  bool whole;
+
+  __device__ void init(const RaggedParams& p, long long begin, long long stop, int b0,
+                       long long pre0) {
+    cur = begin;
+    end = stop;
+    b = b0;
+    pre = pre0;
+    if (cur < end) keys = seq_keys(p, b);
+  }
+  __device__ bool next(const RaggedParams& p) {
+    if (cur >= end) return false;
+    while (cur >= (pre + keys.n) * p.Hkv) {   // cur < end <= total: some later b has tiles
+      pre += keys.n;
+      keys = seq_keys(p, ++b);
+    }
+    const long long off = cur - pre * p.Hkv;
+    kvh = static_cast<int>(off / keys.n);
+    const int t = static_cast<int>(off - static_cast<long long>(kvh) * keys.n);
+    n = static_cast<int>(min(static_cast<long long>(keys.n - t), end - cur));
+    tile0 = keys.tile0 + t;
+    whole = n == keys.n;
+    cur += n;
+    return true;
+  }
+};
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    fa_ragged_kernel(const __grid_constant__ RaggedParams p) {
+  using Cfg = RagCfg<D>;
+  constexpr int NS = Cfg::kStages;
+  using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
+  long long* scan = reinterpret_cast<long long*>(smem + Cfg::kOffScan);
+
+  const uint32_t bar0 = sbase + Cfg::kOffBar;
+  const uint32_t q_ready = bar0;
+  auto k_full = [&](int s) { return bar0 + 8 * (1 + s); };
+  auto k_empty = [&](int s) { return bar0 + 8 * (1 + NS + s); };
+  auto v_full = [&](int s) { return bar0 + 8 * (1 + 2 * NS + s); };
+  auto v_empty = [&](int s) { return bar0 + 8 * (1 + 3 * NS + s); };
+  auto s_full = [&](int b) { return bar0 + 8 * (1 + 4 * NS + b); };
+  auto p_full = [&](int b) { return bar0 + 8 * (3 + 4 * NS + b); };
+  auto pv_done = [&](int b) { return bar0 + 8 * (5 + 4 * NS + b); };
+  const uint32_t drain = bar0 + 8 * (7 + 4 * NS);
+
+  const int warp = static_cast<int>(warp_id());
+  const int lane = static_cast<int>(lane_id());
+  const int cta = static_cast<int>(blockIdx.x);
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_ready, 4);   // one arrival per row warp and segment
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 1);
+    }
+    for (int bb = 0; bb < 2; ++bb) {
+      mbar_init(s_full(bb), 1);
+      mbar_init(p_full(bb), 4);
+      mbar_init(pv_done(bb), 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+
+  // ---- this CTA's share: a scan over the sequences' tile counts ----
+  // thread t holds sequences [t * per, (t + 1) * per)
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b_lo = static_cast<int>(min(static_cast<long long>(p.B),
+                                        static_cast<long long>(threadIdx.x) * per));
+  const int b_hi = min(p.B, b_lo + per);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += seq_keys(p, b).n;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) scan[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  long long pre = incl - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) pre += scan[w];
+    total += scan[w];
+  }
+  total *= p.Hkv;
+  const int shares = n_shares(p, total);
+  const long long begin = cta < shares ? share_begin(total, cta, shares) : 0;
+  const long long end = cta < shares ? share_begin(total, cta + 1, shares) : 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int n = seq_keys(p, b).n;
+    if (begin < end && pre * p.Hkv <= begin && begin < (pre + n) * p.Hkv) {
+      scan[6] = b;
+      scan[7] = pre;
+    }
+    if (cta == 0) p.prefix[b] = pre;
+    pre += n;
+    if (cta == 0 && b == p.B - 1) p.prefix[p.B] = pre;
+  }
+  __syncthreads();
+  // the merge kernel may be scheduled now; it waits for this grid's completion
+  // before it reads anything
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  Segments seg;
+  seg.init(p, begin, end, begin < end ? static_cast<int>(scan[6]) : 0, begin < end ? scan[7] : 0);
+  const long long n_tiles = end - begin;
+
+  if (warp == 0) {
+    // ===================== TMA producer =====================
+    // Each lane i < 128 / box_rows reads the block-table entry of box i of a
+    // tile and issues that box itself. A block past the sequence, or a table
+    // entry outside [0, num_blocks), is loaded from an out-of-range row, which
+    // the copy fills with zeros.
+    const int n_boxes = kTileN / p.box_rows;
+    auto load_part = [&](const CUtensorMap* tm, uint32_t dst, uint32_t bar, int key, int pb) {
+      if (lane >= n_boxes) return;
+      const bool in_range = pb >= 0 && pb < p.num_blocks;
+      const int y = in_range ? key % p.block_size : p.block_size;
+      const int z = in_range ? pb * p.Hkv + seg.kvh : 0;
+      for (int c = 0; c < Cfg::kChunks; ++c)
+        tma_load_3d(dst + c * (kTileN * 128) + lane * p.box_rows * 128, tm, bar, c * kChunk, y, z);
+    };
+    int g = 0;   // tiles whose K load has been issued
+    bool stop = false;
+    while (!stop && seg.next(p)) {
+      const int* table = p.block_table + static_cast<size_t>(seg.b) * p.max_blocks;
+      for (int j = 0; j < seg.n; ++j, ++g) {
+        const int key = (seg.tile0 + j) * kTileN + lane * p.box_rows;
+        const int st = g % NS;
+        const uint32_t use = static_cast<uint32_t>(g / NS);
+        int pb = -1;
+        if (lane < n_boxes && key < seg.keys.len) pb = table[key / p.block_size];
+        int fail = 0;
+        if (lane == 0) {
+          if (g >= NS && !mbar_wait(k_empty(st), (use - 1) & 1, abort_flag, p.status)) fail = 1;
+          else mbar_arrive_expect_tx(k_full(st), Cfg::kTileBytes);
+        }
+        if ((stop = __shfl_sync(0xffffffffu, fail, 0))) break;
+        load_part(&p.tm_k, sbase + Cfg::kOffK + st * Cfg::kTileBytes, k_full(st), key, pb);
+        if (lane == 0) {
+          if (g >= NS && !mbar_wait(v_empty(st), (use - 1) & 1, abort_flag, p.status)) fail = 1;
+          else mbar_arrive_expect_tx(v_full(st), Cfg::kTileBytes);
+        }
+        if ((stop = __shfl_sync(0xffffffffu, fail, 0))) {
+          ++g;   // this tile's K load is in flight
+          break;
+        }
+        load_part(&p.tm_v, sbase + Cfg::kOffV + st * Cfg::kTileBytes, v_full(st), key, pb);
+      }
+    }
+    if (lane == 0 && *abort_flag) {
+      // let every copy already issued land before the CTA releases its memory
+      for (int gg = max(0, g - NS); gg < g; ++gg) {
+        const uint32_t par = static_cast<uint32_t>(gg / NS) & 1;
+        drain_wait_r(k_full(gg % NS), par, p.status);
+        drain_wait_r(v_full(gg % NS), par, p.status);
+      }
+    }
+  } else if (warp == 1) {
+    // ===================== MMA issuer =====================
+    // Tile g's Q K^T goes out ahead of tile g - 1's P V, except the first of a
+    // segment, whose queries are staged after the segment before has been read.
+    if (lane == 0 && n_tiles > 0) {
+      constexpr uint32_t idesc_qk = make_idesc(128, kTileN, kBf16, false, false);
+      constexpr uint32_t idesc_pv = make_idesc(128, D, kBf16, false, true);
+      const uint64_t qa = make_sdesc(sbase + Cfg::kOffQ, 16, 1024);
+      int n_seg = 0;   // segments whose queries have been awaited
+      auto issue_qk = [&](int g, bool first) -> bool {   // S_(g%2) = Q K_g^T
+        const int st = g % NS;
+        if (first && !mbar_wait(q_ready, n_seg++ & 1, abort_flag, p.status)) return false;
+        if (!mbar_wait(k_full(st), static_cast<uint32_t>(g / NS) & 1, abort_flag, p.status))
+          return false;
+        // S_(g%2) held P_(g-2), which P_(g-2) V_(g-2) must have read
+        if (g >= 2 && !mbar_wait(pv_done(g & 1), static_cast<uint32_t>((g - 2) >> 1) & 1,
+                                 abort_flag, p.status))
+          return false;
+        tc_fence_after();
+        const uint64_t kb = make_sdesc(sbase + Cfg::kOffK + st * Cfg::kTileBytes, 16, 1024);
+        mma_ss_product<D / 16, true, kTileM * 128, true, kTileN * 128>(tmem + (g & 1) * 128, qa, kb,
+                                                                       idesc_qk, 0);
+        tc_commit(s_full(g & 1));
+        tc_commit(k_empty(st));
+        return true;
+      };
+      seg.next(p);
+      int left = seg.n;   // tiles of the segment not yet issued
+      bool first = true;  // tile g is its segment's first
+      bool ok = true;
+#ifdef FA_WAIT_TEST
+      // wait-limit test build: nothing completes this phase before the abort
+      // path's own commit, so the wait runs out
+      ok = mbar_wait(drain, 0, abort_flag, p.status);
+#endif
+      if (ok) ok = issue_qk(0, true);
+      --left;
+      for (int g = 0; ok && g < n_tiles; ++g) {
+        const int st = g % NS;
+        const bool more = g + 1 < n_tiles, edge = left == 0;
+        if (more && !edge && !(ok = issue_qk(g + 1, false))) break;
+        if (!(ok = mbar_wait(p_full(g & 1), static_cast<uint32_t>(g >> 1) & 1, abort_flag, p.status)))
+          break;
+        if (!(ok = mbar_wait(v_full(st), static_cast<uint32_t>(g / NS) & 1, abort_flag, p.status)))
+          break;
+        tc_fence_after();
+        const uint64_t vb = make_sdesc(sbase + Cfg::kOffV + st * Cfg::kTileBytes, kTileN * 128, 1024);
+        mma_ts_product8<false, 0>(tmem + 256, tmem + (g & 1) * 128, vb, idesc_pv, first ? 0u : 1u);
+        tc_commit(pv_done(g & 1));
+        tc_commit(v_empty(st));
+        if (more && edge) {
+          seg.next(p);
+          left = seg.n;
+          if (!(ok = issue_qk(g + 1, true))) break;
+        }
+        first = edge;
+        --left;
+      }
+      if (!ok) {
+        // every MMA issued so far must finish before the TMEM is released
+        tc_commit(drain);
+        drain_wait_r(drain, 0, p.status);
+      }
+    }
+  } else {
+    // ===== row warps: stage Q, then softmax per key tile, then the write-out =====
+    const int quarter = warp & 3;               // TMEM lane quarter of this warp
+    const int r = quarter * 32 + lane;          // query-tile row
+    const bool real = r < p.R;
+    const bool busy = quarter * 32 < p.R;       // the warp holds real rows
+    const int gq = real ? r / p.Sq : 0;
+    const int s = real ? r % p.Sq : 0;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t o_tmem = tmem + lane_off + 256;
+    const float c = p.cap_in != 0.f ? 1.f : p.scale_log2;   // capped scores are in the log2 domain
+    // Stage this row of a segment's queries into the 128-byte-swizzled K-major
+    // query tile (16-byte unit u of a 128-byte row sits at unit u ^ (r % 8));
+    // rows past R are zero.
+    auto stage_q = [&](int b, int kvh) {
+      const size_t qrow = (static_cast<size_t>(b) * p.Hq + kvh * p.G + gq) * p.Sq + s;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const Elem*>(p.q) + qrow * D);
+#pragma unroll
+      for (int cc = 0; cc < Cfg::kChunks; ++cc) {
+        uint8_t* dst_row = smem + Cfg::kOffQ + cc * (kTileM * 128) + r * 128;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint4 v = real ? src[cc * 8 + u] : make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(dst_row + ((u ^ (r & 7)) << 4)) = v;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_ready);
+    };
+
+    bool more = seg.next(p);
+    if (more) stage_q(seg.b, seg.kvh);
+    bool ok = true;
+    bool head = true;   // the share's first segment
+    int g = 0;
+    while (more && ok) {
+      const int b = seg.b, kvh = seg.kvh, n = seg.n;
+      const bool whole = seg.whole;
+      const SeqKeys keys = seg.keys;
+      const int tile0 = seg.tile0;
+      const int hq = kvh * p.G + gq;
+      const int pos = keys.len - p.Sq + s;
+      // keys [row_lo, row_hi) of this row; rows past R see what any row does
+      int row_lo = keys.first, row_hi = keys.len;
+      if (real) {
+        row_hi = max(pos + 1, 0);
+        row_lo = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
+      }
+      const float bias = p.slopes ? p.slopes[hq] * (kLog2eR / c) : 0.f;
+      float m_ref = -INFINITY;   // reference max, scaled log2 domain
+      float l = 0.f;
+      for (int j = 0; j < n; ++j, ++g) {
+        const uint32_t s_tmem = tmem + lane_off + (g & 1) * 128;
+        const int kv0 = (tile0 + j) * kTileN;
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full(g & 1), static_cast<uint32_t>(g >> 1) & 1,
+                                               abort_flag, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        if (kv0 < keys.first || kv0 + kTileN > keys.len) {   // clear V rows nobody sees
+          const int st = g % NS;
+          ok = __all_sync(0xffffffffu, mbar_wait(v_full(st), static_cast<uint32_t>(g / NS) & 1,
+                                                 abort_flag, p.status));
+          if (!ok) break;
+          if (kv0 + r < keys.first || kv0 + r >= keys.len) {
+#pragma unroll
+            for (int cc = 0; cc < Cfg::kChunks; ++cc) {
+              uint4* row = reinterpret_cast<uint4*>(smem + Cfg::kOffV + st * Cfg::kTileBytes +
+                                                    cc * (kTileN * 128) + r * 128);
+#pragma unroll
+              for (int u = 0; u < 8; ++u) row[u] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        if (busy) {
+          float sc[kTileN];
+          {
+            uint32_t raw[kTileN];
+#pragma unroll
+            for (int cc = 0; cc < kTileN / 32; ++cc)
+              tmem_ld32(s_tmem + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(raw + cc * 32));
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < kTileN; ++i) sc[i] = __uint_as_float(raw[i]);
+          }
+          if (p.cap_in != 0.f) {
+#pragma unroll
+            for (int i = 0; i < kTileN; ++i)
+              sc[i] = fmaf(-2.f * p.cap_log2, cap_r(sc[i], p.cap_in), p.cap_log2);
+          }
+          if (p.slopes) {
+            const float d0 = static_cast<float>(kv0 - pos);
+#pragma unroll
+            for (int i = 0; i < kTileN; ++i)
+              sc[i] = fmaf(-bias, fabsf(d0 + static_cast<float>(i)), sc[i]);
+          }
+          if (kv0 < row_lo || kv0 + kTileN > row_hi) {
+#pragma unroll
+            for (int h = 0; h < kTileN / 32; ++h) {
+              const uint32_t w = span_bits(row_lo, row_hi, kv0 + h * 32);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((w >> i) & 1u)) sc[h * 32 + i] = -INFINITY;
+            }
+          }
+          float mx0 = sc[0], mx1 = sc[1], mx2 = sc[2], mx3 = sc[3];
+#pragma unroll
+          for (int i = 4; i < kTileN; i += 4) {
+            mx0 = fmaxf(mx0, sc[i]);
+            mx1 = fmaxf(mx1, sc[i + 1]);
+            mx2 = fmaxf(mx2, sc[i + 2]);
+            mx3 = fmaxf(mx3, sc[i + 3]);
+          }
+          const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * c;
+          float m_new = m_ref;
+          if (mx > m_ref + kRescaleThresholdR) m_new = mx;
+          const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
+          const float alpha = ex2(m_ref - m_use);   // 0 when m_ref = -inf
+          const bool moved = (m_new != m_ref);
+          m_ref = m_new;
+
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t pk[32];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float p0 = ex2(fmaf(sc[h * 64 + 2 * i], c, -m_use));
+              const float p1 = ex2(fmaf(sc[h * 64 + 2 * i + 1], c, -m_use));
+              sum[(2 * i) & 3] += p0;
+              sum[(2 * i + 1) & 3] += p1;
+              pk[i] = pack2<kBf16>(p0, p1);
+            }
+            tmem_st32(s_tmem + h * 32, pk);
+          }
+          l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+
+          // O <- alpha * O for rows whose reference max moved (the segment's
+          // first P V overwrites O)
+          if (j > 0 && __any_sync(0xffffffffu, moved)) {
+            ok = __all_sync(0xffffffffu, mbar_wait(pv_done((g - 1) & 1),
+                                                   static_cast<uint32_t>((g - 1) >> 1) & 1,
+                                                   abort_flag, p.status));
+            if (!ok) break;
+            tc_fence_after();
+            const float a = moved ? alpha : 1.f;
+#pragma unroll
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t o[32];
+              tmem_ld32(o_tmem + cc * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+              tmem_st32(o_tmem + cc * 32, o);
+            }
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(g & 1));
+      }
+      if (!ok) break;
+      // the next segment's queries (every Q K^T of this one has been read), then
+      // this segment's result
+      more = seg.next(p);
+      if (more) stage_q(seg.b, seg.kvh);
+      if (busy) {
+        ok = __all_sync(0xffffffffu, mbar_wait(pv_done((g - 1) & 1),
+                                               static_cast<uint32_t>((g - 1) >> 1) & 1, abort_flag,
+                                               p.status));
+        if (!ok) break;
+        tc_fence_after();
+        // a row that sees no key of this range contributes weight 0 to the merge
+        const float inv_l = l > 0.f ? 1.f / l : 0.f;
+        const float lse2 = l > 0.f ? m_ref + __log2f(l) : -INFINITY;
+        const size_t qrow = (static_cast<size_t>(b) * p.Hq + hq) * p.Sq + s;
+        const size_t prow = (static_cast<size_t>(cta) * 2 + (head ? 0 : 1)) * p.R + r;
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(o_tmem + cc * 32, o);
+          tmem_wait_ld();
+          if (!real) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<Elem*>(p.out) + qrow * D + cc * 32);
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              dst[v] = make_uint4(
+                  pack2<kBf16>(__uint_as_float(o[8 * v]) * inv_l, __uint_as_float(o[8 * v + 1]) * inv_l),
+                  pack2<kBf16>(__uint_as_float(o[8 * v + 2]) * inv_l, __uint_as_float(o[8 * v + 3]) * inv_l),
+                  pack2<kBf16>(__uint_as_float(o[8 * v + 4]) * inv_l, __uint_as_float(o[8 * v + 5]) * inv_l),
+                  pack2<kBf16>(__uint_as_float(o[8 * v + 6]) * inv_l, __uint_as_float(o[8 * v + 7]) * inv_l));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(p.part_out + prow * D + cc * 32);
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv_l, __uint_as_float(o[4 * v + 1]) * inv_l,
+                                   __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
+          }
+        }
+        if (real && whole) p.lse[qrow] = lse2 * kLn2R;
+        if (real && !whole) p.part_lse2[prow] = lse2;
+        tc_fence_before();
+      }
+      head = false;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ merge --
+// One warp per output row (b, hq, s); each lane owns d / 32 columns. Joins the
+// parts of rows whose tiles lie in more than one share, in share order, as the
+// split-KV merge does; writes out = 0, LSE = -inf for sequences without keys;
+// leaves rows that one segment wrote whole alone.
+template <int PER>
+struct alignas(4 * PER) PartVec { float x[PER]; };
+
+template <typename T, int PER>
+__global__ void __launch_bounds__(256) ragged_merge_kernel(const __grid_constant__ RaggedParams p) {
+  // programmatic dependent of the ragged kernel: wait until that grid has
+  // completed and its results are visible
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int D = 32 * PER;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long row = static_cast<long long>(blockIdx.x) * 8 + warp;   // (b * Hq + hq) * Sq + s
+  if (row >= static_cast<long long>(p.B) * p.Hq * p.Sq) return;
+  const int s = static_cast<int>(row % p.Sq);
+  const long long bh = row / p.Sq;
+  const int hq = static_cast<int>(bh % p.Hq), b = static_cast<int>(bh / p.Hq);
+  const long long pre = p.prefix[b], nt = p.prefix[b + 1] - pre;
+  T* dst = static_cast<T*>(p.out) + row * D + lane * PER;
+  if (nt == 0) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) dst[e] = static_cast<T>(0.f);
+    if (lane == 0) p.lse[row] = -INFINITY;
+    return;
+  }
+  const long long total = p.prefix[p.B] * p.Hkv;
+  const long long t0 = pre * p.Hkv + static_cast<long long>(hq / p.G) * nt;
+  // share c holds tile t iff total c / n <= t < total (c + 1) / n (rounded down)
+  const int shares = n_shares(p, total);
+  const int c0 = static_cast<int>(((t0 + 1) * shares - 1) / total);
+  const int c1 = static_cast<int>(((t0 + nt) * shares - 1) / total);
+  if (c0 == c1) return;
+  const int r = (hq % p.G) * p.Sq + s;
+  // the parts are the first segments of their shares, but for that of c0 when
+  // its share begins before this head's tiles
+  const bool tail0 = share_begin(total, c0, shares) < t0;
+  auto part = [&](int c) {
+    return (static_cast<size_t>(c) * 2 + ((c == c0 && tail0) ? 1 : 0)) * p.R + r;
+  };
+  float M = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_lse2[part(c)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float acc[PER], L = 0.f;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+#pragma unroll 8
+  for (int c = c0; c <= c1; ++c) {
+    const size_t at = part(c);
+    const float w = M != -INFINITY ? ex2(p.part_lse2[at] - M) : 0.f;
+    const PartVec<PER> v = reinterpret_cast<const PartVec<PER>*>(p.part_out + at * D)[lane];
+    L += w;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v.x[e], acc[e]);
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) dst[e] = static_cast<T>(acc[e] * inv);
+  if (lane == 0) p.lse[row] = L > 0.f ? (M + __log2f(L)) * kLn2R : -INFINITY;
+}
+
+template <int D, bool kBf16>
+cudaError_t launch_ragged_impl(const RaggedParams& p, cudaStream_t stream) {
+  constexpr int smem = RagCfg<D>::kSmemBytes;
+  using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
+  auto kernel = fa_ragged_kernel<D, kBf16>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<static_cast<unsigned>(p.n_ctas), kThreads, smem, stream>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // the merge overlaps its launch with the ragged kernel's tail
+  const long long rows = static_cast<long long>(p.B) * p.Hq * p.Sq;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, ragged_merge_kernel<Elem, D / 32>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_ragged(const RaggedParams& p, int d, bool bf16, cudaStream_t stream) {
+  if (d == 128)
+    return bf16 ? launch_ragged_impl<128, true>(p, stream) : launch_ragged_impl<128, false>(p, stream);
+  return bf16 ? launch_ragged_impl<64, true>(p, stream) : launch_ragged_impl<64, false>(p, stream);
+}
+
+}  // namespace fa

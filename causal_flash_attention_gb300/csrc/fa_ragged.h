@@ -1,0 +1,34 @@
+// Internal interface of the ragged paged decode (fa_fwd_ragged_paged): sequences
+// of unequal length over a paged key/value cache. Not installed.
+#pragma once
+
+#include "fa_internal.h"
+
+namespace fa {
+
+// Work is the list of all key tiles: for every sequence b, for every key/value
+// head, the nt_b tiles of 128 keys that its new rows see. CTA c of
+// the first n = min(n_ctas, total) takes tiles [total c / n, total (c + 1) / n).
+struct RaggedParams {
+  CUtensorMap tm_k;   // [num_blocks*Hkv][block_size][d], box (64, box_rows, 1), 128B swizzle
+  CUtensorMap tm_v;
+  const void* q;      // [B*Hq][Sq][d]
+  void* out;          // [B*Hq][Sq][d]
+  float* lse;         // [B*Hq][Sq]
+  const int* block_table;   // [B][max_blocks]
+  const int* seq_lens;      // [B]
+  const float* slopes;      // [Hq] or null
+  float* part_out;    // [2 * CTAs][R][d] fp32 out = O / l of a part of a (sequence, head)
+  float* part_lse2;   // [2 * CTAs][R]    its log2-sum-exp2 of scaled scores
+  long long* prefix;  // [B + 1] tiles per head before sequence b, written by CTA 0
+  int B, Hq, Hkv, Sq, G, R;
+  int block_size, box_rows, max_blocks, num_blocks;
+  int window;         // keys a row sees, its own position included; 0: all
+  float scale_log2, cap_in, cap_log2;   // as ScoreMod
+  int n_ctas;
+  int* status;
+};
+
+cudaError_t launch_ragged(const RaggedParams& p, int d, bool bf16, cudaStream_t stream);
+
+}  // namespace fa

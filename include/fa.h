@@ -206,6 +206,48 @@ int fa_fwd_splitkv_paged(const void* q, const void* k_cache, const void* v_cache
                          size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * One or a few new tokens of each of B sequences of unequal length over a
+ * paged key/value cache. k_cache, v_cache, block_table, q, out and lse are laid
+ * out as for fa_fwd_splitkv_paged; seq_lens: [B] int32 in device memory, the
+ * keys of each sequence with its Sq new tokens included (values below 0 count
+ * as 0, values above max_blocks * block_size as that). Row s of sequence b
+ * stands at position p = seq_lens[b] - Sq + s and sees keys
+ *
+ *   max(0, p + 1 - window) <= j <= p        (window 0: from key 0),
+ *
+ * with scores capped and biased as by fa_fwd_span (distance p - j). A row that
+ * sees no key (p < 0) gets out = 0 and lse = -infinity.
+ *
+ * The lengths are read on the device only: the call needs no host copy of
+ * them, and a captured graph may be replayed after they change. All key tiles
+ * of all sequences are shared out evenly over one wave of CTAs whatever the
+ * lengths are. Results are the same bits on every call.
+ *
+ * Only table entries of pages that hold a key some row sees are read; an entry
+ * outside [0, num_blocks) reads as zeros. The rest of the cache, rows of a
+ * sequence's last page past its length included, may hold anything.
+ *
+ * G * Sq <= 128 with G = Hq / Hkv, block_size as for fa_fwd_splitkv_paged,
+ * max_blocks >= 1 and window >= 0 (else FA_ERR_SHAPE); softcap finite and >= 0
+ * (else FA_ERR_SCALE); FA_BF16 and FA_F16 only (FA_F32 gives FA_ERR_DTYPE).
+ * workspace: caller-owned, at least fa_fwd_ragged_paged_workspace_bytes(...)
+ * bytes, 256-byte aligned, contents on entry without meaning; calls that may
+ * overlap on the GPU need one each.
+ */
+int fa_fwd_ragged_paged(const void* q, const void* k_cache, const void* v_cache,
+                        const int* block_table, const int* seq_lens, void* out, float* lse,
+                        int B, int Hq, int Hkv, int Sq, int d, int block_size, int num_blocks,
+                        int max_blocks, int window, float scale, float softcap,
+                        const float* slopes, int dtype, void* workspace,
+                        size_t workspace_bytes, fa_stream_t stream);
+
+/* Workspace bytes of fa_fwd_ragged_paged: two partial results of G * Sq rows of
+ * d + 1 floats for each of at most 152 CTAs, and B + 1 64-bit sums, each region
+ * 256-byte aligned. Returns 0 for invalid sizes. */
+size_t fa_fwd_ragged_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int d,
+                                           int block_size, int max_blocks);
+
+/*
  * Attention in which every query row sees its own contiguous range of keys,
  * for packed documents, sliding windows, prefixes seen by all, and padding:
  * row i of batch b sees keys j with
