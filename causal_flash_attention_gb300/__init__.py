@@ -31,12 +31,21 @@ __all__ = [
     "decode_forward", "fa_fwd_splitkv_paged", "decode_forward_paged",
     "fa_fwd_span", "fa_bwd_span", "fa_bwd_span_workspace_bytes", "attention_span_forward",
     "attention_span_backward", "key_spans", "fa_fwd_ragged_paged",
-    "fa_fwd_ragged_paged_workspace_bytes", "decode_forward_ragged",
+    "fa_fwd_ragged_paged_workspace_bytes", "decode_forward_ragged", "fa_qk_norm_rope",
+    "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_bytes", "fa_qk_norm_rope_append",
+    "qk_norm_rope_forward", "qk_norm_rope_backward", "qk_norm_rope_append", "rope_inv_freq",
+    "rope_turns", "decode_step_ragged",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa.so")
 DTYPE_CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _lib = None
+
+
+class _View(ctypes.Structure):
+    """fa_view: a strided [B, H, S, d] tensor whose last dimension is contiguous."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_longlong),
+                ("stride_h", ctypes.c_longlong), ("stride_s", ctypes.c_longlong)]
 
 
 class FAError(RuntimeError):
@@ -83,6 +92,17 @@ def lib() -> ctypes.CDLL:
     L.fa_fwd_ragged_paged.restype = i32
     L.fa_fwd_ragged_paged_workspace_bytes.argtypes = [i32] * 7
     L.fa_fwd_ragged_paged_workspace_bytes.restype = sz
+    vw = ctypes.POINTER(_View)
+    L.fa_qk_norm_rope.argtypes = [vw] * 4 + [vp, vp, f32, vp, vp, i32, i32, f32] + [i32] * 6 + [vp]
+    L.fa_qk_norm_rope.restype = i32
+    L.fa_qk_norm_rope_bwd.argtypes = ([vw] * 6 + [vp] * 4 + [f32, vp, vp, i32, i32, f32]
+                                      + [i32] * 6 + [vp, sz, vp])
+    L.fa_qk_norm_rope_bwd.restype = i32
+    L.fa_qk_norm_rope_bwd_workspace_bytes.argtypes = [i32] * 4
+    L.fa_qk_norm_rope_bwd_workspace_bytes.restype = sz
+    L.fa_qk_norm_rope_append.argtypes = ([vw] * 4 + [vp] * 6 + [f32, vp, i32, i32, f32]
+                                         + [i32] * 9 + [vp])
+    L.fa_qk_norm_rope_append.restype = i32
     L.fa_strerror.argtypes = [i32]
     L.fa_strerror.restype = ctypes.c_char_p
     L.fa_last_device_status.argtypes = [vp, ctypes.POINTER(i32)]
@@ -559,6 +579,224 @@ def decode_forward_ragged(q, k_cache, v_cache, block_table, seq_lens, window=0, 
     fa_fwd_ragged_paged(q, k_cache, v_cache, block_table, seq_lens, out, lse, ws, window, softcap,
                         slopes, scale, stream)
     return out, lse
+
+
+# ------------------------------------------------ query / key preparation --
+def rope_inv_freq(rope_dim, base=10000.0, scaling="none", factor=1.0, trained_len=8192,
+                  low_turns=1.0, high_turns=32.0):
+    """Rotary frequencies (float64 [rope_dim / 2], radians a position) and the rope_scale that
+    goes with them, as (inv_freq, rope_scale). `scaling` stretches a trained context of
+    trained_len positions by `factor`:
+
+    none    base^(-2i / rope_dim)
+    linear  all frequencies divided by factor (positions interpolated)
+    base    the base raised so that the slowest frequency is divided by factor
+    parts   YaRN (Peng et al., 2023): frequencies that turn more than high_turns times within
+            trained_len stay, those that turn less than low_turns times are divided by factor,
+            linear in between; rope_scale = 0.1 ln(factor) + 1
+    """
+    if rope_dim < 2 or rope_dim % 2:
+        raise ValueError("rope_dim must be even and positive")
+    if not (factor >= 1.0 and base > 1.0):
+        raise ValueError("factor must be >= 1 and base > 1")
+    if scaling == "base" and rope_dim > 2:
+        base = base * factor ** (rope_dim / (rope_dim - 2))
+    f = base ** (-torch.arange(0, rope_dim, 2, dtype=torch.float64) / rope_dim)
+    if scaling in ("none", "base"):
+        return f, 1.0
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling == "parts":
+        n = f * trained_len / (2 * math.pi)
+        keep = ((n - low_turns) / (high_turns - low_turns)).clamp(0.0, 1.0)
+        return f * (keep + (1 - keep) / factor), 0.1 * math.log(factor) + 1.0
+    raise ValueError(f"unknown scaling {scaling!r}")
+
+
+def rope_turns(inv_freq, device=None):
+    """The table the rotary calls take: int64 [rope_dim / 2], the frequencies (radians a
+    position) as turns a position in units of 2^-64, modulo a turn."""
+    f = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").reshape(-1)
+    out = []
+    for x in f.tolist():
+        if not math.isfinite(x):
+            raise ValueError("frequencies must be finite")
+        u = int(round(math.fmod(x / (2 * math.pi), 1.0) * 2.0 ** 64)) % (1 << 64)
+        out.append(u - (1 << 64) if u >= 1 << 63 else u)   # the same bits, signed
+    return torch.tensor(out, dtype=torch.int64, device=device)
+
+
+def _views(B, S, d, like, **named):
+    """fa_view arguments from name=(tensor, H); None stays None."""
+    out = []
+    for name, (t, H) in named.items():
+        if t is None:
+            out.append(None)
+            continue
+        if t.device != like.device or t.dtype != like.dtype:
+            raise ValueError(f"{name} must be {like.dtype} on {like.device}")
+        if tuple(t.shape) != (B, H, S, d):
+            raise ValueError(f"{name} must be {(B, H, S, d)}, not {tuple(t.shape)}")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name}: the elements of a head must be contiguous")
+        # a dimension of one row has no stride to keep aligned
+        sb, sh, ss = (0 if n == 1 else st for n, st in zip(t.shape[:3], t.stride()[:3]))
+        out.append(ctypes.byref(_View(t.data_ptr(), sb, sh, ss)))
+    return out
+
+
+def _heads_dims(q, k, turns, positions, q_weight, k_weight):
+    _check_cuda(q)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q [B,Hq,S,d] and k [B,Hkv,S,d] (any strides but the last)")
+    B, Hq, S, d = (int(x) for x in q.shape)
+    n = 0 if turns is None else int(turns.numel())
+    _check_like(q, q.dtype, turns=(turns, (n,), torch.int64),
+                positions=(positions, (B, S), torch.int32), q_weight=(q_weight, (d,), None),
+                k_weight=(k_weight, (d,), None))
+    return B, Hq, int(k.shape[1]), S, d, 2 * n
+
+
+def _check_no_overlap(name, t):
+    """An output view whose elements would share memory cannot be written."""
+    dims = sorted((st, n) for n, st in zip(t.shape, t.stride()) if n > 1)
+    reach = 0
+    for st, n in dims:
+        if st <= reach:
+            raise ValueError(f"{name}: elements overlap in memory")
+        reach += st * (n - 1)
+
+
+def fa_qk_norm_rope(q, k, q_out, k_out, turns, positions=None, q_weight=None, k_weight=None,
+                    eps=1e-6, interleaved=False, rope_scale=1.0, stream=None):
+    """Call fa_qk_norm_rope on views q, q_out [B,Hq,S,d] and k, k_out [B,Hkv,S,d] (any strides
+    but the last); turns as from rope_turns (rope_dim = 2 * its length; None: no rotation);
+    positions int32 [B,S] or None (row s at position s); both weights [d] or neither."""
+    B, Hq, Hkv, S, d, rope_dim = _heads_dims(q, k, turns, positions, q_weight, k_weight)
+    views = _views(B, S, d, q, q=(q, Hq), k=(k, Hkv), q_out=(q_out, Hq), k_out=(k_out, Hkv))
+    _check_no_overlap("q_out", q_out)
+    _check_no_overlap("k_out", k_out)
+    with _on_device(q):
+        rc = lib().fa_qk_norm_rope(*views, _ptr(q_weight), _ptr(k_weight), float(eps),
+                                   _ptr(positions), _ptr(turns), rope_dim, int(bool(interleaved)),
+                                   float(rope_scale), B, Hq, Hkv, S, d,
+                                   DTYPE_CODES.get(q.dtype, -1), _stream(stream, q))
+    if rc != 0:
+        raise FAError(rc, "fa_qk_norm_rope")
+
+
+def fa_qk_norm_rope_bwd_workspace_bytes(B, S, d, norm=True) -> int:
+    return int(lib().fa_qk_norm_rope_bwd_workspace_bytes(B, S, d, int(bool(norm))))
+
+
+def fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, dq_weight, dk_weight, workspace, turns,
+                        positions=None, q_weight=None, k_weight=None, eps=1e-6,
+                        interleaved=False, rope_scale=1.0, stream=None):
+    """Call fa_qk_norm_rope_bwd: views as for fa_qk_norm_rope; dq_weight, dk_weight float32 [d]
+    and `workspace` (fa_qk_norm_rope_bwd_workspace_bytes bytes) with weights, else None."""
+    B, Hq, Hkv, S, d, rope_dim = _heads_dims(dq_out, dk_out, turns, positions, q_weight, k_weight)
+    views = _views(B, S, d, dq_out, dq_out=(dq_out, Hq), dk_out=(dk_out, Hkv), q=(q, Hq),
+                   k=(k, Hkv), dq=(dq, Hq), dk=(dk, Hkv))
+    _check_no_overlap("dq", dq)
+    _check_no_overlap("dk", dk)
+    _check_like(dq_out, torch.float32, dq_weight=(dq_weight, (d,), None),
+                dk_weight=(dk_weight, (d,), None))
+    with _on_device(dq_out):
+        rc = lib().fa_qk_norm_rope_bwd(*views, _ptr(dq_weight), _ptr(dk_weight), _ptr(q_weight),
+                                       _ptr(k_weight), float(eps), _ptr(positions), _ptr(turns),
+                                       rope_dim, int(bool(interleaved)), float(rope_scale), B, Hq,
+                                       Hkv, S, d, DTYPE_CODES.get(dq_out.dtype, -1),
+                                       _ptr(workspace), _workspace_bytes(workspace, dq_out),
+                                       _stream(stream, dq_out))
+    if rc != 0:
+        raise FAError(rc, "fa_qk_norm_rope_bwd")
+
+
+def fa_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, block_table, seq_lens, turns,
+                           q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                           rope_scale=1.0, stream=None):
+    """Call fa_qk_norm_rope_append: the last Sq tokens of sequences of seq_lens tokens; views q,
+    q_out [B,Hq,Sq,d], k, v [B,Hkv,Sq,d]; caches [num_blocks,Hkv,block_size,d] written in place."""
+    B, Hq, Hkv, Sq, d, rope_dim = _heads_dims(q, k, turns, None, q_weight, k_weight)
+    views = _views(B, Sq, d, q, q=(q, Hq), k=(k, Hkv), v=(v, Hkv), q_out=(q_out, Hq))
+    _check_no_overlap("q_out", q_out)
+    if k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("caches [num_blocks,Hkv,block_size,d], table [B,max_blocks]")
+    num_blocks, block_size, max_blocks = k_cache.shape[0], k_cache.shape[2], block_table.shape[1]
+    cache = (num_blocks, Hkv, block_size, d)
+    _check_like(q, q.dtype, k_cache=(k_cache, cache, None), v_cache=(v_cache, cache, None),
+                block_table=(block_table, (B, max_blocks), torch.int32),
+                seq_lens=(seq_lens, (B,), torch.int32))
+    with _on_device(q):
+        rc = lib().fa_qk_norm_rope_append(*views, _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
+                                          _ptr(seq_lens), _ptr(q_weight), _ptr(k_weight),
+                                          float(eps), _ptr(turns), rope_dim,
+                                          int(bool(interleaved)), float(rope_scale), B, Hq, Hkv,
+                                          Sq, d, block_size, num_blocks, max_blocks,
+                                          DTYPE_CODES.get(q.dtype, -1), _stream(stream, q))
+    if rc != 0:
+        raise FAError(rc, "fa_qk_norm_rope_append")
+
+
+def qk_norm_rope_forward(q, k, turns, positions=None, q_weight=None, k_weight=None, eps=1e-6,
+                         interleaved=False, rope_scale=1.0, stream=None):
+    """Allocate contiguous q_out [B,Hq,S,d] and k_out [B,Hkv,S,d] (as the attention calls take
+    them) and run fa_qk_norm_rope. Returns (q_out, k_out)."""
+    _check_cuda(q)
+    with _alloc_stream(stream, q):
+        q_out, k_out = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k))
+    fa_qk_norm_rope(q, k, q_out, k_out, turns, positions, q_weight, k_weight, eps, interleaved,
+                    rope_scale, stream)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, turns, positions=None, q_weight=None,
+                          k_weight=None, eps=1e-6, interleaved=False, rope_scale=1.0, dq=None,
+                          dk=None, stream=None):
+    """Allocate dq, dk (unless given, e.g. as views of a packed gradient; else laid out
+    [B, S, H, d] in memory, as projections give q and k) and, with weights, the float32 weight
+    gradients, and run fa_qk_norm_rope_bwd. Returns (dq, dk, dq_weight, dk_weight), the last two
+    None without weights. Without weights q and k are not read and may be None."""
+    _check_cuda(dq_out, "dq_out")
+    B, _, S, d = dq_out.shape
+    norm = q_weight is not None
+    dwq = dwk = ws = None
+    with _alloc_stream(stream, dq_out):
+        def grad(t):
+            return torch.empty(B, S, t.shape[1], d, dtype=t.dtype, device=t.device).transpose(1, 2)
+        dq = grad(dq_out) if dq is None else dq
+        dk = grad(dk_out) if dk is None else dk
+        if norm:
+            dwq, dwk = torch.empty(2, d, dtype=torch.float32, device=dq_out.device)
+            ws = torch.empty(fa_qk_norm_rope_bwd_workspace_bytes(B, S, d), dtype=torch.uint8,
+                             device=dq_out.device)
+    fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, dwq, dwk, ws, turns, positions, q_weight,
+                        k_weight, eps, interleaved, rope_scale, stream)
+    return dq, dk, dwq, dwk
+
+
+def qk_norm_rope_append(q, k, v, k_cache, v_cache, block_table, seq_lens, turns, q_weight=None,
+                        k_weight=None, eps=1e-6, interleaved=False, rope_scale=1.0, stream=None):
+    """Allocate q_out (contiguous [B,Hq,Sq,d]) and run fa_qk_norm_rope_append, which writes the
+    tokens' keys and values into the caches. Returns q_out."""
+    _check_cuda(q)
+    with _alloc_stream(stream, q):
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    fa_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, block_table, seq_lens, turns,
+                           q_weight, k_weight, eps, interleaved, rope_scale, stream)
+    return q_out
+
+
+def decode_step_ragged(q, k, v, k_cache, v_cache, block_table, seq_lens, turns, q_weight=None,
+                       k_weight=None, eps=1e-6, interleaved=False, rope_scale=1.0, window=0,
+                       softcap=0.0, slopes=None, scale=None, stream=None):
+    """One attention step of a serving loop: qk_norm_rope_append of the new tokens' projections
+    q [B,Hq,Sq,d], k, v [B,Hkv,Sq,d], then decode_forward_ragged over the cache with them.
+    seq_lens counts the new tokens. Returns (out, lse)."""
+    q = qk_norm_rope_append(q, k, v, k_cache, v_cache, block_table, seq_lens, turns, q_weight,
+                            k_weight, eps, interleaved, rope_scale, stream)
+    return decode_forward_ragged(q, k_cache, v_cache, block_table, seq_lens, window, softcap,
+                                 slopes, scale, stream)
 
 
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024   # FA_NOALLOC_SCRATCH_BYTES in include/fa.h

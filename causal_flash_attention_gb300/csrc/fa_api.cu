@@ -7,9 +7,11 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 
 #include "../../include/fa.h"
 #include "fa_decode.h"
+#include "fa_heads.h"
 #include "fa_internal.h"
 #include "fa_ragged.h"
 
@@ -203,11 +205,60 @@ RaggedPlan ragged_plan(int B, int Hq, int Hkv, int Sq, int d, int block_size, in
   return rp;
 }
 
-// Sizes of a paged cache and of few query rows against it.
+// Sizes of a paged cache, and of few query rows against it.
+bool block_sizes_ok(int Hkv, int block_size, int num_blocks, int max_blocks) {
+  return block_size >= 16 && block_size <= 1024 && (block_size & (block_size - 1)) == 0 &&
+         num_blocks >= 1 && static_cast<long long>(num_blocks) * Hkv <= (1LL << 30) &&
+         max_blocks >= 1;
+}
 bool paged_sizes_ok(int Hq, int Hkv, int Sq, int block_size, int num_blocks, int max_blocks) {
-  return static_cast<long long>(Hq / Hkv) * Sq <= kDecodeMaxRows && block_size >= 16 &&
-         block_size <= 1024 && (block_size & (block_size - 1)) == 0 && num_blocks >= 1 &&
-         static_cast<long long>(num_blocks) * Hkv <= (1LL << 30) && max_blocks >= 1;
+  return static_cast<long long>(Hq / Hkv) * Sq <= kDecodeMaxRows &&
+         block_sizes_ok(Hkv, block_size, num_blocks, max_blocks);
+}
+
+// Arguments the query/key preparation entry points share.
+int heads_params(HeadsParams& p, const void* wq, const void* wk, float eps, const int* positions,
+                 const unsigned long long* turns, int rope_dim, int interleaved, float rope_scale,
+                 int B, int Hq, int Hkv, int S, int d, int dtype) {
+  int rc = check_common(B, Hq, Hkv, S, S, d, 0, 1.f, dtype);
+  if (rc != FA_OK) return rc;
+  if (rope_dim < 0 || rope_dim > d || rope_dim % 16 != 0 || Hq > (1 << 20) ||
+      static_cast<long long>(B) * S > (1LL << 33))
+    return FA_ERR_SHAPE;
+  if (!std::isfinite(rope_scale) || (wq && !(std::isfinite(eps) && eps >= 0.f)))
+    return FA_ERR_SCALE;
+  if ((rope_dim > 0 && !turns) || (wq == nullptr) != (wk == nullptr)) return FA_ERR_NULL;
+  if (!aligned16(wq) || !aligned16(wk) || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(turns) & 7u) != 0)
+    return FA_ERR_ALIGN;
+  p.wq = wq;
+  p.wk = wk;
+  p.positions = positions;
+  p.turns = reinterpret_cast<const uint64_t*>(turns);
+  p.eps = eps;
+  p.rope_scale = rope_scale;
+  p.rope_dim = rope_dim;
+  p.interleaved = interleaved != 0;
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.S = S; p.d = d; p.dtype = dtype;
+  return FA_OK;
+}
+
+// Strided views: every head starts on a 16-byte boundary.
+struct ViewArg {
+  const fa_view* from;
+  HeadView* to;
+};
+int take_views(std::initializer_list<ViewArg> views, int dtype) {
+  const long long step = dtype == FA_F32 ? 4 : 8;   // elements in 16 bytes
+  for (const ViewArg& v : views)
+    if (!v.from || !v.from->data) return FA_ERR_NULL;
+  for (const ViewArg& v : views) {
+    if (!aligned16(v.from->data) || v.from->stride_b % step != 0 || v.from->stride_h % step != 0 ||
+        v.from->stride_s % step != 0)
+      return FA_ERR_ALIGN;
+    *v.to = HeadView{v.from->data, v.from->stride_b, v.from->stride_h, v.from->stride_s};
+  }
+  return FA_OK;
 }
 
 // Arguments the span entry points add.
@@ -605,6 +656,81 @@ int fa_fwd_splitkv_paged(const void* q, const void* k_cache, const void* v_cache
   return splitkv_impl(q, k_cache, v_cache, out, lse, B, Hq, Hkv, Sq, Skv, d, causal, scale, dtype,
                       n_splits, workspace, workspace_bytes, stream, block_table, block_size,
                       max_blocks, num_blocks);
+}
+
+int fa_qk_norm_rope(const fa_view* q, const fa_view* k, const fa_view* q_out, const fa_view* k_out,
+                    const void* q_weight, const void* k_weight, float eps, const int* positions,
+                    const unsigned long long* turns, int rope_dim, int interleaved,
+                    float rope_scale, int B, int Hq, int Hkv, int S, int d, int dtype,
+                    fa_stream_t stream) {
+  HeadsParams p{};
+  int rc = heads_params(p, q_weight, k_weight, eps, positions, turns, rope_dim, interleaved,
+                        rope_scale, B, Hq, Hkv, S, d, dtype);
+  if (rc == FA_OK) rc = take_views({{q, &p.q}, {k, &p.k}, {q_out, &p.q_out}, {k_out, &p.k_out}}, dtype);
+  if (rc != FA_OK) return rc;
+  return launch_heads_fwd(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
+                                                                                    : FA_ERR_CUDA;
+}
+
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int S, int d, int norm) {
+  if (B < 1 || S < 1 || (d != 64 && d != 128) || !norm) return 0;
+  return static_cast<size_t>(heads_bwd_blocks(B, S)) * 2 * d * 4;
+}
+
+int fa_qk_norm_rope_bwd(const fa_view* dq_out, const fa_view* dk_out, const fa_view* q,
+                        const fa_view* k, const fa_view* dq, const fa_view* dk, float* dq_weight,
+                        float* dk_weight, const void* q_weight, const void* k_weight, float eps,
+                        const int* positions, const unsigned long long* turns, int rope_dim,
+                        int interleaved, float rope_scale, int B, int Hq, int Hkv, int S, int d,
+                        int dtype, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  HeadsParams p{};
+  int rc = heads_params(p, q_weight, k_weight, eps, positions, turns, rope_dim, interleaved,
+                        rope_scale, B, Hq, Hkv, S, d, dtype);
+  if (rc == FA_OK)
+    rc = take_views({{dq_out, &p.q_out}, {dk_out, &p.k_out}, {dq, &p.dq}, {dk, &p.dk}}, dtype);
+  if (rc != FA_OK) return rc;
+  p.n_blocks = heads_bwd_blocks(B, S);
+  if (q_weight) {
+    if ((rc = take_views({{q, &p.q}, {k, &p.k}}, dtype)) != FA_OK) return rc;
+    if (!dq_weight || !dk_weight) return FA_ERR_NULL;
+    if (((reinterpret_cast<uintptr_t>(dq_weight) | reinterpret_cast<uintptr_t>(dk_weight)) & 3u) != 0)
+      return FA_ERR_ALIGN;
+    if (!workspace || workspace_bytes < fa_qk_norm_rope_bwd_workspace_bytes(B, S, d, 1))
+      return FA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_ALIGN;
+    p.dwq = dq_weight;
+    p.dwk = dk_weight;
+    p.dw_part = static_cast<float*>(workspace);
+  }
+  return launch_heads_bwd(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
+                                                                                    : FA_ERR_CUDA;
+}
+
+int fa_qk_norm_rope_append(const fa_view* q, const fa_view* k, const fa_view* v,
+                           const fa_view* q_out, void* k_cache, void* v_cache,
+                           const int* block_table, const int* seq_lens, const void* q_weight,
+                           const void* k_weight, float eps, const unsigned long long* turns,
+                           int rope_dim, int interleaved, float rope_scale, int B, int Hq, int Hkv,
+                           int Sq, int d, int block_size, int num_blocks, int max_blocks,
+                           int dtype, fa_stream_t stream) {
+  HeadsParams p{};
+  int rc = heads_params(p, q_weight, k_weight, eps, nullptr, turns, rope_dim, interleaved,
+                        rope_scale, B, Hq, Hkv, Sq, d, dtype);
+  if (rc != FA_OK) return rc;
+  if (!block_sizes_ok(Hkv, block_size, num_blocks, max_blocks)) return FA_ERR_SHAPE;
+  if ((rc = take_views({{q, &p.q}, {k, &p.k}, {v, &p.v}, {q_out, &p.q_out}}, dtype)) != FA_OK)
+    return rc;
+  if (!k_cache || !v_cache || !block_table || !seq_lens) return FA_ERR_NULL;
+  if (!aligned16(k_cache) || !aligned16(v_cache) ||
+      ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(seq_lens)) & 3u) != 0)
+    return FA_ERR_ALIGN;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.block_size = block_size; p.num_blocks = num_blocks; p.max_blocks = max_blocks;
+  return launch_heads_append(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK : FA_ERR_CUDA;
 }
 
 int fa_fwd_span(const void* q, const void* k, const void* v, const int* key_begin,

@@ -206,6 +206,85 @@ int fa_fwd_splitkv_paged(const void* q, const void* k_cache, const void* v_cache
                          size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * A strided view [B][H][S][d]: element (b, h, s, e) is at
+ * data[b * stride_b + h * stride_h + s * stride_s + e] (strides in elements, of
+ * any sign; data and every stride a multiple of 16 bytes, else FA_ERR_ALIGN).
+ * A packed projection [B][S][Hq + 2 Hkv][d] is three such views.
+ */
+typedef struct {
+  void* data;
+  long long stride_b, stride_h, stride_s;
+} fa_view;
+
+/*
+ * Queries and keys for the attention calls: an RMS norm of every head, then
+ * rotary positions, in one pass. For each row x (d elements) of q and of k:
+ *
+ *   n = x * (mean_e x_e^2 + eps)^(-1/2) * weight       (both weights NULL: n = x)
+ *   y_a = rope_scale * (cos t * n_a - sin t * n_b)
+ *   y_b = rope_scale * (sin t * n_a + cos t * n_b)
+ *
+ * for the pairs i < rope_dim / 2 of the first rope_dim elements, (a, b) =
+ * (i, i + rope_dim / 2), or (2i, 2i + 1) with interleaved != 0; y = n in the rest
+ * of the head. The angle t is the row's position times the pair's frequency:
+ * turns[i] is that frequency in units of 2^-64 of a turn per position
+ * (frequency in radians / (2 pi) * 2^64, modulo 2^64), so angles are exact
+ * modulo a turn at every int32 position. positions: [B][S] int32, or NULL for
+ * position s at row s. Arithmetic is in fp32; y is rounded once.
+ *
+ * q, q_out have Hq heads, k, k_out Hkv, all S rows of d elements. FA_F32,
+ * FA_F16 or FA_BF16; weights are [d] of that type, 16-byte aligned; turns
+ * 8-byte aligned, may be NULL when rope_dim is 0. rope_dim: a multiple of 16 up
+ * to d. Outputs may be their own inputs, but must not overlap them otherwise.
+ * eps must be finite and >= 0 (read only with weights) and rope_scale finite
+ * (else FA_ERR_SCALE); one weight without the other gives FA_ERR_NULL.
+ */
+int fa_qk_norm_rope(const fa_view* q, const fa_view* k, const fa_view* q_out,
+                    const fa_view* k_out, const void* q_weight, const void* k_weight,
+                    float eps, const int* positions, const unsigned long long* turns,
+                    int rope_dim, int interleaved, float rope_scale, int B, int Hq, int Hkv,
+                    int S, int d, int dtype, fa_stream_t stream);
+
+/*
+ * Backward of fa_qk_norm_rope: from dq_out, dk_out (gradients of its outputs),
+ * its inputs q, k and its other arguments, writes dq, dk and the float32 weight
+ * gradients dq_weight, dk_weight [d], summed over all rows and heads (the same
+ * bits on every call). Without weights q, k, dq_weight, dk_weight and workspace
+ * are not read and may be NULL. dq, dk may be dq_out, dk_out (same views).
+ * workspace: caller-owned, 256-byte aligned, contents on entry without meaning.
+ */
+int fa_qk_norm_rope_bwd(const fa_view* dq_out, const fa_view* dk_out, const fa_view* q,
+                        const fa_view* k, const fa_view* dq, const fa_view* dk,
+                        float* dq_weight, float* dk_weight, const void* q_weight,
+                        const void* k_weight, float eps, const int* positions,
+                        const unsigned long long* turns, int rope_dim, int interleaved,
+                        float rope_scale, int B, int Hq, int Hkv, int S, int d, int dtype,
+                        void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* Workspace bytes of fa_qk_norm_rope_bwd: 2 d floats for each of at most 608
+ * CTAs; 0 without the norm (norm == 0) and for invalid sizes. */
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int S, int d, int norm);
+
+/*
+ * The serving form: the last Sq tokens of each of B sequences. Row s of
+ * sequence b stands at position p = seq_lens[b] - Sq + s (seq_lens: [B] int32 in
+ * device memory, these tokens included, as fa_fwd_ragged_paged reads it). q is
+ * normed and rotated into q_out; k is normed and rotated into row p of the
+ * sequence in k_cache and v copied into v_cache (layouts as for
+ * fa_fwd_splitkv_paged, here of any dtype). A token at p < 0, past the block
+ * table, or in a page whose entry is outside [0, num_blocks) is not stored; its
+ * q_out row is written all the same. Everything else in the caches is left as
+ * it was. Two tokens of a call must not share a cache row.
+ */
+int fa_qk_norm_rope_append(const fa_view* q, const fa_view* k, const fa_view* v,
+                           const fa_view* q_out, void* k_cache, void* v_cache,
+                           const int* block_table, const int* seq_lens, const void* q_weight,
+                           const void* k_weight, float eps, const unsigned long long* turns,
+                           int rope_dim, int interleaved, float rope_scale, int B, int Hq,
+                           int Hkv, int Sq, int d, int block_size, int num_blocks,
+                           int max_blocks, int dtype, fa_stream_t stream);
+
+/*
  * One or a few new tokens of each of B sequences of unequal length over a
  * paged key/value cache. k_cache, v_cache, block_table, q, out and lse are laid
  * out as for fa_fwd_splitkv_paged; seq_lens: [B] int32 in device memory, the
