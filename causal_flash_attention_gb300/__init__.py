@@ -352,47 +352,88 @@ def attention_backward(q, k, v, out, dout, lse, causal=True, scale=None, workspa
 
 
 # ------------------------------------------------------------- key spans --
-def _check_like(ref, dtype, **named):
-    """Every given tensor on ref's device and contiguous, of `dtype` where one is given, with
-    the given shape: named maps a name to (tensor, shape, dtype or None for `dtype`)."""
-    for name, (t, shape, dt) in named.items():
-        if t is None:
-            continue
-        if t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
-        if t.dtype != (dt or dtype):
-            raise ValueError(f"{name} must be {dt or dtype}, not {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+# The calls below check what they are given: a tensor on another device, of
+# another type or size would have the kernels read memory that is not its own.
+# A call is a few microseconds of host time, so the checks are plain
+# comparisons and what a call allocates itself is not checked again.
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _check_cuda(t, name="q"):
-    if not t.is_cuda:
+def _cuda_index(t, name="q"):
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
 
 
-def _alloc_stream(stream, t):
+def _fit(name, t, dev, dtype, shape):
+    """t has to be contiguous on device `dev`, with this dtype and shape."""
+    if (t.get_device() != dev or t.dtype is not dtype or t.shape != shape
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on cuda:{dev}, "
+                         f"not {'a' if t.is_contiguous() else 'a strided'} {t.dtype} tensor "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
+def _run(name, dev, stream, *args):
+    """Call the library on device `dev`; the stream handle goes last."""
+    fn = getattr(_lib or lib(), name)
+    if stream is None:
+        stream = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev == _get_device():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc != 0:
+        raise FAError(rc, name)
+
+
+def _alloc_stream(stream, dev):
     """Where a call on `stream` allocates: that stream's own memory pool, so that the memory's
     earlier and later users are ordered with the call."""
     if stream is None:
         return _NULL_CONTEXT
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=t.device)
+        stream = torch.cuda.ExternalStream(stream, device=dev)
     return torch.cuda.stream(stream)
 
 
-def _span_dims(q, k, v, key_begin, key_end, slopes, **more):
-    _check_cuda(q)
-    B, Hq, Hkv, Sq, Skv, d = _dims_kv(q, k)
-    qs, ks = (B, Hq, Sq, d), (B, Hkv, Skv, d)
-    _check_like(q, q.dtype, q=(q, qs, None), k=(k, ks, None), v=(v, ks, None),
-                key_begin=(key_begin, (B, Sq), torch.int32),
-                key_end=(key_end, (B, Sq), torch.int32), slopes=(slopes, (Hq,), torch.float32),
-                **{n: (t, {"q": qs, "k": ks, "r": qs[:3]}[w], dt)
-                   for n, (t, w, dt) in more.items()})
-    return B, Hq, Hkv, Sq, Skv, d
+def _workspace_bytes(workspace, dev):
+    """Size of a caller's workspace (0 for None), which has to be dense and on device `dev`."""
+    if workspace is None:
+        return 0
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
+    return workspace.numel() * workspace.element_size()
+
+
+def _span_inputs(q, k, v, key_begin, key_end, slopes):
+    """Checks the inputs; (device, (B, Hq, Hkv, Sq, Skv, d))."""
+    dev = _cuda_index(q)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [B, H, S, d]")
+    B, Hq, Sq, d = q.shape
+    _, Hkv, Skv, _ = ks = k.shape
+    dt = q.dtype
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    _fit("k", k, dev, dt, (B, Hkv, Skv, d))
+    _fit("v", v, dev, dt, ks)
+    _fit("key_begin", key_begin, dev, torch.int32, (B, Sq))
+    _fit("key_end", key_end, dev, torch.int32, (B, Sq))
+    if slopes is not None:
+        _fit("slopes", slopes, dev, torch.float32, (Hq,))
+    return dev, (B, Hq, Hkv, Sq, Skv, d)
+
+
+def _span_fwd(dev, dims, q, k, v, key_begin, key_end, out, lse, softcap, slopes, scale, stream):
+    scale = 1.0 / math.sqrt(dims[5]) if scale is None else float(scale)
+    _run("fa_fwd_span", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), key_begin.data_ptr(),
+         key_end.data_ptr(), out.data_ptr(), lse.data_ptr(), *dims, scale, softcap, _ptr(slopes),
+         DTYPE_CODES.get(q.dtype, -1))
 
 
 def fa_fwd_span(q, k, v, key_begin, key_end, out, lse, softcap=0.0, slopes=None, scale=None,
@@ -400,73 +441,62 @@ def fa_fwd_span(q, k, v, key_begin, key_end, out, lse, softcap=0.0, slopes=None,
     """Call fa_fwd_span: row i of batch b sees keys key_begin[b, i] <= j < key_end[b, i]
     (int32 [B,Sq]); scores capped by softcap (0: not) and biased by
     -slopes[h] * |i + Skv - Sq - j| (float32 [Hq], or None)."""
-    B, Hq, Hkv, Sq, Skv, d = _span_dims(q, k, v, key_begin, key_end, slopes,
-                                        out=(out, "q", None), lse=(lse, "r", torch.float32))
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    with _on_device(q):
-        rc = lib().fa_fwd_span(_ptr(q), _ptr(k), _ptr(v), _ptr(key_begin), _ptr(key_end),
-                               _ptr(out), _ptr(lse), B, Hq, Hkv, Sq, Skv, d, scale,
-                               float(softcap), _ptr(slopes), DTYPE_CODES.get(q.dtype, -1),
-                               _stream(stream, q))
-    if rc != 0:
-        raise FAError(rc, "fa_fwd_span")
+    dev, dims = _span_inputs(q, k, v, key_begin, key_end, slopes)
+    _fit("out", out, dev, q.dtype, q.shape)
+    _fit("lse", lse, dev, torch.float32, q.shape[:3])
+    _span_fwd(dev, dims, q, k, v, key_begin, key_end, out, lse, softcap, slopes, scale, stream)
 
 
 def fa_bwd_span_workspace_bytes(B, Hq, Hkv, Sq, Skv, d) -> int:
     return int(lib().fa_bwd_span_workspace_bytes(B, Hq, Hkv, Sq, Skv, d))
 
 
+def _span_bwd(dev, dims, q, k, v, key_begin, key_end, out, dout, lse, dq, dk, dv, workspace,
+              softcap, slopes, scale, stream):
+    _fit("out", out, dev, q.dtype, q.shape)
+    _fit("dout", dout, dev, q.dtype, q.shape)
+    _fit("lse", lse, dev, torch.float32, q.shape[:3])
+    scale = 1.0 / math.sqrt(dims[5]) if scale is None else float(scale)
+    _run("fa_bwd_span", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), key_begin.data_ptr(),
+         key_end.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(),
+         dk.data_ptr(), dv.data_ptr(), *dims, scale, softcap, _ptr(slopes),
+         DTYPE_CODES.get(q.dtype, -1), _ptr(workspace), _workspace_bytes(workspace, dev))
+
+
 def fa_bwd_span(q, k, v, key_begin, key_end, out, dout, lse, dq, dk, dv, workspace, softcap=0.0,
                 slopes=None, scale=None, stream=None):
     """Call fa_bwd_span; `workspace` is a device tensor of at least
     fa_bwd_span_workspace_bytes(...) bytes."""
-    B, Hq, Hkv, Sq, Skv, d = _span_dims(
-        q, k, v, key_begin, key_end, slopes, out=(out, "q", None), dout=(dout, "q", None),
-        lse=(lse, "r", torch.float32), dq=(dq, "q", None), dk=(dk, "k", None), dv=(dv, "k", None))
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    ws_bytes = _workspace_bytes(workspace, q)
-    with _on_device(q):
-        rc = lib().fa_bwd_span(_ptr(q), _ptr(k), _ptr(v), _ptr(key_begin), _ptr(key_end),
-                               _ptr(out), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), B,
-                               Hq, Hkv, Sq, Skv, d, scale, float(softcap), _ptr(slopes),
-                               DTYPE_CODES.get(q.dtype, -1), _ptr(workspace), ws_bytes,
-                               _stream(stream, q))
-    if rc != 0:
-        raise FAError(rc, "fa_bwd_span")
-
-
-def _workspace_bytes(workspace, ref):
-    """Size of a caller's workspace (0 for None), which has to be dense and on ref's device."""
-    if workspace is None:
-        return 0
-    if workspace.device != ref.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {ref.device}")
-    return workspace.numel() * workspace.element_size()
+    dev, dims = _span_inputs(q, k, v, key_begin, key_end, slopes)
+    _fit("dq", dq, dev, q.dtype, q.shape)
+    _fit("dk", dk, dev, q.dtype, k.shape)
+    _fit("dv", dv, dev, q.dtype, k.shape)
+    _span_bwd(dev, dims, q, k, v, key_begin, key_end, out, dout, lse, dq, dk, dv, workspace,
+              softcap, slopes, scale, stream)
 
 
 def attention_span_forward(q, k, v, key_begin, key_end, softcap=0.0, slopes=None, scale=None,
                            stream=None):
     """Allocate out and lse and run fa_fwd_span. Returns (out, lse)."""
-    _check_cuda(q)
-    with _alloc_stream(stream, q):
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    fa_fwd_span(q, k, v, key_begin, key_end, out, lse, softcap, slopes, scale, stream)
+    dev, dims = _span_inputs(q, k, v, key_begin, key_end, slopes)
+    with _alloc_stream(stream, dev):
+        out = torch.empty_like(q)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+    _span_fwd(dev, dims, q, k, v, key_begin, key_end, out, lse, softcap, slopes, scale, stream)
     return out, lse
 
 
 def attention_span_backward(q, k, v, out, dout, lse, key_begin, key_end, softcap=0.0,
                             slopes=None, scale=None, workspace=None, stream=None):
     """Allocate dq, dk, dv (and a workspace unless given) and run fa_bwd_span."""
-    _check_cuda(q)
-    B, Hq, Hkv, Sq, Skv, d = _dims_kv(q, k)
-    with _alloc_stream(stream, q):
-        dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, k))
+    dev, dims = _span_inputs(q, k, v, key_begin, key_end, slopes)
+    with _alloc_stream(stream, dev):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
         if workspace is None:
-            n = fa_bwd_span_workspace_bytes(B, Hq, Hkv, Sq, Skv, d)
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    fa_bwd_span(q, k, v, key_begin, key_end, out, dout, lse, dq, dk, dv, workspace, softcap,
-                slopes, scale, stream)
+            workspace = torch.empty(lib().fa_bwd_span_workspace_bytes(*dims), dtype=torch.uint8,
+                                    device=dev)
+    _span_bwd(dev, dims, q, k, v, key_begin, key_end, out, dout, lse, dq, dk, dv, workspace,
+              softcap, slopes, scale, stream)
     return dq, dk, dv
 
 
@@ -526,22 +556,43 @@ def key_spans(B, Sq, Skv=None, *, causal=True, window=0, doc_lens=None, prefix_l
 
 
 # ------------------------------------------------------ ragged paged cache --
-def _ragged_dims(q, k_cache, v_cache, block_table, seq_lens, **more):
-    _check_cuda(q)
-    if q.dim() != 4 or k_cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("q [B,Hq,Sq,d], caches [num_blocks,Hkv,block_size,d], table [B,max_blocks]")
-    B, Hq, Sq, d = (int(x) for x in q.shape)
-    num_blocks, Hkv, block_size = (int(x) for x in k_cache.shape[:3])
-    max_blocks = int(block_table.shape[1])
-    cache = (num_blocks, Hkv, block_size, d)
-    _check_like(q, q.dtype, q=(q, q.shape, None), k_cache=(k_cache, cache, None), v_cache=(v_cache, cache, None),
-                block_table=(block_table, (B, max_blocks), torch.int32),
-                seq_lens=(seq_lens, (B,), torch.int32), **more)
-    return B, Hq, Hkv, Sq, d, block_size, num_blocks, max_blocks
+def _cache_inputs(dev, dt, B, Hkv, d, k_cache, v_cache, block_table, seq_lens):
+    """Checks a paged cache, its table and the lengths; (block_size, num_blocks, max_blocks)."""
+    if k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("caches [num_blocks,Hkv,block_size,d], table [B,max_blocks]")
+    num_blocks, _, block_size, _ = cs = k_cache.shape
+    _fit("k_cache", k_cache, dev, dt, (num_blocks, Hkv, block_size, d))
+    _fit("v_cache", v_cache, dev, dt, cs)
+    max_blocks = block_table.shape[1]
+    _fit("block_table", block_table, dev, torch.int32, (B, max_blocks))
+    _fit("seq_lens", seq_lens, dev, torch.int32, (B,))
+    return block_size, num_blocks, max_blocks
+
+
+def _ragged_inputs(q, k_cache, v_cache, block_table, seq_lens, slopes):
+    """Checks the inputs; (device, (B, Hq, Hkv, Sq, d, block_size, num_blocks, max_blocks))."""
+    dev = _cuda_index(q)
+    if q.dim() != 4 or k_cache.dim() != 4 or not q.is_contiguous():
+        raise ValueError("q [B,Hq,Sq,d] contiguous, caches [num_blocks,Hkv,block_size,d]")
+    B, Hq, Sq, d = q.shape
+    Hkv = k_cache.shape[1]
+    cache = _cache_inputs(dev, q.dtype, B, Hkv, d, k_cache, v_cache, block_table, seq_lens)
+    if slopes is not None:
+        _fit("slopes", slopes, dev, torch.float32, (Hq,))
+    return dev, (B, Hq, Hkv, Sq, d) + cache
 
 
 def fa_fwd_ragged_paged_workspace_bytes(B, Hq, Hkv, Sq, d, block_size, max_blocks) -> int:
     return int(lib().fa_fwd_ragged_paged_workspace_bytes(B, Hq, Hkv, Sq, d, block_size, max_blocks))
+
+
+def _ragged(dev, dims, q, k_cache, v_cache, block_table, seq_lens, out, lse, workspace, window,
+            softcap, slopes, scale, stream):
+    scale = 1.0 / math.sqrt(dims[4]) if scale is None else float(scale)
+    _run("fa_fwd_ragged_paged", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+         block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), *dims,
+         int(window), scale, softcap, _ptr(slopes), DTYPE_CODES.get(q.dtype, -1), _ptr(workspace),
+         _workspace_bytes(workspace, dev))
 
 
 def fa_fwd_ragged_paged(q, k_cache, v_cache, block_table, seq_lens, out, lse, workspace,
@@ -550,34 +601,24 @@ def fa_fwd_ragged_paged(q, k_cache, v_cache, block_table, seq_lens, out, lse, wo
     k_cache/v_cache [num_blocks,Hkv,block_size,d]; block_table int32 [B,max_blocks];
     seq_lens int32 [B]; `workspace` a device tensor of at least
     fa_fwd_ragged_paged_workspace_bytes(...) bytes."""
-    B, Hq, Hkv, Sq, d, block_size, num_blocks, max_blocks = _ragged_dims(
-        q, k_cache, v_cache, block_table, seq_lens,
-        out=(out, q.shape, None), lse=(lse, q.shape[:3], torch.float32),
-        slopes=(slopes, (q.shape[1],), torch.float32))
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    with _on_device(q):
-        rc = lib().fa_fwd_ragged_paged(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(out),
-            _ptr(lse), B, Hq, Hkv, Sq, d, block_size, num_blocks, max_blocks, int(window), scale,
-            float(softcap), _ptr(slopes), DTYPE_CODES.get(q.dtype, -1), _ptr(workspace),
-            _workspace_bytes(workspace, q), _stream(stream, q))
-    if rc != 0:
-        raise FAError(rc, "fa_fwd_ragged_paged")
+    dev, dims = _ragged_inputs(q, k_cache, v_cache, block_table, seq_lens, slopes)
+    _fit("out", out, dev, q.dtype, q.shape)
+    _fit("lse", lse, dev, torch.float32, q.shape[:3])
+    _ragged(dev, dims, q, k_cache, v_cache, block_table, seq_lens, out, lse, workspace, window,
+            softcap, slopes, scale, stream)
 
 
 def decode_forward_ragged(q, k_cache, v_cache, block_table, seq_lens, window=0, softcap=0.0,
                           slopes=None, scale=None, stream=None):
     """Allocate out, lse and the workspace and run fa_fwd_ragged_paged. Returns (out, lse)."""
-    _check_cuda(q)
-    B, Hq, Sq, d = (int(x) for x in q.shape)
-    n = fa_fwd_ragged_paged_workspace_bytes(B, Hq, int(k_cache.shape[1]), Sq, d,
-                                            int(k_cache.shape[2]), int(block_table.shape[1]))
-    with _alloc_stream(stream, q):
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-        ws = torch.empty(n, dtype=torch.uint8, device=q.device)
-    fa_fwd_ragged_paged(q, k_cache, v_cache, block_table, seq_lens, out, lse, ws, window, softcap,
-                        slopes, scale, stream)
+    dev, dims = _ragged_inputs(q, k_cache, v_cache, block_table, seq_lens, slopes)
+    n = lib().fa_fwd_ragged_paged_workspace_bytes(*dims[:6], dims[7])
+    with _alloc_stream(stream, dev):
+        out = torch.empty_like(q)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _ragged(dev, dims, q, k_cache, v_cache, block_table, seq_lens, out, lse, ws, window, softcap,
+            slopes, scale, stream)
     return out, lse
 
 
@@ -626,45 +667,48 @@ def rope_turns(inv_freq, device=None):
     return torch.tensor(out, dtype=torch.int64, device=device)
 
 
-def _views(B, S, d, like, **named):
-    """fa_view arguments from name=(tensor, H); None stays None."""
-    out = []
-    for name, (t, H) in named.items():
-        if t is None:
-            out.append(None)
-            continue
-        if t.device != like.device or t.dtype != like.dtype:
-            raise ValueError(f"{name} must be {like.dtype} on {like.device}")
-        if tuple(t.shape) != (B, H, S, d):
-            raise ValueError(f"{name} must be {(B, H, S, d)}, not {tuple(t.shape)}")
-        if t.stride(3) != 1:
-            raise ValueError(f"{name}: the elements of a head must be contiguous")
-        # a dimension of one row has no stride to keep aligned
-        sb, sh, ss = (0 if n == 1 else st for n, st in zip(t.shape[:3], t.stride()[:3]))
-        out.append(ctypes.byref(_View(t.data_ptr(), sb, sh, ss)))
-    return out
+def _view(name, t, dev, dtype, shape, written=False):
+    """The fa_view argument of a [B, H, S, d] tensor of any strides but the last."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} tensor {tuple(shape)} on cuda:{dev}, not a "
+                         f"{t.dtype} tensor {tuple(t.shape)} on {t.device}")
+    sb, sh, ss, se = t.stride()
+    if se != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    B, H, S, d = shape
+    if written and not t.is_contiguous():
+        reach = d
+        for st, n in sorted(((sb, B), (sh, H), (ss, S))):
+            if n > 1:
+                if st < reach:
+                    raise ValueError(f"{name}: elements overlap in memory")
+                reach = st * n
+    # a dimension of one row has no stride to keep aligned
+    return ctypes.byref(_View(t.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0,
+                              ss if S > 1 else 0))
 
 
-def _heads_dims(q, k, turns, positions, q_weight, k_weight):
-    _check_cuda(q)
+def _rope_inputs(dev, dt, B, S, d, turns, positions, q_weight, k_weight):
+    """Checks what the three calls share; rope_dim."""
+    n = 0
+    if turns is not None:
+        n = turns.numel()
+        _fit("turns", turns, dev, torch.int64, (n,))
+    if positions is not None:
+        _fit("positions", positions, dev, torch.int32, (B, S))
+    if q_weight is not None:
+        _fit("q_weight", q_weight, dev, dt, (d,))
+    if k_weight is not None:
+        _fit("k_weight", k_weight, dev, dt, (d,))
+    return 2 * n
+
+
+def _qk_dims(q, k, name="q"):
+    dev = _cuda_index(q, name)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q [B,Hq,S,d] and k [B,Hkv,S,d] (any strides but the last)")
-    B, Hq, S, d = (int(x) for x in q.shape)
-    n = 0 if turns is None else int(turns.numel())
-    _check_like(q, q.dtype, turns=(turns, (n,), torch.int64),
-                positions=(positions, (B, S), torch.int32), q_weight=(q_weight, (d,), None),
-                k_weight=(k_weight, (d,), None))
-    return B, Hq, int(k.shape[1]), S, d, 2 * n
-
-
-def _check_no_overlap(name, t):
-    """An output view whose elements would share memory cannot be written."""
-    dims = sorted((st, n) for n, st in zip(t.shape, t.stride()) if n > 1)
-    reach = 0
-    for st, n in dims:
-        if st <= reach:
-            raise ValueError(f"{name}: elements overlap in memory")
-        reach += st * (n - 1)
+    B, Hq, S, d = q.shape
+    return dev, B, Hq, k.shape[1], S, d
 
 
 def fa_qk_norm_rope(q, k, q_out, k_out, turns, positions=None, q_weight=None, k_weight=None,
@@ -672,17 +716,13 @@ def fa_qk_norm_rope(q, k, q_out, k_out, turns, positions=None, q_weight=None, k_
     """Call fa_qk_norm_rope on views q, q_out [B,Hq,S,d] and k, k_out [B,Hkv,S,d] (any strides
     but the last); turns as from rope_turns (rope_dim = 2 * its length; None: no rotation);
     positions int32 [B,S] or None (row s at position s); both weights [d] or neither."""
-    B, Hq, Hkv, S, d, rope_dim = _heads_dims(q, k, turns, positions, q_weight, k_weight)
-    views = _views(B, S, d, q, q=(q, Hq), k=(k, Hkv), q_out=(q_out, Hq), k_out=(k_out, Hkv))
-    _check_no_overlap("q_out", q_out)
-    _check_no_overlap("k_out", k_out)
-    with _on_device(q):
-        rc = lib().fa_qk_norm_rope(*views, _ptr(q_weight), _ptr(k_weight), float(eps),
-                                   _ptr(positions), _ptr(turns), rope_dim, int(bool(interleaved)),
-                                   float(rope_scale), B, Hq, Hkv, S, d,
-                                   DTYPE_CODES.get(q.dtype, -1), _stream(stream, q))
-    if rc != 0:
-        raise FAError(rc, "fa_qk_norm_rope")
+    dev, B, Hq, Hkv, S, d = _qk_dims(q, k)
+    dt, qs, ks = q.dtype, (B, Hq, S, d), (B, Hkv, S, d)
+    rope_dim = _rope_inputs(dev, dt, B, S, d, turns, positions, q_weight, k_weight)
+    _run("fa_qk_norm_rope", dev, stream, _view("q", q, dev, dt, qs), _view("k", k, dev, dt, ks),
+         _view("q_out", q_out, dev, dt, qs, True), _view("k_out", k_out, dev, dt, ks, True),
+         _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions), _ptr(turns), rope_dim,
+         1 if interleaved else 0, rope_scale, B, Hq, Hkv, S, d, DTYPE_CODES.get(dt, -1))
 
 
 def fa_qk_norm_rope_bwd_workspace_bytes(B, S, d, norm=True) -> int:
@@ -694,22 +734,19 @@ def fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, dq_weight, dk_weight, work
                         interleaved=False, rope_scale=1.0, stream=None):
     """Call fa_qk_norm_rope_bwd: views as for fa_qk_norm_rope; dq_weight, dk_weight float32 [d]
     and `workspace` (fa_qk_norm_rope_bwd_workspace_bytes bytes) with weights, else None."""
-    B, Hq, Hkv, S, d, rope_dim = _heads_dims(dq_out, dk_out, turns, positions, q_weight, k_weight)
-    views = _views(B, S, d, dq_out, dq_out=(dq_out, Hq), dk_out=(dk_out, Hkv), q=(q, Hq),
-                   k=(k, Hkv), dq=(dq, Hq), dk=(dk, Hkv))
-    _check_no_overlap("dq", dq)
-    _check_no_overlap("dk", dk)
-    _check_like(dq_out, torch.float32, dq_weight=(dq_weight, (d,), None),
-                dk_weight=(dk_weight, (d,), None))
-    with _on_device(dq_out):
-        rc = lib().fa_qk_norm_rope_bwd(*views, _ptr(dq_weight), _ptr(dk_weight), _ptr(q_weight),
-                                       _ptr(k_weight), float(eps), _ptr(positions), _ptr(turns),
-                                       rope_dim, int(bool(interleaved)), float(rope_scale), B, Hq,
-                                       Hkv, S, d, DTYPE_CODES.get(dq_out.dtype, -1),
-                                       _ptr(workspace), _workspace_bytes(workspace, dq_out),
-                                       _stream(stream, dq_out))
-    if rc != 0:
-        raise FAError(rc, "fa_qk_norm_rope_bwd")
+    dev, B, Hq, Hkv, S, d = _qk_dims(dq_out, dk_out, "dq_out")
+    dt, qs, ks = dq_out.dtype, (B, Hq, S, d), (B, Hkv, S, d)
+    rope_dim = _rope_inputs(dev, dt, B, S, d, turns, positions, q_weight, k_weight)
+    for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
+        if t is not None:
+            _fit(name, t, dev, torch.float32, (d,))
+    _run("fa_qk_norm_rope_bwd", dev, stream, _view("dq_out", dq_out, dev, dt, qs),
+         _view("dk_out", dk_out, dev, dt, ks), q if q is None else _view("q", q, dev, dt, qs),
+         k if k is None else _view("k", k, dev, dt, ks), _view("dq", dq, dev, dt, qs, True),
+         _view("dk", dk, dev, dt, ks, True), _ptr(dq_weight), _ptr(dk_weight), _ptr(q_weight),
+         _ptr(k_weight), eps, _ptr(positions), _ptr(turns), rope_dim, 1 if interleaved else 0,
+         rope_scale, B, Hq, Hkv, S, d, DTYPE_CODES.get(dt, -1), _ptr(workspace),
+         _workspace_bytes(workspace, dev))
 
 
 def fa_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, block_table, seq_lens, turns,
@@ -717,34 +754,26 @@ def fa_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, block_table, seq_le
                            rope_scale=1.0, stream=None):
     """Call fa_qk_norm_rope_append: the last Sq tokens of sequences of seq_lens tokens; views q,
     q_out [B,Hq,Sq,d], k, v [B,Hkv,Sq,d]; caches [num_blocks,Hkv,block_size,d] written in place."""
-    B, Hq, Hkv, Sq, d, rope_dim = _heads_dims(q, k, turns, None, q_weight, k_weight)
-    views = _views(B, Sq, d, q, q=(q, Hq), k=(k, Hkv), v=(v, Hkv), q_out=(q_out, Hq))
-    _check_no_overlap("q_out", q_out)
-    if k_cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("caches [num_blocks,Hkv,block_size,d], table [B,max_blocks]")
-    num_blocks, block_size, max_blocks = k_cache.shape[0], k_cache.shape[2], block_table.shape[1]
-    cache = (num_blocks, Hkv, block_size, d)
-    _check_like(q, q.dtype, k_cache=(k_cache, cache, None), v_cache=(v_cache, cache, None),
-                block_table=(block_table, (B, max_blocks), torch.int32),
-                seq_lens=(seq_lens, (B,), torch.int32))
-    with _on_device(q):
-        rc = lib().fa_qk_norm_rope_append(*views, _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
-                                          _ptr(seq_lens), _ptr(q_weight), _ptr(k_weight),
-                                          float(eps), _ptr(turns), rope_dim,
-                                          int(bool(interleaved)), float(rope_scale), B, Hq, Hkv,
-                                          Sq, d, block_size, num_blocks, max_blocks,
-                                          DTYPE_CODES.get(q.dtype, -1), _stream(stream, q))
-    if rc != 0:
-        raise FAError(rc, "fa_qk_norm_rope_append")
+    dev, B, Hq, Hkv, Sq, d = _qk_dims(q, k)
+    dt, qs, ks = q.dtype, (B, Hq, Sq, d), (B, Hkv, Sq, d)
+    rope_dim = _rope_inputs(dev, dt, B, Sq, d, turns, None, q_weight, k_weight)
+    cache = _cache_inputs(dev, dt, B, Hkv, d, k_cache, v_cache, block_table, seq_lens)
+    _run("fa_qk_norm_rope_append", dev, stream, _view("q", q, dev, dt, qs),
+         _view("k", k, dev, dt, ks), _view("v", v, dev, dt, ks),
+         _view("q_out", q_out, dev, dt, qs, True), k_cache.data_ptr(), v_cache.data_ptr(),
+         block_table.data_ptr(), seq_lens.data_ptr(), _ptr(q_weight), _ptr(k_weight), eps,
+         _ptr(turns), rope_dim, 1 if interleaved else 0, rope_scale, B, Hq, Hkv, Sq, d, *cache,
+         DTYPE_CODES.get(dt, -1))
 
 
 def qk_norm_rope_forward(q, k, turns, positions=None, q_weight=None, k_weight=None, eps=1e-6,
                          interleaved=False, rope_scale=1.0, stream=None):
     """Allocate contiguous q_out [B,Hq,S,d] and k_out [B,Hkv,S,d] (as the attention calls take
     them) and run fa_qk_norm_rope. Returns (q_out, k_out)."""
-    _check_cuda(q)
-    with _alloc_stream(stream, q):
-        q_out, k_out = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k))
+    dev = _cuda_index(q)
+    with _alloc_stream(stream, dev):
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
     fa_qk_norm_rope(q, k, q_out, k_out, turns, positions, q_weight, k_weight, eps, interleaved,
                     rope_scale, stream)
     return q_out, k_out
@@ -757,19 +786,18 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, turns, positions=None, q_weight=
     [B, S, H, d] in memory, as projections give q and k) and, with weights, the float32 weight
     gradients, and run fa_qk_norm_rope_bwd. Returns (dq, dk, dq_weight, dk_weight), the last two
     None without weights. Without weights q and k are not read and may be None."""
-    _check_cuda(dq_out, "dq_out")
-    B, _, S, d = dq_out.shape
-    norm = q_weight is not None
+    dev, B, Hq, Hkv, S, d = _qk_dims(dq_out, dk_out, "dq_out")
     dwq = dwk = ws = None
-    with _alloc_stream(stream, dq_out):
-        def grad(t):
-            return torch.empty(B, S, t.shape[1], d, dtype=t.dtype, device=t.device).transpose(1, 2)
-        dq = grad(dq_out) if dq is None else dq
-        dk = grad(dk_out) if dk is None else dk
-        if norm:
-            dwq, dwk = torch.empty(2, d, dtype=torch.float32, device=dq_out.device)
-            ws = torch.empty(fa_qk_norm_rope_bwd_workspace_bytes(B, S, d), dtype=torch.uint8,
-                             device=dq_out.device)
+    with _alloc_stream(stream, dev):
+        if dq is None:
+            dq = torch.empty((B, S, Hq, d), dtype=dq_out.dtype, device=dev).transpose(1, 2)
+        if dk is None:
+            dk = torch.empty((B, S, Hkv, d), dtype=dq_out.dtype, device=dev).transpose(1, 2)
+        if q_weight is not None:
+            dwq = torch.empty(d, dtype=torch.float32, device=dev)
+            dwk = torch.empty(d, dtype=torch.float32, device=dev)
+            ws = torch.empty(lib().fa_qk_norm_rope_bwd_workspace_bytes(B, S, d, 1),
+                             dtype=torch.uint8, device=dev)
     fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, dwq, dwk, ws, turns, positions, q_weight,
                         k_weight, eps, interleaved, rope_scale, stream)
     return dq, dk, dwq, dwk
@@ -779,9 +807,9 @@ def qk_norm_rope_append(q, k, v, k_cache, v_cache, block_table, seq_lens, turns,
                         k_weight=None, eps=1e-6, interleaved=False, rope_scale=1.0, stream=None):
     """Allocate q_out (contiguous [B,Hq,Sq,d]) and run fa_qk_norm_rope_append, which writes the
     tokens' keys and values into the caches. Returns q_out."""
-    _check_cuda(q)
-    with _alloc_stream(stream, q):
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    dev = _cuda_index(q)
+    with _alloc_stream(stream, dev):
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     fa_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, block_table, seq_lens, turns,
                            q_weight, k_weight, eps, interleaved, rope_scale, stream)
     return q_out
