@@ -98,7 +98,7 @@ def lib() -> ctypes.CDLL:
     L.fa_qk_norm_rope_bwd.argtypes = ([vw] * 6 + [vp] * 4 + [f32, vp, vp, i32, i32, f32]
                                       + [i32] * 6 + [vp, sz, vp])
     L.fa_qk_norm_rope_bwd.restype = i32
-    L.fa_qk_norm_rope_bwd_workspace_bytes.argtypes = [i32] * 4
+    L.fa_qk_norm_rope_bwd_workspace_bytes.argtypes = [i32] * 6
     L.fa_qk_norm_rope_bwd_workspace_bytes.restype = sz
     L.fa_qk_norm_rope_append.argtypes = ([vw] * 4 + [vp] * 6 + [f32, vp, i32, i32, f32]
                                          + [i32] * 9 + [vp])
@@ -725,8 +725,8 @@ def fa_qk_norm_rope(q, k, q_out, k_out, turns, positions=None, q_weight=None, k_
          1 if interleaved else 0, rope_scale, B, Hq, Hkv, S, d, DTYPE_CODES.get(dt, -1))
 
 
-def fa_qk_norm_rope_bwd_workspace_bytes(B, S, d, norm=True) -> int:
-    return int(lib().fa_qk_norm_rope_bwd_workspace_bytes(B, S, d, int(bool(norm))))
+def fa_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hkv, S, d, norm=True) -> int:
+    return int(lib().fa_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hkv, S, d, int(bool(norm))))
 
 
 def fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, dq_weight, dk_weight, workspace, turns,
@@ -796,7 +796,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, turns, positions=None, q_weight=
         if q_weight is not None:
             dwq = torch.empty(d, dtype=torch.float32, device=dev)
             dwk = torch.empty(d, dtype=torch.float32, device=dev)
-            ws = torch.empty(lib().fa_qk_norm_rope_bwd_workspace_bytes(B, S, d, 1),
+            ws = torch.empty(lib().fa_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hkv, S, d, 1),
                              dtype=torch.uint8, device=dev)
     fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, dwq, dwk, ws, turns, positions, q_weight,
                         k_weight, eps, interleaved, rope_scale, stream)

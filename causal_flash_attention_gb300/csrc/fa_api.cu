@@ -223,7 +223,7 @@ int heads_params(HeadsParams& p, const void* wq, const void* wk, float eps, cons
   int rc = check_common(B, Hq, Hkv, S, S, d, 0, 1.f, dtype);
   if (rc != FA_OK) return rc;
   if (rope_dim < 0 || rope_dim > d || rope_dim % 16 != 0 || Hq > (1 << 20) ||
-      static_cast<long long>(B) * S > (1LL << 33))
+      static_cast<long long>(B) * S > 0x7fffffffLL)
     return FA_ERR_SHAPE;
   if (!std::isfinite(rope_scale) || (wq && !(std::isfinite(eps) && eps >= 0.f)))
     return FA_ERR_SCALE;
@@ -672,9 +672,9 @@ int fa_qk_norm_rope(const fa_view* q, const fa_view* k, const fa_view* q_out, co
                                                                                     : FA_ERR_CUDA;
 }
 
-size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int S, int d, int norm) {
-  if (B < 1 || S < 1 || (d != 64 && d != 128) || !norm) return 0;
-  return static_cast<size_t>(heads_bwd_blocks(B, S)) * 2 * d * 4;
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int Hq, int Hkv, int S, int d, int norm) {
+  if (!norm || check_common(B, Hq, Hkv, S, S, d, 0, 1.f, FA_BF16) != FA_OK) return 0;
+  return static_cast<size_t>(heads_bwd_blocks(B, Hq, Hkv, S, d)) * 2 * d * 4;
 }
 
 int fa_qk_norm_rope_bwd(const fa_view* dq_out, const fa_view* dk_out, const fa_view* q,
@@ -689,13 +689,13 @@ int fa_qk_norm_rope_bwd(const fa_view* dq_out, const fa_view* dk_out, const fa_v
   if (rc == FA_OK)
     rc = take_views({{dq_out, &p.q_out}, {dk_out, &p.k_out}, {dq, &p.dq}, {dk, &p.dk}}, dtype);
   if (rc != FA_OK) return rc;
-  p.n_blocks = heads_bwd_blocks(B, S);
+  p.n_blocks = heads_bwd_blocks(B, Hq, Hkv, S, d);
   if (q_weight) {
     if ((rc = take_views({{q, &p.q}, {k, &p.k}}, dtype)) != FA_OK) return rc;
     if (!dq_weight || !dk_weight) return FA_ERR_NULL;
     if (((reinterpret_cast<uintptr_t>(dq_weight) | reinterpret_cast<uintptr_t>(dk_weight)) & 3u) != 0)
       return FA_ERR_ALIGN;
-    if (!workspace || workspace_bytes < fa_qk_norm_rope_bwd_workspace_bytes(B, S, d, 1))
+    if (!workspace || workspace_bytes < fa_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hkv, S, d, 1))
       return FA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_ALIGN;
     p.dwq = dq_weight;

@@ -17,11 +17,19 @@
 // 2^-33 of a turn) go to sincospif.
 //
 // Layout. A head's d elements are held by d / 8 lanes, 8 consecutive elements
-// each (16-byte accesses), so a warp takes 32 / (d / 8) heads of a token at a
-// time. The pair partner of the half layout sits in another lane of the same
-// head (rope_dim is a multiple of 16) and is exchanged by shuffles. A warp does
-// all its heads of one token, so each phase is turned into sin and cos once for
-// many heads. Everything is bound by the bytes of x and y.
+// each (16-byte accesses), so a warp takes a group of 32 / (d / 8) heads of a
+// token at a time. The pair partner of the half layout sits in another lane of
+// the same head (rope_dim is a multiple of 16) and is exchanged by shuffles of
+// the loaded words. A warp stays with one token, walks its query heads, then its
+// key heads (then its value heads), and keeps its columns' factors in registers:
+// the weights are multiplied into sin and cos once per token, so that a group
+// costs a sum of squares and two products an element, in paired fp32
+// instructions. A block's threads turn the phases of its tokens into sin and cos
+// once, in shared memory, while the first loads are on their way.
+//
+// Everything is bound by the bytes of x and y as long as a group costs few
+// instructions: a form that found token and head of every group by division ran
+// at a quarter of this one's rate.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -29,6 +37,7 @@
 #include <type_traits>
 
 #include "fa_heads.h"
+#include "ptx.cuh"
 
 namespace fa {
 namespace {
@@ -37,88 +46,150 @@ constexpr int kSms = 152;
 constexpr int kWarpsH = 8;
 constexpr unsigned kFull = 0xffffffffu;
 
+// 8 elements as loaded: 4 words of two 16-bit elements, or 8 of one fp32.
 template <typename T>
-struct alignas(16) Vec8 { T x[8]; };
-
-template <typename T>
-__device__ __forceinline__ void load8(const void* base, long long at, float (&f)[8]) {
-  const Vec8<T> v = *reinterpret_cast<const Vec8<T>*>(static_cast<const T*>(base) + at);
+struct Raw {
+  static constexpr int kWords = static_cast<int>(sizeof(T)) * 2;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* src) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = static_cast<float>(v.x[e]);
-}
-
-template <typename T>
-__device__ __forceinline__ void store8(void* base, long long at, const float (&f)[8]) {
-  Vec8<T> v;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v.x[e] = static_cast<T>(f[e]);
-  *reinterpret_cast<Vec8<T>*>(static_cast<T*>(base) + at) = v;
-}
-
-// sin and cos of this lane's elements' phases at one position, times
-// rope_scale: element e of the lane belongs to pair i(e), and the rotation is
-// y_e = c_e n_e + s_e n_partner with the sign of the pair's side in s_e. Elements
-// past rope_dim get c = 1, s = 0.
-template <int D>
-struct Turn {
-  float c[8], s[8];
-  __device__ __forceinline__ void set(const HeadsParams& p, int sub, int position) {
-    const int half = p.rope_dim / 2;
-    const int e0 = sub * 8;
-    if (e0 >= p.rope_dim) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        c[e] = 1.f;
-        s[e] = 0.f;
-      }
-      return;
-    }
-    auto phase = [&](int i, float& sn, float& cs) {
-      const uint64_t turn = static_cast<uint64_t>(static_cast<long long>(position)) * p.turns[i];
-      // top 32 bits as a signed fraction of half a turn
-      const float x = static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f;
-      sincospif(x, &sn, &cs);
-      sn *= p.rope_scale;
-      cs *= p.rope_scale;
-    };
-    if (p.interleaved) {
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        float sn, cs;
-        phase((e0 + e) / 2, sn, cs);
-        c[e] = c[e + 1] = cs;
-        s[e] = -sn;
-        s[e + 1] = sn;
-      }
-    } else {
-      const bool second = e0 >= half;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float sn, cs;
-        phase(e0 + e - (second ? half : 0), sn, cs);
-        c[e] = cs;
-        s[e] = second ? sn : -sn;
-      }
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(src)[i];
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
     }
   }
-  // y = R n (sign = 1) or R^T n (sign = -1); every lane of the warp calls it
-  __device__ __forceinline__ void apply(const HeadsParams& p, int lane, float sign,
-                                        float (&n)[8]) const {
-    constexpr int kLanes = D / 8;
-    float o[8];
-    if (p.interleaved) {
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = n[e ^ 1];
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void store(T* dst) const {
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i)
+      reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+  __device__ __forceinline__ Raw from_lane(int src) const {
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) r.w[i] = __shfl_sync(kFull, w[i], src);
+    return r;
+  }
+  // elements 2i and 2i + 1 as a pair of fp32, and back
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    if constexpr (sizeof(T) == 4) {
+      return f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     } else {
-      const int sub = lane % kLanes, h = p.rope_dim / 16;   // lanes of half the rotated part
-      const int src = sub < h ? lane + h : (sub < 2 * h ? lane - h : lane);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(kFull, n[e], src);
+      const float2 f = unpack2<std::is_same<T, __nv_bfloat16>::value>(w[i]);
+      return f2_pack(f.x, f.y);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) n[e] = fmaf(c[e], n[e], sign * s[e] * o[e]);
+  }
+  __device__ __forceinline__ void set_pair(int i, uint64_t v) {
+    float a, b;
+    f2_unpack(v, a, b);
+    if constexpr (sizeof(T) == 4) {
+      w[2 * i] = __float_as_uint(a);
+      w[2 * i + 1] = __float_as_uint(b);
+    } else {
+      w[i] = pack2<std::is_same<T, __nv_bfloat16>::value>(a, b);
+    }
   }
 };
+
+__device__ __forceinline__ uint64_t f2_swap(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return f2_pack(b, a);
+}
+
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// (cos, sin) times rope_scale of pair i at a position: entry i of a token's table.
+__device__ __forceinline__ float2 cos_sin(const HeadsParams& p, int position, int i) {
+  const uint64_t turn = static_cast<uint64_t>(static_cast<long long>(position)) * p.turns[i];
+  // top 32 bits as a signed fraction of half a turn
+  const float x = static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f;
+  float sn, cs;
+  sincospif(x, &sn, &cs);
+  return make_float2(cs * p.rope_scale, sn * p.rope_scale);
+}
+
+// The table of one token, by the warps that share it (warp `w` of `W` here).
+__device__ __forceinline__ void fill_table(const HeadsParams& p, float2* table, int position,
+                                           int lane, int w, int W) {
+  for (int i = w * 32 + lane; i < p.rope_dim / 2; i += 32 * W) table[i] = cos_sin(p, position, i);
+}
+
+// This lane's place in its head, and where its elements' pair partners are.
+template <int D>
+struct Place {
+  int e0;            // first element
+  int partner;       // half layout: partners of e0, e0 + 1, ... (e0 past rope_dim)
+  int src;           // the lane that holds them
+  bool turned, second;
+  __device__ __forceinline__ Place(const HeadsParams& p, int lane) {
+    const int sub = lane % (D / 8), h = p.rope_dim / 16;   // h lanes hold half the rotated part
+    e0 = sub * 8;
+    turned = sub < 2 * h;
+    second = sub >= h;
+    const int shift = (p.interleaved || !turned) ? 0 : (second ? -h : h);
+    partner = e0 + 8 * shift;
+    src = lane + shift;
+  }
+};
+
+// This lane's factors from its token's table: y_e = c_e x_e + s_e x_partner, with
+// the sign of the pair's side (and `sign`: -1 turns back) in s. Elements past
+// rope_dim get c = 1, s = 0.
+template <int D>
+struct Turn {
+  uint64_t c[4], s[4];
+  __device__ __forceinline__ Turn(const HeadsParams& p, const Place<D>& at, const float2* table,
+                                  float sign) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = f2_pack(1.f, 1.f);
+      s[i] = f2_pack(0.f, 0.f);
+    }
+    if (!at.turned) return;
+    if (p.interleaved) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = table[at.e0 / 2 + i];
+        c[i] = f2_pack(t.x, t.x);
+        s[i] = f2_pack(-sign * t.y, sign * t.y);
+      }
+    } else {
+      const float2* t = table + (at.second ? at.partner : at.e0);
+      const float sg = at.second ? sign : -sign;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = t[2 * i], b = t[2 * i + 1];
+        c[i] = f2_pack(a.x, b.x);
+        s[i] = f2_pack(sg * a.y, sg * b.y);
+      }
+    }
+  }
+};
+
+// The partners of a loaded vector's elements (every lane of the warp calls it).
+template <typename T, int D>
+__device__ __forceinline__ void partners(const HeadsParams& p, const Place<D>& at, const Raw<T>& x,
+                                         uint64_t (&o)[4]) {
+  if (p.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = f2_swap(x.pair(i));
+  } else {
+    const Raw<T> r = x.from_lane(at.src);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = r.pair(i);
+  }
+}
 
 template <int D>
 __device__ __forceinline__ float head_sum(float x) {
@@ -127,160 +198,293 @@ __device__ __forceinline__ float head_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) {
-  float s0 = 0.f, s1 = 0.f;
+__device__ __forceinline__ float dot(const uint64_t (&a)[4], const uint64_t (&b)[4]) {
+  uint64_t t = f2_mul(a[0], b[0]);
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    s0 = fmaf(a[e], b[e], s0);
-    s1 = fmaf(a[e + 1], b[e + 1], s1);
-  }
-  return s0 + s1;
+  for (int i = 1; i < 4; ++i) t = f2_fma(a[i], b[i], t);
+  float x, y;
+  f2_unpack(t, x, y);
+  return x + y;
 }
 
+// Tokens a block takes at a time, at most (its table: kTokens * d / 2 pairs).
+constexpr int kTokens = 8;
+// Resident blocks an SM and groups a warp has in flight (16-bit types; fp32, with
+// twice the bytes a group, half). Measured at 8192 tokens, 32 + 8 heads, d = 128,
+// bf16: forward 39.8 us with 4 blocks and 3 groups, 40.0 with 4 and 2, 43.7 with 2
+// and 8, 61.7 with 6 and 1 (registers spill); backward, persistent, 59.2 us with
+// 2 blocks and 4 groups (each a dy and an x), 66 with 2 and 3, 83 with 3 and 4.
+constexpr int kFwdBlocks = 4, kFwdFlight = 3;
+constexpr int kBwdBlocks = 2, kBwdFlight = 4;
+// Warps an SM up to which tokens are spread over more warps than one: a warp's
+// set-up (sin and cos, factors, offsets) is worth about five groups, so more
+// warps than these cost more than they hide (2000 tokens of the same heads:
+// forward 13.0 us at 16, 15.0 at 32; backward 19.6 at 8, 22.1 at 16).
+constexpr int kFwdWarps = 16, kBwdWarps = 8;
+
+// How blocks share the tokens and their head groups: a block takes `tokens`
+// tokens (a power of two), kWarpsH / tokens = 2^log2_warps warps each, or, with
+// one token, one of `splits` parts of its groups (blockIdx.y).
+struct Shares {
+  int tokens, log2_warps, splits;
+  Shares(int tokens, int splits) : tokens(tokens), log2_warps(0), splits(splits) {
+    while (tokens << log2_warps < kWarpsH) ++log2_warps;
+  }
+};
+
+// The warp's groups of one class of H heads: g = start, start + W, ... below
+// `groups`. `before` groups of the token belong to the classes before it, so
+// that warps without a group of one class get the next one's.
+struct Groups {
+  int start, groups;
+  __device__ __forceinline__ Groups(int w, int W, int before, int H, int heads) {
+    groups = (H + heads - 1) / heads;
+    start = (w - before) % W;
+    if (start < 0) start += W;
+  }
+};
+
 // ---------------------------------------------------------------- forward --
-// Warp task: one token, `passes` groups of heads from `chunk * passes` on. Head
-// index h: query heads, then key heads, then (append) value heads, which are
-// copied. Append: row s stands at position seq_lens[b] - S + s and its key and
-// value go to that row of the sequence's pages; a position below 0 or a page
-// outside the cache is not stored.
+// Classes: query, key and (append) value heads, which are copied. Append: row s
+// stands at position seq_lens[b] - S + s and its key and value go to that row of
+// the sequence's pages; a position below 0 or a page outside the cache is not
+// stored.
 template <typename T, int D, bool kAppend>
-__global__ void __launch_bounds__(32 * kWarpsH)
-    heads_fwd_kernel(const __grid_constant__ HeadsParams p, int passes, int chunks) {
-  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;   // lanes a head, heads a pass
-  const int lane = threadIdx.x & 31;
-  const int sub = lane % kLanes;
-  const long long task = static_cast<long long>(blockIdx.x) * kWarpsH + (threadIdx.x >> 5);
-  const long long token = task / chunks;
-  if (token >= static_cast<long long>(p.B) * p.S) return;
-  const int chunk = static_cast<int>(task - token * chunks);
-  const int b = static_cast<int>(token / p.S), s = static_cast<int>(token % p.S);
-  const int H = p.Hq + (kAppend ? 2 : 1) * p.Hkv;
+__global__ void __launch_bounds__(32 * kWarpsH, kFwdBlocks)
+    heads_fwd_kernel(const __grid_constant__ HeadsParams p, const Shares sh) {
+  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;   // lanes a head, heads a group
+  constexpr int kFlight = sizeof(T) == 4 ? (kFwdFlight + 1) / 2 : kFwdFlight;
+  constexpr int kClasses = kAppend ? 3 : 2;
+  __shared__ float2 table[kTokens][D / 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Place<D> at(p, lane);
+  const int hl = lane / kLanes;
+  const int W = kWarpsH / sh.tokens * sh.splits;
+  // this warp's token, and its number among the warps that share it
+  const int t = warp >> sh.log2_warps;
+  const int w = (warp & (kWarpsH / sh.tokens - 1)) + static_cast<int>(blockIdx.y) * kWarpsH;
+  const unsigned token = blockIdx.x * sh.tokens + t;   // B * S < 2^31
+  const bool live = token < static_cast<unsigned>(p.B) * p.S;
+  const int b = live ? static_cast<int>(token / p.S) : 0;
+  const int s = live ? static_cast<int>(token - static_cast<unsigned>(b) * p.S) : 0;
+
+  const T* in;
+  long long in_step;   // between groups of the warp
+  int heads;
+  Groups gr(0, 1, 0, 0, 1);
+  auto enter = [&](int c) {
+    const HeadView& v = c == 0 ? p.q : (c == 1 ? p.k : p.v);
+    heads = c == 0 ? p.Hq : p.Hkv;
+    const int gq = (p.Hq + kHeads - 1) / kHeads, gk = (p.Hkv + kHeads - 1) / kHeads;
+    gr = Groups(w, W, c == 0 ? 0 : (c == 1 ? gq : gq + gk), heads, kHeads);
+    if (!live) gr.groups = 0;
+    in = static_cast<const T*>(v.data) + b * v.sb + s * v.ss + at.e0 + (gr.start * kHeads + hl) * v.sh;
+    in_step = v.sh * (kHeads * W);
+  };
+  Raw<T> raw[kFlight];
+  auto load = [&](int g) {   // groups g, g + W, ...; `in` moves past them
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      raw[u].zero();
+      if (g + u * W < gr.groups && (g + u * W) * kHeads + hl < heads) raw[u].load(in);
+      in += in_step;
+    }
+  };
+  int c = 0;
+  enter(0);
+  while (gr.start >= gr.groups && c < kClasses - 1) enter(++c);
+  load(gr.start);
+
   int position = s;
-  long long page_row = -1;   // append: row of the cache [block][Hkv][block_size], head 0
+  if (live) {
+    if constexpr (kAppend) position = p.seq_lens[b] - p.S + s;
+    else if (p.positions) position = p.positions[token];
+  }
+  fill_table(p, table[t], position, lane, warp & (kWarpsH / sh.tokens - 1), kWarpsH / sh.tokens);
+  long long page_row = -1;   // append: row of the cache [block][Hkv][block_size]
   if constexpr (kAppend) {
-    position = p.seq_lens[b] - p.S + s;
-    if (position >= 0 && position / p.block_size < p.max_blocks) {
+    if (live && position >= 0 && position / p.block_size < p.max_blocks) {
       const int pb = p.block_table[static_cast<size_t>(b) * p.max_blocks + position / p.block_size];
       if (pb >= 0 && pb < p.num_blocks)
         page_row = static_cast<long long>(pb) * p.Hkv * p.block_size + position % p.block_size;
     }
-  } else if (p.positions) {
-    position = p.positions[token];
   }
-  Turn<D> turn;
-  turn.set(p, sub, position);
-  const int h0 = chunk * passes * kHeads + lane / kLanes;
-  for (int i = 0; i < passes; ++i) {
-    const int h = h0 + i * kHeads;
-    const bool live = h < H;
-    const bool is_q = h < p.Hq, is_v = kAppend && h >= p.Hq + p.Hkv;
-    const int hh = is_q ? h : (is_v ? h - p.Hq - p.Hkv : h - p.Hq);
-    const HeadView& in = is_q ? p.q : (is_v ? p.v : p.k);
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (live) load8<T>(in.data, b * in.sb + hh * in.sh + s * in.ss + sub * 8, x);
-    if (p.wq) {
-      const float r = rsqrtf(head_sum<D>(dot8(x, x)) * (1.f / D) + p.eps);
-      if (live && !is_v) {
-        float w[8];
-        load8<T>(is_q ? p.wq : p.wk, sub * 8, w);
+  __syncthreads();
+
+  for (bool loaded = true;; loaded = false) {
+    const T* weight = static_cast<const T*>(c == 0 ? p.wq : p.wk);
+    const bool norm = weight != nullptr;
+    T* out;
+    long long out_step;
+    bool store = true;
+    if (!kAppend || c == 0) {
+      const HeadView& v = c == 0 ? p.q_out : p.k_out;
+      out = static_cast<T*>(v.data) + b * v.sb + s * v.ss;
+      out_step = v.sh;
+    } else {
+      out = static_cast<T*>(c == 1 ? p.k_cache : p.v_cache) + page_row * D;
+      out_step = static_cast<long long>(p.block_size) * D;
+      store = page_row >= 0;
+    }
+    out += at.e0 + (gr.start * kHeads + hl) * out_step;
+    out_step *= kHeads * W;
+    Turn<D> f(p, at, table[t], 1.f);   // the factors of x and of its partner
+    if (norm && c < 2) {
+      Raw<T> mine, other;
+      mine.load(weight + at.e0);
+      other.load(weight + at.partner);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
+      for (int i = 0; i < 4; ++i) {
+        f.c[i] = f2_mul(f.c[i], mine.pair(i));
+        f.s[i] = f2_mul(f.s[i], p.interleaved ? f2_swap(mine.pair(i)) : other.pair(i));
       }
     }
-    float y[8];
+    for (int g = gr.start; g < gr.groups; g += kFlight * W, loaded = false) {
+      if (!loaded) load(g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = x[e];
-    turn.apply(p, lane, 1.f, y);
-    if (!live) continue;
-    if (!kAppend || is_q) {
-      const HeadView& out = is_q ? p.q_out : p.k_out;
-      store8<T>(out.data, b * out.sb + hh * out.sh + s * out.ss + sub * 8, y);
-    } else if (page_row >= 0) {
-      const long long at = (page_row + static_cast<long long>(hh) * p.block_size) * D + sub * 8;
-      if (is_v) store8<T>(p.v_cache, at, x);
-      else store8<T>(p.k_cache, at, y);
+      for (int u = 0; u < kFlight; ++u) {
+        if (g + u * W < gr.groups) {   // warp-uniform
+          if (!kAppend || c < 2) {
+            uint64_t x[4], o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = raw[u].pair(i);
+            partners<T, D>(p, at, raw[u], o);
+            const float r = norm ? rsqrt_approx(head_sum<D>(dot(x, x)) * (1.f / D) + p.eps) : 1.f;
+            const uint64_t rr = f2_pack(r, r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              raw[u].set_pair(i, f2_mul(rr, f2_fma(f.c[i], x[i], f2_mul(f.s[i], o[i]))));
+          }
+          if (store && (g + u * W) * kHeads + hl < heads) raw[u].store(out);
+          out += out_step;
+        }
+      }
     }
+    if (++c >= kClasses) break;
+    enter(c);
   }
 }
 
 // --------------------------------------------------------------- backward --
-// Warps stride over the tokens; each does all heads of a token. A lane's share
-// of dw_q and dw_k (its 8 columns) is summed in registers over all its tokens,
-// then over the block's warps, then over the blocks by the reduce kernel, always
-// in the same order.
+// Blocks stride over groups of tokens, as the forward takes them (splits = 1). A
+// lane's share of dw_q and dw_k (its 8 columns) is summed in registers over all
+// its tokens, then over the block's warps, then over the blocks by the reduce
+// kernel, always in the same order.
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kWarpsH)
-    heads_bwd_kernel(const __grid_constant__ HeadsParams p) {
+__global__ void __launch_bounds__(32 * kWarpsH, kBwdBlocks)
+    heads_bwd_kernel(const __grid_constant__ HeadsParams p, const Shares sh) {
   constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
+  constexpr int kFlight = sizeof(T) == 4 ? kBwdFlight / 2 : kBwdFlight;
+  __shared__ float2 table[2][kTokens][D / 2];
+  __shared__ float part[kWarpsH][2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = lane % kLanes;
-  const int H = p.Hq + p.Hkv;
+  const Place<D> at(p, lane);
+  const int hl = lane / kLanes;
+  const int W = kWarpsH / sh.tokens;
+  const int t = warp >> sh.log2_warps, w = warp & (W - 1);
   const bool norm = p.wq != nullptr;
-  float wq[8], wk[8], dwq[8], dwk[8];
+  uint64_t dw[2][4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.f;
-  if (norm) {
-    load8<T>(p.wq, sub * 8, wq);
-    load8<T>(p.wk, sub * 8, wk);
-  }
-  const long long tokens = static_cast<long long>(p.B) * p.S;
-  for (long long token = static_cast<long long>(blockIdx.x) * kWarpsH + warp; token < tokens;
-       token += static_cast<long long>(gridDim.x) * kWarpsH) {
-    const int b = static_cast<int>(token / p.S), s = static_cast<int>(token % p.S);
-    Turn<D> turn;
-    turn.set(p, sub, p.positions ? p.positions[token] : s);
-    for (int g = 0; g < H; g += kHeads) {
-      const int h = g + lane / kLanes;
-      const bool live = h < H, is_q = h < p.Hq;
-      const int hh = is_q ? h : h - p.Hq;
-      const HeadView& dy = is_q ? p.q_out : p.k_out;
-      const HeadView& in = is_q ? p.q : p.k;
-      const HeadView& dx = is_q ? p.dq : p.dk;
-      float dn[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (live) {
-        load8<T>(dy.data, b * dy.sb + hh * dy.sh + s * dy.ss + sub * 8, dn);
-        if (norm) load8<T>(in.data, b * in.sb + hh * in.sh + s * in.ss + sub * 8, x);
-      }
-      turn.apply(p, lane, -1.f, dn);
+  for (int i = 0; i < 4; ++i) dw[0][i] = dw[1][i] = f2_pack(0.f, 0.f);
+  const unsigned all = static_cast<unsigned>(p.B) * p.S;   // < 2^31
+  int flip = 0;
+  for (unsigned first = blockIdx.x * sh.tokens; first < all; first += gridDim.x * sh.tokens, flip ^= 1) {
+    const unsigned token = first + t;
+    const bool live = token < all;
+    const int b = live ? static_cast<int>(token / p.S) : 0;
+    const int s = live ? static_cast<int>(token - static_cast<unsigned>(b) * p.S) : 0;
+    if (live) fill_table(p, table[flip][t], p.positions ? p.positions[token] : s, lane, w, W);
+    __syncthreads();   // the other table's readers are past it when this one is written again
+    if (!live) continue;
+    const Turn<D> turn(p, at, table[flip][t], -1.f);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const HeadView& vy = c == 0 ? p.q_out : p.k_out;
+      const HeadView& vx = c == 0 ? p.q : p.k;
+      const HeadView& vd = c == 0 ? p.dq : p.dk;
+      const int heads = c == 0 ? p.Hq : p.Hkv;
+      const Groups gr(w, W, c == 0 ? 0 : (p.Hq + kHeads - 1) / kHeads, heads, kHeads);
+      const int h0 = gr.start * kHeads + hl;
+      const T* dy = static_cast<const T*>(vy.data) + b * vy.sb + s * vy.ss + at.e0 + h0 * vy.sh;
+      const T* xs = static_cast<const T*>(vx.data) + b * vx.sb + s * vx.ss + at.e0 + h0 * vx.sh;
+      T* dx = static_cast<T*>(vd.data) + b * vd.sb + s * vd.ss + at.e0 + h0 * vd.sh;
+      const int step = kHeads * W;
+      uint64_t wt[4];
       if (norm) {
-        const float r = rsqrtf(head_sum<D>(dot8(x, x)) * (1.f / D) + p.eps);
-        float gx[8];
+        Raw<T> v;
+        v.load(static_cast<const T*>(c == 0 ? p.wq : p.wk) + at.e0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float t = dn[e] * (x[e] * r);
-          if (is_q) dwq[e] += t;
-          else dwk[e] += t;
-          gx[e] = dn[e] * (is_q ? wq[e] : wk[e]);
-        }
-        const float m = head_sum<D>(dot8(gx, x)) * (1.f / D) * r * r;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dn[e] = r * (gx[e] - x[e] * m);
+        for (int i = 0; i < 4; ++i) wt[i] = v.pair(i);
       }
-      if (live) store8<T>(dx.data, b * dx.sb + hh * dx.sh + s * dx.ss + sub * 8, dn);
+      for (int g = gr.start; g < gr.groups; g += kFlight * W) {
+        Raw<T> ry[kFlight], rx[kFlight];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+          ry[u].zero();
+          rx[u].zero();
+          if (g + u * W < gr.groups && (g + u * W) * kHeads + hl < heads) {
+            ry[u].load(dy);
+            if (norm) rx[u].load(xs);
+          }
+          dy += step * vy.sh;
+          xs += step * vx.sh;
+        }
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+          if (g + u * W < gr.groups) {   // warp-uniform
+            uint64_t dn[4], o[4];
+            partners<T, D>(p, at, ry[u], o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dn[i] = f2_fma(turn.c[i], ry[u].pair(i), f2_mul(turn.s[i], o[i]));
+            if (norm) {
+              uint64_t x[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                x[i] = rx[u].pair(i);
+                o[i] = f2_mul(dn[i], wt[i]);   // g = w dn
+              }
+              const float r = rsqrt_approx(head_sum<D>(dot(x, x)) * (1.f / D) + p.eps);
+              const float m = head_sum<D>(dot(o, x)) * (1.f / D) * r;
+              const uint64_t rr = f2_pack(r, r), nm = f2_pack(-m, -m);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                x[i] = f2_mul(x[i], rr);
+                dw[c][i] = f2_fma(dn[i], x[i], dw[c][i]);
+                dn[i] = f2_mul(rr, f2_fma(nm, x[i], o[i]));
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ry[u].set_pair(i, dn[i]);
+            if ((g + u * W) * kHeads + hl < heads) ry[u].store(dx);
+            dx += step * vd.sh;
+          }
+        }
+      }
     }
   }
   if (!norm) return;
   // lanes of one column group, then warps
-  __shared__ float part[kWarpsH][2][D];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int c = 0; c < 2; ++c) {
 #pragma unroll
-    for (int o = kLanes; o < 32; o <<= 1) {
-      dwq[e] += __shfl_xor_sync(kFull, dwq[e], o);
-      dwk[e] += __shfl_xor_sync(kFull, dwk[e], o);
-    }
-    if (lane < kLanes) {
-      part[warp][0][sub * 8 + e] = dwq[e];
-      part[warp][1][sub * 8 + e] = dwk[e];
+    for (int i = 0; i < 4; ++i) {
+      float v[2];
+      f2_unpack(dw[c][i], v[0], v[1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = kLanes; o < 32; o <<= 1) v[e] += __shfl_xor_sync(kFull, v[e], o);
+        if (lane < kLanes) part[warp][c][at.e0 + 2 * i + e] = v[e];
+      }
     }
   }
   __syncthreads();
   for (int c = threadIdx.x; c < 2 * D; c += blockDim.x) {
-    float t = 0.f;
+    float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarpsH; ++w) t += part[w][c / D][c % D];
-    p.dw_part[static_cast<size_t>(blockIdx.x) * 2 * D + c] = t;
+    for (int i = 0; i < kWarpsH; ++i) sum += part[i][c / D][c % D];
+    p.dw_part[static_cast<size_t>(blockIdx.x) * 2 * D + c] = sum;
   }
 }
 
@@ -302,27 +506,37 @@ __global__ void __launch_bounds__(256) heads_dw_kernel(const __grid_constant__ H
   }
 }
 
-// Head groups a warp takes: all of a token's where the tokens alone fill the GPU
-// with warps (one conversion of phases into sin and cos for all heads), fewer
-// where they do not, down to one.
+// Tokens a block takes at a time: as many as it has warps when the tokens alone
+// give every SM `warps` warps, else fewer, down to one (never more warps a token
+// than it has groups).
+int tokens_per_block(long long tokens, int groups, int warps) {
+  int W = 1;
+  while (W < kWarpsH && W < groups && tokens * W < static_cast<long long>(kSms) * warps) W *= 2;
+  return kWarpsH / W;
+}
+
+int heads_bwd_tokens(int B, int Hq, int Hkv, int S, int d) {
+  const int heads = 32 / (d / 8);
+  return tokens_per_block(static_cast<long long>(B) * S, (Hq + heads - 1) / heads + (Hkv + heads - 1) / heads, kBwdWarps);
+}
+
+// With few tokens, as many blocks a token as give each group a warp of its own.
 template <typename T, int D, bool kAppend>
 cudaError_t launch_fwd_impl(const HeadsParams& p, cudaStream_t stream) {
   constexpr int kHeads = 32 / (D / 8);
-  const int H = p.Hq + (kAppend ? 2 : 1) * p.Hkv;
-  const int groups = (H + kHeads - 1) / kHeads;
   const long long tokens = static_cast<long long>(p.B) * p.S;
-  const long long fill = kSms * 32LL;   // warps
-  const int passes = static_cast<int>(std::max<long long>(1, std::min<long long>(groups, tokens * groups / fill)));
-  const int chunks = (groups + passes - 1) / passes;
-  const long long blocks = (tokens * chunks + kWarpsH - 1) / kWarpsH;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  heads_fwd_kernel<T, D, kAppend><<<static_cast<unsigned>(blocks), 32 * kWarpsH, 0, stream>>>(p, passes, chunks);
+  const int groups = (p.Hq + kHeads - 1) / kHeads + (kAppend ? 2 : 1) * ((p.Hkv + kHeads - 1) / kHeads);
+  Shares sh(tokens_per_block(tokens, groups, kFwdWarps), 1);
+  if (sh.tokens == 1 && tokens < kSms) sh.splits = std::min((groups + kWarpsH - 1) / kWarpsH, 65535);
+  const dim3 grid(static_cast<unsigned>((tokens + sh.tokens - 1) / sh.tokens), sh.splits);
+  heads_fwd_kernel<T, D, kAppend><<<grid, 32 * kWarpsH, 0, stream>>>(p, sh);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t launch_bwd_impl(const HeadsParams& p, cudaStream_t stream) {
-  heads_bwd_kernel<T, D><<<static_cast<unsigned>(p.n_blocks), 32 * kWarpsH, 0, stream>>>(p);
+  const Shares sh(heads_bwd_tokens(p.B, p.Hq, p.Hkv, p.S, p.d), 1);
+  heads_bwd_kernel<T, D><<<static_cast<unsigned>(p.n_blocks), 32 * kWarpsH, 0, stream>>>(p, sh);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.wq) return e;
   heads_dw_kernel<<<2 * D / 32, 256, 0, stream>>>(p);
@@ -343,9 +557,10 @@ cudaError_t dispatch_fwd(const HeadsParams& p, cudaStream_t st) {
 
 }  // namespace
 
-int heads_bwd_blocks(int B, int S) {
+int heads_bwd_blocks(int B, int Hq, int Hkv, int S, int d) {
   const long long tokens = static_cast<long long>(B) * S;
-  return static_cast<int>(std::max<long long>(1, std::min<long long>((tokens + kWarpsH - 1) / kWarpsH, kSms * 4LL)));
+  const int per = heads_bwd_tokens(B, Hq, Hkv, S, d);
+  return static_cast<int>(std::min<long long>((tokens + per - 1) / per, static_cast<long long>(kSms) * kBwdBlocks));
 }
 
 cudaError_t launch_heads_fwd(const HeadsParams& p, cudaStream_t stream) {

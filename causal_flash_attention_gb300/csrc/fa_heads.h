@@ -41,7 +41,7 @@ struct HeadsParams {
 };
 
 // Blocks of the backward (and partial weight gradients) for these sizes.
-int heads_bwd_blocks(int B, int S);
+int heads_bwd_blocks(int B, int Hq, int Hkv, int S, int d);
 
 cudaError_t launch_heads_fwd(const HeadsParams& p, cudaStream_t stream);
 cudaError_t launch_heads_append(const HeadsParams& p, cudaStream_t stream);

@@ -261,9 +261,9 @@ int fa_qk_norm_rope_bwd(const fa_view* dq_out, const fa_view* dk_out, const fa_v
                         float rope_scale, int B, int Hq, int Hkv, int S, int d, int dtype,
                         void* workspace, size_t workspace_bytes, fa_stream_t stream);
 
-/* Workspace bytes of fa_qk_norm_rope_bwd: 2 d floats for each of at most 608
+/* Workspace bytes of fa_qk_norm_rope_bwd: 2 d floats for each of at most 304
  * CTAs; 0 without the norm (norm == 0) and for invalid sizes. */
-size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int S, int d, int norm);
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int Hq, int Hkv, int S, int d, int norm);
 
 /*
  * The serving form: the last Sq tokens of each of B sequences. Row s of

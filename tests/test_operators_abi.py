@@ -152,10 +152,11 @@ def test_append_refuses(fa_lib, kw, code):
 
 
 def test_norm_rope_workspace(fa_lib):
-    assert fa_lib.fa_qk_norm_rope_bwd_workspace_bytes(1, 1, 64) == 2 * 64 * 4
-    assert fa_lib.fa_qk_norm_rope_bwd_workspace_bytes(64, 8192, 128) == 608 * 2 * 128 * 4
-    assert fa_lib.fa_qk_norm_rope_bwd_workspace_bytes(4, 100, 64, norm=False) == 0
-    assert fa_lib.fa_qk_norm_rope_bwd_workspace_bytes(0, 100, 64) == 0
+    f = fa_lib.fa_qk_norm_rope_bwd_workspace_bytes
+    assert f(1, 2, 1, 1, 64) == 2 * 64 * 4                       # one block of partial sums
+    assert f(64, 32, 8, 8192, 128) == 304 * 2 * 128 * 4          # the most
+    assert f(4, 2, 1, 100, 64, norm=False) == 0
+    assert f(0, 2, 1, 100, 64) == 0 and f(1, 3, 2, 100, 64) == 0 and f(1, 2, 1, 100, 80) == 0
 
 
 # --------------------------------------------------------------- the binding --
