@@ -201,7 +201,7 @@ RaggedPlan ragged_plan(int B, int Hq, int Hkv, int Sq, int d, int block_size, in
   rp.part_out = 0;
   rp.part_lse2 = static_cast<size_t>(round_up(rows * d * 4, 256));
   rp.prefix = rp.part_lse2 + static_cast<size_t>(round_up(rows * 4, 256));
-  rp.total = rp.prefix + static_cast<size_t>(round_up((B + 1LL) * 8, 256));
+  rp.total = rp.prefix + static_cast<size_t>(round_up((B + 1LL) * 4, 256));
   return rp;
 }
 
@@ -211,9 +211,13 @@ bool block_sizes_ok(int Hkv, int block_size, int num_blocks, int max_blocks) {
          num_blocks >= 1 && static_cast<long long>(num_blocks) * Hkv <= (1LL << 30) &&
          max_blocks >= 1;
 }
-bool paged_sizes_ok(int Hq, int Hkv, int Sq, int block_size, int num_blocks, int max_blocks) {
-  return static_cast<long long>(Hq / Hkv) * Sq <= kDecodeMaxRows &&
-         block_sizes_ok(Hkv, block_size, num_blocks, max_blocks);
+bool paged_sizes_ok(int B, int Hq, int Hkv, int Sq, int block_size, int num_blocks, int max_blocks) {
+  if (static_cast<long long>(Hq / Hkv) * Sq > kDecodeMaxRows ||
+      !block_sizes_ok(Hkv, block_size, num_blocks, max_blocks))
+    return false;
+  // the list of key tiles is counted in 32 bits
+  const long long tiles = (static_cast<long long>(max_blocks) * block_size + kTileN - 1) / kTileN;
+  return tiles <= 0x7fffffffLL / (static_cast<long long>(B) * Hkv);
 }
 
 // Arguments the query/key preparation entry points share.
@@ -784,7 +788,7 @@ int fa_bwd_span(const void* q, const void* k, const void* v, const int* key_begi
 size_t fa_fwd_ragged_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int d, int block_size,
                                            int max_blocks) {
   if (check_common(B, Hq, Hkv, Sq, Sq, d, 0, 1.f, FA_BF16) != FA_OK ||
-      !paged_sizes_ok(Hq, Hkv, Sq, block_size, 1, max_blocks))
+      !paged_sizes_ok(B, Hq, Hkv, Sq, block_size, 1, max_blocks))
     return 0;
   return ragged_plan(B, Hq, Hkv, Sq, d, block_size, max_blocks).total;
 }
@@ -798,7 +802,7 @@ int fa_fwd_ragged_paged(const void* q, const void* k_cache, const void* v_cache,
   int rc = check_common(B, Hq, Hkv, Sq, Sq, d, 0, scale, dtype);
   if (rc != FA_OK) return rc;
   if (dtype == FA_F32) return FA_ERR_DTYPE;   // the paged path runs on the tensor cores only
-  if (!paged_sizes_ok(Hq, Hkv, Sq, block_size, num_blocks, max_blocks) || window < 0)
+  if (!paged_sizes_ok(B, Hq, Hkv, Sq, block_size, num_blocks, max_blocks) || window < 0)
     return FA_ERR_SHAPE;
   if (!(std::isfinite(softcap) && softcap >= 0.f)) return FA_ERR_SCALE;
   if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !lse) return FA_ERR_NULL;
@@ -827,7 +831,8 @@ int fa_fwd_ragged_paged(const void* q, const void* k_cache, const void* v_cache,
   p.slopes = slopes;
   p.part_out = reinterpret_cast<float*>(wsb + rp.part_out);
   p.part_lse2 = reinterpret_cast<float*>(wsb + rp.part_lse2);
-  p.prefix = reinterpret_cast<long long*>(wsb + rp.prefix);
+  p.prefix = reinterpret_cast<int*>(wsb + rp.prefix);
+  p.capacity = static_cast<int>(std::min(static_cast<long long>(max_blocks) * block_size, 0x7fffff80LL));
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Sq = Sq;
   p.G = Hq / Hkv;
   p.R = rp.R;

@@ -53,7 +53,7 @@ struct RagCfg {
   static constexpr int kNumBars = 1 + 4 * kStages + 6 + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffScan = kOffMisc + 16;            // 6 warp totals, start (b, prefix)
-  static constexpr int kSmemBytes = kOffScan + 64 + 1024;   // + alignment slack
+  static constexpr int kSmemBytes = kOffScan + 32 + 1024;   // + alignment slack
 };
 
 __device__ __forceinline__ void drain_wait_r(uint32_t bar, uint32_t parity, int* status) {
@@ -74,51 +74,101 @@ struct SeqKeys {
 
 __device__ __forceinline__ SeqKeys seq_keys(const RaggedParams& p, int b) {
   SeqKeys s;
-  const long long capacity = static_cast<long long>(p.max_blocks) * p.block_size;
-  s.len = static_cast<int>(
-      min(static_cast<long long>(max(p.seq_lens[b], 0)), min(capacity, 0x7fffff00LL)));
+  s.len = min(max(p.seq_lens[b], 0), p.capacity);
   s.first = p.window > 0 ? max(0, s.len - p.Sq + 1 - p.window) : 0;
   s.tile0 = s.first / kTileN;
   s.n = s.len > 0 ? (s.len + kTileN - 1) / kTileN - s.tile0 : 0;
   return s;
 }
 
-// Shares of a list of `total` tiles: no more than it has tiles, so that none is
+// Even shares of a list of `total` tiles (below 2^31): the first `rest` shares
+// take one tile more than the others. No more shares than tiles, so that none is
 // empty (the merge reads a part of every share between a head's first and last).
-__device__ __forceinline__ int n_shares(const RaggedParams& p, long long total) {
-  return static_cast<int>(min(static_cast<long long>(p.n_ctas), total));
-}
-__device__ __forceinline__ long long share_begin(long long total, int c, int n) {
-  return total * c / n;
+struct ShareOut {
+  int shares, each, rest;
+  __device__ __forceinline__ ShareOut(int n_ctas, int total) {
+    shares = min(n_ctas, total);
+    each = shares > 0 ? total / shares : 0;
+    rest = total - each * shares;
+  }
+  __device__ __forceinline__ int begin(int c) const { return c * each + min(c, rest); }
+  __device__ __forceinline__ int of_tile(int t) const {
+    const int big = rest * (each + 1);   // tiles of the larger shares
+    return t < big ? t / (each + 1) : rest + (t - big) / each;
+  }
+};
+
+// A CTA's share, found by all its threads: a scan over the sequences' tile
+// counts. CTA 0 also writes the sums for the merge. Two barriers.
+struct Share {
+  int begin, end;    // tiles of the list
+  int b, pre;        // the first tile's sequence, and tiles per head before it
+};
+
+__device__ __forceinline__ Share find_share(const RaggedParams& p, int cta, int* scan) {
+  const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
+  // thread t holds sequences [t * per, (t + 1) * per)
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per);
+  const int b_hi = min(p.B, b_lo + per);
+  int mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += seq_keys(p, b).n;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  int pre = incl - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) pre += scan[w];
+    total += scan[w];
+  }
+  const ShareOut out(p.n_ctas, total * p.Hkv);
+  Share s;
+  s.begin = cta < out.shares ? out.begin(cta) : 0;
+  s.end = cta < out.shares ? out.begin(cta + 1) : 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int n = seq_keys(p, b).n;
+    if (s.begin < s.end && pre * p.Hkv <= s.begin && s.begin < (pre + n) * p.Hkv) {
+      scan[6] = b;
+      scan[7] = pre;
+    }
+    if (cta == 0) p.prefix[b] = pre;
+    pre += n;
+    if (cta == 0 && b == p.B - 1) p.prefix[p.B] = pre;
+  }
+  __syncthreads();
+  s.b = s.begin < s.end ? scan[6] : 0;
+  s.pre = s.begin < s.end ? scan[7] : 0;
+  return s;
 }
 
 // The segments of one CTA's share, in order; every role walks its own copy.
 struct Segments {
-  long long cur, end, pre;   // list position, end of the share, tiles per head before b
+  int cur, end, pre;   // list position, end of the share, tiles per head before b
   int b;
   SeqKeys keys;
   // the current segment
   int kvh, tile0, n;
   bool whole;
 
-  __device__ void init(const RaggedParams& p, long long begin, long long stop, int b0,
-                       long long pre0) {
-    cur = begin;
-    end = stop;
-    b = b0;
-    pre = pre0;
+  __device__ __forceinline__ Segments(const RaggedParams& p, const Share& s)
+      : cur(s.begin), end(s.end), pre(s.pre), b(s.b) {
     if (cur < end) keys = seq_keys(p, b);
   }
-  __device__ bool next(const RaggedParams& p) {
+  __device__ __forceinline__ bool next(const RaggedParams& p) {
     if (cur >= end) return false;
     while (cur >= (pre + keys.n) * p.Hkv) {   // cur < end <= total: some later b has tiles
       pre += keys.n;
       keys = seq_keys(p, ++b);
     }
-    const long long off = cur - pre * p.Hkv;
-    kvh = static_cast<int>(off / keys.n);
-    const int t = static_cast<int>(off - static_cast<long long>(kvh) * keys.n);
-    n = static_cast<int>(min(static_cast<long long>(keys.n - t), end - cur));
+    const int off = cur - pre * p.Hkv;
+    kvh = off / keys.n;
+    const int t = off - kvh * keys.n;
+    n = min(keys.n - t, end - cur);
     tile0 = keys.tile0 + t;
     whole = n == keys.n;
     cur += n;
@@ -126,6 +176,71 @@ struct Segments {
   }
 };
 
+// TMA producer warp of both kernels: K and V tiles of the share into rings of
+// kStages. Each lane i < 128 / box_rows reads the block-table entry of box i of a
+// tile and issues that box itself. A block past the sequence, or a table entry
+// outside [0, num_blocks), is loaded from an out-of-range row, which the copy
+// fills with zeros.
+template <int kChunks, int kStages, class Bar>
+__device__ __forceinline__ void produce(const RaggedParams& p, Segments& seg, uint32_t k_ring,
+                                        uint32_t v_ring, Bar k_full, Bar k_empty, Bar v_full,
+                                        Bar v_empty, volatile int* abort_flag) {
+  constexpr int kTileBytes = kChunks * kTileN * 128;
+  const int lane = static_cast<int>(lane_id());
+  const int n_boxes = kTileN / p.box_rows;
+  auto load_part = [&](const CUtensorMap* tm, uint32_t dst, uint32_t bar, int key, int pb) {
+    if (lane >= n_boxes) return;
+    const bool in_range = pb >= 0 && pb < p.num_blocks;
+    const int y = in_range ? key % p.block_size : p.block_size;
+    const int z = in_range ? pb * p.Hkv + seg.kvh : 0;
+    for (int c = 0; c < kChunks; ++c)
+      tma_load_3d(dst + c * (kTileN * 128) + lane * p.box_rows * 128, tm, bar, c * kChunk, y, z);
+  };
+  int g = 0;   // tiles whose K load has been issued
+  bool stop = false;
+  while (!stop && seg.next(p)) {
+    const int* table = p.block_table + static_cast<size_t>(seg.b) * p.max_blocks;
+    for (int j = 0; j < seg.n; ++j, ++g) {
+      const int key = (seg.tile0 + j) * kTileN + lane * p.box_rows;
+      const int st = g % kStages;
+      const uint32_t use = static_cast<uint32_t>(g / kStages);
+      int pb = -1;
+      if (lane < n_boxes && key < seg.keys.len) pb = table[key / p.block_size];
+      int fail = 0;
+      if (lane == 0) {
+        if (g >= kStages && !mbar_wait(k_empty(st), (use - 1) & 1, abort_flag, p.status)) fail = 1;
+        else mbar_arrive_expect_tx(k_full(st), kTileBytes);
+      }
+      if ((stop = __shfl_sync(0xffffffffu, fail, 0))) break;
+      load_part(&p.tm_k, k_ring + st * kTileBytes, k_full(st), key, pb);
+      if (lane == 0) {
+        if (g >= kStages && !mbar_wait(v_empty(st), (use - 1) & 1, abort_flag, p.status)) fail = 1;
+        else mbar_arrive_expect_tx(v_full(st), kTileBytes);
+      }
+      if ((stop = __shfl_sync(0xffffffffu, fail, 0))) {
+        ++g;   // this tile's K load is in flight
+        break;
+      }
+      load_part(&p.tm_v, v_ring + st * kTileBytes, v_full(st), key, pb);
+    }
+  }
+  if (lane == 0 && *abort_flag) {
+    // let every copy already issued land before the CTA releases its memory
+    for (int gg = max(0, g - kStages); gg < g; ++gg) {
+      const uint32_t par = static_cast<uint32_t>(gg / kStages) & 1;
+      drain_wait_r(k_full(gg % kStages), par, p.status);
+      drain_wait_r(v_full(gg % kStages), par, p.status);
+    }
+  }
+}
+
+// One barrier of a group of consecutive 8-byte barriers.
+struct Bars {
+  uint32_t base;
+  __device__ __forceinline__ uint32_t operator()(int i) const { return base + 8 * i; }
+};
+
+// ------------------------------------------------- one thread per query row --
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_ragged_kernel(const __grid_constant__ RaggedParams p) {
@@ -138,18 +253,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
-  long long* scan = reinterpret_cast<long long*>(smem + Cfg::kOffScan);
+  int* scan = reinterpret_cast<int*>(smem + Cfg::kOffScan);
 
-  const uint32_t bar0 = sbase + Cfg::kOffBar;
-  const uint32_t q_ready = bar0;
-  auto k_full = [&](int s) { return bar0 + 8 * (1 + s); };
-  auto k_empty = [&](int s) { return bar0 + 8 * (1 + NS + s); };
-  auto v_full = [&](int s) { return bar0 + 8 * (1 + 2 * NS + s); };
-  auto v_empty = [&](int s) { return bar0 + 8 * (1 + 3 * NS + s); };
-  auto s_full = [&](int b) { return bar0 + 8 * (1 + 4 * NS + b); };
-  auto p_full = [&](int b) { return bar0 + 8 * (3 + 4 * NS + b); };
-  auto pv_done = [&](int b) { return bar0 + 8 * (5 + 4 * NS + b); };
-  const uint32_t drain = bar0 + 8 * (7 + 4 * NS);
+  const uint32_t q_ready = sbase + Cfg::kOffBar;
+  const Bars k_full{q_ready + 8}, k_empty{k_full(NS)}, v_full{k_empty(NS)}, v_empty{v_full(NS)};
+  const Bars s_full{v_empty(NS)}, p_full{s_full(2)}, pv_done{p_full(2)};
+  const uint32_t drain = pv_done(2);
 
   const int warp = static_cast<int>(warp_id());
   const int lane = static_cast<int>(lane_id());
@@ -179,104 +288,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
 
-  // ---- this CTA's share: a scan over the sequences' tile counts ----
-  // thread t holds sequences [t * per, (t + 1) * per)
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int b_lo = static_cast<int>(min(static_cast<long long>(p.B),
-                                        static_cast<long long>(threadIdx.x) * per));
-  const int b_hi = min(p.B, b_lo + per);
-  long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += seq_keys(p, b).n;
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) scan[warp] = incl;
   tc_fence_before();
-  __syncthreads();
+  const Share share = find_share(p, cta, scan);   // with the barriers that order the set-up
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  long long pre = incl - mine, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) pre += scan[w];
-    total += scan[w];
-  }
-  total *= p.Hkv;
-  const int shares = n_shares(p, total);
-  const long long begin = cta < shares ? share_begin(total, cta, shares) : 0;
-  const long long end = cta < shares ? share_begin(total, cta + 1, shares) : 0;
-  for (int b = b_lo; b < b_hi; ++b) {
-    const int n = seq_keys(p, b).n;
-    if (begin < end && pre * p.Hkv <= begin && begin < (pre + n) * p.Hkv) {
-      scan[6] = b;
-      scan[7] = pre;
-    }
-    if (cta == 0) p.prefix[b] = pre;
-    pre += n;
-    if (cta == 0 && b == p.B - 1) p.prefix[p.B] = pre;
-  }
-  __syncthreads();
   // the merge kernel may be scheduled now; it waits for this grid's completion
   // before it reads anything
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  Segments seg;
-  seg.init(p, begin, end, begin < end ? static_cast<int>(scan[6]) : 0, begin < end ? scan[7] : 0);
-  const long long n_tiles = end - begin;
+  Segments seg(p, share);
+  const int n_tiles = share.end - share.begin;
 
   if (warp == 0) {
-    // ===================== TMA producer =====================
-    // Each lane i < 128 / box_rows reads the block-table entry of box i of a
-    // tile and issues that box itself. A block past the sequence, or a table
-    // entry outside [0, num_blocks), is loaded from an out-of-range row, which
-    // the copy fills with zeros.
-    const int n_boxes = kTileN / p.box_rows;
-    auto load_part = [&](const CUtensorMap* tm, uint32_t dst, uint32_t bar, int key, int pb) {
-      if (lane >= n_boxes) return;
-      const bool in_range = pb >= 0 && pb < p.num_blocks;
-      const int y = in_range ? key % p.block_size : p.block_size;
-      const int z = in_range ? pb * p.Hkv + seg.kvh : 0;
-      for (int c = 0; c < Cfg::kChunks; ++c)
-        tma_load_3d(dst + c * (kTileN * 128) + lane * p.box_rows * 128, tm, bar, c * kChunk, y, z);
-    };
-    int g = 0;   // tiles whose K load has been issued
-    bool stop = false;
-    while (!stop && seg.next(p)) {
-      const int* table = p.block_table + static_cast<size_t>(seg.b) * p.max_blocks;
-      for (int j = 0; j < seg.n; ++j, ++g) {
-        const int key = (seg.tile0 + j) * kTileN + lane * p.box_rows;
-        const int st = g % NS;
-        const uint32_t use = static_cast<uint32_t>(g / NS);
-        int pb = -1;
-        if (lane < n_boxes && key < seg.keys.len) pb = table[key / p.block_size];
-        int fail = 0;
-        if (lane == 0) {
-          if (g >= NS && !mbar_wait(k_empty(st), (use - 1) & 1, abort_flag, p.status)) fail = 1;
-          else mbar_arrive_expect_tx(k_full(st), Cfg::kTileBytes);
-        }
-        if ((stop = __shfl_sync(0xffffffffu, fail, 0))) break;
-        load_part(&p.tm_k, sbase + Cfg::kOffK + st * Cfg::kTileBytes, k_full(st), key, pb);
-        if (lane == 0) {
-          if (g >= NS && !mbar_wait(v_empty(st), (use - 1) & 1, abort_flag, p.status)) fail = 1;
-          else mbar_arrive_expect_tx(v_full(st), Cfg::kTileBytes);
-        }
-        if ((stop = __shfl_sync(0xffffffffu, fail, 0))) {
-          ++g;   // this tile's K load is in flight
-          break;
-        }
-        load_part(&p.tm_v, sbase + Cfg::kOffV + st * Cfg::kTileBytes, v_full(st), key, pb);
-      }
-    }
-    if (lane == 0 && *abort_flag) {
-      // let every copy already issued land before the CTA releases its memory
-      for (int gg = max(0, g - NS); gg < g; ++gg) {
-        const uint32_t par = static_cast<uint32_t>(gg / NS) & 1;
-        drain_wait_r(k_full(gg % NS), par, p.status);
-        drain_wait_r(v_full(gg % NS), par, p.status);
-      }
-    }
+    produce<Cfg::kChunks, NS>(p, seg, sbase + Cfg::kOffK, sbase + Cfg::kOffV, k_full, k_empty,
+                              v_full, v_empty, abort_flag);
   } else if (warp == 1) {
     // ===================== MMA issuer =====================
     // Tile g's Q K^T goes out ahead of tile g - 1's P V, except the first of a
@@ -579,7 +604,7 @@ __global__ void __launch_bounds__(256) ragged_merge_kernel(const __grid_constant
   const int s = static_cast<int>(row % p.Sq);
   const long long bh = row / p.Sq;
   const int hq = static_cast<int>(bh % p.Hq), b = static_cast<int>(bh / p.Hq);
-  const long long pre = p.prefix[b], nt = p.prefix[b + 1] - pre;
+  const int pre = p.prefix[b], nt = p.prefix[b + 1] - pre;
   T* dst = static_cast<T*>(p.out) + row * D + lane * PER;
   if (nt == 0) {
 #pragma unroll
@@ -587,17 +612,14 @@ __global__ void __launch_bounds__(256) ragged_merge_kernel(const __grid_constant
     if (lane == 0) p.lse[row] = -INFINITY;
     return;
   }
-  const long long total = p.prefix[p.B] * p.Hkv;
-  const long long t0 = pre * p.Hkv + static_cast<long long>(hq / p.G) * nt;
-  // share c holds tile t iff total c / n <= t < total (c + 1) / n (rounded down)
-  const int shares = n_shares(p, total);
-  const int c0 = static_cast<int>(((t0 + 1) * shares - 1) / total);
-  const int c1 = static_cast<int>(((t0 + nt) * shares - 1) / total);
+  const ShareOut out(p.n_ctas, p.prefix[p.B] * p.Hkv);
+  const int t0 = pre * p.Hkv + hq / p.G * nt;   // this head's tiles: [t0, t0 + nt)
+  const int c0 = out.of_tile(t0), c1 = out.of_tile(t0 + nt - 1);
   if (c0 == c1) return;
   const int r = (hq % p.G) * p.Sq + s;
   // the parts are the first segments of their shares, but for that of c0 when
   // its share begins before this head's tiles
-  const bool tail0 = share_begin(total, c0, shares) < t0;
+  const bool tail0 = out.begin(c0) < t0;
   auto part = [&](int c) {
     return (static_cast<size_t>(c) * 2 + ((c == c0 && tail0) ? 1 : 0)) * p.R + r;
   };

@@ -307,8 +307,8 @@ int fa_qk_norm_rope_append(const fa_view* q, const fa_view* k, const fa_view* v,
  * sequence's last page past its length included, may hold anything.
  *
  * G * Sq <= 128 with G = Hq / Hkv, block_size as for fa_fwd_splitkv_paged,
- * max_blocks >= 1 and window >= 0 (else FA_ERR_SHAPE); softcap finite and >= 0
- * (else FA_ERR_SCALE); FA_BF16 and FA_F16 only (FA_F32 gives FA_ERR_DTYPE).
+ * max_blocks >= 1, window >= 0 and B * Hkv * ceil(max_blocks * block_size / 128)
+ * < 2^31 (else FA_ERR_SHAPE); softcap finite and >= 0 (else FA_ERR_SCALE); FA_BF16 and FA_F16 only (FA_F32 gives FA_ERR_DTYPE).
  * workspace: caller-owned, at least fa_fwd_ragged_paged_workspace_bytes(...)
  * bytes, 256-byte aligned, contents on entry without meaning; calls that may
  * overlap on the GPU need one each.
@@ -321,7 +321,7 @@ int fa_fwd_ragged_paged(const void* q, const void* k_cache, const void* v_cache,
                         size_t workspace_bytes, fa_stream_t stream);
 
 /* Workspace bytes of fa_fwd_ragged_paged: two partial results of G * Sq rows of
- * d + 1 floats for each of at most 152 CTAs, and B + 1 64-bit sums, each region
+ * d + 1 floats for each of at most 152 CTAs, and B + 1 int32 sums, each region
  * 256-byte aligned. Returns 0 for invalid sizes. */
 size_t fa_fwd_ragged_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int d,
                                            int block_size, int max_blocks);

@@ -67,7 +67,7 @@ def ragged(L, q=P, k=P, v=P, table=P, lens=P, out=P, lse=P, B=2, Hq=8, Hkv=2, Sq
 @pytest.mark.parametrize("kw,code", [
     (dict(d=80), SHAPE), (dict(B=0), SHAPE), (dict(Sq=33), SHAPE), (dict(bs=8), SHAPE),
     (dict(bs=2048), SHAPE), (dict(bs=48), SHAPE), (dict(nb=0), SHAPE), (dict(mb=0), SHAPE),
-    (dict(nb=1 << 30), SHAPE), (dict(window=-1), SHAPE), (dict(Hq=256, Hkv=1), SHAPE),
+    (dict(nb=1 << 30), SHAPE), (dict(B=1 << 20, mb=1 << 14), SHAPE), (dict(window=-1), SHAPE), (dict(Hq=256, Hkv=1), SHAPE),
     (dict(dtype=0), DTYPE), (dict(dtype=9), DTYPE), (dict(scale=-1.0), SCALE),
     (dict(softcap=math.nan), SCALE), (dict(softcap=-0.5), SCALE), (dict(table=None), NULL),
     (dict(lens=None), NULL), (dict(k=None), NULL), (dict(table=P + 2), ALIGN),
@@ -83,7 +83,7 @@ def test_ragged_workspace_formula(fa_lib):
                                       (2, 12, 12, 3, 64, 16, 20)]:
         ctas = min(152, B * Hkv * -(-(mb * bs) // 128))
         rows = 2 * ctas * (Hq // Hkv) * Sq
-        want = up(rows * d * 4) + up(rows * 4) + up((B + 1) * 8)
+        want = up(rows * d * 4) + up(rows * 4) + up((B + 1) * 4)
         assert fa_lib.fa_fwd_ragged_paged_workspace_bytes(B, Hq, Hkv, Sq, d, bs, mb) == want
     assert fa_lib.fa_fwd_ragged_paged_workspace_bytes(1, 8, 1, 17, 64, 16, 4) == 0
     assert fa_lib.fa_fwd_ragged_paged_workspace_bytes(1, 8, 1, 1, 64, 24, 4) == 0
