@@ -584,6 +584,420 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ----------------------------------------------------- one thread per key --
+// The form for few rows (R <= NR, 16 or 32): the products are transposed, so that
+// the keys fill the 128 tensor-memory lanes and the rows are the short side,
+//
+//   S^T = K Q^T  (keys x NR),   O^T += V^T P  (d x NR, P as stored: rows x keys),
+//
+// and each of the 128 threads takes one key's NR scores. Where the form above
+// has one warp do 128 exponentials a thread (for R <= 32; the other three idle),
+// here all four warps do NR each. P goes through shared memory, its own buffer,
+// so the score buffers are free as soon as they are read. The running maximum of
+// a row is common to all keys of a tile, so all threads: it moves only when some
+// score exceeds it by 2^8, which one barrier with a vote finds out; then the
+// warps exchange their maxima and rescale O^T. Row sums stay with the threads
+// until the end of a segment.
+//
+// At d = 64 the V tile has one 64-column chunk, but the product's M is 128: its
+// second half reads the 16 KB behind the tile (the next V or K buffer) into
+// lanes 64 .. 127, which nobody reads.
+template <int D, int NR>
+struct RagTCfg {
+  static constexpr int kChunks = D / kChunk;
+  static constexpr int kTileBytes = kTileM * D * 2;
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kQBytes = NR * D * 2;        // [chunk][NR rows][128 bytes]
+  static constexpr int kPBytes = NR * kTileN * 2;   // [64-key chunk][NR rows][128 bytes]
+  static constexpr int kOffV = 0;
+  static constexpr int kOffK = kStages * kTileBytes;
+  static constexpr int kOffQ = 2 * kStages * kTileBytes;   // two buffers
+  static constexpr int kOffP = kOffQ + 2 * kQBytes;        // two buffers
+  static constexpr int kOffBar = kOffP + 2 * kPBytes;
+  // k_full[S], k_empty[S], v_full[S], v_empty[S], q_ready[2], s_full[2],
+  // s_free[2], p_full[2], pv_done[2], drain
+  static constexpr int kNumBars = 4 * kStages + 10 + 1;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffScan = kOffMisc + 16;
+  static constexpr int kOffRed = (kOffScan + 32 + 15) / 16 * 16;   // [2][NR][4 warps] floats
+  static constexpr int kOffRow = kOffRed + 2 * NR * 16;            // [2][NR]: slope, token of the row
+  static constexpr int kSmemBytes = kOffRow + 2 * NR * 4 + 1024;   // + alignment slack
+  static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+};
+
+// Barrier of the four row warps that tells whether any thread's flag is set.
+__device__ __forceinline__ bool row_warps_any(bool flag) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any) : "r"(flag ? 1u : 0u) : "memory");
+  return any != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_n(uint32_t addr, uint32_t (&r)[N]) {
+  if constexpr (N == 16) tmem_ld16(addr, r);
+  else tmem_ld32(addr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_n(uint32_t addr, const uint32_t (&r)[N]) {
+  if constexpr (N == 16) tmem_st16(addr, r);
+  else tmem_st32(addr, r);
+}
+
+template <int D, int NR, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    fa_ragged_keys_kernel(const __grid_constant__ RaggedParams p) {
+  using Cfg = RagTCfg<D, NR>;
+  constexpr int NS = Cfg::kStages;
+  using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
+  float4* red = reinterpret_cast<float4*>(smem + Cfg::kOffRed);   // [NR] maxima, one float a warp
+  float4* red_sum = red + NR;                                     // [NR] sums
+
+  const Bars k_full{sbase + Cfg::kOffBar}, k_empty{k_full(NS)}, v_full{k_empty(NS)};
+  const Bars v_empty{v_full(NS)}, q_ready{v_empty(NS)}, s_full{q_ready(2)}, s_free{s_full(2)};
+  const Bars p_full{s_free(2)}, pv_done{p_full(2)};
+  const uint32_t drain = pv_done(2);
+
+  const int warp = static_cast<int>(warp_id());
+  const int lane = static_cast<int>(lane_id());
+  const int cta = static_cast<int>(blockIdx.x);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_ready(i), 4);   // one arrival per row warp
+      mbar_init(s_full(i), 1);
+      mbar_init(s_free(i), 4);
+      mbar_init(p_full(i), 4);
+      mbar_init(pv_done(i), 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  // tensor memory: S^T buffers at columns 0 and 32, O^T at 64
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 128);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  const Share share = find_share(p, cta, reinterpret_cast<int*>(smem + Cfg::kOffScan));
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // the merge kernel may be scheduled now; it waits for this grid's completion
+  // before it reads anything
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  Segments seg(p, share);
+  const int n_tiles = share.end - share.begin;
+
+  if (warp == 0) {
+    produce<Cfg::kChunks, NS>(p, seg, sbase + Cfg::kOffK, sbase + Cfg::kOffV, k_full, k_empty,
+                              v_full, v_empty, abort_flag);
+  } else if (warp == 1) {
+    // ===================== MMA issuer =====================
+    if (lane == 0 && n_tiles > 0) {
+      constexpr uint32_t idesc_s = make_idesc(128, NR, kBf16, false, false);
+      constexpr uint32_t idesc_o = make_idesc(128, NR, kBf16, true, false);
+      int left = 0, n_seg = 0;   // tiles of the segment whose S^T is still to issue; segments begun
+      auto issue_s = [&](int g) -> bool {   // S^T_(g%2) = K_g Q^T
+        const int st = g % NS;
+        if (left == 0) {
+          seg.next(p);
+          left = seg.n;
+          if (!mbar_wait(q_ready(n_seg & 1), (n_seg >> 1) & 1, abort_flag, p.status)) return false;
+          ++n_seg;
+        }
+        --left;
+        if (!mbar_wait(k_full(st), static_cast<uint32_t>(g / NS) & 1, abort_flag, p.status))
+          return false;
+        if (g >= 2 && !mbar_wait(s_free(g & 1), static_cast<uint32_t>((g - 2) >> 1) & 1, abort_flag,
+                                 p.status))
+          return false;
+        tc_fence_after();
+        const uint64_t ka = make_sdesc(sbase + Cfg::kOffK + st * Cfg::kTileBytes, 16, 1024);
+        const uint64_t qb = make_sdesc(sbase + Cfg::kOffQ + ((n_seg - 1) & 1) * Cfg::kQBytes, 16, 1024);
+        mma_ss_product<D / 16, true, kTileN * 128, true, NR * 128>(tmem + (g & 1) * 32, ka, qb,
+                                                                   idesc_s, 0);
+        tc_commit(s_full(g & 1));
+        tc_commit(k_empty(st));
+        return true;
+      };
+      bool ok = true;
+#ifdef FA_WAIT_TEST
+      // wait-limit test build: nothing completes this phase before the abort
+      // path's own commit, so the wait runs out
+      ok = mbar_wait(drain, 0, abort_flag, p.status);
+#endif
+      bool first = true;   // tile g is its segment's first
+      if (ok) ok = issue_s(0);
+      for (int g = 0; ok && g < n_tiles; ++g) {
+        const int st = g % NS;
+        const bool last = left == 0;   // tile g is its segment's last
+        if (g + 1 < n_tiles && !(ok = issue_s(g + 1))) break;
+        if (!(ok = mbar_wait(p_full(g & 1), static_cast<uint32_t>(g >> 1) & 1, abort_flag, p.status)))
+          break;
+        if (!(ok = mbar_wait(v_full(st), static_cast<uint32_t>(g / NS) & 1, abort_flag, p.status)))
+          break;
+        tc_fence_after();
+        const uint64_t va = make_sdesc(sbase + Cfg::kOffV + st * Cfg::kTileBytes, kTileN * 128, 1024);
+        const uint64_t pb = make_sdesc(sbase + Cfg::kOffP + (g & 1) * Cfg::kPBytes, 16, 1024);
+        mma_ss_product<kTileN / 16, false, 0, true, NR * 128>(tmem + 64, va, pb, idesc_o,
+                                                              first ? 0u : 1u);
+        tc_commit(pv_done(g & 1));
+        tc_commit(v_empty(st));
+        first = last;
+      }
+      if (!ok) {
+        // every MMA issued so far must finish before the TMEM is released
+        tc_commit(drain);
+        drain_wait_r(drain, 0, p.status);
+      }
+    }
+  } else {
+    // ===== row warps: thread = key of the tile, and dimension of O^T =====
+    const int quarter = warp & 3;               // TMEM lane quarter of this warp
+    const int t = quarter * 32 + lane;          // key of the tile; dimension
+    const int tid = static_cast<int>(threadIdx.x) - 64;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t o_tmem = tmem + lane_off + 64;
+    const bool cap = p.cap_in != 0.f;
+    const float c = p.scale_log2;
+    float* row_slope = reinterpret_cast<float*>(smem + Cfg::kOffRow);          // log2 domain
+    int* row_s = reinterpret_cast<int*>(smem + Cfg::kOffRow + NR * 4);         // token of the row
+
+    // A segment's queries: R rows that follow each other in memory. 16-byte unit
+    // u of a 128-byte row r sits at unit u ^ (r % 8); rows past R are zero.
+    constexpr int kUnits = NR * D / 8 / 128;    // 16-byte units a thread
+    uint4 qv[kUnits];
+    auto load_q = [&](const Segments& sg) {
+      const size_t row0 = (static_cast<size_t>(sg.b) * p.Hq + sg.kvh * p.G) * p.Sq;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const Elem*>(p.q) + row0 * D);
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int u = tid + i * 128;
+        qv[i] = u / (D / 8) < p.R ? src[u] : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    auto stage_q = [&](int buffer) {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int u = tid + i * 128, row = u / (D / 8), col = u % (D / 8);
+        *reinterpret_cast<uint4*>(smem + Cfg::kOffQ + buffer * Cfg::kQBytes + (col >> 3) * (NR * 128) +
+                                  row * 128 + (((col & 7) ^ (row & 7)) << 4)) = qv[i];
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_ready(buffer));
+    };
+    // this thread's place in a P buffer: row r of 64-key chunk t / 64, key t % 64
+    const uint32_t p_dst = sbase + Cfg::kOffP + (t >> 6) * (NR * 128) + (t & 7) * 2;
+    const uint32_t p_unit = static_cast<uint32_t>((t & 63) >> 3);
+
+    bool more = seg.next(p);
+    if (more) {
+      load_q(seg);
+      stage_q(0);
+    }
+    // A wait that fails in one warp must not leave the others in a barrier: the
+    // warp goes on without touching anything until the next vote, where all four
+    // learn of it and leave together.
+    bool ok = true;     // no wait of this warp has failed
+    bool dead = false;  // voted: some warp's has
+    bool head = true;   // the share's first segment
+    int g = 0;
+    auto wait = [&](uint32_t bar, int phase) {
+      if (ok)
+        ok = __all_sync(0xffffffffu, mbar_wait(bar, static_cast<uint32_t>(phase) & 1, abort_flag, p.status));
+    };
+    for (int n_seg = 0; more && !dead; ++n_seg) {
+      const int b = seg.b, kvh = seg.kvh, n = seg.n;
+      const bool whole = seg.whole;
+      const SeqKeys keys = seg.keys;
+      const int tile0 = seg.tile0;
+      const int pos0 = keys.len - p.Sq;   // position of row s = 0
+      // rows' slopes and tokens (the readers of the segment before are past its last vote)
+      if (tid < NR) {
+        const int gq = min(tid, p.R - 1) / p.Sq;
+        row_s[tid] = tid < p.R ? tid - gq * p.Sq : 0;
+        row_slope[tid] = p.slopes ? p.slopes[kvh * p.G + gq] * kLog2eR : 0.f;
+      }
+      more = seg.next(p);
+      if (more) load_q(seg);   // the next segment's, stored after the first tile
+      float m[NR], l[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        m[r] = -INFINITY;   // reference max, scaled log2 domain
+        l[r] = 0.f;         // this thread's part of the row sum
+      }
+      for (int j = 0; j < n; ++j, ++g) {
+        const int kv0 = (tile0 + j) * kTileN;
+        const int key = kv0 + t;
+        wait(s_full(g & 1), g >> 1);
+        tc_fence_after();
+        float x[NR];
+        {
+          uint32_t raw[NR];
+          tmem_ld_n<NR>(tmem + lane_off + (g & 1) * 32, raw);
+          tmem_wait_ld();
+#pragma unroll
+          for (int r = 0; r < NR; ++r) x[r] = __uint_as_float(raw[r]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free(g & 1));
+        if (cap) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            x[r] = fmaf(-2.f * p.cap_log2, cap_r(x[r], p.cap_in), p.cap_log2);
+        } else {
+#pragma unroll
+          for (int r = 0; r < NR; ++r) x[r] *= c;
+        }
+        if (j == 0) row_warps_any(false);   // row_slope and row_s are written
+        if (p.slopes) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            x[r] = fmaf(-row_slope[r], fabsf(static_cast<float>(pos0 + row_s[r] - key)), x[r]);
+        }
+        // the first row sees keys up to pos0, the last from first + Sq - 1 on (window)
+        if (kv0 + kTileN > pos0 + 1 || (p.window > 0 && kv0 < pos0 + p.Sq - p.window)) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const int pos = pos0 + row_s[r];
+            if (key > pos || (p.window > 0 && key <= pos - p.window)) x[r] = -INFINITY;
+          }
+        }
+        // V rows nobody sees are cleared
+        const bool edge = kv0 < keys.first || kv0 + kTileN > keys.len;
+        if (edge) {
+          const int st = g % NS;
+          wait(v_full(st), g / NS);
+          if (ok && (key < keys.first || key >= keys.len)) {
+#pragma unroll
+            for (int cc = 0; cc < Cfg::kChunks; ++cc) {
+              uint4* row = reinterpret_cast<uint4*>(smem + Cfg::kOffV + st * Cfg::kTileBytes +
+                                                    cc * (kTileN * 128) + t * 128);
+#pragma unroll
+              for (int u = 0; u < 8; ++u) row[u] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        }
+        float over = -INFINITY;   // how far a score exceeds its row's reference
+#pragma unroll
+        for (int r = 0; r < NR; ++r) over = fmaxf(over, x[r] - m[r]);
+        if (row_warps_any(over > kRescaleThresholdR || !ok)) {
+          // move every row's reference to its maximum so far
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            float v = x[r];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            if (lane == 0) reinterpret_cast<float*>(red + r)[quarter] = v;
+          }
+          // P_(g-1) V_(g-1) is in O^T (the segment's first product overwrites it)
+          if (j > 0) wait(pv_done((g - 1) & 1), (g - 1) >> 1);
+          if ((dead = row_warps_any(!ok))) break;
+          tc_fence_after();
+          uint32_t o[NR];
+          if (j > 0) {
+            tmem_ld_n<NR>(o_tmem, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const float4 v = red[r];
+            const float m_new = fmaxf(fmaxf(m[r], fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
+            const float alpha = m_new == -INFINITY ? 1.f : ex2(m[r] - m_new);   // 0 from m = -inf
+            m[r] = m_new;
+            l[r] *= alpha;
+            if (j > 0) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha);
+          }
+          if (j > 0) {
+            tmem_st_n<NR>(o_tmem, o);
+            tmem_wait_st();
+          }
+        }
+        if (g >= 2) wait(pv_done(g & 1), (g - 2) >> 1);   // P_(g-2) V_(g-2) has read this P buffer
+        if (!ok) continue;   // to the next vote
+        const uint32_t dst = p_dst + (g & 1) * Cfg::kPBytes;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float e = ex2(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+          l[r] += e;
+          const uint32_t h = pack2<kBf16>(e, 0.f);
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + r * 128 + ((p_unit ^ (r & 7)) << 4)),
+                       "h"(static_cast<uint16_t>(h)) : "memory");
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(g & 1));
+        if (j == 0 && more) stage_q((n_seg + 1) & 1);
+      }
+      if (dead) break;
+      // row sums over the 128 keys
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        float v = l[r];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) reinterpret_cast<float*>(red_sum + r)[quarter] = v;
+      }
+      wait(pv_done((g - 1) & 1), (g - 1) >> 1);
+      if ((dead = row_warps_any(!ok))) break;
+      tc_fence_after();
+      uint32_t o[NR];
+      tmem_ld_n<NR>(o_tmem, o);
+      tmem_wait_ld();
+      tc_fence_before();
+      const size_t qrow = (static_cast<size_t>(b) * p.Hq + kvh * p.G) * p.Sq;   // + r
+      const size_t prow = (static_cast<size_t>(cta) * 2 + (head ? 0 : 1)) * p.R;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        if (r >= p.R) break;
+        const float4 v = red_sum[r];
+        const float sum = (v.x + v.y) + (v.z + v.w);
+        // a row that sees no key of this range contributes weight 0 to the merge
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float y = __uint_as_float(o[r]) * inv;
+        if (t < D) {
+          if (whole) static_cast<Elem*>(p.out)[(qrow + r) * D + t] = static_cast<Elem>(y);
+          else p.part_out[(prow + r) * D + t] = y;
+        }
+        if (tid == 0) {
+          const float lse2 = sum > 0.f ? m[r] + __log2f(sum) : -INFINITY;
+          if (whole) p.lse[qrow + r] = lse2 * kLn2R;
+          else p.part_lse2[prow + r] = lse2;
+        }
+      }
+      head = false;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 128);
+  }
+}
+
 // ------------------------------------------------------------------ merge --
 // One warp per output row (b, hq, s); each lane owns d / 32 columns. Joins the
 // parts of rows whose tiles lie in more than one share, in share order, as the
@@ -645,15 +1059,25 @@ __global__ void __launch_bounds__(256) ragged_merge_kernel(const __grid_constant
   if (lane == 0) p.lse[row] = L > 0.f ? (M + __log2f(L)) * kLn2R : -INFINITY;
 }
 
-template <int D, bool kBf16>
-cudaError_t launch_ragged_impl(const RaggedParams& p, cudaStream_t stream) {
-  constexpr int smem = RagCfg<D>::kSmemBytes;
-  using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
-  auto kernel = fa_ragged_kernel<D, kBf16>;
+template <int smem, class Kernel>
+cudaError_t launch_main(Kernel kernel, const RaggedParams& p, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kernel<<<static_cast<unsigned>(p.n_ctas), kThreads, smem, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+template <int D, bool kBf16>
+cudaError_t launch_ragged_impl(const RaggedParams& p, cudaStream_t stream) {
+  using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
+  cudaError_t e;
+  if (p.R <= 16)
+    e = launch_main<RagTCfg<D, 16>::kSmemBytes>(fa_ragged_keys_kernel<D, 16, kBf16>, p, stream);
+  else if (p.R <= 32)
+    e = launch_main<RagTCfg<D, 32>::kSmemBytes>(fa_ragged_keys_kernel<D, 32, kBf16>, p, stream);
+  else
+    e = launch_main<RagCfg<D>::kSmemBytes>(fa_ragged_kernel<D, kBf16>, p, stream);
+  if (e != cudaSuccess) return e;
   // the merge overlaps its launch with the ragged kernel's tail
   const long long rows = static_cast<long long>(p.B) * p.Hq * p.Sq;
   cudaLaunchConfig_t cfg = {};
