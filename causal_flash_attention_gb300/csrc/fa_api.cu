@@ -215,9 +215,9 @@ bool paged_sizes_ok(int B, int Hq, int Hkv, int Sq, int block_size, int num_bloc
   if (static_cast<long long>(Hq / Hkv) * Sq > kDecodeMaxRows ||
       !block_sizes_ok(Hkv, block_size, num_blocks, max_blocks))
     return false;
-  // the list of key tiles is counted in 32 bits
+  // the list of key tiles, and a few units a head beside them, is counted in 32 bits
   const long long tiles = (static_cast<long long>(max_blocks) * block_size + kTileN - 1) / kTileN;
-  return tiles <= 0x7fffffffLL / (static_cast<long long>(B) * Hkv);
+  return tiles + 8 <= 0x7fffffffLL / (static_cast<long long>(B) * Hkv);
 }
 
 // Arguments the query/key preparation entry points share.

@@ -81,9 +81,17 @@ __device__ __forceinline__ SeqKeys seq_keys(const RaggedParams& p, int b) {
   return s;
 }
 
-// Even shares of a list of `total` tiles (below 2^31): the first `rest` shares
-// take one tile more than the others. No more shares than tiles, so that none is
-// empty (the merge reads a part of every share between a head's first and last).
+// The list that is shared out counts units: one a key tile and kSegmentUnits for
+// every (sequence, head) that has tiles, in front of them, for what a segment
+// costs beside its tiles. Measured at 32 + 8 heads, d = 128, 66137 keys in 16
+// sequences of 8 to 8192 and (second) 65521 + 15 x 1 keys: with no such units one
+// CTA got dozens of one-tile segments, 76.0 and 144 us; 1 unit 59.4 and 73.0; 2
+// units 52.0 and 57.6; 3 units 52.9 and 57.0.
+constexpr int kSegmentUnits = 2;
+__device__ __forceinline__ int units_of(int tiles) { return tiles > 0 ? tiles + kSegmentUnits : 0; }
+
+// Even shares of a list of `total` units (below 2^31): the first `rest` shares
+// take one unit more than the others.
 struct ShareOut {
   int shares, each, rest;
   __device__ __forceinline__ ShareOut(int n_ctas, int total) {
@@ -92,17 +100,17 @@ struct ShareOut {
     rest = total - each * shares;
   }
   __device__ __forceinline__ int begin(int c) const { return c * each + min(c, rest); }
-  __device__ __forceinline__ int of_tile(int t) const {
-    const int big = rest * (each + 1);   // tiles of the larger shares
+  __device__ __forceinline__ int of_unit(int t) const {
+    const int big = rest * (each + 1);   // units of the larger shares
     return t < big ? t / (each + 1) : rest + (t - big) / each;
   }
 };
 
-// A CTA's share, found by all its threads: a scan over the sequences' tile
-// counts. CTA 0 also writes the sums for the merge. Two barriers.
+// A CTA's share, found by all its threads: a scan over the sequences' units. CTA
+// 0 also writes the sums for the merge. Two barriers.
 struct Share {
-  int begin, end;    // tiles of the list
-  int b, pre;        // the first tile's sequence, and tiles per head before it
+  int begin, end;    // units of the list
+  int b, pre;        // the first unit's sequence, and units per head before it
 };
 
 __device__ __forceinline__ Share find_share(const RaggedParams& p, int cta, int* scan) {
@@ -112,7 +120,7 @@ __device__ __forceinline__ Share find_share(const RaggedParams& p, int cta, int*
   const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per);
   const int b_hi = min(p.B, b_lo + per);
   int mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += seq_keys(p, b).n;
+  for (int b = b_lo; b < b_hi; ++b) mine += units_of(seq_keys(p, b).n);
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -131,7 +139,7 @@ __device__ __forceinline__ Share find_share(const RaggedParams& p, int cta, int*
   s.begin = cta < out.shares ? out.begin(cta) : 0;
   s.end = cta < out.shares ? out.begin(cta + 1) : 0;
   for (int b = b_lo; b < b_hi; ++b) {
-    const int n = seq_keys(p, b).n;
+    const int n = units_of(seq_keys(p, b).n);
     if (s.begin < s.end && pre * p.Hkv <= s.begin && s.begin < (pre + n) * p.Hkv) {
       scan[6] = b;
       scan[7] = pre;
@@ -148,7 +156,7 @@ __device__ __forceinline__ Share find_share(const RaggedParams& p, int cta, int*
 
 // The segments of one CTA's share, in order; every role walks its own copy.
 struct Segments {
-  int cur, end, pre;   // list position, end of the share, tiles per head before b
+  int cur, end, pre;   // list position, end of the share, units per head before b
   int b;
   SeqKeys keys;
   // the current segment
@@ -160,27 +168,51 @@ struct Segments {
     if (cur < end) keys = seq_keys(p, b);
   }
   __device__ __forceinline__ bool next(const RaggedParams& p) {
-    if (cur >= end) return false;
-    while (cur >= (pre + keys.n) * p.Hkv) {   // cur < end <= total: some later b has tiles
-      pre += keys.n;
-      keys = seq_keys(p, ++b);
+    while (cur < end) {
+      int units = units_of(keys.n);
+      while (cur >= (pre + units) * p.Hkv) {   // cur < end <= total: some later b has units
+        pre += units;
+        keys = seq_keys(p, ++b);
+        units = units_of(keys.n);
+      }
+      const int off = cur - pre * p.Hkv;
+      kvh = off / units;
+      const int u = off - kvh * units;
+      const int take = min(units - u, end - cur);
+      cur += take;
+      const int t0 = max(u - kSegmentUnits, 0), t1 = max(u + take - kSegmentUnits, 0);
+      if (t1 == t0) continue;   // the share ends with the units in front of a head's tiles
+      n = t1 - t0;
+      tile0 = keys.tile0 + t0;
+      whole = n == keys.n;
+      return true;
     }
-    const int off = cur - pre * p.Hkv;
-    kvh = off / keys.n;
-    const int t = off - kvh * keys.n;
-    n = min(keys.n - t, end - cur);
-    tile0 = keys.tile0 + t;
-    whole = n == keys.n;
-    cur += n;
+    return false;
+  }
+};
+
+// The tiles of a share in order, for the MMA issuers: whether there is a next
+// one, and whether it begins a segment.
+struct TileWalk {
+  Segments& seg;
+  int left = 0;
+  bool first = false;
+  __device__ __forceinline__ bool next(const RaggedParams& p) {
+    first = left == 0;
+    if (first) {
+      if (!seg.next(p)) return false;
+      left = seg.n;
+    }
+    --left;
     return true;
   }
 };
 
 // TMA producer warp of both kernels: K and V tiles of the share into rings of
 // kStages. Each lane i < 128 / box_rows reads the block-table entry of box i of a
-// tile and issues that box itself. A block past the sequence, or a table entry
-// outside [0, num_blocks), is loaded from an out-of-range row, which the copy
-// fills with zeros.
+// tile and issues that box itself. A box past the sequence or before every row's
+// window, or a table entry outside [0, num_blocks), is loaded from an
+// out-of-range row, which the copy fills with zeros.
 template <int kChunks, int kStages, class Bar>
 __device__ __forceinline__ void produce(const RaggedParams& p, Segments& seg, uint32_t k_ring,
                                         uint32_t v_ring, Bar k_full, Bar k_empty, Bar v_full,
@@ -205,7 +237,8 @@ __device__ __forceinline__ void produce(const RaggedParams& p, Segments& seg, ui
       const int st = g % kStages;
       const uint32_t use = static_cast<uint32_t>(g / kStages);
       int pb = -1;
-      if (lane < n_boxes && key < seg.keys.len) pb = table[key / p.block_size];
+      if (lane < n_boxes && key < seg.keys.len && key + p.box_rows > seg.keys.first)
+        pb = table[key / p.block_size];
       int fail = 0;
       if (lane == 0) {
         if (g >= kStages && !mbar_wait(k_empty(st), (use - 1) & 1, abort_flag, p.status)) fail = 1;
@@ -231,6 +264,35 @@ __device__ __forceinline__ void produce(const RaggedParams& p, Segments& seg, ui
       drain_wait_r(k_full(gg % kStages), par, p.status);
       drain_wait_r(v_full(gg % kStages), par, p.status);
     }
+  }
+}
+
+// Keys of a tile that nobody sees but that were loaded with others' boxes: rows
+// [a0, a1) before the window and [b0, b1) past the sequence.
+struct HiddenRows {
+  int a0, a1, b0, b1;
+  __device__ __forceinline__ HiddenRows(const RaggedParams& p, const SeqKeys& k, int kv0) {
+    a1 = min(max(k.first - kv0, 0), kTileN);
+    a0 = max(a1 - (k.first & (p.box_rows - 1)), 0);
+    b0 = min(max(k.len - kv0, 0), kTileN);
+    b1 = min(b0 + (-k.len & (p.box_rows - 1)), kTileN);
+    if (k.first < kv0 || k.first >= kv0 + kTileN) a0 = a1 = 0;
+    if (k.len < kv0 || k.len >= kv0 + kTileN) b0 = b1 = 0;
+  }
+  __device__ __forceinline__ bool any() const { return a0 < a1 || b0 < b1; }
+};
+
+// Clears those rows of a V tile (`chunks` 64-column chunks of 128-byte rows), by
+// 128 threads, a 16-byte unit each at a time.
+template <int kChunks>
+__device__ __forceinline__ void clear_rows(const HiddenRows& h, uint8_t* tile, int tid) {
+  const int na = h.a1 - h.a0, n = na + h.b1 - h.b0;
+  for (int i = tid; i < n * 8; i += 128) {
+    const int r = (i >> 3) < na ? h.a0 + (i >> 3) : h.b0 + (i >> 3) - na;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+      *reinterpret_cast<uint4*>(tile + c * (kTileN * 128) + r * 128 + (i & 7) * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -297,7 +359,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   Segments seg(p, share);
-  const int n_tiles = share.end - share.begin;
 
   if (warp == 0) {
     produce<Cfg::kChunks, NS>(p, seg, sbase + Cfg::kOffK, sbase + Cfg::kOffV, k_full, k_empty,
@@ -306,14 +367,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ===================== MMA issuer =====================
     // Tile g's Q K^T goes out ahead of tile g - 1's P V, except the first of a
     // segment, whose queries are staged after the segment before has been read.
-    if (lane == 0 && n_tiles > 0) {
+    if (lane == 0) {
       constexpr uint32_t idesc_qk = make_idesc(128, kTileN, kBf16, false, false);
       constexpr uint32_t idesc_pv = make_idesc(128, D, kBf16, false, true);
       const uint64_t qa = make_sdesc(sbase + Cfg::kOffQ, 16, 1024);
+      TileWalk walk{seg};
       int n_seg = 0;   // segments whose queries have been awaited
-      auto issue_qk = [&](int g, bool first) -> bool {   // S_(g%2) = Q K_g^T
+      auto issue_qk = [&](int g) -> bool {   // S_(g%2) = Q K_g^T
         const int st = g % NS;
-        if (first && !mbar_wait(q_ready, n_seg++ & 1, abort_flag, p.status)) return false;
+        if (walk.first && !mbar_wait(q_ready, n_seg++ & 1, abort_flag, p.status)) return false;
         if (!mbar_wait(k_full(st), static_cast<uint32_t>(g / NS) & 1, abort_flag, p.status))
           return false;
         // S_(g%2) held P_(g-2), which P_(g-2) V_(g-2) must have read
@@ -328,21 +390,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit(k_empty(st));
         return true;
       };
-      seg.next(p);
-      int left = seg.n;   // tiles of the segment not yet issued
-      bool first = true;  // tile g is its segment's first
-      bool ok = true;
+      bool ok = true, have = walk.next(p);
 #ifdef FA_WAIT_TEST
       // wait-limit test build: nothing completes this phase before the abort
       // path's own commit, so the wait runs out
-      ok = mbar_wait(drain, 0, abort_flag, p.status);
+      if (have) ok = mbar_wait(drain, 0, abort_flag, p.status);
 #endif
-      if (ok) ok = issue_qk(0, true);
-      --left;
-      for (int g = 0; ok && g < n_tiles; ++g) {
+      if (ok && have) ok = issue_qk(0);
+      for (int g = 0; ok && have; ++g) {
         const int st = g % NS;
-        const bool more = g + 1 < n_tiles, edge = left == 0;
-        if (more && !edge && !(ok = issue_qk(g + 1, false))) break;
+        const bool first = walk.first;   // tile g is its segment's first
+        have = walk.next(p);
+        if (have && !walk.first && !(ok = issue_qk(g + 1))) break;
         if (!(ok = mbar_wait(p_full(g & 1), static_cast<uint32_t>(g >> 1) & 1, abort_flag, p.status)))
           break;
         if (!(ok = mbar_wait(v_full(st), static_cast<uint32_t>(g / NS) & 1, abort_flag, p.status)))
@@ -352,13 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_ts_product8<false, 0>(tmem + 256, tmem + (g & 1) * 128, vb, idesc_pv, first ? 0u : 1u);
         tc_commit(pv_done(g & 1));
         tc_commit(v_empty(st));
-        if (more && edge) {
-          seg.next(p);
-          left = seg.n;
-          if (!(ok = issue_qk(g + 1, true))) break;
-        }
-        first = edge;
-        --left;
+        if (have && walk.first && !(ok = issue_qk(g + 1))) break;
       }
       if (!ok) {
         // every MMA issued so far must finish before the TMEM is released
@@ -425,20 +478,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                abort_flag, p.status));
         if (!ok) break;
         tc_fence_after();
-        if (kv0 < keys.first || kv0 + kTileN > keys.len) {   // clear V rows nobody sees
+        const HiddenRows hidden(p, keys, kv0);
+        if (hidden.any()) {
           const int st = g % NS;
           ok = __all_sync(0xffffffffu, mbar_wait(v_full(st), static_cast<uint32_t>(g / NS) & 1,
                                                  abort_flag, p.status));
           if (!ok) break;
-          if (kv0 + r < keys.first || kv0 + r >= keys.len) {
-#pragma unroll
-            for (int cc = 0; cc < Cfg::kChunks; ++cc) {
-              uint4* row = reinterpret_cast<uint4*>(smem + Cfg::kOffV + st * Cfg::kTileBytes +
-                                                    cc * (kTileN * 128) + r * 128);
-#pragma unroll
-              for (int u = 0; u < 8; ++u) row[u] = make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
+          clear_rows<Cfg::kChunks>(hidden, smem + Cfg::kOffV + st * Cfg::kTileBytes, r);
           fence_proxy_async_smem();
         }
         if (busy) {
@@ -625,6 +671,32 @@ struct RagTCfg {
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 };
 
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Sums of N columns over the warp's lanes: each exchange halves the columns a
+// lane holds (the lanes of a pair keep one half each), so N columns take N
+// shuffles; lane l ends with the sum of column l % N (both lanes l and l + 16 for
+// N = 16).
+template <int N>
+__device__ __forceinline__ float column_sums(float (&v)[N], int lane) {
+  static_assert(N == 16 || N == 32, "columns");
+#pragma unroll
+  for (int h = N / 2; h > 0; h >>= 1) {
+    const bool up = (lane & h) != 0;   // keeps the upper half of its columns
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float keep = up ? v[i + h] : v[i], give = up ? v[i] : v[i + h];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, h);
+    }
+  }
+  if (N == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+  return v[0];
+}
+
 // Barrier of the four row warps that tells whether any thread's flag is set.
 __device__ __forceinline__ bool row_warps_any(bool flag) {
   uint32_t any;
@@ -704,26 +776,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   Segments seg(p, share);
-  const int n_tiles = share.end - share.begin;
 
   if (warp == 0) {
     produce<Cfg::kChunks, NS>(p, seg, sbase + Cfg::kOffK, sbase + Cfg::kOffV, k_full, k_empty,
                               v_full, v_empty, abort_flag);
   } else if (warp == 1) {
     // ===================== MMA issuer =====================
-    if (lane == 0 && n_tiles > 0) {
+    if (lane == 0) {
       constexpr uint32_t idesc_s = make_idesc(128, NR, kBf16, false, false);
       constexpr uint32_t idesc_o = make_idesc(128, NR, kBf16, true, false);
-      int left = 0, n_seg = 0;   // tiles of the segment whose S^T is still to issue; segments begun
+      TileWalk walk{seg};
+      int n_seg = 0;   // segments begun
       auto issue_s = [&](int g) -> bool {   // S^T_(g%2) = K_g Q^T
         const int st = g % NS;
-        if (left == 0) {
-          seg.next(p);
-          left = seg.n;
+        if (walk.first) {
           if (!mbar_wait(q_ready(n_seg & 1), (n_seg >> 1) & 1, abort_flag, p.status)) return false;
           ++n_seg;
         }
-        --left;
         if (!mbar_wait(k_full(st), static_cast<uint32_t>(g / NS) & 1, abort_flag, p.status))
           return false;
         if (g >= 2 && !mbar_wait(s_free(g & 1), static_cast<uint32_t>((g - 2) >> 1) & 1, abort_flag,
@@ -738,18 +807,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit(k_empty(st));
         return true;
       };
-      bool ok = true;
+      bool ok = true, have = walk.next(p);
 #ifdef FA_WAIT_TEST
       // wait-limit test build: nothing completes this phase before the abort
       // path's own commit, so the wait runs out
-      ok = mbar_wait(drain, 0, abort_flag, p.status);
+      if (have) ok = mbar_wait(drain, 0, abort_flag, p.status);
 #endif
-      bool first = true;   // tile g is its segment's first
-      if (ok) ok = issue_s(0);
-      for (int g = 0; ok && g < n_tiles; ++g) {
+      if (ok && have) ok = issue_s(0);
+      for (int g = 0; ok && have; ++g) {
         const int st = g % NS;
-        const bool last = left == 0;   // tile g is its segment's last
-        if (g + 1 < n_tiles && !(ok = issue_s(g + 1))) break;
+        const bool first = walk.first;   // tile g is its segment's first
+        have = walk.next(p);
+        if (have && !(ok = issue_s(g + 1))) break;
         if (!(ok = mbar_wait(p_full(g & 1), static_cast<uint32_t>(g >> 1) & 1, abort_flag, p.status)))
           break;
         if (!(ok = mbar_wait(v_full(st), static_cast<uint32_t>(g / NS) & 1, abort_flag, p.status)))
@@ -761,7 +830,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                               first ? 0u : 1u);
         tc_commit(pv_done(g & 1));
         tc_commit(v_empty(st));
-        first = last;
       }
       if (!ok) {
         // every MMA issued so far must finish before the TMEM is released
@@ -883,20 +951,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (key > pos || (p.window > 0 && key <= pos - p.window)) x[r] = -INFINITY;
           }
         }
-        // V rows nobody sees are cleared
-        const bool edge = kv0 < keys.first || kv0 + kTileN > keys.len;
-        if (edge) {
+        const HiddenRows hidden(p, keys, kv0);
+        if (hidden.any()) {
           const int st = g % NS;
           wait(v_full(st), g / NS);
-          if (ok && (key < keys.first || key >= keys.len)) {
-#pragma unroll
-            for (int cc = 0; cc < Cfg::kChunks; ++cc) {
-              uint4* row = reinterpret_cast<uint4*>(smem + Cfg::kOffV + st * Cfg::kTileBytes +
-                                                    cc * (kTileN * 128) + t * 128);
-#pragma unroll
-              for (int u = 0; u < 8; ++u) row[u] = make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
+          if (ok) clear_rows<Cfg::kChunks>(hidden, smem + Cfg::kOffV + st * Cfg::kTileBytes, tid);
         }
         float over = -INFINITY;   // how far a score exceeds its row's reference
 #pragma unroll
@@ -905,9 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // move every row's reference to its maximum so far
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            float v = x[r];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            const float v = warp_max(x[r]);
             if (lane == 0) reinterpret_cast<float*>(red + r)[quarter] = v;
           }
           // P_(g-1) V_(g-1) is in O^T (the segment's first product overwrites it)
@@ -952,13 +1009,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (dead) break;
       // row sums over the 128 keys
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        float v = l[r];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) reinterpret_cast<float*>(red_sum + r)[quarter] = v;
-      }
+      const float sum_l = column_sums<NR>(l, lane);
+      if (lane < NR) reinterpret_cast<float*>(red_sum + lane)[quarter] = sum_l;
       wait(pv_done((g - 1) & 1), (g - 1) >> 1);
       if ((dead = row_warps_any(!ok))) break;
       tc_fence_after();
@@ -1018,22 +1070,22 @@ __global__ void __launch_bounds__(256) ragged_merge_kernel(const __grid_constant
   const int s = static_cast<int>(row % p.Sq);
   const long long bh = row / p.Sq;
   const int hq = static_cast<int>(bh % p.Hq), b = static_cast<int>(bh / p.Hq);
-  const int pre = p.prefix[b], nt = p.prefix[b + 1] - pre;
+  const int pre = p.prefix[b], units = p.prefix[b + 1] - pre;
   T* dst = static_cast<T*>(p.out) + row * D + lane * PER;
-  if (nt == 0) {
+  if (units == 0) {
 #pragma unroll
     for (int e = 0; e < PER; ++e) dst[e] = static_cast<T>(0.f);
     if (lane == 0) p.lse[row] = -INFINITY;
     return;
   }
   const ShareOut out(p.n_ctas, p.prefix[p.B] * p.Hkv);
-  const int t0 = pre * p.Hkv + hq / p.G * nt;   // this head's tiles: [t0, t0 + nt)
-  const int c0 = out.of_tile(t0), c1 = out.of_tile(t0 + nt - 1);
+  const int u0 = pre * p.Hkv + hq / p.G * units;   // this head's units: [u0, u0 + units)
+  const int c0 = out.of_unit(u0 + kSegmentUnits), c1 = out.of_unit(u0 + units - 1);
   if (c0 == c1) return;
   const int r = (hq % p.G) * p.Sq + s;
   // the parts are the first segments of their shares, but for that of c0 when
-  // its share begins before this head's tiles
-  const bool tail0 = out.begin(c0) < t0;
+  // its share begins before this head's units (and so with another's tiles)
+  const bool tail0 = out.begin(c0) < u0;
   auto part = [&](int c) {
     return (static_cast<size_t>(c) * 2 + ((c == c0 && tail0) ? 1 : 0)) * p.R + r;
   };

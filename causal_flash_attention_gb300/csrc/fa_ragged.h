@@ -6,9 +6,9 @@
 
 namespace fa {
 
-// Work is the list of all key tiles: for every sequence b, for every key/value
-// head, the nt_b tiles of 128 keys that its new rows see. The list is cut into
-// even shares, one a CTA.
+// Work is the list of all key tiles: for every sequence, for every key/value
+// head, the tiles of 128 keys that its new rows see. The list is cut into even
+// shares, one a CTA.
 struct RaggedParams {
   CUtensorMap tm_k;   // [num_blocks*Hkv][block_size][d], box (64, box_rows, 1), 128B swizzle
   CUtensorMap tm_v;
@@ -20,7 +20,7 @@ struct RaggedParams {
   const float* slopes;      // [Hq] or null
   float* part_out;    // [2 * CTAs][R][d] fp32 out = O / l of a part of a (sequence, head)
   float* part_lse2;   // [2 * CTAs][R]    its log2-sum-exp2 of scaled scores
-  int* prefix;        // [B + 1] tiles per head before sequence b, written by CTA 0
+  int* prefix;        // [B + 1] units per head before sequence b, written by CTA 0
   int B, Hq, Hkv, Sq, G, R;
   int block_size, box_rows, max_blocks, num_blocks;
   int capacity;       // keys a table row can hold (at most 2^31 - 128)
