@@ -1055,22 +1055,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 // parts of rows whose tiles lie in more than one share, in share order, as the
 // split-KV merge does; writes out = 0, LSE = -inf for sequences without keys;
 // leaves rows that one segment wrote whole alone.
+constexpr int kMergeRows = 4;     // rows (warps) a block: fits beside the ragged kernel's CTA
+constexpr int kMergeBatch = 20;   // 152 shares of one sequence with 8 heads: 20 parts a head
 template <int PER>
 struct alignas(4 * PER) PartVec { float x[PER]; };
 
 template <typename T, int PER>
-__global__ void __launch_bounds__(256) ragged_merge_kernel(const __grid_constant__ RaggedParams p) {
+__global__ void __launch_bounds__(32 * kMergeRows) ragged_merge_kernel(const __grid_constant__ RaggedParams p) {
   // programmatic dependent of the ragged kernel: wait until that grid has
   // completed and its results are visible
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int D = 32 * PER;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 8 + warp;   // (b * Hq + hq) * Sq + s
+  const long long row = static_cast<long long>(blockIdx.x) * kMergeRows + warp;   // (b * Hq + hq) * Sq + s
   if (row >= static_cast<long long>(p.B) * p.Hq * p.Sq) return;
   const int s = static_cast<int>(row % p.Sq);
   const long long bh = row / p.Sq;
   const int hq = static_cast<int>(bh % p.Hq), b = static_cast<int>(bh / p.Hq);
-  const int pre = p.prefix[b], units = p.prefix[b + 1] - pre;
+  const int all = p.prefix[p.B], pre = p.prefix[b], units = p.prefix[b + 1] - pre;
   T* dst = static_cast<T*>(p.out) + row * D + lane * PER;
   if (units == 0) {
 #pragma unroll
@@ -1078,7 +1080,7 @@ __global__ void __launch_bounds__(256) ragged_merge_kernel(const __grid_constant
     if (lane == 0) p.lse[row] = -INFINITY;
     return;
   }
-  const ShareOut out(p.n_ctas, p.prefix[p.B] * p.Hkv);
+  const ShareOut out(p.n_ctas, all * p.Hkv);
   const int u0 = pre * p.Hkv + hq / p.G * units;   // this head's units: [u0, u0 + units)
   const int c0 = out.of_unit(u0 + kSegmentUnits), c1 = out.of_unit(u0 + units - 1);
   if (c0 == c1) return;
@@ -1089,21 +1091,36 @@ __global__ void __launch_bounds__(256) ragged_merge_kernel(const __grid_constant
   auto part = [&](int c) {
     return (static_cast<size_t>(c) * 2 + ((c == c0 && tail0) ? 1 : 0)) * p.R + r;
   };
+  // Bound by latency (a few KB a row): a batch's loads go out together, the first
+  // batch's with those of the maximum over all parts.
+  PartVec<PER> v[kMergeBatch];
+  float lv[kMergeBatch];
+  auto load = [&](int c) {
+#pragma unroll
+    for (int k = 0; k < kMergeBatch; ++k)
+      if (c + k <= c1) {
+        const size_t at = part(c + k);
+        v[k] = reinterpret_cast<const PartVec<PER>*>(p.part_out + at * D)[lane];
+        lv[k] = p.part_lse2[at];
+      }
+  };
+  load(c0);
   float M = -INFINITY;
   for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_lse2[part(c)]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  M = warp_max(M);
   float acc[PER], L = 0.f;
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-#pragma unroll 8
-  for (int c = c0; c <= c1; ++c) {
-    const size_t at = part(c);
-    const float w = M != -INFINITY ? ex2(p.part_lse2[at] - M) : 0.f;
-    const PartVec<PER> v = reinterpret_cast<const PartVec<PER>*>(p.part_out + at * D)[lane];
-    L += w;
+  for (int c = c0; c <= c1; c += kMergeBatch) {
+    if (c > c0) load(c);
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v.x[e], acc[e]);
+    for (int k = 0; k < kMergeBatch; ++k)
+      if (c + k <= c1) {
+        const float w = M != -INFINITY ? ex2(lv[k] - M) : 0.f;
+        L += w;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k].x[e], acc[e]);
+      }
   }
   const float inv = L > 0.f ? 1.f / L : 0.f;
 #pragma unroll
@@ -1133,8 +1150,8 @@ cudaError_t launch_ragged_impl(const RaggedParams& p, cudaStream_t stream) {
   // the merge overlaps its launch with the ragged kernel's tail
   const long long rows = static_cast<long long>(p.B) * p.Hq * p.Sq;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows));
+  cfg.blockDim = dim3(32 * kMergeRows);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
