@@ -289,6 +289,15 @@ ScoreMod make_mod(const SpanArgs& m, int Sq, int Skv, float scale) {
   r.slopes = m.slopes;
   r.cap_in = m.softcap > 0.f ? 2.f * kLog2e * scale / m.softcap : 0.f;
   r.cap_log2 = m.softcap * kLog2e;
+  // tanh u / u in powers of u^2 on |u| <= 3/4 (score_mod.cuh), scaled; within these
+  // ratios no power of the scale leaves the range of fp32
+  static const double a[5] = {0.9999971985816956, -0.33323076367378235, 0.13226088881492615,
+                              -0.04928038269281387, 0.012318773195147514};
+  const double ratio = m.softcap > 0.f ? static_cast<double>(scale) / m.softcap : 0.0;
+  const bool poly = ratio >= 1e-4 && ratio <= 1e3;
+  for (int i = 0; i < 5; ++i)
+    r.cap_a[i] = poly ? static_cast<float>(a[i] * m.softcap * kLog2e * std::pow(ratio, 2 * i + 1)) : 0.f;
+  r.cap_limit = poly ? static_cast<float>(0.75 / ratio) : 0.f;
   r.pos_offset = Skv - Sq;
   return r;
 }

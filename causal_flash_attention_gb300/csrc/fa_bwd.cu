@@ -291,7 +291,8 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdParams& p, int w) {
   return it;
 }
 
-template <int D, bool kBf16, bool kSpan>
+// kSpan: 0 causal or all keys; 1 key spans; 2 key spans with a cap or a bias
+template <int D, bool kBf16, int kSpan>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa_bwd_kernel(const __grid_constant__ BwdParams p) {
   using Cfg = BwdCfg<D>;
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int k = 0; ok; ++k) {
         BwdItem I{};
         if (w < n_items) {
-          I = bwd_item<kSpan>(p, w);
+          I = bwd_item<kSpan != 0>(p, w);
           if (!(ok = load_step(I, 0))) break;
         }
         if (k > 0) {
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!ok) break;
         w = atomicAdd(p.work, 1);
         if (w < n_items) {   // the next item's K_j, V_j into L2 while this item runs
-          const BwdItem J = bwd_item<kSpan>(p, w);
+          const BwdItem J = bwd_item<kSpan != 0>(p, w);
           for (int c = 0; c < Cfg::kChunks; ++c) {
             tma_prefetch_l2_3d(&p.tm_k, c * kChunk, J.j * kTileN, J.bkv);
             tma_prefetch_l2_3d(&p.tm_v, c * kChunk, J.j * kTileN, J.bkv);
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (k == 0 && !(ok = mbar_wait(drain, 0, abort_flag, p.status))) break;
 #endif
         tr(9);
-        const int N = bwd_item<kSpan>(p, w).n_iter;
+        const int N = bwd_item<kSpan != 0>(p, w).n_iter;
         if (!(ok = issue_s(g) && issue_dp(g))) break;
         for (int n = 0; n < N; ++n, ++g) {
           const int st = g % NQ;
@@ -720,12 +721,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!ok) break;
       const int w = *item_slot;
       if (w >= n_items) break;
-      const BwdItem I = bwd_item<kSpan>(p, w);
+      const BwdItem I = bwd_item<kSpan != 0>(p, w);
       const int kv = I.j * kTileN + r;
       for (int it = 0; it < I.n_iter; ++it, ++g) {
         const int st = g % NQ;
         const uint32_t par = static_cast<uint32_t>(g / NQ) & 1;
         const int i = I.i_start + it % I.n_i;
+        const int q0 = i * kTileM + c0;
+        // kSpan: the spans of query columns 2 l and 2 l + 1 of this warp's half
+        int4 sp = make_int4(0, 0, 0, 0);
+        if constexpr (kSpan)
+          sp = reinterpret_cast<const int4*>(
+              p.spans + (static_cast<size_t>(I.b) * p.Sq_pad + q0))[lane];
         const float* rowv = reinterpret_cast<const float*>(smem + Cfg::kOffRow + st * 1024);
         const float* l2s = rowv + c0;          // L * log2(e) per query column
         const float* dls = rowv + 128 + c0;    // D per query column
@@ -739,24 +746,27 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // query's position q + kv_offset. Column e of this warp's half is masked
         // iff e < thr; thr <= 0 on every tile that is neither diagonal nor
         // ragged, which skip the selects.
-        const int q0 = i * kTileM + c0;
-        const int thr = kv >= p.Skv ? 64 : (p.causal ? min(kv - p.kv_offset - q0, 64) : 0);
-        const bool any_mask = __any_sync(0xffffffffu, thr > 0);
-        uint32_t ppk[32];   // P^T, packed (span form with a cap: P^T (1 - tanh^2))
+        // kSpan: this lane's key row sees column 2 l by bit l of vis0, 2 l + 1 of vis1.
+        int thr = 0;
+        bool any_mask;
+        uint32_t vis0 = 0xffffffffu, vis1 = 0xffffffffu;
         if constexpr (kSpan) {
-          // this lane's key row against query columns 2 l (vis0 bit l) and 2 l + 1 (vis1)
-          const int4 sp = reinterpret_cast<const int4*>(
-              p.spans + (static_cast<size_t>(I.b) * p.Sq_pad + q0))[lane];
           const int k0 = kv - lane;   // this warp's first key
-          const bool partial = __any_sync(
-              0xffffffffu, sp.x > k0 || sp.y < k0 + 32 || sp.z > k0 || sp.w < k0 + 32);
-          uint32_t vis0 = 0xffffffffu, vis1 = 0xffffffffu;
-          if (partial) {
+          any_mask = __any_sync(0xffffffffu,
+                                sp.x > k0 || sp.y < k0 + 32 || sp.z > k0 || sp.w < k0 + 32);
+          if (any_mask) {
             vis0 = transpose_bits(span_bits(sp.x, sp.y, k0), lane);
             vis1 = transpose_bits(span_bits(sp.z, sp.w, k0), lane);
           }
+        } else {
+          thr = kv >= p.Skv ? 64 : (p.causal ? min(kv - p.kv_offset - q0, 64) : 0);
+          any_mask = __any_sync(0xffffffffu, thr > 0);
+        }
+        uint32_t ppk[32];   // P^T, packed (kSpan 2 with a cap: P^T (1 - tanh^2))
+        if constexpr (kSpan == 2) {
           const bool cap = p.mod.cap_in != 0.f;
           const float cs = cap ? 1.f : c;
+          const float inv_cap = cap ? 1.f / p.mod.cap_log2 : 0.f;
           const float bias =
               p.mod.slopes ? p.mod.slopes[I.g * (p.Hq / p.Hkv) + it / I.n_i] * (kLog2eF / cs) : 0.f;
           const float d0 = static_cast<float>(q0 + p.mod.pos_offset - kv);
@@ -784,14 +794,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               tmem_st16(p_dst, pk);
             }
             if (cap) {
-              const float cl = p.mod.cap_log2;
+              float big = 0.f;
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float r0 = cap_r(__uint_as_float(raw[e]), p.mod.cap_in);
-                const float r1 = cap_r(__uint_as_float(raw[e + 1]), p.mod.cap_in);
-                raw[e] = __float_as_uint(fmaf(-2.f * cl, r0, cl));
-                raw[e + 1] = __float_as_uint(fmaf(-2.f * cl, r1, cl));
-                fac[e / 2] = pack2<false>(4.f * r0 * (1.f - r0), 4.f * r1 * (1.f - r1));
+              for (int e = 0; e < 32; e += 2)
+                big = fmax3(big, fabsf(__uint_as_float(raw[e])), fabsf(__uint_as_float(raw[e + 1])));
+              if (__any_sync(0xffffffffu, !(big <= p.mod.cap_limit))) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  const float r0 = cap_r(__uint_as_float(raw[e]), p.mod.cap_in);
+                  const float r1 = cap_r(__uint_as_float(raw[e + 1]), p.mod.cap_in);
+                  raw[e] = __float_as_uint(fmaf(-2.f * p.mod.cap_log2, r0, p.mod.cap_log2));
+                  raw[e + 1] = __float_as_uint(fmaf(-2.f * p.mod.cap_log2, r1, p.mod.cap_log2));
+                  fac[e / 2] = pack2<false>(4.f * r0 * (1.f - r0), 4.f * r1 * (1.f - r1));
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  const float y0 = cap_poly(__uint_as_float(raw[e]), p.mod);
+                  const float y1 = cap_poly(__uint_as_float(raw[e + 1]), p.mod);
+                  raw[e] = __float_as_uint(y0);
+                  raw[e + 1] = __float_as_uint(y1);
+                  const float t0 = y0 * inv_cap, t1 = y1 * inv_cap;   // tanh
+                  fac[e / 2] = pack2<false>(fmaf(-t0, t0, 1.f), fmaf(-t1, t1, 1.f));
+                }
               }
             }
             if (p.mod.slopes) {
@@ -800,7 +825,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 raw[e] = __float_as_uint(fmaf(-bias, fabsf(d0 + static_cast<float>(hh * 32 + e)),
                                               __uint_as_float(raw[e])));
             }
-            if (partial) {
+            if (any_mask) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (!((((e & 1) ? vis1 : vis0) >> (hh * 16 + e / 2)) & 1u))
@@ -831,8 +856,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (lane == 0) mbar_arrive(s_free);
           }
           if (any_mask) {
+            if constexpr (kSpan) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e) raw[e] = (e < thr) ? __float_as_uint(-INFINITY) : raw[e];
+              for (int e = 0; e < 64; ++e)
+                if (!((((e & 1) ? vis1 : vis0) >> (e / 2)) & 1u)) raw[e] = __float_as_uint(-INFINITY);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 64; ++e) raw[e] = (e < thr) ? __float_as_uint(-INFINITY) : raw[e];
+            }
           }
           const uint64_t c2 = f2_pack(c, c);
 #pragma unroll
@@ -1000,7 +1031,7 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 block, siz
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D, bool kBf16, bool kSpan = false>
+template <int D, bool kBf16, int kSpan = 0>
 cudaError_t launch_bwd_impl(const BwdParams& p, cudaStream_t stream) {
   constexpr int smem = BwdCfg<D>::kSmemBytes;
   auto kernel = fa_bwd_kernel<D, kBf16, kSpan>;
@@ -1047,11 +1078,17 @@ cudaError_t launch_bwd_pre_span(const BwdPreParams& p0, cudaStream_t stream) {
 }
 
 cudaError_t launch_bwd_span(const BwdParams& p, int d, bool bf16, cudaStream_t stream) {
+  const bool plain = p.mod.cap_in == 0.f && !p.mod.slopes;
+  auto run = [&](auto D, auto B) {
+    return plain ? launch_bwd_impl<D.value, B.value, 1>(p, stream)
+                 : launch_bwd_impl<D.value, B.value, 2>(p, stream);
+  };
+  using std::integral_constant;
   if (d == 128)
-    return bf16 ? launch_bwd_impl<128, true, true>(p, stream)
-                : launch_bwd_impl<128, false, true>(p, stream);
-  return bf16 ? launch_bwd_impl<64, true, true>(p, stream)
-              : launch_bwd_impl<64, false, true>(p, stream);
+    return bf16 ? run(integral_constant<int, 128>{}, std::true_type{})
+                : run(integral_constant<int, 128>{}, std::false_type{});
+  return bf16 ? run(integral_constant<int, 64>{}, std::true_type{})
+              : run(integral_constant<int, 64>{}, std::false_type{});
 }
 
 cudaError_t launch_bwd_tc(const BwdParams& p, int d, bool bf16, cudaStream_t stream) {

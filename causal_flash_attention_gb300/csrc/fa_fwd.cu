@@ -49,8 +49,8 @@
 // Span form (kSpan, one tile per CTA): row i sees the keys of its own span
 // [key_begin_i, key_end_i) instead of the causal range. The CTA walks the key
 // tiles from the least begin to the greatest end of its 128 rows; a row masks
-// a tile that its span does not cover by a bit mask per 32 keys. Scores may be
-// capped (softcap * tanh(s / softcap)) and biased by distance
+// a tile that its span does not cover by a bit mask per 32 keys. kSpan = 2: scores
+// may be capped (softcap * tanh(s / softcap)) and biased by distance
 // (-slope_h |i + Skv - Sq - j|) before the mask, in place of S in registers. A
 // row that sees nothing gets out = 0 and LSE = -inf.
 #include <algorithm>
@@ -124,7 +124,8 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, int* s
   }
 }
 
-template <int D, bool kBf16, int T, bool kSpan>
+// kSpan: 0 causal or all keys; 1 key spans; 2 key spans with a cap or a bias
+template <int D, bool kBf16, int T, int kSpan>
 __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
     fa_fwd_kernel(const __grid_constant__ FwdParams p) {
   static_assert(!kSpan || T == 1, "the span form has one query tile per CTA");
@@ -373,9 +374,9 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
     const uint32_t o_tmem = tmem + lane_off + 128 * T + t * 128;
     const uint32_t p_tmem = Cfg::kSepP ? o_tmem + D : s_tmem;
     // span form with a cap: the capped scores come out in the log2 domain
-    const float c = (kSpan && p.mod.cap_in != 0.f) ? 1.f : p.scale_log2;
-    float bias = 0.f;   // span form: the distance bias per key, in units of 1 / c
-    if constexpr (kSpan)
+    const float c = (kSpan == 2 && p.mod.cap_in != 0.f) ? 1.f : p.scale_log2;
+    float bias = 0.f;   // kSpan 2: the distance bias per key, in units of 1 / c
+    if constexpr (kSpan == 2)
       if (p.mod.slopes) bias = p.mod.slopes[hq] * (kLog2eF / c);
 
     Tracer tr(((warp == 2 || warp == 6) && lane == 0) ? p.trace : nullptr, 2 + t);
@@ -405,21 +406,41 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
         if (lane == 0) mbar_arrive(bars.sfr(t));
       }
       const int kv0 = (tile0 + j) * kTileN;
+      float row_off = 0.f;   // kSpan 2: added to every scaled score of the row
       // inline mask: causal (key after the query's position) and keys past the
       // sequence end; lim = last visible key of this row (rows past Sq are
       // never stored, so their limit may run past Skv - 1)
       if constexpr (kSpan) {
-        if (p.mod.cap_in != 0.f) {
-          const float cap = p.mod.cap_log2;
+        if constexpr (kSpan == 2) {
+          if (p.mod.cap_in != 0.f) {
+            float big = 0.f;
 #pragma unroll
-          for (int i = 0; i < kTileN; ++i)
-            s[i] = fmaf(-2.f * cap, cap_r(s[i], p.mod.cap_in), cap);
-        }
-        if (p.mod.slopes) {
-          const float d0 = static_cast<float>(kv0 - row - p.mod.pos_offset);
+            for (int i = 0; i < kTileN; i += 2) big = fmax3(big, fabsf(s[i]), fabsf(s[i + 1]));
+            if (__any_sync(0xffffffffu, !(big <= p.mod.cap_limit))) {
 #pragma unroll
-          for (int i = 0; i < kTileN; ++i)
-            s[i] = fmaf(-bias, fabsf(d0 + static_cast<float>(i)), s[i]);
+              for (int i = 0; i < kTileN; ++i) s[i] = cap_exact(s[i], p.mod);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kTileN; ++i) s[i] = cap_poly(s[i], p.mod);
+            }
+          }
+          if (p.mod.slopes) {
+            // |distance| is d0 + i or -d0 - i; on a tile to one side of the row the
+            // part without i waits in row_off
+            const int d0 = kv0 - row - p.mod.pos_offset;
+            const bool after = d0 >= 0, before = d0 <= 1 - kTileN;
+            if (__all_sync(0xffffffffu, after || before)) {
+              const float step = after ? -bias : bias;
+              row_off = step * static_cast<float>(d0) * c;
+#pragma unroll
+              for (int i = 0; i < kTileN; ++i) s[i] = fmaf(step, static_cast<float>(i), s[i]);
+            } else {
+              const float d = static_cast<float>(d0);
+#pragma unroll
+              for (int i = 0; i < kTileN; ++i)
+                s[i] = fmaf(-bias, fabsf(d + static_cast<float>(i)), s[i]);
+            }
+          }
         }
         if (kv0 < row_lo || kv0 + kTileN > row_hi) {
 #pragma unroll
@@ -460,13 +481,15 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
           mx3 = fmaxf(mx3, s[i + 3]);
         }
       }
-      const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * c;
+      float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * c;
+      if (kSpan == 2) mx += row_off;
       float m_new = m_ref;
       if (mx > m_ref + kRescaleThreshold) m_new = mx;
       const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
       const float alpha = ex2(m_ref - m_use);   // 0 when m_ref = -inf
       const bool moved = (m_new != m_ref);
       m_ref = m_new;
+      const float sub = kSpan == 2 ? m_use - row_off : m_use;
 
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
       uint32_t pk[32];
@@ -475,7 +498,7 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
         if constexpr (Cfg::kPaired) {
           // element e adds into sum[e % 4] as in the scalar form: pairs with
           // i even into (sum0, sum1), i odd into (sum2, sum3)
-          const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_use, -m_use);
+          const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-sub, -sub);
           uint64_t s01 = f2_pack(sum[0], sum[1]), s23 = f2_pack(sum[2], sum[3]);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -491,8 +514,8 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float p0 = ex2(fmaf(s[h * 64 + 2 * i], c, -m_use));
-            const float p1 = ex2(fmaf(s[h * 64 + 2 * i + 1], c, -m_use));
+            const float p0 = ex2(fmaf(s[h * 64 + 2 * i], c, -sub));
+            const float p1 = ex2(fmaf(s[h * 64 + 2 * i + 1], c, -sub));
             sum[(2 * i) & 3] += p0;
             sum[(2 * i + 1) & 3] += p1;
             pk[i] = pack2<kBf16>(p0, p1);
@@ -587,7 +610,7 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
   }
 }
 
-template <int D, bool kBf16, int T, bool kSpan = false>
+template <int D, bool kBf16, int T, int kSpan = 0>
 cudaError_t launch_fwd_impl(const FwdParams& p0, cudaStream_t stream) {
   constexpr int smem = kSpan ? FwdCfg<D, T>::kSmemBytesSpan : FwdCfg<D, T>::kSmemBytes;
   auto kernel = fa_fwd_kernel<D, kBf16, T, kSpan>;
@@ -632,11 +655,17 @@ cudaError_t launch_fwd_d(const FwdParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_fwd_span(const FwdParams& p, int d, bool bf16, cudaStream_t stream) {
+  const bool plain = p.mod.cap_in == 0.f && !p.mod.slopes;
+  auto run = [&](auto D, auto B) {
+    return plain ? launch_fwd_impl<D.value, B.value, 1, 1>(p, stream)
+                 : launch_fwd_impl<D.value, B.value, 1, 2>(p, stream);
+  };
+  using std::integral_constant;
   if (d == 128)
-    return bf16 ? launch_fwd_impl<128, true, 1, true>(p, stream)
-                : launch_fwd_impl<128, false, 1, true>(p, stream);
-  return bf16 ? launch_fwd_impl<64, true, 1, true>(p, stream)
-              : launch_fwd_impl<64, false, 1, true>(p, stream);
+    return bf16 ? run(integral_constant<int, 128>{}, std::true_type{})
+                : run(integral_constant<int, 128>{}, std::false_type{});
+  return bf16 ? run(integral_constant<int, 64>{}, std::true_type{})
+              : run(integral_constant<int, 64>{}, std::false_type{});
 }
 
 cudaError_t launch_fwd_tc(const FwdParams& p, int d, bool bf16, cudaStream_t stream) {

@@ -47,4 +47,20 @@ __device__ __forceinline__ float cap_r(float s, float cap_in) {
   return rcp_approx(1.f + ex2(s * cap_in));
 }
 
+// The cap by a polynomial where every score of the warp is inside |u| <= 3/4,
+// u = s * scale / softcap: tanh u = u (a0 + a1 w + ... + a4 w^4), w = u^2, a
+// degree-9 minimax fit (by reweighted least squares) off by 1.9e-7, 2.7e-7 in fp32.
+// Seven multiply-adds and no special function, which the softmax is short of; the
+// coefficients come with the powers of scale / softcap and softcap * log2(e)
+// multiplied in, so y = softcap log2(e) tanh u directly from the unscaled score.
+__device__ __forceinline__ float cap_poly(float s, const ScoreMod& m) {
+  const float w = s * s;
+  return s * fmaf(w, fmaf(w, fmaf(w, fmaf(w, m.cap_a[4], m.cap_a[3]), m.cap_a[2]), m.cap_a[1]),
+                  m.cap_a[0]);
+}
+// Past that, by the exponential form.
+__device__ __forceinline__ float cap_exact(float s, const ScoreMod& m) {
+  return fmaf(-2.f * m.cap_log2, cap_r(s, m.cap_in), m.cap_log2);
+}
+
 }  // namespace fa
