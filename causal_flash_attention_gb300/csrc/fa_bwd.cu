@@ -765,20 +765,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         uint32_t ppk[32];   // P^T, packed (kSpan 2 with a cap: P^T (1 - tanh^2))
         if constexpr (kSpan == 2) {
           const bool cap = p.mod.cap_in != 0.f;
-          const float cs = cap ? 1.f : c;
           const float inv_cap = cap ? 1.f / p.mod.cap_log2 : 0.f;
           const float bias =
-              p.mod.slopes ? p.mod.slopes[I.g * (p.Hq / p.Hkv) + it / I.n_i] * (kLog2eF / cs) : 0.f;
+              p.mod.slopes ? p.mod.slopes[I.g * (p.Hq / p.Hkv) + it / I.n_i] * kLog2eF : 0.f;
           const float d0 = static_cast<float>(q0 + p.mod.pos_offset - kv);
-          // Two halves of 32 columns, so that the cap's factors fit into
-          // registers. Packed P^T goes over score columns this warp has read
-          // itself, or into the P^T buffer at d = 64: the first half's after the
-          // second half has been read.
+          // Two halves of 32 columns, for the registers. Packed P^T goes over score
+          // columns this warp has read itself, or into the P^T buffer at d = 64: the
+          // first half's after the second half has been read.
           const uint32_t p_dst = Cfg::kSepQ ? t_p + half * 32 : t_s + half * 96;
           uint32_t pk[16];
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
-            uint32_t raw[32], fac[16];
+            uint32_t raw[32];
             tmem_ld32(t_s + c0 + hh * 32, raw);
             tmem_wait_ld();
             if (hh == 1) {
@@ -800,47 +798,58 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 big = fmax3(big, fabsf(__uint_as_float(raw[e])), fabsf(__uint_as_float(raw[e + 1])));
               if (__any_sync(0xffffffffu, !(big <= p.mod.cap_limit))) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                  const float r0 = cap_r(__uint_as_float(raw[e]), p.mod.cap_in);
-                  const float r1 = cap_r(__uint_as_float(raw[e + 1]), p.mod.cap_in);
-                  raw[e] = __float_as_uint(fmaf(-2.f * p.mod.cap_log2, r0, p.mod.cap_log2));
-                  raw[e + 1] = __float_as_uint(fmaf(-2.f * p.mod.cap_log2, r1, p.mod.cap_log2));
-                  fac[e / 2] = pack2<false>(4.f * r0 * (1.f - r0), 4.f * r1 * (1.f - r1));
-                }
+                for (int e = 0; e < 32; ++e)
+                  raw[e] = __float_as_uint(cap_exact(__uint_as_float(raw[e]), p.mod));
               } else {
+                const CapPoly poly(p.mod);
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                  const float y0 = cap_poly(__uint_as_float(raw[e]), p.mod);
-                  const float y1 = cap_poly(__uint_as_float(raw[e + 1]), p.mod);
+                  float y0, y1;
+                  f2_unpack(poly(f2_pack(__uint_as_float(raw[e]), __uint_as_float(raw[e + 1]))), y0, y1);
                   raw[e] = __float_as_uint(y0);
                   raw[e + 1] = __float_as_uint(y1);
-                  const float t0 = y0 * inv_cap, t1 = y1 * inv_cap;   // tanh
-                  fac[e / 2] = pack2<false>(fmaf(-t0, t0, 1.f), fmaf(-t1, t1, 1.f));
                 }
               }
             }
-            if (p.mod.slopes) {
+            // P = 2^(y c - L) with the bias, packed; and with a cap P (1 - tanh^2),
+            // tanh = y / (softcap log2(e))
+            auto weights = [&](auto capped, auto biased) {
+              const uint64_t c2 = f2_pack(c, c), ic2 = f2_pack(inv_cap, inv_cap);
+              const uint64_t nb2 = f2_pack(-bias, -bias), one2 = f2_pack(1.f, 1.f);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                raw[e] = __float_as_uint(fmaf(-bias, fabsf(d0 + static_cast<float>(hh * 32 + e)),
-                                              __uint_as_float(raw[e])));
-            }
+              for (int e = 0; e < 32; e += 2) {
+                const float2 l2 = *reinterpret_cast<const float2*>(l2s + hh * 32 + e);
+                const uint64_t y = f2_pack(__uint_as_float(raw[e]), __uint_as_float(raw[e + 1]));
+                uint64_t x = f2_pack(-l2.x, -l2.y);
+                x = capped.value ? f2_add(y, x) : f2_fma(y, c2, x);
+                if (biased.value)
+                  x = f2_fma(nb2, f2_pack(fabsf(d0 + static_cast<float>(hh * 32 + e)),
+                                          fabsf(d0 + static_cast<float>(hh * 32 + e + 1))), x);
+                float p0, p1;
+                f2_unpack(x, p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                pk[e / 2] = pack2<kBf16>(p0, p1);
+                if (capped.value) {
+                  const uint64_t t = f2_mul(y, ic2);
+                  f2_unpack(f2_mul(f2_pack(p0, p1), f2_sub(one2, f2_mul(t, t))), p0, p1);
+                  ppk[hh * 16 + e / 2] = pack2<kBf16>(p0, p1);
+                } else {
+                  ppk[hh * 16 + e / 2] = pk[e / 2];
+                }
+              }
+            };
+            if (!cap) weights(std::false_type{}, std::true_type{});
+            else if (p.mod.slopes) weights(std::true_type{}, std::true_type{});
+            else weights(std::true_type{}, std::false_type{});
+            // masked entries, whatever they came to, are cleared in the packed words
             if (any_mask) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((((e & 1) ? vis1 : vis0) >> (hh * 16 + e / 2)) & 1u))
-                  raw[e] = __float_as_uint(-INFINITY);
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 l2 = *reinterpret_cast<const float2*>(l2s + hh * 32 + e);
-              const float p0 = ex2(fmaf(__uint_as_float(raw[e]), cs, -l2.x));
-              const float p1 = ex2(fmaf(__uint_as_float(raw[e + 1]), cs, -l2.y));
-              pk[e / 2] = pack2<kBf16>(p0, p1);
-              ppk[hh * 16 + e / 2] = pk[e / 2];
-              if (cap) {
-                const float2 f = unpack2<false>(fac[e / 2]);
-                ppk[hh * 16 + e / 2] = pack2<kBf16>(p0 * f.x, p1 * f.y);
+              for (int e = 0; e < 16; ++e) {
+                const uint32_t keep = (((vis0 >> (hh * 16 + e)) & 1u) ? 0x0000ffffu : 0u) |
+                                      (((vis1 >> (hh * 16 + e)) & 1u) ? 0xffff0000u : 0u);
+                pk[e] &= keep;
+                ppk[hh * 16 + e] &= keep;
               }
             }
           }

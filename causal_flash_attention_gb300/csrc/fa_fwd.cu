@@ -420,8 +420,10 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
 #pragma unroll
               for (int i = 0; i < kTileN; ++i) s[i] = cap_exact(s[i], p.mod);
             } else {
+              const CapPoly poly(p.mod);
 #pragma unroll
-              for (int i = 0; i < kTileN; ++i) s[i] = cap_poly(s[i], p.mod);
+              for (int i = 0; i < kTileN; i += 2)
+                f2_unpack(poly(f2_pack(s[i], s[i + 1])), s[i], s[i + 1]);
             }
           }
           if (p.mod.slopes) {

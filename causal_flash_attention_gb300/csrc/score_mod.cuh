@@ -53,11 +53,18 @@ __device__ __forceinline__ float cap_r(float s, float cap_in) {
 // Seven multiply-adds and no special function, which the softmax is short of; the
 // coefficients come with the powers of scale / softcap and softcap * log2(e)
 // multiplied in, so y = softcap log2(e) tanh u directly from the unscaled score.
-__device__ __forceinline__ float cap_poly(float s, const ScoreMod& m) {
-  const float w = s * s;
-  return s * fmaf(w, fmaf(w, fmaf(w, fmaf(w, m.cap_a[4], m.cap_a[3]), m.cap_a[2]), m.cap_a[1]),
-                  m.cap_a[0]);
-}
+struct CapPoly {
+  uint64_t a[5];
+  __device__ __forceinline__ explicit CapPoly(const ScoreMod& m) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) a[i] = f2_pack(m.cap_a[i], m.cap_a[i]);
+  }
+  // two scores at a time, in paired fp32 instructions
+  __device__ __forceinline__ uint64_t operator()(uint64_t s) const {
+    const uint64_t w = f2_mul(s, s);
+    return f2_mul(s, f2_fma(w, f2_fma(w, f2_fma(w, f2_fma(w, a[4], a[3]), a[2]), a[1]), a[0]));
+  }
+};
 // Past that, by the exponential form.
 __device__ __forceinline__ float cap_exact(float s, const ScoreMod& m) {
   return fmaf(-2.f * m.cap_log2, cap_r(s, m.cap_in), m.cap_log2);
