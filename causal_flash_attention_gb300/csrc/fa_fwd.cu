@@ -132,6 +132,9 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
   using Cfg = FwdCfg<D, T>;
   static_assert(!kSpan || Cfg::kOffSpan % 16 == 0, "read as 16-byte vectors");
   constexpr int NS = Cfg::kStages;
+  // with a cap or a bias the paired form pays at d = 128 (2048 rows over 8192 keys
+  // with a cap, 32 heads: 319 us against 337), and at d = 64 its spills cost what it gains
+  constexpr bool kPaired = kSpan == 2 ? D == 128 : Cfg::kPaired;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
         }
       }
       float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
-      if constexpr (Cfg::kPaired) {
+      if constexpr (kPaired) {
 #pragma unroll
         for (int i = 4; i + 8 <= kTileN; i += 8) {
           mx0 = fmax3(mx0, s[i], s[i + 4]);
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
       uint32_t pk[32];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if constexpr (Cfg::kPaired) {
+        if constexpr (kPaired) {
           // element e adds into sum[e % 4] as in the scalar form: pairs with
           // i even into (sum0, sum1), i odd into (sum2, sum3)
           const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-sub, -sub);
