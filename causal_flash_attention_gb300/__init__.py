@@ -11,8 +11,13 @@ kernels; there is no other code path. `attention_forward` / `attention_backward`
 additionally allocate their outputs (and the backward workspace) with
 PyTorch.
 
-The library is built in-tree by `causal_flash_attention_gb300.build.build()`;
-loading it raises if it has not been built.
+The calls for span attention, the ragged paged cache and query/key preparation
+go through a native module beside the library (_fa_torch, csrc/fa_torch.cpp), which
+checks the tensors, allocates what is missing and makes the library call: one of
+them is a few microseconds of host time.
+
+Library and module are built in-tree by `causal_flash_attention_gb300.build.build()`;
+loading them raises if they have not been built.
 """
 from __future__ import annotations
 
@@ -352,88 +357,31 @@ def attention_backward(q, k, v, out, dout, lse, causal=True, scale=None, workspa
 
 
 # ------------------------------------------------------------- key spans --
-# The calls below check what they are given: a tensor on another device, of
-# another type or size would have the kernels read memory that is not its own.
-# A call is a few microseconds of host time, so the checks are plain
-# comparisons and what a call allocates itself is not checked again.
-_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_native_module = None
 
 
-def _cuda_index(t, name="q"):
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return dev
+def _native():
+    """The native part of the binding (loaded once)."""
+    global _native_module
+    if _native_module is None:
+        try:
+            from . import _fa_torch
+        except ImportError as e:
+            raise RuntimeError("the native binding module is missing: build it with "
+                               "causal_flash_attention_gb300.build.build()") from e
+        _native_module = _fa_torch
+    return _native_module
 
 
-def _fit(name, t, dev, dtype, shape):
-    """t has to be contiguous on device `dev`, with this dtype and shape."""
-    if (t.get_device() != dev or t.dtype is not dtype or t.shape != shape
-            or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on cuda:{dev}, "
-                         f"not {'a' if t.is_contiguous() else 'a strided'} {t.dtype} tensor "
-                         f"{tuple(t.shape)} on {t.device}")
-
-
-def _run(name, dev, stream, *args):
-    """Call the library on device `dev`; the stream handle goes last."""
-    fn = getattr(_lib or lib(), name)
-    if stream is None:
-        stream = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
-    elif not isinstance(stream, int):
+def _call(name, where, *args, stream=None):
+    """Call the native function `name` with the loaded library; FAError for the library's
+    error codes, named after its entry point `where`."""
+    if stream is not None and not isinstance(stream, int):
         stream = stream.cuda_stream
-    if dev == _get_device():
-        rc = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, stream)
-    if rc != 0:
-        raise FAError(rc, name)
-
-
-def _alloc_stream(stream, dev):
-    """Where a call on `stream` allocates: that stream's own memory pool, so that the memory's
-    earlier and later users are ordered with the call."""
-    if stream is None:
-        return _NULL_CONTEXT
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=dev)
-    return torch.cuda.stream(stream)
-
-
-def _workspace_bytes(workspace, dev):
-    """Size of a caller's workspace (0 for None), which has to be dense and on device `dev`."""
-    if workspace is None:
-        return 0
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
-    return workspace.numel() * workspace.element_size()
-
-
-def _span_inputs(q, k, v, key_begin, key_end, slopes):
-    """Checks the inputs; (device, (B, Hq, Hkv, Sq, Skv, d))."""
-    dev = _cuda_index(q)
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q and k must be [B, H, S, d]")
-    B, Hq, Sq, d = q.shape
-    _, Hkv, Skv, _ = ks = k.shape
-    dt = q.dtype
-    if not q.is_contiguous():
-        raise ValueError("q must be contiguous")
-    _fit("k", k, dev, dt, (B, Hkv, Skv, d))
-    _fit("v", v, dev, dt, ks)
-    _fit("key_begin", key_begin, dev, torch.int32, (B, Sq))
-    _fit("key_end", key_end, dev, torch.int32, (B, Sq))
-    if slopes is not None:
-        _fit("slopes", slopes, dev, torch.float32, (Hq,))
-    return dev, (B, Hq, Hkv, Sq, Skv, d)
-
-
-def _span_fwd(dev, dims, q, k, v, key_begin, key_end, out, lse, softcap, slopes, scale, stream):
-    scale = 1.0 / math.sqrt(dims[5]) if scale is None else float(scale)
-    _run("fa_fwd_span", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), key_begin.data_ptr(),
-         key_end.data_ptr(), out.data_ptr(), lse.data_ptr(), *dims, scale, softcap, _ptr(slopes),
-         DTYPE_CODES.get(q.dtype, -1))
+    r = getattr(_native_module or _native(), name)((_lib or lib())._handle, *args, stream)
+    if type(r) is int:
+        raise FAError(r, where)
+    return r
 
 
 def fa_fwd_span(q, k, v, key_begin, key_end, out, lse, softcap=0.0, slopes=None, scale=None,
@@ -441,63 +389,43 @@ def fa_fwd_span(q, k, v, key_begin, key_end, out, lse, softcap=0.0, slopes=None,
     """Call fa_fwd_span: row i of batch b sees keys key_begin[b, i] <= j < key_end[b, i]
     (int32 [B,Sq]); scores capped by softcap (0: not) and biased by
     -slopes[h] * |i + Skv - Sq - j| (float32 [Hq], or None)."""
-    dev, dims = _span_inputs(q, k, v, key_begin, key_end, slopes)
-    _fit("out", out, dev, q.dtype, q.shape)
-    _fit("lse", lse, dev, torch.float32, q.shape[:3])
-    _span_fwd(dev, dims, q, k, v, key_begin, key_end, out, lse, softcap, slopes, scale, stream)
+    _given(out=out, lse=lse)
+    _call("span_forward", "fa_fwd_span", q, k, v, key_begin, key_end, out, lse, softcap, slopes,
+          scale, stream=stream)
+
+
+def _given(**named):
+    """The tensors a caller of the C-named functions has to bring."""
+    for name, t in named.items():
+        if t is None:
+            raise ValueError(f"{name} must be a tensor")
 
 
 def fa_bwd_span_workspace_bytes(B, Hq, Hkv, Sq, Skv, d) -> int:
     return int(lib().fa_bwd_span_workspace_bytes(B, Hq, Hkv, Sq, Skv, d))
 
 
-def _span_bwd(dev, dims, q, k, v, key_begin, key_end, out, dout, lse, dq, dk, dv, workspace,
-              softcap, slopes, scale, stream):
-    _fit("out", out, dev, q.dtype, q.shape)
-    _fit("dout", dout, dev, q.dtype, q.shape)
-    _fit("lse", lse, dev, torch.float32, q.shape[:3])
-    scale = 1.0 / math.sqrt(dims[5]) if scale is None else float(scale)
-    _run("fa_bwd_span", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), key_begin.data_ptr(),
-         key_end.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(),
-         dk.data_ptr(), dv.data_ptr(), *dims, scale, softcap, _ptr(slopes),
-         DTYPE_CODES.get(q.dtype, -1), _ptr(workspace), _workspace_bytes(workspace, dev))
-
-
 def fa_bwd_span(q, k, v, key_begin, key_end, out, dout, lse, dq, dk, dv, workspace, softcap=0.0,
                 slopes=None, scale=None, stream=None):
     """Call fa_bwd_span; `workspace` is a device tensor of at least
     fa_bwd_span_workspace_bytes(...) bytes."""
-    dev, dims = _span_inputs(q, k, v, key_begin, key_end, slopes)
-    _fit("dq", dq, dev, q.dtype, q.shape)
-    _fit("dk", dk, dev, q.dtype, k.shape)
-    _fit("dv", dv, dev, q.dtype, k.shape)
-    _span_bwd(dev, dims, q, k, v, key_begin, key_end, out, dout, lse, dq, dk, dv, workspace,
-              softcap, slopes, scale, stream)
+    _given(dq=dq, dk=dk, dv=dv, workspace=workspace)
+    _call("span_backward", "fa_bwd_span", q, k, v, key_begin, key_end, out, dout, lse, dq, dk, dv,
+          workspace, softcap, slopes, scale, stream=stream)
 
 
 def attention_span_forward(q, k, v, key_begin, key_end, softcap=0.0, slopes=None, scale=None,
                            stream=None):
     """Allocate out and lse and run fa_fwd_span. Returns (out, lse)."""
-    dev, dims = _span_inputs(q, k, v, key_begin, key_end, slopes)
-    with _alloc_stream(stream, dev):
-        out = torch.empty_like(q)
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
-    _span_fwd(dev, dims, q, k, v, key_begin, key_end, out, lse, softcap, slopes, scale, stream)
-    return out, lse
+    return _call("span_forward", "fa_fwd_span", q, k, v, key_begin, key_end, None, None, softcap,
+                 slopes, scale, stream=stream)
 
 
 def attention_span_backward(q, k, v, out, dout, lse, key_begin, key_end, softcap=0.0,
                             slopes=None, scale=None, workspace=None, stream=None):
     """Allocate dq, dk, dv (and a workspace unless given) and run fa_bwd_span."""
-    dev, dims = _span_inputs(q, k, v, key_begin, key_end, slopes)
-    with _alloc_stream(stream, dev):
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
-        if workspace is None:
-            workspace = torch.empty(lib().fa_bwd_span_workspace_bytes(*dims), dtype=torch.uint8,
-                                    device=dev)
-    _span_bwd(dev, dims, q, k, v, key_begin, key_end, out, dout, lse, dq, dk, dv, workspace,
-              softcap, slopes, scale, stream)
-    return dq, dk, dv
+    return _call("span_backward", "fa_bwd_span", q, k, v, key_begin, key_end, out, dout, lse, None,
+                 None, None, workspace, softcap, slopes, scale, stream=stream)
 
 
 def key_spans(B, Sq, Skv=None, *, causal=True, window=0, doc_lens=None, prefix_lens=None,
@@ -556,43 +484,8 @@ def key_spans(B, Sq, Skv=None, *, causal=True, window=0, doc_lens=None, prefix_l
 
 
 # ------------------------------------------------------ ragged paged cache --
-def _cache_inputs(dev, dt, B, Hkv, d, k_cache, v_cache, block_table, seq_lens):
-    """Checks a paged cache, its table and the lengths; (block_size, num_blocks, max_blocks)."""
-    if k_cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("caches [num_blocks,Hkv,block_size,d], table [B,max_blocks]")
-    num_blocks, _, block_size, _ = cs = k_cache.shape
-    _fit("k_cache", k_cache, dev, dt, (num_blocks, Hkv, block_size, d))
-    _fit("v_cache", v_cache, dev, dt, cs)
-    max_blocks = block_table.shape[1]
-    _fit("block_table", block_table, dev, torch.int32, (B, max_blocks))
-    _fit("seq_lens", seq_lens, dev, torch.int32, (B,))
-    return block_size, num_blocks, max_blocks
-
-
-def _ragged_inputs(q, k_cache, v_cache, block_table, seq_lens, slopes):
-    """Checks the inputs; (device, (B, Hq, Hkv, Sq, d, block_size, num_blocks, max_blocks))."""
-    dev = _cuda_index(q)
-    if q.dim() != 4 or k_cache.dim() != 4 or not q.is_contiguous():
-        raise ValueError("q [B,Hq,Sq,d] contiguous, caches [num_blocks,Hkv,block_size,d]")
-    B, Hq, Sq, d = q.shape
-    Hkv = k_cache.shape[1]
-    cache = _cache_inputs(dev, q.dtype, B, Hkv, d, k_cache, v_cache, block_table, seq_lens)
-    if slopes is not None:
-        _fit("slopes", slopes, dev, torch.float32, (Hq,))
-    return dev, (B, Hq, Hkv, Sq, d) + cache
-
-
 def fa_fwd_ragged_paged_workspace_bytes(B, Hq, Hkv, Sq, d, block_size, max_blocks) -> int:
     return int(lib().fa_fwd_ragged_paged_workspace_bytes(B, Hq, Hkv, Sq, d, block_size, max_blocks))
-
-
-def _ragged(dev, dims, q, k_cache, v_cache, block_table, seq_lens, out, lse, workspace, window,
-            softcap, slopes, scale, stream):
-    scale = 1.0 / math.sqrt(dims[4]) if scale is None else float(scale)
-    _run("fa_fwd_ragged_paged", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-         block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), *dims,
-         int(window), scale, softcap, _ptr(slopes), DTYPE_CODES.get(q.dtype, -1), _ptr(workspace),
-         _workspace_bytes(workspace, dev))
 
 
 def fa_fwd_ragged_paged(q, k_cache, v_cache, block_table, seq_lens, out, lse, workspace,
@@ -601,25 +494,16 @@ def fa_fwd_ragged_paged(q, k_cache, v_cache, block_table, seq_lens, out, lse, wo
     k_cache/v_cache [num_blocks,Hkv,block_size,d]; block_table int32 [B,max_blocks];
     seq_lens int32 [B]; `workspace` a device tensor of at least
     fa_fwd_ragged_paged_workspace_bytes(...) bytes."""
-    dev, dims = _ragged_inputs(q, k_cache, v_cache, block_table, seq_lens, slopes)
-    _fit("out", out, dev, q.dtype, q.shape)
-    _fit("lse", lse, dev, torch.float32, q.shape[:3])
-    _ragged(dev, dims, q, k_cache, v_cache, block_table, seq_lens, out, lse, workspace, window,
-            softcap, slopes, scale, stream)
+    _given(out=out, lse=lse, workspace=workspace)
+    _call("ragged", "fa_fwd_ragged_paged", q, k_cache, v_cache, block_table, seq_lens, out, lse,
+          workspace, window, softcap, slopes, scale, stream=stream)
 
 
 def decode_forward_ragged(q, k_cache, v_cache, block_table, seq_lens, window=0, softcap=0.0,
                           slopes=None, scale=None, stream=None):
     """Allocate out, lse and the workspace and run fa_fwd_ragged_paged. Returns (out, lse)."""
-    dev, dims = _ragged_inputs(q, k_cache, v_cache, block_table, seq_lens, slopes)
-    n = lib().fa_fwd_ragged_paged_workspace_bytes(*dims[:6], dims[7])
-    with _alloc_stream(stream, dev):
-        out = torch.empty_like(q)
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    _ragged(dev, dims, q, k_cache, v_cache, block_table, seq_lens, out, lse, ws, window, softcap,
-            slopes, scale, stream)
-    return out, lse
+    return _call("ragged", "fa_fwd_ragged_paged", q, k_cache, v_cache, block_table, seq_lens, None,
+                 None, None, window, softcap, slopes, scale, stream=stream)
 
 
 # ------------------------------------------------ query / key preparation --
@@ -667,62 +551,14 @@ def rope_turns(inv_freq, device=None):
     return torch.tensor(out, dtype=torch.int64, device=device)
 
 
-def _view(name, t, dev, dtype, shape, written=False):
-    """The fa_view argument of a [B, H, S, d] tensor of any strides but the last."""
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name} must be a {dtype} tensor {tuple(shape)} on cuda:{dev}, not a "
-                         f"{t.dtype} tensor {tuple(t.shape)} on {t.device}")
-    sb, sh, ss, se = t.stride()
-    if se != 1:
-        raise ValueError(f"{name}: the elements of a head must be contiguous")
-    B, H, S, d = shape
-    if written and not t.is_contiguous():
-        reach = d
-        for st, n in sorted(((sb, B), (sh, H), (ss, S))):
-            if n > 1:
-                if st < reach:
-                    raise ValueError(f"{name}: elements overlap in memory")
-                reach = st * n
-    # a dimension of one row has no stride to keep aligned
-    return ctypes.byref(_View(t.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0,
-                              ss if S > 1 else 0))
-
-
-def _rope_inputs(dev, dt, B, S, d, turns, positions, q_weight, k_weight):
-    """Checks what the three calls share; rope_dim."""
-    n = 0
-    if turns is not None:
-        n = turns.numel()
-        _fit("turns", turns, dev, torch.int64, (n,))
-    if positions is not None:
-        _fit("positions", positions, dev, torch.int32, (B, S))
-    if q_weight is not None:
-        _fit("q_weight", q_weight, dev, dt, (d,))
-    if k_weight is not None:
-        _fit("k_weight", k_weight, dev, dt, (d,))
-    return 2 * n
-
-
-def _qk_dims(q, k, name="q"):
-    dev = _cuda_index(q, name)
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q [B,Hq,S,d] and k [B,Hkv,S,d] (any strides but the last)")
-    B, Hq, S, d = q.shape
-    return dev, B, Hq, k.shape[1], S, d
-
-
 def fa_qk_norm_rope(q, k, q_out, k_out, turns, positions=None, q_weight=None, k_weight=None,
                     eps=1e-6, interleaved=False, rope_scale=1.0, stream=None):
     """Call fa_qk_norm_rope on views q, q_out [B,Hq,S,d] and k, k_out [B,Hkv,S,d] (any strides
     but the last); turns as from rope_turns (rope_dim = 2 * its length; None: no rotation);
     positions int32 [B,S] or None (row s at position s); both weights [d] or neither."""
-    dev, B, Hq, Hkv, S, d = _qk_dims(q, k)
-    dt, qs, ks = q.dtype, (B, Hq, S, d), (B, Hkv, S, d)
-    rope_dim = _rope_inputs(dev, dt, B, S, d, turns, positions, q_weight, k_weight)
-    _run("fa_qk_norm_rope", dev, stream, _view("q", q, dev, dt, qs), _view("k", k, dev, dt, ks),
-         _view("q_out", q_out, dev, dt, qs, True), _view("k_out", k_out, dev, dt, ks, True),
-         _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions), _ptr(turns), rope_dim,
-         1 if interleaved else 0, rope_scale, B, Hq, Hkv, S, d, DTYPE_CODES.get(dt, -1))
+    _given(q_out=q_out, k_out=k_out)
+    _call("norm_rope", "fa_qk_norm_rope", q, k, q_out, k_out, turns, positions, q_weight, k_weight,
+          eps, interleaved, rope_scale, stream=stream)
 
 
 def fa_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hkv, S, d, norm=True) -> int:
@@ -734,19 +570,9 @@ def fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, dq_weight, dk_weight, work
                         interleaved=False, rope_scale=1.0, stream=None):
     """Call fa_qk_norm_rope_bwd: views as for fa_qk_norm_rope; dq_weight, dk_weight float32 [d]
     and `workspace` (fa_qk_norm_rope_bwd_workspace_bytes bytes) with weights, else None."""
-    dev, B, Hq, Hkv, S, d = _qk_dims(dq_out, dk_out, "dq_out")
-    dt, qs, ks = dq_out.dtype, (B, Hq, S, d), (B, Hkv, S, d)
-    rope_dim = _rope_inputs(dev, dt, B, S, d, turns, positions, q_weight, k_weight)
-    for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
-        if t is not None:
-            _fit(name, t, dev, torch.float32, (d,))
-    _run("fa_qk_norm_rope_bwd", dev, stream, _view("dq_out", dq_out, dev, dt, qs),
-         _view("dk_out", dk_out, dev, dt, ks), q if q is None else _view("q", q, dev, dt, qs),
-         k if k is None else _view("k", k, dev, dt, ks), _view("dq", dq, dev, dt, qs, True),
-         _view("dk", dk, dev, dt, ks, True), _ptr(dq_weight), _ptr(dk_weight), _ptr(q_weight),
-         _ptr(k_weight), eps, _ptr(positions), _ptr(turns), rope_dim, 1 if interleaved else 0,
-         rope_scale, B, Hq, Hkv, S, d, DTYPE_CODES.get(dt, -1), _ptr(workspace),
-         _workspace_bytes(workspace, dev))
+    _call("norm_rope_bwd", "fa_qk_norm_rope_bwd", dq_out, dk_out, q, k, dq, dk, dq_weight,
+          dk_weight, workspace, turns, positions, q_weight, k_weight, eps, interleaved, rope_scale,
+          False, stream=stream)
 
 
 def fa_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, block_table, seq_lens, turns,
@@ -754,29 +580,17 @@ def fa_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, block_table, seq_le
                            rope_scale=1.0, stream=None):
     """Call fa_qk_norm_rope_append: the last Sq tokens of sequences of seq_lens tokens; views q,
     q_out [B,Hq,Sq,d], k, v [B,Hkv,Sq,d]; caches [num_blocks,Hkv,block_size,d] written in place."""
-    dev, B, Hq, Hkv, Sq, d = _qk_dims(q, k)
-    dt, qs, ks = q.dtype, (B, Hq, Sq, d), (B, Hkv, Sq, d)
-    rope_dim = _rope_inputs(dev, dt, B, Sq, d, turns, None, q_weight, k_weight)
-    cache = _cache_inputs(dev, dt, B, Hkv, d, k_cache, v_cache, block_table, seq_lens)
-    _run("fa_qk_norm_rope_append", dev, stream, _view("q", q, dev, dt, qs),
-         _view("k", k, dev, dt, ks), _view("v", v, dev, dt, ks),
-         _view("q_out", q_out, dev, dt, qs, True), k_cache.data_ptr(), v_cache.data_ptr(),
-         block_table.data_ptr(), seq_lens.data_ptr(), _ptr(q_weight), _ptr(k_weight), eps,
-         _ptr(turns), rope_dim, 1 if interleaved else 0, rope_scale, B, Hq, Hkv, Sq, d, *cache,
-         DTYPE_CODES.get(dt, -1))
+    _given(q_out=q_out)
+    _call("append", "fa_qk_norm_rope_append", q, k, v, q_out, k_cache, v_cache, block_table,
+          seq_lens, turns, q_weight, k_weight, eps, interleaved, rope_scale, stream=stream)
 
 
 def qk_norm_rope_forward(q, k, turns, positions=None, q_weight=None, k_weight=None, eps=1e-6,
                          interleaved=False, rope_scale=1.0, stream=None):
     """Allocate contiguous q_out [B,Hq,S,d] and k_out [B,Hkv,S,d] (as the attention calls take
     them) and run fa_qk_norm_rope. Returns (q_out, k_out)."""
-    dev = _cuda_index(q)
-    with _alloc_stream(stream, dev):
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    fa_qk_norm_rope(q, k, q_out, k_out, turns, positions, q_weight, k_weight, eps, interleaved,
-                    rope_scale, stream)
-    return q_out, k_out
+    return _call("norm_rope", "fa_qk_norm_rope", q, k, None, None, turns, positions, q_weight,
+                 k_weight, eps, interleaved, rope_scale, stream=stream)
 
 
 def qk_norm_rope_backward(dq_out, dk_out, q, k, turns, positions=None, q_weight=None,
@@ -786,33 +600,17 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, turns, positions=None, q_weight=
     [B, S, H, d] in memory, as projections give q and k) and, with weights, the float32 weight
     gradients, and run fa_qk_norm_rope_bwd. Returns (dq, dk, dq_weight, dk_weight), the last two
     None without weights. Without weights q and k are not read and may be None."""
-    dev, B, Hq, Hkv, S, d = _qk_dims(dq_out, dk_out, "dq_out")
-    dwq = dwk = ws = None
-    with _alloc_stream(stream, dev):
-        if dq is None:
-            dq = torch.empty((B, S, Hq, d), dtype=dq_out.dtype, device=dev).transpose(1, 2)
-        if dk is None:
-            dk = torch.empty((B, S, Hkv, d), dtype=dq_out.dtype, device=dev).transpose(1, 2)
-        if q_weight is not None:
-            dwq = torch.empty(d, dtype=torch.float32, device=dev)
-            dwk = torch.empty(d, dtype=torch.float32, device=dev)
-            ws = torch.empty(lib().fa_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hkv, S, d, 1),
-                             dtype=torch.uint8, device=dev)
-    fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, dwq, dwk, ws, turns, positions, q_weight,
-                        k_weight, eps, interleaved, rope_scale, stream)
-    return dq, dk, dwq, dwk
+    return _call("norm_rope_bwd", "fa_qk_norm_rope_bwd", dq_out, dk_out, q, k, dq, dk, None, None,
+                 None, turns, positions, q_weight, k_weight, eps, interleaved, rope_scale,
+                 True, stream=stream)
 
 
 def qk_norm_rope_append(q, k, v, k_cache, v_cache, block_table, seq_lens, turns, q_weight=None,
                         k_weight=None, eps=1e-6, interleaved=False, rope_scale=1.0, stream=None):
     """Allocate q_out (contiguous [B,Hq,Sq,d]) and run fa_qk_norm_rope_append, which writes the
     tokens' keys and values into the caches. Returns q_out."""
-    dev = _cuda_index(q)
-    with _alloc_stream(stream, dev):
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    fa_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, block_table, seq_lens, turns,
-                           q_weight, k_weight, eps, interleaved, rope_scale, stream)
-    return q_out
+    return _call("append", "fa_qk_norm_rope_append", q, k, v, None, k_cache, v_cache, block_table,
+                 seq_lens, turns, q_weight, k_weight, eps, interleaved, rope_scale, stream=stream)
 
 
 def decode_step_ragged(q, k, v, k_cache, v_cache, block_table, seq_lens, turns, q_weight=None,

@@ -1,5 +1,6 @@
 """Build libfa.so in-tree: nvcc for sm_103a only, one object per source file,
-compiled in parallel, linked with the static CUDA runtime.
+compiled in parallel, linked with the static CUDA runtime; and _fa_torch, the
+native part of the Python binding (host C++ against the installed torch).
 
     python -m causal_flash_attention_gb300.build            # libfa.so
     python -m causal_flash_attention_gb300.build --all      # + libfa_waittest.so
@@ -21,6 +22,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -41,6 +43,11 @@ VARIANTS = {
     "trace": ["-DFA_TRACE"],
     "waittest": ["-DFA_WAIT_TEST", f"-DFA_WAIT_LIMIT_CYCLES={WAIT_TEST_LIMIT_CYCLES}LL"],
 }
+
+
+# the Python binding's native module, beside the library
+BINDING_SRC = os.path.join(CSRC, "fa_torch.cpp")
+BINDING = os.path.join(PKG, "_fa_torch" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 
 def nvcc() -> str:
@@ -66,6 +73,27 @@ def _paths(variant: str):
     return bdir, lib_path(variant)
 
 
+def _binding_command(out: str) -> list:
+    """The compile-and-link line of the binding, for the torch that is installed."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(root, "lib")
+    cxx = shutil.which("g++") or shutil.which("c++") or "g++"
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *("-isystem" + i for i in inc), BINDING_SRC, "-o", out, "-L" + lib, "-Wl,-rpath," + lib,
+            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-ldl"]
+
+
+def _binding_stale() -> bool:
+    import torch
+    return _stale(BINDING, [BINDING_SRC, os.path.join(CSRC, "..", "..", "include", "fa.h"),
+                            torch.__file__])
+
+
 def build_variants(variants, verbose: bool = False, force: bool = False,
                    ptxas_verbose: bool = False) -> list:
     """Compile every stale object of the given variants in one parallel pool,
@@ -85,6 +113,10 @@ def build_variants(variants, verbose: bool = False, force: bool = False,
                     cmd += ["-Xptxas", "-v"]
                 jobs.append(cmd)
 
+    binding = force or _binding_stale()
+    if binding:
+        jobs.append(_binding_command(BINDING + ".tmp"))
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -94,7 +126,9 @@ def build_variants(variants, verbose: bool = False, force: bool = False,
             if verbose or ptxas_verbose or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError(f"nvcc failed for {cmd[-3]}")
+                raise RuntimeError(f"compilation failed: {' '.join(cmd)}")
+    if binding:
+        os.replace(BINDING + ".tmp", BINDING)
     libs = []
     for variant in variants:
         bdir, lib = _paths(variant)
