@@ -302,17 +302,34 @@ ScoreMod make_mod(const SpanArgs& m, int Sq, int Skv, float scale) {
   return r;
 }
 
-// Extra workspace of the span backward behind ws_layout's.
+// Extra workspace of the span backward behind ws_layout's: the padded spans, and
+// the work list with the partial results of cut tiles (planned) or each key
+// tile's query-tile range.
 struct SpanWs {
-  size_t spans, plan, total;
+  size_t spans, plan, slices, splits, parts, total;
+  bool planned;
+  int max_parts;
 };
 
-SpanWs span_ws(const WsLayout& w, int B, int Sq, int Skv) {
-  SpanWs s;
+SpanWs span_ws(const WsLayout& w, int B, int Hq, int Hkv, int Sq, int Skv, int d) {
+  SpanWs s{};
+  const long long tiles = (Skv + kTileN - 1LL) / kTileN * B, rows = round_up(Sq, kTileM) * B;
+  s.planned = tiles <= kPlanMax && rows <= kPlanRows;
   s.spans = w.total;
-  s.plan = s.spans + static_cast<size_t>(round_up(round_up(Sq, kTileM) * B * 8, 256));
-  const long long n_kv = (Skv + kTileN - 1) / kTileN;
-  s.total = s.plan + static_cast<size_t>(round_up(n_kv * B * 8, 256));
+  s.plan = s.spans + static_cast<size_t>(round_up(rows * 8, 256));
+  if (!s.planned) {
+    s.total = s.plan + static_cast<size_t>(round_up(tiles * 8, 256));
+    return s;
+  }
+  // cut only where there are fewer than two items an SM
+  const long long items = tiles * Hkv;
+  const long long steps = static_cast<long long>(Hq / Hkv) * (rows / B / kTileM);   // of an item, at most
+  s.max_parts = items >= kMaxParts ? 0 : static_cast<int>(std::min<long long>(kMaxParts, items * steps));
+  s.slices = s.plan + 256;   // behind the list's head
+  s.splits = s.slices + static_cast<size_t>(
+                            round_up(std::max<long long>(tiles, s.max_parts) * sizeof(SpanSlice), 256));
+  s.parts = s.splits + static_cast<size_t>(round_up(s.max_parts * 16LL, 256));
+  s.total = s.parts + static_cast<size_t>(s.max_parts) * 2 * kTileN * d * 4;
   return s;
 }
 
@@ -356,7 +373,7 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* out, const
                           scale, dtype);
   if (rc != FA_OK) return rc;
   const WsLayout ws = ws_layout(B, Hq, Sq, d);
-  const SpanWs sws = span_ws(ws, B, Sq, Skv);
+  const SpanWs sws = span_ws(ws, B, Hq, Hkv, Sq, Skv, d);
   if (!workspace || workspace_bytes < (mod ? sws.total : ws.total)) return FA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_ALIGN;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -403,8 +420,30 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* out, const
     pre.key_end = mod->key_end;
     pre.spans = reinterpret_cast<int2*>(wsb + sws.spans);
     pre.plan = reinterpret_cast<int2*>(wsb + sws.plan);
+    p.spans = pre.spans;
+    if (sws.planned) {
+      SpanPlanParams sp{};
+      sp.key_begin = mod->key_begin;
+      sp.key_end = mod->key_end;
+      sp.spans = pre.spans;
+      sp.head = reinterpret_cast<int*>(wsb + sws.plan);
+      sp.slices = reinterpret_cast<SpanSlice*>(wsb + sws.slices);
+      sp.splits = reinterpret_cast<int4*>(wsb + sws.splits);
+      sp.B = B; sp.Sq = Sq; sp.Sq_pad = Sq_pad; sp.Skv = Skv;
+      sp.n_kv_tiles = pre.n_kv_tiles;
+      sp.Hkv = Hkv;
+      sp.G = Hq / Hkv;
+      sp.n_sm = kDecodeWaveCtas;
+      sp.max_parts = sws.max_parts;
+      p.slices = sp.slices;
+      p.list_head = sp.head;
+      p.parts = sws.max_parts > 0 ? reinterpret_cast<float*>(wsb + sws.parts) : nullptr;
+      if (launch_span_plan(sp, st) != cudaSuccess) return FA_ERR_CUDA;
+    } else {
+      p.plan = pre.plan;
+    }
   }
-  if ((mod ? launch_bwd_pre_span(pre, st) : launch_bwd_pre(pre, st)) != cudaSuccess)
+  if ((mod ? launch_bwd_pre_span(pre, sws.planned, st) : launch_bwd_pre(pre, st)) != cudaSuccess)
     return FA_ERR_CUDA;
 
   if (dtype == FA_F32) {
@@ -440,20 +479,25 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* out, const
   p.n_q_tiles = (Sq + kTileM - 1) / kTileM;
   p.trace = FA_TRACE_PTR;
   p.status = status;
-  if (mod) {
-    p.mod = make_mod(*mod, Sq, Skv, scale);
-    p.spans = pre.spans;
-    p.plan = pre.plan;
-  }
+  if (mod) p.mod = make_mod(*mod, Sq, Skv, scale);
   if ((mod ? launch_bwd_span(p, d, bf16, st) : launch_bwd_tc(p, d, bf16, st)) != cudaSuccess)
     return FA_ERR_CUDA;
 
-  DqConvertParams cv;
+  DqConvertParams cv{};
   cv.dq_acc = dq_acc;
   cv.dq = dq;
   cv.BH = BH; cv.Sq = Sq; cv.Sq_pad = Sq_pad; cv.d = d;
   cv.scale = scale;
   cv.dtype = dtype;
+  if (mod && p.parts) {
+    cv.n_part_blocks = 4 * (sws.max_parts / 2);   // a cut tile of one head has two parts at least
+    cv.list_head = p.list_head;
+    cv.splits = reinterpret_cast<const int4*>(wsb + sws.splits);
+    cv.parts = p.parts;
+    cv.dk = dk;
+    cv.dv = dv;
+    cv.Hkv = Hkv; cv.Skv = Skv; cv.n_kv_tiles = p.n_kv_tiles;
+  }
   return launch_dq_convert(cv, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -777,7 +821,7 @@ int fa_fwd_span(const void* q, const void* k, const void* v, const int* key_begi
 
 size_t fa_bwd_span_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Skv, int d) {
   if (check_common(B, Hq, Hkv, Sq, Skv, d, 0, 1.f, FA_BF16) != FA_OK) return 0;
-  return span_ws(ws_layout(B, Hq, Sq, d), B, Sq, Skv).total;
+  return span_ws(ws_layout(B, Hq, Sq, d), B, Hq, Hkv, Sq, Skv, d).total;
 }
 
 int fa_bwd_span(const void* q, const void* k, const void* v, const int* key_begin,

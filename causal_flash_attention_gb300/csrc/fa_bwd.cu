@@ -49,10 +49,11 @@
 // S^T(i+1) is issued once the compute warps have read S^T(i), dP^T(i+1)
 // right after dQ(i), and the warps read dQ(i) out after P^T(i+1).
 //
-// Span form (kSpan): query row i sees the keys of its own span. Extra blocks of
-// the pre-pass clamp and pad the spans and find, for every key tile, the first
-// and last query tile with a row whose span reaches into it; an item walks that
-// range. The mask of a warp's 32 key rows against its 64 query columns is formed
+// Span form (kSpan): query row i sees the keys of its own span. The plan kernel
+// (fa_span_plan.cu), or for many key tiles extra blocks of the pre-pass, clamps and
+// pads the spans and finds, for every key tile, the first and last query tile
+// with a row whose span reaches into it; an item walks that range, or with a work
+// list a slice of it. The mask of a warp's 32 key rows against its 64 query columns is formed
 // as one word per column and transposed across the warp, so that each key row
 // holds its own 64 bits; tiles that every span covers skip it. With a cap, dS =
 // P (1 - tanh^2) (dP - D): the product P (1 - tanh^2) is kept, rounded to 16
@@ -232,18 +233,66 @@ __global__ void __launch_bounds__(256, 8) bwd_pre_kernel(const BwdPreParams p) {
     }
   }
   if (p.work && block == 0 && threadIdx.x == 0) *p.work = 0;
+  // span form behind the plan kernel: this grid's completion, which the main
+  // kernel waits for, stands for the plan's too
+  if constexpr (kSpan) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // -------------------------------------------------------------- convert --
-// dq = scale * dq_acc (rows < Sq), 8 elements per thread.
+// dk = scale * sum, dv = sum over the parts of a cut tile, in slice order: four
+// blocks a (tile, key/value head), 32 key rows each, one row a lane and 8 columns
+// of dk or dv a warp at a time.
 template <bool kBf16>
+__device__ __forceinline__ void add_parts(const DqConvertParams& p) {
+  const int pair = blockIdx.x / 4;
+  if (pair >= p.list_head[1] * p.Hkv) return;
+  const int4 s = p.splits[pair / p.Hkv];
+  const int g = pair % p.Hkv;
+  const int b = s.x / p.n_kv_tiles, j = s.x % p.n_kv_tiles;
+  const int row = (blockIdx.x & 3) * 32 + (threadIdx.x & 31);
+  const int key = j * kTileN + row;
+  if (key >= p.Skv) return;
+  const size_t stride = static_cast<size_t>(p.Hkv) * 2 * kTileN * p.d;   // between a head's parts
+  for (int c = (threadIdx.x >> 5) * 8; c < 2 * p.d; c += 64) {
+    const float* src = p.parts + (static_cast<size_t>(s.y) * p.Hkv + g) * 2 * kTileN * p.d +
+                       static_cast<size_t>(c) * kTileN + row;   // dV's columns follow dK's
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = src[e * kTileN];
+    for (int k = 1; k < s.z; ++k) {
+      src += stride;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += src[e * kTileN];
+    }
+    const bool is_dk = c < p.d;
+    const float f = is_dk ? p.scale : 1.f;
+    uint4 w;
+    w.x = pack2<kBf16>(acc[0] * f, acc[1] * f);
+    w.y = pack2<kBf16>(acc[2] * f, acc[3] * f);
+    w.z = pack2<kBf16>(acc[4] * f, acc[5] * f);
+    w.w = pack2<kBf16>(acc[6] * f, acc[7] * f);
+    const size_t at = ((static_cast<size_t>(b) * p.Hkv + g) * p.Skv + key) * p.d + (is_dk ? c : c - p.d);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_dk ? p.dk : p.dv) + at) = w;
+  }
+}
+
+// dq = scale * dq_acc (rows < Sq), 8 elements per thread.
+template <bool kBf16, bool kParts>
 __global__ void __launch_bounds__(256, 8) dq_convert_kernel(const DqConvertParams p) {
   // launched as the main kernel's programmatic dependent: wait for that grid
   // (and the pre-pass before it) to complete and its writes to be visible
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (kParts) {
+    if (static_cast<int>(blockIdx.x) < p.n_part_blocks) {
+      add_parts<kBf16>(p);
+      return;
+    }
+  }
+  const unsigned block = blockIdx.x - (kParts ? p.n_part_blocks : 0);
+  const unsigned n_blocks = gridDim.x - (kParts ? p.n_part_blocks : 0);
   const long long n8 = static_cast<long long>(p.BH) * p.Sq * p.d / 8;
-  for (long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; t < n8;
-       t += static_cast<long long>(gridDim.x) * blockDim.x) {
+  for (long long t = static_cast<long long>(block) * blockDim.x + threadIdx.x; t < n8;
+       t += static_cast<long long>(n_blocks) * blockDim.x) {
     const long long e = t * 8;
     const long long rowd = e / p.d;                      // bh * Sq + i
     const int col = static_cast<int>(e % p.d);
@@ -267,11 +316,28 @@ __global__ void __launch_bounds__(256, 8) dq_convert_kernel(const DqConvertParam
 struct BwdItem {
   int j, bkv, b, g;
   int i_start, n_i, n_iter;
+  int step0, part;   // span form: first step, and the partial result it leaves (-1: none)
 };
 
 template <bool kSpan>
 __device__ __forceinline__ BwdItem bwd_item(const BwdParams& p, int w) {
   BwdItem it;
+  it.step0 = 0;
+  it.part = -1;
+  if (kSpan && p.slices) {
+    const int4* e = reinterpret_cast<const int4*>(p.slices + w / p.Hkv);
+    const int4 x = e[0], y = e[1];
+    it.g = w % p.Hkv;
+    it.b = x.x / p.n_kv_tiles;
+    it.j = x.x % p.n_kv_tiles;
+    it.bkv = it.b * p.Hkv + it.g;
+    it.step0 = x.y;
+    it.n_iter = x.z;
+    it.part = x.w < 0 ? -1 : x.w * p.Hkv + it.g;
+    it.i_start = y.x;
+    it.n_i = y.y;
+    return it;
+  }
   const int BHkv = p.B * p.Hkv;
   it.j = w / BHkv;
   it.bkv = w % BHkv;
@@ -335,7 +401,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   const int warp = static_cast<int>(warp_id());
   const int lane = static_cast<int>(lane_id());
-  const int n_items = p.n_kv_tiles * p.B * p.Hkv;
   if (threadIdx.x == 0) {
     trace_span(p.trace, 0, clock64());
     trace_span(p.trace, 1, smid());
@@ -378,6 +443,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // alongside it; the D, L, zeroed dQ rows and the zeroed item counter it
   // writes are read below
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n_items =
+      (kSpan && p.slices) ? p.list_head[0] * p.Hkv : p.n_kv_tiles * p.B * p.Hkv;
 
   // Steps (one query tile of one query head against the item's key tile) are
   // counted across the CTA's items, so every ring slot and barrier phase
@@ -402,8 +469,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       bool ok = true;
       // one step's Q (with its L, D rows) and dO
       auto load_step = [&](const BwdItem& I, int s) -> bool {
-        const int bh = I.b * p.Hq + I.g * (p.Hq / p.Hkv) + s / I.n_i;
-        const int i = I.i_start + s % I.n_i;
+        const int bh = I.b * p.Hq + I.g * (p.Hq / p.Hkv) + (I.step0 + s) / I.n_i;
+        const int i = I.i_start + (I.step0 + s) % I.n_i;
         const int sq = nq % NQ;
         if (nq >= NQ &&
             !mbar_wait(q_empty(sq), static_cast<uint32_t>(nq / NQ - 1) & 1, abort_flag, p.status))
@@ -726,7 +793,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int it = 0; it < I.n_iter; ++it, ++g) {
         const int st = g % NQ;
         const uint32_t par = static_cast<uint32_t>(g / NQ) & 1;
-        const int i = I.i_start + it % I.n_i;
+        const int i = I.i_start + (I.step0 + it) % I.n_i;
         const int q0 = i * kTileM + c0;
         // kSpan: the spans of query columns 2 l and 2 l + 1 of this warp's half
         int4 sp = make_int4(0, 0, 0, 0);
@@ -767,7 +834,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           const bool cap = p.mod.cap_in != 0.f;
           const float inv_cap = cap ? 1.f / p.mod.cap_log2 : 0.f;
           const float bias =
-              p.mod.slopes ? p.mod.slopes[I.g * (p.Hq / p.Hkv) + it / I.n_i] * kLog2eF : 0.f;
+              p.mod.slopes ? p.mod.slopes[I.g * (p.Hq / p.Hkv) + (I.step0 + it) / I.n_i] * kLog2eF : 0.f;
           const float d0 = static_cast<float>(q0 + p.mod.pos_offset - kv);
           // Two halves of 32 columns, for the registers. Packed P^T goes over score
           // columns this warp has read itself, or into the P^T buffer at d = 64: the
@@ -948,7 +1015,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           tr(34);
         }
 
-        const int bh = I.b * p.Hq + I.g * (p.Hq / p.Hkv) + it / I.n_i;
+        const int bh = I.b * p.Hq + I.g * (p.Hq / p.Hkv) + (I.step0 + it) / I.n_i;
         if (!Cfg::kSepQ || it + 1 == I.n_iter) {   // else after the next step's P^T
           if (!(ok = read_dq(g, i, bh))) break;
         }
@@ -969,7 +1036,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!ok) break;
       tr(93);
       tc_fence_after();
-      {
+      if (kSpan && I.part >= 0) {
+        // a slice of a cut item: its sums as fp32 columns of 128 rows (a warp's 32
+        // rows of a column are one 128-byte line), for the convert kernel to add up
+        float* dst = p.parts + (static_cast<size_t>(I.part) * 2 + half) * (kTileN * D) + r;
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lane_off + half * 128 + cc * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) dst[(cc * 32 + e) * kTileN] = __uint_as_float(o[e]);
+        }
+      } else {
         const float f = half == 0 ? p.scale : 1.f;
         const uint32_t box0 = sbase + Cfg::kOffDS + half * (kTileN * 128) + quarter * 32 * 128;
         if (lane == 0) bulk_wait_read_all();   // the dQ box's last reduce has read it
@@ -1052,7 +1131,8 @@ cudaError_t launch_bwd_impl(const BwdParams& p, cudaStream_t stream) {
   e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const long long n_items = static_cast<long long>(p.n_kv_tiles) * p.B * p.Hkv;
+  long long n_items = static_cast<long long>(p.n_kv_tiles) * p.B * p.Hkv;
+  if (kSpan && p.parts) n_items = std::max<long long>(n_items, kMaxParts);   // before cuts
   const unsigned grid = static_cast<unsigned>(std::min<long long>(n_items, std::max(n_sm, 1)));
   e = launch_dependent(kernel, dim3(grid), dim3(kBwdThreads), smem, stream, p);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -1077,12 +1157,15 @@ cudaError_t launch_bwd_pre(const BwdPreParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_bwd_pre_span(const BwdPreParams& p0, cudaStream_t stream) {
+cudaError_t launch_bwd_pre_span(const BwdPreParams& p0, bool after_plan, cudaStream_t stream) {
   BwdPreParams p = p0;
+  auto kernel = p.dtype == 1 ? bwd_pre_kernel<__half, true> : bwd_pre_kernel<__nv_bfloat16, true>;
+  if (after_plan) {
+    p.n_plan_blocks = 0;
+    return launch_dependent(kernel, dim3(pre_row_blocks(p)), dim3(256), 0, stream, p);
+  }
   p.n_plan_blocks = p.B * ((p.n_kv_tiles + kPlanTiles - 1) / kPlanTiles);
-  const unsigned grid = pre_row_blocks(p) + static_cast<unsigned>(p.n_plan_blocks);
-  if (p.dtype == 1) bwd_pre_kernel<__half, true><<<grid, 256, 0, stream>>>(p);
-  else bwd_pre_kernel<__nv_bfloat16, true><<<grid, 256, 0, stream>>>(p);
+  kernel<<<pre_row_blocks(p) + static_cast<unsigned>(p.n_plan_blocks), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -1108,9 +1191,11 @@ cudaError_t launch_bwd_tc(const BwdParams& p, int d, bool bf16, cudaStream_t str
 cudaError_t launch_dq_convert(const DqConvertParams& p, cudaStream_t stream) {
   const long long n8 = static_cast<long long>(p.BH) * p.Sq * p.d / 8;
   const unsigned grid = static_cast<unsigned>(std::min<long long>((n8 + 255) / 256, 152LL * 16));
-  const cudaError_t e =
-      p.dtype == 2 ? launch_dependent(dq_convert_kernel<true>, dim3(grid), dim3(256), 0, stream, p)
-                   : launch_dependent(dq_convert_kernel<false>, dim3(grid), dim3(256), 0, stream, p);
+  auto kernel = p.n_part_blocks > 0
+                    ? (p.dtype == 2 ? dq_convert_kernel<true, true> : dq_convert_kernel<false, true>)
+                    : (p.dtype == 2 ? dq_convert_kernel<true, false> : dq_convert_kernel<false, false>);
+  const cudaError_t e = launch_dependent(kernel, dim3(grid + static_cast<unsigned>(p.n_part_blocks)),
+                                         dim3(256), 0, stream, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -119,14 +119,51 @@ def test_steep_distance_bias_far_from_the_row(fa):
 
 
 def test_causal_spans_agree_with_the_causal_call(fa):
-    x = [t.to(DEV) for t in inputs(1, 4, 2, 700, 700, 128, "bf16", 8)]
-    begin, end = fa.key_spans(1, 700, device=DEV)
-    out, lse = fa.attention_span_forward(*x[:3], begin, end)
-    out2, lse2 = fa.attention_forward(*x[:3])
-    g = fa.attention_span_backward(*x[:3], out, x[3], lse, begin, end)
-    g2 = fa.attention_backward(*x[:3], out2, x[3], lse2)
-    assert torch.equal(out, out2) and torch.equal(lse, lse2)
-    assert torch.equal(g[1], g2[1]) and torch.equal(g[2], g2[2])
+    """Forward bit for bit; the gradients of few key tiles are summed in slices, so they are held
+    to their bounds, and of many (no slices) dk and dv agree bit for bit too."""
+    for Hkv, S in ((2, 700), (12, 3300)):
+        x = inputs(1, 2 * Hkv, Hkv, S, S, 128, "bf16", 8)
+        dev = [t.to(DEV) for t in x]
+        begin, end = fa.key_spans(1, S)
+        lo, hi = begin.to(DEV), end.to(DEV)
+        out, lse = fa.attention_span_forward(*dev[:3], lo, hi)
+        out2, lse2 = fa.attention_forward(*dev[:3])
+        g = fa.attention_span_backward(*dev[:3], out, dev[3], lse, lo, hi)
+        g2 = fa.attention_backward(*dev[:3], out2, dev[3], lse2)
+        torch.cuda.synchronize()
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+        if Hkv == 2:
+            compare(dict(zip(("dq", "dk", "dv"), g)), *x, begin, end)
+        else:
+            assert torch.equal(g[1], g2[1]) and torch.equal(g[2], g2[2])
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,Sq,Skv,mask", [
+    (1, 8, 1, 1000, 1000, dict()),                       # 8 tiles of 8 to 64 steps: many slices
+    (3, 4, 2, 900, 900, dict(kv_lens=[900, 130, 517])),  # uneven sequences
+    (2, 6, 2, 300, 700, dict(window=90)),                # key tiles that nothing sees
+    (1, 16, 2, 130, 2000, dict(causal=False)),
+])
+@pytest.mark.parametrize("d", [64, 128])
+def test_items_cut_into_slices(fa, B, Hq, Hkv, Sq, Skv, mask, d):
+    """Few key tiles with many steps each: their dk and dv are joined from slices, and repeat."""
+    x = inputs(B, Hq, Hkv, Sq, Skv, d, "fp16", Sq)
+    begin, end = fa.key_spans(B, Sq, Skv, **mask)
+    got = run(fa, *x, begin, end)
+    compare(got, *x, begin, end)
+    again = run(fa, *x, begin, end)
+    assert torch.equal(got["dk"], again["dk"]) and torch.equal(got["dv"], again["dv"])
+
+
+def test_more_key_tiles_than_the_work_list_holds(fa):
+    """Above 1024 key tiles over the batch the ranges come from the pre-pass: one row over many
+    keys, and a batch of many short sequences."""
+    x = inputs(1, 1, 1, 3, 131300, 64, "bf16", 3)
+    begin, end = fa.key_spans(1, 3, 131300, window=200)
+    compare(run(fa, *x, begin, end), *x, begin, end)
+    x = inputs(1100, 1, 1, 20, 20, 64, "fp16", 4)
+    begin, end = random_spans(1100, 20, 20, 5)
+    compare(run(fa, *x, begin, end), *x, begin, end)
 
 
 def test_same_bits_again_and_captured_with_changed_spans(fa):
