@@ -29,8 +29,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_pair.cu", "fa_bwd.cu", "fa_simt.cu", "fa_noalloc.cu",
-           "fa_decode.cu", "fa_ragged.cu", "fa_heads.cu", "fa_span_plan.cu"]
-HEADERS = ["ptx.cuh", "score_mod.cuh", "fa_internal.h", "fa_decode.h", "fa_ragged.h", "fa_heads.h",
+           "fa_decode.cu", "fa_ragged.cu", "fa_heads.cu"]
+HEADERS = ["ptx.cuh", "score_mod.cuh", "span_plan.cuh", "fa_internal.h", "fa_decode.h", "fa_ragged.h", "fa_heads.h",
            os.path.join("..", "..", "include", "fa.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -302,33 +302,26 @@ ScoreMod make_mod(const SpanArgs& m, int Sq, int Skv, float scale) {
   return r;
 }
 
-// Extra workspace of the span backward behind ws_layout's: the padded spans, and
-// the work list with the partial results of cut tiles (planned) or each key
-// tile's query-tile range.
+// Extra workspace of the span backward behind ws_layout's: the padded spans, each
+// key tile's query-tile range and, where items may be cut (there is a work list,
+// and fewer than two items an SM), the cut tiles and their partial results.
 struct SpanWs {
-  size_t spans, plan, slices, splits, parts, total;
-  bool planned;
+  size_t spans, plan, splits, parts, total;
   int max_parts;
 };
 
 SpanWs span_ws(const WsLayout& w, int B, int Hq, int Hkv, int Sq, int Skv, int d) {
   SpanWs s{};
   const long long tiles = (Skv + kTileN - 1LL) / kTileN * B, rows = round_up(Sq, kTileM) * B;
-  s.planned = tiles <= kPlanMax && rows <= kPlanRows;
-  s.spans = w.total;
-  s.plan = s.spans + static_cast<size_t>(round_up(rows * 8, 256));
-  if (!s.planned) {
-    s.total = s.plan + static_cast<size_t>(round_up(tiles * 8, 256));
-    return s;
-  }
-  // cut only where there are fewer than two items an SM
   const long long items = tiles * Hkv;
   const long long steps = static_cast<long long>(Hq / Hkv) * (rows / B / kTileM);   // of an item, at most
-  s.max_parts = items >= kMaxParts ? 0 : static_cast<int>(std::min<long long>(kMaxParts, items * steps));
-  s.slices = s.plan + 256;   // behind the list's head
-  s.splits = s.slices + static_cast<size_t>(
-                            round_up(std::max<long long>(tiles, s.max_parts) * sizeof(SpanSlice), 256));
-  s.parts = s.splits + static_cast<size_t>(round_up(s.max_parts * 16LL, 256));
+  if (tiles <= kListTiles && items < kMaxParts)
+    s.max_parts = static_cast<int>(std::min<long long>(kMaxParts, items * steps));
+  s.spans = w.total;
+  s.plan = s.spans + static_cast<size_t>(round_up(rows * 8, 256));
+  s.splits = s.plan + static_cast<size_t>(round_up(tiles * 8, 256));
+  // the number of cut tiles, then they
+  s.parts = s.splits + (s.max_parts > 0 ? static_cast<size_t>(round_up(16 + s.max_parts * 16LL, 256)) : 0);
   s.total = s.parts + static_cast<size_t>(s.max_parts) * 2 * kTileN * d * 4;
   return s;
 }
@@ -418,32 +411,20 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* out, const
     pre.n_kv_tiles = (Skv + kTileN - 1) / kTileN;
     pre.key_begin = mod->key_begin;
     pre.key_end = mod->key_end;
-    pre.spans = reinterpret_cast<int2*>(wsb + sws.spans);
-    pre.plan = reinterpret_cast<int2*>(wsb + sws.plan);
-    p.spans = pre.spans;
-    if (sws.planned) {
-      SpanPlanParams sp{};
-      sp.key_begin = mod->key_begin;
-      sp.key_end = mod->key_end;
-      sp.spans = pre.spans;
-      sp.head = reinterpret_cast<int*>(wsb + sws.plan);
-      sp.slices = reinterpret_cast<SpanSlice*>(wsb + sws.slices);
-      sp.splits = reinterpret_cast<int4*>(wsb + sws.splits);
-      sp.B = B; sp.Sq = Sq; sp.Sq_pad = Sq_pad; sp.Skv = Skv;
-      sp.n_kv_tiles = pre.n_kv_tiles;
-      sp.Hkv = Hkv;
-      sp.G = Hq / Hkv;
-      sp.n_sm = kDecodeWaveCtas;
-      sp.max_parts = sws.max_parts;
-      p.slices = sp.slices;
-      p.list_head = sp.head;
-      p.parts = sws.max_parts > 0 ? reinterpret_cast<float*>(wsb + sws.parts) : nullptr;
-      if (launch_span_plan(sp, st) != cudaSuccess) return FA_ERR_CUDA;
-    } else {
-      p.plan = pre.plan;
+    p.spans = pre.spans = reinterpret_cast<int2*>(wsb + sws.spans);
+    p.plan = pre.plan = reinterpret_cast<int2*>(wsb + sws.plan);
+    // a list for up to four items an SM: 512 items of documents take 298 us with it
+    // and 326 without, 768 short items of a window 66.4 and 63.0
+    const long long tiles = static_cast<long long>(B) * pre.n_kv_tiles;
+    p.listed = tiles <= kListTiles && tiles * Hkv <= 4 * kDecodeWaveCtas;
+    p.n_slots = kDecodeWaveCtas;
+    if (sws.max_parts > 0) {
+      p.n_splits = reinterpret_cast<int*>(wsb + sws.splits);
+      p.splits = reinterpret_cast<int4*>(wsb + sws.splits + 16);
+      p.parts = reinterpret_cast<float*>(wsb + sws.parts);
     }
   }
-  if ((mod ? launch_bwd_pre_span(pre, sws.planned, st) : launch_bwd_pre(pre, st)) != cudaSuccess)
+  if ((mod ? launch_bwd_pre_span(pre, st) : launch_bwd_pre(pre, st)) != cudaSuccess)
     return FA_ERR_CUDA;
 
   if (dtype == FA_F32) {
@@ -491,8 +472,8 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* out, const
   cv.dtype = dtype;
   if (mod && p.parts) {
     cv.n_part_blocks = 4 * (sws.max_parts / 2);   // a cut tile of one head has two parts at least
-    cv.list_head = p.list_head;
-    cv.splits = reinterpret_cast<const int4*>(wsb + sws.splits);
+    cv.n_splits = p.n_splits;
+    cv.splits = p.splits;
     cv.parts = p.parts;
     cv.dk = dk;
     cv.dv = dv;

@@ -49,11 +49,10 @@
 // S^T(i+1) is issued once the compute warps have read S^T(i), dP^T(i+1)
 // right after dQ(i), and the warps read dQ(i) out after P^T(i+1).
 //
-// Span form (kSpan): query row i sees the keys of its own span. The plan kernel
-// (fa_span_plan.cu), or for many key tiles extra blocks of the pre-pass, clamps and
-// pads the spans and finds, for every key tile, the first and last query tile
-// with a row whose span reaches into it; an item walks that range, or with a work
-// list a slice of it. The mask of a warp's 32 key rows against its 64 query columns is formed
+// Span form (kSpan): query row i sees the keys of its own span. Extra blocks of
+// the pre-pass clamp and pad the spans and find, for every key tile, the first
+// and last query tile with a row whose span reaches into it; an item walks that
+// range, or with a work list (span_plan.cuh) a slice of it. The mask of a warp's 32 key rows against its 64 query columns is formed
 // as one word per column and transposed across the warp, so that each key row
 // holds its own 64 bits; tiles that every span covers skip it. With a cap, dS =
 // P (1 - tanh^2) (dP - D): the product P (1 - tanh^2) is kept, rounded to 16
@@ -65,6 +64,7 @@
 #include "fa_internal.h"
 #include "ptx.cuh"
 #include "score_mod.cuh"
+#include "span_plan.cuh"
 
 namespace fa {
 namespace {
@@ -102,7 +102,14 @@ struct BwdCfg {
   // dp_full, p_full, ds_full, dv_done, dq_full, dq_empty, ds_empty, kd_done, drain
   static constexpr int kNumBars = 2 + 2 * kQStages + 2 * kDoStages + 10 + (kSepQ ? 1 : 0);
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  // behind the tensor-memory address, the abort flag and the item index: the item
+  // as the producer decoded it (span form)
+  static constexpr int kOffItem = kOffMisc + 16;
   static constexpr int kSmemBytes = kOffMisc + 16;
+  static constexpr int kOffList = kOffItem + 48;            // work list (span_plan.cuh)
+  static constexpr int kListEntries = kMaxParts > kListTiles ? kMaxParts : kListTiles;
+  static constexpr int kSmemBytesSpan = kOffList + kListEntries * 2;
+  static_assert(kSmemBytesSpan <= 232448, "shared memory of one CTA");
 };
 
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, int* status) {
@@ -233,9 +240,6 @@ __global__ void __launch_bounds__(256, 8) bwd_pre_kernel(const BwdPreParams p) {
     }
   }
   if (p.work && block == 0 && threadIdx.x == 0) *p.work = 0;
-  // span form behind the plan kernel: this grid's completion, which the main
-  // kernel waits for, stands for the plan's too
-  if constexpr (kSpan) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // -------------------------------------------------------------- convert --
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(256, 8) bwd_pre_kernel(const BwdPreParams p) {
 template <bool kBf16>
 __device__ __forceinline__ void add_parts(const DqConvertParams& p) {
   const int pair = blockIdx.x / 4;
-  if (pair >= p.list_head[1] * p.Hkv) return;
+  if (pair >= *p.n_splits * p.Hkv) return;
   const int4 s = p.splits[pair / p.Hkv];
   const int g = pair % p.Hkv;
   const int b = s.x / p.n_kv_tiles, j = s.x % p.n_kv_tiles;
@@ -322,27 +326,13 @@ struct BwdItem {
 template <bool kSpan>
 __device__ __forceinline__ BwdItem bwd_item(const BwdParams& p, int w) {
   BwdItem it;
-  it.step0 = 0;
-  it.part = -1;
-  if (kSpan && p.slices) {
-    const int4* e = reinterpret_cast<const int4*>(p.slices + w / p.Hkv);
-    const int4 x = e[0], y = e[1];
-    it.g = w % p.Hkv;
-    it.b = x.x / p.n_kv_tiles;
-    it.j = x.x % p.n_kv_tiles;
-    it.bkv = it.b * p.Hkv + it.g;
-    it.step0 = x.y;
-    it.n_iter = x.z;
-    it.part = x.w < 0 ? -1 : x.w * p.Hkv + it.g;
-    it.i_start = y.x;
-    it.n_i = y.y;
-    return it;
-  }
   const int BHkv = p.B * p.Hkv;
   it.j = w / BHkv;
   it.bkv = w % BHkv;
   it.b = it.bkv / p.Hkv;
   it.g = it.bkv % p.Hkv;
+  it.step0 = 0;
+  it.part = -1;
   // causal: the first query tile holding a row at position >= this tile's
   // first key (query row i stands at position i + kv_offset)
   if constexpr (kSpan) {
@@ -354,6 +344,28 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdParams& p, int w) {
     it.n_i = p.n_q_tiles - it.i_start;
   }
   it.n_iter = (p.Hq / p.Hkv) * it.n_i;
+  return it;
+}
+
+// Item w of a work list: entry w / Hkv, key/value head w % Hkv.
+__device__ __forceinline__ BwdItem bwd_listed_item(const BwdParams& p, int limit,
+                                                   const uint16_t* entries, int w) {
+  BwdItem it;
+  const int e = w / p.Hkv;
+  it.g = w - e * p.Hkv;
+  const int tile = entries[e] & 127, slice = entries[e] >> 7;
+  it.b = tile / p.n_kv_tiles;
+  it.j = tile - it.b * p.n_kv_tiles;
+  it.bkv = it.b * p.Hkv + it.g;
+  const int2 r = p.plan[tile];
+  it.i_start = r.x;
+  it.n_i = r.y;
+  const int steps = (p.Hq / p.Hkv) * it.n_i;
+  int slices, len;
+  span_cut(steps, limit, slices, len);
+  it.step0 = slice * len;
+  it.n_iter = min(len, steps - it.step0);
+  it.part = slices > 1 ? e * p.Hkv + it.g : -1;
   return it;
 }
 
@@ -379,6 +391,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
   // the work item whose K_j, V_j the current kv_full phase delivers
   volatile int* item_slot = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 8);
+
+  // span form: the item that goes with item_slot; the others read it here, not from
+  // the lists in global memory, whose latency would stand at the start of each item
+  BwdItem* item_info = reinterpret_cast<BwdItem*>(smem + Cfg::kOffItem);
+  static_assert(sizeof(BwdItem) <= 44, "its place in shared memory, before the list's limit");
 
   const uint32_t bar0 = sbase + Cfg::kOffBar;
   const uint32_t kv_full = bar0;
@@ -443,8 +460,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // alongside it; the D, L, zeroed dQ rows and the zeroed item counter it
   // writes are read below
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n_items =
-      (kSpan && p.slices) ? p.list_head[0] * p.Hkv : p.n_kv_tiles * p.B * p.Hkv;
+  int n_items = p.n_kv_tiles * p.B * p.Hkv;
+  uint16_t* entries = reinterpret_cast<uint16_t*>(smem + Cfg::kOffList);
+  int* list_limit = reinterpret_cast<int*>(smem + Cfg::kOffItem + 44);
+  if constexpr (kSpan) {
+    if (p.listed) {
+      // scratch: the K tile's place, which the first load takes after the barrier
+      n_items = p.Hkv * span_list(p, *reinterpret_cast<SpanScratch*>(smem + Cfg::kOffK), entries,
+                                  list_limit, kBwdThreads);
+      fence_proxy_async_smem();
+      __syncthreads();
+    }
+  }
+  auto item_of = [&](int w) {   // the producer's
+    if (kSpan && p.listed) return bwd_listed_item(p, *list_limit, entries, w);
+    return bwd_item<kSpan != 0>(p, w);
+  };
 
   // Steps (one query tile of one query head against the item's key tile) are
   // counted across the CTA's items, so every ring slot and barrier phase
@@ -502,7 +533,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int k = 0; ok; ++k) {
         BwdItem I{};
         if (w < n_items) {
-          I = bwd_item<kSpan != 0>(p, w);
+          I = item_of(w);
           if (!(ok = load_step(I, 0))) break;
         }
         if (k > 0) {
@@ -511,6 +542,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         tr(95);
         *item_slot = w;
+        if constexpr (kSpan) *item_info = I;
         if (w >= n_items) {
           mbar_arrive(kv_full);
           break;
@@ -527,7 +559,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!ok) break;
         w = atomicAdd(p.work, 1);
         if (w < n_items) {   // the next item's K_j, V_j into L2 while this item runs
-          const BwdItem J = bwd_item<kSpan != 0>(p, w);
+          const BwdItem J = item_of(w);
           for (int c = 0; c < Cfg::kChunks; ++c) {
             tma_prefetch_l2_3d(&p.tm_k, c * kChunk, J.j * kTileN, J.bkv);
             tma_prefetch_l2_3d(&p.tm_v, c * kChunk, J.j * kTileN, J.bkv);
@@ -627,7 +659,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (k == 0 && !(ok = mbar_wait(drain, 0, abort_flag, p.status))) break;
 #endif
         tr(9);
-        const int N = bwd_item<kSpan != 0>(p, w).n_iter;
+        const int N = kSpan ? item_info->n_iter : bwd_item<false>(p, w).n_iter;
         if (!(ok = issue_s(g) && issue_dp(g))) break;
         for (int n = 0; n < N; ++n, ++g) {
           const int st = g % NQ;
@@ -788,7 +820,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!ok) break;
       const int w = *item_slot;
       if (w >= n_items) break;
-      const BwdItem I = bwd_item<kSpan != 0>(p, w);
+      BwdItem I;
+      if constexpr (kSpan) I = *item_info;
+      else I = bwd_item<false>(p, w);
       const int kv = I.j * kTileN + r;
       for (int it = 0; it < I.n_iter; ++it, ++g) {
         const int st = g % NQ;
@@ -1121,7 +1155,7 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 block, siz
 
 template <int D, bool kBf16, int kSpan = 0>
 cudaError_t launch_bwd_impl(const BwdParams& p, cudaStream_t stream) {
-  constexpr int smem = BwdCfg<D>::kSmemBytes;
+  constexpr int smem = kSpan ? BwdCfg<D>::kSmemBytesSpan : BwdCfg<D>::kSmemBytes;
   auto kernel = fa_bwd_kernel<D, kBf16, kSpan>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -1157,15 +1191,12 @@ cudaError_t launch_bwd_pre(const BwdPreParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_bwd_pre_span(const BwdPreParams& p0, bool after_plan, cudaStream_t stream) {
+cudaError_t launch_bwd_pre_span(const BwdPreParams& p0, cudaStream_t stream) {
   BwdPreParams p = p0;
-  auto kernel = p.dtype == 1 ? bwd_pre_kernel<__half, true> : bwd_pre_kernel<__nv_bfloat16, true>;
-  if (after_plan) {
-    p.n_plan_blocks = 0;
-    return launch_dependent(kernel, dim3(pre_row_blocks(p)), dim3(256), 0, stream, p);
-  }
   p.n_plan_blocks = p.B * ((p.n_kv_tiles + kPlanTiles - 1) / kPlanTiles);
-  kernel<<<pre_row_blocks(p) + static_cast<unsigned>(p.n_plan_blocks), 256, 0, stream>>>(p);
+  const unsigned grid = pre_row_blocks(p) + static_cast<unsigned>(p.n_plan_blocks);
+  if (p.dtype == 1) bwd_pre_kernel<__half, true><<<grid, 256, 0, stream>>>(p);
+  else bwd_pre_kernel<__nv_bfloat16, true><<<grid, 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

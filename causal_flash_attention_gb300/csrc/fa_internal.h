@@ -54,30 +54,11 @@ struct FwdParams {
   ScoreMod mod;
 };
 
-// Work list of the span backward (fa_span_plan.cu), for up to kPlanMax key tiles
-// over all batches (and kPlanRows query rows, which one block reads).
-constexpr int kPlanMax = 1024;
-constexpr int kPlanRows = 1 << 17;
-constexpr int kMaxParts = 304;   // partial dK, dV of slices: two rounds over 152 SMs
-
-// Steps [step0, step0 + n_steps) of key tile `tile` (batch * n_kv_tiles + j) of
-// every key/value head g; step s is query tile i_start + s % n_i of query head s /
-// n_i of the group. part: partial result part * Hkv + g, or -1 for all steps.
-struct alignas(16) SpanSlice {
-  int tile, step0, n_steps, part, i_start, n_i, unused0, unused1;
-};
-
-struct SpanPlanParams {
-  const int* key_begin;   // [B][Sq]
-  const int* key_end;     // [B][Sq]
-  int2* spans;            // [B][Sq_pad] clamped (begin, end), empty spans as (0, 0)
-  int* head;              // number of slices, number of cut tiles
-  SpanSlice* slices;      // longest first
-  int4* splits;           // cut tiles: (tile, first part, parts, 0)
-  int B, Sq, Sq_pad, Skv, n_kv_tiles, Hkv, G;
-  int n_sm;
-  int max_parts;          // 0: nothing is cut
-};
+// Work list of the span backward (span_plan.cuh): for up to this many key tiles
+// over the batch, with partial results of so many slices of cut tiles (two rounds
+// over 152 SMs).
+constexpr int kListTiles = 128;
+constexpr int kMaxParts = 304;
 
 struct BwdPreParams {
   const void* out;    // [B*Hq][Sq][d]
@@ -122,10 +103,13 @@ struct BwdParams {
   // span backward only
   ScoreMod mod;
   const int2* spans;  // [B][Sq_pad], written by the pre-pass
-  const int2* plan;   // [B][n_kv_tiles], written by the pre-pass (slices null)
-  const SpanSlice* slices;   // work list, or null: every key tile uncut in index order
-  const int* list_head;      // its length
-  float* parts;       // [part][dK, dV][d][128] fp32, of slices of cut tiles
+  const int2* plan;   // [B][n_kv_tiles], written by the pre-pass
+  int listed;         // B * n_kv_tiles <= kListTiles: items go by a work list
+  int n_slots;        // SMs the list is made for
+  float* parts;       // [entry * Hkv + g][dK, dV][d][128] fp32 of the slices of cut
+                      // tiles, or null: nothing is cut
+  int4* splits;       // cut tiles, for the convert kernel: (tile, first entry, entries, 0)
+  int* n_splits;
 };
 
 struct DqConvertParams {
@@ -134,10 +118,10 @@ struct DqConvertParams {
   int BH, Sq, Sq_pad, d;
   float scale;
   int dtype;
-  // span backward with a work list: n_part_blocks blocks more, which add up the
-  // parts of cut tiles into dk and dv
+  // span backward with cuts: n_part_blocks blocks more, which add up the parts of
+  // cut tiles into dk and dv
   int n_part_blocks;
-  const int* list_head;
+  const int* n_splits;
   const int4* splits;
   const float* parts;
   void* dk;
@@ -169,9 +153,7 @@ cudaError_t launch_fwd_span(const FwdParams& p, int d, bool bf16, cudaStream_t s
 cudaError_t launch_fwd_pair(const FwdParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_bwd_pre(const BwdPreParams& p, cudaStream_t stream);
 cudaError_t launch_bwd_tc(const BwdParams& p, int d, bool bf16, cudaStream_t stream);
-cudaError_t launch_span_plan(const SpanPlanParams& p, cudaStream_t stream);
-// after_plan: launched behind launch_span_plan, as its programmatic dependent
-cudaError_t launch_bwd_pre_span(const BwdPreParams& p, bool after_plan, cudaStream_t stream);
+cudaError_t launch_bwd_pre_span(const BwdPreParams& p, cudaStream_t stream);
 cudaError_t launch_bwd_span(const BwdParams& p, int d, bool bf16, cudaStream_t stream);
 cudaError_t launch_dq_convert(const DqConvertParams& p, cudaStream_t stream);
 cudaError_t launch_fwd_simt(const SimtParams& p, cudaStream_t stream);

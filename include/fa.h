@@ -361,8 +361,9 @@ int fa_fwd_span(const void* q, const void* k, const void* v, const int* key_begi
                 fa_stream_t stream);
 
 /* Workspace bytes of fa_bwd_span: fa_bwd_kv_workspace_bytes, then the padded
- * spans ([B][Sq rounded up to 128] pairs of int32) and the work list, and, where
- * there are fewer than 304 pairs of a key tile and a key/value head, up to 304
+ * spans ([B][Sq rounded up to 128] pairs of int32), the query-tile range of every
+ * key tile ([B][ceil(Skv / 128)] pairs) and, for at most 128 key tiles over the
+ * batch and fewer than 304 pairs of a key tile and a key/value head, up to 304
  * partial results of cut tiles (2 * 128 * d floats each); each region 256-byte
  * aligned. Returns 0 for invalid sizes. */
 size_t fa_bwd_span_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Skv, int d);

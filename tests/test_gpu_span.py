@@ -156,7 +156,7 @@ def test_items_cut_into_slices(fa, B, Hq, Hkv, Sq, Skv, mask, d):
 
 
 def test_more_key_tiles_than_the_work_list_holds(fa):
-    """Above 1024 key tiles over the batch the ranges come from the pre-pass: one row over many
+    """Above 128 key tiles over the batch items go in index order, uncut: a few rows over many
     keys, and a batch of many short sequences."""
     x = inputs(1, 1, 1, 3, 131300, 64, "bf16", 3)
     begin, end = fa.key_spans(1, 3, 131300, window=200)

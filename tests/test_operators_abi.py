@@ -51,15 +51,13 @@ def test_span_backward_refuses(fa_lib, kw, code):
 def test_span_workspace_formula(fa_lib):
     up = lambda x: -(-x // 256) * 256
     for B, Hq, Hkv, Sq, Skv, d in [(1, 2, 1, 1, 1, 64), (3, 8, 2, 1537, 200, 128),
-                                   (1, 32, 8, 8192, 8192, 128), (2, 2, 1, 64, 100000, 64)]:
+                                   (1, 32, 8, 8192, 8192, 128), (2, 2, 1, 64, 100000, 64),
+                                   (3, 2, 1, 8000, 8000, 64)]:
         tiles, rows = B * -(-Skv // 128), B * -(-Sq // 128) * 128
-        want = fa_lib.fa_bwd_kv_workspace_bytes(B, Hq, Hkv, Sq, Skv, d) + up(rows * 8)
-        if tiles > 1024:                 # a range for every key tile
-            want += up(tiles * 8)
-        else:                            # list head, slices, cut tiles, partial results
-            items, steps = tiles * Hkv, Hq // Hkv * rows // B // 128
-            parts = 0 if items >= 304 else min(304, items * steps)
-            want += 256 + up(max(tiles, parts) * 32) + up(parts * 16) + parts * 2 * 128 * d * 4
+        want = fa_lib.fa_bwd_kv_workspace_bytes(B, Hq, Hkv, Sq, Skv, d) + up(rows * 8) + up(tiles * 8)
+        if tiles <= 128 and tiles * Hkv < 304:     # cut tiles and partial results
+            parts = min(304, tiles * Hkv * (Hq // Hkv) * (rows // B // 128))
+            want += up(16 + parts * 16) + parts * 2 * 128 * d * 4
         assert fa_lib.fa_bwd_span_workspace_bytes(B, Hq, Hkv, Sq, Skv, d) == want
     assert fa_lib.fa_bwd_span_workspace_bytes(1, 3, 2, 9, 9, 64) == 0
 
