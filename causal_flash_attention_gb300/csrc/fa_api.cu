@@ -471,7 +471,7 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* out, const
   cv.scale = scale;
   cv.dtype = dtype;
   if (mod && p.parts) {
-    cv.n_part_blocks = 4 * (sws.max_parts / 2);   // a cut tile of one head has two parts at least
+    cv.max_pairs = sws.max_parts / 2;   // a cut tile of one head has two parts at least
     cv.n_splits = p.n_splits;
     cv.splits = p.splits;
     cv.parts = p.parts;

@@ -243,46 +243,48 @@ __global__ void __launch_bounds__(256, 8) bwd_pre_kernel(const BwdPreParams p) {
 }
 
 // -------------------------------------------------------------- convert --
-// dk = scale * sum, dv = sum over the parts of a cut tile, in slice order: four
-// blocks a (tile, key/value head), 32 key rows each, one row a lane and 8 columns
-// of dk or dv a warp at a time.
+// dk = scale * sum, dv = sum over the parts of a cut tile, in slice order: eight
+// blocks a (tile, key/value head), one for 32 key rows of dk or dv each, one row a
+// lane and 8 columns a warp at a time. A part's columns are lines of 128 rows, so
+// the reads are whole lines; four parts' are in flight.
+constexpr int kPartBlocks = 8;
+
 template <bool kBf16>
 __device__ __forceinline__ void add_parts(const DqConvertParams& p) {
-  const int pair = blockIdx.x / 4;
+  const int pair = blockIdx.x / kPartBlocks, which = blockIdx.x % kPartBlocks;
   if (pair >= *p.n_splits * p.Hkv) return;
   const int4 s = p.splits[pair / p.Hkv];
   const int g = pair % p.Hkv;
   const int b = s.x / p.n_kv_tiles, j = s.x % p.n_kv_tiles;
-  const int row = (blockIdx.x & 3) * 32 + (threadIdx.x & 31);
+  const bool is_dk = which < 4;
+  const int row = (which & 3) * 32 + (threadIdx.x & 31);
   const int key = j * kTileN + row;
   if (key >= p.Skv) return;
-  const size_t stride = static_cast<size_t>(p.Hkv) * 2 * kTileN * p.d;   // between a head's parts
-  for (int c = (threadIdx.x >> 5) * 8; c < 2 * p.d; c += 64) {
-    const float* src = p.parts + (static_cast<size_t>(s.y) * p.Hkv + g) * 2 * kTileN * p.d +
-                       static_cast<size_t>(c) * kTileN + row;   // dV's columns follow dK's
-    float acc[8];
+  const size_t part = static_cast<size_t>(kTileN) * p.d;
+  const size_t stride = static_cast<size_t>(p.Hkv) * 2 * part;   // between a head's parts
+  const float* base = p.parts + (static_cast<size_t>(s.y) * p.Hkv + g) * 2 * part +
+                      (is_dk ? 0 : part) + row;
+  const float f = is_dk ? p.scale : 1.f;
+  for (int c = (threadIdx.x >> 5) * 8; c < p.d; c += 64) {
+    const float* src = base + static_cast<size_t>(c) * kTileN;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < s.z; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = src[e * kTileN];
-    for (int k = 1; k < s.z; ++k) {
-      src += stride;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += src[e * kTileN];
-    }
-    const bool is_dk = c < p.d;
-    const float f = is_dk ? p.scale : 1.f;
+      for (int e = 0; e < 8; ++e) acc[e] += src[k * stride + e * kTileN];
     uint4 w;
     w.x = pack2<kBf16>(acc[0] * f, acc[1] * f);
     w.y = pack2<kBf16>(acc[2] * f, acc[3] * f);
     w.z = pack2<kBf16>(acc[4] * f, acc[5] * f);
     w.w = pack2<kBf16>(acc[6] * f, acc[7] * f);
-    const size_t at = ((static_cast<size_t>(b) * p.Hkv + g) * p.Skv + key) * p.d + (is_dk ? c : c - p.d);
+    const size_t at = ((static_cast<size_t>(b) * p.Hkv + g) * p.Skv + key) * p.d + c;
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_dk ? p.dk : p.dv) + at) = w;
   }
 }
 
 // dq = scale * dq_acc (rows < Sq), 8 elements per thread.
 template <bool kBf16, bool kParts>
-__global__ void __launch_bounds__(256, 8) dq_convert_kernel(const DqConvertParams p) {
+__global__ void __launch_bounds__(256, kParts ? 4 : 8) dq_convert_kernel(const DqConvertParams p) {
   // launched as the main kernel's programmatic dependent: wait for that grid
   // (and the pre-pass before it) to complete and its writes to be visible
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1219,13 +1221,16 @@ cudaError_t launch_bwd_tc(const BwdParams& p, int d, bool bf16, cudaStream_t str
   return bf16 ? launch_bwd_impl<64, true>(p, stream) : launch_bwd_impl<64, false>(p, stream);
 }
 
-cudaError_t launch_dq_convert(const DqConvertParams& p, cudaStream_t stream) {
+cudaError_t launch_dq_convert(const DqConvertParams& p0, cudaStream_t stream) {
+  DqConvertParams p = p0;
+  p.n_part_blocks = kPartBlocks * p.max_pairs;
   const long long n8 = static_cast<long long>(p.BH) * p.Sq * p.d / 8;
   const unsigned grid = static_cast<unsigned>(std::min<long long>((n8 + 255) / 256, 152LL * 16));
+  const unsigned part_blocks = static_cast<unsigned>(p.n_part_blocks);
   auto kernel = p.n_part_blocks > 0
                     ? (p.dtype == 2 ? dq_convert_kernel<true, true> : dq_convert_kernel<false, true>)
                     : (p.dtype == 2 ? dq_convert_kernel<true, false> : dq_convert_kernel<false, false>);
-  const cudaError_t e = launch_dependent(kernel, dim3(grid + static_cast<unsigned>(p.n_part_blocks)),
+  const cudaError_t e = launch_dependent(kernel, dim3(grid + part_blocks),
                                          dim3(256), 0, stream, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

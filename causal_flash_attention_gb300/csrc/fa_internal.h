@@ -118,9 +118,9 @@ struct DqConvertParams {
   int BH, Sq, Sq_pad, d;
   float scale;
   int dtype;
-  // span backward with cuts: n_part_blocks blocks more, which add up the parts of
-  // cut tiles into dk and dv
-  int n_part_blocks;
+  // span backward with cuts: blocks more, which add up the parts of cut tiles into
+  // dk and dv, for up to max_pairs (cut tile, key/value head) pairs (0: no cuts)
+  int max_pairs, n_part_blocks;
   const int* n_splits;
   const int4* splits;
   const float* parts;

@@ -97,7 +97,11 @@ int integer(PyObject* o) {
   if (x != static_cast<int>(x)) throw BadArgument{"an integer argument does not fit into 32 bits"};
   return static_cast<int>(x);
 }
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject* o) {
+  const int x = PyObject_IsTrue(o);
+  if (x < 0) throw BadArgument{""};
+  return x == 1;
+}
 
 int dtype_code(const Tensor& t) {
   switch (t.scalar_type()) {
