@@ -217,6 +217,15 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
     mbar_init(bars.drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    if constexpr (kSpan) {
+      // the queries are on their way while the spans are read
+      mbar_arrive_expect_tx(bars.q_full, Cfg::kTileBytes);
+      for (int c = 0; c < Cfg::kChunks; ++c)
+        tma_load_3d(sbase + Cfg::kOffQ + c * (kTileM * 128), &p.tm_q, bars.q_full, c * kChunk,
+                    unit * kTileM, bh);
+      tma_prefetch_desc(&p.tm_k);
+      tma_prefetch_desc(&p.tm_v);
+    }
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
@@ -238,19 +247,24 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
   if (warp == 0) {
     // ===================== TMA producer =====================
     if (lane == 0) {
-      tma_prefetch_desc(&p.tm_q);
-      tma_prefetch_desc(&p.tm_k);
-      tma_prefetch_desc(&p.tm_v);
-      const uint32_t q_bytes = (n_t[0] > 0 ? Cfg::kTileBytes : 0) + (n_t[1] > 0 ? Cfg::kTileBytes : 0);
-      if (q_bytes) {
-        mbar_arrive_expect_tx(bars.q_full, q_bytes);
-        for (int t = 0; t < T; ++t) {
-          if (n_t[t] == 0) continue;
-          const int q0 = unit * T * kTileM + t * kTileM;
-          for (int c = 0; c < Cfg::kChunks; ++c)
-            tma_load_3d(sbase + Cfg::kOffQ + t * Cfg::kTileBytes + c * (kTileM * 128), &p.tm_q,
-                        bars.q_full, c * kChunk, q0, bh);
+      uint32_t q_bytes = Cfg::kTileBytes;   // kSpan: issued above
+      if constexpr (!kSpan) {
+        tma_prefetch_desc(&p.tm_q);
+        tma_prefetch_desc(&p.tm_k);
+        tma_prefetch_desc(&p.tm_v);
+        q_bytes = (n_t[0] > 0 ? Cfg::kTileBytes : 0) + (n_t[1] > 0 ? Cfg::kTileBytes : 0);
+        if (q_bytes) {
+          mbar_arrive_expect_tx(bars.q_full, q_bytes);
+          for (int t = 0; t < T; ++t) {
+            if (n_t[t] == 0) continue;
+            const int q0 = unit * T * kTileM + t * kTileM;
+            for (int c = 0; c < Cfg::kChunks; ++c)
+              tma_load_3d(sbase + Cfg::kOffQ + t * Cfg::kTileBytes + c * (kTileM * 128), &p.tm_q,
+                          bars.q_full, c * kChunk, q0, bh);
+          }
         }
+      } else if (n_load == 0) {
+        drain_wait(bars.q_full, 0, p.status);   // no product waits for the queries
       }
       int j = 0;
       for (; j < n_load; ++j) {

@@ -114,6 +114,10 @@ struct Share {
 };
 
 __device__ __forceinline__ Share find_share(const RaggedParams& p, int cta, int* scan) {
+  // launched as a programmatic dependent of whatever runs before on the stream
+  // (the merge of the call before lets it start early): the barriers, tensor memory
+  // and descriptors above are set up meanwhile, memory is touched from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
   // thread t holds sequences [t * per, (t + 1) * per)
   const int per = (p.B + kThreads - 1) / kThreads;
@@ -1063,7 +1067,9 @@ struct alignas(4 * PER) PartVec { float x[PER]; };
 template <typename T, int PER>
 __global__ void __launch_bounds__(32 * kMergeRows) ragged_merge_kernel(const __grid_constant__ RaggedParams p) {
   // programmatic dependent of the ragged kernel: wait until that grid has
-  // completed and its results are visible
+  // completed and its results are visible; a ragged kernel that follows on the
+  // stream may set itself up beside this grid
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int D = 32 * PER;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1128,12 +1134,28 @@ __global__ void __launch_bounds__(32 * kMergeRows) ragged_merge_kernel(const __g
   if (lane == 0) p.lse[row] = L > 0.f ? (M + __log2f(L)) * kLn2R : -INFINITY;
 }
 
+// Launch as the programmatic dependent of the kernel before on the stream.
+template <class Kernel>
+cudaError_t launch_dependent(Kernel kernel, unsigned grid, unsigned block, size_t smem,
+                             const RaggedParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 template <int smem, class Kernel>
 cudaError_t launch_main(Kernel kernel, const RaggedParams& p, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<static_cast<unsigned>(p.n_ctas), kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(kernel, static_cast<unsigned>(p.n_ctas), kThreads, smem, p, stream);
 }
 
 template <int D, bool kBf16>
@@ -1149,16 +1171,9 @@ cudaError_t launch_ragged_impl(const RaggedParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // the merge overlaps its launch with the ragged kernel's tail
   const long long rows = static_cast<long long>(p.B) * p.Hq * p.Sq;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows));
-  cfg.blockDim = dim3(32 * kMergeRows);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, ragged_merge_kernel<Elem, D / 32>, p);
+  return launch_dependent(ragged_merge_kernel<Elem, D / 32>,
+                          static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows),
+                          32 * kMergeRows, 0, p, stream);
 }
 
 }  // namespace
