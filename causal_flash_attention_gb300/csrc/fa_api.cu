@@ -871,7 +871,8 @@ int fa_fwd_ragged_paged(const void* q, const void* k_cache, const void* v_cache,
   p.G = Hq / Hkv;
   p.R = rp.R;
   p.block_size = block_size; p.max_blocks = max_blocks; p.num_blocks = num_blocks;
-  p.window = window;
+  // a window that no position outgrows hides nothing (and would overflow positions)
+  p.window = window < p.capacity ? window : 0;
   p.scale_log2 = scale * kLog2e;
   p.cap_in = mod.cap_in;
   p.cap_log2 = mod.cap_log2;

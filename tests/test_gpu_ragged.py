@@ -65,6 +65,8 @@ CASES = [
     ([700, 129, 640], 4, 2, 3, 64, "fp16", 128, 1, 0.0, False),     # a window of one key
     ([2000, 1999], 2, 1, 5, 128, "fp16", 16, 333, 15.0, True),
     ([4000], 2, 2, 1, 64, "bf16", 64, 0, 0.0, True),
+    ([3, 1, 0, 200], 4, 2, 4, 64, "bf16", 16, 2 ** 31 - 1, 0.0, False),   # the largest window
+    ([2, 200], 16, 1, 5, 64, "bf16", 16, 208, 0.0, False),          # as many keys as the table
     ([40] * 160, 2, 1, 1, 64, "fp16", 16, 0, 0.0, False),           # as many tiles as CTAs, and more
     ([130] * 77, 3, 3, 1, 128, "bf16", 32, 0, 0.0, False),
     ([5] * 200 + [3000] + [0] * 200, 2, 1, 1, 64, "bf16", 64, 0, 0.0, False),
