@@ -103,9 +103,12 @@ __device__ __forceinline__ uint64_t f2_swap(uint64_t v) {
   return f2_pack(b, a);
 }
 
-__device__ __forceinline__ float rsqrt_approx(float x) {
+// (mean x^2 + eps)^(-1/2), the sum at least the least normal number: with eps = 0 a
+// head of zeros (a lane past the last head holds one) gives finite factors, not 0 * inf.
+__device__ __forceinline__ float inv_rms(float mean, float eps) {
   float y;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\trsqrt.approx.ftz.f32 %0, t;\n\t}"
+      : "=f"(y) : "f"(mean + eps), "f"(0x1p-126f));   // a NaN stays one
   return y;
 }
 
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(32 * kWarpsH, kFwdBlocks)
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = raw[u].pair(i);
             partners<T, D>(p, at, raw[u], o);
-            const float r = norm ? rsqrt_approx(head_sum<D>(dot(x, x)) * (1.f / D) + p.eps) : 1.f;
+            const float r = norm ? inv_rms(head_sum<D>(dot(x, x)) * (1.f / D), p.eps) : 1.f;
             const uint64_t rr = f2_pack(r, r);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(32 * kWarpsH, kBwdBlocks)
                 x[i] = rx[u].pair(i);
                 o[i] = f2_mul(dn[i], wt[i]);   // g = w dn
               }
-              const float r = rsqrt_approx(head_sum<D>(dot(x, x)) * (1.f / D) + p.eps);
+              const float r = inv_rms(head_sum<D>(dot(x, x)) * (1.f / D), p.eps);
               const float m = head_sum<D>(dot(o, x)) * (1.f / D) * r;
               const uint64_t rr = f2_pack(r, r), nm = f2_pack(-m, -m);
 #pragma unroll

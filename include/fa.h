@@ -220,7 +220,8 @@ typedef struct {
  * Queries and keys for the attention calls: an RMS norm of every head, then
  * rotary positions, in one pass. For each row x (d elements) of q and of k:
  *
- *   n = x * (mean_e x_e^2 + eps)^(-1/2) * weight       (both weights NULL: n = x)
+ *   n = x * (mean_e x_e^2 + eps)^(-1/2) * weight       (both weights NULL: n = x;
+ *       a mean plus eps below 2^-126 counts as that, so a row of zeros gives zeros)
  *   y_a = rope_scale * (cos t * n_a - sin t * n_b)
  *   y_b = rope_scale * (sin t * n_a + cos t * n_b)
  *

@@ -129,6 +129,26 @@ def test_in_place_and_into_views(fa):
     assert torch.equal(got_g[2], want_g[2]) and torch.equal(got_g[3], want_g[3])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_eps_zero(fa, d):
+    """With eps = 0 only a head of zeros has no norm: it gives zeros, and neither it nor the
+    lanes past the last head (one key head here) reach the weight gradients."""
+    q, k, _, w = make(1, 3, 1, 21, d, "bf16", True, "packed", 8)
+    outs, grads = run_both(fa, q, k, w, freqs(d), None, 0.0, False, 1.0)
+    turns = fa.rope_turns(freqs(d), DEV)
+    kw = dict(q_weight=w[0], k_weight=w[1], eps=0.0)
+    q, dy = q.clone(), [torch.randn_like(t) for t in outs]
+    dy[0][0, 1, 4] = 0
+    want = fa.qk_norm_rope_backward(*dy, q, k, turns, **kw)   # this head's dy is 0: no share of dw
+    q[0, 1, 4] = 0
+    assert (fa.qk_norm_rope_forward(q, k, turns, **kw)[0][0, 1, 4] == 0).all()
+    got = fa.qk_norm_rope_backward(*dy, q, k, turns, **kw)
+    assert torch.equal(got[2], want[2]) and torch.equal(got[3], want[3])
+    assert (got[0][0, 1, 4] == 0).all()
+    q[0, 2, 9, 3] = float("nan")
+    assert fa.qk_norm_rope_forward(q, k, turns, **kw)[0][0, 2, 9].isnan().all()
+
+
 def test_a_bad_row_stays_its_own(fa):
     """NaN and infinity in one head of one token reach no other head or token."""
     q, k, _, w = make(1, 4, 2, 20, 64, "bf16", True, "packed", 7)
