@@ -8,6 +8,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <initializer_list>
+#include <limits>
 
 #include "../../include/fa.h"
 #include "fa_decode.h"
@@ -273,8 +274,16 @@ struct SpanArgs {
   float softcap;
 };
 
-int check_span(const SpanArgs& m) {
-  if (!(std::isfinite(m.softcap) && m.softcap >= 0.f)) return FA_ERR_SCALE;
+// Scores are scaled by scale / softcap and by softcap in fp32, and by the latter's
+// inverse: factors far from any use are refused before one leaves the range.
+bool cap_ok(float softcap, float scale) {
+  if (softcap == 0.f) return true;
+  const double c = softcap, ratio = scale / c;
+  return c >= 0x1p-60 && c <= 0x1p60 && ratio >= 0x1p-60 && ratio <= 0x1p60;
+}
+
+int check_span(const SpanArgs& m, float scale) {
+  if (!cap_ok(m.softcap, scale)) return FA_ERR_SCALE;
   if (!m.key_begin || !m.key_end) return FA_ERR_NULL;
   if (((reinterpret_cast<uintptr_t>(m.key_begin) | reinterpret_cast<uintptr_t>(m.key_end) |
         reinterpret_cast<uintptr_t>(m.slopes)) & 3u) != 0)
@@ -289,14 +298,18 @@ ScoreMod make_mod(const SpanArgs& m, int Sq, int Skv, float scale) {
   r.slopes = m.slopes;
   r.cap_in = m.softcap > 0.f ? 2.f * kLog2e * scale / m.softcap : 0.f;
   r.cap_log2 = m.softcap * kLog2e;
-  // tanh u / u in powers of u^2 on |u| <= 3/4 (score_mod.cuh), scaled; within these
-  // ratios no power of the scale leaves the range of fp32
+  // tanh u / u in powers of u^2 on |u| <= 3/4 (score_mod.cuh), scaled; left out (limit
+  // 0) where a coefficient would leave the range of fp32
   static const double a[5] = {0.9999971985816956, -0.33323076367378235, 0.13226088881492615,
                               -0.04928038269281387, 0.012318773195147514};
   const double ratio = m.softcap > 0.f ? static_cast<double>(scale) / m.softcap : 0.0;
-  const bool poly = ratio >= 1e-4 && ratio <= 1e3;
-  for (int i = 0; i < 5; ++i)
-    r.cap_a[i] = poly ? static_cast<float>(a[i] * m.softcap * kLog2e * std::pow(ratio, 2 * i + 1)) : 0.f;
+  bool poly = ratio >= 1e-4 && ratio <= 1e3;
+  double power = m.softcap * kLog2e * ratio;
+  for (int i = 0; i < 5; ++i, power *= ratio * ratio) {
+    const double x = std::fabs(a[i] * power);
+    poly = poly && x >= std::numeric_limits<float>::min() && x <= std::numeric_limits<float>::max();
+    r.cap_a[i] = poly ? static_cast<float>(a[i] * power) : 0.f;
+  }
   r.cap_limit = poly ? static_cast<float>(0.75 / ratio) : 0.f;
   r.pos_offset = Skv - Sq;
   return r;
@@ -779,7 +792,7 @@ int fa_fwd_span(const void* q, const void* k, const void* v, const int* key_begi
   if (rc != FA_OK) return rc;
   if (dtype == FA_F32) return FA_ERR_DTYPE;   // the span path runs on the tensor cores only
   const SpanArgs mod{key_begin, key_end, slopes, softcap};
-  if ((rc = check_span(mod)) != FA_OK) return rc;
+  if ((rc = check_span(mod, scale)) != FA_OK) return rc;
   if (!q || !k || !v || !out || !lse) return FA_ERR_NULL;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(lse))
     return FA_ERR_ALIGN;
@@ -813,7 +826,7 @@ int fa_bwd_span(const void* q, const void* k, const void* v, const int* key_begi
   if (dtype == FA_F32) return FA_ERR_DTYPE;
   const SpanArgs mod{key_begin, key_end, slopes, softcap};
   int rc = check_common(B, Hq, Hkv, Sq, Skv, d, 0, scale, dtype);
-  if (rc == FA_OK) rc = check_span(mod);
+  if (rc == FA_OK) rc = check_span(mod, scale);
   if (rc != FA_OK) return rc;
   return bwd_impl(q, k, v, out, dout, lse, dq, dk, dv, B, Hq, Hkv, Sq, Skv, d, 0, scale, dtype,
                   workspace, workspace_bytes, stream, &mod);
@@ -838,7 +851,7 @@ int fa_fwd_ragged_paged(const void* q, const void* k_cache, const void* v_cache,
   if (dtype == FA_F32) return FA_ERR_DTYPE;   // the paged path runs on the tensor cores only
   if (!paged_sizes_ok(B, Hq, Hkv, Sq, block_size, num_blocks, max_blocks) || window < 0)
     return FA_ERR_SHAPE;
-  if (!(std::isfinite(softcap) && softcap >= 0.f)) return FA_ERR_SCALE;
+  if (!cap_ok(softcap, scale)) return FA_ERR_SCALE;
   if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !lse) return FA_ERR_NULL;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
       !aligned16(lse) ||

@@ -309,7 +309,8 @@ int fa_qk_norm_rope_append(const fa_view* q, const fa_view* k, const fa_view* v,
  *
  * G * Sq <= 128 with G = Hq / Hkv, block_size as for fa_fwd_splitkv_paged,
  * max_blocks >= 1, window >= 0 and B * Hkv * (ceil(max_blocks * block_size /
- * 128) + 8) < 2^31 (else FA_ERR_SHAPE); softcap finite and >= 0 (else FA_ERR_SCALE); FA_BF16 and FA_F16 only (FA_F32 gives FA_ERR_DTYPE).
+ * 128) + 8) < 2^31 (else FA_ERR_SHAPE); softcap as for fa_fwd_span (else
+ * FA_ERR_SCALE); FA_BF16 and FA_F16 only (FA_F32 gives FA_ERR_DTYPE).
  * workspace: caller-owned, at least fa_fwd_ragged_paged_workspace_bytes(...)
  * bytes, 256-byte aligned, contents on entry without meaning; calls that may
  * overlap on the GPU need one each.
@@ -351,10 +352,12 @@ size_t fa_fwd_ragged_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int d
  * dO, Q, K (backward) of the same 128-row tile, so q, k, v, out and dout must
  * be finite everywhere, padding included.
  *
- * FA_BF16 and FA_F16 only (FA_F32 gives FA_ERR_DTYPE). softcap must be finite
- * and >= 0 (else FA_ERR_SCALE); key_begin, key_end and slopes need 4-byte
- * alignment. dk and dv have the same bits on every call; dq is summed with
- * fp32 additions in global memory whose order, and so its last bits, may differ.
+ * FA_BF16 and FA_F16 only (FA_F32 gives FA_ERR_DTYPE). softcap must be 0, or it
+ * and scale / softcap within 2^-60 .. 2^60 (else FA_ERR_SCALE); a capped score is
+ * off by up to softcap * 2^-20, whatever its size. key_begin, key_end and slopes
+ * need 4-byte alignment. dk and dv have the same bits on every call; dq is summed
+ * with fp32 additions in global memory whose order, and so its last bits, may
+ * differ.
  */
 int fa_fwd_span(const void* q, const void* k, const void* v, const int* key_begin,
                 const int* key_end, void* out, float* lse, int B, int Hq, int Hkv, int Sq,

@@ -29,7 +29,9 @@ SPAN_BAD = [
     (dict(d=96), SHAPE), (dict(Sq=0), SHAPE), (dict(Skv=0), SHAPE), (dict(Hq=3, Hkv=2), SHAPE),
     (dict(B=1 << 30, Hq=4, Hkv=4), SHAPE), (dict(dtype=0), DTYPE), (dict(dtype=5), DTYPE),
     (dict(scale=0.0), SCALE), (dict(scale=math.nan), SCALE), (dict(softcap=-1.0), SCALE),
-    (dict(softcap=math.inf), SCALE), (dict(softcap=math.nan), SCALE), (dict(begin=None), NULL),
+    (dict(softcap=math.inf), SCALE), (dict(softcap=math.nan), SCALE),
+    (dict(softcap=1e-20), SCALE), (dict(softcap=1e20), SCALE), (dict(softcap=50.0, scale=1e-20), SCALE),
+    (dict(softcap=1e-10, scale=1e10), SCALE), (dict(begin=None), NULL),
     (dict(end=None), NULL), (dict(q=None), NULL), (dict(lse=None), NULL), (dict(begin=P + 2), ALIGN),
     (dict(end=P + 1), ALIGN), (dict(slopes=P + 2), ALIGN), (dict(v=P + 8), ALIGN),
     (dict(out=P + 4), ALIGN),
@@ -74,7 +76,7 @@ def ragged(L, q=P, k=P, v=P, table=P, lens=P, out=P, lse=P, B=2, Hq=8, Hkv=2, Sq
     (dict(bs=2048), SHAPE), (dict(bs=48), SHAPE), (dict(nb=0), SHAPE), (dict(mb=0), SHAPE),
     (dict(nb=1 << 30), SHAPE), (dict(B=1 << 20, mb=1 << 14), SHAPE), (dict(window=-1), SHAPE), (dict(Hq=256, Hkv=1), SHAPE),
     (dict(dtype=0), DTYPE), (dict(dtype=9), DTYPE), (dict(scale=-1.0), SCALE),
-    (dict(softcap=math.nan), SCALE), (dict(softcap=-0.5), SCALE), (dict(table=None), NULL),
+    (dict(softcap=math.nan), SCALE), (dict(softcap=-0.5), SCALE), (dict(softcap=1e-30), SCALE), (dict(softcap=1e30), SCALE), (dict(table=None), NULL),
     (dict(lens=None), NULL), (dict(k=None), NULL), (dict(table=P + 2), ALIGN),
     (dict(lens=P + 1), ALIGN), (dict(slopes=P + 3), ALIGN), (dict(q=P + 8), ALIGN),
     (dict(ws=None), WORKSPACE), (dict(ws_bytes=64), WORKSPACE), (dict(ws=P + 32), ALIGN)])
