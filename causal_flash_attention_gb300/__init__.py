@@ -437,7 +437,7 @@ def key_spans(B, Sq, Skv=None, *, causal=True, window=0, doc_lens=None, prefix_l
     window       only the last `window` keys up to the row's position (0: all)
     doc_lens     lengths of the documents packed along the keys, the same in every sequence
                  (a list) or one list per sequence: a row sees its own document only, and rows
-                 past the last document see nothing
+                 outside all documents see nothing
     prefix_lens  one number, or one per sequence: the first keys (of the row's document, with
                  doc_lens) that every row sees although they lie after it
     kv_lens      one number, or one per sequence: real keys; rows and keys past them are padding
@@ -466,6 +466,7 @@ def key_spans(B, Sq, Skv=None, *, causal=True, window=0, doc_lens=None, prefix_l
             edges = torch.cat((torch.zeros(1, dtype=torch.int64), ends, ends[-1:] if lens else
                                torch.zeros(1, dtype=torch.int64)))
             begin[b], last[b] = edges[which], edges[which + 1]
+        last = torch.where(pos < 0, begin, last)   # fewer keys than rows: before every document
     if kv_lens is not None:
         n = column(kv_lens)
         last = torch.where(pos < n, torch.minimum(last, n), torch.zeros_like(last))
@@ -522,8 +523,8 @@ def rope_inv_freq(rope_dim, base=10000.0, scaling="none", factor=1.0, trained_le
     """
     if rope_dim < 2 or rope_dim % 2:
         raise ValueError("rope_dim must be even and positive")
-    if not (factor >= 1.0 and base > 1.0):
-        raise ValueError("factor must be >= 1 and base > 1")
+    if not (factor >= 1.0 and base > 1.0 and high_turns > low_turns):
+        raise ValueError("factor must be >= 1, base > 1 and high_turns > low_turns")
     if scaling == "base" and rope_dim > 2:
         base = base * factor ** (rope_dim / (rope_dim - 2))
     f = base ** (-torch.arange(0, rope_dim, 2, dtype=torch.float64) / rope_dim)

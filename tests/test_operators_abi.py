@@ -187,7 +187,8 @@ def test_turns_table(fa_lib):
     assert t.tolist() == [1 << 62, -(1 << 62), -(1 << 63), 0]
     with pytest.raises(ValueError):
         fa_lib.rope_turns([math.inf])
-    for bad in (dict(rope_dim=3), dict(rope_dim=8, factor=0.5), dict(rope_dim=8, scaling="other")):
+    for bad in (dict(rope_dim=3), dict(rope_dim=8, factor=0.5), dict(rope_dim=8, scaling="other"),
+                dict(rope_dim=8, scaling="parts", low_turns=4.0, high_turns=4.0)):
         with pytest.raises(ValueError):
             fa_lib.rope_inv_freq(**bad)
 
@@ -231,6 +232,17 @@ def test_key_spans(fa_lib, kw, ref, Sq, Skv):
     j = torch.arange(Skv)
     got = (j >= begin[..., None]) & (j < end[..., None])
     assert (got.numpy() == brute(2, Sq, Skv, **ref)).all()
+
+
+def test_key_spans_of_rows_before_the_keys(fa_lib):
+    """Fewer keys than rows: documents hold no row before the first key; without documents and
+    without the causal mask every row sees every key."""
+    begin, end = fa_lib.key_spans(1, 8, 5, doc_lens=[3, 2], causal=False)
+    assert (end - begin).tolist() == [[0, 0, 0, 3, 3, 3, 2, 2]]
+    begin, end = fa_lib.key_spans(1, 8, 5, causal=False)
+    assert (end - begin).tolist() == [[5] * 8]
+    begin, end = fa_lib.key_spans(1, 8, 5)
+    assert (end - begin).tolist() == [[0, 0, 0, 1, 2, 3, 4, 5]]
 
 
 @pytest.mark.parametrize("kw", [dict(doc_lens=[20]), dict(doc_lens=[-1, 2]), dict(kv_lens=[1, 2, 3]),
