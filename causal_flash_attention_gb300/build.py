@@ -85,7 +85,7 @@ def _binding_command(out: str) -> list:
     return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *("-isystem" + i for i in inc), BINDING_SRC, "-o", out, "-L" + lib, "-Wl,-rpath," + lib,
-            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-ldl"]
+            "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-ldl"]
 
 
 def _binding_stale() -> bool:
