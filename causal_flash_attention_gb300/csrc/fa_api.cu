@@ -291,6 +291,20 @@ int check_span(const SpanArgs& m, float scale) {
   return FA_OK;
 }
 
+// Coefficients of softcap log2(e) tanh(s ratio) / s from those of tanh u / u. False: one
+// would leave the range of fp32, the polynomial is not to be used.
+template <int N>
+bool scale_poly(const double (&from)[N], float (&to)[N], double ratio, double cap_log2) {
+  bool ok = ratio >= 1e-4 && ratio <= 1e3;
+  double power = cap_log2 * ratio;
+  for (int i = 0; i < N; ++i, power *= ratio * ratio) {
+    const double x = std::fabs(from[i] * power);
+    ok = ok && x >= std::numeric_limits<float>::min() && x <= std::numeric_limits<float>::max();
+    to[i] = ok ? static_cast<float>(from[i] * power) : 0.f;
+  }
+  return ok;
+}
+
 ScoreMod make_mod(const SpanArgs& m, int Sq, int Skv, float scale) {
   ScoreMod r;
   r.key_begin = m.key_begin;
@@ -298,19 +312,14 @@ ScoreMod make_mod(const SpanArgs& m, int Sq, int Skv, float scale) {
   r.slopes = m.slopes;
   r.cap_in = m.softcap > 0.f ? 2.f * kLog2e * scale / m.softcap : 0.f;
   r.cap_log2 = m.softcap * kLog2e;
-  // tanh u / u in powers of u^2 on |u| <= 3/4 (score_mod.cuh), scaled; left out (limit
-  // 0) where a coefficient would leave the range of fp32
+  // tanh u / u in powers of u^2 on |u| <= 3/4 and on |u| <= 0.3 (score_mod.cuh), scaled
   static const double a[5] = {0.9999971985816956, -0.33323076367378235, 0.13226088881492615,
                               -0.04928038269281387, 0.012318773195147514};
+  static const double b[3] = {0.9999960104045702, -0.3329747978841012, 0.12522591724872847};
   const double ratio = m.softcap > 0.f ? static_cast<double>(scale) / m.softcap : 0.0;
-  bool poly = ratio >= 1e-4 && ratio <= 1e3;
-  double power = m.softcap * kLog2e * ratio;
-  for (int i = 0; i < 5; ++i, power *= ratio * ratio) {
-    const double x = std::fabs(a[i] * power);
-    poly = poly && x >= std::numeric_limits<float>::min() && x <= std::numeric_limits<float>::max();
-    r.cap_a[i] = poly ? static_cast<float>(a[i] * power) : 0.f;
-  }
-  r.cap_limit = poly ? static_cast<float>(0.75 / ratio) : 0.f;
+  const double cap_log2 = static_cast<double>(m.softcap) * kLog2e;
+  r.cap_limit_a = scale_poly(a, r.cap_a, ratio, cap_log2) ? static_cast<float>(0.75 / ratio) : 0.f;
+  r.cap_limit_b = scale_poly(b, r.cap_b, ratio, cap_log2) ? static_cast<float>(0.3 / ratio) : 0.f;
   r.pos_offset = Skv - Sq;
   return r;
 }

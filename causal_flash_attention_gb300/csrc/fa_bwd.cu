@@ -894,26 +894,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               }
               tmem_st16(p_dst, pk);
             }
-            if (cap) {
-              float big = 0.f;
+            float sc[32];
 #pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                big = fmax3(big, fabsf(__uint_as_float(raw[e])), fabsf(__uint_as_float(raw[e + 1])));
-              if (__any_sync(0xffffffffu, !(big <= p.mod.cap_limit))) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  raw[e] = __float_as_uint(cap_exact(__uint_as_float(raw[e]), p.mod));
-              } else {
-                const CapPoly poly(p.mod);
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                  float y0, y1;
-                  f2_unpack(poly(f2_pack(__uint_as_float(raw[e]), __uint_as_float(raw[e + 1]))), y0, y1);
-                  raw[e] = __float_as_uint(y0);
-                  raw[e + 1] = __float_as_uint(y1);
-                }
-              }
-            }
+            for (int e = 0; e < 32; ++e) sc[e] = __uint_as_float(raw[e]);
+            if (cap) cap_scores(sc, p.mod);
             // P = 2^(y c - L) with the bias, packed; and with a cap P (1 - tanh^2),
             // tanh = y / (softcap log2(e))
             auto weights = [&](auto capped, auto biased) {
@@ -922,7 +906,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 const float2 l2 = *reinterpret_cast<const float2*>(l2s + hh * 32 + e);
-                const uint64_t y = f2_pack(__uint_as_float(raw[e]), __uint_as_float(raw[e + 1]));
+                const uint64_t y = f2_pack(sc[e], sc[e + 1]);
                 uint64_t x = f2_pack(-l2.x, -l2.y);
                 x = capped.value ? f2_add(y, x) : f2_fma(y, c2, x);
                 if (biased.value)

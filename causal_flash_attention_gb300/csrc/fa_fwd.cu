@@ -429,20 +429,7 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
       // never stored, so their limit may run past Skv - 1)
       if constexpr (kSpan) {
         if constexpr (kSpan == 2) {
-          if (p.mod.cap_in != 0.f) {
-            float big = 0.f;
-#pragma unroll
-            for (int i = 0; i < kTileN; i += 2) big = fmax3(big, fabsf(s[i]), fabsf(s[i + 1]));
-            if (__any_sync(0xffffffffu, !(big <= p.mod.cap_limit))) {
-#pragma unroll
-              for (int i = 0; i < kTileN; ++i) s[i] = cap_exact(s[i], p.mod);
-            } else {
-              const CapPoly poly(p.mod);
-#pragma unroll
-              for (int i = 0; i < kTileN; i += 2)
-                f2_unpack(poly(f2_pack(s[i], s[i + 1])), s[i], s[i + 1]);
-            }
-          }
+          if (p.mod.cap_in != 0.f) cap_scores(s, p.mod);
           if (p.mod.slopes) {
             // |distance| is d0 + i or -d0 - i; on a tile to one side of the row the
             // part without i waits in row_off

@@ -24,8 +24,8 @@ struct ScoreMod {
   const float* slopes;    // [Hq], or null: no distance bias
   float cap_in;           // 2 log2(e) scale / softcap: e^(2 s / softcap) = 2^(cap_in <q, k>); 0: no cap
   float cap_log2;         // softcap * log2(e)
-  float cap_a[5];         // odd polynomial of the cap, for unscaled scores up to
-  float cap_limit;        // this size (0: not to be used)
+  float cap_a[5], cap_b[3];           // odd polynomials of the cap, each for unscaled
+  float cap_limit_a, cap_limit_b;     // scores up to this size (0: not to be used)
   int pos_offset;         // Skv - Sq: query row i stands at position i + pos_offset
 };
 

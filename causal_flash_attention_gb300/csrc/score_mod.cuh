@@ -47,27 +47,51 @@ __device__ __forceinline__ float cap_r(float s, float cap_in) {
   return rcp_approx(1.f + ex2(s * cap_in));
 }
 
-// The cap by a polynomial where every score of the warp is inside |u| <= 3/4,
-// u = s * scale / softcap: tanh u = u (a0 + a1 w + ... + a4 w^4), w = u^2, a
-// degree-9 minimax fit (by reweighted least squares) off by 1.9e-7, 2.7e-7 in fp32.
-// Seven multiply-adds and no special function, which the softmax is short of; the
-// coefficients come with the powers of scale / softcap and softcap * log2(e)
-// multiplied in, so y = softcap log2(e) tanh u directly from the unscaled score.
+// The cap by a polynomial where the warp's scores allow it, u = s * scale / softcap:
+// tanh u = u (a0 + a1 w + ...), w = u^2, minimax fits (by reweighted least squares) of
+// degree 9 for |u| <= 3/4, off by 1.9e-7, 2.6e-7 in fp32, and of degree 5 for
+// |u| <= 0.3, off by 1.7e-7, 1.9e-7 in fp32. No special function, which the softmax is
+// short of; the coefficients come with the powers of scale / softcap and softcap *
+// log2(e) multiplied in, so y = softcap log2(e) tanh u directly from the unscaled score.
+template <int N>
 struct CapPoly {
-  uint64_t a[5];
-  __device__ __forceinline__ explicit CapPoly(const ScoreMod& m) {
+  uint64_t a[N];
+  __device__ __forceinline__ explicit CapPoly(const float (&from)[N]) {
 #pragma unroll
-    for (int i = 0; i < 5; ++i) a[i] = f2_pack(m.cap_a[i], m.cap_a[i]);
+    for (int i = 0; i < N; ++i) a[i] = f2_pack(from[i], from[i]);
   }
-  // two scores at a time, in paired fp32 instructions
-  __device__ __forceinline__ uint64_t operator()(uint64_t s) const {
-    const uint64_t w = f2_mul(s, s);
-    return f2_mul(s, f2_fma(w, f2_fma(w, f2_fma(w, f2_fma(w, a[4], a[3]), a[2]), a[1]), a[0]));
+  // scores in place, two at a time, in paired fp32 instructions
+  template <int M>
+  __device__ __forceinline__ void operator()(float (&s)[M]) const {
+#pragma unroll
+    for (int i = 0; i < M; i += 2) {
+      const uint64_t x = f2_pack(s[i], s[i + 1]), w = f2_mul(x, x);
+      uint64_t y = a[N - 1];
+#pragma unroll
+      for (int k = N - 2; k >= 0; --k) y = f2_fma(w, y, a[k]);
+      f2_unpack(f2_mul(x, y), s[i], s[i + 1]);
+    }
   }
 };
 // Past that, by the exponential form.
 __device__ __forceinline__ float cap_exact(float s, const ScoreMod& m) {
   return fmaf(-2.f * m.cap_log2, cap_r(s, m.cap_in), m.cap_log2);
+}
+
+// A warp's unscaled scores to capped ones in the log2 domain (every lane calls it).
+template <int M>
+__device__ __forceinline__ void cap_scores(float (&s)[M], const ScoreMod& m) {
+  float big = 0.f;
+#pragma unroll
+  for (int i = 0; i < M; i += 2) big = fmax3(big, fabsf(s[i]), fabsf(s[i + 1]));
+  if (!__any_sync(0xffffffffu, !(big <= m.cap_limit_b))) {
+    CapPoly<3>(m.cap_b)(s);
+  } else if (!__any_sync(0xffffffffu, !(big <= m.cap_limit_a))) {
+    CapPoly<5>(m.cap_a)(s);
+  } else {
+#pragma unroll
+    for (int i = 0; i < M; ++i) s[i] = cap_exact(s[i], m);
+  }
 }
 
 }  // namespace fa
