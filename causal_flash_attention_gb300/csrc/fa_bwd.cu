@@ -320,9 +320,24 @@ __global__ void __launch_bounds__(256, kParts ? 4 : 8) dq_convert_kernel(const D
 // w = j * B * Hkv + (b * Hkv + g), so that low j (most query tiles under the
 // causal mask) comes first.
 struct BwdItem {
-  int j, bkv, b, g;
-  int i_start, n_i, n_iter;
-  int step0, part;   // span form: first step, and the partial result it leaves (-1: none)
+  int j, bkv, b;
+  int i_start, i_end;   // query tiles of every query head
+  int n_iter;           // steps
+  int i0, bh0;          // query tile and (batch, query head) of the first step
+  int part;             // span form: the partial result it leaves (-1: none)
+};
+
+// The steps of an item in order: query tiles, then query heads. (Found by division at
+// each step, they cost the compute warps 0.3 us of a 2.8 us step.)
+struct BwdSteps {
+  int i, bh;
+  __device__ __forceinline__ explicit BwdSteps(const BwdItem& I) : i(I.i0), bh(I.bh0) {}
+  __device__ __forceinline__ void next(const BwdItem& I) {
+    if (++i == I.i_end) {
+      i = I.i_start;
+      ++bh;
+    }
+  }
 };
 
 template <bool kSpan>
@@ -332,20 +347,21 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdParams& p, int w) {
   it.j = w / BHkv;
   it.bkv = w % BHkv;
   it.b = it.bkv / p.Hkv;
-  it.g = it.bkv % p.Hkv;
-  it.step0 = 0;
+  const int G = p.Hq / p.Hkv;
+  it.bh0 = it.bkv * G;   // b * Hq + (key/value head) * G
   it.part = -1;
   // causal: the first query tile holding a row at position >= this tile's
   // first key (query row i stands at position i + kv_offset)
   if constexpr (kSpan) {
     const int2 r = p.plan[static_cast<size_t>(it.b) * p.n_kv_tiles + it.j];
     it.i_start = r.x;
-    it.n_i = r.y;
+    it.i_end = r.x + r.y;
   } else {
     it.i_start = p.causal ? max(0, it.j * kTileN - p.kv_offset) / kTileM : 0;
-    it.n_i = p.n_q_tiles - it.i_start;
+    it.i_end = p.n_q_tiles;
   }
-  it.n_iter = (p.Hq / p.Hkv) * it.n_i;
+  it.i0 = it.i_start;
+  it.n_iter = G * (it.i_end - it.i_start);
   return it;
 }
 
@@ -354,20 +370,22 @@ __device__ __forceinline__ BwdItem bwd_listed_item(const BwdParams& p, int limit
                                                    const uint16_t* entries, int w) {
   BwdItem it;
   const int e = w / p.Hkv;
-  it.g = w - e * p.Hkv;
+  const int g = w - e * p.Hkv, G = p.Hq / p.Hkv;
   const int tile = entries[e] & 127, slice = entries[e] >> 7;
   it.b = tile / p.n_kv_tiles;
   it.j = tile - it.b * p.n_kv_tiles;
-  it.bkv = it.b * p.Hkv + it.g;
+  it.bkv = it.b * p.Hkv + g;
   const int2 r = p.plan[tile];
   it.i_start = r.x;
-  it.n_i = r.y;
-  const int steps = (p.Hq / p.Hkv) * it.n_i;
+  it.i_end = r.x + r.y;
+  const int steps = G * r.y;
   int slices, len;
   span_cut(steps, limit, slices, len);
-  it.step0 = slice * len;
-  it.n_iter = min(len, steps - it.step0);
-  it.part = slices > 1 ? e * p.Hkv + it.g : -1;
+  const int step0 = slice * len;
+  it.i0 = r.x + step0 % r.y;
+  it.bh0 = it.bkv * G + step0 / r.y;
+  it.n_iter = min(len, steps - step0);
+  it.part = slices > 1 ? e * p.Hkv + g : -1;
   return it;
 }
 
@@ -501,9 +519,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       int kv_pending = -1;   // kv_full phase whose K, V loads may be in flight
       bool ok = true;
       // one step's Q (with its L, D rows) and dO
-      auto load_step = [&](const BwdItem& I, int s) -> bool {
-        const int bh = I.b * p.Hq + I.g * (p.Hq / p.Hkv) + (I.step0 + s) / I.n_i;
-        const int i = I.i_start + (I.step0 + s) % I.n_i;
+      auto load_step = [&](int i, int bh) -> bool {
         const int sq = nq % NQ;
         if (nq >= NQ &&
             !mbar_wait(q_empty(sq), static_cast<uint32_t>(nq / NQ - 1) & 1, abort_flag, p.status))
@@ -534,10 +550,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       int w = atomicAdd(p.work, 1);
       for (int k = 0; ok; ++k) {
         BwdItem I{};
-        if (w < n_items) {
-          I = item_of(w);
-          if (!(ok = load_step(I, 0))) break;
-        }
+        if (w < n_items) I = item_of(w);
+        BwdSteps at(I);
+        if (w < n_items && !(ok = load_step(at.i, at.bh))) break;
         if (k > 0) {
           if (!(ok = mbar_wait(kv_empty, (k - 1) & 1, abort_flag, p.status))) break;
           kv_pending = -1;
@@ -557,7 +572,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                       I.j * kTileN, I.bkv);
         }
         kv_pending = k;
-        for (int s = 1; ok && s < I.n_iter; ++s) ok = load_step(I, s);
+        for (int s = 1; ok && s < I.n_iter; ++s) {
+          at.next(I);
+          ok = load_step(at.i, at.bh);
+        }
         if (!ok) break;
         w = atomicAdd(p.work, 1);
         if (w < n_items) {   // the next item's K_j, V_j into L2 while this item runs
@@ -826,11 +844,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if constexpr (kSpan) I = *item_info;
       else I = bwd_item<false>(p, w);
       const int kv = I.j * kTileN + r;
-      for (int it = 0; it < I.n_iter; ++it, ++g) {
+      BwdSteps at(I);
+      for (int it = 0; it < I.n_iter; ++it, ++g, at.next(I)) {
         const int st = g % NQ;
         const uint32_t par = static_cast<uint32_t>(g / NQ) & 1;
-        const int i = I.i_start + (I.step0 + it) % I.n_i;
-        const int q0 = i * kTileM + c0;
+        const int q0 = at.i * kTileM + c0;
         // kSpan: the spans of query columns 2 l and 2 l + 1 of this warp's half
         int4 sp = make_int4(0, 0, 0, 0);
         if constexpr (kSpan)
@@ -870,7 +888,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           const bool cap = p.mod.cap_in != 0.f;
           const float inv_cap = cap ? 1.f / p.mod.cap_log2 : 0.f;
           const float bias =
-              p.mod.slopes ? p.mod.slopes[I.g * (p.Hq / p.Hkv) + (I.step0 + it) / I.n_i] * kLog2eF : 0.f;
+              p.mod.slopes ? p.mod.slopes[at.bh - I.b * p.Hq] * kLog2eF : 0.f;
           const float d0 = static_cast<float>(q0 + p.mod.pos_offset - kv);
           // Two halves of 32 columns, for the registers. Packed P^T goes over score
           // columns this warp has read itself, or into the P^T buffer at d = 64: the
@@ -901,7 +919,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             // P = 2^(y c - L) with the bias, packed; and with a cap P (1 - tanh^2),
             // tanh = y / (softcap log2(e))
             auto weights = [&](auto capped, auto biased) {
-              const uint64_t c2 = f2_pack(c, c), ic2 = f2_pack(inv_cap, inv_cap);
+              const uint64_t c2 = f2_pack(c, c), nic2 = f2_pack(-inv_cap * inv_cap, -inv_cap * inv_cap);
               const uint64_t nb2 = f2_pack(-bias, -bias), one2 = f2_pack(1.f, 1.f);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
@@ -918,8 +936,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 p1 = ex2(p1);
                 pk[e / 2] = pack2<kBf16>(p0, p1);
                 if (capped.value) {
-                  const uint64_t t = f2_mul(y, ic2);
-                  f2_unpack(f2_mul(f2_pack(p0, p1), f2_sub(one2, f2_mul(t, t))), p0, p1);
+                  f2_unpack(f2_mul(f2_pack(p0, p1), f2_fma(f2_mul(y, y), nic2, one2)), p0, p1);
                   ppk[hh * 16 + e / 2] = pack2<kBf16>(p0, p1);
                 } else {
                   ppk[hh * 16 + e / 2] = pk[e / 2];
@@ -1035,12 +1052,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           tr(34);
         }
 
-        const int bh = I.b * p.Hq + I.g * (p.Hq / p.Hkv) + (I.step0 + it) / I.n_i;
         if (!Cfg::kSepQ || it + 1 == I.n_iter) {   // else after the next step's P^T
-          if (!(ok = read_dq(g, i, bh))) break;
+          if (!(ok = read_dq(g, at.i, at.bh))) break;
         }
-        prev_i = i;
-        prev_bh = bh;
+        prev_i = at.i;
+        prev_bh = at.bh;
       }
       if (!ok) break;
       if (pend_x >= 0) reduce_box(dq_pend, pend_x, pend_y, pend_bh);
