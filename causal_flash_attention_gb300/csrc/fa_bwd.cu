@@ -857,8 +857,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const float* rowv = reinterpret_cast<const float*>(smem + Cfg::kOffRow + st * 1024);
         const float* l2s = rowv + c0;          // L * log2(e) per query column
         const float* dls = rowv + 128 + c0;    // D per query column
-        ok = __all_sync(0xffffffffu, mbar_wait(q_full(st), par, abort_flag, p.status));
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full, g & 1, abort_flag, p.status));
+        ok = __all_sync(0xffffffffu, mbar_wait(q_full(st), par, abort_flag, p.status) &&
+                                         mbar_wait(s_full, g & 1, abort_flag, p.status));
         if (!ok) break;
         tr(20);
         if (g == 0 && warp == 2 && lane == 0) trace_span(p.trace, 3, clock64());
@@ -1005,8 +1005,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tr(21);
         if (Cfg::kSepQ && it > 0 && !(ok = read_dq(g - 1, prev_i, prev_bh))) break;
 
-        if (g > 0) ok = __all_sync(0xffffffffu, mbar_wait(ds_empty, (g - 1) & 1, abort_flag, p.status));
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(dp_full, g & 1, abort_flag, p.status));
+        ok = __all_sync(0xffffffffu,
+                        (g == 0 || mbar_wait(ds_empty, (g - 1) & 1, abort_flag, p.status)) &&
+                            mbar_wait(dp_full, g & 1, abort_flag, p.status));
         if (!ok) break;
         tr(22);
         tc_fence_after();
