@@ -915,7 +915,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             float sc[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) sc[e] = __uint_as_float(raw[e]);
-            if (cap) cap_scores(sc, p.mod);
+            if (cap) cap_scores(sc, warp_abs_max(sc), p.mod);
             // P = 2^(y c - L) with the bias, packed; and with a cap P (1 - tanh^2),
             // tanh = y / (softcap log2(e))
             auto weights = [&](auto capped, auto biased) {

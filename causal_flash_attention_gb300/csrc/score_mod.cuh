@@ -60,16 +60,27 @@ struct CapPoly {
 #pragma unroll
     for (int i = 0; i < N; ++i) a[i] = f2_pack(from[i], from[i]);
   }
-  // scores in place, two at a time, in paired fp32 instructions
+  // capped score / score, of two at a time, in paired fp32 instructions
+  __device__ __forceinline__ uint64_t factor(uint64_t s) const {
+    const uint64_t w = f2_mul(s, s);
+    uint64_t y = a[N - 1];
+#pragma unroll
+    for (int k = N - 2; k >= 0; --k) y = f2_fma(w, y, a[k]);
+    return y;
+  }
+  __device__ __forceinline__ float one(float s) const {
+    const uint64_t x = f2_pack(s, s);
+    float y0, y1;
+    f2_unpack(f2_mul(x, factor(x)), y0, y1);
+    return y0;
+  }
+  // scores in place
   template <int M>
   __device__ __forceinline__ void operator()(float (&s)[M]) const {
 #pragma unroll
     for (int i = 0; i < M; i += 2) {
-      const uint64_t x = f2_pack(s[i], s[i + 1]), w = f2_mul(x, x);
-      uint64_t y = a[N - 1];
-#pragma unroll
-      for (int k = N - 2; k >= 0; --k) y = f2_fma(w, y, a[k]);
-      f2_unpack(f2_mul(x, y), s[i], s[i + 1]);
+      const uint64_t x = f2_pack(s[i], s[i + 1]);
+      f2_unpack(f2_mul(x, factor(x)), s[i], s[i + 1]);
     }
   }
 };
@@ -78,15 +89,21 @@ __device__ __forceinline__ float cap_exact(float s, const ScoreMod& m) {
   return fmaf(-2.f * m.cap_log2, cap_r(s, m.cap_in), m.cap_log2);
 }
 
-// A warp's unscaled scores to capped ones in the log2 domain (every lane calls it).
+// The greatest |score| of a warp's, for the choice of form (a NaN stays one in each).
 template <int M>
-__device__ __forceinline__ void cap_scores(float (&s)[M], const ScoreMod& m) {
+__device__ __forceinline__ float warp_abs_max(const float (&s)[M]) {
   float big = 0.f;
 #pragma unroll
   for (int i = 0; i < M; i += 2) big = fmax3(big, fabsf(s[i]), fabsf(s[i + 1]));
-  if (!__any_sync(0xffffffffu, !(big <= m.cap_limit_b))) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+}
+
+// A warp's unscaled scores to capped ones in the log2 domain.
+template <int M>
+__device__ __forceinline__ void cap_scores(float (&s)[M], float big, const ScoreMod& m) {
+  if (big <= m.cap_limit_b) {
     CapPoly<3>(m.cap_b)(s);
-  } else if (!__any_sync(0xffffffffu, !(big <= m.cap_limit_a))) {
+  } else if (big <= m.cap_limit_a) {
     CapPoly<5>(m.cap_a)(s);
   } else {
 #pragma unroll
