@@ -16,9 +16,10 @@
 // position, and no range reduction follows: its top 32 bits (a phase within
 // 2^-33 of a turn) go to sincospif.
 //
-// Layout. A head's d elements are held by d / 8 lanes, 8 consecutive elements
-// each (16-byte accesses), so a warp takes a group of 32 / (d / 8) heads of a
-// token at a time. The pair partner of the half layout sits in another lane of
+// Layout. A head's d elements are held by d / 8 lanes, 8 elements each, so a warp
+// takes a group of 32 / (d / 8) heads of a token at a time. Forward, a lane holds two
+// chunks of 4 that are each other's partners in the half layout. Backward, it holds 8
+// consecutive elements (16-byte accesses); the partner sits in another lane of
 // the same head (rope_dim is a multiple of 16) and is exchanged by shuffles of
 // the loaded words. A warp stays with one token, walks its query heads, then its
 // key heads (then its value heads), and keeps its columns' factors in registers:
@@ -29,7 +30,9 @@
 //
 // Everything is bound by the bytes of x and y as long as a group costs few
 // instructions: a form that found token and head of every group by division ran
-// at a quarter of this one's rate.
+// at a quarter of this one's rate. At 8192 tokens, 32 + 8 heads, d = 128: forward 32.7 us
+// in bf16 (168 MB, 5.1 TB/s) and 55.9 us in fp32 (6.0 TB/s), backward 57.4 us (252 MB,
+// 4.4 TB/s: a group is still about 165 instructions there) and 89 us (5.7 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -69,6 +72,26 @@ struct Raw {
 #pragma unroll
     for (int i = 0; i < kWords / 4; ++i)
       reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+  // the same in two chunks of 4 elements
+  __device__ __forceinline__ void load(const T* a, const T* b) {
+    if constexpr (sizeof(T) == 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(a), y = *reinterpret_cast<const uint4*>(b);
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+      w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(a), y = *reinterpret_cast<const uint2*>(b);
+      w[0] = x.x; w[1] = x.y; w[2] = y.x; w[3] = y.y;
+    }
+  }
+  __device__ __forceinline__ void store(T* a, T* b) const {
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<uint4*>(a) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(b) = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+      *reinterpret_cast<uint2*>(a) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(b) = make_uint2(w[2], w[3]);
+    }
   }
   __device__ __forceinline__ Raw from_lane(int src) const {
     Raw r;
@@ -128,7 +151,67 @@ __device__ __forceinline__ void fill_table(const HeadsParams& p, float2* table, 
   for (int i = w * 32 + lane; i < p.rope_dim / 2; i += 32 * W) table[i] = cos_sin(p, position, i);
 }
 
-// This lane's place in its head, and where its elements' pair partners are.
+// Forward: this lane's two chunks of 4 elements of its head. In the rotated part's half
+// layout they are each other's partners (chunk A in the first half, B in the second);
+// past the rotated part, and interleaved, they follow each other. Against one chunk of
+// 8 and shuffles for the partners (the backward's layout): 40.0 -> 32 us at 8192 tokens, 32 +
+// 8 heads, d = 128, bf16. The backward, with its loads of two tensors and more values
+// to keep, loses what it gains (59 us with shuffles, 64 to 80 without).
+template <int D>
+struct Chunks {
+  int a, b;            // first element of each chunk
+  bool turned, halves;
+  __device__ __forceinline__ Chunks(const HeadsParams& p, int lane) {
+    const int sub = lane % (D / 8);
+    turned = sub < p.rope_dim / 8;   // rope_dim / 8 lanes hold the rotated part
+    halves = turned && !p.interleaved;
+    a = halves ? sub * 4 : sub * 8;
+    b = a + (halves ? p.rope_dim / 2 : 4);
+  }
+};
+
+// This lane's factors from its token's table: y_e = c_e x_e + s_e x_partner, with
+// the sign of the pair's side in s.
+template <int D>
+struct ChunkTurn {
+  uint64_t c[4], s[4];
+  __device__ __forceinline__ ChunkTurn(const Chunks<D>& at, const float2* table) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = f2_pack(1.f, 1.f);
+      s[i] = f2_pack(0.f, 0.f);
+    }
+    if (!at.turned) return;
+    if (at.halves) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 u = table[at.a + 2 * i], v = table[at.a + 2 * i + 1];
+        c[i] = c[i + 2] = f2_pack(u.x, v.x);
+        s[i] = f2_pack(-u.y, -v.y);
+        s[i + 2] = f2_pack(u.y, v.y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = table[at.a / 2 + i];
+        c[i] = f2_pack(t.x, t.x);
+        s[i] = f2_pack(-t.y, t.y);
+      }
+    }
+  }
+};
+
+// c x + s (partner of x), pair i of a lane's elements. kWhole: the half layout over the
+// whole head. Else x past rope_dim takes no part of another element, were it infinite.
+template <bool kWhole, int D>
+__device__ __forceinline__ uint64_t turned(const HeadsParams& p, const Chunks<D>& at,
+                                           const ChunkTurn<D>& f, const uint64_t (&x)[4], int i) {
+  const uint64_t y = f2_mul(f.c[i], x[i]);
+  if constexpr (kWhole) return f2_fma(f.s[i], x[i ^ 2], y);
+  return at.turned ? f2_fma(f.s[i], p.interleaved ? f2_swap(x[i]) : x[i ^ 2], y) : y;
+}
+
+// Backward: this lane's place in its head, and where its elements' pair partners are.
 template <int D>
 struct Place {
   int e0;            // first element
@@ -214,15 +297,16 @@ __device__ __forceinline__ float dot(const uint64_t (&a)[4], const uint64_t (&b)
 constexpr int kTokens = 8;
 // Resident blocks an SM and groups a warp has in flight (16-bit types; fp32, with
 // twice the bytes a group, half). Measured at 8192 tokens, 32 + 8 heads, d = 128,
-// bf16: forward 39.8 us with 4 blocks and 3 groups, 40.0 with 4 and 2, 43.7 with 2
-// and 8, 61.7 with 6 and 1 (registers spill); backward, persistent, 59.2 us with
-// 2 blocks and 4 groups (each a dy and an x), 66 with 2 and 3, 83 with 3 and 4.
-constexpr int kFwdBlocks = 4, kFwdFlight = 3;
+// bf16: forward 32.7 us with 4 blocks and 4 groups, 34.9 with 4 and 3, 37.7 with 3
+// and 5, 49.5 with 5 and 3 (registers spill, as they do with 4 and 4 in the appending
+// form, which takes 3); backward, persistent, 59.2 us with 2 blocks and 4 groups (each
+// a dy and an x), 66 with 2 and 3, 83 with 3 and 4.
+constexpr int kFwdBlocks = 4, kFwdFlight = 4;
 constexpr int kBwdBlocks = 2, kBwdFlight = 4;
 // Warps an SM up to which tokens are spread over more warps than one: a warp's
 // set-up (sin and cos, factors, offsets) is worth about five groups, so more
 // warps than these cost more than they hide (2000 tokens of the same heads:
-// forward 13.0 us at 16, 15.0 at 32; backward 19.6 at 8, 22.1 at 16).
+// forward 13.0 us at 16, 15.0 at 32, with three groups in flight; backward 19.6 at 8, 22.1 at 16).
 constexpr int kFwdWarps = 16, kBwdWarps = 8;
 
 // How blocks share the tokens and their head groups: a block takes `tokens`
@@ -256,11 +340,13 @@ template <typename T, int D, bool kAppend>
 __global__ void __launch_bounds__(32 * kWarpsH, kFwdBlocks)
     heads_fwd_kernel(const __grid_constant__ HeadsParams p, const Shares sh) {
   constexpr int kLanes = D / 8, kHeads = 32 / kLanes;   // lanes a head, heads a group
-  constexpr int kFlight = sizeof(T) == 4 ? (kFwdFlight + 1) / 2 : kFwdFlight;
+  constexpr int kFlight = sizeof(T) == 4 ? kFwdFlight / 2 : (kAppend ? kFwdFlight - 1 : kFwdFlight);
   constexpr int kClasses = kAppend ? 3 : 2;
   __shared__ float2 table[kTokens][D / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Place<D> at(p, lane);
+  const Chunks<D> at(p, lane);
+  const bool whole = p.rope_dim == D && !p.interleaved;
+  const int ab = at.b - at.a;
   const int hl = lane / kLanes;
   const int W = kWarpsH / sh.tokens * sh.splits;
   // this warp's token, and its number among the warps that share it
@@ -281,16 +367,18 @@ __global__ void __launch_bounds__(32 * kWarpsH, kFwdBlocks)
     const int gq = (p.Hq + kHeads - 1) / kHeads, gk = (p.Hkv + kHeads - 1) / kHeads;
     gr = Groups(w, W, c == 0 ? 0 : (c == 1 ? gq : gq + gk), heads, kHeads);
     if (!live) gr.groups = 0;
-    in = static_cast<const T*>(v.data) + b * v.sb + s * v.ss + at.e0 + (gr.start * kHeads + hl) * v.sh;
+    in = static_cast<const T*>(v.data) + b * v.sb + s * v.ss + at.a + (gr.start * kHeads + hl) * v.sh;
     in_step = v.sh * (kHeads * W);
   };
   Raw<T> raw[kFlight];
   auto load = [&](int g) {   // groups g, g + W, ...; `in` moves past them
 #pragma unroll
     for (int u = 0; u < kFlight; ++u) {
-      raw[u].zero();
-      if (g + u * W < gr.groups && (g + u * W) * kHeads + hl < heads) raw[u].load(in);
-      in += in_step;
+      if (g + u * W < gr.groups) {   // warp-uniform
+        if ((g + u * W) * kHeads + hl < heads) raw[u].load(in, in + ab);
+        else raw[u].zero();
+        in += in_step;
+      }
     }
   };
   int c = 0;
@@ -329,40 +417,43 @@ __global__ void __launch_bounds__(32 * kWarpsH, kFwdBlocks)
       out_step = static_cast<long long>(p.block_size) * D;
       store = page_row >= 0;
     }
-    out += at.e0 + (gr.start * kHeads + hl) * out_step;
+    out += at.a + (gr.start * kHeads + hl) * out_step;
     out_step *= kHeads * W;
-    Turn<D> f(p, at, table[t], 1.f);   // the factors of x and of its partner
+    ChunkTurn<D> f(at, table[t]);   // the factors of x and of its partner
     if (norm && c < 2) {
-      Raw<T> mine, other;
-      mine.load(weight + at.e0);
-      other.load(weight + at.partner);
+      Raw<T> w;
+      w.load(weight + at.a, weight + at.b);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        f.c[i] = f2_mul(f.c[i], mine.pair(i));
-        f.s[i] = f2_mul(f.s[i], p.interleaved ? f2_swap(mine.pair(i)) : other.pair(i));
+        f.c[i] = f2_mul(f.c[i], w.pair(i));
+        f.s[i] = f2_mul(f.s[i], p.interleaved ? f2_swap(w.pair(i)) : w.pair(i ^ 2));
       }
     }
-    for (int g = gr.start; g < gr.groups; g += kFlight * W, loaded = false) {
-      if (!loaded) load(g);
+    auto walk = [&](auto rotates, auto whole) {
+      for (int g = gr.start; g < gr.groups; g += kFlight * W, loaded = false) {
+        if (!loaded) load(g);
 #pragma unroll
-      for (int u = 0; u < kFlight; ++u) {
-        if (g + u * W < gr.groups) {   // warp-uniform
-          if (!kAppend || c < 2) {
-            uint64_t x[4], o[4];
+        for (int u = 0; u < kFlight; ++u) {
+          if (g + u * W < gr.groups) {   // warp-uniform
+            if constexpr (rotates.value) {
+              uint64_t x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = raw[u].pair(i);
-            partners<T, D>(p, at, raw[u], o);
-            const float r = norm ? inv_rms(head_sum<D>(dot(x, x)) * (1.f / D), p.eps) : 1.f;
-            const uint64_t rr = f2_pack(r, r);
+              for (int i = 0; i < 4; ++i) x[i] = raw[u].pair(i);
+              const float r = norm ? inv_rms(head_sum<D>(dot(x, x)) * (1.f / D), p.eps) : 1.f;
+              const uint64_t rr = f2_pack(r, r);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              raw[u].set_pair(i, f2_mul(rr, f2_fma(f.c[i], x[i], f2_mul(f.s[i], o[i]))));
+              for (int i = 0; i < 4; ++i)
+                raw[u].set_pair(i, f2_mul(rr, turned<whole.value>(p, at, f, x, i)));
+            }
+            if (store && (g + u * W) * kHeads + hl < heads) raw[u].store(out, out + ab);
+            out += out_step;
           }
-          if (store && (g + u * W) * kHeads + hl < heads) raw[u].store(out);
-          out += out_step;
         }
       }
-    }
+    };
+    if (kAppend && c == 2) walk(std::false_type{}, std::false_type{});
+    else if (whole) walk(std::true_type{}, std::true_type{});
+    else walk(std::true_type{}, std::false_type{});
     if (++c >= kClasses) break;
     enter(c);
   }
@@ -397,7 +488,10 @@ __global__ void __launch_bounds__(32 * kWarpsH, kBwdBlocks)
     const int b = live ? static_cast<int>(token / p.S) : 0;
     const int s = live ? static_cast<int>(token - static_cast<unsigned>(b) * p.S) : 0;
     if (live) fill_table(p, table[flip][t], p.positions ? p.positions[token] : s, lane, w, W);
-    __syncthreads();   // the other table's readers are past it when this one is written again
+    // a token of one warp has a table of its own; else the other table's readers are
+    // past it when this one is written again
+    if (W == 1) __syncwarp();
+    else __syncthreads();
     if (!live) continue;
     const Turn<D> turn(p, at, table[flip][t], -1.f);
 #pragma unroll
