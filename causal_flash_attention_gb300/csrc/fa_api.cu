@@ -435,8 +435,8 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* out, const
     pre.key_end = mod->key_end;
     p.spans = pre.spans = reinterpret_cast<int2*>(wsb + sws.spans);
     p.plan = pre.plan = reinterpret_cast<int2*>(wsb + sws.plan);
-    // a list for up to four items an SM: 512 items of documents take 298 us with it
-    // and 326 without, 768 short items of a window 66.4 and 63.0
+    // a list for up to four items an SM: 512 items of documents take 295 us with it
+    // and 319 without, 768 short items of a window 63.9 and 60.4
     const long long tiles = static_cast<long long>(B) * pre.n_kv_tiles;
     p.listed = tiles <= kListTiles && tiles * Hkv <= 4 * kDecodeWaveCtas;
     p.n_slots = kDecodeWaveCtas;

@@ -52,12 +52,22 @@
 // Span form (kSpan): query row i sees the keys of its own span. Extra blocks of
 // the pre-pass clamp and pad the spans and find, for every key tile, the first
 // and last query tile with a row whose span reaches into it; an item walks that
-// range, or with a work list (span_plan.cuh) a slice of it. The mask of a warp's 32 key rows against its 64 query columns is formed
-// as one word per column and transposed across the warp, so that each key row
-// holds its own 64 bits; tiles that every span covers skip it. With a cap, dS =
-// P (1 - tanh^2) (dP - D): the product P (1 - tanh^2) is kept, rounded to 16
-// bits as P itself is, in place of P, so it costs no registers. A row that sees
-// nothing has LSE = -inf and takes part with P = 0.
+// range, or with a work list (span_plan.cuh) a slice of it. The mask of a warp's 32
+// key rows against its 64 query columns is formed as one word per column and
+// transposed across the warp, so that each key row holds its own 64 bits; tiles that
+// every span covers skip it. A row that sees nothing has LSE = -inf and takes part
+// with P = 0.
+//
+// dS = P (dP - D) takes P as dV does, rounded to 16 bits: packed, it waits for dP in
+// half the registers, which are all in use. dQ and dK come out with a relative error
+// (root mean square) of 3.0e-3 in bf16, from this rounding, that of dS for its
+// products and that of the result, about 1.7e-3 each. With a cap, dS = P (1 -
+// tanh^2) (dP - D): the product P (1 - tanh^2) is kept in place of P.
+//
+// Measured at 8192 causal spans, 32 + 8 heads, d = 128, bf16: 1239 us (1109
+// TFLOP/s; the causal form 1221), with a bias 1382, with a cap 1736; packed documents
+// 293 us, 42 of them the pre-pass and 26 the convert pass. Bound by the compute warps'
+// phases: a step of 128 x 128 takes 2.8 us at d = 128, 4 with a cap.
 #include <algorithm>
 #include <type_traits>
 
