@@ -161,6 +161,18 @@ def test_a_bad_row_stays_its_own(fa):
     assert torch.equal(got[0][same], clean[0][same]) and torch.equal(got[1], clean[1])
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_infinity_past_the_rotated_part_stays_where_it_is(fa, interleaved):
+    q, k, _, w = make(1, 2, 1, 5, 64, "fp16", False, "packed", 8)
+    turns = fa.rope_turns(freqs(32), DEV)
+    clean = fa.qk_norm_rope_forward(q, k, turns, interleaved=interleaved)
+    q, k = q.clone(), k.clone()
+    q[0, 1, 3, 40], k[0, 0, 2, 63] = float("inf"), float("-inf")
+    got = fa.qk_norm_rope_forward(q, k, turns, interleaved=interleaved)
+    clean[0][0, 1, 3, 40], clean[1][0, 0, 2, 63] = float("inf"), float("-inf")
+    assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
+
+
 # ------------------------------------------------------------------ append --
 def cache(nb, Hkv, bs, d, dtype):
     return torch.full((nb, Hkv, bs, d), 9.0, dtype=DT[dtype], device=DEV)
@@ -215,6 +227,26 @@ def test_append_outside_the_cache_stores_nothing(fa):
                            q_weight=w[0], k_weight=w[1])
     torch.cuda.synchronize()
     assert (kc == 9.0).all() and (vc == 9.0).all()
+
+
+def test_pages_past_two_to_the_31_elements(fa):
+    """The same step on a cache whose pages lie past 2^31 elements, and on a small one."""
+    Hkv, d, bs, lens = 8, 128, 64, [130, 64]
+    q, k, v, w = make(2, 16, Hkv, 1, d, "bf16", True, "packed", 11)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    turns = fa.rope_turns(freqs(d), DEV)
+    small = [torch.randn(4, Hkv, bs, d, generator=torch.Generator().manual_seed(i)).to(q) for i in (1, 2)]
+    nb = (1 << 31) // (Hkv * bs * d) + 50
+    big = [torch.empty(nb, Hkv, bs, d, dtype=q.dtype, device=DEV) for _ in range(2)]
+    for s, t in zip(small, big):
+        t[nb - 4:] = s
+    table = torch.tensor([[2, 0, 3], [1, -1, -1]], dtype=torch.int32, device=DEV)
+    got = [fa.decode_step_ragged(q, k, v, *c, t, n, turns, w[0], w[1])
+           for c, t in ((small, table), (big, torch.where(table < 0, table, table + nb - 4)))]
+    torch.cuda.synchronize()
+    assert fa.fa_last_device_status() == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert all(torch.equal(t[nb - 4:], s) for s, t in zip(small, big))
 
 
 # ---------------------------------------------------------------- together --

@@ -110,6 +110,18 @@ def test_scores_far_beyond_the_cap(fa):
     compare(run(fa, *x, begin, end, 2.0, None, 1.0), *x, begin, end, 2.0, None, 1.0)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("most", [0.02, 0.29, 0.31, 0.74, 0.76, 4.0])
+def test_scores_on_both_sides_of_the_cap_forms(fa, d, most):
+    """The greatest |score| just inside and outside 0.3 and 0.75 of the cap, where the capping
+    changes form; whole tiles and, at the last keys, partly masked ones."""
+    x = inputs(1, 2, 1, 130, 390, d, "bf16", 8)
+    s = torch.einsum("bhid,bhjd->bhij", x[0].float(), x[1].float().repeat_interleave(2, 1))
+    scale = most * 10.0 / s.abs().max().item()
+    begin, end = fa.key_spans(1, 130, 390, kv_lens=389, causal=False)
+    compare(run(fa, *x, begin, end, 10.0, None, scale), *x, begin, end, 10.0, None, scale)
+
+
 def test_steep_distance_bias_far_from_the_row(fa):
     """A bias of -40 a key over 3000 keys: far tiles underflow, the nearest keys decide."""
     x = inputs(1, 1, 1, 40, 3001, 64, "bf16", 7)
