@@ -178,7 +178,8 @@ struct Segments {
       int units = units_of(keys.n);
       while (cur >= (pre + units) * p.Hkv) {   // cur < end <= total: some later b has units
         pre += units;
-        keys = seq_keys(p, ++b);
+        if (++b >= p.B) return false;   // only if the lengths changed meanwhile
+        keys = seq_keys(p, b);
         units = units_of(keys.n);
       }
       const int off = cur - pre * p.Hkv;

@@ -298,8 +298,9 @@ int fa_qk_norm_rope_append(const fa_view* q, const fa_view* k, const fa_view* v,
  * with scores capped and biased as by fa_fwd_span (distance p - j). A row that
  * sees no key (p < 0) gets out = 0 and lse = -infinity.
  *
- * The lengths are read on the device only: the call needs no host copy of
- * them, and a captured graph may be replayed after they change. All key tiles
+ * The lengths are read on the device only, and must not change while the call
+ * runs: it needs no host copy of them, and a captured graph may be replayed
+ * after they change. All key tiles
  * of all sequences are shared out evenly over one wave of CTAs whatever the
  * lengths are. Results are the same bits on every call.
  *
