@@ -852,6 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t o_tmem = tmem + lane_off + 64;
     const bool cap = p.cap_in != 0.f;
+    const bool same_rows = p.Sq == 1 && !p.slopes;   // rows do not differ in position or slope
     const float c = p.scale_log2;
     float* row_slope = reinterpret_cast<float*>(smem + Cfg::kOffRow);          // log2 domain
     int* row_s = reinterpret_cast<int*>(smem + Cfg::kOffRow + NR * 4);         // token of the row
@@ -907,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tile0 = seg.tile0;
       const int pos0 = keys.len - p.Sq;   // position of row s = 0
       // rows' slopes and tokens (the readers of the segment before are past its last vote)
-      if (tid < NR) {
+      if (!same_rows && tid < NR) {
         const int gq = min(tid, p.R - 1) / p.Sq;
         row_s[tid] = tid < p.R ? tid - gq * p.Sq : 0;
         row_slope[tid] = p.slopes ? p.slopes[kvh * p.G + gq] * kLog2eR : 0.f;
@@ -944,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int r = 0; r < NR; ++r) x[r] *= c;
         }
-        if (j == 0) row_warps_any(false);   // row_slope and row_s are written
+        if (j == 0 && !same_rows) row_warps_any(false);   // row_slope and row_s are written
         if (p.slopes) {
 #pragma unroll
           for (int r = 0; r < NR; ++r)
@@ -954,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kv0 + kTileN > pos0 + 1 || (p.window > 0 && kv0 < pos0 + p.Sq - p.window)) {
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            const int pos = pos0 + row_s[r];
+            const int pos = same_rows ? pos0 : pos0 + row_s[r];
             if (key > pos || (p.window > 0 && key <= pos - p.window)) x[r] = -INFINITY;
           }
         }
@@ -967,7 +968,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float over = -INFINITY;   // how far a score exceeds its row's reference
 #pragma unroll
         for (int r = 0; r < NR; ++r) over = fmaxf(over, x[r] - m[r]);
-        if (row_warps_any(over > kRescaleThresholdR || !ok)) {
+        // (a segment's first tile sets them; the last vote, at the end of the segment
+        // before, was after the last use of `red`)
+        if (j == 0 || row_warps_any(over > kRescaleThresholdR || !ok)) {
           // move every row's reference to its maximum so far
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
