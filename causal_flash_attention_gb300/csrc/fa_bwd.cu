@@ -211,6 +211,8 @@ __global__ void __launch_bounds__(256, 8) bwd_pre_kernel(const BwdPreParams p) {
   // grid's completion before it reads anything this pass writes
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if constexpr (kSpan) {
+    // itself the dependent of whatever runs before (the forward, often)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (static_cast<int>(blockIdx.x) < p.n_plan_blocks) {
       bwd_plan(p);
       return;
@@ -1147,25 +1149,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 }
 
-// Launch as the programmatic dependent of the kernel before it on the stream:
-// the new grid may start before that one completes and synchronizes with it
-// through griddepcontrol.wait.
-template <typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem,
-                             cudaStream_t stream, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int D, bool kBf16, int kSpan = 0>
 cudaError_t launch_bwd_impl(const BwdParams& p, cudaStream_t stream) {
   constexpr int smem = kSpan ? BwdCfg<D>::kSmemBytesSpan : BwdCfg<D>::kSmemBytes;
@@ -1208,9 +1191,8 @@ cudaError_t launch_bwd_pre_span(const BwdPreParams& p0, cudaStream_t stream) {
   BwdPreParams p = p0;
   p.n_plan_blocks = p.B * ((p.n_kv_tiles + kPlanTiles - 1) / kPlanTiles);
   const unsigned grid = pre_row_blocks(p) + static_cast<unsigned>(p.n_plan_blocks);
-  if (p.dtype == 1) bwd_pre_kernel<__half, true><<<grid, 256, 0, stream>>>(p);
-  else bwd_pre_kernel<__nv_bfloat16, true><<<grid, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(p.dtype == 1 ? bwd_pre_kernel<__half, true> : bwd_pre_kernel<__nv_bfloat16, true>,
+                          dim3(grid), dim3(256), 0, stream, p);
 }
 
 cudaError_t launch_bwd_span(const BwdParams& p, int d, bool bf16, cudaStream_t stream) {

@@ -185,7 +185,10 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
   // the CTA's rows (known after the set-up barrier below)
   int row_lo = 0, row_hi = 0, tile0 = 0;
   if constexpr (kSpan) {
+    // programmatic dependent of the kernel before: every warp that reads or writes
+    // global memory waits for it (the set-up below does not)
     if (warp >= 2) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       const int row = unit * kTileM + (warp & 3) * 32 + lane;
       if (row < p.Sq) {
         const size_t at = static_cast<size_t>(b) * p.Sq + row;
@@ -224,6 +227,7 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
     fence_mbar_init();
     if constexpr (kSpan) {
       // the queries are on their way while the spans are read
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       mbar_arrive_expect_tx(bars.q_full, Cfg::kTileBytes);
       for (int c = 0; c < Cfg::kChunks; ++c)
         tma_load_3d(sbase + Cfg::kOffQ + c * (kTileM * 128), &p.tm_q, bars.q_full, c * kChunk,
@@ -240,6 +244,7 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (kSpan) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if constexpr (kSpan) {
     const int4 a = *reinterpret_cast<const int4*>(smem + Cfg::kOffSpan);
     const int4 c = *reinterpret_cast<const int4*>(smem + Cfg::kOffSpan + 16);
@@ -649,6 +654,8 @@ cudaError_t launch_fwd_impl(const FwdParams& p0, cudaStream_t stream) {
   p.n_units = (p.Sq + T * kTileM - 1) / (T * kTileM);   // T query tiles per CTA
   const unsigned grid =
       static_cast<unsigned>(static_cast<long long>(p.B) * p.Hq * p.n_units);   // < 2^31
+  if (kSpan)
+    return launch_dependent(kernel, dim3(grid), dim3(FwdCfg<D, T>::kThreads), smem, stream, p);
   kernel<<<grid, FwdCfg<D, T>::kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }

@@ -40,6 +40,7 @@
 #include <type_traits>
 
 #include "fa_heads.h"
+#include "fa_internal.h"
 #include "ptx.cuh"
 
 namespace fa {
@@ -124,6 +125,13 @@ __device__ __forceinline__ uint64_t f2_swap(uint64_t v) {
   float a, b;
   f2_unpack(v, a, b);
   return f2_pack(b, a);
+}
+
+// In front of a kernel's first access to memory: lets the next kernel on the stream
+// set itself up, and waits for the one before.
+__device__ __forceinline__ void start_dependent() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // (mean x^2 + eps)^(-1/2), the sum at least the least normal number: with eps = 0 a
@@ -356,6 +364,7 @@ __global__ void __launch_bounds__(32 * kWarpsH, kFwdBlocks)
   const bool live = token < static_cast<unsigned>(p.B) * p.S;
   const int b = live ? static_cast<int>(token / p.S) : 0;
   const int s = live ? static_cast<int>(token - static_cast<unsigned>(b) * p.S) : 0;
+  start_dependent();
 
   const T* in;
   long long in_step;   // between groups of the warp
@@ -477,6 +486,7 @@ __global__ void __launch_bounds__(32 * kWarpsH, kBwdBlocks)
   const int W = kWarpsH / sh.tokens;
   const int t = warp >> sh.log2_warps, w = warp & (W - 1);
   const bool norm = p.wq != nullptr;
+  start_dependent();
   uint64_t dw[2][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) dw[0][i] = dw[1][i] = f2_pack(0.f, 0.f);
@@ -590,6 +600,7 @@ __global__ void __launch_bounds__(32 * kWarpsH, kBwdBlocks)
 __global__ void __launch_bounds__(256) heads_dw_kernel(const __grid_constant__ HeadsParams p) {
   __shared__ float part[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  start_dependent();
   const int c = blockIdx.x * 32 + lane;
   float t = 0.f;
   for (int i = warp; i < p.n_blocks; i += 8) t += p.dw_part[static_cast<size_t>(i) * 2 * p.d + c];
@@ -626,18 +637,16 @@ cudaError_t launch_fwd_impl(const HeadsParams& p, cudaStream_t stream) {
   Shares sh(tokens_per_block(tokens, groups, kFwdWarps), 1);
   if (sh.tokens == 1 && tokens < kSms) sh.splits = std::min((groups + kWarpsH - 1) / kWarpsH, 65535);
   const dim3 grid(static_cast<unsigned>((tokens + sh.tokens - 1) / sh.tokens), sh.splits);
-  heads_fwd_kernel<T, D, kAppend><<<grid, 32 * kWarpsH, 0, stream>>>(p, sh);
-  return cudaGetLastError();
+  return launch_dependent(heads_fwd_kernel<T, D, kAppend>, grid, dim3(32 * kWarpsH), 0, stream, p, sh);
 }
 
 template <typename T, int D>
 cudaError_t launch_bwd_impl(const HeadsParams& p, cudaStream_t stream) {
   const Shares sh(heads_bwd_tokens(p.B, p.Hq, p.Hkv, p.S, p.d), 1);
-  heads_bwd_kernel<T, D><<<static_cast<unsigned>(p.n_blocks), 32 * kWarpsH, 0, stream>>>(p, sh);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(heads_bwd_kernel<T, D>, dim3(static_cast<unsigned>(p.n_blocks)),
+                                         dim3(32 * kWarpsH), 0, stream, p, sh);
   if (e != cudaSuccess || !p.wq) return e;
-  heads_dw_kernel<<<2 * D / 32, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(heads_dw_kernel, dim3(2 * D / 32), dim3(256), 0, stream, p);
 }
 
 template <bool kAppend>

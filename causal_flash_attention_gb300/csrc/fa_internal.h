@@ -9,6 +9,26 @@
 
 namespace fa {
 
+// Launch as the programmatic dependent of the kernel before it on the stream:
+// the new grid may start before that one completes and synchronizes with it
+// through griddepcontrol.wait, in front of its first access to memory. (A kernel that
+// lets its dependents start early has all its blocks resident by then.)
+template <typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Tile geometry shared by the tensor-core kernels: 128 query rows per tile,
 // 128 key/value rows per tile, 64-element (128-byte) column chunks.
 constexpr int kTileM = 128;

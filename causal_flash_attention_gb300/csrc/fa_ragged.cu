@@ -1140,28 +1140,11 @@ __global__ void __launch_bounds__(32 * kMergeRows) ragged_merge_kernel(const __g
   if (lane == 0) p.lse[row] = L > 0.f ? (M + __log2f(L)) * kLn2R : -INFINITY;
 }
 
-// Launch as the programmatic dependent of the kernel before on the stream.
-template <class Kernel>
-cudaError_t launch_dependent(Kernel kernel, unsigned grid, unsigned block, size_t smem,
-                             const RaggedParams& p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 template <int smem, class Kernel>
 cudaError_t launch_main(Kernel kernel, const RaggedParams& p, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kernel, static_cast<unsigned>(p.n_ctas), kThreads, smem, p, stream);
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(p.n_ctas)), dim3(kThreads), smem, stream, p);
 }
 
 template <int D, bool kBf16>
@@ -1178,8 +1161,8 @@ cudaError_t launch_ragged_impl(const RaggedParams& p, cudaStream_t stream) {
   // the merge overlaps its launch with the ragged kernel's tail
   const long long rows = static_cast<long long>(p.B) * p.Hq * p.Sq;
   return launch_dependent(ragged_merge_kernel<Elem, D / 32>,
-                          static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows),
-                          32 * kMergeRows, 0, p, stream);
+                          dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows)),
+                          dim3(32 * kMergeRows), 0, stream, p);
 }
 
 }  // namespace
