@@ -30,9 +30,9 @@
 //
 // Everything is bound by the bytes of x and y as long as a group costs few
 // instructions: a form that found token and head of every group by division ran
-// at a quarter of this one's rate. At 8192 tokens, 32 + 8 heads, d = 128: forward 32.7 us
-// in bf16 (168 MB, 5.1 TB/s) and 55.9 us in fp32 (6.0 TB/s), backward 57.4 us (252 MB,
-// 4.4 TB/s: a group is still about 165 instructions there) and 89 us (5.7 TB/s).
+// at a quarter of this one's rate. At 8192 tokens, 32 + 8 heads, d = 128: forward 32.4 us
+// in bf16 (168 MB, 5.2 TB/s) and 55.3 us in fp32 (6.1 TB/s), backward 56.7 us (252 MB,
+// 4.4 TB/s: a group is still about 165 instructions there) and 88.5 us (5.7 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -127,10 +127,9 @@ __device__ __forceinline__ uint64_t f2_swap(uint64_t v) {
   return f2_pack(b, a);
 }
 
-// In front of a kernel's first access to memory: lets the next kernel on the stream
-// set itself up, and waits for the one before.
-__device__ __forceinline__ void start_dependent() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+// In front of a kernel's first access to memory: programmatic dependent of the kernel
+// before on the stream.
+__device__ __forceinline__ void wait_for_kernel_before() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
@@ -364,7 +363,11 @@ __global__ void __launch_bounds__(32 * kWarpsH, kFwdBlocks)
   const bool live = token < static_cast<unsigned>(p.B) * p.S;
   const int b = live ? static_cast<int>(token / p.S) : 0;
   const int s = live ? static_cast<int>(token - static_cast<unsigned>(b) * p.S) : 0;
-  start_dependent();
+  wait_for_kernel_before();
+  // Where the grid leaves room on every SM, the next kernel's blocks may take their
+  // places beside this one's (16 tokens into the cache: 4.0 us a call, 4.3 without); with
+  // more blocks they would fill the SMs unevenly (3075 tokens: 8.5 us, 7.4 without).
+  if (gridDim.x * gridDim.y <= kSms) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const T* in;
   long long in_step;   // between groups of the warp
@@ -486,7 +489,7 @@ __global__ void __launch_bounds__(32 * kWarpsH, kBwdBlocks)
   const int W = kWarpsH / sh.tokens;
   const int t = warp >> sh.log2_warps, w = warp & (W - 1);
   const bool norm = p.wq != nullptr;
-  start_dependent();
+  wait_for_kernel_before();
   uint64_t dw[2][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) dw[0][i] = dw[1][i] = f2_pack(0.f, 0.f);
@@ -600,7 +603,7 @@ __global__ void __launch_bounds__(32 * kWarpsH, kBwdBlocks)
 __global__ void __launch_bounds__(256) heads_dw_kernel(const __grid_constant__ HeadsParams p) {
   __shared__ float part[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  start_dependent();
+  wait_for_kernel_before();
   const int c = blockIdx.x * 32 + lane;
   float t = 0.f;
   for (int i = warp; i < p.n_blocks; i += 8) t += p.dw_part[static_cast<size_t>(i) * 2 * p.d + c];
