@@ -282,6 +282,57 @@ def test_training_step_of_an_attention_layer(fa):
         check("dw", gw, dw, dw_tol)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_steps_back_to_back_over_the_same_buffers(fa, captured):
+    """Training steps one after the other without a wait, every step over the same intermediate
+    buffers and workspaces, each kernel set up beside the one before: the same results as step
+    by step (dq is summed in any order, all that does not depend on it has the same bits)."""
+    B, Hq, Hkv, S, d, steps = 1, 4, 2, 260, 128, 12
+    turns = fa.rope_turns(freqs(d), DEV)
+    begin, end = fa.key_spans(B, S, window=100, device=DEV)
+    xs = [make(B, Hq, Hkv, S, d, "bf16", True, "packed", 20 + i) for i in range(steps)]
+    e = lambda H, *s: torch.empty(B, H, *s, dtype=torch.bfloat16, device=DEV)
+    qr, kr, out, dq, dk, dv = e(Hq, S, d), e(Hkv, S, d), e(Hq, S, d), e(Hq, S, d), e(Hkv, S, d), e(Hkv, S, d)
+    lse = torch.empty(B, Hq, S, device=DEV)
+    ws = torch.empty(fa.fa_bwd_span_workspace_bytes(B, Hq, Hkv, S, S, d), dtype=torch.uint8, device=DEV)
+    ws2 = torch.empty(fa.fa_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hkv, S, d), dtype=torch.uint8, device=DEV)
+    do = torch.randn(B, Hq, S, d, generator=torch.Generator().manual_seed(1)).to(out)
+
+    def step(x, r):
+        q, k, v, w = x
+        fa.fa_qk_norm_rope(q, k, qr, kr, turns, None, *w)
+        fa.fa_fwd_span(qr, kr, r["v"], begin, end, out, lse, 20.0)
+        fa.fa_bwd_span(qr, kr, r["v"], begin, end, out, do, lse, dq, dk, dv, ws, 20.0)
+        fa.fa_qk_norm_rope_bwd(dq, dk, q, k, r["dq"], r["dk"], r["dwq"], r["dwk"], ws2, turns, None, *w)
+
+    def results():
+        return [dict(v=x[2].contiguous(), dq=e(Hq, S, d), dk=e(Hkv, S, d),
+                     dwq=torch.empty(d, device=DEV), dwk=torch.empty(d, device=DEV)) for x in xs]
+
+    want, got = results(), results()
+    for x, r in zip(xs, want):
+        step(x, r)
+        torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for x, r in zip(xs, got):
+                step(x, r)
+        for _ in range(3):
+            graph.replay()
+    else:
+        for _ in range(3):
+            for x, r in zip(xs, got):
+                step(x, r)
+    torch.cuda.synchronize()
+    assert fa.fa_last_device_status() == 0
+    for a, b in zip(got, want):
+        assert torch.equal(a["dk"], b["dk"]) and torch.equal(a["dwk"], b["dwk"])
+        # one rounding of bf16 each way where the sums of dq differ in their last bits
+        most = b["dq"].float().abs().max().item()
+        assert (a["dq"].float() - b["dq"].float()).abs().max().item() <= 2 * 2.0 ** -8 * most
+
+
 def test_serving_loop(fa):
     """Prompts of unequal length into the cache, then steps of new tokens, captured once and
     replayed: every step against the 64-bit definition on the cache as it stands."""
