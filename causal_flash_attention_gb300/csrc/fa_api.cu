@@ -188,7 +188,7 @@ SplitPlan split_plan(int B, int Hq, int Hkv, int Sq, int Skv, int d, int n_split
 // hold that many key tiles), two partial results a CTA.
 struct RaggedPlan {
   int n_ctas, R;
-  size_t part_out, part_lse2, prefix, total;
+  size_t part_out, part_lse2, starts, total;
 };
 
 RaggedPlan ragged_plan(int B, int Hq, int Hkv, int Sq, int d, int block_size, int max_blocks) {
@@ -201,8 +201,8 @@ RaggedPlan ragged_plan(int B, int Hq, int Hkv, int Sq, int d, int block_size, in
   const long long rows = 2LL * rp.n_ctas * rp.R;
   rp.part_out = 0;
   rp.part_lse2 = static_cast<size_t>(round_up(rows * d * 4, 256));
-  rp.prefix = rp.part_lse2 + static_cast<size_t>(round_up(rows * 4, 256));
-  rp.total = rp.prefix + static_cast<size_t>(round_up((B + 1LL) * 4, 256));
+  rp.starts = rp.part_lse2 + static_cast<size_t>(round_up(rows * 4, 256));
+  rp.total = rp.starts + static_cast<size_t>(round_up(rp.n_ctas * 16LL, 256));
   return rp;
 }
 
@@ -887,7 +887,7 @@ int fa_fwd_ragged_paged(const void* q, const void* k_cache, const void* v_cache,
   p.slopes = slopes;
   p.part_out = reinterpret_cast<float*>(wsb + rp.part_out);
   p.part_lse2 = reinterpret_cast<float*>(wsb + rp.part_lse2);
-  p.prefix = reinterpret_cast<int*>(wsb + rp.prefix);
+  p.starts = reinterpret_cast<int4*>(wsb + rp.starts);
   p.capacity = static_cast<int>(std::min(static_cast<long long>(max_blocks) * block_size, 0x7fffff80LL));
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Sq = Sq;
   p.G = Hq / Hkv;

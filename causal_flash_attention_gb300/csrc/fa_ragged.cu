@@ -108,8 +108,9 @@ struct ShareOut {
   }
 };
 
-// A CTA's share, found by all its threads: a scan over the sequences' units. CTA
-// 0 also writes the sums for the merge. Two barriers.
+// A CTA's share, found by all its threads: a scan over the sequences' units. Where it
+// begins is also written for the merge: (sequence, units per head before it, its units,
+// units of all sequences per head). Two barriers.
 struct Share {
   int begin, end;    // units of the list
   int b, pre;        // the first unit's sequence, and units per head before it
@@ -149,11 +150,11 @@ __device__ __forceinline__ Share find_share(const RaggedParams& p, int cta, int*
     if (s.begin < s.end && pre * p.Hkv <= s.begin && s.begin < (pre + n) * p.Hkv) {
       scan[6] = b;
       scan[7] = pre;
+      p.starts[cta] = make_int4(b, pre, n, total);
     }
-    if (cta == 0) p.prefix[b] = pre;
     pre += n;
-    if (cta == 0 && b == p.B - 1) p.prefix[p.B] = pre;
   }
+  if (total == 0 && cta == 0 && threadIdx.x == 0) p.starts[0] = make_int4(0, 0, 0, 0);
   __syncthreads();
   s.b = s.begin < s.end ? scan[6] : 0;
   s.pre = s.begin < s.end ? scan[7] : 0;
@@ -1061,10 +1062,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ merge --
-// One warp per output row (b, hq, s); each lane owns d / 32 columns. Joins the
-// parts of rows whose tiles lie in more than one share, in share order, as the
-// split-KV merge does; writes out = 0, LSE = -inf for sequences without keys;
-// leaves rows that one segment wrote whole alone.
+// Joins the parts of (sequence, head)s whose tiles lie in more than one share, in
+// share order, as the split-KV merge does: block (c, y) takes rows [kMergeRows y,
+// + kMergeRows) of the one whose second part is in share c, one warp a row, each
+// lane d / 32 columns. So the grid goes by the shares, not by the batch (128
+// sequences of 512 keys, 32 heads: 60.7 us a call with a warp for each of the 4096
+// rows, most of which one segment has written whole). Also writes out = 0, LSE = -inf
+// for sequences without keys.
 constexpr int kMergeRows = 4;     // rows (warps) a block: fits beside the ragged kernel's CTA
 constexpr int kMergeBatch = 20;   // 152 shares of one sequence with 8 heads: 20 parts a head
 template <int PER>
@@ -1079,55 +1083,61 @@ __global__ void __launch_bounds__(32 * kMergeRows) ragged_merge_kernel(const __g
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int D = 32 * PER;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * kMergeRows + warp;   // (b * Hq + hq) * Sq + s
-  if (row >= static_cast<long long>(p.B) * p.Hq * p.Sq) return;
-  const int s = static_cast<int>(row % p.Sq);
-  const long long bh = row / p.Sq;
-  const int hq = static_cast<int>(bh % p.Hq), b = static_cast<int>(bh / p.Hq);
-  const int all = p.prefix[p.B], pre = p.prefix[b], units = p.prefix[b + 1] - pre;
-  T* dst = static_cast<T*>(p.out) + row * D + lane * PER;
-  if (units == 0) {
+  const int c = static_cast<int>(blockIdx.x);
+  if (blockIdx.y == 0) {
+    for (int b = c; b < p.B; b += static_cast<int>(gridDim.x)) {
+      if (seq_keys(p, b).n > 0) continue;
+      const long long rows = static_cast<long long>(p.Hq) * p.Sq;
+      for (long long i = warp; i < rows; i += kMergeRows) {
+        const long long row = b * rows + i;
+        T* dst = static_cast<T*>(p.out) + row * D + lane * PER;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) dst[e] = static_cast<T>(0.f);
-    if (lane == 0) p.lse[row] = -INFINITY;
-    return;
+        for (int e = 0; e < PER; ++e) dst[e] = static_cast<T>(0.f);
+        if (lane == 0) p.lse[row] = -INFINITY;
+      }
+    }
   }
-  const ShareOut out(p.n_ctas, all * p.Hkv);
-  const int u0 = pre * p.Hkv + hq / p.G * units;   // this head's units: [u0, u0 + units)
+  const int r = static_cast<int>(blockIdx.y) * kMergeRows + warp;
+  const int total = p.starts[0].w;
+  const int4 start = p.starts[c];   // without meaning past the shares
+  const ShareOut out(p.n_ctas, total * p.Hkv);
+  if (c == 0 || c >= out.shares || r >= p.R) return;
+  const int b = start.x, units = start.z;
+  const int kvh = (out.begin(c) - start.y * p.Hkv) / units;
+  const int u0 = start.y * p.Hkv + kvh * units;   // this head's units: [u0, u0 + units)
   const int c0 = out.of_unit(u0 + kSegmentUnits), c1 = out.of_unit(u0 + units - 1);
-  if (c0 == c1) return;
-  const int r = (hq % p.G) * p.Sq + s;
+  if (c != c0 + 1 || c0 == c1) return;
   // the parts are the first segments of their shares, but for that of c0 when
   // its share begins before this head's units (and so with another's tiles)
   const bool tail0 = out.begin(c0) < u0;
-  auto part = [&](int c) {
-    return (static_cast<size_t>(c) * 2 + ((c == c0 && tail0) ? 1 : 0)) * p.R + r;
+  auto part = [&](int i) {
+    return (static_cast<size_t>(i) * 2 + ((i == c0 && tail0) ? 1 : 0)) * p.R + r;
   };
   // Bound by latency (a few KB a row): a batch's loads go out together, the first
   // batch's with those of the maximum over all parts.
   PartVec<PER> v[kMergeBatch];
   float lv[kMergeBatch];
-  auto load = [&](int c) {
+  auto load = [&](int i) {
 #pragma unroll
     for (int k = 0; k < kMergeBatch; ++k)
-      if (c + k <= c1) {
-        const size_t at = part(c + k);
+      if (i + k <= c1) {
+        const size_t at = part(i + k);
         v[k] = reinterpret_cast<const PartVec<PER>*>(p.part_out + at * D)[lane];
         lv[k] = p.part_lse2[at];
       }
   };
   load(c0);
   float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_lse2[part(c)]);
+  for (int i = c0 + lane; i <= c1; i += 32) M = fmaxf(M, p.part_lse2[part(i)]);
   M = warp_max(M);
   float acc[PER], L = 0.f;
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  for (int c = c0; c <= c1; c += kMergeBatch) {
-    if (c > c0) load(c);
+  for (int i = c0; i <= c1; i += kMergeBatch) {
+    if (i > c0) load(i);
 #pragma unroll
     for (int k = 0; k < kMergeBatch; ++k)
-      if (c + k <= c1) {
+      if (i + k <= c1) {
         const float w = M != -INFINITY ? ex2(lv[k] - M) : 0.f;
         L += w;
 #pragma unroll
@@ -1135,6 +1145,9 @@ __global__ void __launch_bounds__(32 * kMergeRows) ragged_merge_kernel(const __g
       }
   }
   const float inv = L > 0.f ? 1.f / L : 0.f;
+  const int gq = r / p.Sq;
+  const long long row = (static_cast<long long>(b) * p.Hq + kvh * p.G + gq) * p.Sq + r - gq * p.Sq;
+  T* dst = static_cast<T*>(p.out) + row * D + lane * PER;
 #pragma unroll
   for (int e = 0; e < PER; ++e) dst[e] = static_cast<T>(acc[e] * inv);
   if (lane == 0) p.lse[row] = L > 0.f ? (M + __log2f(L)) * kLn2R : -INFINITY;
@@ -1159,9 +1172,9 @@ cudaError_t launch_ragged_impl(const RaggedParams& p, cudaStream_t stream) {
     e = launch_main<RagCfg<D>::kSmemBytes>(fa_ragged_kernel<D, kBf16>, p, stream);
   if (e != cudaSuccess) return e;
   // the merge overlaps its launch with the ragged kernel's tail
-  const long long rows = static_cast<long long>(p.B) * p.Hq * p.Sq;
   return launch_dependent(ragged_merge_kernel<Elem, D / 32>,
-                          dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows)),
+                          dim3(static_cast<unsigned>(p.n_ctas),
+                               static_cast<unsigned>((p.R + kMergeRows - 1) / kMergeRows)),
                           dim3(32 * kMergeRows), 0, stream, p);
 }
 

@@ -20,7 +20,7 @@ struct RaggedParams {
   const float* slopes;      // [Hq] or null
   float* part_out;    // [2 * CTAs][R][d] fp32 out = O / l of a part of a (sequence, head)
   float* part_lse2;   // [2 * CTAs][R]    its log2-sum-exp2 of scaled scores
-  int* prefix;        // [B + 1] units per head before sequence b, written by CTA 0
+  int4* starts;       // [CTAs] where each CTA's share begins, written by it (find_share)
   int B, Hq, Hkv, Sq, G, R;
   int block_size, box_rows, max_blocks, num_blocks;
   int capacity;       // keys a table row can hold (at most 2^31 - 128)

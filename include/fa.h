@@ -324,7 +324,7 @@ int fa_fwd_ragged_paged(const void* q, const void* k_cache, const void* v_cache,
                         size_t workspace_bytes, fa_stream_t stream);
 
 /* Workspace bytes of fa_fwd_ragged_paged: two partial results of G * Sq rows of
- * d + 1 floats for each of at most 152 CTAs, and B + 1 int32 sums, each region
+ * d + 1 floats for each of at most 152 CTAs, and 16 bytes a CTA, each region
  * 256-byte aligned. Returns 0 for invalid sizes. */
 size_t fa_fwd_ragged_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int d,
                                            int block_size, int max_blocks);

@@ -90,7 +90,7 @@ def test_ragged_workspace_formula(fa_lib):
                                       (2, 12, 12, 3, 64, 16, 20)]:
         ctas = min(152, B * Hkv * -(-(mb * bs) // 128))
         rows = 2 * ctas * (Hq // Hkv) * Sq
-        want = up(rows * d * 4) + up(rows * 4) + up((B + 1) * 4)
+        want = up(rows * d * 4) + up(rows * 4) + up(16 * ctas)
         assert fa_lib.fa_fwd_ragged_paged_workspace_bytes(B, Hq, Hkv, Sq, d, bs, mb) == want
     assert fa_lib.fa_fwd_ragged_paged_workspace_bytes(1, 8, 1, 17, 64, 16, 4) == 0
     assert fa_lib.fa_fwd_ragged_paged_workspace_bytes(1, 8, 1, 1, 64, 24, 4) == 0
