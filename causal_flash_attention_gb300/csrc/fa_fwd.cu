@@ -602,8 +602,10 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
       if (warp == 2 && lane == 0) trace_span(p.trace, 4, clock64());
       if (ok) {
         tc_fence_after();
-        // span form: a row that sees nothing has O = 0, l = 0
-        const float inv_l = (kSpan && !(l > 0.f)) ? 0.f : 1.f / l;
+        // span form: a row that sees nothing has O = 0, l = 0 (and only its own span says so:
+        // a row of NaN or -infinite scores has no sum either)
+        const bool none = kSpan && row_hi == 0;
+        const float inv_l = none ? 0.f : 1.f / l;
         using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
         Elem* orow = reinterpret_cast<Elem*>(p.out) + (static_cast<size_t>(bh) * p.Sq + row) * D;
 #pragma unroll
@@ -625,7 +627,7 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
         }
         if (row < p.Sq)
           p.lse[static_cast<size_t>(bh) * p.Sq + row] =
-              (kSpan && !(l > 0.f)) ? -INFINITY : (m_ref + __log2f(l)) * kLn2;
+              none ? -INFINITY : (m_ref + __log2f(l)) * kLn2;
       }
     }
     if constexpr (kSpan) {
