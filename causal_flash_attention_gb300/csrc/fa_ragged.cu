@@ -304,6 +304,18 @@ __device__ __forceinline__ void clear_rows(const HiddenRows& h, uint8_t* tile, i
   }
 }
 
+// What a row's sum of weights (relative to 2^m) makes of a key range: the factor of O and
+// the log2-sum. A sum of 0 is a range of which the row sees nothing, or only scores of
+// -infinity: weight 0 in the merge; but a row whose whole range it is (`sees`) has no
+// weights then, and gets NaN like one whose sum is NaN.
+struct PartSum {
+  float inv, lse2;
+  __device__ __forceinline__ PartSum(float l, float m, bool sees) {
+    inv = l == 0.f && !sees ? 0.f : 1.f / l;
+    lse2 = l == 0.f ? -INFINITY : m + __log2f(l);
+  }
+};
+
 // One barrier of a group of consecutive 8-byte barriers.
 struct Bars {
   uint32_t base;
@@ -594,9 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                p.status));
         if (!ok) break;
         tc_fence_after();
-        // a row that sees no key of this range contributes weight 0 to the merge
-        const float inv_l = l > 0.f ? 1.f / l : 0.f;
-        const float lse2 = l > 0.f ? m_ref + __log2f(l) : -INFINITY;
+        const PartSum sum(l, m_ref, whole && row_hi > 0);
         const size_t qrow = (static_cast<size_t>(b) * p.Hq + hq) * p.Sq + s;
         const size_t prow = (static_cast<size_t>(cta) * 2 + (head ? 0 : 1)) * p.R + r;
 #pragma unroll
@@ -610,20 +620,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int v = 0; v < 4; ++v)
               dst[v] = make_uint4(
-                  pack2<kBf16>(__uint_as_float(o[8 * v]) * inv_l, __uint_as_float(o[8 * v + 1]) * inv_l),
-                  pack2<kBf16>(__uint_as_float(o[8 * v + 2]) * inv_l, __uint_as_float(o[8 * v + 3]) * inv_l),
-                  pack2<kBf16>(__uint_as_float(o[8 * v + 4]) * inv_l, __uint_as_float(o[8 * v + 5]) * inv_l),
-                  pack2<kBf16>(__uint_as_float(o[8 * v + 6]) * inv_l, __uint_as_float(o[8 * v + 7]) * inv_l));
+                  pack2<kBf16>(__uint_as_float(o[8 * v]) * sum.inv, __uint_as_float(o[8 * v + 1]) * sum.inv),
+                  pack2<kBf16>(__uint_as_float(o[8 * v + 2]) * sum.inv, __uint_as_float(o[8 * v + 3]) * sum.inv),
+                  pack2<kBf16>(__uint_as_float(o[8 * v + 4]) * sum.inv, __uint_as_float(o[8 * v + 5]) * sum.inv),
+                  pack2<kBf16>(__uint_as_float(o[8 * v + 6]) * sum.inv, __uint_as_float(o[8 * v + 7]) * sum.inv));
           } else {
             float4* dst = reinterpret_cast<float4*>(p.part_out + prow * D + cc * 32);
 #pragma unroll
             for (int v = 0; v < 8; ++v)
-              dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv_l, __uint_as_float(o[4 * v + 1]) * inv_l,
-                                   __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
+              dst[v] = make_float4(__uint_as_float(o[4 * v]) * sum.inv, __uint_as_float(o[4 * v + 1]) * sum.inv,
+                                   __uint_as_float(o[4 * v + 2]) * sum.inv, __uint_as_float(o[4 * v + 3]) * sum.inv);
           }
         }
-        if (real && whole) p.lse[qrow] = lse2 * kLn2R;
-        if (real && !whole) p.part_lse2[prow] = lse2;
+        if (real && whole) p.lse[qrow] = sum.lse2 * kLn2R;
+        if (real && !whole) p.part_lse2[prow] = sum.lse2;
         tc_fence_before();
       }
       head = false;
@@ -1035,18 +1045,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r = 0; r < NR; ++r) {
         if (r >= p.R) break;
         const float4 v = red_sum[r];
-        const float sum = (v.x + v.y) + (v.z + v.w);
-        // a row that sees no key of this range contributes weight 0 to the merge
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        const float y = __uint_as_float(o[r]) * inv;
+        const PartSum sum((v.x + v.y) + (v.z + v.w), m[r],
+                          whole && (pos0 >= 0 || pos0 + r % p.Sq >= 0));
+        const float y = __uint_as_float(o[r]) * sum.inv;
         if (t < D) {
           if (whole) static_cast<Elem*>(p.out)[(qrow + r) * D + t] = static_cast<Elem>(y);
           else p.part_out[(prow + r) * D + t] = y;
         }
         if (tid == 0) {
-          const float lse2 = sum > 0.f ? m[r] + __log2f(sum) : -INFINITY;
-          if (whole) p.lse[qrow + r] = lse2 * kLn2R;
-          else p.part_lse2[prow + r] = lse2;
+          if (whole) p.lse[qrow + r] = sum.lse2 * kLn2R;
+          else p.part_lse2[prow + r] = sum.lse2;
         }
       }
       head = false;
@@ -1129,7 +1137,8 @@ __global__ void __launch_bounds__(32 * kMergeRows) ragged_merge_kernel(const __g
   load(c0);
   float M = -INFINITY;
   for (int i = c0 + lane; i <= c1; i += 32) M = fmaxf(M, p.part_lse2[part(i)]);
-  M = warp_max(M);
+  M = warp_max(M);   // without NaN parts: their weight is NaN whatever it is
+  if (M == -INFINITY) M = 0.f;
   float acc[PER], L = 0.f;
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
@@ -1138,19 +1147,19 @@ __global__ void __launch_bounds__(32 * kMergeRows) ragged_merge_kernel(const __g
 #pragma unroll
     for (int k = 0; k < kMergeBatch; ++k)
       if (i + k <= c1) {
-        const float w = M != -INFINITY ? ex2(lv[k] - M) : 0.f;
+        const float w = ex2(lv[k] - M);
         L += w;
 #pragma unroll
         for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k].x[e], acc[e]);
       }
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  const int gq = r / p.Sq;
-  const long long row = (static_cast<long long>(b) * p.Hq + kvh * p.G + gq) * p.Sq + r - gq * p.Sq;
+  const int gq = r / p.Sq, s = r - gq * p.Sq;
+  const PartSum sum(L, M, seq_keys(p, b).len - p.Sq + s >= 0);
+  const long long row = (static_cast<long long>(b) * p.Hq + kvh * p.G + gq) * p.Sq + s;
   T* dst = static_cast<T*>(p.out) + row * D + lane * PER;
 #pragma unroll
-  for (int e = 0; e < PER; ++e) dst[e] = static_cast<T>(acc[e] * inv);
-  if (lane == 0) p.lse[row] = L > 0.f ? (M + __log2f(L)) * kLn2R : -INFINITY;
+  for (int e = 0; e < PER; ++e) dst[e] = static_cast<T>(acc[e] * sum.inv);
+  if (lane == 0) p.lse[row] = sum.lse2 * kLn2R;
 }
 
 template <int smem, class Kernel>
