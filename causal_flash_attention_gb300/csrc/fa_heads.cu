@@ -13,8 +13,8 @@
 //
 // The angle. Frequencies come as turns per position in 64-bit fixed point, so
 // the token's phase is one wrapping integer product, exact modulo a turn at any
-// position, and no range reduction follows: its top 32 bits (a phase within
-// 2^-33 of a turn) go to sincospif.
+// position, and no range reduction follows: rounded to 32 bits (2^-33 of a turn), then to
+// fp32 (another 2^-26 of a turn at most, near half a turn) it goes to sincospif.
 //
 // Layout. A head's d elements are held by d / 8 lanes, 8 elements each, so a warp
 // takes a group of 32 / (d / 8) heads of a token at a time. Forward, a lane holds two
@@ -145,8 +145,8 @@ __device__ __forceinline__ float inv_rms(float mean, float eps) {
 // (cos, sin) times rope_scale of pair i at a position: entry i of a token's table.
 __device__ __forceinline__ float2 cos_sin(const HeadsParams& p, int position, int i) {
   const uint64_t turn = static_cast<uint64_t>(static_cast<long long>(position)) * p.turns[i];
-  // top 32 bits as a signed fraction of half a turn
-  const float x = static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f;
+  // top 32 bits, rounded, as a signed fraction of half a turn
+  const float x = static_cast<float>(static_cast<int>((turn + 0x80000000u) >> 32)) * 0x1p-31f;
   float sn, cs;
   sincospif(x, &sn, &cs);
   return make_float2(cs * p.rope_scale, sn * p.rope_scale);

@@ -1,7 +1,11 @@
 """Query/key preparation at the edges of its arguments."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
+from bounds import f64
 from test_gpu_heads import freqs, make
 
 pytestmark = pytest.mark.gpu
@@ -23,3 +27,27 @@ def test_infinite_gradient_past_the_rotated_part_stays_where_it_is(fa, interleav
     got = fa.qk_norm_rope_backward(*dy, q, k, turns, interleaved=interleaved)
     torch.cuda.synchronize()
     assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_phases_between_two_steps(fa, interleaved):
+    """A phase is taken to the nearest of 2^32 steps a turn: angles this small come out to half
+    such a step (2 pi 2^-33), both ways, on either side of zero."""
+    F = 2.0 ** -24
+    turns = [int((n + f) * 2 ** 32) for n, f in ((0, 0.99), (0, 0.51), (0, 0.3), (3, 0.999),
+                                                 (-1, 0.4), (-1, 0.01), (-5, 0.75), (7, 0.25))]
+    t = 2 * math.pi * np.array(turns, dtype=np.float64) * 2.0 ** -64
+    i = np.arange(8)
+    ia, ib = (2 * i, 2 * i + 1) if interleaved else (i, i + 8)
+    q, k = torch.zeros(1, 1, 2, 64, device=DEV), torch.zeros(1, 1, 2, 64, device=DEV)
+    q[..., ia] = 1.0       # sin t appears alone in the pairs' second elements
+    k[..., ib] = 1.0       # and -sin t in their first
+    table = torch.tensor(turns, dtype=torch.int64, device=DEV)
+    yq, yk = fa.qk_norm_rope_forward(q, k, table, interleaved=interleaved)
+    dq, dk = fa.qk_norm_rope_backward(q, k, None, None, table, interleaved=interleaved)[:2]
+    torch.cuda.synchronize()
+    tol = 2 * math.pi * 2.0 ** -33 + 4 * F * np.abs(t)
+    for y, at, want in ((yq, ib, np.sin(t)), (yk, ia, -np.sin(t)), (dq, ib, -np.sin(t)),
+                        (dk, ia, np.sin(t))):
+        off = np.abs(f64(y)[0, 0, 1][at] - want)       # row 1 stands at position 1
+        assert (off <= tol).all(), off / tol
