@@ -143,8 +143,8 @@ __device__ __forceinline__ float inv_rms(float mean, float eps) {
 }
 
 // (cos, sin) times rope_scale of pair i at a position: entry i of a token's table.
-__device__ __forceinline__ float2 cos_sin(const HeadsParams& p, int position, int i) {
-  const uint64_t turn = static_cast<uint64_t>(static_cast<long long>(position)) * p.turns[i];
+__device__ __forceinline__ float2 cos_sin(const HeadsParams& p, long long position, int i) {
+  const uint64_t turn = static_cast<uint64_t>(position) * p.turns[i];
   // top 32 bits, rounded, as a signed fraction of half a turn
   const float x = static_cast<float>(static_cast<int>((turn + 0x80000000u) >> 32)) * 0x1p-31f;
   float sn, cs;
@@ -153,7 +153,7 @@ __device__ __forceinline__ float2 cos_sin(const HeadsParams& p, int position, in
 }
 
 // The table of one token, by the warps that share it (warp `w` of `W` here).
-__device__ __forceinline__ void fill_table(const HeadsParams& p, float2* table, int position,
+__device__ __forceinline__ void fill_table(const HeadsParams& p, float2* table, long long position,
                                            int lane, int w, int W) {
   for (int i = w * 32 + lane; i < p.rope_dim / 2; i += 32 * W) table[i] = cos_sin(p, position, i);
 }
@@ -398,18 +398,20 @@ __global__ void __launch_bounds__(32 * kWarpsH, kFwdBlocks)
   while (gr.start >= gr.groups && c < kClasses - 1) enter(++c);
   load(gr.start);
 
-  int position = s;
+  long long position = s;
   if (live) {
-    if constexpr (kAppend) position = p.seq_lens[b] - p.S + s;
+    // (a length may be any int32, and so far below 0 that 32 bits would wrap around)
+    if constexpr (kAppend) position = static_cast<long long>(p.seq_lens[b]) - p.S + s;
     else if (p.positions) position = p.positions[token];
   }
   fill_table(p, table[t], position, lane, warp & (kWarpsH / sh.tokens - 1), kWarpsH / sh.tokens);
   long long page_row = -1;   // append: row of the cache [block][Hkv][block_size]
   if constexpr (kAppend) {
-    if (live && position >= 0 && position / p.block_size < p.max_blocks) {
-      const int pb = p.block_table[static_cast<size_t>(b) * p.max_blocks + position / p.block_size];
+    const int row = static_cast<int>(position);   // below 2^31 where it is not below 0
+    if (live && position >= 0 && row / p.block_size < p.max_blocks) {
+      const int pb = p.block_table[static_cast<size_t>(b) * p.max_blocks + row / p.block_size];
       if (pb >= 0 && pb < p.num_blocks)
-        page_row = static_cast<long long>(pb) * p.Hkv * p.block_size + position % p.block_size;
+        page_row = static_cast<long long>(pb) * p.Hkv * p.block_size + row % p.block_size;
     }
   }
   __syncthreads();

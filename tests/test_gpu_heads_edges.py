@@ -5,8 +5,9 @@ import numpy as np
 import pytest
 import torch
 
-from bounds import f64
-from test_gpu_heads import freqs, make
+from bounds import check, f64, half_step, norm_rope_bounds
+from oracle import operators as ops
+from test_gpu_heads import cache, freqs, make
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -51,3 +52,22 @@ def test_phases_between_two_steps(fa, interleaved):
                         (dk, ia, np.sin(t))):
         off = np.abs(f64(y)[0, 0, 1][at] - want)       # row 1 stands at position 1
         assert (off <= tol).all(), off / tol
+
+
+def test_append_at_the_least_length(fa):
+    """Row s of a sequence of -2^31 tokens stands before the cache, at -2^31 - Sq + s: nothing is
+    stored, however long the table, and q is rotated by that position."""
+    q, k, v, w = make(2, 2, 1, 2, 64, "bf16", True, "packed", 9)
+    kc, vc = cache(2, 1, 1024, 64, "bf16"), cache(2, 1, 1024, 64, "bf16")
+    lens = [-2 ** 31, -2 ** 31 + 1]
+    table = torch.zeros(2, 1 << 21, dtype=torch.int32, device=DEV)
+    f = freqs(64)
+    got = fa.qk_norm_rope_append(q, k, v, kc, vc, table,
+                                 torch.tensor(lens, dtype=torch.int32, device=DEV),
+                                 fa.rope_turns(f, DEV), q_weight=w[0], k_weight=w[1])
+    torch.cuda.synchronize()
+    assert (kc == 9.0).all() and (vc == 9.0).all()
+    a = dict(inv_freq=f, positions=np.array(lens)[:, None] - 2 + np.arange(2), eps=1e-6,
+             interleaved=False, rope_scale=1.0)
+    check("q", got, ops.norm_rope(f64(q), f64(w[0]), **a),
+          norm_rope_bounds(f64(q), f64(w[0]), u=half_step(q.dtype), **a))
