@@ -295,7 +295,7 @@ int check_span(const SpanArgs& m, float scale) {
 // would leave the range of fp32, the polynomial is not to be used.
 template <int N>
 bool scale_poly(const double (&from)[N], float (&to)[N], double ratio, double cap_log2) {
-  bool ok = ratio >= 1e-4 && ratio <= 1e3;
+  bool ok = true;
   double power = cap_log2 * ratio;
   for (int i = 0; i < N; ++i, power *= ratio * ratio) {
     const double x = std::fabs(from[i] * power);
@@ -319,7 +319,14 @@ ScoreMod make_mod(const SpanArgs& m, int Sq, int Skv, float scale) {
   const double ratio = m.softcap > 0.f ? static_cast<double>(scale) / m.softcap : 0.0;
   const double cap_log2 = static_cast<double>(m.softcap) * kLog2e;
   r.cap_limit_a = scale_poly(a, r.cap_a, ratio, cap_log2) ? static_cast<float>(0.75 / ratio) : 0.f;
-  r.cap_limit_b = scale_poly(b, r.cap_b, ratio, cap_log2) ? static_cast<float>(0.3 / ratio) : 0.f;
+  if (scale_poly(b, r.cap_b, ratio, cap_log2)) {
+    r.cap_limit_b = static_cast<float>(0.3 / ratio);
+  } else if (m.softcap > 0.f && ratio < 1.0) {
+    // a cap some 10^9 times the scale or more: tanh u = u, to 2^-25 of it, up to u = 2^-12
+    r.cap_b[0] = static_cast<float>(cap_log2 * ratio);
+    r.cap_b[1] = r.cap_b[2] = 0.f;
+    r.cap_limit_b = static_cast<float>(0x1p-12 / ratio);
+  }
   r.pos_offset = Skv - Sq;
   return r;
 }

@@ -354,11 +354,14 @@ size_t fa_fwd_ragged_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int d
  * be finite everywhere, padding included.
  *
  * FA_BF16 and FA_F16 only (FA_F32 gives FA_ERR_DTYPE). softcap must be 0, or it
- * and scale / softcap within 2^-60 .. 2^60 (else FA_ERR_SCALE); a capped score is
- * off by up to softcap * 2^-20, whatever its size. key_begin, key_end and slopes
- * need 4-byte alignment. dk and dv have the same bits on every call; dq is summed
- * with fp32 additions in global memory whose order, and so its last bits, may
- * differ.
+ * and scale / softcap within 2^-60 .. 2^60 (else FA_ERR_SCALE). A capped score is
+ * off by up to softcap * 2^-20; where no score of the warp that caps it (32 rows of
+ * a tile of 128 keys, masked ones included) is above 0.3 softcap, or 2^-12 softcap
+ * for caps above 10^9 scale, by up to 2^-17 of itself. So the last bits of a row
+ * may depend on what stands beside it. key_begin, key_end and slopes need 4-byte
+ * alignment. dk and dv have the same bits on every call with the same spans (how
+ * their sums are cut goes by the spans of the whole batch); dq is summed with fp32
+ * additions in global memory whose order, and so its last bits, may differ.
  */
 int fa_fwd_span(const void* q, const void* k, const void* v, const int* key_begin,
                 const int* key_end, void* out, float* lse, int B, int Hq, int Hkv, int Sq,
