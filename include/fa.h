@@ -296,7 +296,8 @@ int fa_qk_norm_rope_append(const fa_view* q, const fa_view* k, const fa_view* v,
  *   max(0, p + 1 - window) <= j <= p        (window 0: from key 0),
  *
  * with scores capped and biased as by fa_fwd_span (distance p - j). A row that
- * sees no key (p < 0) gets out = 0 and lse = -infinity.
+ * sees no key (p < 0), or whose scores are all -infinity, gets out = 0 and lse =
+ * -infinity; a row with a NaN or +infinity among its scores gets NaN in both.
  *
  * The lengths are read on the device only, and must not change while the call
  * runs: it needs no host copy of them, and a captured graph may be replayed
