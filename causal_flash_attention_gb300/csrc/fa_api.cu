@@ -885,13 +885,18 @@ int fa_fwd_ragged_paged(const void* q, const void* k_cache, const void* v_cache,
   if (!make_tmap(&p.tm_k, k_cache, num_blocks * Hkv, block_size, d, bf16, p.box_rows) ||
       !make_tmap(&p.tm_v, v_cache, num_blocks * Hkv, block_size, d, bf16, p.box_rows))
     return FA_ERR_TMA;
-  const ScoreMod mod = make_mod(SpanArgs{nullptr, nullptr, slopes, softcap}, 0, 0, scale);
+  p.mod = make_mod(SpanArgs{nullptr, nullptr, slopes, softcap}, 0, 0, scale);
+  // The exponential form is off by up to softcap 2^-20: for caps up to 128 no more than
+  // 2^-13 of a weight, half of what rounding it to fp16 is. Choosing the form by the scores
+  // gains nothing there (4 tokens of 2 sequences of 20000 and 32768 keys, 32 + 8 heads,
+  // d = 128: 46.3 us, by the scores 47.1; 40 rows of 24 sequences of 2000 keys, scores up to
+  // the cap: 20.7, by the scores 23.0), so that is for larger caps.
+  p.large_cap = softcap > 128.f;
   p.q = q;
   p.out = out;
   p.lse = lse;
   p.block_table = block_table;
   p.seq_lens = seq_lens;
-  p.slopes = slopes;
   p.part_out = reinterpret_cast<float*>(wsb + rp.part_out);
   p.part_lse2 = reinterpret_cast<float*>(wsb + rp.part_lse2);
   p.starts = reinterpret_cast<int4*>(wsb + rp.starts);
@@ -903,8 +908,6 @@ int fa_fwd_ragged_paged(const void* q, const void* k_cache, const void* v_cache,
   // a window that no position outgrows hides nothing (and would overflow positions)
   p.window = window < p.capacity ? window : 0;
   p.scale_log2 = scale * kLog2e;
-  p.cap_in = mod.cap_in;
-  p.cap_log2 = mod.cap_log2;
   p.n_ctas = rp.n_ctas;
   p.status = status_ptr();
   if (!p.status) return FA_ERR_CUDA;

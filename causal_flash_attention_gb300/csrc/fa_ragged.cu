@@ -324,7 +324,10 @@ struct Bars {
 };
 
 // ------------------------------------------------- one thread per query row --
-template <int D, bool kBf16>
+// (kLargeCap: p.large_cap. A kernel of its own: with the forms in it the other's loop is
+// slower, 24 sequences of 2000 keys with 40 rows 20.2 us -> 21.4, of 4000 keys with 32
+// rows at d = 64 38.1 -> 40.5.)
+template <int D, bool kBf16, bool kLargeCap>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_ragged_kernel(const __grid_constant__ RaggedParams p) {
   using Cfg = RagCfg<D>;
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = real ? r % p.Sq : 0;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t o_tmem = tmem + lane_off + 256;
-    const float c = p.cap_in != 0.f ? 1.f : p.scale_log2;   // capped scores are in the log2 domain
+    const float c = p.mod.cap_in != 0.f ? 1.f : p.scale_log2;   // capped scores are in the log2 domain
     // Stage this row of a segment's queries into the 128-byte-swizzled K-major
     // query tile (16-byte unit u of a 128-byte row sits at unit u ^ (r % 8));
     // rows past R are zero.
@@ -489,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         row_hi = max(pos + 1, 0);
         row_lo = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
       }
-      const float bias = p.slopes ? p.slopes[hq] * (kLog2eR / c) : 0.f;
+      const float bias = p.mod.slopes ? p.mod.slopes[hq] * (kLog2eR / c) : 0.f;
       float m_ref = -INFINITY;   // reference max, scaled log2 domain
       float l = 0.f;
       for (int j = 0; j < n; ++j, ++g) {
@@ -519,12 +522,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kTileN; ++i) sc[i] = __uint_as_float(raw[i]);
           }
-          if (p.cap_in != 0.f) {
+          if constexpr (kLargeCap) {
+            if (hidden.any()) {   // keys that may hold anything do not choose the cap's form
 #pragma unroll
-            for (int i = 0; i < kTileN; ++i)
-              sc[i] = fmaf(-2.f * p.cap_log2, cap_r(sc[i], p.cap_in), p.cap_log2);
+              for (int h = 0; h < kTileN / 32; ++h) {
+                const uint32_t w = span_bits(keys.first, keys.len, kv0 + h * 32);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!((w >> i) & 1u)) sc[h * 32 + i] = 0.f;
+              }
+            }
+            cap_scores(sc, warp_abs_max(sc), p.mod);
+          } else if (p.mod.cap_in != 0.f) {
+#pragma unroll
+            for (int i = 0; i < kTileN; ++i) sc[i] = cap_exact(sc[i], p.mod);
           }
-          if (p.slopes) {
+          if (p.mod.slopes) {
             const float d0 = static_cast<float>(kv0 - pos);
 #pragma unroll
             for (int i = 0; i < kTileN; ++i)
@@ -737,7 +750,7 @@ __device__ __forceinline__ void tmem_st_n(uint32_t addr, const uint32_t (&r)[N])
   else tmem_st32(addr, r);
 }
 
-template <int D, int NR, bool kBf16>
+template <int D, int NR, bool kBf16, bool kLargeCap>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_ragged_keys_kernel(const __grid_constant__ RaggedParams p) {
   using Cfg = RagTCfg<D, NR>;
@@ -863,8 +876,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = static_cast<int>(threadIdx.x) - 64;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t o_tmem = tmem + lane_off + 64;
-    const bool cap = p.cap_in != 0.f;
-    const bool same_rows = p.Sq == 1 && !p.slopes;   // rows do not differ in position or slope
+    const bool cap = p.mod.cap_in != 0.f;
+    const bool same_rows = p.Sq == 1 && !p.mod.slopes;   // rows do not differ in position or slope
     const float c = p.scale_log2;
     float* row_slope = reinterpret_cast<float*>(smem + Cfg::kOffRow);          // log2 domain
     int* row_s = reinterpret_cast<int*>(smem + Cfg::kOffRow + NR * 4);         // token of the row
@@ -923,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!same_rows && tid < NR) {
         const int gq = min(tid, p.R - 1) / p.Sq;
         row_s[tid] = tid < p.R ? tid - gq * p.Sq : 0;
-        row_slope[tid] = p.slopes ? p.slopes[kvh * p.G + gq] * kLog2eR : 0.f;
+        row_slope[tid] = p.mod.slopes ? p.mod.slopes[kvh * p.G + gq] * kLog2eR : 0.f;
       }
       more = seg.next(p);
       if (more) load_q(seg);   // the next segment's, stored after the first tile
@@ -949,16 +962,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_free(g & 1));
-        if (cap) {
+        if constexpr (kLargeCap) {
+          if (key < keys.first || key >= keys.len) {   // a key that may hold anything does not
 #pragma unroll
-          for (int r = 0; r < NR; ++r)
-            x[r] = fmaf(-2.f * p.cap_log2, cap_r(x[r], p.cap_in), p.cap_log2);
+            for (int r = 0; r < NR; ++r) x[r] = 0.f;   // choose the cap's form
+          }
+          cap_scores(x, warp_abs_max(x), p.mod);
+        } else if (cap) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r) x[r] = cap_exact(x[r], p.mod);
         } else {
 #pragma unroll
           for (int r = 0; r < NR; ++r) x[r] *= c;
         }
         if (j == 0 && !same_rows) row_warps_any(false);   // row_slope and row_s are written
-        if (p.slopes) {
+        if (p.mod.slopes) {
 #pragma unroll
           for (int r = 0; r < NR; ++r)
             x[r] = fmaf(-row_slope[r], fabsf(static_cast<float>(pos0 + row_s[r] - key)), x[r]);
@@ -1169,16 +1187,20 @@ cudaError_t launch_main(Kernel kernel, const RaggedParams& p, cudaStream_t strea
   return launch_dependent(kernel, dim3(static_cast<unsigned>(p.n_ctas)), dim3(kThreads), smem, stream, p);
 }
 
+template <int D, bool kBf16, bool kLargeCap>
+cudaError_t launch_form(const RaggedParams& p, cudaStream_t stream) {
+  if (p.R <= 16)
+    return launch_main<RagTCfg<D, 16>::kSmemBytes>(fa_ragged_keys_kernel<D, 16, kBf16, kLargeCap>, p, stream);
+  if (p.R <= 32)
+    return launch_main<RagTCfg<D, 32>::kSmemBytes>(fa_ragged_keys_kernel<D, 32, kBf16, kLargeCap>, p, stream);
+  return launch_main<RagCfg<D>::kSmemBytes>(fa_ragged_kernel<D, kBf16, kLargeCap>, p, stream);
+}
+
 template <int D, bool kBf16>
 cudaError_t launch_ragged_impl(const RaggedParams& p, cudaStream_t stream) {
   using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
-  cudaError_t e;
-  if (p.R <= 16)
-    e = launch_main<RagTCfg<D, 16>::kSmemBytes>(fa_ragged_keys_kernel<D, 16, kBf16>, p, stream);
-  else if (p.R <= 32)
-    e = launch_main<RagTCfg<D, 32>::kSmemBytes>(fa_ragged_keys_kernel<D, 32, kBf16>, p, stream);
-  else
-    e = launch_main<RagCfg<D>::kSmemBytes>(fa_ragged_kernel<D, kBf16>, p, stream);
+  const cudaError_t e = p.large_cap ? launch_form<D, kBf16, true>(p, stream)
+                                    : launch_form<D, kBf16, false>(p, stream);
   if (e != cudaSuccess) return e;
   // the merge overlaps its launch with the ragged kernel's tail
   return launch_dependent(ragged_merge_kernel<Elem, D / 32>,

@@ -17,7 +17,6 @@ struct RaggedParams {
   float* lse;         // [B*Hq][Sq]
   const int* block_table;   // [B][max_blocks]
   const int* seq_lens;      // [B]
-  const float* slopes;      // [Hq] or null
   float* part_out;    // [2 * CTAs][R][d] fp32 out = O / l of a part of a (sequence, head)
   float* part_lse2;   // [2 * CTAs][R]    its log2-sum-exp2 of scaled scores
   int4* starts;       // [CTAs] where each CTA's share begins, written by it (find_share)
@@ -25,7 +24,9 @@ struct RaggedParams {
   int block_size, box_rows, max_blocks, num_blocks;
   int capacity;       // keys a table row can hold (at most 2^31 - 128)
   int window;         // keys a row sees, its own position included; 0: all
-  float scale_log2, cap_in, cap_log2;   // as ScoreMod
+  float scale_log2;
+  ScoreMod mod;       // cap and slopes; key spans and pos_offset are not used here
+  bool large_cap;     // the cap's form goes by the scores (cap_scores), not the exponential always
   int n_ctas;
   int* status;
 };

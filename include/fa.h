@@ -312,7 +312,9 @@ int fa_qk_norm_rope_append(const fa_view* q, const fa_view* k, const fa_view* v,
  * G * Sq <= 128 with G = Hq / Hkv, block_size as for fa_fwd_splitkv_paged,
  * max_blocks >= 1, window >= 0 and B * Hkv * (ceil(max_blocks * block_size /
  * 128) + 8) < 2^31 (else FA_ERR_SHAPE); softcap as for fa_fwd_span (else
- * FA_ERR_SCALE); FA_BF16 and FA_F16 only (FA_F32 gives FA_ERR_DTYPE).
+ * FA_ERR_SCALE), its error too, but softcap * 2^-20 always for caps up to 128 (a
+ * warp caps 32 rows of 128 keys, or up to 32 rows of 32 keys; keys that no row
+ * sees do not count there); FA_BF16 and FA_F16 only (FA_F32 gives FA_ERR_DTYPE).
  * workspace: caller-owned, at least fa_fwd_ragged_paged_workspace_bytes(...)
  * bytes, 256-byte aligned, contents on entry without meaning; calls that may
  * overlap on the GPU need one each.

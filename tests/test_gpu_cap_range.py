@@ -48,3 +48,27 @@ def test_span(fa, relative, softcap, d, dtype):
                               None, f64(do), half_step(q.dtype))
     for name, t in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
         check(name, t, want[name], want[name + "_tol"])
+
+
+@pytest.mark.parametrize("softcap", CAPS)
+@pytest.mark.parametrize("Hq,Hkv,Sq", [(4, 2, 1), (24, 1, 1), (40, 1, 1), (8, 1, 16)])
+@pytest.mark.parametrize("garbage", [False, True])
+def test_ragged(fa, relative, softcap, Hq, Hkv, Sq, garbage):
+    """Also with infinities in rows of the last pages that no row sees, which do not decide how
+    the scores beside them are capped."""
+    d, bs, lens = 128, 64, [900, 300, 70]
+    g = torch.Generator().manual_seed(Hq)
+    q, (kc, vc) = 3 * randn(g, "bf16", 3, Hq, Sq, d), randn(g, "bf16", 2, 45, Hkv, bs, d)
+    table = torch.randperm(45, generator=g).to(torch.int32).view(3, 15)
+    if garbage:
+        for b, n in enumerate(lens):
+            kc[table[b, n // bs], :, n % bs:] = float("inf")
+            kc[table[b, n // bs], :, n % bs:, ::2] = -3e38
+    x = [q, kc, vc, table, torch.tensor(lens, dtype=torch.int32)]
+    out, lse = fa.decode_forward_ragged(*(t.to(DEV) for t in x), softcap=softcap)
+    torch.cuda.synchronize()
+    kc = torch.where(kc.abs() < 1e30, kc, torch.zeros_like(kc))
+    want = ops.ragged_attention(f64(q), f64(kc), f64(vc), table.numpy(), lens, d ** -0.5, 0, softcap,
+                                u=half_step(q.dtype))
+    check("out", out, want["out"], want["out_tol"])
+    check("lse", lse, want["lse"], want["lse_tol"])
