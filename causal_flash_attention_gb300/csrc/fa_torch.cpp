@@ -153,6 +153,22 @@ T* data(const Tensor& t) {
   return t.defined() ? static_cast<T*>(t.data_ptr()) : nullptr;
 }
 
+// Other Python threads run while a call allocates and launches, either of which may wait
+// for the GPU (memory to be freed, a full launch queue). From here to end() nothing
+// touches a Python object.
+class Released {
+  PyThreadState* state_ = PyEval_SaveThread();
+
+ public:
+  Released() = default;
+  Released(const Released&) = delete;
+  ~Released() { end(); }
+  void end() {
+    if (state_) PyEval_RestoreThread(state_);
+    state_ = nullptr;
+  }
+};
+
 // Where a call runs and allocates: the tensors' device, and the current stream
 // or the one given by its handle. Memory comes from that stream's own pool, so
 // that its earlier and later users are ordered with the call.
@@ -246,28 +262,31 @@ float scale_of(PyObject* o, int d) {
 
 // (handle, q, k, v, key_begin, key_end, out, lse, softcap, slopes, scale, stream)
 PyObject* span_forward(PyObject* const* a) {
-  const Library& lib = library(a[0]);
+  const Library lib = library(a[0]);
   const Tensor &q = tensor(a[1], "q"), &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
   const Tensor &begin = tensor(a[4], "key_begin"), &end = tensor(a[5], "key_end");
   Tensor out = maybe(a[6], "out"), lse = maybe(a[7], "lse");
   const Tensor slopes = maybe(a[9], "slopes");
   const SpanDims n = span_inputs(q, k, v, begin, end, slopes);
+  const float scale = scale_of(a[10], n.d), softcap = real(a[8]);
   const Place at(q.device(), a[11]);
+  Released released;
   if (out.defined()) fit("out", out, q.device(), q.scalar_type(), q.sizes());
   else out = empty(q.sizes(), q.device(), q.scalar_type());
   if (lse.defined()) fit("lse", lse, q.device(), at::kFloat, q.sizes().slice(0, 3));
   else lse = empty(q.sizes().slice(0, 3), q.device(), at::kFloat);
   const int rc = lib.fwd_span(q.data_ptr(), k.data_ptr(), v.data_ptr(), data<int>(begin),
                               data<int>(end), out.data_ptr(), data<float>(lse), n.B, n.Hq, n.Hkv,
-                              n.Sq, n.Skv, n.d, scale_of(a[10], n.d), real(a[8]),
-                              data<float>(slopes), dtype_code(q), at.stream);
+                              n.Sq, n.Skv, n.d, scale, softcap, data<float>(slopes),
+                              dtype_code(q), at.stream);
+  released.end();
   return rc ? PyLong_FromLong(rc) : tensors({out, lse});
 }
 
 // (handle, q, k, v, key_begin, key_end, out, dout, lse, dq, dk, dv, workspace, softcap, slopes,
 //  scale, stream)
 PyObject* span_backward(PyObject* const* a) {
-  const Library& lib = library(a[0]);
+  const Library lib = library(a[0]);
   const Tensor &q = tensor(a[1], "q"), &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
   const Tensor &begin = tensor(a[4], "key_begin"), &end = tensor(a[5], "key_end");
   const Tensor &out = tensor(a[6], "out"), &dout = tensor(a[7], "dout"), &lse = tensor(a[8], "lse");
@@ -280,7 +299,9 @@ PyObject* span_backward(PyObject* const* a) {
   fit("out", out, dev, dt, q.sizes());
   fit("dout", dout, dev, dt, q.sizes());
   fit("lse", lse, dev, at::kFloat, q.sizes().slice(0, 3));
+  const float scale = scale_of(a[15], n.d), softcap = real(a[13]);
   const Place at(dev, a[16]);
+  Released released;
   for (auto& [name, g, like] : {std::tuple<const char*, Tensor&, const Tensor&>{"dq", dq, q},
                                 {"dk", dk, k}, {"dv", dv, k}}) {
     if (g.defined()) fit(name, g, dev, dt, like.sizes());
@@ -290,8 +311,9 @@ PyObject* span_backward(PyObject* const* a) {
   const int rc = lib.bwd_span(q.data_ptr(), k.data_ptr(), v.data_ptr(), data<int>(begin),
                               data<int>(end), out.data_ptr(), dout.data_ptr(), data<float>(lse),
                               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), n.B, n.Hq, n.Hkv, n.Sq,
-                              n.Skv, n.d, scale_of(a[15], n.d), real(a[13]), data<float>(slopes),
-                              dtype_code(q), ws.data_ptr(), workspace_bytes(ws, dev), at.stream);
+                              n.Skv, n.d, scale, softcap, data<float>(slopes), dtype_code(q),
+                              ws.data_ptr(), workspace_bytes(ws, dev), at.stream);
+  released.end();
   return rc ? PyLong_FromLong(rc) : tensors({dq, dk, dv});
 }
 
@@ -313,7 +335,7 @@ CacheDims cache_inputs(at::Device dev, at::ScalarType dt, int64_t B, int64_t Hkv
 // (handle, q, k_cache, v_cache, block_table, seq_lens, out, lse, workspace, window, softcap,
 //  slopes, scale, stream)
 PyObject* ragged(PyObject* const* a) {
-  const Library& lib = library(a[0]);
+  const Library lib = library(a[0]);
   const Tensor &q = tensor(a[1], "q"), &kc = tensor(a[2], "k_cache"), &vc = tensor(a[3], "v_cache");
   const Tensor &table = tensor(a[4], "block_table"), &lens = tensor(a[5], "seq_lens");
   Tensor out = maybe(a[6], "out"), lse = maybe(a[7], "lse"), ws = maybe(a[8], "workspace");
@@ -326,7 +348,10 @@ PyObject* ragged(PyObject* const* a) {
   const int Hkv = narrow(kc.size(1));
   const CacheDims c = cache_inputs(dev, dt, B, Hkv, d, kc, vc, table, lens);
   if (slopes.defined()) fit("slopes", slopes, dev, at::kFloat, {Hq});
+  const int window = integer(a[9]);
+  const float scale = scale_of(a[12], d), softcap = real(a[10]);
   const Place at(dev, a[13]);
+  Released released;
   if (out.defined()) fit("out", out, dev, dt, q.sizes());
   else out = empty(q.sizes(), dev, dt);
   if (lse.defined()) fit("lse", lse, dev, at::kFloat, q.sizes().slice(0, 3));
@@ -335,9 +360,10 @@ PyObject* ragged(PyObject* const* a) {
     ws = workspace_of(lib.ragged_bytes(B, Hq, Hkv, Sq, d, c.block_size, c.max_blocks), dev);
   const int rc = lib.ragged(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), data<int>(table),
                             data<int>(lens), out.data_ptr(), data<float>(lse), B, Hq, Hkv, Sq, d,
-                            c.block_size, c.num_blocks, c.max_blocks, integer(a[9]),
-                            scale_of(a[12], d), real(a[10]), data<float>(slopes), dtype_code(q),
+                            c.block_size, c.num_blocks, c.max_blocks, window, scale, softcap,
+                            data<float>(slopes), dtype_code(q),
                             ws.data_ptr(), workspace_bytes(ws, dev), at.stream);
+  released.end();
   return rc ? PyLong_FromLong(rc) : tensors({out, lse});
 }
 
@@ -400,22 +426,26 @@ HeadDims head_dims(const Tensor& q, const Tensor& k, const char* name) {
 // (handle, q, k, q_out, k_out, turns, positions, q_weight, k_weight, eps, interleaved,
 //  rope_scale, stream)
 PyObject* norm_rope(PyObject* const* a) {
-  const Library& lib = library(a[0]);
+  const Library lib = library(a[0]);
   const Tensor &q = tensor(a[1], "q"), &k = tensor(a[2], "k");
   Tensor qo = maybe(a[3], "q_out"), ko = maybe(a[4], "k_out");
   const HeadDims n = head_dims(q, k, "q");
   const RopeArgs r = rope_inputs(n.dev, n.dt, n.B, n.S, n.d, a[5], a[6], a[7], a[8]);
   const Sizes qs = {n.B, n.Hq, n.S, n.d}, ks = {n.B, n.Hkv, n.S, n.d};
   const fa_view vq = view("q", q, n.dev, n.dt, qs), vk = view("k", k, n.dev, n.dt, ks);
+  const float eps = real(a[9]), rope_scale = real(a[11]);
+  const bool interleaved = truth(a[10]);
   const Place at(n.dev, a[12]);
+  Released released;
   if (!qo.defined()) qo = empty(q.sizes(), n.dev, n.dt);
   if (!ko.defined()) ko = empty(k.sizes(), n.dev, n.dt);
   const fa_view vqo = view("q_out", qo, n.dev, n.dt, qs, true);
   const fa_view vko = view("k_out", ko, n.dev, n.dt, ks, true);
-  const int rc = lib.norm_rope(&vq, &vk, &vqo, &vko, data<void>(r.wq), data<void>(r.wk), real(a[9]),
+  const int rc = lib.norm_rope(&vq, &vk, &vqo, &vko, data<void>(r.wq), data<void>(r.wk), eps,
                                data<int>(r.positions), data<unsigned long long>(r.turns), r.rope_dim,
-                               truth(a[10]), real(a[11]), n.B, n.Hq, n.Hkv, n.S, n.d, dtype_code(q),
+                               interleaved, rope_scale, n.B, n.Hq, n.Hkv, n.S, n.d, dtype_code(q),
                                at.stream);
+  released.end();
   return rc ? PyLong_FromLong(rc) : tensors({qo, ko});
 }
 
@@ -423,7 +453,7 @@ PyObject* norm_rope(PyObject* const* a) {
 //  q_weight, k_weight, eps, interleaved, rope_scale, allocate, stream); allocate: give what is
 //  missing, dq and dk as projections lay q and k out
 PyObject* norm_rope_bwd(PyObject* const* a) {
-  const Library& lib = library(a[0]);
+  const Library lib = library(a[0]);
   const Tensor &dqo = tensor(a[1], "dq_out"), &dko = tensor(a[2], "dk_out");
   const Tensor q = maybe(a[3], "q"), k = maybe(a[4], "k");
   Tensor dq = maybe(a[5], "dq"), dk = maybe(a[6], "dk"), dwq = maybe(a[7], "dq_weight"),
@@ -435,8 +465,11 @@ PyObject* norm_rope_bwd(PyObject* const* a) {
   fa_view vq{}, vk{};
   if (q.defined()) vq = view("q", q, n.dev, n.dt, qs);
   if (k.defined()) vk = view("k", k, n.dev, n.dt, ks);
+  const float eps = real(a[14]), rope_scale = real(a[16]);
+  const bool interleaved = truth(a[15]), allocate = truth(a[17]);
   const Place at(n.dev, a[18]);
-  if (truth(a[17])) {
+  Released released;
+  if (allocate) {
     if (!dq.defined()) dq = empty_tokens_first(n.B, n.Hq, n.S, n.d, n.dev, n.dt);
     if (!dk.defined()) dk = empty_tokens_first(n.B, n.Hkv, n.S, n.d, n.dev, n.dt);
     if (r.wq.defined()) {
@@ -452,17 +485,18 @@ PyObject* norm_rope_bwd(PyObject* const* a) {
   if (dwk.defined()) fit("dk_weight", dwk, n.dev, at::kFloat, {n.d});
   const int rc = lib.norm_rope_bwd(
       &vdqo, &vdko, q.defined() ? &vq : nullptr, k.defined() ? &vk : nullptr, &vdq, &vdk,
-      data<float>(dwq), data<float>(dwk), data<void>(r.wq), data<void>(r.wk), real(a[14]),
-      data<int>(r.positions), data<unsigned long long>(r.turns), r.rope_dim, truth(a[15]),
-      real(a[16]), n.B, n.Hq, n.Hkv, n.S, n.d, dtype_code(dqo), data<void>(ws),
+      data<float>(dwq), data<float>(dwk), data<void>(r.wq), data<void>(r.wk), eps,
+      data<int>(r.positions), data<unsigned long long>(r.turns), r.rope_dim, interleaved, rope_scale,
+      n.B, n.Hq, n.Hkv, n.S, n.d, dtype_code(dqo), data<void>(ws),
       workspace_bytes(ws, n.dev), at.stream);
+  released.end();
   return rc ? PyLong_FromLong(rc) : tensors({dq, dk, dwq, dwk});
 }
 
 // (handle, q, k, v, q_out, k_cache, v_cache, block_table, seq_lens, turns, q_weight, k_weight,
 //  eps, interleaved, rope_scale, stream)
 PyObject* append(PyObject* const* a) {
-  const Library& lib = library(a[0]);
+  const Library lib = library(a[0]);
   const Tensor &q = tensor(a[1], "q"), &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
   Tensor qo = maybe(a[4], "q_out");
   const Tensor &kc = tensor(a[5], "k_cache"), &vc = tensor(a[6], "v_cache");
@@ -473,14 +507,18 @@ PyObject* append(PyObject* const* a) {
   const Sizes qs = {n.B, n.Hq, n.S, n.d}, ks = {n.B, n.Hkv, n.S, n.d};
   const fa_view vq = view("q", q, n.dev, n.dt, qs), vk = view("k", k, n.dev, n.dt, ks),
                 vv = view("v", v, n.dev, n.dt, ks);
+  const float eps = real(a[12]), rope_scale = real(a[14]);
+  const bool interleaved = truth(a[13]);
   const Place at(n.dev, a[15]);
+  Released released;
   if (!qo.defined()) qo = empty(q.sizes(), n.dev, n.dt);
   const fa_view vqo = view("q_out", qo, n.dev, n.dt, qs, true);
   const int rc = lib.append(&vq, &vk, &vv, &vqo, kc.data_ptr(), vc.data_ptr(), data<int>(table),
-                            data<int>(lens), data<void>(r.wq), data<void>(r.wk), real(a[12]),
-                            data<unsigned long long>(r.turns), r.rope_dim, truth(a[13]), real(a[14]),
+                            data<int>(lens), data<void>(r.wq), data<void>(r.wk), eps,
+                            data<unsigned long long>(r.turns), r.rope_dim, interleaved, rope_scale,
                             n.B, n.Hq, n.Hkv, n.S, n.d, c.block_size, c.num_blocks, c.max_blocks,
                             dtype_code(q), at.stream);
+  released.end();
   return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(qo);
 }
 
