@@ -619,11 +619,11 @@ def decode_step_ragged(q, k, v, k_cache, v_cache, block_table, seq_lens, turns, 
                        softcap=0.0, slopes=None, scale=None, stream=None):
     """One attention step of a serving loop: qk_norm_rope_append of the new tokens' projections
     q [B,Hq,Sq,d], k, v [B,Hkv,Sq,d], then decode_forward_ragged over the cache with them.
-    seq_lens counts the new tokens. Returns (out, lse)."""
-    q = qk_norm_rope_append(q, k, v, k_cache, v_cache, block_table, seq_lens, turns, q_weight,
-                            k_weight, eps, interleaved, rope_scale, stream)
-    return decode_forward_ragged(q, k_cache, v_cache, block_table, seq_lens, window, softcap,
-                                 slopes, scale, stream)
+    seq_lens counts the new tokens. Returns (out, lse). Arguments that either refuses are refused
+    before the caches are written."""
+    return _call("step", "decode_step_ragged", q, k, v, k_cache, v_cache, block_table, seq_lens,
+                 turns, q_weight, k_weight, eps, interleaved, rope_scale, window, softcap, slopes,
+                 scale, stream=stream)
 
 
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024   # FA_NOALLOC_SCRATCH_BYTES in include/fa.h

@@ -874,6 +874,8 @@ int fa_fwd_ragged_paged(const void* q, const void* k_cache, const void* v_cache,
       ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(seq_lens) |
         reinterpret_cast<uintptr_t>(slopes)) & 3u) != 0)
     return FA_ERR_ALIGN;
+  // (the last of the checks that depend on the caller's arguments, but for its alignment: a
+  // call without a workspace tells whether the others pass)
   const RaggedPlan rp = ragged_plan(B, Hq, Hkv, Sq, d, block_size, max_blocks);
   if (!workspace || workspace_bytes < rp.total) return FA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_ALIGN;

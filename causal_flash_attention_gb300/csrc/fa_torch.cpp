@@ -522,6 +522,53 @@ PyObject* append(PyObject* const* a) {
   return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(qo);
 }
 
+// append, then ragged over the cache with it. What either refuses is found out before the
+// append writes: the ragged call is made first without a workspace, which the library looks
+// at after everything else.
+// (handle, q, k, v, k_cache, v_cache, block_table, seq_lens, turns, q_weight, k_weight, eps,
+//  interleaved, rope_scale, window, softcap, slopes, scale, stream)
+PyObject* step(PyObject* const* a) {
+  const Library lib = library(a[0]);
+  const Tensor &q = tensor(a[1], "q"), &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
+  const Tensor &kc = tensor(a[4], "k_cache"), &vc = tensor(a[5], "v_cache");
+  const Tensor &table = tensor(a[6], "block_table"), &lens = tensor(a[7], "seq_lens");
+  const Tensor slopes = maybe(a[16], "slopes");
+  const HeadDims n = head_dims(q, k, "q");
+  const RopeArgs r = rope_inputs(n.dev, n.dt, n.B, n.S, n.d, a[8], Py_None, a[9], a[10]);
+  const CacheDims c = cache_inputs(n.dev, n.dt, n.B, n.Hkv, n.d, kc, vc, table, lens);
+  const Sizes qs = {n.B, n.Hq, n.S, n.d}, ks = {n.B, n.Hkv, n.S, n.d};
+  const fa_view vq = view("q", q, n.dev, n.dt, qs), vk = view("k", k, n.dev, n.dt, ks),
+                vv = view("v", v, n.dev, n.dt, ks);
+  if (slopes.defined()) fit("slopes", slopes, n.dev, at::kFloat, {n.Hq});
+  const float eps = real(a[11]), rope_scale = real(a[13]), softcap = real(a[15]);
+  const float scale = scale_of(a[17], n.d);
+  const bool interleaved = truth(a[12]);
+  const int window = integer(a[14]);
+  const Place at(n.dev, a[18]);
+  Released released;
+  const Tensor qo = empty(q.sizes(), n.dev, n.dt), out = empty(q.sizes(), n.dev, n.dt);
+  const Tensor lse = empty(q.sizes().slice(0, 3), n.dev, at::kFloat);
+  const Tensor ws =
+      workspace_of(lib.ragged_bytes(n.B, n.Hq, n.Hkv, n.S, n.d, c.block_size, c.max_blocks), n.dev);
+  const fa_view vqo = view("q_out", qo, n.dev, n.dt, qs, true);
+  auto attend = [&](void* workspace, size_t bytes) {
+    return lib.ragged(qo.data_ptr(), kc.data_ptr(), vc.data_ptr(), data<int>(table), data<int>(lens),
+                      out.data_ptr(), data<float>(lse), n.B, n.Hq, n.Hkv, n.S, n.d, c.block_size,
+                      c.num_blocks, c.max_blocks, window, scale, softcap, data<float>(slopes),
+                      dtype_code(q), workspace, bytes, at.stream);
+  };
+  int rc = attend(nullptr, 0);
+  if (rc == FA_ERR_WORKSPACE)
+    rc = lib.append(&vq, &vk, &vv, &vqo, kc.data_ptr(), vc.data_ptr(), data<int>(table),
+                    data<int>(lens), data<void>(r.wq), data<void>(r.wk), eps,
+                    data<unsigned long long>(r.turns), r.rope_dim, interleaved, rope_scale, n.B, n.Hq,
+                    n.Hkv, n.S, n.d, c.block_size, c.num_blocks, c.max_blocks, dtype_code(q),
+                    at.stream);
+  if (rc == FA_OK) rc = attend(ws.data_ptr(), workspace_bytes(ws, n.dev));
+  released.end();
+  return rc ? PyLong_FromLong(rc) : tensors({out, lse});
+}
+
 // ----------------------------------------------------------------- module --
 // Nothing thrown leaves a function: bad arguments become ValueError (or the
 // Python error already set), anything else RuntimeError.
@@ -562,6 +609,7 @@ PyMethodDef methods[] = {
     method<span_forward, 12>("span_forward"), method<span_backward, 17>("span_backward"),
     method<ragged, 14>("ragged"),             method<norm_rope, 13>("norm_rope"),
     method<norm_rope_bwd, 19>("norm_rope_bwd"), method<append, 16>("append"),
+    method<step, 19>("step"),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_fa_torch", nullptr, -1, methods,
