@@ -521,13 +521,16 @@ const char* fa_strerror(int code) {
   switch (code) {
     case FA_OK: return "ok";
     case FA_ERR_SHAPE:
-      return "invalid shape (B, Hq, Hkv, S >= 1, Hq % Hkv == 0, d in {64, 128}, causal Skv >= Sq)";
-    case FA_ERR_DTYPE: return "unsupported dtype (FA_F32, FA_F16 or FA_BF16)";
+      return "invalid shape (B, Hq, Hkv, S >= 1, Hq % Hkv == 0, d in {64, 128}, causal Skv >= Sq; "
+             "paged: block_size a power of two from 16 to 1024, Hq / Hkv * Sq <= 128, window >= 0; "
+             "rope_dim a multiple of 16 up to d)";
+    case FA_ERR_DTYPE: return "dtype not FA_F32, FA_F16 or FA_BF16, or one this call does not take";
     case FA_ERR_NULL: return "a required pointer is NULL";
-    case FA_ERR_ALIGN: return "a pointer is not 16-byte aligned";
-    case FA_ERR_WORKSPACE: return "workspace missing or smaller than fa_bwd_workspace_bytes()";
+    case FA_ERR_ALIGN: return "a pointer or stride is not aligned (tensors and strides 16 bytes, workspace 256, int32 and float "
+                              "arguments 4, turns 8)";
+    case FA_ERR_WORKSPACE: return "workspace missing or smaller than the call's *_workspace_bytes()";
     case FA_ERR_CUDA: return "a CUDA runtime call or kernel launch failed";
-    case FA_ERR_SCALE: return "scale must be finite and > 0";
+    case FA_ERR_SCALE: return "scale must be finite and > 0, softcap 0 or in its range, rope_scale finite, eps finite and >= 0";
     case FA_ERR_TMA: return "the driver rejected a tensor-memory-access descriptor";
     case FA_ERR_NOALLOC_LIMIT:
       return "sizes need more scratch than fa_bwd_noalloc's fixed FA_NOALLOC_SCRATCH_BYTES";

@@ -64,13 +64,15 @@ typedef enum { FA_F32 = 0, FA_F16 = 1, FA_BF16 = 2 } fa_dtype;
 enum {
   FA_OK = 0,
   FA_ERR_SHAPE = -1,        /* B, Hq, Hkv, S < 1, Hq % Hkv != 0, d not 64/128, causal with
-                               Skv < Sq (fa_*_kv), or too large */
-  FA_ERR_DTYPE = -2,        /* dtype not one of fa_dtype */
+                               Skv < Sq (fa_*_kv), a size the call refuses, or too large */
+  FA_ERR_DTYPE = -2,        /* dtype not one of fa_dtype, or one the call does not take */
   FA_ERR_NULL = -3,         /* a required pointer is NULL */
-  FA_ERR_ALIGN = -4,        /* a pointer is not 16-byte aligned */
-  FA_ERR_WORKSPACE = -5,    /* workspace NULL or smaller than fa_bwd_workspace_bytes */
+  FA_ERR_ALIGN = -4,        /* a pointer (tensors 16 bytes, workspace 256, others as stated)
+                               or a view's stride is not aligned */
+  FA_ERR_WORKSPACE = -5,    /* workspace NULL or smaller than the call's *_workspace_bytes */
   FA_ERR_CUDA = -6,         /* a CUDA runtime call or kernel launch failed */
-  FA_ERR_SCALE = -7,        /* scale not finite and > 0 */
+  FA_ERR_SCALE = -7,        /* scale not finite and > 0, or softcap, rope_scale or eps out of
+                               the call's range */
   FA_ERR_TMA = -8,          /* the driver rejected a tensor-memory-access descriptor */
   FA_ERR_NOALLOC_LIMIT = -9 /* fa_bwd_noalloc: sizes need more than FA_NOALLOC_SCRATCH_BYTES */
 };
