@@ -436,24 +436,28 @@ def key_spans(B, Sq, Skv=None, *, causal=True, window=0, doc_lens=None, prefix_l
     causal       up to the row's own position
     window       only the last `window` keys up to the row's position (0: all)
     doc_lens     lengths of the documents packed along the keys, the same in every sequence
-                 (a list) or one list per sequence: a row sees its own document only, and rows
+                 (a list or tensor) or one list per sequence: a row sees its own document only, and rows
                  outside all documents see nothing
     prefix_lens  one number, or one per sequence: the first keys (of the row's document, with
                  doc_lens) that every row sees although they lie after it
     kv_lens      one number, or one per sequence: real keys; rows and keys past them are padding
     """
     Skv = Sq if Skv is None else Skv
+    if window < 0:
+        raise ValueError("window must be >= 0")
     pos = torch.arange(Sq, dtype=torch.int64)[None, :].expand(B, Sq) + (Skv - Sq)
 
     def column(x):
         t = torch.as_tensor(x, dtype=torch.int64).reshape(-1)
         if t.numel() not in (1, B):
             raise ValueError(f"one value or {B} wanted, not {t.numel()}")
+        if (t < 0).any():
+            raise ValueError("lengths must be >= 0")
         return t[:, None].expand(B, 1)
 
     begin, last = torch.zeros(B, Sq, dtype=torch.int64), torch.full((B, Sq), Skv)
     if doc_lens is not None:
-        rows = list(doc_lens)
+        rows = [x.tolist() if isinstance(x, torch.Tensor) else x for x in doc_lens]
         if not rows or not isinstance(rows[0], (list, tuple)):
             rows = [rows] * B
         if len(rows) != B:
