@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ----------------------------------------------------- one thread per key --
-// The form for few rows (R <= NR, 16 or 32): the products are transposed, so that
+// The form for few rows (R <= NR; 16, or 32 with a cap: launch_form): the products are transposed, so that
 // the keys fill the 128 tensor-memory lanes and the rows are the short side,
 //
 //   S^T = K Q^T  (keys x NR),   O^T += V^T P  (d x NR, P as stored: rows x keys),
@@ -876,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = static_cast<int>(threadIdx.x) - 64;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t o_tmem = tmem + lane_off + 64;
-    const bool cap = p.mod.cap_in != 0.f;
+    const bool cap = NR == 32 || p.mod.cap_in != 0.f;
     const bool same_rows = p.Sq == 1 && !p.mod.slopes;   // rows do not differ in position or slope
     const float c = p.scale_log2;
     float* row_slope = reinterpret_cast<float*>(smem + Cfg::kOffRow);          // log2 domain
@@ -1187,11 +1187,21 @@ cudaError_t launch_main(Kernel kernel, const RaggedParams& p, cudaStream_t strea
   return launch_dependent(kernel, dim3(static_cast<unsigned>(p.n_ctas)), dim3(kThreads), smem, stream, p);
 }
 
+// The form by the rows R of a key/value head and whether there is a cap. Measured (us, each
+// a thread a key | a thread a row; bf16; A: 40 sequences of 4000 keys, 2 key/value heads,
+// B: one of 500 keys, 4 heads):
+//            d = 128: A    A, cap 50          B     d = 64: A    A, cap 50          B
+//   R =  4  35.9 | 41.1  36.1 | 65.8  10.1 | 11.3  26.8 | 30.6  27.4 | 56.1   9.3 | 9.4
+//   R = 16  39.4 | 42.5  39.5 | 66.9  11.5 | 11.3  31.9 | 30.7  32.4 | 56.1  11.1 | 9.4
+//   R = 20  51.1 | 43.2  54.4 | 67.4  14.4 | 12.0  39.2 | 31.0  42.9 | 56.0  13.5 | 9.8
+//   R = 32  63.9 | 45.0  64.5 | 68.9  16.2 | 11.6  48.5 | 32.0  51.6 | 56.8  15.4 | 9.5
+// A thread a key shares the exponentials of few rows among four warps; its work grows with
+// the rows, that of a thread a row does not, until a cap doubles the special functions.
 template <int D, bool kBf16, bool kLargeCap>
 cudaError_t launch_form(const RaggedParams& p, cudaStream_t stream) {
   if (p.R <= 16)
     return launch_main<RagTCfg<D, 16>::kSmemBytes>(fa_ragged_keys_kernel<D, 16, kBf16, kLargeCap>, p, stream);
-  if (p.R <= 32)
+  if (p.R <= 32 && p.mod.cap_in != 0.f)
     return launch_main<RagTCfg<D, 32>::kSmemBytes>(fa_ragged_keys_kernel<D, 32, kBf16, kLargeCap>, p, stream);
   return launch_main<RagCfg<D>::kSmemBytes>(fa_ragged_kernel<D, kBf16, kLargeCap>, p, stream);
 }
