@@ -521,9 +521,12 @@ def rope_inv_freq(rope_dim, base=10000.0, scaling="none", factor=1.0, trained_le
     none    base^(-2i / rope_dim)
     linear  all frequencies divided by factor (positions interpolated)
     base    the base raised so that the slowest frequency is divided by factor
-    parts   YaRN (Peng et al., 2023): frequencies that turn more than high_turns times within
-            trained_len stay, those that turn less than low_turns times are divided by factor,
-            linear in between; rope_scale = 0.1 ln(factor) + 1
+    parts   YaRN as the paper writes it (Peng et al., 2023): frequencies that turn more than
+            high_turns times within trained_len stay, those that turn less than low_turns times
+            are divided by factor, in between linear in the number of turns;
+            rope_scale = 0.1 ln(factor) + 1. (Programs that run published checkpoints often take
+            a ramp linear in the pair's index instead, which gives other frequencies in between:
+            pass such a table to rope_turns.)
     """
     if rope_dim < 2 or rope_dim % 2:
         raise ValueError("rope_dim must be even and positive")

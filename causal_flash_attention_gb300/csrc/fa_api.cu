@@ -442,8 +442,12 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* out, const
     pre.key_end = mod->key_end;
     p.spans = pre.spans = reinterpret_cast<int2*>(wsb + sws.spans);
     p.plan = pre.plan = reinterpret_cast<int2*>(wsb + sws.plan);
-    // a list for up to four items an SM: 512 items of documents take 295 us with it
-    // and 319 without, 768 short items of a window 63.9 and 60.4
+    // A list for up to four items an SM. It pays where items are long and uneven, and costs
+    // its making where they are short and alike; their lengths are known on the device only.
+    // With it and without: 512 items of documents (8192 tokens, 8 key/value heads, d = 128)
+    // 319 and 330 us, of 4096 causal tokens (16 heads) 184 and 181, of a window of 256 (8192
+    // tokens, 8 heads, d = 64) 63.5 and 60.2; 768 of documents 141 and 143, of the window 77.7
+    // and 74.2; 1024 of it (d = 128) 131 and 127.5.
     const long long tiles = static_cast<long long>(B) * pre.n_kv_tiles;
     p.listed = tiles <= kListTiles && tiles * Hkv <= 4 * kDecodeWaveCtas;
     p.n_slots = kDecodeWaveCtas;

@@ -244,9 +244,10 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // the next kernel's blocks may take their places beside this grid's where it leaves room
-  // on every SM (77 rows: 4.9 us a call, 5.4 without), not in a grid of more (documents,
-  // forward and backward: 407 us, 402 without)
+  // the next kernel's blocks may take their places beside this grid's where it has at most
+  // one block an SM (77 rows: 4.9 us a call, 5.4 without; in a captured graph the same within
+  // 1%), not beside more, although two fit (512 rows of 50 heads, 200 blocks: 11.8 us, 10.3
+  // without; of 76 heads, 304 blocks: 13.6, 11.2; documents, forward and backward: 407, 402)
   if constexpr (kSpan)
     if (gridDim.x <= 152) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if constexpr (kSpan) {

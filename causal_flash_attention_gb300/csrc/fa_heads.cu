@@ -30,9 +30,9 @@
 //
 // Everything is bound by the bytes of x and y as long as a group costs few
 // instructions: a form that found token and head of every group by division ran
-// at a quarter of this one's rate. At 8192 tokens, 32 + 8 heads, d = 128: forward 32.4 us
-// in bf16 (168 MB, 5.2 TB/s) and 55.3 us in fp32 (6.1 TB/s), backward 56.7 us (252 MB,
-// 4.4 TB/s: a group is still about 165 instructions there) and 88.5 us (5.7 TB/s).
+// at a quarter of this one's rate. At 8192 tokens, 32 + 8 heads, d = 128: forward 32.0 us
+// in bf16 (168 MB, 5.2 TB/s) and 54.3 us in fp32 (6.2 TB/s), backward 57.0 us (252 MB,
+// 4.4 TB/s: a group is still about 165 instructions there) and 87.5 us (5.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -160,10 +160,10 @@ __device__ __forceinline__ void fill_table(const HeadsParams& p, float2* table, 
 
 // Forward: this lane's two chunks of 4 elements of its head. In the rotated part's half
 // layout they are each other's partners (chunk A in the first half, B in the second);
-// past the rotated part, and interleaved, they follow each other. Against one chunk of
-// 8 and shuffles for the partners (the backward's layout): 40.0 -> 32 us at 8192 tokens, 32 +
-// 8 heads, d = 128, bf16. The backward, with its loads of two tensors and more values
-// to keep, loses what it gains (59 us with shuffles, 64 to 80 without).
+// past the rotated part, and interleaved, they follow each other. One chunk of 8 and
+// shuffles for the partners (the backward's layout) take a quarter longer at 8192 tokens,
+// 32 + 8 heads, d = 128, bf16. The backward, with its loads of two tensors and more values
+// to keep, loses what it gains (8 to 35% slower without shuffles).
 template <int D>
 struct Chunks {
   int a, b;            // first element of each chunk
@@ -303,11 +303,11 @@ __device__ __forceinline__ float dot(const uint64_t (&a)[4], const uint64_t (&b)
 // Tokens a block takes at a time, at most (its table: kTokens * d / 2 pairs).
 constexpr int kTokens = 8;
 // Resident blocks an SM and groups a warp has in flight (16-bit types; fp32, with
-// twice the bytes a group, half). Measured at 8192 tokens, 32 + 8 heads, d = 128,
-// bf16: forward 32.7 us with 4 blocks and 4 groups, 34.9 with 4 and 3, 37.7 with 3
-// and 5, 49.5 with 5 and 3 (registers spill, as they do with 4 and 4 in the appending
-// form, which takes 3); backward, persistent, 59.2 us with 2 blocks and 4 groups (each
-// a dy and an x), 66 with 2 and 3, 83 with 3 and 4.
+// twice the bytes a group, half). Against these, at 8192 tokens, 32 + 8 heads, d = 128,
+// bf16: forward, 4 blocks and 4 groups, 7% longer with 4 and 3, 15% with 3 and 5, 51%
+// with 5 and 3 (registers spill, as they do with 4 and 4 in the appending form, which
+// takes 3); backward, persistent, 2 blocks and 4 groups (each a dy and an x), 11%
+// longer with 2 and 3, 40% with 3 and 4.
 constexpr int kFwdBlocks = 4, kFwdFlight = 4;
 constexpr int kBwdBlocks = 2, kBwdFlight = 4;
 // Warps an SM up to which tokens are spread over more warps than one: a warp's
@@ -364,9 +364,11 @@ __global__ void __launch_bounds__(32 * kWarpsH, kFwdBlocks)
   const int b = live ? static_cast<int>(token / p.S) : 0;
   const int s = live ? static_cast<int>(token - static_cast<unsigned>(b) * p.S) : 0;
   wait_for_kernel_before();
-  // Where the grid leaves room on every SM, the next kernel's blocks may take their
-  // places beside this one's (16 tokens into the cache: 4.0 us a call, 4.3 without); with
-  // more blocks they would fill the SMs unevenly (3075 tokens: 8.5 us, 7.4 without).
+  // Where there is at most one block an SM, the next kernel's blocks may take their
+  // places beside this one's (16 tokens into the cache: 4.0 us a call, 4.3 without; 16 tokens
+  // of 32 + 8 heads 2.76, 2.85); with more blocks they would fill the SMs unevenly (375 blocks,
+  // 1500 tokens of 12 + 12 heads, d = 64: 5.3 us, 4.6 without; 300 to 600 tokens of 32 + 8
+  // heads within 2% either way; 3075 tokens 8.5, 7.4 without).
   if (gridDim.x * gridDim.y <= kSms) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const T* in;

@@ -18,12 +18,19 @@
 //     last of a share) write a partial result, which the merge kernel joins in
 //     the order of the shares, so results do not depend on scheduling.
 //
-// The kernel is bound by the bytes of K and V (G * Sq <= 128 rows share each
-// tile): at 32 + 8 heads, d = 128, bf16, 16 sequences of 4096 keys take 51.8 us (5.2
-// TB/s) and of 8192 keys 89.7 us (6.0 TB/s). About 10 us of each call are the scan, the first
-// loads, the unequal ends and the merge; one sequence of 500 keys takes 10. Rows of the cache outside a sequence's keys (the tail of its last page,
-// keys before every row's window) are cleared in the V tile before use, so that
-// whatever they hold, NaN included, cannot reach O through a probability of 0.
+// Up to 16 rows a key/value head (G * Sq <= 128 rows share each tile) the kernel is bound by
+// the bytes of K and V: at 32 + 8 heads, d = 128, bf16, 16 sequences of 4096 keys take 50.8 us
+// (5.3 TB/s) and of 8192 keys 88.8 us (6.0 TB/s). About 10 us of each call are the scan, the
+// first loads, the unequal ends and the merge; one sequence of 500 keys takes 9. With more
+// rows the softmax counts (the figures stand at launch_form).
+//
+// Rows of the cache outside a sequence's keys (the tail of its last page, keys before
+// every row's window) are cleared in the V tile before use, so that whatever they hold, NaN
+// included, cannot reach O through a probability of 0. A NaN among the scores that a row
+// sees comes out as NaN in its out and its LSE, through the merge too.
+//
+// A row's last bits depend on where the shares cut its keys, and so on the lengths of the
+// other sequences.
 //
 // Warp roles and tensor memory: as fa_decode.cu.
 #include <algorithm>

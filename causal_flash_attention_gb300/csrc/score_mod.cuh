@@ -49,8 +49,10 @@ __device__ __forceinline__ float cap_r(float s, float cap_in) {
 
 // The cap by a polynomial where the warp's scores allow it, u = s * scale / softcap:
 // tanh u = u (a0 + a1 w + ...), w = u^2, minimax fits (by reweighted least squares) of
-// degree 9 for |u| <= 3/4, off by 1.9e-7, 2.6e-7 in fp32, and of degree 5 for
-// |u| <= 0.3, off by 1.7e-7, 1.9e-7 in fp32. No special function, which the softmax is
+// degree 9 for |u| <= 3/4, off by 2.1e-7, 2.9e-7 in fp32, and of degree 5 for
+// |u| <= 0.3, off by 1.7e-7, 2.1e-7 in fp32 (of tanh u itself by 2.8e-6 and 4.0e-6 at most,
+// for small u). The greatest score counts masked keys too, so a row's last bits may
+// depend on what stands beside it. No special function, which the softmax is
 // short of; the coefficients come with the powers of scale / softcap and softcap *
 // log2(e) multiplied in, so y = softcap log2(e) tanh u directly from the unscaled score.
 template <int N>

@@ -305,7 +305,8 @@ int fa_qk_norm_rope_append(const fa_view* q, const fa_view* k, const fa_view* v,
  * runs: it needs no host copy of them, and a captured graph may be replayed
  * after they change. All key tiles
  * of all sequences are shared out evenly over one wave of CTAs whatever the
- * lengths are. Results are the same bits on every call.
+ * lengths are. Results are the same bits on every call with the same lengths (where
+ * a row's keys are cut, and so its last bits, goes by the lengths of all sequences).
  *
  * Only table entries of pages that hold a key some row sees are read; an entry
  * outside [0, num_blocks) reads as zeros. The rest of the cache, rows of a
@@ -356,7 +357,8 @@ size_t fa_fwd_ragged_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int d
  *
  * Masked positions: a masked probability of 0 still multiplies V (forward) and
  * dO, Q, K (backward) of the same 128-row tile, so q, k, v, out and dout must
- * be finite everywhere, padding included.
+ * be finite everywhere, padding included. (A NaN score that a row sees gives NaN in
+ * its out and lse, as in fa_fwd, and NaN gradients at least where they depend on it.)
  *
  * FA_BF16 and FA_F16 only (FA_F32 gives FA_ERR_DTYPE). softcap must be 0, or it
  * and scale / softcap within 2^-60 .. 2^60 (else FA_ERR_SCALE). A capped score is
