@@ -31,6 +31,7 @@ LIB = os.path.join(PKG, "libfa.so")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_pair.cu", "fa_bwd.cu", "fa_simt.cu", "fa_noalloc.cu",
            "fa_decode.cu", "fa_ragged.cu", "fa_heads.cu"]
 HEADERS = ["ptx.cuh", "score_mod.cuh", "span_plan.cuh", "fa_internal.h", "fa_decode.h", "fa_ragged.h", "fa_heads.h",
+           "ragged_shares.cuh",
            os.path.join("..", "..", "include", "fa.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

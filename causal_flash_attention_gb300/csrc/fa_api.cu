@@ -22,15 +22,6 @@ namespace fa {
 // up a wait instead of hanging.
 __device__ int g_status;
 
-namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = [] {
     void* f = nullptr;
@@ -47,7 +38,7 @@ EncodeTiledFn encode_fn() {
 // Device address of g_status on the current device, looked up once per
 // device (the lookup is a runtime call worth microseconds of host time).
 constexpr int kMaxDevices = 128;
-std::atomic<int*> g_status_ptr[kMaxDevices];
+static std::atomic<int*> g_status_ptr[kMaxDevices];
 
 int* status_ptr() {
   int dev = -1;
@@ -58,6 +49,10 @@ int* status_ptr() {
   g_status_ptr[dev].store(p, std::memory_order_release);
   return p;
 }
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
 
 // 3-D view [rows = BH][S][d] of a contiguous 16-bit tensor; box = 64 columns
 // (128 bytes, one swizzle span) x 128 sequence rows x 1 head.

@@ -167,6 +167,15 @@ int check_bwd_args(const void* q, const void* k, const void* v, const void* out,
                    const void* dv, int B, int Hq, int Hkv, int Sq, int Skv, int d, int causal,
                    float scale, int dtype);
 
+// The driver's descriptor encoder and the current device's status word (null: not to be
+// had). Defined in fa_api.cu.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+int* status_ptr();
+
 // Launchers; each returns a cudaError_t from the launch.
 cudaError_t launch_fwd_tc(const FwdParams& p, int d, bool bf16, cudaStream_t stream);
 cudaError_t launch_fwd_span(const FwdParams& p, int d, bool bf16, cudaStream_t stream);

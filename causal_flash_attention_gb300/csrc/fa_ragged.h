@@ -10,6 +10,7 @@ namespace fa {
 // head, the tiles of 128 keys that its new rows see. The list is cut into even
 // shares, one a CTA.
 struct RaggedParams {
+  static constexpr int kTileKeys = kTileN;
   CUtensorMap tm_k;   // [num_blocks*Hkv][block_size][d], box (64, box_rows, 1), 128B swizzle
   CUtensorMap tm_v;
   const void* q;      // [B*Hq][Sq][d]
