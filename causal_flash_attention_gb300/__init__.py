@@ -11,8 +11,8 @@ kernels; there is no other code path. `attention_forward` / `attention_backward`
 additionally allocate their outputs (and the backward workspace) with
 PyTorch.
 
-The calls for span attention, the ragged paged cache and query/key preparation
-go through a native module beside the library (_fa_torch, csrc/fa_torch.cpp), which
+The calls for span attention, the ragged paged cache, query/key preparation and latent
+attention go through a native module beside the library (_fa_torch, csrc/fa_torch.cpp), which
 checks the tensors, allocates what is missing and makes the library call: one of
 them is a few microseconds of host time.
 
@@ -39,7 +39,10 @@ __all__ = [
     "fa_fwd_ragged_paged_workspace_bytes", "decode_forward_ragged", "fa_qk_norm_rope",
     "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_bytes", "fa_qk_norm_rope_append",
     "qk_norm_rope_forward", "qk_norm_rope_backward", "qk_norm_rope_append", "rope_inv_freq",
-    "rope_turns", "decode_step_ragged",
+    "rope_turns", "decode_step_ragged", "fa_fwd_latent", "fa_bwd_latent",
+    "fa_bwd_latent_workspace_bytes", "attention_latent_forward", "attention_latent_backward",
+    "fa_fwd_latent_paged", "fa_fwd_latent_paged_workspace_bytes", "decode_latent_paged",
+    "fa_latent_append", "latent_append", "tree_masks",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa.so")
@@ -108,6 +111,19 @@ def lib() -> ctypes.CDLL:
     L.fa_qk_norm_rope_append.argtypes = ([vw] * 4 + [vp] * 6 + [f32, vp, i32, i32, f32]
                                          + [i32] * 9 + [vp])
     L.fa_qk_norm_rope_append.restype = i32
+    L.fa_fwd_latent.argtypes = [vw] * 4 + [vp, vp, vw, vp] + [i32] * 5 + [f32, i32, vp]
+    L.fa_fwd_latent.restype = i32
+    L.fa_bwd_latent_workspace_bytes.argtypes = [i32] * 5
+    L.fa_bwd_latent_workspace_bytes.restype = sz
+    L.fa_bwd_latent.argtypes = ([vw] * 4 + [vp, vp, vw, vw, vp] + [vw] * 4 + [i32] * 5
+                                + [f32, i32, vp, sz, vp])
+    L.fa_bwd_latent.restype = i32
+    L.fa_fwd_latent_paged.argtypes = ([vw] + [vp] * 6 + [i32] * 8 + [f32, i32, vp, sz, vp])
+    L.fa_fwd_latent_paged.restype = i32
+    L.fa_fwd_latent_paged_workspace_bytes.argtypes = [i32] * 6
+    L.fa_fwd_latent_paged_workspace_bytes.restype = sz
+    L.fa_latent_append.argtypes = ([vw] * 4 + [vp] * 5 + [f32, vp, i32, f32] + [i32] * 8 + [vp])
+    L.fa_latent_append.restype = i32
     L.fa_strerror.argtypes = [i32]
     L.fa_strerror.restype = ctypes.c_char_p
     L.fa_last_device_status.argtypes = [vp, ctypes.POINTER(i32)]
@@ -631,6 +647,117 @@ def decode_step_ragged(q, k, v, k_cache, v_cache, block_table, seq_lens, turns, 
     return _call("step", "decode_step_ragged", q, k, v, k_cache, v_cache, block_table, seq_lens,
                  turns, q_weight, k_weight, eps, interleaved, rope_scale, window, softcap, slopes,
                  scale, stream=stream)
+
+
+# ------------------------------------------------------- latent attention --
+def fa_fwd_latent(q, k, k_rope, v, key_begin, key_end, out, lse, scale=None, stream=None):
+    """Call fa_fwd_latent: q [B,H,Sq,d+64], k and v [B,H,Skv,d], k_rope [B,Skv,64] shared by the
+    heads (views of any positive strides but the last); key_begin and key_end int32 [B,Sq] as for
+    fa_fwd_span, or None twice: causal; out [B,H,Sq,d] a view, lse float32 [B,H,Sq]. scale
+    defaults to (d + 64)^-1/2."""
+    _given(out=out, lse=lse)
+    _call("latent_forward", "fa_fwd_latent", q, k, k_rope, v, key_begin, key_end, out, lse, scale,
+          stream=stream)
+
+
+def fa_bwd_latent_workspace_bytes(B, H, Sq, Skv, d) -> int:
+    return int(lib().fa_bwd_latent_workspace_bytes(B, H, Sq, Skv, d))
+
+
+def fa_bwd_latent(q, k, k_rope, v, key_begin, key_end, out, dout, lse, dq, dk, dk_rope, dv,
+                  workspace, scale=None, stream=None):
+    """Call fa_bwd_latent; gradients are views laid out like their tensors, `workspace` a device
+    tensor of at least fa_bwd_latent_workspace_bytes(...) bytes."""
+    _given(dq=dq, dk=dk, dk_rope=dk_rope, dv=dv, workspace=workspace)
+    _call("latent_backward", "fa_bwd_latent", q, k, k_rope, v, key_begin, key_end, out, dout, lse,
+          dq, dk, dk_rope, dv, workspace, scale, stream=stream)
+
+
+def attention_latent_forward(q, k, k_rope, v, key_begin=None, key_end=None, scale=None,
+                             stream=None):
+    """Allocate out (laid out [B,Sq,H,d] in memory, as an output projection takes it) and lse and
+    run fa_fwd_latent. Returns (out, lse)."""
+    return _call("latent_forward", "fa_fwd_latent", q, k, k_rope, v, key_begin, key_end, None, None,
+                 scale, stream=stream)
+
+
+def attention_latent_backward(q, k, k_rope, v, out, dout, lse, key_begin=None, key_end=None,
+                              scale=None, dq=None, dk=None, dk_rope=None, dv=None, workspace=None,
+                              stream=None):
+    """Allocate the gradients that are not given (tokens first in memory, as projections give
+    q, k and v) and the workspace, and run fa_bwd_latent. Returns (dq, dk, dk_rope, dv)."""
+    return _call("latent_backward", "fa_bwd_latent", q, k, k_rope, v, key_begin, key_end, out, dout,
+                 lse, dq, dk, dk_rope, dv, workspace, scale, stream=stream)
+
+
+def fa_fwd_latent_paged_workspace_bytes(B, H, Sq, rank, block_size, max_blocks) -> int:
+    return int(lib().fa_fwd_latent_paged_workspace_bytes(B, H, Sq, rank, block_size, max_blocks))
+
+
+def fa_fwd_latent_paged(q, cache, block_table, seq_lens, out, lse, workspace, scale, window=0,
+                        tree_masks=None, stream=None):
+    """Call fa_fwd_latent_paged: absorbed queries q [B,H,Sq,rank+64] (a view), the last Sq tokens
+    of each sequence; cache [num_blocks,block_size,rank+64]; block_table int32 [B,max_blocks];
+    seq_lens int32 [B]; tree_masks int64 [B,Sq] or None; out [B,H,Sq,rank]; `workspace` a device
+    tensor of at least fa_fwd_latent_paged_workspace_bytes(...) bytes."""
+    _given(out=out, lse=lse, workspace=workspace)
+    _call("latent_paged", "fa_fwd_latent_paged", q, cache, block_table, seq_lens, tree_masks, out,
+          lse, workspace, window, scale, stream=stream)
+
+
+def decode_latent_paged(q, cache, block_table, seq_lens, scale, window=0, tree_masks=None,
+                        stream=None):
+    """Allocate out, lse and the workspace and run fa_fwd_latent_paged. Returns (out, lse). scale
+    is that of the queries before they were absorbed, (d + 64)^-1/2 for heads of d + 64."""
+    return _call("latent_paged", "fa_fwd_latent_paged", q, cache, block_table, seq_lens, tree_masks,
+                 None, None, None, window, scale, stream=stream)
+
+
+def fa_latent_append(latent, k_rope, q_rope, q_out, cache, block_table, seq_lens, turns,
+                     weight=None, eps=1e-6, positions=None, interleaved=False, rope_scale=1.0,
+                     stream=None):
+    """Call fa_latent_append: the last Sq tokens of sequences of seq_lens tokens; views latent
+    [B,Sq,rank], k_rope [B,Sq,64], q_rope and q_out [B,H,Sq,64]; cache [num_blocks,block_size,
+    rank+64] written in place; turns as from rope_turns (32 of them); weight [rank] of the norm or
+    None; positions int32 [B,Sq] or None (a token's place in its sequence)."""
+    _given(q_out=q_out)
+    _call("latent_append", "fa_latent_append", latent, k_rope, q_rope, q_out, cache, block_table,
+          seq_lens, positions, weight, turns, eps, interleaved, rope_scale, stream=stream)
+
+
+def latent_append(latent, k_rope, q_rope, cache, block_table, seq_lens, turns, weight=None,
+                  eps=1e-6, positions=None, interleaved=False, rope_scale=1.0, q_out=None,
+                  stream=None):
+    """Allocate q_out (unless given, e.g. as the last 64 elements of the absorbed queries) and run
+    fa_latent_append, which writes the tokens' latents and key parts into the cache. Returns
+    q_out."""
+    return _call("latent_append", "fa_latent_append", latent, k_rope, q_rope, q_out, cache,
+                 block_table, seq_lens, positions, weight, turns, eps, interleaved, rope_scale,
+                 stream=stream)
+
+
+def tree_masks(parents, device=None):
+    """(masks, depths) of drafted tokens that form trees: parents [B,Sq] (or [Sq]) gives every
+    token's parent among its sequence's drafted tokens, which comes before it, or -1. masks
+    int64 [B,Sq]: bit t of masks[b,s] is set where token t is s or one of its ancestors, as
+    decode_latent_paged takes them; depths int32 [B,Sq]: 0 at a root (a token's position is the
+    position of the first drafted token plus its depth)."""
+    rows = torch.as_tensor(parents, dtype=torch.int64, device="cpu")
+    rows = rows[None] if rows.dim() == 1 else rows
+    if rows.dim() != 2 or not 1 <= rows.shape[1] <= 64:
+        raise ValueError("parents must be [B, Sq] with 1 to 64 drafted tokens")
+    masks, depths = [], []
+    for row in rows.tolist():
+        m, d = [], []
+        for s, up in enumerate(row):
+            if not -1 <= up < s:
+                raise ValueError("a token's parent must come before it, or be -1")
+            m.append((1 << s) | (m[up] if up >= 0 else 0))
+            d.append(d[up] + 1 if up >= 0 else 0)
+        masks.append([x - (1 << 64) if x >= 1 << 63 else x for x in m])   # the same bits, signed
+        depths.append(d)
+    return (torch.tensor(masks, dtype=torch.int64, device=device),
+            torch.tensor(depths, dtype=torch.int32, device=device))
 
 
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024   # FA_NOALLOC_SCRATCH_BYTES in include/fa.h

@@ -1,0 +1,735 @@
+// Backward of latent attention in its expanded form (fa_latent_fwd.cu). With the shared
+// rotated part written as the last 64 columns of every head's key, K'_j = [K_j, KR_j],
+//
+//   p_ij = e^(s_ij - L_i), ds_ij = p_ij (<dO_i, V_j> - D_i), D_i = <dO_i, O_i>,
+//   dQ_i = scale sum_j ds_ij K'_j, [dK_j, dKR_j of the head] = scale sum_i ds_ij Q_i,
+//   dV_j = sum_i p_ij dO_i, dKR_j = sum over the heads.
+//
+// Two kernels, each of which recomputes S and dP, instead of one that keeps everything: dK'
+// (192 columns at d = 128) and dV leave no room in tensor memory for a dQ of 192 columns
+// beside S and dP, and a dQ kernel of its own needs no sum over key tiles in global
+// memory (so gradients have the same bits on every call). Two products more of seven.
+//   1. dQ:      a CTA per 128 query rows walks their key tiles; it also forms D and leaves
+//               it with L and the rows' key ranges for the second.
+//   2. dK, dV:  a CTA per 128 keys of a head walks the query rows, 64 at a time.
+//   3. dKR:     adds up the heads' parts, in head order.
+// Warp roles of 1 and 2: warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 softmax
+// gradient, two warps a tensor-memory lane quarter with half the columns each. P and dS
+// go back to tensor memory as the A operands of the products, so shared memory holds
+// only what TMA loads.
+#include <algorithm>
+#include <type_traits>
+
+#include "fa_latent.h"
+#include "ptx.cuh"
+#include "score_mod.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreadsB = 320;
+constexpr float kLog2eB = 1.4426950408889634f;
+
+__device__ __forceinline__ void drain_wait_b(uint32_t bar, uint32_t parity, int* status) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > kDrainLimitCycles) {
+      atomicOr(status, kStatusWaitTimeout);
+      return;
+    }
+  }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float dot16(const uint4& a, const uint4& b, float s) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 u = unpack2<kBf16>(x[e]), v = unpack2<kBf16>(y[e]);
+    s = fmaf(u.x, v.x, s);
+    s = fmaf(u.y, v.y, s);
+  }
+  return s;
+}
+
+// 32 accumulator columns times f, rounded, to 32 consecutive elements of a row.
+template <bool kBf16>
+__device__ __forceinline__ void store32(void* row, const uint32_t (&o)[32], float f) {
+  uint4* dst = static_cast<uint4*>(row);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = pack2<kBf16>(__uint_as_float(o[8 * v + 2 * e]) * f, __uint_as_float(o[8 * v + 2 * e + 1]) * f);
+    dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// --------------------------------------------------------------------- dQ --
+// Tensor memory: S [0, 128), dP [128, 256), dQ [256, 256 + d + 64), dS (16-bit) [448, 512).
+// S and dP of the next tile are formed while the warps work on this tile's, which they
+// have copied to registers.
+template <int D>
+struct LatDqCfg {
+  static constexpr int kW = D + kRope;                  // columns of a key
+  static constexpr int kKChunks = kW / kChunk, kVChunks = D / kChunk;
+  static constexpr int CB = kTileN * 128;
+  static constexpr int kKBytes = kKChunks * CB, kVBytes = kVChunks * CB;
+  static constexpr int NK = 2, NV = D == 128 ? 1 : 2;
+  static constexpr int kOffDO = kKBytes;                // Q first
+  static constexpr int kOffK = kOffDO + kVBytes;
+  static constexpr int kOffV = kOffK + NK * kKBytes;
+  static constexpr int kOffBar = kOffV + NV * kVBytes;
+  // q_full, k_full[], k_empty[], v_full[], v_empty[], s_full, dp_full, s_free, ds_full, dq_done, drain
+  static constexpr int kNumBars = 1 + 2 * NK + 2 * NV + 6;
+  static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
+  static constexpr int kOffSpan = kOffMisc + 16;        // 4 warps' (begin, end)
+  static constexpr int kOffDelta = kOffSpan + 32;       // [2][128] halves of D
+  static constexpr int kSmemBytes = kOffDelta + 1024;
+  static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+};
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreadsB, 1)
+    latent_dq_kernel(const __grid_constant__ LatentBwdParams p) {
+  using Cfg = LatDqCfg<D>;
+  constexpr int NK = Cfg::NK, NV = Cfg::NV, CB = Cfg::CB, W = Cfg::kW;
+  using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {   // the 128-byte swizzle needs 1024-byte aligned tiles
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusBadLaunch);
+    return;
+  }
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
+  int2* ranges = reinterpret_cast<int2*>(smem + Cfg::kOffSpan);
+  float* halves = reinterpret_cast<float*>(smem + Cfg::kOffDelta);
+
+  const uint32_t q_full = sbase + Cfg::kOffBar;
+  auto bars = [&](int first) { return [=](int i) { return q_full + 8 * (first + i); }; };
+  const auto k_full = bars(1), k_empty = bars(1 + NK), v_full = bars(1 + 2 * NK);
+  const auto v_empty = bars(1 + 2 * NK + NV);
+  const uint32_t s_full = q_full + 8 * (1 + 2 * NK + 2 * NV);
+  const uint32_t dp_full = s_full + 8, s_free = s_full + 16, ds_full = s_full + 24;
+  const uint32_t dq_done = s_full + 32, drain = s_full + 40;
+
+  const int warp = static_cast<int>(warp_id());
+  const int lane = static_cast<int>(lane_id());
+  const int BH = p.B * p.H;
+  const int unit = p.n_units - 1 - static_cast<int>(blockIdx.x) / BH;   // heaviest first
+  const int bh = static_cast<int>(blockIdx.x) % BH;
+  const int b = bh / p.H, h = bh % p.H;
+  const int q0 = unit * kTileM;
+  const int quarter = warp & 3, half = (warp - 2) >> 2;
+  const int row = q0 + quarter * 32 + lane;
+
+  int row_lo = 0, row_hi = 0;
+  float l2 = INFINITY;
+  if (warp >= 2) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int2 s = p.mask.span(b, row);
+    row_lo = s.x;
+    row_hi = s.y;
+    if (half == 0) {
+      const int lo = __reduce_min_sync(0xffffffffu, row_hi > 0 ? row_lo : 0x7fffffff);
+      const int hi = __reduce_max_sync(0xffffffffu, row_hi);
+      if (lane == 0) ranges[quarter] = make_int2(lo, hi);
+    }
+    // this thread's half of D, and L
+    float d = 0.f;
+    if (row < p.mask.Sq) {
+      const Elem* o = static_cast<const Elem*>(p.out.data) + b * p.out.sb + h * p.out.sh + row * p.out.ss + half * (D / 2);
+      const Elem* g = static_cast<const Elem*>(p.dout.data) + b * p.dout.sb + h * p.dout.sh + row * p.dout.ss + half * (D / 2);
+#pragma unroll
+      for (int u = 0; u < D / 16; ++u)
+        d = dot16<kBf16>(reinterpret_cast<const uint4*>(o)[u], reinterpret_cast<const uint4*>(g)[u], d);
+      l2 = p.lse[static_cast<size_t>(bh) * p.mask.Sq + row] * kLog2eB;
+      if (row_hi == 0) l2 = INFINITY;   // sees nothing: P = 0
+    }
+    halves[half * 128 + quarter * 32 + lane] = d;
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < NK; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+    }
+    for (int s = 0; s < NV; ++s) {
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(s_free, 8);   // one arrival per compute warp
+    mbar_init(ds_full, 8);
+    mbar_init(dq_done, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    mbar_arrive_expect_tx(q_full, Cfg::kKBytes + Cfg::kVBytes);
+    for (int r = 0; r < 2; ++r) {
+      for (int c = 0; c < Cfg::kKChunks; ++c)
+        tma_load_4d(sbase + c * CB + r * (CB / 2), &p.tm_q, q_full, c * kChunk, q0 + r * 64, h, b);
+      for (int c = 0; c < Cfg::kVChunks; ++c)
+        tma_load_4d(sbase + Cfg::kOffDO + c * CB + r * (CB / 2), &p.tm_do, q_full, c * kChunk, q0 + r * 64, h, b);
+    }
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_kr);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  int lo = 0x7fffffff, hi = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    lo = min(lo, ranges[w].x);
+    hi = max(hi, ranges[w].y);
+  }
+  const int tile0 = hi > 0 ? lo / kTileN : 0;
+  const int n = hi > 0 ? (hi + kTileN - 1) / kTileN - tile0 : 0;
+
+  if (warp == 0) {
+    // ===================== TMA producer =====================
+    if (lane == 0) {
+      if (n == 0) drain_wait_b(q_full, 0, p.status);   // no product waits for the queries
+      int jk = 0, jv = 0;
+      while (jk < n) {
+        const int sk = jk % NK, sv = jv % NV;
+        const int y = (tile0 + jk) * kTileN;
+        if (jk >= NK && !mbar_wait(k_empty(sk), (jk / NK - 1) & 1, abort_flag, p.status)) break;
+        mbar_arrive_expect_tx(k_full(sk), Cfg::kKBytes);
+        for (int c = 0; c < Cfg::kVChunks; ++c)
+          tma_load_4d(sbase + Cfg::kOffK + sk * Cfg::kKBytes + c * CB, &p.tm_k, k_full(sk), c * kChunk, y, h, b);
+        tma_load_4d(sbase + Cfg::kOffK + sk * Cfg::kKBytes + Cfg::kVChunks * CB, &p.tm_kr, k_full(sk), 0, y, 0, b);
+        ++jk;
+        if (jv >= NV && !mbar_wait(v_empty(sv), (jv / NV - 1) & 1, abort_flag, p.status)) break;
+        mbar_arrive_expect_tx(v_full(sv), Cfg::kVBytes);
+        for (int c = 0; c < Cfg::kVChunks; ++c)
+          tma_load_4d(sbase + Cfg::kOffV + sv * Cfg::kVBytes + c * CB, &p.tm_v, v_full(sv), c * kChunk, y, h, b);
+        ++jv;
+      }
+      if (*abort_flag) {
+        // let every copy already issued land before the CTA releases its memory
+        drain_wait_b(q_full, 0, p.status);
+        for (int j = max(0, jk - NK); j < jk; ++j) drain_wait_b(k_full(j % NK), (j / NK) & 1, p.status);
+        for (int j = max(0, jv - NV); j < jv; ++j) drain_wait_b(v_full(j % NV), (j / NV) & 1, p.status);
+      }
+    }
+  } else if (warp == 1) {
+    // ===================== MMA issuer =====================
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t idesc_s = make_idesc(128, kTileN, kBf16, false, false);
+      constexpr uint32_t idesc_q = make_idesc(128, W, kBf16, false, true);
+      constexpr uint64_t kStep = CB >> 4;
+      const uint64_t qa = make_sdesc(sbase, 16, 1024);
+      const uint64_t oa = make_sdesc(sbase + Cfg::kOffDO, 16, 1024);
+      bool ok = mbar_wait(q_full, 0, abort_flag, p.status);
+#ifdef FA_WAIT_TEST
+      // wait-limit test build: nothing completes this phase before the abort
+      // path's own commit, so the wait runs out
+      if (ok) ok = mbar_wait(drain, 0, abort_flag, p.status);
+#endif
+      auto scores = [&](int j) -> bool {   // S = Q K'_j^T, dP = dO V_j^T
+        if (!mbar_wait(k_full(j % NK), (j / NK) & 1, abort_flag, p.status)) return false;
+        if (j > 0 && !mbar_wait(s_free, (j - 1) & 1, abort_flag, p.status)) return false;
+        tc_fence_after();
+        const uint64_t kb = make_sdesc(sbase + Cfg::kOffK + (j % NK) * Cfg::kKBytes, 16, 1024);
+#pragma unroll
+        for (int c = 0; c < Cfg::kKChunks; ++c)
+          mma_ss_product<4, true, CB, true, CB>(tmem, qa + c * kStep, kb + c * kStep, idesc_s, c > 0 ? 1u : 0u);
+        tc_commit(s_full);
+        if (!mbar_wait(v_full(j % NV), (j / NV) & 1, abort_flag, p.status)) return false;
+        const uint64_t vb = make_sdesc(sbase + Cfg::kOffV + (j % NV) * Cfg::kVBytes, 16, 1024);
+#pragma unroll
+        for (int c = 0; c < Cfg::kVChunks; ++c)
+          mma_ss_product<4, true, CB, true, CB>(tmem + 128, oa + c * kStep, vb + c * kStep, idesc_s, c > 0 ? 1u : 0u);
+        tc_commit(dp_full);
+        tc_commit(v_empty(j % NV));
+        return true;
+      };
+      if (ok) ok = scores(0);
+      for (int j = 0; ok && j < n; ++j) {
+        if (j + 1 < n && !(ok = scores(j + 1))) break;
+        if (!(ok = mbar_wait(ds_full, j & 1, abort_flag, p.status))) break;
+        tc_fence_after();
+        const uint64_t kb = make_sdesc(sbase + Cfg::kOffK + (j % NK) * Cfg::kKBytes, CB, 1024);
+        mma_ts_product8<false, 0>(tmem + 256, tmem + 448, kb, idesc_q, j > 0 ? 1u : 0u);
+        tc_commit(dq_done);
+        tc_commit(k_empty(j % NK));
+      }
+      if (!ok) {
+        // every MMA issued so far must finish before the TMEM is released
+        tc_commit(drain);
+        drain_wait_b(drain, 0, p.status);
+      }
+    }
+  } else {
+    // ===================== softmax gradient, two threads a row =====================
+    const float delta = halves[quarter * 32 + lane] + halves[128 + quarter * 32 + lane];
+    if (half == 0) {
+      const size_t at = static_cast<size_t>(bh) * p.Sq_pad + row;
+      p.lse2[at] = l2;
+      p.delta[at] = delta;
+      if (h == 0 && lane == 0 && (quarter & 1) == 0) {
+        const int2 u = ranges[quarter], v = ranges[quarter + 1];
+        p.ranges[static_cast<size_t>(b) * (p.Sq_pad / 64) + unit * 2 + quarter / 2] =
+            make_int2(min(u.x, v.x), max(u.y, v.y));
+      }
+    }
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t t_s = tmem + lane_off + half * 64;
+    const float c = p.scale_log2;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      ok = __all_sync(0xffffffffu, mbar_wait(s_full, j & 1, abort_flag, p.status));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[64];
+      tmem_ld32(t_s, *reinterpret_cast<uint32_t(*)[32]>(s));
+      tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+      tmem_wait_ld();
+      const int kv0 = (tile0 + j) * kTileN + half * 64;
+      if (kv0 < row_lo || kv0 + 64 > row_hi) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t see = span_bits(row_lo, row_hi, kv0 + w * 32);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!((see >> i) & 1u)) s[w * 32 + i] = __float_as_uint(-INFINITY);
+        }
+      }
+      const uint64_t c2 = f2_pack(c, c), nl2 = f2_pack(-l2, -l2), nd2 = f2_pack(-delta, -delta);
+#pragma unroll
+      for (int i = 0; i < 64; i += 2) {   // P, in fp32
+        float x0, x1;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, nl2), x0, x1);
+        s[i] = __float_as_uint(ex2(x0));
+        s[i + 1] = __float_as_uint(ex2(x1));
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, abort_flag, p.status));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t ds[32];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint32_t g[32];
+        tmem_ld32(t_s + 128 + w * 32, g);
+        tmem_wait_ld();
+        if (w == 1) {   // S and dP are in registers: the next tile's may overwrite them
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const uint64_t x = f2_add(f2_pack(__uint_as_float(g[i]), __uint_as_float(g[i + 1])), nd2);
+          float d0, d1;
+          f2_unpack(f2_mul(f2_pack(__uint_as_float(s[w * 32 + i]), __uint_as_float(s[w * 32 + i + 1])), x), d0, d1);
+          ds[(w * 32 + i) / 2] = pack2<kBf16>(d0, d1);
+        }
+      }
+      if (j > 0) {   // dQ += dS_(j-1) K'_(j-1) has read the buffer
+        ok = __all_sync(0xffffffffu, mbar_wait(dq_done, (j - 1) & 1, abort_flag, p.status));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      tmem_st32(tmem + lane_off + 448 + half * 32, ds);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
+    }
+    if (ok && n > 0)
+      ok = __all_sync(0xffffffffu, mbar_wait(dq_done, (n - 1) & 1, abort_flag, p.status));
+    if (ok) {
+      tc_fence_after();
+      Elem* dst = static_cast<Elem*>(p.dq.data) + b * p.dq.sb + h * p.dq.sh + row * p.dq.ss + half * (W / 2);
+#pragma unroll
+      for (int cc = 0; cc < W / 64; ++cc) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32(tmem + lane_off + 256 + half * (W / 2) + cc * 32, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        if (row < p.mask.Sq) store32<kBf16>(dst + cc * 32, o, p.scale);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ----------------------------------------------------------------- dK, dV --
+// Transposed products, keys on the tensor-memory lanes, 64 query rows a step:
+// S^T = K' Q^T, dP^T = V dO^T, dV += P^T dO, dK' += dS^T Q. Tensor memory: dV [0, d),
+// dK' [128, 128 + d + 64), S^T [320, 384), dP^T [384, 448), P^T and dS^T (16-bit)
+// [448, 480) and [480, 512).
+template <int D>
+struct LatDkvCfg {
+  static constexpr int kW = D + kRope;
+  static constexpr int kKChunks = kW / kChunk, kVChunks = D / kChunk;
+  static constexpr int CB = kTileN * 128;               // a chunk of 128 keys
+  static constexpr int kRows = 64;                      // query rows a step
+  static constexpr int QB = kRows * 128;                // a chunk of 64 query rows
+  static constexpr int NS = 3;
+  static constexpr int kOffV = kKChunks * CB;           // K' first
+  static constexpr int kOffQ = kOffV + kVChunks * CB;   // stages: Q, dO, L, D
+  static constexpr int kStageBytes = (kKChunks + kVChunks) * QB;
+  static constexpr int kOffRow = kOffQ + NS * kStageBytes;
+  static constexpr int kOffBar = kOffRow + NS * 2 * kRows * 4;
+  // kv_full, full[], empty[], s_full, dp_full, s_free, ds_full, kd_done, drain
+  static constexpr int kNumBars = 1 + 2 * NS + 6;
+  static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // tmem, abort, first, last
+  static constexpr int kSmemBytes = kOffMisc + 16;
+  static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+};
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreadsB, 1)
+    latent_dkv_kernel(const __grid_constant__ LatentBwdParams p) {
+  using Cfg = LatDkvCfg<D>;
+  constexpr int NS = Cfg::NS, CB = Cfg::CB, QB = Cfg::QB, W = Cfg::kW, R = Cfg::kRows;
+  using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusBadLaunch);
+    return;
+  }
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
+  int* steps = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 8);   // first and last step
+
+  const uint32_t kv_full = sbase + Cfg::kOffBar;
+  auto full = [&](int s) { return kv_full + 8 * (1 + s); };
+  auto empty = [&](int s) { return kv_full + 8 * (1 + NS + s); };
+  const uint32_t s_full = kv_full + 8 * (1 + 2 * NS);
+  const uint32_t dp_full = s_full + 8, s_free = s_full + 16, ds_full = s_full + 24;
+  const uint32_t kd_done = s_full + 32, drain = s_full + 40;
+
+  const int warp = static_cast<int>(warp_id());
+  const int lane = static_cast<int>(lane_id());
+  const int BH = p.B * p.H;
+  const int kv0 = static_cast<int>(blockIdx.x) / BH * kTileN;   // most query rows first (causal)
+  const int bh = static_cast<int>(blockIdx.x) % BH;
+  const int b = bh / p.H, h = bh % p.H;
+  const int n_steps = p.Sq_pad / R;
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(s_free, 8);
+    mbar_init(ds_full, 8);
+    mbar_init(kd_done, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    steps[0] = 0x7fffffff;
+    steps[1] = -1;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_q);
+    tma_prefetch_desc(&p.tm_do);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the dQ kernel's L, D and ranges
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(kv_full, (Cfg::kKChunks + Cfg::kVChunks) * CB);
+    for (int c = 0; c < Cfg::kVChunks; ++c) {
+      tma_load_4d(sbase + c * CB, &p.tm_k, kv_full, c * kChunk, kv0, h, b);
+      tma_load_4d(sbase + Cfg::kOffV + c * CB, &p.tm_v, kv_full, c * kChunk, kv0, h, b);
+    }
+    tma_load_4d(sbase + Cfg::kVChunks * CB, &p.tm_kr, kv_full, 0, kv0, 0, b);
+  }
+  // the steps with a row whose span reaches into the tile, and those between them
+  {
+    const int2* ranges = p.ranges + static_cast<size_t>(b) * n_steps;
+    int lo = 0x7fffffff, hi = -1;
+    for (int i = threadIdx.x; i < n_steps; i += kThreadsB) {
+      const int2 r = ranges[i];
+      if (r.y > kv0 && r.x < kv0 + kTileN) {
+        lo = min(lo, i);
+        hi = i;
+      }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0 && hi >= 0) {
+      atomicMin(&steps[0], lo);
+      atomicMax(&steps[1], hi);
+    }
+  }
+  __syncthreads();
+  const int i0 = steps[1] < 0 ? 0 : steps[0];
+  const int n = steps[1] + 1 - i0;   // 0: nothing sees the tile
+
+  if (warp == 0) {
+    // ===================== TMA producer =====================
+    if (lane == 0) {
+      if (n == 0) drain_wait_b(kv_full, 0, p.status);
+      int g = 0;
+      for (; g < n; ++g) {
+        const int st = g % NS;
+        if (g >= NS && !mbar_wait(empty(st), (g / NS - 1) & 1, abort_flag, p.status)) break;
+        const uint32_t f = full(st), dst = sbase + Cfg::kOffQ + st * Cfg::kStageBytes;
+        const int y = (i0 + g) * R;
+        mbar_arrive_expect_tx(f, Cfg::kStageBytes + 2 * R * 4);
+        for (int c = 0; c < Cfg::kKChunks; ++c) tma_load_4d(dst + c * QB, &p.tm_q, f, c * kChunk, y, h, b);
+        const size_t at = static_cast<size_t>(bh) * p.Sq_pad + y;
+        bulk_load(sbase + Cfg::kOffRow + st * (2 * R * 4), p.lse2 + at, R * 4, f);
+        for (int c = 0; c < Cfg::kVChunks; ++c)
+          tma_load_4d(dst + (Cfg::kKChunks + c) * QB, &p.tm_do, f, c * kChunk, y, h, b);
+        bulk_load(sbase + Cfg::kOffRow + st * (2 * R * 4) + R * 4, p.delta + at, R * 4, f);
+      }
+      if (*abort_flag) {
+        drain_wait_b(kv_full, 0, p.status);
+        for (int j = max(0, g - NS); j < g; ++j) drain_wait_b(full(j % NS), (j / NS) & 1, p.status);
+      }
+    }
+  } else if (warp == 1) {
+    // ===================== MMA issuer =====================
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t idesc_s = make_idesc(128, R, kBf16, false, false);
+      constexpr uint32_t idesc_v = make_idesc(128, D, kBf16, false, true);
+      constexpr uint32_t idesc_k = make_idesc(128, W, kBf16, false, true);
+      constexpr uint64_t kA = CB >> 4, kB = QB >> 4;
+      const uint64_t ka = make_sdesc(sbase, 16, 1024), va = make_sdesc(sbase + Cfg::kOffV, 16, 1024);
+      bool ok = mbar_wait(kv_full, 0, abort_flag, p.status);
+#ifdef FA_WAIT_TEST
+      if (ok) ok = mbar_wait(drain, 0, abort_flag, p.status);   // runs out, as in the dQ kernel
+#endif
+      auto scores = [&](int g) -> bool {   // S^T and dP^T of step g
+        if (!mbar_wait(full(g % NS), (g / NS) & 1, abort_flag, p.status)) return false;
+        if (g > 0 && !mbar_wait(s_free, (g - 1) & 1, abort_flag, p.status)) return false;
+        tc_fence_after();
+        const uint64_t qb = make_sdesc(sbase + Cfg::kOffQ + (g % NS) * Cfg::kStageBytes, 16, 1024);
+#pragma unroll
+        for (int c = 0; c < Cfg::kKChunks; ++c)
+          mma_ss_product<4, true, CB, true, QB>(tmem + 320, ka + c * kA, qb + c * kB, idesc_s, c > 0 ? 1u : 0u);
+        tc_commit(s_full);
+#pragma unroll
+        for (int c = 0; c < Cfg::kVChunks; ++c)
+          mma_ss_product<4, true, CB, true, QB>(tmem + 384, va + c * kA, qb + (Cfg::kKChunks + c) * kB, idesc_s,
+                                                c > 0 ? 1u : 0u);
+        tc_commit(dp_full);
+        return true;
+      };
+      if (ok) ok = scores(0);
+      for (int g = 0; ok && g < n; ++g) {
+        if (g + 1 < n && !(ok = scores(g + 1))) break;
+        if (!(ok = mbar_wait(ds_full, g & 1, abort_flag, p.status))) break;
+        tc_fence_after();
+        const uint32_t st = sbase + Cfg::kOffQ + (g % NS) * Cfg::kStageBytes;
+        const uint64_t qb = make_sdesc(st, QB, 1024), ob = make_sdesc(st + Cfg::kKChunks * QB, QB, 1024);
+        mma_ts_product4<false, 0>(tmem, tmem + 448, ob, idesc_v, g > 0 ? 1u : 0u);
+        mma_ts_product4<false, 0>(tmem + 128, tmem + 480, qb, idesc_k, g > 0 ? 1u : 0u);
+        tc_commit(kd_done);
+        tc_commit(empty(g % NS));
+      }
+      if (!ok) {
+        tc_commit(drain);
+        drain_wait_b(drain, 0, p.status);
+      }
+    }
+  } else {
+    // ===================== softmax gradient, two threads a key =====================
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int key0 = kv0 + quarter * 32, key = key0 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t t_s = tmem + lane_off + 320 + half * 32;
+    const float c = p.scale_log2;
+    // the span of query column `lane` of this warp's half of step g
+    auto span_of = [&](int g) { return p.mask.span(b, (i0 + g) * R + half * 32 + lane); };
+    int2 sp = n > 0 ? span_of(0) : make_int2(0, 0);
+    bool ok = true;
+    for (int g = 0; g < n; ++g) {
+      const int st = g % NS;
+      uint32_t vis = 0xffffffffu;   // bit e: this lane's key is seen by query column e
+      if (__any_sync(0xffffffffu, sp.x > key0 || sp.y < key0 + 32))
+        vis = transpose_bits(span_bits(sp.x, sp.y, key0), lane);
+      if (g + 1 < n) sp = span_of(g + 1);
+      ok = __all_sync(0xffffffffu, mbar_wait(full(st), (g / NS) & 1, abort_flag, p.status) &&
+                                       mbar_wait(s_full, g & 1, abort_flag, p.status));
+      if (!ok) break;
+      tc_fence_after();
+      const float* l2 = reinterpret_cast<const float*>(smem + Cfg::kOffRow + st * (2 * R * 4)) + half * 32;
+      uint32_t s[32];
+      tmem_ld32(t_s, s);
+      tmem_wait_ld();
+      if (vis != 0xffffffffu) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (!((vis >> e) & 1u)) s[e] = __float_as_uint(-INFINITY);
+      }
+      const uint64_t c2 = f2_pack(c, c);
+      uint32_t pk[16], ds[16];
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        const float2 l = *reinterpret_cast<const float2*>(l2 + e);
+        float x0, x1;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, f2_pack(-l.x, -l.y)), x0, x1);
+        x0 = ex2(x0);
+        x1 = ex2(x1);
+        pk[e / 2] = pack2<kBf16>(x0, x1);
+        s[e] = __float_as_uint(x0);
+        s[e + 1] = __float_as_uint(x1);
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(dp_full, g & 1, abort_flag, p.status));
+      if (!ok) break;
+      tc_fence_after();
+      {
+        uint32_t d[32];
+        tmem_ld32(t_s + 64, d);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 dl = *reinterpret_cast<const float2*>(l2 + R + e);
+          float d0, d1;
+          f2_unpack(f2_mul(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
+                           f2_sub(f2_pack(__uint_as_float(d[e]), __uint_as_float(d[e + 1])), f2_pack(dl.x, dl.y))),
+                    d0, d1);
+          ds[e / 2] = pack2<kBf16>(d0, d1);
+        }
+      }
+      if (g > 0) {   // the products of step g - 1 have read P^T and dS^T
+        ok = __all_sync(0xffffffffu, mbar_wait(kd_done, (g - 1) & 1, abort_flag, p.status));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      tmem_st16(tmem + lane_off + 448 + half * 16, pk);
+      tmem_st16(tmem + lane_off + 480 + half * 16, ds);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
+    }
+    if (ok && n > 0)
+      ok = __all_sync(0xffffffffu, mbar_wait(kd_done, (n - 1) & 1, abort_flag, p.status));
+    if (ok) {
+      tc_fence_after();
+      // warps 2-5 write dK, warps 6-9 dV, each half the shared part
+      const HeadView& v = half == 0 ? p.dk : p.dv;
+      const float f = half == 0 ? p.scale : 1.f;
+      Elem* dst = static_cast<Elem*>(v.data) + b * v.sb + h * v.sh + key * v.ss;
+      auto load = [&](int col, uint32_t (&o)[32]) {
+        if (n > 0) {
+          tmem_ld32(tmem + lane_off + col, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+      };
+      uint32_t o[32];
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc) {
+        load((half == 0 ? 128 : 0) + cc * 32, o);
+        if (key < p.mask.Skv) store32<kBf16>(dst + cc * 32, o, f);
+      }
+      load(128 + D + half * 32, o);
+      if (key < p.mask.Skv) {
+        float4* part = reinterpret_cast<float4*>(p.part + (static_cast<size_t>(bh) * p.mask.Skv + key) * kRope + half * 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          part[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// -------------------------------------------------------------------- dKR --
+// dKR_j = scale * the heads' parts, added in head order; 8 elements a thread. Bandwidth-bound.
+template <bool kBf16>
+__global__ void __launch_bounds__(256) latent_dkr_kernel(const __grid_constant__ LatentBwdParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long at = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const long long tokens = static_cast<long long>(p.B) * p.mask.Skv;
+  const long long token = at / (kRope / 8);
+  const int u = static_cast<int>(at % (kRope / 8));
+  if (token >= tokens) return;
+  const int b = static_cast<int>(token / p.mask.Skv), j = static_cast<int>(token % p.mask.Skv);
+  const size_t step = static_cast<size_t>(p.mask.Skv) * kRope;
+  const float* src = p.part + static_cast<size_t>(b) * p.H * step + static_cast<size_t>(j) * kRope + u * 8;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int h = 0; h < p.H; ++h) {
+    const float4 x = reinterpret_cast<const float4*>(src + h * step)[0];
+    const float4 y = reinterpret_cast<const float4*>(src + h * step)[1];
+    acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+    acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+  }
+  uint16_t* dst = static_cast<uint16_t*>(p.dk_rope.data) + b * p.dk_rope.sb + j * p.dk_rope.ss + u * 8;
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = pack2<kBf16>(acc[2 * e] * p.scale, acc[2 * e + 1] * p.scale);
+  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int D, bool kBf16>
+cudaError_t launch_impl(const LatentBwdParams& p0, cudaStream_t stream) {
+  auto dq = latent_dq_kernel<D, kBf16>;
+  auto dkv = latent_dkv_kernel<D, kBf16>;
+  cudaError_t e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, LatDqCfg<D>::kSmemBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, LatDkvCfg<D>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  LatentBwdParams p = p0;
+  const long long bh = static_cast<long long>(p.B) * p.H;
+  p.n_units = p.Sq_pad / kTileM;
+  e = launch_dependent(dq, dim3(static_cast<unsigned>(bh * p.n_units)), dim3(kThreadsB),
+                       LatDqCfg<D>::kSmemBytes, stream, p);
+  if (e != cudaSuccess) return e;
+  p.n_units = (p.mask.Skv + kTileN - 1) / kTileN;
+  e = launch_dependent(dkv, dim3(static_cast<unsigned>(bh * p.n_units)), dim3(kThreadsB),
+                       LatDkvCfg<D>::kSmemBytes, stream, p);
+  if (e != cudaSuccess) return e;
+  const long long threads = static_cast<long long>(p.B) * p.mask.Skv * (kRope / 8);
+  return launch_dependent(latent_dkr_kernel<kBf16>, dim3(static_cast<unsigned>((threads + 255) / 256)),
+                          dim3(256), 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_bwd(const LatentBwdParams& p, int d, bool bf16, cudaStream_t stream) {
+  if (d == 128) return bf16 ? launch_impl<128, true>(p, stream) : launch_impl<128, false>(p, stream);
+  return bf16 ? launch_impl<64, true>(p, stream) : launch_impl<64, false>(p, stream);
+}
+
+}  // namespace fa

@@ -1,0 +1,447 @@
+// Forward of latent attention in its expanded form: every head has keys K [Skv, d] and
+// values V [Skv, d] (expanded from the tokens' latents by the caller) and all heads of a
+// token share a rotated key part KR [Skv, 64], so that
+//
+//   s_ij = scale (<Q_i[0:d], K_j> + <Q_i[d:], KR_j>),  out = softmax(s) V, LSE_i = log sum_j e^s_ij
+//
+// under one key range per row. The shared part is loaded beside each head's keys, as a
+// third chunk of the key tile; it is never copied out to the heads in memory.
+//
+// As the forward in fa_fwd.cu: T query tiles of 128 rows per CTA, TMA producer (warp 0),
+// MMA issuer (warp 1), four softmax warps a tile with a thread a row, online softmax with
+// a lazily moved reference maximum, P over S's columns (T = 2) or beside them (T = 1).
+#include <type_traits>
+
+#include "fa_latent.h"
+#include "ptx.cuh"
+#include "score_mod.cuh"
+
+namespace fa {
+namespace {
+
+constexpr float kLn2L = 0.6931471805599453f;
+constexpr float kRescaleL = 8.0f;   // the reference maximum moves when exceeded by 2^8
+
+template <int D>
+struct LatFwdCfg {
+  static constexpr int T = D == 128 ? 2 : 1;            // query tiles a CTA
+  static constexpr int kCtasPerSm = 3 - T;
+  static constexpr int kThreads = 64 + 128 * T;
+  static constexpr bool kSepP = T == 1;                 // P has columns of its own
+  static constexpr int kTmemCols = 256 * T;
+  static constexpr int kKChunks = D / kChunk + 1;       // key chunks, the shared one last
+  static constexpr int kVChunks = D / kChunk;
+  static constexpr int kChunkBytes = kTileN * 128;
+  static constexpr int kKBytes = kKChunks * kChunkBytes, kVBytes = kVChunks * kChunkBytes;
+  static constexpr int kKStages = 2, kVStages = 1;
+  static constexpr int kOffK = T * kKBytes;             // Q tiles first
+  static constexpr int kOffV = kOffK + kKStages * kKBytes;
+  static constexpr int kOffBar = kOffV + kVStages * kVBytes;
+  // q_full, k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], pv_done[2],
+  // s_free, drain
+  static constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 8;
+  static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // tmem base, abort flag
+  static constexpr int kOffSpan = kOffMisc + 16;        // (begin, end) of each softmax warp's rows
+  static constexpr int kSmemBytes = kOffSpan + 4 * T * 8;
+  static_assert(kSmemBytes <= 232448 && (T == 2 || 2 * (kSmemBytes + 1024) <= 233472), "shared memory");
+};
+
+__device__ __forceinline__ void drain_wait_l(uint32_t bar, uint32_t parity, int* status) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > kDrainLimitCycles) {
+      atomicOr(status, kStatusWaitTimeout);
+      return;
+    }
+  }
+}
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPerSm)
+    latent_fwd_kernel(const __grid_constant__ LatentFwdParams p) {
+  using Cfg = LatFwdCfg<D>;
+  constexpr int T = Cfg::T, NK = Cfg::kKStages, NV = Cfg::kVStages, CB = Cfg::kChunkBytes;
+  using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {   // the 128-byte swizzle needs 1024-byte aligned tiles
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusBadLaunch);
+    return;
+  }
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
+  int2* ranges = reinterpret_cast<int2*>(smem + Cfg::kOffSpan);
+
+  const uint32_t q_full = sbase + Cfg::kOffBar;
+  auto bars = [&](int first) { return [=](int i) { return q_full + 8 * (first + i); }; };
+  const auto k_full = bars(1), k_empty = bars(1 + NK), v_full = bars(1 + 2 * NK);
+  const auto v_empty = bars(1 + 2 * NK + NV), s_full = bars(1 + 2 * NK + 2 * NV);
+  const auto p_full = bars(3 + 2 * NK + 2 * NV), pv_done = bars(5 + 2 * NK + 2 * NV);
+  const uint32_t s_free = q_full + 8 * (7 + 2 * NK + 2 * NV), drain = s_free + 8;
+
+  const int warp = static_cast<int>(warp_id());
+  const int lane = static_cast<int>(lane_id());
+  // heaviest tiles first, as under the causal mask
+  const int BH = p.B * p.H;
+  const int unit = p.n_units - 1 - static_cast<int>(blockIdx.x) / BH;
+  const int bh = static_cast<int>(blockIdx.x) % BH;
+  const int b = bh / p.H, h = bh % p.H;
+  const int q0 = unit * T * kTileM;
+
+  int row_lo = 0, row_hi = 0;   // a softmax thread's row
+  if (warp >= 2) {
+    // programmatic dependent of the kernel before: waited for in front of the first access
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int t = (warp - 2) / 4;
+    const int2 s = p.mask.span(b, q0 + t * kTileM + (warp & 3) * 32 + lane);
+    row_lo = s.x;
+    row_hi = s.y;
+    const int lo = __reduce_min_sync(0xffffffffu, row_hi > 0 ? row_lo : 0x7fffffff);
+    const int hi = __reduce_max_sync(0xffffffffu, row_hi);
+    if (lane == 0) ranges[t * 4 + (warp & 3)] = make_int2(lo, hi);
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < NK; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+    }
+    for (int s = 0; s < NV; ++s) {
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(s_full(t), 1);
+      mbar_init(p_full(t), 4);   // one arrival per softmax warp
+      mbar_init(pv_done(t), 1);
+    }
+    mbar_init(s_free, 4);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    // the queries are on their way while the spans are read (rows past Sq come as zeros)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    mbar_arrive_expect_tx(q_full, T * Cfg::kKBytes);
+    for (int t = 0; t < T; ++t)
+      for (int c = 0; c < Cfg::kKChunks; ++c)
+        tma_load_4d(sbase + t * Cfg::kKBytes + c * CB, &p.tm_q, q_full, c * kChunk, q0 + t * kTileM, h, b);
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_kr);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (gridDim.x <= 152) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // key tiles [tile0, tile0 + n_load); query tile t takes those from first[t] to last[t]
+  int first[2] = {0, 0}, last[2] = {0, 0};
+  int tile0 = 0x7fffffff, tile1 = 0;
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    int lo = 0x7fffffff, hi = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      lo = min(lo, ranges[t * 4 + w].x);
+      hi = max(hi, ranges[t * 4 + w].y);
+    }
+    if (hi > 0) {
+      first[t] = lo / kTileN;
+      last[t] = (hi + kTileN - 1) / kTileN;
+      tile0 = min(tile0, first[t]);
+      tile1 = max(tile1, last[t]);
+    }
+  }
+  if (tile1 == 0) tile0 = 0;
+  const int n_load = tile1 - tile0;
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    if (last[t] == 0) first[t] = last[t] = 0;   // sees nothing
+    else {
+      first[t] -= tile0;
+      last[t] -= tile0;
+    }
+  }
+
+  if (warp == 0) {
+    // ===================== TMA producer =====================
+    if (lane == 0) {
+      if (n_load == 0) drain_wait_l(q_full, 0, p.status);   // no product waits for the queries
+      int jk = 0, jv = 0;   // K and V tiles issued
+      for (; jk < n_load;) {
+        const int sk = jk % NK, sv = jv % NV;
+        const int y = (tile0 + jk) * kTileN;
+        if (jk >= NK && !mbar_wait(k_empty(sk), (jk / NK - 1) & 1, abort_flag, p.status)) break;
+        mbar_arrive_expect_tx(k_full(sk), Cfg::kKBytes);
+        for (int c = 0; c < Cfg::kVChunks; ++c)
+          tma_load_4d(sbase + Cfg::kOffK + sk * Cfg::kKBytes + c * CB, &p.tm_k, k_full(sk), c * kChunk, y, h, b);
+        tma_load_4d(sbase + Cfg::kOffK + sk * Cfg::kKBytes + Cfg::kVChunks * CB, &p.tm_kr, k_full(sk), 0, y, 0, b);
+        ++jk;
+        if (jv >= NV && !mbar_wait(v_empty(sv), (jv / NV - 1) & 1, abort_flag, p.status)) break;
+        mbar_arrive_expect_tx(v_full(sv), Cfg::kVBytes);
+        for (int c = 0; c < Cfg::kVChunks; ++c)
+          tma_load_4d(sbase + Cfg::kOffV + sv * Cfg::kVBytes + c * CB, &p.tm_v, v_full(sv), c * kChunk, y, h, b);
+        ++jv;
+      }
+      if (*abort_flag) {
+        // let every copy already issued land before the CTA releases its memory
+        drain_wait_l(q_full, 0, p.status);
+        for (int j = max(0, jk - NK); j < jk; ++j) drain_wait_l(k_full(j % NK), (j / NK) & 1, p.status);
+        for (int j = max(0, jv - NV); j < jv; ++j) drain_wait_l(v_full(j % NV), (j / NV) & 1, p.status);
+      }
+    }
+  } else if (warp == 1) {
+    // ===================== MMA issuer =====================
+    if (lane == 0 && n_load > 0) {
+      constexpr uint32_t idesc_qk = make_idesc(128, kTileN, kBf16, false, false);
+      constexpr uint32_t idesc_pv = make_idesc(128, D, kBf16, false, true);
+      bool ok = mbar_wait(q_full, 0, abort_flag, p.status);
+#ifdef FA_WAIT_TEST
+      // wait-limit test build: nothing completes this phase before the abort
+      // path's own commit, so the wait runs out
+      if (ok) ok = mbar_wait(drain, 0, abort_flag, p.status);
+#endif
+      auto active = [&](int t, int j) { return j >= first[t] && j < last[t]; };
+      auto issue_qk = [&](int t, int j) {   // S_t = Q_t K_j^T
+        const uint64_t qa = make_sdesc(sbase + t * Cfg::kKBytes, 16, 1024);
+        const uint64_t kb = make_sdesc(sbase + Cfg::kOffK + (j % NK) * Cfg::kKBytes, 16, 1024);
+        constexpr uint64_t kStep = CB >> 4;
+#pragma unroll
+        for (int c = 0; c < Cfg::kKChunks; ++c)
+          mma_ss_product<4, true, CB, true, CB>(tmem + t * 128, qa + c * kStep, kb + c * kStep, idesc_qk,
+                                                c > 0 ? 1u : 0u);
+        tc_commit(s_full(t));
+      };
+      auto issue_pv = [&](int t, int j) {   // O_t (+)= P_t V_j
+        const uint64_t vb = make_sdesc(sbase + Cfg::kOffV + (j % NV) * Cfg::kVBytes, CB, 1024);
+        const uint32_t o_t = tmem + 128 * T + t * 128;
+        mma_ts_product8<false, 0>(o_t, Cfg::kSepP ? o_t + D : tmem + t * 128, vb, idesc_pv,
+                                  j > first[t] ? 1u : 0u);
+        tc_commit(pv_done(t));
+      };
+      if (ok) ok = mbar_wait(k_full(0), 0, abort_flag, p.status);
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < T; ++t)
+          if (active(t, 0)) issue_qk(t, 0);
+        tc_commit(k_empty(0));
+      }
+      for (int j = 0; ok && j < n_load; ++j) {
+        const uint32_t par_k1 = static_cast<uint32_t>((j + 1) / NK) & 1;
+        const uint32_t par_v = static_cast<uint32_t>(j / NV) & 1;
+        bool k_next = false, v_cur = false;   // K_{j+1}, V_j seen landed
+        for (int t = 0; t < T && ok; ++t) {
+          const bool now = active(t, j), then = active(t, j + 1);
+          const int n = j - first[t];   // tiles of this query tile before j
+          auto next_qk = [&]() -> bool {
+            if (!k_next && !mbar_wait(k_full((j + 1) % NK), par_k1, abort_flag, p.status)) return false;
+            k_next = true;
+            // S_t has been read (or holds P_t that P_t V_j has read)
+            if (now && !mbar_wait(Cfg::kSepP ? s_free : pv_done(t), n & 1, abort_flag, p.status)) return false;
+            tc_fence_after();
+            issue_qk(t, j + 1);
+            return true;
+          };
+          if (Cfg::kSepP && then && !(ok = next_qk())) break;
+          if (now) {
+            if (!v_cur && !(ok = mbar_wait(v_full(j % NV), par_v, abort_flag, p.status))) break;
+            v_cur = true;
+            if (!(ok = mbar_wait(p_full(t), n & 1, abort_flag, p.status))) break;
+            tc_fence_after();
+            issue_pv(t, j);
+          }
+          if (!Cfg::kSepP && then && !(ok = next_qk())) break;
+        }
+        if (!ok) break;
+        // (a tile that no row of either query tile wants: its loads are waited for, so that
+        // none is in flight at the end)
+        if (!v_cur && !(ok = mbar_wait(v_full(j % NV), par_v, abort_flag, p.status))) break;
+        tc_commit(v_empty(j % NV));
+        if (j + 1 < n_load) {
+          if (!k_next && !(ok = mbar_wait(k_full((j + 1) % NK), par_k1, abort_flag, p.status))) break;
+          tc_commit(k_empty((j + 1) % NK));
+        }
+      }
+      if (!ok) {
+        // every MMA issued so far must finish before the TMEM is released
+        tc_commit(drain);
+        drain_wait_l(drain, 0, p.status);
+      }
+    }
+  } else {
+    // ===================== softmax / correction / epilogue =====================
+    const int t = (warp - 2) / 4;
+    const int quarter = warp & 3;               // TMEM lane quarter of this warp
+    const int row = q0 + t * kTileM + quarter * 32 + lane;
+    const int n = last[t] - first[t];
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_tmem = tmem + lane_off + t * 128;
+    const uint32_t o_tmem = tmem + lane_off + 128 * T + t * 128;
+    const uint32_t p_tmem = Cfg::kSepP ? o_tmem + D : s_tmem;
+    const float c = p.scale_log2;
+    float m_ref = -INFINITY;   // reference max, scaled log2 domain
+    float l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      ok = __all_sync(0xffffffffu, mbar_wait(s_full(t), j & 1, abort_flag, p.status));
+      if (!ok) break;
+      tc_fence_after();
+      float s[kTileN];
+      {
+        uint32_t raw[kTileN];
+#pragma unroll
+        for (int cc = 0; cc < kTileN / 32; ++cc)
+          tmem_ld32(s_tmem + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(raw + cc * 32));
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < kTileN; ++i) s[i] = __uint_as_float(raw[i]);
+      }
+      if constexpr (Cfg::kSepP) {   // the issuer may overwrite S with the next tile's
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free);
+      }
+      const int kv0 = (tile0 + first[t] + j) * kTileN;
+      if (kv0 < row_lo || kv0 + kTileN > row_hi) {
+#pragma unroll
+        for (int w = 0; w < kTileN / 32; ++w) {
+          const uint32_t see = span_bits(row_lo, row_hi, kv0 + w * 32);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!((see >> i) & 1u)) s[w * 32 + i] = -INFINITY;
+        }
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int i = 4; i + 8 <= kTileN; i += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmax3(mx[e], s[i + e], s[i + 4 + e]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[kTileN - 4 + e]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+      const float m_new = top > m_ref + kRescaleL ? top : m_ref;
+      const float m_use = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = ex2(m_ref - m_use);   // 0 when m_ref = -inf
+      const bool moved = m_new != m_ref;
+      m_ref = m_new;
+
+      const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_use, -m_use);
+      uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float x0, x1;
+          f2_unpack(f2_fma(f2_pack(s[w * 64 + 2 * i], s[w * 64 + 2 * i + 1]), c2, nm2), x0, x1);
+          const float p0 = ex2(x0), p1 = ex2(x1);
+          if (i & 1) sum1 = f2_add(sum1, f2_pack(p0, p1));
+          else sum0 = f2_add(sum0, f2_pack(p0, p1));
+          pk[i] = pack2<kBf16>(p0, p1);
+        }
+        if (Cfg::kSepP && w == 0 && j > 0) {
+          // P_(j-1) V_(j-1) has read the P buffer (and O may be rescaled)
+          ok = __all_sync(0xffffffffu, mbar_wait(pv_done(t), (j - 1) & 1, abort_flag, p.status));
+          tc_fence_after();
+        }
+        tmem_st32(p_tmem + w * 32, pk);
+      }
+      if (!ok) break;
+      float a0, a1, a2, a3;
+      f2_unpack(sum0, a0, a1);
+      f2_unpack(sum1, a2, a3);
+      l = l * alpha + ((a0 + a1) + (a2 + a3));
+
+      // O <- alpha O for rows whose reference max moved (the first P V overwrites O)
+      if (j > 0 && __any_sync(0xffffffffu, moved)) {
+        if constexpr (!Cfg::kSepP) {
+          ok = __all_sync(0xffffffffu, mbar_wait(pv_done(t), (j - 1) & 1, abort_flag, p.status));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const float a = moved ? alpha : 1.f;
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(o_tmem + cc * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+          tmem_st32(o_tmem + cc * 32, o);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(t));
+    }
+
+    if (ok && n > 0)
+      ok = __all_sync(0xffffffffu, mbar_wait(pv_done(t), (n - 1) & 1, abort_flag, p.status));
+    if (ok) {
+      tc_fence_after();
+      // a row that sees nothing has O = 0, l = 0 (and only its own span says so: a row of NaN
+      // or -infinite scores has no sum either)
+      const bool none = row_hi == 0;
+      const float inv_l = none ? 0.f : 1.f / l;
+      Elem* orow = static_cast<Elem*>(p.out.data) + b * p.out.sb + h * p.out.sh + row * p.out.ss;
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32(o_tmem + cc * 32, o);
+          tmem_wait_ld();
+        }
+        if (row < p.mask.Sq) {
+          uint4* dst = reinterpret_cast<uint4*>(orow + cc * 32);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = none ? 0u : pack2<kBf16>(__uint_as_float(o[8 * v + 2 * e]) * inv_l,
+                                              __uint_as_float(o[8 * v + 2 * e + 1]) * inv_l);
+            dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (row < p.mask.Sq)
+        p.lse[static_cast<size_t>(bh) * p.mask.Sq + row] =
+            none ? -INFINITY : (m_ref + __log2f(l)) * kLn2L;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::kTmemCols);
+  }
+}
+
+template <int D, bool kBf16>
+cudaError_t launch_impl(const LatentFwdParams& p0, cudaStream_t stream) {
+  using Cfg = LatFwdCfg<D>;
+  auto kernel = latent_fwd_kernel<D, kBf16>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  LatentFwdParams p = p0;
+  p.n_units = (p.mask.Sq + Cfg::T * kTileM - 1) / (Cfg::T * kTileM);
+  const unsigned grid = static_cast<unsigned>(static_cast<long long>(p.B) * p.H * p.n_units);   // < 2^31
+  return launch_dependent(kernel, dim3(grid), dim3(Cfg::kThreads), Cfg::kSmemBytes, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_fwd(const LatentFwdParams& p, int d, bool bf16, cudaStream_t stream) {
+  if (d == 128) return bf16 ? launch_impl<128, true>(p, stream) : launch_impl<128, false>(p, stream);
+  return bf16 ? launch_impl<64, true>(p, stream) : launch_impl<64, false>(p, stream);
+}
+
+}  // namespace fa

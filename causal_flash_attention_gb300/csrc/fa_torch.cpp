@@ -1,4 +1,4 @@
-// Native part of the Python binding: the span, ragged and query/key-preparation
+// Native part of the Python binding: the span, ragged, query/key-preparation and latent
 // calls of libfa (include/fa.h) on torch tensors. Each function checks its
 // tensors (a tensor on another device, of another type or size would have the
 // kernels read memory that is not its own), allocates what the caller did not
@@ -53,6 +53,12 @@ struct Library {
   decltype(&fa_qk_norm_rope_bwd) norm_rope_bwd;
   decltype(&fa_qk_norm_rope_bwd_workspace_bytes) norm_rope_bwd_bytes;
   decltype(&fa_qk_norm_rope_append) append;
+  decltype(&fa_fwd_latent) latent_fwd;
+  decltype(&fa_bwd_latent) latent_bwd;
+  decltype(&fa_bwd_latent_workspace_bytes) latent_bwd_bytes;
+  decltype(&fa_fwd_latent_paged) latent_paged;
+  decltype(&fa_fwd_latent_paged_workspace_bytes) latent_paged_bytes;
+  decltype(&fa_latent_append) latent_append;
 };
 
 template <typename F>
@@ -76,6 +82,12 @@ const Library& library(PyObject* o) {
   find(handle, "fa_qk_norm_rope_bwd", l.norm_rope_bwd);
   find(handle, "fa_qk_norm_rope_bwd_workspace_bytes", l.norm_rope_bwd_bytes);
   find(handle, "fa_qk_norm_rope_append", l.append);
+  find(handle, "fa_fwd_latent", l.latent_fwd);
+  find(handle, "fa_bwd_latent", l.latent_bwd);
+  find(handle, "fa_bwd_latent_workspace_bytes", l.latent_bwd_bytes);
+  find(handle, "fa_fwd_latent_paged", l.latent_paged);
+  find(handle, "fa_fwd_latent_paged_workspace_bytes", l.latent_paged_bytes);
+  find(handle, "fa_latent_append", l.latent_append);
   l.handle = handle;
   lib = l;
   return lib;
@@ -569,6 +581,174 @@ PyObject* step(PyObject* const* a) {
   return rc ? PyLong_FromLong(rc) : tensors({out, lse});
 }
 
+// ----------------------------------------------------------------- latent --
+constexpr int64_t kRope = 64;   // elements of the rotated key part
+
+// The fa_view of a [B, S, d] tensor (no heads).
+fa_view flat_view(const char* name, const Tensor& t, at::Device dev, at::ScalarType dt, int64_t B, int64_t S,
+                  int64_t d, bool written = false) {
+  const Sizes sizes = {B, S, d};
+  const at::IntArrayRef want(sizes.begin(), sizes.size());
+  if (t.device() != dev || t.scalar_type() != dt || t.sizes() != want) misfit(name, t, "", dev, dt, want);
+  return view(name, t.unsqueeze(1), dev, dt, {B, 1, S, d}, written);
+}
+
+struct LatentInputs {
+  at::Device dev;
+  at::ScalarType dt;
+  int B, H, Sq, Skv, d;
+  fa_view q, k, kr, v;
+};
+LatentInputs latent_inputs(const Tensor& q, const Tensor& k, const Tensor& kr, const Tensor& v,
+                           const Tensor& begin, const Tensor& end) {
+  const at::Device dev = cuda_device(q, "q");
+  four_dims(q, "q [B,H,Sq,d+64], k and v [B,H,Skv,d], k_rope [B,Skv,64] (any strides but the last)");
+  four_dims(k, "q [B,H,Sq,d+64], k and v [B,H,Skv,d], k_rope [B,Skv,64] (any strides but the last)");
+  LatentInputs n{dev, q.scalar_type(), narrow(q.size(0)), narrow(q.size(1)), narrow(q.size(2)),
+                 narrow(k.size(2)), narrow(k.size(3)), {}, {}, {}, {}};
+  n.q = view("q", q, dev, n.dt, {n.B, n.H, n.Sq, n.d + kRope});
+  n.k = view("k", k, dev, n.dt, {n.B, n.H, n.Skv, n.d});
+  n.kr = flat_view("k_rope", kr, dev, n.dt, n.B, n.Skv, kRope);
+  n.v = view("v", v, dev, n.dt, {n.B, n.H, n.Skv, n.d});
+  if (begin.defined() != end.defined()) throw BadArgument{"key_begin and key_end go together"};
+  if (begin.defined()) {
+    fit("key_begin", begin, dev, at::kInt, {n.B, n.Sq});
+    fit("key_end", end, dev, at::kInt, {n.B, n.Sq});
+  }
+  return n;
+}
+
+// (handle, q, k, k_rope, v, key_begin, key_end, out, lse, scale, stream)
+PyObject* latent_forward(PyObject* const* a) {
+  const Library lib = library(a[0]);
+  const Tensor &q = tensor(a[1], "q"), &k = tensor(a[2], "k"), &kr = tensor(a[3], "k_rope"), &v = tensor(a[4], "v");
+  const Tensor begin = maybe(a[5], "key_begin"), end = maybe(a[6], "key_end");
+  Tensor out = maybe(a[7], "out"), lse = maybe(a[8], "lse");
+  const LatentInputs n = latent_inputs(q, k, kr, v, begin, end);
+  const float scale = scale_of(a[9], n.d + static_cast<int>(kRope));
+  const Place at(n.dev, a[10]);
+  Released released;
+  if (!out.defined()) out = empty_tokens_first(n.B, n.H, n.Sq, n.d, n.dev, n.dt);
+  const fa_view vo = view("out", out, n.dev, n.dt, {n.B, n.H, n.Sq, n.d}, true);
+  if (lse.defined()) fit("lse", lse, n.dev, at::kFloat, {n.B, n.H, n.Sq});
+  else lse = empty({n.B, n.H, n.Sq}, n.dev, at::kFloat);
+  const int rc = lib.latent_fwd(&n.q, &n.k, &n.kr, &n.v, data<int>(begin), data<int>(end), &vo, data<float>(lse), n.B,
+                                n.H, n.Sq, n.Skv, n.d, scale, dtype_code(q), at.stream);
+  released.end();
+  return rc ? PyLong_FromLong(rc) : tensors({out, lse});
+}
+
+// (handle, q, k, k_rope, v, key_begin, key_end, out, dout, lse, dq, dk, dk_rope, dv, workspace,
+//  scale, stream)
+PyObject* latent_backward(PyObject* const* a) {
+  const Library lib = library(a[0]);
+  const Tensor &q = tensor(a[1], "q"), &k = tensor(a[2], "k"), &kr = tensor(a[3], "k_rope"), &v = tensor(a[4], "v");
+  const Tensor begin = maybe(a[5], "key_begin"), end = maybe(a[6], "key_end");
+  const Tensor &out = tensor(a[7], "out"), &dout = tensor(a[8], "dout"), &lse = tensor(a[9], "lse");
+  Tensor dq = maybe(a[10], "dq"), dk = maybe(a[11], "dk"), dkr = maybe(a[12], "dk_rope"), dv = maybe(a[13], "dv");
+  Tensor ws = maybe(a[14], "workspace");
+  const LatentInputs n = latent_inputs(q, k, kr, v, begin, end);
+  const Sizes os = {n.B, n.H, n.Sq, n.d}, ks = {n.B, n.H, n.Skv, n.d};
+  const fa_view vo = view("out", out, n.dev, n.dt, os), vg = view("dout", dout, n.dev, n.dt, os);
+  fit("lse", lse, n.dev, at::kFloat, {n.B, n.H, n.Sq});
+  const float scale = scale_of(a[15], n.d + static_cast<int>(kRope));
+  const Place at(n.dev, a[16]);
+  Released released;
+  if (!dq.defined()) dq = empty_tokens_first(n.B, n.H, n.Sq, n.d + kRope, n.dev, n.dt);
+  if (!dk.defined()) dk = empty_tokens_first(n.B, n.H, n.Skv, n.d, n.dev, n.dt);
+  if (!dkr.defined()) dkr = empty({n.B, n.Skv, kRope}, n.dev, n.dt);
+  if (!dv.defined()) dv = empty_tokens_first(n.B, n.H, n.Skv, n.d, n.dev, n.dt);
+  if (!ws.defined()) ws = workspace_of(lib.latent_bwd_bytes(n.B, n.H, n.Sq, n.Skv, n.d), n.dev);
+  const fa_view vdq = view("dq", dq, n.dev, n.dt, {n.B, n.H, n.Sq, n.d + kRope}, true);
+  const fa_view vdk = view("dk", dk, n.dev, n.dt, ks, true), vdv = view("dv", dv, n.dev, n.dt, ks, true);
+  const fa_view vdkr = flat_view("dk_rope", dkr, n.dev, n.dt, n.B, n.Skv, kRope, true);
+  const int rc = lib.latent_bwd(&n.q, &n.k, &n.kr, &n.v, data<int>(begin), data<int>(end), &vo, &vg, data<float>(lse),
+                                &vdq, &vdk, &vdkr, &vdv, n.B, n.H, n.Sq, n.Skv, n.d, scale, dtype_code(q),
+                                ws.data_ptr(), workspace_bytes(ws, n.dev), at.stream);
+  released.end();
+  return rc ? PyLong_FromLong(rc) : tensors({dq, dk, dkr, dv});
+}
+
+// A cache [num_blocks, block_size, rank + 64] with its table and lengths; its rank.
+int latent_cache(CacheDims& c, at::Device dev, at::ScalarType dt, int64_t B, const Tensor& cache, const Tensor& table,
+                 const Tensor& lens) {
+  if (cache.dim() != 3 || table.dim() != 2 || cache.size(2) <= kRope)
+    throw BadArgument{"cache [num_blocks,block_size,rank+64], table [B,max_blocks]"};
+  fit("cache", cache, dev, dt, cache.sizes());
+  fit("block_table", table, dev, at::kInt, {B, table.size(1)});
+  fit("seq_lens", lens, dev, at::kInt, {B});
+  c = {narrow(cache.size(1)), narrow(cache.size(0)), narrow(table.size(1))};
+  return narrow(cache.size(2) - kRope);
+}
+
+// (handle, q, cache, block_table, seq_lens, tree_masks, out, lse, workspace, window, scale, stream)
+PyObject* latent_paged(PyObject* const* a) {
+  const Library lib = library(a[0]);
+  const Tensor &q = tensor(a[1], "q"), &cache = tensor(a[2], "cache");
+  const Tensor &table = tensor(a[3], "block_table"), &lens = tensor(a[4], "seq_lens");
+  const Tensor tree = maybe(a[5], "tree_masks");
+  Tensor out = maybe(a[6], "out"), lse = maybe(a[7], "lse"), ws = maybe(a[8], "workspace");
+  const at::Device dev = cuda_device(q, "q");
+  const auto dt = q.scalar_type();
+  four_dims(q, "q must be [B,H,Sq,rank+64] (any strides but the last)");
+  const int B = narrow(q.size(0)), H = narrow(q.size(1)), Sq = narrow(q.size(2));
+  CacheDims c;
+  const int rank = latent_cache(c, dev, dt, B, cache, table, lens);
+  const fa_view vq = view("q", q, dev, dt, {B, H, Sq, rank + kRope});
+  if (tree.defined()) fit("tree_masks", tree, dev, at::kLong, {B, Sq});
+  const int window = integer(a[9]);
+  const float scale = real(a[10]);
+  const Place at(dev, a[11]);
+  Released released;
+  if (out.defined()) fit("out", out, dev, dt, {B, H, Sq, rank});
+  else out = empty({B, H, Sq, rank}, dev, dt);
+  if (lse.defined()) fit("lse", lse, dev, at::kFloat, {B, H, Sq});
+  else lse = empty({B, H, Sq}, dev, at::kFloat);
+  if (!ws.defined()) ws = workspace_of(lib.latent_paged_bytes(B, H, Sq, rank, c.block_size, c.max_blocks), dev);
+  const int rc = lib.latent_paged(&vq, cache.data_ptr(), data<int>(table), data<int>(lens), data<long long>(tree),
+                                  out.data_ptr(), data<float>(lse), B, H, Sq, rank, c.block_size, c.num_blocks,
+                                  c.max_blocks, window, scale, dtype_code(q), ws.data_ptr(),
+                                  workspace_bytes(ws, dev), at.stream);
+  released.end();
+  return rc ? PyLong_FromLong(rc) : tensors({out, lse});
+}
+
+// (handle, latent, k_rope, q_rope, q_out, cache, block_table, seq_lens, positions, weight, turns, eps,
+//  interleaved, rope_scale, stream)
+PyObject* latent_append(PyObject* const* a) {
+  const Library lib = library(a[0]);
+  const Tensor &latent = tensor(a[1], "latent"), &kr = tensor(a[2], "k_rope"), &qr = tensor(a[3], "q_rope");
+  Tensor qo = maybe(a[4], "q_out");
+  const Tensor &cache = tensor(a[5], "cache"), &table = tensor(a[6], "block_table"), &lens = tensor(a[7], "seq_lens");
+  const Tensor positions = maybe(a[8], "positions"), weight = maybe(a[9], "weight");
+  const Tensor& turns = tensor(a[10], "turns");
+  const at::Device dev = cuda_device(latent, "latent");
+  const auto dt = latent.scalar_type();
+  if (latent.dim() != 3 || qr.dim() != 4)
+    throw BadArgument{"latent [B,Sq,rank], k_rope [B,Sq,64], q_rope [B,H,Sq,64] (any strides but the last)"};
+  const int B = narrow(latent.size(0)), Sq = narrow(latent.size(1)), H = narrow(qr.size(1));
+  CacheDims c;
+  const int rank = latent_cache(c, dev, dt, B, cache, table, lens);
+  const Sizes qs = {B, H, Sq, kRope};
+  const fa_view vl = flat_view("latent", latent, dev, dt, B, Sq, rank), vk = flat_view("k_rope", kr, dev, dt, B, Sq, kRope),
+                vq = view("q_rope", qr, dev, dt, qs);
+  fit("turns", turns, dev, at::kLong, {kRope / 2});
+  if (positions.defined()) fit("positions", positions, dev, at::kInt, {B, Sq});
+  if (weight.defined()) fit("weight", weight, dev, dt, {rank});
+  const float eps = real(a[11]), rope_scale = real(a[13]);
+  const bool interleaved = truth(a[12]);
+  const Place at(dev, a[14]);
+  Released released;
+  if (!qo.defined()) qo = empty({B, H, Sq, kRope}, dev, dt);
+  const fa_view vqo = view("q_out", qo, dev, dt, qs, true);
+  const int rc = lib.latent_append(&vl, &vk, &vq, &vqo, cache.data_ptr(), data<int>(table), data<int>(lens),
+                                   data<int>(positions), data<void>(weight), eps, data<unsigned long long>(turns),
+                                   interleaved, rope_scale, B, H, Sq, rank, c.block_size, c.num_blocks, c.max_blocks,
+                                   dtype_code(latent), at.stream);
+  released.end();
+  return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(qo);
+}
+
 // ----------------------------------------------------------------- module --
 // Nothing thrown leaves a function: bad arguments become ValueError (or the
 // Python error already set), anything else RuntimeError.
@@ -610,6 +790,8 @@ PyMethodDef methods[] = {
     method<ragged, 14>("ragged"),             method<norm_rope, 13>("norm_rope"),
     method<norm_rope_bwd, 19>("norm_rope_bwd"), method<append, 16>("append"),
     method<step, 19>("step"),
+    method<latent_forward, 11>("latent_forward"), method<latent_backward, 17>("latent_backward"),
+    method<latent_paged, 12>("latent_paged"), method<latent_append, 15>("latent_append"),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_fa_torch", nullptr, -1, methods,

@@ -390,6 +390,104 @@ int fa_bwd_span(const void* q, const void* k, const void* v, const int* key_begi
                 size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * Latent attention, expanded: the keys and values of every head come from one latent
+ * vector a token (expanded by the caller's projection), and a rotated part of the key is
+ * shared by all heads. With q of d + 64 elements, k and v of d:
+ *
+ *   s_ij = scale * (<q_i[0:d], k_j> + <q_i[d:d+64], k_rope_j>)
+ *   P_ij = exp(s_ij - lse_i),  lse_i = log(sum_j exp(s_ij)),  out_i = sum_j P_ij v_j
+ *
+ * for the keys that row i sees: key_begin, key_end ([B][Sq] int32) as for fa_fwd_span, or
+ * both NULL: 0 <= j <= i + Skv - Sq. A row that sees no key gets out = 0 and lse =
+ * -infinity. Sq and Skv are unrelated; d is 64 or 128.
+ *
+ * q [B][H][Sq][d+64], k, v [B][H][Skv][d], k_rope [B][1][Skv][64] (its stride_h is not read)
+ * and out [B][H][Sq][d] are views; here strides must be positive where a dimension has more
+ * than one row (else FA_ERR_SHAPE) and multiples of 16 bytes. So q is a projection's rows
+ * [B][Sq][H][d+64], k and v the two parts of another's [B][Skv][H][2d]. lse is [B][H][Sq]
+ * float32. FA_BF16 and FA_F16 only (else FA_ERR_DTYPE). As for fa_fwd_span, q, k, k_rope, v,
+ * out and dout must be finite everywhere, masked positions included; a NaN score that a row
+ * sees gives NaN in its out and lse.
+ */
+int fa_fwd_latent(const fa_view* q, const fa_view* k, const fa_view* k_rope, const fa_view* v,
+                  const int* key_begin, const int* key_end, const fa_view* out, float* lse, int B,
+                  int H, int Sq, int Skv, int d, float scale, int dtype, fa_stream_t stream);
+
+/*
+ * Backward of fa_fwd_latent: dq, dk, dv, views like q, k, v, and dk_rope like k_rope, summed
+ * over the heads. Same bits on every call. Rows that see nothing contribute nothing; keys
+ * that no row sees get zeros. Views that are written must not overlap anything.
+ * workspace: caller-owned, 256-byte aligned, contents on entry without meaning; calls that
+ * may overlap on the GPU need one each.
+ */
+int fa_bwd_latent(const fa_view* q, const fa_view* k, const fa_view* k_rope, const fa_view* v,
+                  const int* key_begin, const int* key_end, const fa_view* out, const fa_view* dout,
+                  const float* lse, const fa_view* dq, const fa_view* dk, const fa_view* dk_rope,
+                  const fa_view* dv, int B, int H, int Sq, int Skv, int d, float scale, int dtype,
+                  void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* Workspace bytes of fa_bwd_latent: two floats a query row (Sq rounded up to 128), 8 bytes for
+ * 64 of them in each batch, 64 floats a key of every head, each region 256-byte aligned.
+ * Returns 0 for invalid sizes. */
+size_t fa_bwd_latent_workspace_bytes(int B, int H, int Sq, int Skv, int d);
+
+/*
+ * Latent attention, absorbed: one or a few new tokens of each of B sequences of unequal length
+ * over a paged cache of one row a token, [latent (rank) | rotated key part (64)], which is key
+ * and, its first rank elements, value of every head:
+ *
+ *   s_j = scale * <q, c_j>,  out = sum_j softmax(s)_j c_j[0:rank],  lse = log(sum_j exp(s_j))
+ *
+ * with q [B][H][Sq][rank+64] absorbed into the latent's space (the query's part for k times the
+ * head's key expansion, beside its rotated part; scale is that of the query before). Then out
+ * [B][H][Sq][rank], contiguous like lse, times the head's value expansion is that head's output.
+ *
+ * cache: [num_blocks][block_size][rank+64], contiguous; block_table, seq_lens, the keys a row
+ * sees (window), rows that see nothing, what of table and cache is read, and replays with other
+ * lengths are as for fa_fwd_ragged_paged. tree_masks (or NULL): [B][Sq] 64-bit words in device
+ * memory for drafted tokens that form a tree. Row s then sees every key before the Sq new
+ * tokens, and new token t (at key seq_lens[b] - Sq + t) where bit t of tree_masks[b][s] is
+ * set, its own included; bits from Sq on are not looked at.
+ *
+ * q is a view with positive strides, as for fa_fwd_latent. rank is 256 or 512, H * Sq <= 1024,
+ * block_size and max_blocks as for fa_fwd_ragged_paged, with tree_masks Sq <= 64 and no window
+ * (else FA_ERR_SHAPE). FA_BF16 and FA_F16 only. workspace: as for fa_fwd_ragged_paged. Results
+ * are the same bits on every call with the same lengths.
+ */
+int fa_fwd_latent_paged(const fa_view* q, const void* cache, const int* block_table,
+                        const int* seq_lens, const long long* tree_masks, void* out, float* lse,
+                        int B, int H, int Sq, int rank, int block_size, int num_blocks,
+                        int max_blocks, int window, float scale, int dtype, void* workspace,
+                        size_t workspace_bytes, fa_stream_t stream);
+
+/* Workspace bytes of fa_fwd_latent_paged: two partial results of H * Sq rows of rank + 1 floats
+ * and 16 bytes for each of at most 152 / ceil(H * Sq / 64) shares of the keys, each region
+ * 256-byte aligned. Returns 0 for invalid sizes. */
+size_t fa_fwd_latent_paged_workspace_bytes(int B, int H, int Sq, int rank, int block_size,
+                                           int max_blocks);
+
+/*
+ * The last Sq tokens of each of B sequences into the paged latent cache: for the token at row
+ * p = seq_lens[b] - Sq + s of its sequence,
+ *
+ *   cache row = [ latent * (mean latent^2 + eps)^(-1/2) * weight | rotated k_rope ]
+ *   q_out     = rotated q_rope                                    (weight NULL: no norm)
+ *
+ * Norm, rotation (here of all 64 elements, turns [32]), interleaved and rope_scale are as for
+ * fa_qk_norm_rope, tokens that are not stored and what else stays as it was as for
+ * fa_qk_norm_rope_append. A token's position is p, or positions[b][s] ([B][Sq] int32; drafted
+ * tokens of a tree stand at their depth). latent [B][1][Sq][rank], k_rope [B][1][Sq][64],
+ * q_rope and q_out [B][H][Sq][64] are views as for fa_fwd_latent; q_out may be q_rope. cache:
+ * [num_blocks][block_size][rank+64]. FA_F32, FA_F16 or FA_BF16; rank 256 or 512.
+ */
+int fa_latent_append(const fa_view* latent, const fa_view* k_rope, const fa_view* q_rope,
+                     const fa_view* q_out, void* cache, const int* block_table,
+                     const int* seq_lens, const int* positions, const void* weight, float eps,
+                     const unsigned long long* turns, int interleaved, float rope_scale, int B,
+                     int H, int Sq, int rank, int block_size, int num_blocks, int max_blocks,
+                     int dtype, fa_stream_t stream);
+
+/*
  * Size of the fixed device scratch array behind fa_bwd_noalloc (32 MiB). A
  * call fits when fa_bwd_workspace_bytes(B, Hq, Hkv, S, d) is at most this,
  * e.g. B*Hq = 96 heads at S = 1024, d = 64 (about 25.9 MB). The limit uses

@@ -141,6 +141,59 @@ def ragged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, window=0
     return res
 
 
+def latent_attention(q, k, k_rope, v, begin, end, scale, dout=None, u=0.0):
+    """Expanded latent attention: q [B, H, Sq, d + r], k, v [B, H, Skv, d], k_rope [B, Skv, r]
+    shared by the heads. Each head is span attention over keys [k, k_rope]; the gradient of the
+    shared part is the heads' sum, in fp32 before its one rounding."""
+    B, H, Sq, _ = q.shape
+    d, out = k.shape[-1], {}
+    for b in range(B):
+        for h in range(H):
+            r = span_head(q[b, h], np.concatenate((k[b, h], k_rope[b]), 1), v[b, h], begin[b], end[b],
+                          scale, dout=None if dout is None else dout[b, h], u=u)
+            if dout is not None:
+                for n in ("dk", "dk_tol"):
+                    r["dk_rope" + n[2:]], r[n] = r[n][:, d:], r[n][:, :d]
+            for n, x in r.items():
+                a = out.setdefault(n, np.zeros((B,) + x.shape if n.startswith("dk_rope") else (B, H) + x.shape))
+                if n.startswith("dk_rope"):
+                    a[b] += x
+                else:
+                    a[b, h] = x
+    if dout is not None:
+        out["dk_rope_tol"] += 1.01 * u * np.abs(out["dk_rope"]) + \
+            H * F32 * np.abs(out["dk_rope"]) + 1e-30
+    return out
+
+
+def latent_paged(q, cache, block_table, seq_lens, scale, window=0, tree=None, u=0.0):
+    """New tokens q [B, H, Sq, rank + 64] over pages [num_blocks, block_size, rank + 64], which are
+    keys and, their first rank elements, values; tree [B, Sq]: bit t for new token t."""
+    B, H, Sq, w = q.shape
+    nb, bs, rank = cache.shape[0], cache.shape[1], w - 64
+    res = {"out": np.zeros((B, H, Sq, rank)), "out_tol": np.zeros((B, H, Sq, rank)),
+           "lse": np.full((B, H, Sq), -np.inf), "lse_tol": np.zeros((B, H, Sq))}
+    for b in range(B):
+        n = min(max(int(seq_lens[b]), 0), block_table.shape[1] * bs)
+        first = max(0, n - Sq + 1 - window) if window else 0
+        K = np.zeros((n, w))
+        for j in range(first, n):
+            page = block_table[b, j // bs]
+            if 0 <= page < nb:
+                K[j] = cache[page, j % bs]
+        for s in range(Sq if n else 0):
+            if tree is None:
+                p = n - Sq + s
+                seen = np.arange(max(0, p + 1 - window) if window else 0, max(p + 1, 0))
+            else:
+                seen = np.array([j for j in range(n) if j < n - Sq or (int(tree[b, s]) >> (j - n + Sq)) & 1], int)
+            x = q[b, :, s]
+            r = span_head(x, K[seen], K[seen][:, :rank], np.zeros(H, int), np.full(H, len(seen)), scale, u=u)
+            for name in res:
+                res[name][b, :, s] = r[name]
+    return res
+
+
 def norm_rope(x, w, inv_freq, positions, eps=1e-6, interleaved=False, rope_scale=1.0, dy=None):
     """x [B, H, S, d], positions [B, S]: y, or given dy (dx, dw)."""
     d, half = x.shape[-1], len(inv_freq)

@@ -1,0 +1,127 @@
+"""Latent attention with expanded keys and values on the GPU, forward and backward, against the
+64-bit definition within derived bounds, and its gradients against differences."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from bounds import DT, check, f64, half_step
+from oracle import operators as ops
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def make(B, H, Sq, Skv, d, dtype, seed=0, packed=True, scale_q=1.0):
+    """q, k, k_rope, v, dout on the CPU; packed: as views of two projections' rows."""
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)
+    q = (r(B, Sq, H, d + 64) * scale_q).to(DT[dtype]).transpose(1, 2)
+    kv = r(B, Skv, H, 2 * d).to(DT[dtype]).transpose(1, 2)
+    k, v = kv[..., :d], kv[..., d:]
+    down = r(B, Skv, 96 + 64).to(DT[dtype])[..., 96:]
+    dout = r(B, Sq, H, d).to(DT[dtype]).transpose(1, 2)
+    x = [q, k, down, v, dout]
+    return x if packed else [t.contiguous() for t in x]
+
+
+def to_dev(x):
+    """On the device with the strides it has."""
+    if x is None or x.is_contiguous():
+        return None if x is None else x.to(DEV)
+    base = torch.empty(x.untyped_storage().nbytes() // x.element_size(), dtype=x.dtype, device=DEV)
+    y = base.as_strided(x.shape, x.stride(), x.storage_offset())
+    y.copy_(x)
+    return y
+
+
+def run(fa, x, spans=None, scale=None, backward=True):
+    q, k, kr, v, do = (to_dev(t) for t in x)
+    b, e = (None, None) if spans is None else (t.to(DEV) for t in spans)
+    out, lse = fa.attention_latent_forward(q, k, kr, v, b, e, scale=scale)
+    res = dict(out=out, lse=lse)
+    if backward:
+        g = fa.attention_latent_backward(q, k, kr, v, out, do, lse, b, e, scale=scale)
+        res.update(zip(("dq", "dk", "dk_rope", "dv"), g))
+    torch.cuda.synchronize()
+    assert fa.fa_last_device_status() == 0
+    return res
+
+
+def compare(got, x, spans=None, scale=None):
+    q, k, kr, v, do = (f64(t) for t in x)
+    B, H, Sq, w = q.shape
+    Skv = k.shape[2]
+    if spans is None:
+        end = np.tile(np.clip(np.arange(Sq) + Skv - Sq + 1, 0, Skv), (B, 1))
+        begin = np.zeros_like(end)
+    else:
+        begin, end = (t.numpy() for t in spans)
+    want = ops.latent_attention(q, k, kr, v, begin, end, w ** -0.5 if scale is None else scale,
+                                do if "dq" in got else None, half_step(x[0].dtype))
+    for n in got:
+        check(n, got[n], want[n], want[n + "_tol"])
+
+
+CASES = [
+    # B, H, Sq, Skv, d, dtype, mask
+    (1, 1, 1, 1, 64, "bf16", None),
+    (1, 1, 1, 1, 128, "fp16", None),
+    (1, 2, 1, 300, 128, "bf16", None),            # one query at the end of a longer context
+    (2, 3, 127, 127, 128, "bf16", None),
+    (1, 2, 129, 129, 64, "fp16", None),
+    (1, 2, 257, 257, 128, "fp16", None),
+    (2, 2, 300, 200, 128, "bf16", None),          # fewer keys than queries: rows that see nothing
+    (1, 2, 200, 450, 64, "bf16", None),
+    (3, 1, 65, 1000, 128, "bf16", None),
+    (1, 3, 640, 640, 128, "bf16", "documents"),
+    (2, 2, 500, 500, 64, "fp16", "documents"),
+    (1, 2, 700, 700, 128, "fp16", "window"),
+    (2, 2, 333, 333, 128, "bf16", "padded"),
+    (1, 2, 333, 600, 64, "bf16", "prefix"),
+    (1, 1, 400, 900, 128, "bf16", "gaps"),
+    (1, 2, 384, 384, 64, "fp16", "gaps"),
+    (2, 1, 260, 260, 128, "bf16", "nothing"),
+    (1, 2, 130, 70, 64, "bf16", "all"),
+    (1, 40, 64, 64, 64, "bf16", None),
+]
+
+
+def spans_of(fa, mask, B, Sq, Skv, seed):
+    if mask is None:
+        return None
+    g = torch.Generator().manual_seed(seed)
+    if mask == "documents":
+        return fa.key_spans(B, Sq, Skv, doc_lens=[[100, 28, 1, 200, 60 + b] for b in range(B)])
+    if mask == "window":
+        return fa.key_spans(B, Sq, Skv, window=150)
+    if mask == "padded":
+        return fa.key_spans(B, Sq, Skv, kv_lens=[Skv - 70 - 130 * b for b in range(B)])
+    if mask == "prefix":
+        return fa.key_spans(B, Sq, Skv, prefix_lens=Skv - Sq + 200)
+    if mask == "all":
+        return fa.key_spans(B, Sq, Skv, causal=False)
+    if mask == "nothing":
+        return torch.full((B, Sq), 7, dtype=torch.int32), torch.full((B, Sq), 7, dtype=torch.int32)
+    # any ranges, in no order, some empty, some reaching outside the keys
+    begin = torch.randint(-20, Skv, (B, Sq), generator=g, dtype=torch.int32)
+    end = begin + torch.randint(-30, Skv // 3, (B, Sq), generator=g, dtype=torch.int32)
+    begin[:, 128:200] = Skv + 5      # rows of a tile that see nothing
+    return begin, end
+
+
+@pytest.mark.parametrize("B,H,Sq,Skv,d,dtype,mask", CASES)
+def test_expanded(fa, B, H, Sq, Skv, d, dtype, mask):
+    x = make(B, H, Sq, Skv, d, dtype, seed=Sq + Skv + d)
+    spans = spans_of(fa, mask, B, Sq, Skv, Sq)
+    compare(run(fa, x, spans), x, spans)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_scores(fa, d):
+    """Scores of tens: the reference maximum moves from tile to tile."""
+    x = make(1, 2, 400, 400, d, "bf16", seed=9, scale_q=30.0)
+    compare(run(fa, x), x)
+    x = make(1, 2, 400, 400, d, "fp16", seed=10)
+    compare(run(fa, x, scale=1.0), x, scale=1.0)
