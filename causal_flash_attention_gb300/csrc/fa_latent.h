@@ -89,7 +89,7 @@ struct LatentPagedParams {
   static constexpr int kTileKeys = 64;
   static constexpr int Hkv = 1;
   CUtensorMap tm;          // [num_blocks][block_size][rank + 64], box (64, box_rows, 1), 128B swizzle
-  HeadView q;              // [B][H][Sq][rank + 64]
+  CUtensorMap tm_q;        // 4-D (rank + 64, Sq, H, B), box (64, group_tokens, group_heads, 1)
   void* out;               // [B][R][rank]
   float* lse;              // [B][R]
   const int* block_table;  // [B][max_blocks]
@@ -98,7 +98,8 @@ struct LatentPagedParams {
   float* part_out;         // [2 * n_ctas][R][rank] fp32 out = O / l of a part of a sequence
   float* part_lse2;        // [2 * n_ctas][R]       its log2-sum-exp2 of scaled scores
   int4* starts;            // [n_ctas] where each share begins
-  int B, H, Sq, R, groups, group_rows;
+  // a group's rows: all tokens (up to 64) of group_heads heads, or 64 tokens of one head
+  int B, H, Sq, R, groups, group_heads, group_tokens;
   int block_size, box_rows, max_blocks, num_blocks;
   int capacity;            // keys a table row can hold (at most 2^31 - 128)
   int window;              // keys a row sees, its own position included; 0: all

@@ -54,15 +54,17 @@ int take(std::initializer_list<ViewOf> views, int B, int dtype) {
 }
 
 // 4-D view (d, S, H, B) of a strided 16-bit tensor; box = 64 columns (128 bytes, one
-// swizzle span) x box_rows rows.
-bool make_map(CUtensorMap* m, const HeadView& v, int B, int H, int S, int d, int box_rows, bool bf16) {
+// swizzle span) x box_rows rows x box_heads heads.
+bool make_map(CUtensorMap* m, const HeadView& v, int B, int H, int S, int d, int box_rows, bool bf16,
+              int box_heads = 1) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(S), static_cast<cuuint64_t>(H),
                               static_cast<cuuint64_t>(B)};
   auto bytes = [&](long long stride) { return static_cast<cuuint64_t>(stride > 0 ? stride * 2 : d * 2); };
   const cuuint64_t strides[3] = {bytes(v.ss), bytes(v.sh), bytes(v.sb)};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(kChunk), static_cast<cuuint32_t>(box_rows), 1, 1};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(kChunk), static_cast<cuuint32_t>(box_rows),
+                             static_cast<cuuint32_t>(box_heads), 1};
   const cuuint32_t one[4] = {1, 1, 1, 1};
   return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, v.data, dims, strides,
              box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -98,14 +100,16 @@ bool blocks_ok(int block_size, int num_blocks, int max_blocks) {
 constexpr int kMaxRows = 1024;   // H * Sq
 constexpr int kGroupRows = 64;
 struct PagedPlan {
-  int groups, group_rows, shares;
+  int groups, group_heads, group_tokens, shares;
   size_t part_out, part_lse2, starts, total;
 };
 PagedPlan paged_plan(int B, int H, int Sq, int rank, int block_size, int max_blocks) {
   PagedPlan w;
   const long long R = static_cast<long long>(H) * Sq;
-  w.groups = static_cast<int>((R + kGroupRows - 1) / kGroupRows);
-  w.group_rows = static_cast<int>((R + w.groups - 1) / w.groups);
+  w.group_tokens = std::min(Sq, kGroupRows);
+  const int heads = kGroupRows / w.group_tokens;   // of a group, at most
+  w.groups = Sq > kGroupRows ? H * ((Sq + kGroupRows - 1) / kGroupRows) : (H + heads - 1) / heads;
+  w.group_heads = Sq > kGroupRows ? 1 : (H + w.groups - 1) / w.groups;
   const long long tiles =
       (static_cast<long long>(max_blocks) * block_size + LatentPagedParams::kTileKeys - 1) / LatentPagedParams::kTileKeys;
   w.shares = static_cast<int>(std::min<long long>(152 / w.groups, B * tiles));
@@ -224,7 +228,8 @@ int fa_fwd_latent_paged(const fa_view* q, const void* cache, const int* block_ta
   if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_SCALE;
   LatentPagedParams p;
   std::memset(&p, 0, sizeof(p));
-  const int rc = take({{q, H, Sq, &p.q}}, B, dtype);
+  HeadView vq;
+  const int rc = take({{q, H, Sq, &vq}}, B, dtype);
   if (rc != FA_OK) return rc;
   if (!cache || !block_table || !seq_lens || !out || !lse) return FA_ERR_NULL;
   if (!aligned(cache, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
@@ -245,7 +250,8 @@ int fa_fwd_latent_paged(const fa_view* q, const void* cache, const int* block_ta
   if (!enc || enc(&p.tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                   const_cast<void*>(cache), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+      !make_map(&p.tm_q, vq, B, H, Sq, width, w.group_tokens, bf16, w.group_heads))
     return FA_ERR_TMA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.out = out;
@@ -259,7 +265,8 @@ int fa_fwd_latent_paged(const fa_view* q, const void* cache, const int* block_ta
   p.B = B; p.H = H; p.Sq = Sq;
   p.R = H * Sq;
   p.groups = w.groups;
-  p.group_rows = w.group_rows;
+  p.group_heads = w.group_heads;
+  p.group_tokens = w.group_tokens;
   p.block_size = block_size; p.max_blocks = max_blocks; p.num_blocks = num_blocks;
   p.capacity = static_cast<int>(std::min(static_cast<long long>(max_blocks) * block_size, 0x7fffff80LL));
   // a window that no position outgrows hides nothing (and would overflow positions)

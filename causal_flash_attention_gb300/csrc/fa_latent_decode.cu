@@ -124,8 +124,12 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
   const int warp = static_cast<int>(warp_id());
   const int lane = static_cast<int>(lane_id());
   const int share_id = static_cast<int>(blockIdx.x) / p.groups;
-  const int row0 = static_cast<int>(blockIdx.x) % p.groups * p.group_rows;   // this CTA's rows of a sequence
-  const int rows = min(p.group_rows, p.R - row0);
+  // this CTA's rows of a sequence: from token s0 of head h0 on
+  const int group = static_cast<int>(blockIdx.x) % p.groups;
+  const int per_head = (p.Sq + p.group_tokens - 1) / p.group_tokens;   // groups a head is cut into
+  const int h0 = group / per_head * p.group_heads, s0 = group % per_head * p.group_tokens;
+  const int row0 = h0 * p.Sq + s0;
+  const int rows = min(p.group_heads, p.H - h0) * min(p.group_tokens, p.Sq - s0);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NP; ++s) {
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
       mbar_init(x_full(s), 1);
       mbar_init(x_empty(s), 1);
     }
-    mbar_init(q_ready, 4);   // one arrival per softmax warp and segment
+    mbar_init(q_ready, 1);   // once a segment
     mbar_init(s_full(0), 1);
     mbar_init(s_full(1), 1);
     mbar_init(p_full, 4);
@@ -145,6 +149,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.tm);
+    tma_prefetch_desc(&p.tm_q);
   }
   // tensor memory: S at columns 0 and 64, O^T part m at 128 + m NR
   if (warp == 1) {
@@ -280,40 +285,30 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
       }
     }
   } else {
-    // ===== stage Q, softmax per tile, O^T =====
+    // ===== queries, softmax per tile, O^T =====
     const int quarter = warp & 3;               // TMEM lane quarter of this warp
     const int tid = static_cast<int>(threadIdx.x) - 64;
     const int r = quarter * 16 + lane;          // this thread's row of the group, if any
     const bool busy = quarter * 16 < rows;      // the warp holds rows
     const bool real = lane < 16 && r < rows;
-    const int s = real ? (row0 + r) % p.Sq : 0;
+    const int s = real ? s0 + r % p.group_tokens : 0;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t o_tmem = tmem + lane_off + 128;
     const float c = p.scale_log2;
     uint8_t* const p_row = smem + Cfg::kOffP + (lane < 16 && r < NR ? r : 0) * 128;
 
-    // A segment's queries: 16-byte unit u of a 128-byte row r sits at unit u ^ (r % 8); rows
-    // past the group's are zero.
-    auto stage_q = [&](int b) {
-      constexpr int kUnits = (RANK + kRope) / 8;   // 16-byte units a row
-      const Elem* q = static_cast<const Elem*>(p.q.data) + b * p.q.sb;
-      for (int i = tid; i < NR * kUnits; i += 128) {
-        const int row = i / kUnits, u = i - row * kUnits;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (row < rows) {
-          const int h = (row0 + row) / p.Sq, t = (row0 + row) - h * p.Sq;
-          v = *reinterpret_cast<const uint4*>(q + h * p.q.sh + t * p.q.ss + u * 8);
-        }
-        *reinterpret_cast<uint4*>(smem + (u >> 3) * Cfg::kQB + row * 128 +
-                                  (((u & 7) ^ (row & 7)) << 4)) = v;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_ready);
+    // A segment's queries (heads past the last come as zeros; rows past the group's are whatever
+    // the memory held, and so are their scores, which nobody reads).
+    auto load_q = [&](int b) {
+      if (tid != 0) return;
+      mbar_arrive_expect_tx(q_ready, Cfg::kChunks * p.group_heads * p.group_tokens * 128);
+      for (int cc = 0; cc < Cfg::kChunks; ++cc)
+        tma_load_4d(sbase + cc * Cfg::kQB, &p.tm_q, q_ready, cc * kChunk, s0, h0, b);
     };
 
     bool more = seg.next(p);
-    if (more) stage_q(seg.b);
+    if (more) load_q(seg.b);
+    int n_q = 1;        // segments whose queries have been asked for
     // A wait that fails in one warp must not leave the others in a barrier: the warp goes on
     // without touching anything until the next vote, where all four learn of it.
     bool ok = true, dead = false;
@@ -327,6 +322,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
       const int b = seg.b, n = seg.n, tile0 = seg.tile0;
       const bool whole = seg.whole;
       const SeqKeys keys = seg.keys;
+      more = seg.next(p);
       const int pos = keys.len - p.Sq + s;
       int row_lo = 0, row_hi = 0;   // keys of this row
       uint64_t tree = 0;
@@ -344,6 +340,10 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
         const int kv0 = (tile0 + j) * kTile;
         wait(s_full(g & 1), g >> 1);
         tc_fence_after();
+        if (j == n - 1 && more && ok) {   // every S of this segment has been formed
+          load_q(seg.b);
+          ++n_q;
+        }
         const HiddenRows hidden(p, keys, kv0);
         if (hidden.any() && ok) {   // rows that nobody sees must not reach O^T through P = 0
           const int na = hidden.a1 - hidden.a0, nh = na + hidden.b1 - hidden.b0;
@@ -440,10 +440,6 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
         if (lane == 0) mbar_arrive(p_full);
       }
       if (dead) break;
-      // the next segment's queries (every S of this one has been formed), then this
-      // segment's result
-      more = seg.next(p);
-      if (more && ok) stage_q(seg.b);
       if (real) {
         const PartSum sum(l, m_ref);
         row_f[r] = sum.inv;
@@ -477,6 +473,8 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
       row_warps_any(false);   // the factors have been read
       head = false;
     }
+    // the last queries asked for land before the CTA releases its memory
+    if (tid == 0 && *abort_flag && share.begin < share.end) drain_wait_d(q_ready, (n_q - 1) & 1, p.status);
   }
 
   tc_fence_before();
@@ -589,9 +587,10 @@ cudaError_t launch_main(const LatentPagedParams& p, cudaStream_t stream) {
 template <int RANK, bool kBf16>
 cudaError_t launch_impl(const LatentPagedParams& p, cudaStream_t stream) {
   using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
-  const cudaError_t e = p.group_rows <= 16   ? launch_main<RANK, 16, kBf16>(p, stream)
-                        : p.group_rows <= 32 ? launch_main<RANK, 32, kBf16>(p, stream)
-                                             : launch_main<RANK, 64, kBf16>(p, stream);
+  const int rows = p.group_heads * p.group_tokens;
+  const cudaError_t e = rows <= 16   ? launch_main<RANK, 16, kBf16>(p, stream)
+                        : rows <= 32 ? launch_main<RANK, 32, kBf16>(p, stream)
+                                     : launch_main<RANK, 64, kBf16>(p, stream);
   if (e != cudaSuccess) return e;
   const int y = std::min(p.R, std::max(16, 2048 / p.n_ctas));
   return launch_dependent(latent_merge_kernel<Elem, RANK>, dim3(static_cast<unsigned>(p.n_ctas), y),

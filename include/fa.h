@@ -461,8 +461,9 @@ int fa_fwd_latent_paged(const fa_view* q, const void* cache, const int* block_ta
                         size_t workspace_bytes, fa_stream_t stream);
 
 /* Workspace bytes of fa_fwd_latent_paged: two partial results of H * Sq rows of rank + 1 floats
- * and 16 bytes for each of at most 152 / ceil(H * Sq / 64) shares of the keys, each region
- * 256-byte aligned. Returns 0 for invalid sizes. */
+ * and 16 bytes for each of at most 152 / groups shares of the keys, each region 256-byte
+ * aligned, with groups of rows: H / floor(64 / Sq), or H * ceil(Sq / 64) for Sq above 64, rounded
+ * up. Returns 0 for invalid sizes. */
 size_t fa_fwd_latent_paged_workspace_bytes(int B, int H, int Sq, int rank, int block_size,
                                            int max_blocks);
 

@@ -65,6 +65,9 @@ CASES = [
     ([900, 899], 16, 5, 256, "bf16", 16, 333),
     ([4000], 16, 1, 512, "bf16", 64, 0),                  # one sequence cut into many shares
     ([3000], 128, 8, 256, "bf16", 64, 0),                 # the most rows
+    ([500, 333], 7, 130, 256, "bf16", 64, 0),             # heads cut into groups of tokens
+    ([90, 700], 11, 33, 512, "bf16", 64, 100),            # one head a group
+    ([90, 700], 10, 20, 512, "fp16", 64, 0),              # three heads a group, the last of one
     ([3, 1, 0, 200], 4, 4, 256, "bf16", 16, 2 ** 31 - 1),
     ([40] * 160, 2, 1, 256, "fp16", 16, 0),               # as many tiles as CTAs, and more
     ([5] * 200 + [2000] + [0] * 200, 2, 1, 256, "bf16", 64, 0),

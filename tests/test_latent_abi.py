@@ -87,8 +87,11 @@ def test_paged_refuses(fa_lib, kw, code):
 
 def test_paged_workspace_formula(fa_lib):
     up = lambda x: -(-x // 256) * 256
-    for B, H, Sq, rank, bs, mb in [(1, 1, 1, 256, 16, 1), (16, 128, 1, 512, 64, 128), (2, 128, 8, 512, 16, 20)]:
-        shares = min(152 // -(-H * Sq // 64), B * -(-(mb * bs) // 64))
+    for (B, H, Sq, rank, bs, mb), groups in [((1, 1, 1, 256, 16, 1), 1), ((16, 128, 1, 512, 64, 128), 2),
+                                             ((2, 128, 8, 512, 16, 20), 16), ((4, 20, 3, 512, 64, 9), 1),
+                                             ((4, 22, 3, 512, 64, 9), 2), ((1, 7, 130, 256, 64, 9), 21),
+                                             ((1, 31, 33, 256, 64, 90), 31)]:
+        shares = min(152 // groups, B * -(-(mb * bs) // 64))
         rows = 2 * shares * H * Sq
         want = up(rows * rank * 4) + up(rows * 4) + up(16 * shares)
         assert fa_lib.fa_fwd_latent_paged_workspace_bytes(B, H, Sq, rank, bs, mb) == want
