@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
   const Bars s_full{q_ready + 8};
   const uint32_t p_full = s_full(2), pv_done = p_full + 8, drain = p_full + 16;
 
-  const int warp = static_cast<int>(warp_id());
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(warp_id()), 0);
   const int lane = static_cast<int>(lane_id());
   const int share_id = static_cast<int>(blockIdx.x) / p.groups;
   // this CTA's rows of a sequence: from token s0 of head h0 on
@@ -221,69 +221,112 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
       for (int i = max(0, n_x - NX); i < n_x; ++i) drain_wait_d(x_full(i % NX), (i / NX) & 1, p.status);
     }
   } else if (warp == 1) {
-    // ===================== MMA issuer =====================
-    // Tile g's S goes out ahead of tile g - 1's O^T, except the first of a segment, whose
-    // queries are staged after the segment before has been read.
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = make_idesc(64, kTile, kBf16, false, false);
-      constexpr uint32_t idesc_o = make_idesc(128, NR, kBf16, true, false);
-      TileWalk walk{seg};
-      Ring<NP> at_s, at_o;
-      Ring<NX> xt;
-      int n_seg = 0;   // segments whose queries have been awaited
-      auto issue_s = [&](int g) -> bool {
-        if (walk.first && !mbar_wait(q_ready, n_seg++ & 1, abort_flag, p.status)) return false;
-        // (S_(g-2) has been read: p_full of tile g - 2 has been waited for)
-        const uint32_t d = tmem + (g & 1) * 64;
-        const uint64_t qa = make_sdesc(sbase, 16, 1024);
-        const uint64_t tb = make_sdesc(sbase + Cfg::kOffC, 16, 1024);
-        for (int m = 0; m < kPairs; ++m) {
-          if (!mbar_wait(full(at_s.slot), at_s.parity, abort_flag, p.status)) return false;
-          tc_fence_after();
-          const uint64_t a = qa + static_cast<uint64_t>(2 * m) * (Cfg::kQB >> 4);
-          const uint64_t bd = tb + static_cast<uint64_t>(at_s.slot) * (2 * CB >> 4);
-          mma_ss_product<8, true, Cfg::kQB, true, CB>(d, a, bd, idesc_s, m > 0 ? 1u : 0u);
-          at_s.next();
-        }
-        if (!mbar_wait(x_full(xt.slot), xt.parity, abort_flag, p.status)) return false;
-        tc_fence_after();
-        mma_ss_product<4, true, Cfg::kQB, true, CB>(
-            d, qa + static_cast<uint64_t>(2 * kPairs) * (Cfg::kQB >> 4),
-            make_sdesc(sbase + Cfg::kOffX + xt.slot * CB, 16, 1024), idesc_s, 1u);
-        tc_commit(s_full(g & 1));
-        tc_commit(x_empty(xt.slot));
-        xt.next();
-        return true;
-      };
-      bool ok = true, have = walk.next(p);
+    // ===================== MMA issuer (the whole warp, one lane of it the MMAs) =====================
+    // Two streams of work, whichever is ready first: tile gs's S, once
+    // it has landed, and tile go's O^T once its P is there. (In a fixed order, S of the next tile
+    // first, a late load held up O^T, which frees the ring for the load after it.)
+    constexpr uint32_t idesc_s = make_idesc(64, kTile, kBf16, false, false);
+    constexpr uint32_t idesc_o = make_idesc(128, NR, kBf16, true, false);
+    TileWalk walk{seg};
+    Ring<NP> at_s, at_o;
+    Ring<NX> xt;
+    int n_seg = 0;      // segments whose queries have landed
+    int gs = 0, go = 0; // the next tile of either stream
+    bool begins = false;   // tile gs is its segment's first, and its queries have landed
+    bool first_of[2] = {false, false};   // the same of the tiles whose S is formed, by g % 2
+    const uint64_t qa = make_sdesc(sbase, 16, 1024);
+    const uint64_t pb = make_sdesc(sbase + Cfg::kOffP, 16, 1024);
+    auto ready = [](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)); };
+    // (votes make what was loaded the same in every lane for the compiler too, and with it the
+    // control flow and the descriptors: elect_one)
+    bool first_s = false;
+    auto next = [&]() {
+      const bool more = __all_sync(0xffffffffu, walk.next(p));
+      first_s = __all_sync(0xffffffffu, walk.first);
+      return more;
+    };
+    bool ok = true, have = next();
 #ifdef FA_WAIT_TEST
-      // wait-limit test build: nothing completes this phase before the abort
-      // path's own commit, so the wait runs out
-      if (have) ok = mbar_wait(drain, 0, abort_flag, p.status);
+    // wait-limit test build: nothing completes this phase before the abort
+    // path's own commit, so the wait runs out
+    if (have) ok = warp_wait(drain, 0, abort_flag, p.status);
 #endif
-      if (ok && have) ok = issue_s(0);
-      for (int g = 0; ok && have; ++g) {
-        const bool first = walk.first;   // tile g is its segment's first
-        have = walk.next(p);
-        if (have && !walk.first && !(ok = issue_s(g + 1))) break;
-        if (!(ok = mbar_wait(p_full, g & 1, abort_flag, p.status))) break;
+    long long idle_since = clock64();
+    uint32_t idle = 0;
+    while (ok && (have || go < gs)) {
+      bool worked = false;
+      // S_gs goes over S_(gs-2), which has been read when P_(gs-2) is there
+      if (have && gs <= go + 1) {
+        if (first_s && ready(q_ready, n_seg & 1)) {
+          ++n_seg;
+          first_s = false;
+          begins = true;
+        }
+        // the tile's last part has landed, and so, soon or already, have the others
+        if (!first_s && ready(x_full(xt.slot), xt.parity)) {
+          first_of[gs & 1] = begins;
+          begins = false;
+          const uint32_t d = tmem + (gs & 1) * 64;
+#pragma unroll
+          for (int m = 0; m < kPairs; ++m) {
+            if (!(ok = warp_wait(full(at_s.slot), at_s.parity, abort_flag, p.status))) break;
+            tc_fence_after();
+            const uint64_t cb = make_sdesc(sbase + Cfg::kOffC + at_s.slot * 2 * CB, 16, 1024);
+            if (elect_one())
+              mma_ss_steps<8, true, Cfg::kQB, true, CB>(d, qa + 2 * m * (Cfg::kQB >> 4), cb, idesc_s, m > 0 ? 1u : 0u);
+            at_s.next();
+          }
+          if (!ok) break;
+          const uint64_t xb = make_sdesc(sbase + Cfg::kOffX + xt.slot * CB, 16, 1024);
+          if (elect_one()) {
+            mma_ss_steps<4, true, Cfg::kQB, true, CB>(d, qa + 2 * kPairs * (Cfg::kQB >> 4), xb, idesc_s, 1u);
+            tc_commit(s_full(gs & 1));
+            tc_commit(x_empty(xt.slot));
+          }
+          xt.next();
+          ++gs;
+          have = next();
+          worked = true;
+        }
+      }
+      if (go < gs && ready(p_full, go & 1)) {
         tc_fence_after();
-        const uint64_t pb = make_sdesc(sbase + Cfg::kOffP, 16, 1024);
+        const uint32_t more = first_of[go & 1] ? 0u : 1u, o_t = tmem + 128;
+#pragma unroll
         for (int m = 0; m < kPairs; ++m) {   // O^T part m (+)= C_m^T P
           const uint64_t ca = make_sdesc(sbase + Cfg::kOffC + at_o.slot * 2 * CB, CB, 1024);
-          mma_ss_product<kTile / 16, false, 0, true, Cfg::kP>(tmem + 128 + m * NR, ca, pb, idesc_o, first ? 0u : 1u);
-          tc_commit(empty(at_o.slot));
+          if (elect_one()) {
+            mma_ss_steps<kTile / 16, false, 0, true, Cfg::kP>(o_t + m * NR, ca, pb, idesc_o, more);
+            tc_commit(empty(at_o.slot));
+            if (m == kPairs - 1) tc_commit(pv_done);
+          }
           at_o.next();
         }
-        tc_commit(pv_done);
-        if (have && walk.first && !(ok = issue_s(g + 1))) break;
+        ++go;
+        worked = true;
       }
-      if (!ok) {
-        // every MMA issued so far must finish before the TMEM is released
-        tc_commit(drain);
-        drain_wait_d(drain, 0, p.status);
+      if (worked) {
+        idle = 0;
+      } else if ((++idle & 15u) == 0) {   // as mbar_wait
+        if (idle == 16) idle_since = clock64();
+        bool stop = false;
+        if (lane == 0) {
+          stop = *abort_flag;
+          if (!stop && clock64() - idle_since > kWaitLimitCycles) {
+            *abort_flag = 1;
+            atomicOr(p.status, kStatusWaitTimeout);
+            stop = true;
+          }
+        }
+        ok = !__any_sync(0xffffffffu, stop);
       }
     }
+    if (!ok) {
+      // every MMA issued so far must finish before the TMEM is released
+      if (elect_one()) tc_commit(drain);
+      drain_wait_d(drain, 0, p.status);
+    }
+    __syncwarp();
   } else {
     // ===== queries, softmax per tile, O^T =====
     const int quarter = warp & 3;               // TMEM lane quarter of this warp
@@ -454,18 +497,26 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
         if (whole) p.lse[orow + tid] = row_lse[tid] * kLn2D;
         else p.part_lse2[prow + tid] = row_lse[tid];
       }
-      for (int m = 0; m < kPairs; ++m) {
-        const int e = m * 128 + quarter * 32 + lane;   // element of the latent
-        for (int cc = 0; cc < rows; cc += 16) {
+      for (int cc = 0; cc < rows; cc += 16) {
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(f + 4 * i) = reinterpret_cast<const float4*>(row_f + cc)[i];
+#pragma unroll
+        for (int m = 0; m < kPairs; ++m) {
+          const int e = m * 128 + quarter * 32 + lane;   // element of the latent
           uint32_t o[16];
           tmem_ld16(o_tmem + m * NR + cc, o);
           tmem_wait_ld();
+          if (whole) {
+            Elem* dst = static_cast<Elem*>(p.out) + (orow + cc) * RANK + e;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (cc + i >= rows) break;
-            const float y = __uint_as_float(o[i]) * row_f[cc + i];
-            if (whole) static_cast<Elem*>(p.out)[(orow + cc + i) * RANK + e] = static_cast<Elem>(y);
-            else p.part_out[(prow + cc + i) * RANK + e] = y;
+            for (int i = 0; i < 16; ++i)
+              if (cc + i < rows) dst[i * RANK] = static_cast<Elem>(__uint_as_float(o[i]) * f[i]);
+          } else {
+            float* dst = p.part_out + (prow + cc) * RANK + e;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (cc + i < rows) dst[i * RANK] = __uint_as_float(o[i]) * f[i];
           }
         }
       }

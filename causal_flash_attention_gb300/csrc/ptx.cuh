@@ -114,6 +114,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same without ever being held: for a thread that watches more than one barrier.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait until the phase with the given parity has completed. Gives up (and
 // returns false) when `abort_flag` is set by another warp or after
 // kWaitLimitCycles; in the latter case it raises the abort flag and the
@@ -402,6 +415,38 @@ __device__ __forceinline__ void mma_ts_product4(uint32_t d_tmem, uint32_t a_tmem
       "r"(a_tmem), "l"(b0), "r"(idesc), "r"(accumulate),
       "n"(desc_step<kBK, kBC>(1)), "n"(desc_step<kBK, kBC>(2)), "n"(desc_step<kBK, kBC>(3))
       : "memory");
+}
+
+// ---- whole-warp issue --------------------------------------------------------
+// A warp that issues products as a whole: waits have one outcome for the warp (warp_wait), so
+// that control flow and descriptors are the same in every lane, and one elected lane (always
+// the same one: a commit covers its thread's own MMAs) executes the MMAs inside a branch
+// on elect_one(). The compiler then keeps the descriptors in uniform registers, where
+// tcgen05.mma takes them from; a loop inside `if (lane == 0)` moves them there for every MMA,
+// 45 cycles of issue each, twice that beside a polling warp on the same scheduler.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// mbar_wait by a whole warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+}
+// mma_ss_product and mma_ts_product for that lane, of any number of K-steps.
+template <int STEPS, bool kAK, int kAC, bool kBK, int kBC>
+__device__ __forceinline__ void mma_ss_steps(uint32_t d_tmem, uint64_t a0, uint64_t b0, uint32_t idesc,
+                                             uint32_t accumulate) {
+#pragma unroll
+  for (int ks = 0; ks < STEPS; ++ks)
+    mma_ss(d_tmem, a0 + desc_step<kAK, kAC>(ks), b0 + desc_step<kBK, kBC>(ks), idesc, ks > 0 ? 1u : accumulate);
+}
+template <int STEPS, bool kBK, int kBC>
+__device__ __forceinline__ void mma_ts_steps(uint32_t d_tmem, uint32_t a_tmem, uint64_t b0, uint32_t idesc,
+                                             uint32_t accumulate) {
+#pragma unroll
+  for (int ks = 0; ks < STEPS; ++ks)
+    mma_ts(d_tmem, a_tmem + 8 * ks, b0 + desc_step<kBK, kBC>(ks), idesc, ks > 0 ? 1u : accumulate);
 }
 
 // ---- CTA pairs (cta_group::2) ----------------------------------------------
