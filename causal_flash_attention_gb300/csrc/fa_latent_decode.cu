@@ -22,9 +22,9 @@
 // tile goes through a ring of 16 KB pairs of 64-column chunks, each freed as soon as its
 // own part of O^T is issued.
 //
-// Warp roles (192 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 softmax (a
-// thread a row: lanes 0-15 of a warp hold rows 16 w .. 16 w + 15, the M = 64 layout) and
-// O^T (all lanes).
+// Warp roles (320 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 softmax (lanes
+// 0-15 of the two warps of a tensor-memory quarter w hold rows 16 w .. 16 w + 15, the M = 64
+// layout, each warp 32 of the tile's keys) and O^T (all lanes, each warp half its parts).
 #include <algorithm>
 #include <type_traits>
 
@@ -37,6 +37,7 @@ namespace fa {
 namespace {
 
 constexpr int kTile = LatentPagedParams::kTileKeys;
+constexpr int kThreadsD = 320, kSoftThreads = 256;
 constexpr float kLn2D = 0.6931471805599453f;
 constexpr float kRescaleD = 8.0f;   // the reference maximum moves when exceeded by 2^8
 
@@ -61,8 +62,8 @@ struct LatDecCfg {
   static constexpr int kNumBars = 2 * NP + 2 * NX + 6;
   static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // tmem, abort
   static constexpr int kOffScan = kOffMisc + 16;        // find_share
-  static constexpr int kOffRow = kOffScan + 32;         // [64] factor, [64] log2-sum of a row
-  static constexpr int kSmemBytes = kOffRow + 512;
+  static constexpr int kOffRow = kOffScan + 48;         // [64] factor, [64] log2-sum, [2][64] halves of a row
+  static constexpr int kSmemBytes = kOffRow + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 };
 
@@ -100,7 +101,7 @@ __device__ __forceinline__ uint64_t tree_bits(uint64_t w, int first, int kv0) {
 }
 
 template <int RANK, int NR, bool kBf16>
-__global__ void __launch_bounds__(kRaggedThreads, 1)
+__global__ void __launch_bounds__(kThreadsD, 1)
     latent_paged_kernel(const __grid_constant__ LatentPagedParams p) {
   using Cfg = LatDecCfg<RANK, NR>;
   using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
   float* row_f = reinterpret_cast<float*>(smem + Cfg::kOffRow);
   float* row_lse = row_f + 64;
+  float* halves = row_f + 128;   // [2][64]
 
   const Bars full{sbase + Cfg::kOffBar}, empty{full(NP)}, x_full{empty(NP)}, x_empty{x_full(NX)};
   const uint32_t q_ready = x_empty(NX);
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
     mbar_init(q_ready, 1);   // once a segment
     mbar_init(s_full(0), 1);
     mbar_init(s_full(1), 1);
-    mbar_init(p_full, 4);
+    mbar_init(p_full, 8);   // one arrival per softmax warp
     mbar_init(pv_done, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  const Share share = find_share(p, share_id, reinterpret_cast<int*>(smem + Cfg::kOffScan));
+  const Share share = find_share<kThreadsD>(p, share_id, reinterpret_cast<int*>(smem + Cfg::kOffScan));
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // the merge kernel may be scheduled now; it waits for this grid's completion
@@ -222,8 +224,8 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
     }
   } else if (warp == 1) {
     // ===================== MMA issuer (the whole warp, one lane of it the MMAs) =====================
-    // Two streams of work, whichever is ready first: tile gs's S, once
-    // it has landed, and tile go's O^T once its P is there. (In a fixed order, S of the next tile
+    // Two streams of work, whichever is ready first: tile gs's S, a pair of chunks at a time as
+    // they land, and tile go's O^T once its P is there. (In a fixed order, S of the next tile
     // first, a late load held up O^T, which frees the ring for the load after it.)
     constexpr uint32_t idesc_s = make_idesc(64, kTile, kBf16, false, false);
     constexpr uint32_t idesc_o = make_idesc(128, NR, kBf16, true, false);
@@ -232,8 +234,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
     Ring<NX> xt;
     int n_seg = 0;      // segments whose queries have landed
     int gs = 0, go = 0; // the next tile of either stream
-    bool begins = false;   // tile gs is its segment's first, and its queries have landed
-    bool first_of[2] = {false, false};   // the same of the tiles whose S is formed, by g % 2
+    bool first_of[2] = {false, false};   // of the tiles whose S is formed, by g % 2: a segment's first
     const uint64_t qa = make_sdesc(sbase, 16, 1024);
     const uint64_t pb = make_sdesc(sbase + Cfg::kOffP, 16, 1024);
     auto ready = [](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)); };
@@ -251,76 +252,77 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
     // path's own commit, so the wait runs out
     if (have) ok = warp_wait(drain, 0, abort_flag, p.status);
 #endif
-    long long idle_since = clock64();
-    uint32_t idle = 0;
-    while (ok && (have || go < gs)) {
-      bool worked = false;
-      // S_gs goes over S_(gs-2), which has been read when P_(gs-2) is there
-      if (have && gs <= go + 1) {
-        if (first_s && ready(q_ready, n_seg & 1)) {
-          ++n_seg;
-          first_s = false;
-          begins = true;
-        }
-        // the tile's last part has landed, and so, soon or already, have the others
-        if (!first_s && ready(x_full(xt.slot), xt.parity)) {
-          first_of[gs & 1] = begins;
-          begins = false;
-          const uint32_t d = tmem + (gs & 1) * 64;
+    auto issue_o = [&]() {   // O^T (+)= C_go^T P
+      tc_fence_after();
+      const uint32_t more = first_of[go & 1] ? 0u : 1u, o_t = tmem + 128;
 #pragma unroll
-          for (int m = 0; m < kPairs; ++m) {
-            if (!(ok = warp_wait(full(at_s.slot), at_s.parity, abort_flag, p.status))) break;
-            tc_fence_after();
-            const uint64_t cb = make_sdesc(sbase + Cfg::kOffC + at_s.slot * 2 * CB, 16, 1024);
-            if (elect_one())
-              mma_ss_steps<8, true, Cfg::kQB, true, CB>(d, qa + 2 * m * (Cfg::kQB >> 4), cb, idesc_s, m > 0 ? 1u : 0u);
-            at_s.next();
-          }
-          if (!ok) break;
-          const uint64_t xb = make_sdesc(sbase + Cfg::kOffX + xt.slot * CB, 16, 1024);
-          if (elect_one()) {
-            mma_ss_steps<4, true, Cfg::kQB, true, CB>(d, qa + 2 * kPairs * (Cfg::kQB >> 4), xb, idesc_s, 1u);
-            tc_commit(s_full(gs & 1));
-            tc_commit(x_empty(xt.slot));
-          }
-          xt.next();
-          ++gs;
-          have = next();
-          worked = true;
+      for (int m = 0; m < kPairs; ++m) {   // a part a pair
+        const uint64_t ca = make_sdesc(sbase + Cfg::kOffC + at_o.slot * 2 * CB, CB, 1024);
+        if (elect_one()) {
+          mma_ss_steps<kTile / 16, false, 0, true, Cfg::kP>(o_t + m * NR, ca, pb, idesc_o, more);
+          tc_commit(empty(at_o.slot));
+          if (m == kPairs - 1) tc_commit(pv_done);
         }
+        at_o.next();
       }
-      if (go < gs && ready(p_full, go & 1)) {
-        tc_fence_after();
-        const uint32_t more = first_of[go & 1] ? 0u : 1u, o_t = tmem + 128;
-#pragma unroll
-        for (int m = 0; m < kPairs; ++m) {   // O^T part m (+)= C_m^T P
-          const uint64_t ca = make_sdesc(sbase + Cfg::kOffC + at_o.slot * 2 * CB, CB, 1024);
-          if (elect_one()) {
-            mma_ss_steps<kTile / 16, false, 0, true, Cfg::kP>(o_t + m * NR, ca, pb, idesc_o, more);
-            tc_commit(empty(at_o.slot));
-            if (m == kPairs - 1) tc_commit(pv_done);
-          }
-          at_o.next();
+      ++go;
+    };
+    // Wait for a barrier of the S stream, issuing O^T meanwhile when its P comes first; without a
+    // barrier, for the next P. Bounded as mbar_wait.
+    auto until = [&](uint32_t bar, uint32_t parity) -> bool {
+      long long since = 0;
+      for (uint32_t idle = 0;;) {
+        if (bar && ready(bar, parity)) return true;
+        if (go < gs && ready(p_full, go & 1)) {
+          issue_o();
+          if (!bar) return true;
+          idle = 0;
+          continue;
         }
-        ++go;
-        worked = true;
-      }
-      if (worked) {
-        idle = 0;
-      } else if ((++idle & 15u) == 0) {   // as mbar_wait
-        if (idle == 16) idle_since = clock64();
+        if ((++idle & 15u) != 0) continue;
+        if (idle == 16) since = clock64();
         bool stop = false;
         if (lane == 0) {
           stop = *abort_flag;
-          if (!stop && clock64() - idle_since > kWaitLimitCycles) {
+          if (!stop && clock64() - since > kWaitLimitCycles) {
             *abort_flag = 1;
             atomicOr(p.status, kStatusWaitTimeout);
             stop = true;
           }
         }
-        ok = !__any_sync(0xffffffffu, stop);
+        if (__any_sync(0xffffffffu, stop)) return false;
       }
+    };
+    while (ok && have) {
+      // S_gs goes over S_(gs-2), which has been read when P_(gs-2) is there
+      while (ok && gs > go + 1) ok = until(0, 0);
+      if (!ok) break;
+      const bool begins = first_s;
+      if (begins && !(ok = until(q_ready, n_seg++ & 1))) break;
+      const uint32_t d = tmem + (gs & 1) * 64;
+#pragma unroll
+      for (int m = 0; m < kPairs; ++m) {
+        if (!(ok = until(full(at_s.slot), at_s.parity))) break;
+        tc_fence_after();
+        const uint64_t cb = make_sdesc(sbase + Cfg::kOffC + at_s.slot * 2 * CB, 16, 1024);
+        if (elect_one())
+          mma_ss_steps<8, true, Cfg::kQB, true, CB>(d, qa + 2 * m * (Cfg::kQB >> 4), cb, idesc_s, m > 0 ? 1u : 0u);
+        at_s.next();
+      }
+      if (!ok || !(ok = until(x_full(xt.slot), xt.parity))) break;
+      tc_fence_after();
+      const uint64_t xb = make_sdesc(sbase + Cfg::kOffX + xt.slot * CB, 16, 1024);
+      if (elect_one()) {
+        mma_ss_steps<4, true, Cfg::kQB, true, CB>(d, qa + 2 * kPairs * (Cfg::kQB >> 4), xb, idesc_s, 1u);
+        tc_commit(s_full(gs & 1));
+        tc_commit(x_empty(xt.slot));
+      }
+      xt.next();
+      first_of[gs & 1] = begins;
+      ++gs;
+      have = next();
     }
+    while (ok && go < gs) ok = until(0, 0);
     if (!ok) {
       // every MMA issued so far must finish before the TMEM is released
       if (elect_one()) tc_commit(drain);
@@ -330,6 +332,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
   } else {
     // ===== queries, softmax per tile, O^T =====
     const int quarter = warp & 3;               // TMEM lane quarter of this warp
+    const int half = (warp - 2) >> 2;           // its half of a tile's keys, and of the parts of O^T
     const int tid = static_cast<int>(threadIdx.x) - 64;
     const int r = quarter * 16 + lane;          // this thread's row of the group, if any
     const bool busy = quarter * 16 < rows;      // the warp holds rows
@@ -338,7 +341,9 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t o_tmem = tmem + lane_off + 128;
     const float c = p.scale_log2;
+    constexpr int kHalf = kTile / 2, kOwn = kPairs / 2;   // keys of a warp, its parts of O^T
     uint8_t* const p_row = smem + Cfg::kOffP + (lane < 16 && r < NR ? r : 0) * 128;
+    auto any = [](bool flag) { return row_warps_any<kSoftThreads>(flag); };
 
     // A segment's queries (heads past the last come as zeros; rows past the group's are whatever
     // the memory held, and so are their scores, which nobody reads).
@@ -353,7 +358,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
     if (more) load_q(seg.b);
     int n_q = 1;        // segments whose queries have been asked for
     // A wait that fails in one warp must not leave the others in a barrier: the warp goes on
-    // without touching anything until the next vote, where all four learn of it.
+    // without touching anything until the next vote, where all learn of it.
     bool ok = true, dead = false;
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, abort_flag, p.status));
@@ -392,7 +397,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
           const int na = hidden.a1 - hidden.a0, nh = na + hidden.b1 - hidden.b0;
           Ring<NP> pair = at;
           for (int m = 0; m < kPairs; ++m, pair.next())
-            for (int i = tid; i < nh * 16; i += 128) {
+            for (int i = tid; i < nh * 16; i += kSoftThreads) {
               const int k = i >> 4;
               const int row = k < na ? hidden.a0 + k : hidden.b0 + k - na;
               *reinterpret_cast<uint4*>(smem + Cfg::kOffC + pair.slot * 2 * CB + ((i >> 3) & 1) * CB + row * 128 + (i & 7) * 16) =
@@ -401,47 +406,50 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
           fence_proxy_async_smem();
         }
         for (int m = 0; m < kPairs; ++m) at.next();
-        float x[kTile];
-        float alpha = 1.f;
-        bool moved = false;
+        float x[kHalf], top = -INFINITY;   // scores, and the greatest in the log2 domain
         if (busy && ok) {
-          uint32_t raw[kTile];
-          tmem_ld32(tmem + lane_off + (g & 1) * 64, *reinterpret_cast<uint32_t(*)[32]>(raw));
-          tmem_ld32(tmem + lane_off + (g & 1) * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(raw + 32));
+          const int k0 = kv0 + half * kHalf;
+          uint32_t raw[kHalf];
+          tmem_ld32(tmem + lane_off + (g & 1) * 64 + half * kHalf, raw);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < kTile; ++i) x[i] = __uint_as_float(raw[i]);
-          if (kv0 < row_lo || kv0 + kTile > row_hi || (p.tree && kv0 + kTile > keys.len - p.Sq)) {
-            uint32_t see[2] = {span_bits(row_lo, row_hi, kv0), span_bits(row_lo, row_hi, kv0 + 32)};
-            if (p.tree) {
-              const uint64_t t = tree_bits(tree, keys.len - p.Sq, kv0);
-              see[0] &= static_cast<uint32_t>(t);
-              see[1] &= static_cast<uint32_t>(t >> 32);
-            }
+          for (int i = 0; i < kHalf; ++i) x[i] = __uint_as_float(raw[i]);
+          if (k0 < row_lo || k0 + kHalf > row_hi || (p.tree && k0 + kHalf > keys.len - p.Sq)) {
+            uint32_t see = span_bits(row_lo, row_hi, k0);
+            if (p.tree) see &= static_cast<uint32_t>(tree_bits(tree, keys.len - p.Sq, k0));
 #pragma unroll
-            for (int i = 0; i < kTile; ++i)
-              if (!((see[i / 32] >> (i & 31)) & 1u)) x[i] = -INFINITY;
+            for (int i = 0; i < kHalf; ++i)
+              if (!((see >> i) & 1u)) x[i] = -INFINITY;
           }
           float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int i = 4; i < kTile; i += 4)
+          for (int i = 4; i + 8 <= kHalf; i += 8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[i + e]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-          const float m_new = top > m_ref + kRescaleD ? top : m_ref;
-          moved = real && m_new != m_ref;
-          alpha = m_new == -INFINITY ? 1.f : ex2(m_ref - m_new);   // 0 from m = -inf
-          m_ref = m_new;
+            for (int e = 0; e < 4; ++e) mx[e] = fmax3(mx[e], x[i + e], x[i + 4 + e]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[kHalf - 4 + e]);
+          top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
         }
-        // P_(g-1) has been read, and its product is in O^T
-        if (g > 0) wait(pv_done, g - 1);
-        // O^T <- alpha O^T where a row's reference moved (the segment's first product overwrites O^T)
-        if (j > 0) {
-          if (row_warps_any(moved || !ok)) {
-            if (real) row_f[r] = moved ? alpha : 1.f;
-            if ((dead = row_warps_any(!ok))) break;
+        // A row's reference moves when a score of either half exceeds it by 2^8: one vote tells
+        // whether any does; then the halves exchange their maxima and O^T <- alpha O^T. (A
+        // segment's first tile sets it; its first product overwrites O^T.)
+        if (j == 0 || any((real && top > m_ref + kRescaleD) || !ok)) {
+          if (real) halves[half * 64 + r] = top;
+          if (j > 0) wait(pv_done, g - 1);   // its product is in O^T
+          if ((dead = any(!ok))) break;
+          float alpha = 1.f;
+          if (real) {
+            const float both = fmaxf(halves[r], halves[64 + r]);
+            const float m_new = both > m_ref + kRescaleD ? both : m_ref;
+            alpha = m_new == -INFINITY ? 1.f : ex2(m_ref - m_new);   // 0 from m = -inf
+            m_ref = m_new;
+            l *= alpha;
+          }
+          if (j > 0) {
+            if (real && half == 0) row_f[r] = alpha;
+            any(false);
             tc_fence_after();
-            for (int m = 0; m < kPairs; ++m)
+            for (int m = half * kOwn; m < (half + 1) * kOwn; ++m)
 #pragma unroll
               for (int cc = 0; cc < NR; cc += 16) {
                 if (cc >= rows) break;
@@ -454,28 +462,35 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
                 tmem_st16(o_tmem + m * NR + cc, o);
               }
             tmem_wait_st();
-            row_warps_any(false);   // the factors have been read
+            any(false);   // the factors have been read
           }
         }
-        if (!ok) continue;   // to the next vote
-        if (busy) {
+        uint32_t pk[kHalf / 2];
+        if (busy && ok) {
           const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          uint32_t pk[kTile / 2];
+          const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_use, -m_use);
+          uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-          for (int i = 0; i < kTile; i += 2) {
-            const float p0 = ex2(fmaf(x[i], c, -m_use)), p1 = ex2(fmaf(x[i + 1], c, -m_use));
-            sum[i & 3] += p0;
-            sum[(i + 1) & 3] += p1;
+          for (int i = 0; i < kHalf; i += 2) {
+            float p0, p1;
+            f2_unpack(f2_fma(f2_pack(x[i], x[i + 1]), c2, nm2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            if (i & 2) sum1 = f2_add(sum1, f2_pack(p0, p1));
+            else sum0 = f2_add(sum0, f2_pack(p0, p1));
             pk[i / 2] = pack2<kBf16>(p0, p1);
           }
-          l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
-          if (lane < 16 && r < NR) {
+          float a0, a1;
+          f2_unpack(f2_add(sum0, sum1), a0, a1);
+          l += a0 + a1;
+        }
+        if (g > 0) wait(pv_done, g - 1);   // P_(g-1) has been read
+        if (!ok) continue;   // to the next vote
+        if (busy && lane < 16 && r < NR) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              *reinterpret_cast<uint4*>(p_row + ((u ^ (r & 7)) << 4)) =
-                  real ? make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]) : make_uint4(0u, 0u, 0u, 0u);
-          }
+          for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(p_row + (((half * 4 + u) ^ (r & 7)) << 4)) =
+                real ? make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]) : make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -483,13 +498,15 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
         if (lane == 0) mbar_arrive(p_full);
       }
       if (dead) break;
-      if (real) {
-        const PartSum sum(l, m_ref);
+      if (real) halves[half * 64 + r] = l;
+      wait(pv_done, g - 1);
+      if ((dead = any(!ok))) break;
+      if (real && half == 0) {
+        const PartSum sum(l + halves[64 + r], m_ref);
         row_f[r] = sum.inv;
         row_lse[r] = sum.lse2;
       }
-      wait(pv_done, g - 1);
-      if ((dead = row_warps_any(!ok))) break;
+      any(false);
       tc_fence_after();
       const size_t orow = static_cast<size_t>(b) * p.R + row0;                                  // + row
       const size_t prow = (static_cast<size_t>(share_id) * 2 + (head ? 0 : 1)) * p.R + row0;    // + row
@@ -502,7 +519,8 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(f + 4 * i) = reinterpret_cast<const float4*>(row_f + cc)[i];
 #pragma unroll
-        for (int m = 0; m < kPairs; ++m) {
+        for (int mm = 0; mm < kOwn; ++mm) {
+          const int m = half * kOwn + mm;
           const int e = m * 128 + quarter * 32 + lane;   // element of the latent
           uint32_t o[16];
           tmem_ld16(o_tmem + m * NR + cc, o);
@@ -521,7 +539,7 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
         }
       }
       tc_fence_before();
-      row_warps_any(false);   // the factors have been read
+      any(false);   // the factors have been read
       head = false;
     }
     // the last queries asked for land before the CTA releases its memory
@@ -537,91 +555,109 @@ __global__ void __launch_bounds__(kRaggedThreads, 1)
 }
 
 // ------------------------------------------------------------------ merge --
-// Joins the parts of sequences whose tiles lie in more than one share, in share order:
-// block (c, y) takes rows y, y + gridDim.y, ... of the sequence whose second part is in
-// share c. kLanes sets of rank / 4 threads take every kLanes-th part, four elements a
-// thread; their sums are added in a fixed order. Also writes out = 0, LSE = -inf for
-// sequences without keys.
-constexpr int kMergeLanes = 4, kMergeFlight = 8;
+// Joins the parts of sequences whose tiles lie in more than one share, in share order: a
+// warp takes 128 elements of a row. Up to as many sequences as shares, block (b, y) takes
+// sequence b, found by a scan over the lengths as the main kernel's; more sequences than
+// shares, block (c, y) the one whose second part is in share c. Also writes out = 0, LSE =
+// -inf for sequences without keys. Bound by latency (10 KB a row from L2).
+constexpr int kMergeWarps = 4, kMergeFlight = 12;
 
 template <typename T, int RANK>
-__global__ void __launch_bounds__(kMergeLanes * RANK / 4) latent_merge_kernel(const __grid_constant__ LatentPagedParams p) {
+__global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __grid_constant__ LatentPagedParams p) {
   // programmatic dependent of the main kernel; a main kernel that follows on the stream may
   // set itself up beside this grid
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kThreads = kMergeLanes * RANK / 4;
-  __shared__ float4 sums[kMergeLanes][RANK / 4];
-  __shared__ float weights[kMergeLanes];
-  const int c = static_cast<int>(blockIdx.x);
-  const int set = threadIdx.x / (RANK / 4), e = threadIdx.x % (RANK / 4);
-  for (int b = c; b < p.B; b += static_cast<int>(gridDim.x)) {
-    if (seq_keys(p, b).n > 0) continue;
-    for (int r = blockIdx.y; r < p.R; r += gridDim.y) {
-      const size_t row = static_cast<size_t>(b) * p.R + r;
-      for (int i = threadIdx.x; i < RANK; i += kThreads) static_cast<T*>(p.out)[row * RANK + i] = static_cast<T>(0.f);
-      if (threadIdx.x == 0) p.lse[row] = -INFINITY;
+  constexpr int kParts = RANK / 128, kRows = kMergeWarps / kParts;   // warps a row, rows a block
+  constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+  __shared__ int2 sums[kMergeWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = static_cast<int>(blockIdx.y) * kRows + warp / kParts;
+  const int e = warp % kParts * 128 + lane * 4;   // this lane's four elements
+  int b, u0, units, total;   // a sequence, its units [u0, u0 + units), all units
+  auto nothing = [&](int seq) {
+    if (r >= p.R) return;
+    const size_t row = static_cast<size_t>(seq) * p.R + r;
+    *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * RANK + e) = make_uint2(0u, 0u);
+    if (e == 0) p.lse[row] = -INFINITY;
+  };
+  if (p.B <= p.n_ctas) {
+    b = static_cast<int>(blockIdx.x);
+    units = units_of(seq_keys(p, b).n);
+    int before = 0, all = 0;
+    for (int i = threadIdx.x; i < p.B; i += 32 * kMergeWarps) {
+      const int n = units_of(seq_keys(p, i).n);
+      all += n;
+      if (i < b) before += n;
     }
+    before = __reduce_add_sync(0xffffffffu, before);
+    all = __reduce_add_sync(0xffffffffu, all);
+    if (lane == 0) sums[warp] = make_int2(before, all);
+    __syncthreads();
+    u0 = total = 0;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+      u0 += sums[w].x;
+      total += sums[w].y;
+    }
+    if (units == 0) {
+      nothing(b);
+      return;
+    }
+  } else {
+    for (int i = blockIdx.x; i < p.B; i += gridDim.x)
+      if (seq_keys(p, i).n == 0) nothing(i);
+    total = p.starts[0].w;
+    const int4 start = p.starts[blockIdx.x];   // without meaning past the shares
+    b = start.x;
+    u0 = start.y;
+    units = start.z;
   }
-  const int total = p.starts[0].w;
-  const int4 start = p.starts[c];   // without meaning past the shares
   const ShareOut out(p.n_ctas, total);
-  if (c == 0 || c >= out.shares) return;
-  const int b = start.x, u0 = start.y;   // the sequence's units: [u0, u0 + start.z)
-  const int c0 = out.of_unit(u0 + kSegmentUnits), c1 = out.of_unit(u0 + start.z - 1);
-  if (c != c0 + 1 || c0 == c1) return;
+  if (r >= p.R || (p.B > p.n_ctas && static_cast<int>(blockIdx.x) >= out.shares)) return;
+  const int c0 = out.of_unit(u0 + kSegmentUnits), c1 = out.of_unit(u0 + units - 1);
+  if (c0 == c1 || (p.B > p.n_ctas && static_cast<int>(blockIdx.x) != c0 + 1)) return;
   // the parts are the first segments of their shares, but for that of c0 when its share
   // begins before this sequence's units (and so with another's tiles)
   const bool tail0 = out.begin(c0) < u0;
-  for (int r = blockIdx.y; r < p.R; r += gridDim.y) {
-    auto part = [&](int i) { return (static_cast<size_t>(i) * 2 + ((i == c0 && tail0) ? 1 : 0)) * p.R + r; };
-    float M = -INFINITY;
-    for (int i = c0 + (threadIdx.x & 31); i <= c1; i += 32) M = fmaxf(M, p.part_lse2[part(i)]);
-    M = warp_max(M);   // without NaN parts: their weight is NaN whatever it is
-    if (M == -INFINITY) M = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f;
-    for (int i = c0 + set; i <= c1; i += kMergeLanes * kMergeFlight) {
-      float4 v[kMergeFlight];
-      float lv[kMergeFlight];
+  auto part = [&](int i) { return (static_cast<size_t>(i) * 2 + ((i == c0 && tail0) ? 1 : 0)) * p.R + r; };
+  // a batch's loads go out together, the first batch's with those of the maximum
+  float4 v[kMergeFlight];
+  float lv[kMergeFlight];
+  auto load = [&](int i) {
 #pragma unroll
-      for (int k = 0; k < kMergeFlight; ++k)
-        if (i + k * kMergeLanes <= c1) {
-          const size_t at = part(i + k * kMergeLanes);
-          v[k] = reinterpret_cast<const float4*>(p.part_out + at * RANK)[e];
-          lv[k] = p.part_lse2[at];
-        }
-#pragma unroll
-      for (int k = 0; k < kMergeFlight; ++k)
-        if (i + k * kMergeLanes <= c1) {
-          const float w = ex2(lv[k] - M);
-          L += w;
-          acc.x = fmaf(w, v[k].x, acc.x);
-          acc.y = fmaf(w, v[k].y, acc.y);
-          acc.z = fmaf(w, v[k].z, acc.z);
-          acc.w = fmaf(w, v[k].w, acc.w);
-        }
-    }
-    sums[set][e] = acc;
-    if (e == 0) weights[set] = L;
-    __syncthreads();
-    if (set == 0) {
-      L = weights[0];
-#pragma unroll
-      for (int k = 1; k < kMergeLanes; ++k) {
-        const float4 v = sums[k][e];
-        L += weights[k];
-        acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    for (int k = 0; k < kMergeFlight; ++k)
+      if (i + k <= c1) {
+        const size_t at = part(i + k);
+        v[k] = *reinterpret_cast<const float4*>(p.part_out + at * RANK + e);
+        lv[k] = p.part_lse2[at];
       }
-      const PartSum sum(L, M);
-      const size_t row = static_cast<size_t>(b) * p.R + r;
-      constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
-      reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * RANK)[e] =
-          make_uint2(pack2<kBf>(acc.x * sum.inv, acc.y * sum.inv), pack2<kBf>(acc.z * sum.inv, acc.w * sum.inv));
-      if (e == 0) p.lse[row] = sum.lse2 * kLn2D;
-    }
-    __syncthreads();
+  };
+  load(c0);
+  float M = -INFINITY;
+  for (int i = c0 + lane; i <= c1; i += 32) M = fmaxf(M, p.part_lse2[part(i)]);
+  M = warp_max(M);   // without NaN parts: their weight is NaN whatever it is
+  if (M == -INFINITY) M = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float L = 0.f;
+  for (int i = c0; i <= c1; i += kMergeFlight) {
+    if (i > c0) load(i);
+#pragma unroll
+    for (int k = 0; k < kMergeFlight; ++k)
+      if (i + k <= c1) {
+        const float w = ex2(lv[k] - M);
+        L += w;
+        acc.x = fmaf(w, v[k].x, acc.x);
+        acc.y = fmaf(w, v[k].y, acc.y);
+        acc.z = fmaf(w, v[k].z, acc.z);
+        acc.w = fmaf(w, v[k].w, acc.w);
+      }
   }
+  const PartSum sum(L, M);
+  const size_t row = static_cast<size_t>(b) * p.R + r;
+  *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * RANK + e) =
+      make_uint2(pack2<kBf>(acc.x * sum.inv, acc.y * sum.inv), pack2<kBf>(acc.z * sum.inv, acc.w * sum.inv));
+  if (e == 0) p.lse[row] = sum.lse2 * kLn2D;
 }
 
 template <int RANK, int NR, bool kBf16>
@@ -631,7 +667,7 @@ cudaError_t launch_main(const LatentPagedParams& p, cudaStream_t stream) {
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kernel, dim3(static_cast<unsigned>(p.n_ctas * p.groups)), dim3(kRaggedThreads),
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(p.n_ctas * p.groups)), dim3(kThreadsD),
                           Cfg::kSmemBytes, stream, p);
 }
 
@@ -643,9 +679,10 @@ cudaError_t launch_impl(const LatentPagedParams& p, cudaStream_t stream) {
                         : rows <= 32 ? launch_main<RANK, 32, kBf16>(p, stream)
                                      : launch_main<RANK, 64, kBf16>(p, stream);
   if (e != cudaSuccess) return e;
-  const int y = std::min(p.R, std::max(16, 2048 / p.n_ctas));
-  return launch_dependent(latent_merge_kernel<Elem, RANK>, dim3(static_cast<unsigned>(p.n_ctas), y),
-                          dim3(kMergeLanes * RANK / 4), 0, stream, p);
+  constexpr int kRows = kMergeWarps / (RANK / 128);
+  return launch_dependent(latent_merge_kernel<Elem, RANK>,
+                          dim3(static_cast<unsigned>(std::min(p.B, p.n_ctas)), static_cast<unsigned>((p.R + kRows - 1) / kRows)),
+                          dim3(32 * kMergeWarps), 0, stream, p);
 }
 
 }  // namespace

@@ -66,7 +66,7 @@ struct ShareOut {
   }
 };
 
-// A CTA's share, found by all its threads: a scan over the sequences' units. Where it
+// A CTA's share, found by all its kThreads threads (scan: kThreads / 32 + 2 words): a scan over the sequences' units. Where it
 // begins is also written for the merge: (sequence, units per head before it, its units,
 // units of all sequences per head). Two barriers.
 struct Share {
@@ -74,15 +74,16 @@ struct Share {
   int b, pre;        // the first unit's sequence, and units per head before it
 };
 
-template <class P>
+template <int kThreads = kRaggedThreads, class P>
 __device__ __forceinline__ Share find_share(const P& p, int cta, int* scan) {
+  constexpr int kWarps = kThreads / 32;
   // launched as a programmatic dependent of whatever runs before on the stream
   // (the merge of the call before lets it start early): the barriers, tensor memory
   // and descriptors above are set up meanwhile, memory is touched from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
   // thread t holds sequences [t * per, (t + 1) * per)
-  const int per = (p.B + kRaggedThreads - 1) / kRaggedThreads;
+  const int per = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per);
   const int b_hi = min(p.B, b_lo + per);
   int mine = 0;
@@ -96,7 +97,7 @@ __device__ __forceinline__ Share find_share(const P& p, int cta, int* scan) {
   if (lane == 31) scan[warp] = incl;
   __syncthreads();
   int pre = incl - mine, total = 0;
-  for (int w = 0; w < kRaggedThreads / 32; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < warp) pre += scan[w];
     total += scan[w];
   }
@@ -107,16 +108,16 @@ __device__ __forceinline__ Share find_share(const P& p, int cta, int* scan) {
   for (int b = b_lo; b < b_hi; ++b) {
     const int n = units_of(seq_keys(p, b).n);
     if (s.begin < s.end && pre * p.Hkv <= s.begin && s.begin < (pre + n) * p.Hkv) {
-      scan[6] = b;
-      scan[7] = pre;
+      scan[kWarps] = b;
+      scan[kWarps + 1] = pre;
       p.starts[cta] = make_int4(b, pre, n, total);
     }
     pre += n;
   }
   if (total == 0 && cta == 0 && threadIdx.x == 0) p.starts[0] = make_int4(0, 0, 0, 0);
   __syncthreads();
-  s.b = s.begin < s.end ? scan[6] : 0;
-  s.pre = s.begin < s.end ? scan[7] : 0;
+  s.b = s.begin < s.end ? scan[kWarps] : 0;
+  s.pre = s.begin < s.end ? scan[kWarps + 1] : 0;
   return s;
 }
 
@@ -219,13 +220,14 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
-// Barrier of the four row warps that tells whether any thread's flag is set.
+// Barrier of the row warps (kThreads threads) that tells whether any thread's flag is set.
+template <int kThreads = 128>
 __device__ __forceinline__ bool row_warps_any(bool flag) {
   uint32_t any;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(any) : "r"(flag ? 1u : 0u) : "memory");
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any) : "r"(flag ? 1u : 0u), "n"(kThreads) : "memory");
   return any != 0;
 }
 
