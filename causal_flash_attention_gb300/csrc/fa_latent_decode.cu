@@ -135,11 +135,11 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NP; ++s) {
-      mbar_init(full(s), 1);
+      mbar_init(full(s), kTile / p.box_rows);   // an arrival a box
       mbar_init(empty(s), 1);
     }
     for (int s = 0; s < NX; ++s) {
-      mbar_init(x_full(s), 1);
+      mbar_init(x_full(s), kTile / p.box_rows);
       mbar_init(x_empty(s), 1);
     }
     mbar_init(q_ready, 1);   // once a segment
@@ -169,59 +169,65 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 
   if (warp == 0) {
     // ===================== TMA producer =====================
-    // Lane i reads the table entry of box i of a tile and issues its copies. A box past the
-    // sequence or before every row's window, or an entry outside [0, num_blocks), is loaded
-    // from an out-of-range row, which the copy fills with zeros.
-    const int n_boxes = kTile / p.box_rows;
-    Ring<NP> at;
-    Ring<NX> xt;
-    int n_p = 0, n_x = 0;   // pairs and rotated parts issued
-    bool stop = false;
-    while (!stop && seg.next(p)) {
-      const int* table = p.block_table + static_cast<size_t>(seg.b) * p.max_blocks;
-      for (int j = 0; j < seg.n && !stop; ++j) {
+    // Lane i takes box i of every tile, by itself: it reads the box's table entry (a tile ahead:
+    // the read would stand before every tile's copies), waits for the ring's slots and issues
+    // the copies (a barrier counts the boxes' arrivals). A box past the sequence or before
+    // every row's window, or an entry outside [0, num_blocks), is loaded from an out-of-range
+    // row, which the copy fills with zeros.
+    if (lane < kTile / p.box_rows) {
+      Ring<NP> at;
+      Ring<NX> xt;
+      int n_p = 0, n_x = 0;   // pairs and rotated parts issued
+      const uint32_t box_bytes = p.box_rows * 128, box = lane * box_bytes;
+      auto free = [&](bool used, uint32_t bar, uint32_t parity) {
+        return !used || mbar_wait(bar, parity ^ 1u, abort_flag, p.status);
+      };
+      int j = 0;
+      auto page = [&]() -> int {   // of this lane's box of tile j of the segment
         const int key = (seg.tile0 + j) * kTile + lane * p.box_rows;
-        int pb = -1;
-        if (lane < n_boxes && key < seg.keys.len && key + p.box_rows > seg.keys.first)
-          pb = table[key / p.block_size];
+        if (key >= seg.keys.len || key + p.box_rows <= seg.keys.first) return -1;
+        return p.block_table[static_cast<size_t>(seg.b) * p.max_blocks + key / p.block_size];
+      };
+      bool have = seg.next(p), ok = true;
+      int pb = have ? page() : -1;
+      while (ok && have) {
         const bool in_range = pb >= 0 && pb < p.num_blocks;
-        const int y = in_range ? key % p.block_size : p.block_size;
+        const int y = in_range ? ((seg.tile0 + j) * kTile + lane * p.box_rows) % p.block_size : p.block_size;
         const int z = in_range ? pb : 0;
-        const uint32_t box = lane * p.box_rows * 128;
-        for (int m = 0; m <= kPairs && !stop; ++m) {   // the rotated part goes with the last
-          const bool is_x = m == kPairs;
-          const uint32_t f = is_x ? x_full(xt.slot) : full(at.slot);
-          int fail = 0;
-          if (lane == 0) {
-            const bool wait = is_x ? n_x >= NX : n_p >= NP;
-            if (wait && !mbar_wait(is_x ? x_empty(xt.slot) : empty(at.slot), (is_x ? xt.parity : at.parity) ^ 1u,
-                                   abort_flag, p.status))
-              fail = 1;
-            else
-              mbar_arrive_expect_tx(f, is_x ? CB : 2 * CB);
-          }
-          if ((stop = __shfl_sync(0xffffffffu, fail, 0))) break;
-          if (is_x) {
-            if (lane < n_boxes) tma_load_3d(sbase + Cfg::kOffX + xt.slot * CB + box, &p.tm, f, RANK, y, z);
-            xt.next();
-            ++n_x;
-          } else {
-            if (lane < n_boxes) {
-              const uint32_t dst = sbase + Cfg::kOffC + at.slot * 2 * CB + box;
-              tma_load_3d(dst, &p.tm, f, m * 128, y, z);
-              tma_load_3d(dst + CB, &p.tm, f, m * 128 + kChunk, y, z);
-            }
-            at.next();
-            ++n_p;
-          }
+        if (++j == seg.n) {
+          j = 0;
+          have = seg.next(p);
         }
+        if (have) pb = page();
+#pragma unroll
+        for (int m = 0; m < kPairs; ++m) {
+          if (!(ok = free(n_p >= NP, empty(at.slot), at.parity))) break;
+          const uint32_t f = full(at.slot), dst = sbase + Cfg::kOffC + at.slot * 2 * CB + box;
+          mbar_arrive_expect_tx(f, 2 * box_bytes);
+          tma_load_3d(dst, &p.tm, f, m * 128, y, z);
+          tma_load_3d(dst + CB, &p.tm, f, m * 128 + kChunk, y, z);
+          at.next();
+          ++n_p;
+        }
+        if (!ok || !(ok = free(n_x >= NX, x_empty(xt.slot), xt.parity))) break;
+        const uint32_t f = x_full(xt.slot);
+        mbar_arrive_expect_tx(f, box_bytes);
+        tma_load_3d(sbase + Cfg::kOffX + xt.slot * CB + box, &p.tm, f, RANK, y, z);
+        xt.next();
+        ++n_x;
+      }
+      // Aborted: every copy lands before the CTA releases its memory. (A lane that gave up a slot
+      // before another did arrives there without a copy, so that the phase completes.)
+      const uint32_t lanes = (1u << (kTile / p.box_rows)) - 1;
+      if (__any_sync(lanes, *abort_flag)) {
+        const int most_p = __reduce_max_sync(lanes, n_p), most_x = __reduce_max_sync(lanes, n_x);
+        for (; n_p < most_p; ++n_p) mbar_arrive(full(n_p % NP));
+        for (; n_x < most_x; ++n_x) mbar_arrive(x_full(n_x % NX));
+        for (int i = max(0, n_p - NP); i < n_p; ++i) drain_wait_d(full(i % NP), (i / NP) & 1, p.status);
+        for (int i = max(0, n_x - NX); i < n_x; ++i) drain_wait_d(x_full(i % NX), (i / NX) & 1, p.status);
       }
     }
-    if (lane == 0 && *abort_flag) {
-      // let every copy already issued land before the CTA releases its memory
-      for (int i = max(0, n_p - NP); i < n_p; ++i) drain_wait_d(full(i % NP), (i / NP) & 1, p.status);
-      for (int i = max(0, n_x - NX); i < n_x; ++i) drain_wait_d(x_full(i % NX), (i / NX) & 1, p.status);
-    }
+    __syncwarp();
   } else if (warp == 1) {
     // ===================== MMA issuer (the whole warp, one lane of it the MMAs) =====================
     // Two streams of work, whichever is ready first: tile gs's S, a pair of chunks at a time as
