@@ -100,7 +100,7 @@ struct LatentPagedParams {
   int4* starts;            // [n_ctas] where each share begins
   // a group's rows: all tokens (up to 64) of group_heads heads, or 64 tokens of one head
   int B, H, Sq, R, groups, group_heads, group_tokens;
-  int block_size, box_rows, max_blocks, num_blocks;
+  int block_size, block_shift, box_rows, max_blocks, num_blocks;   // block_size = 2^block_shift
   int capacity;            // keys a table row can hold (at most 2^31 - 128)
   int window;              // keys a row sees, its own position included; 0: all
   float scale_log2;

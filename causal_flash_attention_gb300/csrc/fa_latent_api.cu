@@ -268,6 +268,7 @@ int fa_fwd_latent_paged(const fa_view* q, const void* cache, const int* block_ta
   p.group_heads = w.group_heads;
   p.group_tokens = w.group_tokens;
   p.block_size = block_size; p.max_blocks = max_blocks; p.num_blocks = num_blocks;
+  while (1 << p.block_shift < block_size) ++p.block_shift;
   p.capacity = static_cast<int>(std::min(static_cast<long long>(max_blocks) * block_size, 0x7fffff80LL));
   // a window that no position outgrows hides nothing (and would overflow positions)
   p.window = window < p.capacity ? window : 0;

@@ -20,7 +20,8 @@
 // O stands transposed in tensor memory because rows are the short side (rank / 128 * rows
 // columns: 256 at rank 512 with 64 rows; the other way around it would take all 512). The
 // tile goes through a ring of 16 KB pairs of 64-column chunks, each freed as soon as its
-// own part of O^T is issued.
+// own part of O^T is formed; one barrier a tile tells that it has landed (a wait costs the
+// issuer 100 cycles, three products).
 //
 // Warp roles (320 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 softmax (lanes
 // 0-15 of the two warps of a tensor-memory quarter w hold rows 16 w .. 16 w + 15, the M = 64
@@ -58,8 +59,10 @@ struct LatDecCfg {
   static constexpr int kOffX = kOffP + kP;
   static constexpr int kOffC = kOffX + NX * CB;
   static constexpr int kOffBar = kOffC + NP * 2 * CB;
-  // full[NP], empty[NP], x_full[NX], x_empty[NX], q_ready, s_full[2], p_full, pv_done, drain
-  static constexpr int kNumBars = 2 * NP + 2 * NX + 6;
+  static constexpr int NT = 8;   // tiles in the ring at a time, at most (NP / kPairs and parts of two more)
+  static_assert(NP / kPairs + 2 <= NT, "a barrier a tile");
+  // full[NT], empty[NP], x_empty[NX], q_ready, s_full[2], p_full, pv_done, drain
+  static constexpr int kNumBars = NT + NP + NX + 6;
   static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // tmem, abort
   static constexpr int kOffScan = kOffMisc + 16;        // find_share
   static constexpr int kOffRow = kOffScan + 48;         // [64] factor, [64] log2-sum, [2][64] halves of a row
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     latent_paged_kernel(const __grid_constant__ LatentPagedParams p) {
   using Cfg = LatDecCfg<RANK, NR>;
   using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
-  constexpr int NP = Cfg::NP, NX = Cfg::NX, CB = Cfg::CB, kPairs = Cfg::kPairs;
+  constexpr int NP = Cfg::NP, NX = Cfg::NX, NT = Cfg::NT, CB = Cfg::CB, kPairs = Cfg::kPairs;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {   // the 128-byte swizzle needs 1024-byte aligned tiles
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
   float* row_lse = row_f + 64;
   float* halves = row_f + 128;   // [2][64]
 
-  const Bars full{sbase + Cfg::kOffBar}, empty{full(NP)}, x_full{empty(NP)}, x_empty{x_full(NX)};
+  const Bars full{sbase + Cfg::kOffBar}, empty{full(NT)}, x_empty{empty(NP)};
   const uint32_t q_ready = x_empty(NX);
   const Bars s_full{q_ready + 8};
   const uint32_t p_full = s_full(2), pv_done = p_full + 8, drain = p_full + 16;
@@ -134,14 +137,9 @@ __global__ void __launch_bounds__(kThreadsD, 1)
   const int rows = min(p.group_heads, p.H - h0) * min(p.group_tokens, p.Sq - s0);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NP; ++s) {
-      mbar_init(full(s), kTile / p.box_rows);   // an arrival a box
-      mbar_init(empty(s), 1);
-    }
-    for (int s = 0; s < NX; ++s) {
-      mbar_init(x_full(s), kTile / p.box_rows);
-      mbar_init(x_empty(s), 1);
-    }
+    for (int s = 0; s < NT; ++s) mbar_init(full(s), kTile / p.box_rows);   // an arrival a box
+    for (int s = 0; s < NP; ++s) mbar_init(empty(s), 1);
+    for (int s = 0; s < NX; ++s) mbar_init(x_empty(s), 1);
     mbar_init(q_ready, 1);   // once a segment
     mbar_init(s_full(0), 1);
     mbar_init(s_full(1), 1);
@@ -178,6 +176,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       Ring<NP> at;
       Ring<NX> xt;
       int n_p = 0, n_x = 0;   // pairs and rotated parts issued
+      int n_t = 0;            // tiles arrived for
       const uint32_t box_bytes = p.box_rows * 128, box = lane * box_bytes;
       auto free = [&](bool used, uint32_t bar, uint32_t parity) {
         return !used || mbar_wait(bar, parity ^ 1u, abort_flag, p.status);
@@ -186,52 +185,53 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       auto page = [&]() -> int {   // of this lane's box of tile j of the segment
         const int key = (seg.tile0 + j) * kTile + lane * p.box_rows;
         if (key >= seg.keys.len || key + p.box_rows <= seg.keys.first) return -1;
-        return p.block_table[static_cast<size_t>(seg.b) * p.max_blocks + key / p.block_size];
+        return p.block_table[static_cast<size_t>(seg.b) * p.max_blocks + (key >> p.block_shift)];
       };
       bool have = seg.next(p), ok = true;
       int pb = have ? page() : -1;
-      while (ok && have) {
+      while (have) {
         const bool in_range = pb >= 0 && pb < p.num_blocks;
-        const int y = in_range ? ((seg.tile0 + j) * kTile + lane * p.box_rows) % p.block_size : p.block_size;
+        const int y = in_range ? ((seg.tile0 + j) * kTile + lane * p.box_rows) & (p.block_size - 1) : p.block_size;
         const int z = in_range ? pb : 0;
         if (++j == seg.n) {
           j = 0;
           have = seg.next(p);
         }
         if (have) pb = page();
+        const uint32_t f = full(n_t % NT);
+        // the tile's bytes are announced copy by copy, its arrival comes at the end
 #pragma unroll
         for (int m = 0; m < kPairs; ++m) {
           if (!(ok = free(n_p >= NP, empty(at.slot), at.parity))) break;
-          const uint32_t f = full(at.slot), dst = sbase + Cfg::kOffC + at.slot * 2 * CB + box;
-          mbar_arrive_expect_tx(f, 2 * box_bytes);
+          const uint32_t dst = sbase + Cfg::kOffC + at.slot * 2 * CB + box;
+          mbar_expect_tx(f, 2 * box_bytes);
           tma_load_3d(dst, &p.tm, f, m * 128, y, z);
           tma_load_3d(dst + CB, &p.tm, f, m * 128 + kChunk, y, z);
           at.next();
           ++n_p;
         }
         if (!ok || !(ok = free(n_x >= NX, x_empty(xt.slot), xt.parity))) break;
-        const uint32_t f = x_full(xt.slot);
         mbar_arrive_expect_tx(f, box_bytes);
         tma_load_3d(sbase + Cfg::kOffX + xt.slot * CB + box, &p.tm, f, RANK, y, z);
         xt.next();
         ++n_x;
+        ++n_t;
       }
-      // Aborted: every copy lands before the CTA releases its memory. (A lane that gave up a slot
-      // before another did arrives there without a copy, so that the phase completes.)
+      // Aborted: every copy lands before the CTA releases its memory. (A tile given up half-way is
+      // arrived for, and so is one that another lane went on to, so that the phases complete.)
       const uint32_t lanes = (1u << (kTile / p.box_rows)) - 1;
       if (__any_sync(lanes, *abort_flag)) {
-        const int most_p = __reduce_max_sync(lanes, n_p), most_x = __reduce_max_sync(lanes, n_x);
-        for (; n_p < most_p; ++n_p) mbar_arrive(full(n_p % NP));
-        for (; n_x < most_x; ++n_x) mbar_arrive(x_full(n_x % NX));
-        for (int i = max(0, n_p - NP); i < n_p; ++i) drain_wait_d(full(i % NP), (i / NP) & 1, p.status);
-        for (int i = max(0, n_x - NX); i < n_x; ++i) drain_wait_d(x_full(i % NX), (i / NX) & 1, p.status);
+        if (!ok) mbar_arrive(full(n_t++ % NT));
+        const int most = __reduce_max_sync(lanes, n_t);
+        for (; n_t < most; ++n_t) mbar_arrive(full(n_t % NT));
+        for (int i = max(0, most - NT); i < most; ++i) drain_wait_d(full(i % NT), (i / NT) & 1, p.status);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ===================== MMA issuer (the whole warp, one lane of it the MMAs) =====================
-    // Two streams of work, whichever is ready first: tile gs's S, a pair of chunks at a time as
-    // they land, and tile go's O^T once its P is there. (In a fixed order, S of the next tile
+    // Two streams of work, whichever is ready first: tile gs's S, once it has landed, and
+    // tile go's O^T once its P is there. (In a fixed order, S of the next tile
     // first, a late load held up O^T, which frees the ring for the load after it.)
     constexpr uint32_t idesc_s = make_idesc(64, kTile, kBf16, false, false);
     constexpr uint32_t idesc_o = make_idesc(128, NR, kBf16, true, false);
@@ -305,18 +305,16 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       if (!ok) break;
       const bool begins = first_s;
       if (begins && !(ok = until(q_ready, n_seg++ & 1))) break;
+      if (!(ok = until(full(gs % NT), (gs / NT) & 1))) break;
+      tc_fence_after();
       const uint32_t d = tmem + (gs & 1) * 64;
 #pragma unroll
       for (int m = 0; m < kPairs; ++m) {
-        if (!(ok = until(full(at_s.slot), at_s.parity))) break;
-        tc_fence_after();
         const uint64_t cb = make_sdesc(sbase + Cfg::kOffC + at_s.slot * 2 * CB, 16, 1024);
         if (elect_one())
           mma_ss_steps<8, true, Cfg::kQB, true, CB>(d, qa + 2 * m * (Cfg::kQB >> 4), cb, idesc_s, m > 0 ? 1u : 0u);
         at_s.next();
       }
-      if (!ok || !(ok = until(x_full(xt.slot), xt.parity))) break;
-      tc_fence_after();
       const uint64_t xb = make_sdesc(sbase + Cfg::kOffX + xt.slot * CB, 16, 1024);
       if (elect_one()) {
         mma_ss_steps<4, true, Cfg::kQB, true, CB>(d, qa + 2 * kPairs * (Cfg::kQB >> 4), xb, idesc_s, 1u);

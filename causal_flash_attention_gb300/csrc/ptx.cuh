@@ -99,6 +99,11 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t byt
                : "memory");
 }
 
+// More bytes to come in the current phase, without an arrival.
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // Test for completion of the phase with the given parity (the thread may be
 // held briefly inside the instruction). No suspend-time hint is passed: on the
 // critical paths here, a suspended waiter wakes later than a polling one.
