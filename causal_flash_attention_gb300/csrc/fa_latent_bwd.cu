@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   const uint32_t dq_done = s_full + 32, drain = s_full + 40;
   auto swap = [&](int quarter) { return s_full + 48 + 8 * quarter; };
 
-  const int warp = static_cast<int>(warp_id());
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(warp_id()), 0);
   const int lane = static_cast<int>(lane_id());
   const int BH = p.B * p.H;
   const int unit = p.n_units - 1 - static_cast<int>(blockIdx.x) / BH;   // heaviest first
@@ -229,52 +229,55 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       }
     }
   } else if (warp == 1) {
-    // ===================== MMA issuer =====================
-    if (lane == 0 && n > 0) {
+    // ===================== MMA issuer (the whole warp, one lane of it the MMAs) =====================
+    if (n > 0) {
       constexpr uint32_t idesc_s = make_idesc(128, kTileN, kBf16, false, false);
       constexpr uint32_t idesc_q = make_idesc(128, W, kBf16, false, true);
-      constexpr uint64_t kStep = CB >> 4;
       const uint64_t qa = make_sdesc(sbase, 16, 1024);
       const uint64_t oa = make_sdesc(sbase + Cfg::kOffDO, 16, 1024);
-      bool ok = mbar_wait(q_full, 0, abort_flag, p.status);
+      auto wait = [&](uint32_t bar, uint32_t parity) { return warp_wait(bar, parity, abort_flag, p.status); };
+      bool ok = wait(q_full, 0);
 #ifdef FA_WAIT_TEST
       // wait-limit test build: nothing completes this phase before the abort
       // path's own commit, so the wait runs out
-      if (ok) ok = mbar_wait(drain, 0, abort_flag, p.status);
+      if (ok) ok = wait(drain, 0);
 #endif
       auto scores = [&](int j) -> bool {   // S = Q K'_j^T, dP = dO V_j^T
-        if (!mbar_wait(k_full(j % NK), (j / NK) & 1, abort_flag, p.status)) return false;
-        if (j > 0 && !mbar_wait(s_free, (j - 1) & 1, abort_flag, p.status)) return false;
+        if (!wait(k_full(j % NK), (j / NK) & 1)) return false;
+        if (j > 0 && !wait(s_free, (j - 1) & 1)) return false;
         tc_fence_after();
         const uint64_t kb = make_sdesc(sbase + Cfg::kOffK + (j % NK) * Cfg::kKBytes, 16, 1024);
-#pragma unroll
-        for (int c = 0; c < Cfg::kKChunks; ++c)
-          mma_ss_product<4, true, CB, true, CB>(tmem, qa + c * kStep, kb + c * kStep, idesc_s, c > 0 ? 1u : 0u);
-        tc_commit(s_full);
-        if (!mbar_wait(v_full(j % NV), (j / NV) & 1, abort_flag, p.status)) return false;
+        if (elect_one()) {
+          mma_ss_steps<4 * Cfg::kKChunks, true, CB, true, CB>(tmem, qa, kb, idesc_s, 0u);
+          tc_commit(s_full);
+        }
+        if (!wait(v_full(j % NV), (j / NV) & 1)) return false;
         const uint64_t vb = make_sdesc(sbase + Cfg::kOffV + (j % NV) * Cfg::kVBytes, 16, 1024);
-#pragma unroll
-        for (int c = 0; c < Cfg::kVChunks; ++c)
-          mma_ss_product<4, true, CB, true, CB>(tmem + 128, oa + c * kStep, vb + c * kStep, idesc_s, c > 0 ? 1u : 0u);
-        tc_commit(dp_full);
-        tc_commit(v_empty(j % NV));
+        if (elect_one()) {
+          mma_ss_steps<4 * Cfg::kVChunks, true, CB, true, CB>(tmem + 128, oa, vb, idesc_s, 0u);
+          tc_commit(dp_full);
+          tc_commit(v_empty(j % NV));
+        }
         return true;
       };
       if (ok) ok = scores(0);
       for (int j = 0; ok && j < n; ++j) {
         if (j + 1 < n && !(ok = scores(j + 1))) break;
-        if (!(ok = mbar_wait(ds_full, j & 1, abort_flag, p.status))) break;
+        if (!(ok = wait(ds_full, j & 1))) break;
         tc_fence_after();
         const uint64_t kb = make_sdesc(sbase + Cfg::kOffK + (j % NK) * Cfg::kKBytes, CB, 1024);
-        mma_ts_product8<false, 0>(tmem + 256, tmem + 448, kb, idesc_q, j > 0 ? 1u : 0u);
-        tc_commit(dq_done);
-        tc_commit(k_empty(j % NK));
+        if (elect_one()) {
+          mma_ts_steps<8, false, 0>(tmem + 256, tmem + 448, kb, idesc_q, j > 0 ? 1u : 0u);
+          tc_commit(dq_done);
+          tc_commit(k_empty(j % NK));
+        }
       }
       if (!ok) {
         // every MMA issued so far must finish before the TMEM is released
-        tc_commit(drain);
+        if (elect_one()) tc_commit(drain);
         drain_wait_b(drain, 0, p.status);
       }
+      __syncwarp();
     }
   } else {
     // ===================== softmax gradient, two threads a row =====================
@@ -451,7 +454,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   const uint32_t dp_full = s_full + 8, s_free = s_full + 16, ds_full = s_full + 24;
   const uint32_t kd_done = s_full + 32, drain = s_full + 40;
 
-  const int warp = static_cast<int>(warp_id());
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(warp_id()), 0);
   const int lane = static_cast<int>(lane_id());
   const int BH = p.B * p.H;
   const int kv0 = static_cast<int>(blockIdx.x) / BH * kTileN;   // most query rows first (causal)
@@ -541,49 +544,52 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       }
     }
   } else if (warp == 1) {
-    // ===================== MMA issuer =====================
-    if (lane == 0 && n > 0) {
+    // ===================== MMA issuer (the whole warp, one lane of it the MMAs) =====================
+    if (n > 0) {
       constexpr uint32_t idesc_s = make_idesc(128, R, kBf16, false, false);
       constexpr uint32_t idesc_v = make_idesc(128, D, kBf16, false, true);
       constexpr uint32_t idesc_k = make_idesc(128, W, kBf16, false, true);
-      constexpr uint64_t kA = CB >> 4, kB = QB >> 4;
       const uint64_t ka = make_sdesc(sbase, 16, 1024), va = make_sdesc(sbase + Cfg::kOffV, 16, 1024);
-      bool ok = mbar_wait(kv_full, 0, abort_flag, p.status);
+      auto wait = [&](uint32_t bar, uint32_t parity) { return warp_wait(bar, parity, abort_flag, p.status); };
+      bool ok = wait(kv_full, 0);
 #ifdef FA_WAIT_TEST
-      if (ok) ok = mbar_wait(drain, 0, abort_flag, p.status);   // runs out, as in the dQ kernel
+      if (ok) ok = wait(drain, 0);   // runs out, as in the dQ kernel
 #endif
       auto scores = [&](int g) -> bool {   // S^T and dP^T of step g
-        if (!mbar_wait(full(g % NS), (g / NS) & 1, abort_flag, p.status)) return false;
-        if (g > 0 && !mbar_wait(s_free, (g - 1) & 1, abort_flag, p.status)) return false;
+        if (!wait(full(g % NS), (g / NS) & 1)) return false;
+        if (g > 0 && !wait(s_free, (g - 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t qb = make_sdesc(sbase + Cfg::kOffQ + (g % NS) * Cfg::kStageBytes, 16, 1024);
-#pragma unroll
-        for (int c = 0; c < Cfg::kKChunks; ++c)
-          mma_ss_product<4, true, CB, true, QB>(tmem + 320, ka + c * kA, qb + c * kB, idesc_s, c > 0 ? 1u : 0u);
-        tc_commit(s_full);
-#pragma unroll
-        for (int c = 0; c < Cfg::kVChunks; ++c)
-          mma_ss_product<4, true, CB, true, QB>(tmem + 384, va + c * kA, qb + (Cfg::kKChunks + c) * kB, idesc_s,
-                                                c > 0 ? 1u : 0u);
-        tc_commit(dp_full);
+        const uint32_t st = sbase + Cfg::kOffQ + (g % NS) * Cfg::kStageBytes;
+        const uint64_t qb = make_sdesc(st, 16, 1024), ob = make_sdesc(st + Cfg::kKChunks * QB, 16, 1024);
+        if (elect_one()) {
+          mma_ss_steps<4 * Cfg::kKChunks, true, CB, true, QB>(tmem + 320, ka, qb, idesc_s, 0u);
+          tc_commit(s_full);
+        }
+        if (elect_one()) {
+          mma_ss_steps<4 * Cfg::kVChunks, true, CB, true, QB>(tmem + 384, va, ob, idesc_s, 0u);
+          tc_commit(dp_full);
+        }
         return true;
       };
       if (ok) ok = scores(0);
       for (int g = 0; ok && g < n; ++g) {
         if (g + 1 < n && !(ok = scores(g + 1))) break;
-        if (!(ok = mbar_wait(ds_full, g & 1, abort_flag, p.status))) break;
+        if (!(ok = wait(ds_full, g & 1))) break;
         tc_fence_after();
         const uint32_t st = sbase + Cfg::kOffQ + (g % NS) * Cfg::kStageBytes;
         const uint64_t qb = make_sdesc(st, QB, 1024), ob = make_sdesc(st + Cfg::kKChunks * QB, QB, 1024);
-        mma_ts_product4<false, 0>(tmem, tmem + 448, ob, idesc_v, g > 0 ? 1u : 0u);
-        mma_ts_product4<false, 0>(tmem + 128, tmem + 480, qb, idesc_k, g > 0 ? 1u : 0u);
-        tc_commit(kd_done);
-        tc_commit(empty(g % NS));
+        if (elect_one()) {
+          mma_ts_steps<4, false, 0>(tmem, tmem + 448, ob, idesc_v, g > 0 ? 1u : 0u);
+          mma_ts_steps<4, false, 0>(tmem + 128, tmem + 480, qb, idesc_k, g > 0 ? 1u : 0u);
+          tc_commit(kd_done);
+          tc_commit(empty(g % NS));
+        }
       }
       if (!ok) {
-        tc_commit(drain);
+        if (elect_one()) tc_commit(drain);
         drain_wait_b(drain, 0, p.status);
       }
+      __syncwarp();
     }
   } else {
     // ===================== softmax gradient, two threads a key =====================

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
   const auto p_full = bars(3 + 2 * NK + 2 * NV), pv_done = bars(5 + 2 * NK + 2 * NV);
   const uint32_t s_free = q_full + 8 * (7 + 2 * NK + 2 * NV), drain = s_free + 8;
 
-  const int warp = static_cast<int>(warp_id());
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(warp_id()), 0);
   const int lane = static_cast<int>(lane_id());
   // heaviest tiles first, as under the causal mask
   const int BH = p.B * p.H;
@@ -196,62 +196,68 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
       }
     }
   } else if (warp == 1) {
-    // ===================== MMA issuer =====================
-    if (lane == 0 && n_load > 0) {
+    // ===================== MMA issuer (the whole warp, one lane of it the MMAs) =====================
+    if (n_load > 0) {
       constexpr uint32_t idesc_qk = make_idesc(128, kTileN, kBf16, false, false);
       constexpr uint32_t idesc_pv = make_idesc(128, D, kBf16, false, true);
-      bool ok = mbar_wait(q_full, 0, abort_flag, p.status);
+      auto wait = [&](uint32_t bar, uint32_t parity) { return warp_wait(bar, parity, abort_flag, p.status); };
+      bool ok = wait(q_full, 0);
 #ifdef FA_WAIT_TEST
       // wait-limit test build: nothing completes this phase before the abort
       // path's own commit, so the wait runs out
-      if (ok) ok = mbar_wait(drain, 0, abort_flag, p.status);
+      if (ok) ok = wait(drain, 0);
 #endif
       auto active = [&](int t, int j) { return j >= first[t] && j < last[t]; };
       auto issue_qk = [&](int t, int j) {   // S_t = Q_t K_j^T
         const uint64_t qa = make_sdesc(sbase + t * Cfg::kKBytes, 16, 1024);
         const uint64_t kb = make_sdesc(sbase + Cfg::kOffK + (j % NK) * Cfg::kKBytes, 16, 1024);
-        constexpr uint64_t kStep = CB >> 4;
-#pragma unroll
-        for (int c = 0; c < Cfg::kKChunks; ++c)
-          mma_ss_product<4, true, CB, true, CB>(tmem + t * 128, qa + c * kStep, kb + c * kStep, idesc_qk,
-                                                c > 0 ? 1u : 0u);
-        tc_commit(s_full(t));
+        constexpr int kSteps = 4 * Cfg::kKChunks;
+        if (elect_one()) {
+          mma_ss_steps<kSteps, true, CB, true, CB>(tmem + t * 128, qa, kb, idesc_qk, 0u);
+          tc_commit(s_full(t));
+        }
       };
       auto issue_pv = [&](int t, int j) {   // O_t (+)= P_t V_j
         const uint64_t vb = make_sdesc(sbase + Cfg::kOffV + (j % NV) * Cfg::kVBytes, CB, 1024);
         const uint32_t o_t = tmem + 128 * T + t * 128;
-        mma_ts_product8<false, 0>(o_t, Cfg::kSepP ? o_t + D : tmem + t * 128, vb, idesc_pv,
-                                  j > first[t] ? 1u : 0u);
-        tc_commit(pv_done(t));
+        if (elect_one()) {
+          mma_ts_steps<8, false, 0>(o_t, Cfg::kSepP ? o_t + D : tmem + t * 128, vb, idesc_pv, j > first[t] ? 1u : 0u);
+          tc_commit(pv_done(t));
+        }
       };
-      if (ok) ok = mbar_wait(k_full(0), 0, abort_flag, p.status);
+      auto commit = [&](uint32_t bar) {
+        if (elect_one()) tc_commit(bar);
+      };
+      if (ok) ok = wait(k_full(0), 0);
       if (ok) {
         tc_fence_after();
+#pragma unroll
         for (int t = 0; t < T; ++t)
           if (active(t, 0)) issue_qk(t, 0);
-        tc_commit(k_empty(0));
+        commit(k_empty(0));
       }
       for (int j = 0; ok && j < n_load; ++j) {
         const uint32_t par_k1 = static_cast<uint32_t>((j + 1) / NK) & 1;
         const uint32_t par_v = static_cast<uint32_t>(j / NV) & 1;
         bool k_next = false, v_cur = false;   // K_{j+1}, V_j seen landed
-        for (int t = 0; t < T && ok; ++t) {
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
           const bool now = active(t, j), then = active(t, j + 1);
           const int n = j - first[t];   // tiles of this query tile before j
           auto next_qk = [&]() -> bool {
-            if (!k_next && !mbar_wait(k_full((j + 1) % NK), par_k1, abort_flag, p.status)) return false;
+            if (!k_next && !wait(k_full((j + 1) % NK), par_k1)) return false;
             k_next = true;
             // S_t has been read (or holds P_t that P_t V_j has read)
-            if (now && !mbar_wait(Cfg::kSepP ? s_free : pv_done(t), n & 1, abort_flag, p.status)) return false;
+            if (now && !wait(Cfg::kSepP ? s_free : pv_done(t), n & 1)) return false;
             tc_fence_after();
             issue_qk(t, j + 1);
             return true;
           };
           if (Cfg::kSepP && then && !(ok = next_qk())) break;
           if (now) {
-            if (!v_cur && !(ok = mbar_wait(v_full(j % NV), par_v, abort_flag, p.status))) break;
+            if (!v_cur && !(ok = wait(v_full(j % NV), par_v))) break;
             v_cur = true;
-            if (!(ok = mbar_wait(p_full(t), n & 1, abort_flag, p.status))) break;
+            if (!(ok = wait(p_full(t), n & 1))) break;
             tc_fence_after();
             issue_pv(t, j);
           }
@@ -260,18 +266,19 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
         if (!ok) break;
         // (a tile that no row of either query tile wants: its loads are waited for, so that
         // none is in flight at the end)
-        if (!v_cur && !(ok = mbar_wait(v_full(j % NV), par_v, abort_flag, p.status))) break;
-        tc_commit(v_empty(j % NV));
+        if (!v_cur && !(ok = wait(v_full(j % NV), par_v))) break;
+        commit(v_empty(j % NV));
         if (j + 1 < n_load) {
-          if (!k_next && !(ok = mbar_wait(k_full((j + 1) % NK), par_k1, abort_flag, p.status))) break;
-          tc_commit(k_empty((j + 1) % NK));
+          if (!k_next && !(ok = wait(k_full((j + 1) % NK), par_k1))) break;
+          commit(k_empty((j + 1) % NK));
         }
       }
       if (!ok) {
         // every MMA issued so far must finish before the TMEM is released
-        tc_commit(drain);
+        commit(drain);
         drain_wait_l(drain, 0, p.status);
       }
+      __syncwarp();
     }
   } else {
     // ===================== softmax / correction / epilogue =====================

@@ -403,25 +403,6 @@ __device__ __forceinline__ void mma_ts_product8(uint32_t d_tmem, uint32_t a_tmem
       : "memory");
 }
 
-// The same in 4 K-steps.
-template <bool kBK, int kBC>
-__device__ __forceinline__ void mma_ts_product4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b0,
-                                                uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred pf, pt;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
-      "setp.ne.b32 pf, %4, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pf;\n\t"
-      "add.s32 a, %1, 8;\n\tadd.s64 b, %2, %5;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, pt;\n\t"
-      "add.s32 a, %1, 16;\n\tadd.s64 b, %2, %6;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, pt;\n\t"
-      "add.s32 a, %1, 24;\n\tadd.s64 b, %2, %7;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, pt;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b0), "r"(idesc), "r"(accumulate),
-      "n"(desc_step<kBK, kBC>(1)), "n"(desc_step<kBK, kBC>(2)), "n"(desc_step<kBK, kBC>(3))
-      : "memory");
-}
-
 // ---- whole-warp issue --------------------------------------------------------
 // A warp that issues products as a whole: waits have one outcome for the warp (warp_wait), so
 // that control flow and descriptors are the same in every lane, and one elected lane (always
