@@ -32,14 +32,15 @@ struct LatFwdCfg {
   static constexpr int kKChunks = D / kChunk + 1;       // key chunks, the shared one last
   static constexpr int kVChunks = D / kChunk;
   static constexpr int kChunkBytes = kTileN * 128;
-  static constexpr int kKBytes = kKChunks * kChunkBytes, kVBytes = kVChunks * kChunkBytes;
-  static constexpr int kKStages = 2, kVStages = 1;
-  static constexpr int kOffK = T * kKBytes;             // Q tiles first
-  static constexpr int kOffV = kOffK + kKStages * kKBytes;
-  static constexpr int kOffBar = kOffV + kVStages * kVBytes;
-  // q_full, k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], pv_done[2],
-  // s_free, drain
-  static constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 8;
+  static constexpr int kKBytes = kKChunks * kChunkBytes;
+  // One ring of chunks for K' and V, in the order in which they are freed: K_0 V_0 K_1 V_1 ..., or
+  // K_0 K_1 V_0 K_2 V_1 ... where the next S is formed ahead of P V. (Stages of two K' and one V,
+  // the same memory, left every V tile's load uncovered, 2000 of 4800 cycles a step at d = 128.)
+  static constexpr int kSlots = T == 2 ? 8 : 5;
+  static constexpr int kOffRing = T * kKBytes;          // Q tiles first
+  static constexpr int kOffBar = kOffRing + kSlots * kChunkBytes;
+  // q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2], s_free, drain
+  static constexpr int kNumBars = 1 + 8 + 8;
   static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // tmem base, abort flag
   static constexpr int kOffSpan = kOffMisc + 16;        // (begin, end) of each softmax warp's rows
   static constexpr int kSmemBytes = kOffSpan + 4 * T * 8;
@@ -60,7 +61,7 @@ template <int D, bool kBf16>
 __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPerSm)
     latent_fwd_kernel(const __grid_constant__ LatentFwdParams p) {
   using Cfg = LatFwdCfg<D>;
-  constexpr int T = Cfg::T, NK = Cfg::kKStages, NV = Cfg::kVStages, CB = Cfg::kChunkBytes;
+  constexpr int T = Cfg::T, NS = Cfg::kSlots, CB = Cfg::kChunkBytes, KC = Cfg::kKChunks, VC = Cfg::kVChunks;
   using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -74,10 +75,9 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
 
   const uint32_t q_full = sbase + Cfg::kOffBar;
   auto bars = [&](int first) { return [=](int i) { return q_full + 8 * (first + i); }; };
-  const auto k_full = bars(1), k_empty = bars(1 + NK), v_full = bars(1 + 2 * NK);
-  const auto v_empty = bars(1 + 2 * NK + NV), s_full = bars(1 + 2 * NK + 2 * NV);
-  const auto p_full = bars(3 + 2 * NK + 2 * NV), pv_done = bars(5 + 2 * NK + 2 * NV);
-  const uint32_t s_free = q_full + 8 * (7 + 2 * NK + 2 * NV), drain = s_free + 8;
+  const auto k_full = bars(1), k_empty = bars(3), v_full = bars(5), v_empty = bars(7);   // by tile % 2
+  const auto s_full = bars(9), p_full = bars(11), pv_done = bars(13);
+  const uint32_t s_free = q_full + 8 * 15, drain = s_free + 8;
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(warp_id()), 0);
   const int lane = static_cast<int>(lane_id());
@@ -102,13 +102,11 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
   }
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    for (int s = 0; s < NK; ++s) {
-      mbar_init(k_full(s), 1);
-      mbar_init(k_empty(s), 1);
-    }
-    for (int s = 0; s < NV; ++s) {
-      mbar_init(v_full(s), 1);
-      mbar_init(v_empty(s), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full(i), 1);
+      mbar_init(k_empty(i), 1);
+      mbar_init(v_full(i), 1);
+      mbar_init(v_empty(i), 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full(t), 1);
@@ -172,27 +170,40 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
     // ===================== TMA producer =====================
     if (lane == 0) {
       if (n_load == 0) drain_wait_l(q_full, 0, p.status);   // no product waits for the queries
-      int jk = 0, jv = 0;   // K and V tiles issued
-      for (; jk < n_load;) {
-        const int sk = jk % NK, sv = jv % NV;
-        const int y = (tile0 + jk) * kTileN;
-        if (jk >= NK && !mbar_wait(k_empty(sk), (jk / NK - 1) & 1, abort_flag, p.status)) break;
-        mbar_arrive_expect_tx(k_full(sk), Cfg::kKBytes);
-        for (int c = 0; c < Cfg::kVChunks; ++c)
-          tma_load_4d(sbase + Cfg::kOffK + sk * Cfg::kKBytes + c * CB, &p.tm_k, k_full(sk), c * kChunk, y, h, b);
-        tma_load_4d(sbase + Cfg::kOffK + sk * Cfg::kKBytes + Cfg::kVChunks * CB, &p.tm_kr, k_full(sk), 0, y, 0, b);
-        ++jk;
-        if (jv >= NV && !mbar_wait(v_empty(sv), (jv / NV - 1) & 1, abort_flag, p.status)) break;
-        mbar_arrive_expect_tx(v_full(sv), Cfg::kVBytes);
-        for (int c = 0; c < Cfg::kVChunks; ++c)
-          tma_load_4d(sbase + Cfg::kOffV + sv * Cfg::kVBytes + c * CB, &p.tm_v, v_full(sv), c * kChunk, y, h, b);
-        ++jv;
+      // units of the ring, in order: K or V of a tile
+      auto is_k = [](int u) { return Cfg::kSepP ? u == 0 || u % 2 == 1 : u % 2 == 0; };
+      auto tile_of = [&](int u) { return Cfg::kSepP ? (u == 0 ? 0 : is_k(u) ? (u + 1) / 2 : u / 2 - 1) : u / 2; };
+      const int n_units = 2 * n_load + (Cfg::kSepP ? 1 : 0);   // (with a K past the last tile, skipped)
+      int slot = 0, used = 0, oldest = 0, jk = 0, jv = 0;   // jk, jv: K and V tiles issued
+      for (int u = 0; u < n_units; ++u) {
+        const int j = tile_of(u), n = is_k(u) ? KC : VC;
+        if (j >= n_load) continue;
+        bool ok = true;
+        for (; used + n > NS; ++oldest) {
+          const int o = tile_of(oldest);
+          if (!(ok = mbar_wait(is_k(oldest) ? k_empty(o & 1) : v_empty(o & 1), (o >> 1) & 1, abort_flag, p.status))) break;
+          used -= is_k(oldest) ? KC : VC;
+        }
+        if (!ok) break;
+        const uint32_t f = is_k(u) ? k_full(j & 1) : v_full(j & 1);
+        const int y = (tile0 + j) * kTileN;
+        mbar_arrive_expect_tx(f, n * CB);
+        for (int c = 0; c < n; ++c) {
+          const uint32_t dst = sbase + Cfg::kOffRing + slot * CB;
+          if (!is_k(u)) tma_load_4d(dst, &p.tm_v, f, c * kChunk, y, h, b);
+          else if (c < VC) tma_load_4d(dst, &p.tm_k, f, c * kChunk, y, h, b);
+          else tma_load_4d(dst, &p.tm_kr, f, 0, y, 0, b);
+          slot = slot + 1 == NS ? 0 : slot + 1;
+        }
+        used += n;
+        if (is_k(u)) ++jk;
+        else ++jv;
       }
       if (*abort_flag) {
         // let every copy already issued land before the CTA releases its memory
         drain_wait_l(q_full, 0, p.status);
-        for (int j = max(0, jk - NK); j < jk; ++j) drain_wait_l(k_full(j % NK), (j / NK) & 1, p.status);
-        for (int j = max(0, jv - NV); j < jv; ++j) drain_wait_l(v_full(j % NV), (j / NV) & 1, p.status);
+        for (int j = max(0, jk - 2); j < jk; ++j) drain_wait_l(k_full(j & 1), (j >> 1) & 1, p.status);
+        for (int j = max(0, jv - 2); j < jv; ++j) drain_wait_l(v_full(j & 1), (j >> 1) & 1, p.status);
       }
     }
   } else if (warp == 1) {
@@ -208,21 +219,52 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
       if (ok) ok = wait(drain, 0);
 #endif
       auto active = [&](int t, int j) { return j >= first[t] && j < last[t]; };
-      auto issue_qk = [&](int t, int j) {   // S_t = Q_t K_j^T
-        const uint64_t qa = make_sdesc(sbase + t * Cfg::kKBytes, 16, 1024);
-        const uint64_t kb = make_sdesc(sbase + Cfg::kOffK + (j % NK) * Cfg::kKBytes, 16, 1024);
-        constexpr int kSteps = 4 * Cfg::kKChunks;
-        if (elect_one()) {
-          mma_ss_steps<kSteps, true, CB, true, CB>(tmem + t * 128, qa, kb, idesc_qk, 0u);
-          tc_commit(s_full(t));
+      // the ring's slots of the K tile and the V tile in turn
+      int next_slot = 0, k_slot[KC], v_slot[VC];
+      auto take = [&](int (&slots)[KC]) {
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          slots[c] = next_slot;
+          next_slot = next_slot + 1 == NS ? 0 : next_slot + 1;
         }
       };
-      auto issue_pv = [&](int t, int j) {   // O_t (+)= P_t V_j
-        const uint64_t vb = make_sdesc(sbase + Cfg::kOffV + (j % NV) * Cfg::kVBytes, CB, 1024);
+      auto take_v = [&]() {
+#pragma unroll
+        for (int c = 0; c < VC; ++c) {
+          v_slot[c] = next_slot;
+          next_slot = next_slot + 1 == NS ? 0 : next_slot + 1;
+        }
+      };
+      const uint64_t ring = make_sdesc(sbase + Cfg::kOffRing, 16, 1024);   // K-major
+      const uint64_t ring_mn = make_sdesc(sbase + Cfg::kOffRing, CB, 1024);
+      constexpr uint64_t kSlot = CB >> 4;
+      auto issue_qk = [&](int t) {   // S_t = Q_t K^T
+        const uint64_t qa = make_sdesc(sbase + t * Cfg::kKBytes, 16, 1024);
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          const uint64_t kb = ring + k_slot[c] * kSlot;
+          if (elect_one()) {
+            mma_ss_steps<4, true, CB, true, CB>(tmem + t * 128, qa + c * kSlot, kb, idesc_qk, c > 0 ? 1u : 0u);
+            if (c == KC - 1) tc_commit(s_full(t));
+          }
+        }
+      };
+      auto issue_pv = [&](int t, bool more) {   // O_t (+)= P_t V
         const uint32_t o_t = tmem + 128 * T + t * 128;
-        if (elect_one()) {
-          mma_ts_steps<8, false, 0>(o_t, Cfg::kSepP ? o_t + D : tmem + t * 128, vb, idesc_pv, j > first[t] ? 1u : 0u);
-          tc_commit(pv_done(t));
+        const uint32_t p_t = Cfg::kSepP ? o_t + D : tmem + t * 128;
+        if (VC == 2 && v_slot[VC - 1] == 0) {   // the tile's chunks are not next to each other
+          const uint64_t v0 = ring_mn + v_slot[0] * kSlot, v1 = ring_mn;
+          if (elect_one()) {
+            mma_ts_steps<8, false, 0>(o_t, p_t, v0, make_idesc(128, 64, kBf16, false, true), more ? 1u : 0u);
+            mma_ts_steps<8, false, 0>(o_t + 64, p_t, v1, make_idesc(128, 64, kBf16, false, true), more ? 1u : 0u);
+            tc_commit(pv_done(t));
+          }
+        } else {
+          const uint64_t vb = ring_mn + v_slot[0] * kSlot;
+          if (elect_one()) {
+            mma_ts_steps<8, false, 0>(o_t, p_t, vb, idesc_pv, more ? 1u : 0u);
+            tc_commit(pv_done(t));
+          }
         }
       };
       auto commit = [&](uint32_t bar) {
@@ -231,46 +273,63 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
       if (ok) ok = wait(k_full(0), 0);
       if (ok) {
         tc_fence_after();
+        take(k_slot);
 #pragma unroll
         for (int t = 0; t < T; ++t)
-          if (active(t, 0)) issue_qk(t, 0);
+          if (active(t, 0)) issue_qk(t);
         commit(k_empty(0));
       }
       for (int j = 0; ok && j < n_load; ++j) {
-        const uint32_t par_k1 = static_cast<uint32_t>((j + 1) / NK) & 1;
-        const uint32_t par_v = static_cast<uint32_t>(j / NV) & 1;
-        bool k_next = false, v_cur = false;   // K_{j+1}, V_j seen landed
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-          const bool now = active(t, j), then = active(t, j + 1);
-          const int n = j - first[t];   // tiles of this query tile before j
-          auto next_qk = [&]() -> bool {
-            if (!k_next && !wait(k_full((j + 1) % NK), par_k1)) return false;
-            k_next = true;
-            // S_t has been read (or holds P_t that P_t V_j has read)
-            if (now && !wait(Cfg::kSepP ? s_free : pv_done(t), n & 1)) return false;
+        const bool last_tile = j + 1 == n_load;
+        // a tile that no row of either query tile wants is waited for all the same, so that none is
+        // in flight at the end
+        auto next_k = [&]() -> bool {
+          if (!last_tile) take(k_slot);
+          return last_tile || wait(k_full((j + 1) & 1), ((j + 1) >> 1) & 1);
+        };
+        if constexpr (Cfg::kSepP) {   // S of the next tile once S has been read, then P V
+          const bool now = active(0, j), then = active(0, j + 1);
+          if (!(ok = next_k())) break;
+          if (then) {
+            if (now && !(ok = wait(s_free, (j - first[0]) & 1))) break;
             tc_fence_after();
-            issue_qk(t, j + 1);
-            return true;
-          };
-          if (Cfg::kSepP && then && !(ok = next_qk())) break;
-          if (now) {
-            if (!v_cur && !(ok = wait(v_full(j % NV), par_v))) break;
-            v_cur = true;
-            if (!(ok = wait(p_full(t), n & 1))) break;
-            tc_fence_after();
-            issue_pv(t, j);
+            issue_qk(0);
           }
-          if (!Cfg::kSepP && then && !(ok = next_qk())) break;
-        }
-        if (!ok) break;
-        // (a tile that no row of either query tile wants: its loads are waited for, so that
-        // none is in flight at the end)
-        if (!v_cur && !(ok = wait(v_full(j % NV), par_v))) break;
-        commit(v_empty(j % NV));
-        if (j + 1 < n_load) {
-          if (!k_next && !(ok = wait(k_full((j + 1) % NK), par_k1))) break;
-          commit(k_empty((j + 1) % NK));
+          if (!last_tile) commit(k_empty((j + 1) & 1));
+          take_v();
+          if (!(ok = wait(v_full(j & 1), (j >> 1) & 1))) break;
+          if (now) {
+            if (!(ok = wait(p_full(0), (j - first[0]) & 1))) break;
+            tc_fence_after();
+            issue_pv(0, j > first[0]);
+          }
+          commit(v_empty(j & 1));
+        } else {   // P_t V, then S_t of the next tile over P_t, for either query tile in turn
+          take_v();
+          if (!(ok = wait(v_full(j & 1), (j >> 1) & 1))) break;
+          bool k_seen = false;
+#pragma unroll
+          for (int t = 0; t < T; ++t) {
+            const bool now = active(t, j), then = active(t, j + 1);
+            const int n = j - first[t];   // tiles of this query tile before j
+            if (now) {
+              if (!(ok = wait(p_full(t), n & 1))) break;
+              tc_fence_after();
+              issue_pv(t, n > 0);
+            }
+            if (!k_seen && (t == T - 1 || then)) {
+              if (!(ok = next_k())) break;
+              k_seen = true;
+            }
+            if (then) {
+              if (now && !(ok = wait(pv_done(t), n & 1))) break;   // P_t V has read P_t
+              tc_fence_after();
+              issue_qk(t);
+            }
+          }
+          if (!ok) break;
+          commit(v_empty(j & 1));
+          if (!last_tile) commit(k_empty((j + 1) & 1));
         }
       }
       if (!ok) {
