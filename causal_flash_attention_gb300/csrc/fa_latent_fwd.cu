@@ -317,6 +317,8 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
               tc_fence_after();
               issue_pv(t, n > 0);
             }
+            // (a commit covers all that was issued before it: V's comes before the next S)
+            if (t == T - 1) commit(v_empty(j & 1));
             if (!k_seen && (t == T - 1 || then)) {
               if (!(ok = next_k())) break;
               k_seen = true;
@@ -328,7 +330,6 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
             }
           }
           if (!ok) break;
-          commit(v_empty(j & 1));
           if (!last_tile) commit(k_empty((j + 1) & 1));
         }
       }
