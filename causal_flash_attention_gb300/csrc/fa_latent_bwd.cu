@@ -67,35 +67,38 @@ __device__ __forceinline__ void store32(void* row, const uint32_t (&o)[32], floa
 }
 
 // --------------------------------------------------------------------- dQ --
-// Tensor memory: S [0, 128), dP [128, 256), dQ [256, 256 + d + 64), dS (16-bit) [448, 512).
-// S and dP of the next tile are formed while the warps work on this tile's, which they
-// have copied to registers.
+// Q and dO stay in tensor memory, as A operands, for the whole CTA, which leaves shared memory to
+// a deep ring of 64-key tiles (with both in shared memory there was room for two K' tiles of
+// 128 keys and one of V, whose loads stood in every step: 3700 cycles for 128 keys, of 2048 of
+// products), and lets products 64 keys wide run at the tensor core's rate. Tensor memory: S
+// [0, 64), dP [64, 128), dQ [128, 192 + d), dS (16-bit) [192 + d, 224 + d), Q, dO behind it: 512
+// columns in all at d = 128. S and dP of the next tile are formed while the warps work on this
+// tile's, which they have copied to registers.
 template <int D>
 struct LatDqCfg {
   static constexpr int kW = D + kRope;                  // columns of a key
+  static constexpr int kKeys = 64;                      // keys of a tile
   static constexpr int kKChunks = kW / kChunk, kVChunks = D / kChunk;
-  static constexpr int CB = kTileN * 128;
-  static constexpr int kKBytes = kKChunks * CB, kVBytes = kVChunks * CB;
-  static constexpr int NK = 2, NV = D == 128 ? 1 : 2;
-  static constexpr int kOffDO = kKBytes;                // Q first
-  static constexpr int kOffK = kOffDO + kVBytes;
-  static constexpr int kOffV = kOffK + NK * kKBytes;
-  static constexpr int kOffBar = kOffV + NV * kVBytes;
-  // q_full, k_full[], k_empty[], v_full[], v_empty[], s_full, dp_full, s_free, ds_full, dq_done,
-  // drain, swap[4]
-  static constexpr int kNumBars = 1 + 2 * NK + 2 * NV + 10;
+  static constexpr int CB = kKeys * 128;
+  static constexpr int kStageBytes = (kKChunks + kVChunks) * CB;   // K', then V
+  static constexpr int NS = 5;
+  static constexpr int kOffBar = NS * kStageBytes;
+  // full[], empty[], s_full, dp_full, s_free, ds_full, dq_done, drain, swap[4]
+  static constexpr int kNumBars = 2 * NS + 10;
   static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kOffSpan = kOffMisc + 16;        // 4 warps' (begin, end)
   static constexpr int kOffDelta = kOffSpan + 32;       // two buffers of [2][128] halves of D
   static constexpr int kSmemBytes = kOffDelta + 2048;
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+  static constexpr int kColDq = 128, kColDs = kColDq + kW, kColQ = kColDs + 32, kColDO = kColQ + kW / 2;
+  static_assert(kColDO + D / 2 <= 512, "tensor memory");
 };
 
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreadsB, 1)
     latent_dq_kernel(const __grid_constant__ LatentBwdParams p) {
   using Cfg = LatDqCfg<D>;
-  constexpr int NK = Cfg::NK, NV = Cfg::NV, CB = Cfg::CB, W = Cfg::kW;
+  constexpr int NS = Cfg::NS, CB = Cfg::CB, W = Cfg::kW, KT = Cfg::kKeys;
   using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -108,11 +111,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   int2* ranges = reinterpret_cast<int2*>(smem + Cfg::kOffSpan);
   float* halves = reinterpret_cast<float*>(smem + Cfg::kOffDelta);
 
-  const uint32_t q_full = sbase + Cfg::kOffBar;
-  auto bars = [&](int first) { return [=](int i) { return q_full + 8 * (first + i); }; };
-  const auto k_full = bars(1), k_empty = bars(1 + NK), v_full = bars(1 + 2 * NK);
-  const auto v_empty = bars(1 + 2 * NK + NV);
-  const uint32_t s_full = q_full + 8 * (1 + 2 * NK + 2 * NV);
+  const uint32_t bar0 = sbase + Cfg::kOffBar;
+  auto full = [&](int s) { return bar0 + 8 * s; };
+  auto empty = [&](int s) { return bar0 + 8 * (NS + s); };
+  const uint32_t s_full = bar0 + 8 * 2 * NS;
   const uint32_t dp_full = s_full + 8, s_free = s_full + 16, ds_full = s_full + 24;
   const uint32_t dq_done = s_full + 32, drain = s_full + 40;
   auto swap = [&](int quarter) { return s_full + 48 + 8 * quarter; };
@@ -125,8 +127,31 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   const int b = bh / p.H, h = bh % p.H;
   const int q0 = unit * kTileM;
   const int quarter = warp & 3, half = (warp - 2) >> 2;
-  const int row = q0 + quarter * 32 + lane;
+  const int rr = quarter * 32 + lane, row = q0 + rr;
+  const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
 
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(s_free, 8);   // one arrival per compute warp
+    mbar_init(ds_full, 8);
+    mbar_init(dq_done, 1);
+    mbar_init(drain, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(swap(i), 2);   // the two warps of a lane quarter
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_kr);
+    tma_prefetch_desc(&p.tm_v);
+  }
   int row_lo = 0, row_hi = 0;
   float l2 = INFINITY;
   if (warp >= 2) {
@@ -139,56 +164,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       const int hi = __reduce_max_sync(0xffffffffu, row_hi);
       if (lane == 0) ranges[quarter] = make_int2(lo, hi);
     }
-    // this thread's half of D, and L
-    float d = 0.f;
-    if (row < p.mask.Sq) {
-      const Elem* o = static_cast<const Elem*>(p.out.data) + b * p.out.sb + h * p.out.sh + row * p.out.ss + half * (D / 2);
-      const Elem* g = static_cast<const Elem*>(p.dout.data) + b * p.dout.sb + h * p.dout.sh + row * p.dout.ss + half * (D / 2);
-#pragma unroll
-      for (int u = 0; u < D / 16; ++u)
-        d = dot16<kBf16>(reinterpret_cast<const uint4*>(o)[u], reinterpret_cast<const uint4*>(g)[u], d);
-      l2 = p.lse[static_cast<size_t>(bh) * p.mask.Sq + row] * kLog2eB;
-      if (row_hi == 0) l2 = INFINITY;   // sees nothing: P = 0
-    }
-    halves[half * 128 + quarter * 32 + lane] = d;
-  }
-  if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    for (int s = 0; s < NK; ++s) {
-      mbar_init(k_full(s), 1);
-      mbar_init(k_empty(s), 1);
-    }
-    for (int s = 0; s < NV; ++s) {
-      mbar_init(v_full(s), 1);
-      mbar_init(v_empty(s), 1);
-    }
-    mbar_init(s_full, 1);
-    mbar_init(dp_full, 1);
-    mbar_init(s_free, 8);   // one arrival per compute warp
-    mbar_init(ds_full, 8);
-    mbar_init(dq_done, 1);
-    mbar_init(drain, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(swap(i), 2);   // the two warps of a lane quarter
-    *abort_flag = 0;
-    fence_mbar_init();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    mbar_arrive_expect_tx(q_full, Cfg::kKBytes + Cfg::kVBytes);
-    for (int r = 0; r < 2; ++r) {
-      for (int c = 0; c < Cfg::kKChunks; ++c)
-        tma_load_4d(sbase + c * CB + r * (CB / 2), &p.tm_q, q_full, c * kChunk, q0 + r * 64, h, b);
-      for (int c = 0; c < Cfg::kVChunks; ++c)
-        tma_load_4d(sbase + Cfg::kOffDO + c * CB + r * (CB / 2), &p.tm_do, q_full, c * kChunk, q0 + r * 64, h, b);
-    }
-    tma_prefetch_desc(&p.tm_k);
-    tma_prefetch_desc(&p.tm_kr);
-    tma_prefetch_desc(&p.tm_v);
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  __syncthreads();   // tensor memory, barriers, ranges
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -198,65 +176,95 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     lo = min(lo, ranges[w].x);
     hi = max(hi, ranges[w].y);
   }
-  const int tile0 = hi > 0 ? lo / kTileN : 0;
-  const int n = hi > 0 ? (hi + kTileN - 1) / kTileN - tile0 : 0;
+  const int tile0 = hi > 0 ? lo / KT : 0;
+  const int n = hi > 0 ? (hi + KT - 1) / KT - tile0 : 0;
+
+  if (warp >= 2) {
+    // this thread's halves of its row of Q and dO into tensor memory, its half of D, and L
+    constexpr int QW = W / 4, OW = D / 4;   // words of a half
+    uint32_t qw[QW], ow[OW];
+    float d = 0.f;
+#pragma unroll
+    for (int i = 0; i < QW; ++i) qw[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < OW; ++i) ow[i] = 0u;
+    if (row < p.mask.Sq) {
+      auto at = [&](const HeadView& v, int e) {
+        return reinterpret_cast<const uint4*>(static_cast<const Elem*>(v.data) + b * v.sb + h * v.sh + row * v.ss + e);
+      };
+      const uint4 *q = at(p.q, half * (W / 2)), *g = at(p.dout, half * (D / 2)), *o = at(p.out, half * (D / 2));
+#pragma unroll
+      for (int u = 0; u < QW / 4; ++u) *reinterpret_cast<uint4*>(qw + 4 * u) = q[u];
+#pragma unroll
+      for (int u = 0; u < OW / 4; ++u) *reinterpret_cast<uint4*>(ow + 4 * u) = g[u];
+#pragma unroll
+      for (int u = 0; u < OW / 4; ++u) d = dot16<kBf16>(o[u], *reinterpret_cast<const uint4*>(ow + 4 * u), d);
+      l2 = p.lse[static_cast<size_t>(bh) * p.mask.Sq + row] * kLog2eB;
+      if (row_hi == 0) l2 = INFINITY;   // sees nothing: P = 0
+    }
+#pragma unroll
+    for (int i = 0; i < QW / 16; ++i)
+      tmem_st16(tmem + lane_off + Cfg::kColQ + half * QW + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(qw + 16 * i));
+#pragma unroll
+    for (int i = 0; i < OW / 16; ++i)
+      tmem_st16(tmem + lane_off + Cfg::kColDO + half * OW + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(ow + 16 * i));
+    halves[half * 128 + rr] = d;
+    tmem_wait_st();
+  }
+  if (warp == 0 && lane == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the first tiles are on their way meanwhile
+  auto load = [&](int j) {
+    const uint32_t f = full(j % NS), dst = sbase + (j % NS) * Cfg::kStageBytes;
+    const int y = (tile0 + j) * KT;
+    mbar_arrive_expect_tx(f, Cfg::kStageBytes);
+    for (int c = 0; c < Cfg::kVChunks; ++c) {
+      tma_load_4d(dst + c * CB, &p.tm_k, f, c * kChunk, y, h, b);
+      tma_load_4d(dst + (Cfg::kKChunks + c) * CB, &p.tm_v, f, c * kChunk, y, h, b);
+    }
+    tma_load_4d(dst + Cfg::kVChunks * CB, &p.tm_kr, f, 0, y, 0, b);
+  };
+  if (warp == 0 && lane == 0)
+    for (int j = 0; j < min(n, NS); ++j) load(j);
+  tc_fence_before();
+  __syncthreads();   // Q, dO and the halves of D
+  tc_fence_after();
 
   if (warp == 0) {
     // ===================== TMA producer =====================
     if (lane == 0) {
-      if (n == 0) drain_wait_b(q_full, 0, p.status);   // no product waits for the queries
-      int jk = 0, jv = 0;
-      while (jk < n) {
-        const int sk = jk % NK, sv = jv % NV;
-        const int y = (tile0 + jk) * kTileN;
-        if (jk >= NK && !mbar_wait(k_empty(sk), (jk / NK - 1) & 1, abort_flag, p.status)) break;
-        mbar_arrive_expect_tx(k_full(sk), Cfg::kKBytes);
-        for (int c = 0; c < Cfg::kVChunks; ++c)
-          tma_load_4d(sbase + Cfg::kOffK + sk * Cfg::kKBytes + c * CB, &p.tm_k, k_full(sk), c * kChunk, y, h, b);
-        tma_load_4d(sbase + Cfg::kOffK + sk * Cfg::kKBytes + Cfg::kVChunks * CB, &p.tm_kr, k_full(sk), 0, y, 0, b);
-        ++jk;
-        if (jv >= NV && !mbar_wait(v_empty(sv), (jv / NV - 1) & 1, abort_flag, p.status)) break;
-        mbar_arrive_expect_tx(v_full(sv), Cfg::kVBytes);
-        for (int c = 0; c < Cfg::kVChunks; ++c)
-          tma_load_4d(sbase + Cfg::kOffV + sv * Cfg::kVBytes + c * CB, &p.tm_v, v_full(sv), c * kChunk, y, h, b);
-        ++jv;
+      int j = min(n, NS);
+      for (; j < n; ++j) {
+        if (!mbar_wait(empty(j % NS), (j / NS - 1) & 1, abort_flag, p.status)) break;
+        load(j);
       }
-      if (*abort_flag) {
-        // let every copy already issued land before the CTA releases its memory
-        drain_wait_b(q_full, 0, p.status);
-        for (int j = max(0, jk - NK); j < jk; ++j) drain_wait_b(k_full(j % NK), (j / NK) & 1, p.status);
-        for (int j = max(0, jv - NV); j < jv; ++j) drain_wait_b(v_full(j % NV), (j / NV) & 1, p.status);
-      }
+      if (*abort_flag)   // let every copy already issued land before the CTA releases its memory
+        for (int i = max(0, j - NS); i < j; ++i) drain_wait_b(full(i % NS), (i / NS) & 1, p.status);
     }
   } else if (warp == 1) {
     // ===================== MMA issuer (the whole warp, one lane of it the MMAs) =====================
     if (n > 0) {
-      constexpr uint32_t idesc_s = make_idesc(128, kTileN, kBf16, false, false);
+      constexpr uint32_t idesc_s = make_idesc(128, KT, kBf16, false, false);
       constexpr uint32_t idesc_q = make_idesc(128, W, kBf16, false, true);
-      const uint64_t qa = make_sdesc(sbase, 16, 1024);
-      const uint64_t oa = make_sdesc(sbase + Cfg::kOffDO, 16, 1024);
       auto wait = [&](uint32_t bar, uint32_t parity) { return warp_wait(bar, parity, abort_flag, p.status); };
-      bool ok = wait(q_full, 0);
+      bool ok = true;
 #ifdef FA_WAIT_TEST
       // wait-limit test build: nothing completes this phase before the abort
       // path's own commit, so the wait runs out
-      if (ok) ok = wait(drain, 0);
+      ok = wait(drain, 0);
 #endif
       auto scores = [&](int j) -> bool {   // S = Q K'_j^T, dP = dO V_j^T
-        if (!wait(k_full(j % NK), (j / NK) & 1)) return false;
+        if (!wait(full(j % NS), (j / NS) & 1)) return false;
         if (j > 0 && !wait(s_free, (j - 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t kb = make_sdesc(sbase + Cfg::kOffK + (j % NK) * Cfg::kKBytes, 16, 1024);
+        const uint32_t st = sbase + (j % NS) * Cfg::kStageBytes;
+        const uint64_t kb = make_sdesc(st, 16, 1024), vb = make_sdesc(st + Cfg::kKChunks * CB, 16, 1024);
         if (elect_one()) {
-          mma_ss_steps<4 * Cfg::kKChunks, true, CB, true, CB>(tmem, qa, kb, idesc_s, 0u);
+          mma_ts_steps<W / 16, true, CB>(tmem, tmem + Cfg::kColQ, kb, idesc_s, 0u);
           tc_commit(s_full);
         }
-        if (!wait(v_full(j % NV), (j / NV) & 1)) return false;
-        const uint64_t vb = make_sdesc(sbase + Cfg::kOffV + (j % NV) * Cfg::kVBytes, 16, 1024);
         if (elect_one()) {
-          mma_ss_steps<4 * Cfg::kVChunks, true, CB, true, CB>(tmem + 128, oa, vb, idesc_s, 0u);
+          mma_ts_steps<D / 16, true, CB>(tmem + KT, tmem + Cfg::kColDO, vb, idesc_s, 0u);
           tc_commit(dp_full);
-          tc_commit(v_empty(j % NV));
         }
         return true;
       };
@@ -265,11 +273,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         if (j + 1 < n && !(ok = scores(j + 1))) break;
         if (!(ok = wait(ds_full, j & 1))) break;
         tc_fence_after();
-        const uint64_t kb = make_sdesc(sbase + Cfg::kOffK + (j % NK) * Cfg::kKBytes, CB, 1024);
+        const uint64_t kb = make_sdesc(sbase + (j % NS) * Cfg::kStageBytes, CB, 1024);
         if (elect_one()) {
-          mma_ts_steps<8, false, 0>(tmem + 256, tmem + 448, kb, idesc_q, j > 0 ? 1u : 0u);
-          tc_commit(dq_done);
-          tc_commit(k_empty(j % NK));
+          mma_ts_steps<KT / 16, false, 0>(tmem + Cfg::kColDq, tmem + Cfg::kColDs, kb, idesc_q, j > 0 ? 1u : 0u);
+          tc_commit(empty(j % NS));   // (before the one that is waited for at the end: a commit
+          tc_commit(dq_done);         // that arrived after the CTA had exited would be a fault)
         }
       }
       if (!ok) {
@@ -281,42 +289,34 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     }
   } else {
     // ===================== softmax gradient, two threads a row =====================
-    const int rr = quarter * 32 + lane;
     float delta = halves[rr] + halves[128 + rr];
     int n_swap = 0;   // exchanges of half sums with the other warp of the rows
-    if (half == 0) {
-      if (h == 0 && lane == 0 && (quarter & 1) == 0) {
-        const int2 u = ranges[quarter], v = ranges[quarter + 1];
-        p.ranges[static_cast<size_t>(b) * (p.Sq_pad / 64) + unit * 2 + quarter / 2] =
-            make_int2(min(u.x, v.x), max(u.y, v.y));
-      }
+    if (half == 0 && h == 0 && lane == 0 && (quarter & 1) == 0) {
+      const int2 u = ranges[quarter], v = ranges[quarter + 1];
+      p.ranges[static_cast<size_t>(b) * (p.Sq_pad / 64) + unit * 2 + quarter / 2] =
+          make_int2(min(u.x, v.x), max(u.y, v.y));
     }
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_s = tmem + lane_off + half * 64;
+    const uint32_t t_s = tmem + lane_off + half * 32;
     const float c = p.scale_log2;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       ok = __all_sync(0xffffffffu, mbar_wait(s_full, j & 1, abort_flag, p.status));
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[64];
-      tmem_ld32(t_s, *reinterpret_cast<uint32_t(*)[32]>(s));
-      tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+      uint32_t s[32], g[32];
+      tmem_ld32(t_s, s);
       tmem_wait_ld();
-      const int kv0 = (tile0 + j) * kTileN + half * 64;
-      const bool inside = row_hi > 0 && row_lo >= kv0 - half * 64 && row_hi <= kv0 - half * 64 + kTileN;
-      if (kv0 < row_lo || kv0 + 64 > row_hi) {
+      const int tile_k0 = (tile0 + j) * KT, k0 = tile_k0 + half * 32;
+      const bool inside = row_hi > 0 && row_lo >= tile_k0 && row_hi <= tile_k0 + KT;
+      if (k0 < row_lo || k0 + 32 > row_hi) {
+        const uint32_t see = span_bits(row_lo, row_hi, k0);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const uint32_t see = span_bits(row_lo, row_hi, kv0 + w * 32);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!((see >> i) & 1u)) s[w * 32 + i] = __float_as_uint(-INFINITY);
-        }
+        for (int i = 0; i < 32; ++i)
+          if (!((see >> i) & 1u)) s[i] = __float_as_uint(-INFINITY);
       }
       const uint64_t c2 = f2_pack(c, c), nl2 = f2_pack(-l2, -l2);
 #pragma unroll
-      for (int i = 0; i < 64; i += 2) {   // P, in fp32
+      for (int i = 0; i < 32; i += 2) {   // P, in fp32
         float x0, x1;
         f2_unpack(f2_fma(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, nl2), x0, x1);
         s[i] = __float_as_uint(ex2(x0));
@@ -325,9 +325,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, abort_flag, p.status));
       if (!ok) break;
       tc_fence_after();
-      uint32_t g[64];
-      tmem_ld32(t_s + 128, *reinterpret_cast<uint32_t(*)[32]>(g));
-      tmem_ld32(t_s + 160, *reinterpret_cast<uint32_t(*)[32]>(g + 32));
+      tmem_ld32(t_s + KT, g);
       tmem_wait_ld();
       tc_fence_before();   // S and dP are in registers: the next tile's may overwrite them
       __syncwarp();
@@ -339,7 +337,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (__any_sync(0xffffffffu, inside)) {   // the same in the warp of the other half
         uint64_t sum = f2_pack(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 64; i += 2)
+        for (int i = 0; i < 32; i += 2)
           sum = f2_fma(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
                        f2_pack(__uint_as_float(g[i]), __uint_as_float(g[i + 1])), sum);
         float a0, a1;
@@ -355,9 +353,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         if (inside) delta = buf[rr] + buf[128 + rr];
       }
       const uint64_t nd2 = f2_pack(-delta, -delta);
-      uint32_t ds[32];
+      uint32_t ds[16];
 #pragma unroll
-      for (int i = 0; i < 64; i += 2) {
+      for (int i = 0; i < 32; i += 2) {
         const uint64_t x = f2_add(f2_pack(__uint_as_float(g[i]), __uint_as_float(g[i + 1])), nd2);
         float d0, d1;
         f2_unpack(f2_mul(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), x), d0, d1);
@@ -368,7 +366,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         if (!ok) break;
         tc_fence_after();
       }
-      tmem_st32(tmem + lane_off + 448 + half * 32, ds);
+      tmem_st16(tmem + lane_off + Cfg::kColDs + half * 16, ds);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -388,7 +386,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       for (int cc = 0; cc < W / 64; ++cc) {
         uint32_t o[32];
         if (n > 0) {
-          tmem_ld32(tmem + lane_off + 256 + half * (W / 2) + cc * 32, o);
+          tmem_ld32(tmem + lane_off + Cfg::kColDq + half * (W / 2) + cc * 32, o);
           tmem_wait_ld();
         } else {
 #pragma unroll
@@ -492,11 +490,14 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the dQ kernel's L, D and ranges
   if (threadIdx.x == 0) {
     mbar_arrive_expect_tx(kv_full, (Cfg::kKChunks + Cfg::kVChunks) * CB);
-    for (int c = 0; c < Cfg::kVChunks; ++c) {
-      tma_load_4d(sbase + c * CB, &p.tm_k, kv_full, c * kChunk, kv0, h, b);
-      tma_load_4d(sbase + Cfg::kOffV + c * CB, &p.tm_v, kv_full, c * kChunk, kv0, h, b);
+    for (int r = 0; r < 2; ++r) {   // boxes of 64 rows
+      const int y = kv0 + r * 64, at = r * (CB / 2);
+      for (int c = 0; c < Cfg::kVChunks; ++c) {
+        tma_load_4d(sbase + c * CB + at, &p.tm_k, kv_full, c * kChunk, y, h, b);
+        tma_load_4d(sbase + Cfg::kOffV + c * CB + at, &p.tm_v, kv_full, c * kChunk, y, h, b);
+      }
+      tma_load_4d(sbase + Cfg::kVChunks * CB + at, &p.tm_kr, kv_full, 0, y, 0, b);
     }
-    tma_load_4d(sbase + Cfg::kVChunks * CB, &p.tm_kr, kv_full, 0, kv0, 0, b);
   }
   // the steps with a row whose span reaches into the tile, and those between them
   {
@@ -581,8 +582,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         if (elect_one()) {
           mma_ts_steps<4, false, 0>(tmem, tmem + 448, ob, idesc_v, g > 0 ? 1u : 0u);
           mma_ts_steps<4, false, 0>(tmem + 128, tmem + 480, qb, idesc_k, g > 0 ? 1u : 0u);
-          tc_commit(kd_done);
           tc_commit(empty(g % NS));
+          tc_commit(kd_done);
         }
       }
       if (!ok) {

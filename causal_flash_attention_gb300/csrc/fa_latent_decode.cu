@@ -318,8 +318,8 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       const uint64_t xb = make_sdesc(sbase + Cfg::kOffX + xt.slot * CB, 16, 1024);
       if (elect_one()) {
         mma_ss_steps<4, true, Cfg::kQB, true, CB>(d, qa + 2 * kPairs * (Cfg::kQB >> 4), xb, idesc_s, 1u);
-        tc_commit(s_full(gs & 1));
         tc_commit(x_empty(xt.slot));
+        tc_commit(s_full(gs & 1));
       }
       xt.next();
       first_of[gs & 1] = begins;

@@ -238,18 +238,24 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
       const uint64_t ring = make_sdesc(sbase + Cfg::kOffRing, 16, 1024);   // K-major
       const uint64_t ring_mn = make_sdesc(sbase + Cfg::kOffRing, CB, 1024);
       constexpr uint64_t kSlot = CB >> 4;
-      auto issue_qk = [&](int t) {   // S_t = Q_t K^T
+      // Commits that free slots come before one that a softmax warp waits for before the CTA's end:
+      // a commit that arrived after the CTA had exited would be a fault. (Where a step issues
+      // nothing, slots are freed by a plain arrival.)
+      auto issue_qk = [&](int t, uint32_t freed) {   // S_t = Q_t K^T; freed: the slots' barrier, or 0
         const uint64_t qa = make_sdesc(sbase + t * Cfg::kKBytes, 16, 1024);
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
           const uint64_t kb = ring + k_slot[c] * kSlot;
           if (elect_one()) {
             mma_ss_steps<4, true, CB, true, CB>(tmem + t * 128, qa + c * kSlot, kb, idesc_qk, c > 0 ? 1u : 0u);
-            if (c == KC - 1) tc_commit(s_full(t));
+            if (c == KC - 1) {
+              if (freed) tc_commit(freed);
+              tc_commit(s_full(t));
+            }
           }
         }
       };
-      auto issue_pv = [&](int t, bool more) {   // O_t (+)= P_t V
+      auto issue_pv = [&](int t, bool more, uint32_t freed) {   // O_t (+)= P_t V
         const uint32_t o_t = tmem + 128 * T + t * 128;
         const uint32_t p_t = Cfg::kSepP ? o_t + D : tmem + t * 128;
         if (VC == 2 && v_slot[VC - 1] == 0) {   // the tile's chunks are not next to each other
@@ -257,53 +263,49 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
           if (elect_one()) {
             mma_ts_steps<8, false, 0>(o_t, p_t, v0, make_idesc(128, 64, kBf16, false, true), more ? 1u : 0u);
             mma_ts_steps<8, false, 0>(o_t + 64, p_t, v1, make_idesc(128, 64, kBf16, false, true), more ? 1u : 0u);
+            if (freed) tc_commit(freed);
             tc_commit(pv_done(t));
           }
         } else {
           const uint64_t vb = ring_mn + v_slot[0] * kSlot;
           if (elect_one()) {
             mma_ts_steps<8, false, 0>(o_t, p_t, vb, idesc_pv, more ? 1u : 0u);
+            if (freed) tc_commit(freed);
             tc_commit(pv_done(t));
           }
         }
       };
-      auto commit = [&](uint32_t bar) {
-        if (elect_one()) tc_commit(bar);
+      // (a tile that no row of either query tile wants is waited for all the same, so that none is
+      // in flight at the end)
+      auto skip = [&](uint32_t freed) {
+        if (elect_one()) mbar_arrive(freed);
       };
       if (ok) ok = wait(k_full(0), 0);
       if (ok) {
         tc_fence_after();
         take(k_slot);
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-          if (active(t, 0)) issue_qk(t);
-        commit(k_empty(0));
+        if (T == 2 && active(0, 0)) issue_qk(0, active(1, 0) ? 0 : k_empty(0));
+        if (active(T - 1, 0)) issue_qk(T - 1, k_empty(0));
       }
       for (int j = 0; ok && j < n_load; ++j) {
         const bool last_tile = j + 1 == n_load;
-        // a tile that no row of either query tile wants is waited for all the same, so that none is
-        // in flight at the end
+        const uint32_t v_freed = v_empty(j & 1), k_freed = k_empty((j + 1) & 1);
         auto next_k = [&]() -> bool {
           if (!last_tile) take(k_slot);
           return last_tile || wait(k_full((j + 1) & 1), ((j + 1) >> 1) & 1);
         };
         if constexpr (Cfg::kSepP) {   // S of the next tile once S has been read, then P V
-          const bool now = active(0, j), then = active(0, j + 1);
+          const uint32_t n = j - first[0];
           if (!(ok = next_k())) break;
-          if (then) {
-            if (now && !(ok = wait(s_free, (j - first[0]) & 1))) break;
+          if (!last_tile) {
+            if (!(ok = wait(s_free, n & 1))) break;
             tc_fence_after();
-            issue_qk(0);
+            issue_qk(0, k_freed);
           }
-          if (!last_tile) commit(k_empty((j + 1) & 1));
           take_v();
-          if (!(ok = wait(v_full(j & 1), (j >> 1) & 1))) break;
-          if (now) {
-            if (!(ok = wait(p_full(0), (j - first[0]) & 1))) break;
-            tc_fence_after();
-            issue_pv(0, j > first[0]);
-          }
-          commit(v_empty(j & 1));
+          if (!(ok = wait(v_full(j & 1), (j >> 1) & 1) && wait(p_full(0), n & 1))) break;
+          tc_fence_after();
+          issue_pv(0, n > 0, v_freed);
         } else {   // P_t V, then S_t of the next tile over P_t, for either query tile in turn
           take_v();
           if (!(ok = wait(v_full(j & 1), (j >> 1) & 1))) break;
@@ -312,13 +314,15 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
           for (int t = 0; t < T; ++t) {
             const bool now = active(t, j), then = active(t, j + 1);
             const int n = j - first[t];   // tiles of this query tile before j
+            // the last user of V_j, and of K_(j+1), frees its slots
+            const bool ends_v = t == T - 1 || !active(T - 1, j), ends_k = t == T - 1 || !active(T - 1, j + 1);
             if (now) {
               if (!(ok = wait(p_full(t), n & 1))) break;
               tc_fence_after();
-              issue_pv(t, n > 0);
+              issue_pv(t, n > 0, ends_v ? v_freed : 0);
+            } else if (t == T - 1 && !active(0, j)) {
+              skip(v_freed);
             }
-            // (a commit covers all that was issued before it: V's comes before the next S)
-            if (t == T - 1) commit(v_empty(j & 1));
             if (!k_seen && (t == T - 1 || then)) {
               if (!(ok = next_k())) break;
               k_seen = true;
@@ -326,16 +330,17 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
             if (then) {
               if (now && !(ok = wait(pv_done(t), n & 1))) break;   // P_t V has read P_t
               tc_fence_after();
-              issue_qk(t);
+              issue_qk(t, ends_k ? k_freed : 0);
+            } else if (t == T - 1 && !last_tile && !active(0, j + 1)) {
+              skip(k_freed);
             }
           }
           if (!ok) break;
-          if (!last_tile) commit(k_empty((j + 1) & 1));
         }
       }
       if (!ok) {
         // every MMA issued so far must finish before the TMEM is released
-        commit(drain);
+        if (elect_one()) tc_commit(drain);
         drain_wait_l(drain, 0, p.status);
       }
       __syncwarp();
