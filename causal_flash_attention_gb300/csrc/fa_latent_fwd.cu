@@ -174,12 +174,16 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
       auto is_k = [](int u) { return Cfg::kSepP ? u == 0 || u % 2 == 1 : u % 2 == 0; };
       auto tile_of = [&](int u) { return Cfg::kSepP ? (u == 0 ? 0 : is_k(u) ? (u + 1) / 2 : u / 2 - 1) : u / 2; };
       const int n_units = 2 * n_load + (Cfg::kSepP ? 1 : 0);   // (with a K past the last tile, skipped)
-      int slot = 0, used = 0, oldest = 0, jk = 0, jv = 0;   // jk, jv: K and V tiles issued
+      // At most three units are out at once: each pair of
+      // barriers serves every other tile, and a copy announced on a barrier whose phase still waits
+      // for bytes of the tile two before it would be a second arrival of a phase that expects one.
+      // (The slots alone do not see to that where the last tiles' V follow one another.)
+      int slot = 0, used = 0, held = 0, oldest = 0, jk = 0, jv = 0;   // jk, jv: K and V tiles issued
       for (int u = 0; u < n_units; ++u) {
         const int j = tile_of(u), n = is_k(u) ? KC : VC;
         if (j >= n_load) continue;
         bool ok = true;
-        for (; used + n > NS; ++oldest) {
+        for (; used + n > NS || held == 3; ++oldest, --held) {
           const int o = tile_of(oldest);
           if (!(ok = mbar_wait(is_k(oldest) ? k_empty(o & 1) : v_empty(o & 1), (o >> 1) & 1, abort_flag, p.status))) break;
           used -= is_k(oldest) ? KC : VC;
@@ -196,6 +200,7 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
           slot = slot + 1 == NS ? 0 : slot + 1;
         }
         used += n;
+        ++held;
         if (is_k(u)) ++jk;
         else ++jv;
       }
