@@ -51,10 +51,11 @@ struct LatentFwdParams {
 struct LatentBwdParams {
   CUtensorMap tm_q;    // 4-D (d + 64, Sq, H, B), box (64, 64, 1, 1), 128B swizzle
   CUtensorMap tm_do;   // (d, Sq, H, B), box of 64 rows
+  CUtensorMap tm_o;    // as tm_do
   CUtensorMap tm_k;    // (d, Skv, H, B), as the rest
   CUtensorMap tm_kr;   // (64, Skv, 1, B)
   CUtensorMap tm_v;    // (d, Skv, H, B)
-  HeadView q, out, dout, dq, dk, dk_rope, dv;
+  HeadView out, dout, dq, dk, dk_rope, dv;
   const float* lse;    // [B*H][Sq]
   float* lse2;         // [B*H][Sq_pad]  LSE log2(e), +inf on rows that see nothing
   float* delta;        // [B*H][Sq_pad]  <dO, O>

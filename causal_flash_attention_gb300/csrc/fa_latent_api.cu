@@ -180,8 +180,8 @@ int fa_bwd_latent(const fa_view* q, const fa_view* k, const fa_view* k_rope, con
   if (rc != FA_OK) return rc;
   LatentBwdParams p;
   std::memset(&p, 0, sizeof(p));
-  HeadView vk, vr, vv;
-  if ((rc = take({{q, H, Sq, &p.q}, {k, H, Skv, &vk}, {k_rope, 1, Skv, &vr}, {v, H, Skv, &vv}, {out, H, Sq, &p.out},
+  HeadView vq, vk, vr, vv;
+  if ((rc = take({{q, H, Sq, &vq}, {k, H, Skv, &vk}, {k_rope, 1, Skv, &vr}, {v, H, Skv, &vv}, {out, H, Sq, &p.out},
                   {dout, H, Sq, &p.dout}, {dq, H, Sq, &p.dq}, {dk, H, Skv, &p.dk}, {dk_rope, 1, Skv, &p.dk_rope},
                   {dv, H, Skv, &p.dv}}, B, dtype)) != FA_OK)
     return rc;
@@ -191,7 +191,8 @@ int fa_bwd_latent(const fa_view* q, const fa_view* k, const fa_view* k_rope, con
   if (!workspace || workspace_bytes < w.total) return FA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return FA_ERR_ALIGN;
   const bool bf16 = dtype == FA_BF16;
-  if (!make_map(&p.tm_q, p.q, B, H, Sq, d + kRope, 64, bf16) || !make_map(&p.tm_do, p.dout, B, H, Sq, d, 64, bf16) ||
+  if (!make_map(&p.tm_q, vq, B, H, Sq, d + kRope, 64, bf16) || !make_map(&p.tm_do, p.dout, B, H, Sq, d, 64, bf16) ||
+      !make_map(&p.tm_o, p.out, B, H, Sq, d, 64, bf16) ||
       !make_map(&p.tm_k, vk, B, H, Skv, d, 64, bf16) || !make_map(&p.tm_kr, vr, B, 1, Skv, kRope, 64, bf16) ||
       !make_map(&p.tm_v, vv, B, H, Skv, d, 64, bf16))
     return FA_ERR_TMA;

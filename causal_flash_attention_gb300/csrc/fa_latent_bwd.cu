@@ -81,10 +81,15 @@ struct LatDqCfg {
   static constexpr int kKChunks = kW / kChunk, kVChunks = D / kChunk;
   static constexpr int CB = kKeys * 128;
   static constexpr int kStageBytes = (kKChunks + kVChunks) * CB;   // K', then V
-  static constexpr int NS = 5;
+  static constexpr int NS = D == 128 ? 5 : 6;
   static constexpr int kOffBar = NS * kStageBytes;
-  // full[], empty[], s_full, dp_full, s_free, ds_full, dq_done, drain, swap[4]
-  static constexpr int kNumBars = 2 * NS + 10;
+  // the rows of O, Q and dO pass through the last stages on their way in
+  static constexpr int kFirst = 2;                      // stages for the first tiles meanwhile
+  static constexpr int RB = kTileM * 128;               // a chunk of 128 rows
+  static constexpr int kOffO = kFirst * kStageBytes, kOffQ = kOffO + kVChunks * RB, kOffDO = kOffQ + kKChunks * RB;
+  static_assert(kOffDO + kVChunks * RB <= NS * kStageBytes, "O, Q and dO in the ring");
+  // full[], empty[], s_full, dp_full, s_free, dp_free, ds_full, dq_done, drain, q_full, swap[4]
+  static constexpr int kNumBars = 2 * NS + 12;
   static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kOffSpan = kOffMisc + 16;        // 4 warps' (begin, end)
   static constexpr int kOffDelta = kOffSpan + 32;       // two buffers of [2][128] halves of D
@@ -115,9 +120,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (NS + s); };
   const uint32_t s_full = bar0 + 8 * 2 * NS;
-  const uint32_t dp_full = s_full + 8, s_free = s_full + 16, ds_full = s_full + 24;
-  const uint32_t dq_done = s_full + 32, drain = s_full + 40;
-  auto swap = [&](int quarter) { return s_full + 48 + 8 * quarter; };
+  const uint32_t dp_full = s_full + 8, s_free = s_full + 16, dp_free = s_full + 24, ds_full = s_full + 32;
+  const uint32_t dq_done = s_full + 40, drain = s_full + 48, q_full = s_full + 56;
+  auto swap = [&](int quarter) { return s_full + 64 + 8 * quarter; };
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(warp_id()), 0);
   const int lane = static_cast<int>(lane_id());
@@ -142,12 +147,26 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
     mbar_init(s_free, 8);   // one arrival per compute warp
+    mbar_init(dp_free, 8);
     mbar_init(ds_full, 8);
     mbar_init(dq_done, 1);
     mbar_init(drain, 1);
+    mbar_init(q_full, 1);
     for (int i = 0; i < 4; ++i) mbar_init(swap(i), 2);   // the two warps of a lane quarter
     *abort_flag = 0;
     fence_mbar_init();
+    // rows past Sq come as zeros
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    mbar_arrive_expect_tx(q_full, (Cfg::kKChunks + 2 * Cfg::kVChunks) * Cfg::RB);
+    for (int r = 0; r < 2; ++r) {
+      const int y = q0 + r * 64, at = r * (Cfg::RB / 2);
+      for (int c = 0; c < Cfg::kKChunks; ++c)
+        tma_load_4d(sbase + Cfg::kOffQ + c * Cfg::RB + at, &p.tm_q, q_full, c * kChunk, y, h, b);
+      for (int c = 0; c < Cfg::kVChunks; ++c) {
+        tma_load_4d(sbase + Cfg::kOffDO + c * Cfg::RB + at, &p.tm_do, q_full, c * kChunk, y, h, b);
+        tma_load_4d(sbase + Cfg::kOffO + c * Cfg::RB + at, &p.tm_o, q_full, c * kChunk, y, h, b);
+      }
+    }
     tma_prefetch_desc(&p.tm_k);
     tma_prefetch_desc(&p.tm_kr);
     tma_prefetch_desc(&p.tm_v);
@@ -179,40 +198,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   const int tile0 = hi > 0 ? lo / KT : 0;
   const int n = hi > 0 ? (hi + KT - 1) / KT - tile0 : 0;
 
-  if (warp >= 2) {
-    // this thread's halves of its row of Q and dO into tensor memory, its half of D, and L
-    constexpr int QW = W / 4, OW = D / 4;   // words of a half
-    uint32_t qw[QW], ow[OW];
-    float d = 0.f;
-#pragma unroll
-    for (int i = 0; i < QW; ++i) qw[i] = 0u;
-#pragma unroll
-    for (int i = 0; i < OW; ++i) ow[i] = 0u;
-    if (row < p.mask.Sq) {
-      auto at = [&](const HeadView& v, int e) {
-        return reinterpret_cast<const uint4*>(static_cast<const Elem*>(v.data) + b * v.sb + h * v.sh + row * v.ss + e);
-      };
-      const uint4 *q = at(p.q, half * (W / 2)), *g = at(p.dout, half * (D / 2)), *o = at(p.out, half * (D / 2));
-#pragma unroll
-      for (int u = 0; u < QW / 4; ++u) *reinterpret_cast<uint4*>(qw + 4 * u) = q[u];
-#pragma unroll
-      for (int u = 0; u < OW / 4; ++u) *reinterpret_cast<uint4*>(ow + 4 * u) = g[u];
-#pragma unroll
-      for (int u = 0; u < OW / 4; ++u) d = dot16<kBf16>(o[u], *reinterpret_cast<const uint4*>(ow + 4 * u), d);
-      l2 = p.lse[static_cast<size_t>(bh) * p.mask.Sq + row] * kLog2eB;
-      if (row_hi == 0) l2 = INFINITY;   // sees nothing: P = 0
-    }
-#pragma unroll
-    for (int i = 0; i < QW / 16; ++i)
-      tmem_st16(tmem + lane_off + Cfg::kColQ + half * QW + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(qw + 16 * i));
-#pragma unroll
-    for (int i = 0; i < OW / 16; ++i)
-      tmem_st16(tmem + lane_off + Cfg::kColDO + half * OW + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(ow + 16 * i));
-    halves[half * 128 + rr] = d;
-    tmem_wait_st();
-  }
-  if (warp == 0 && lane == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-  // the first tiles are on their way meanwhile
   auto load = [&](int j) {
     const uint32_t f = full(j % NS), dst = sbase + (j % NS) * Cfg::kStageBytes;
     const int y = (tile0 + j) * KT;
@@ -224,7 +209,40 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     tma_load_4d(dst + Cfg::kVChunks * CB, &p.tm_kr, f, 0, y, 0, b);
   };
   if (warp == 0 && lane == 0)
-    for (int j = 0; j < min(n, NS); ++j) load(j);
+    for (int j = 0; j < min(n, Cfg::kFirst); ++j) load(j);
+  bool ok = true;
+  if (warp >= 2) {
+    // this thread's halves of its row of Q and dO into tensor memory, its half of D, and L
+    if (row < p.mask.Sq && row_hi > 0) l2 = p.lse[static_cast<size_t>(bh) * p.mask.Sq + row] * kLog2eB;
+    // (one outcome for the warp, as for every wait: tensor-memory instructions have to find it whole)
+    ok = warp_wait(q_full, 0, abort_flag, p.status);
+    constexpr int QU = W / 16, OU = D / 16;   // 16-byte units of a half row
+    auto unit = [&](int off, int u) {   // unit u of this row, chunks of 128 rows with the 128-byte swizzle
+      return *reinterpret_cast<const uint4*>(smem + off + (u >> 3) * Cfg::RB + rr * 128 + (((u & 7) ^ (rr & 7)) << 4));
+    };
+    auto put = [&](uint32_t col, int off, int first, auto units) {
+      constexpr int N = decltype(units)::value;
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 v = unit(off, first + i + k);
+          w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+        }
+        tmem_st16(tmem + lane_off + col + (first + i) * 4, w);
+      }
+    };
+    put(Cfg::kColQ, Cfg::kOffQ, half * QU, std::integral_constant<int, QU>{});
+    put(Cfg::kColDO, Cfg::kOffDO, half * OU, std::integral_constant<int, OU>{});
+    float d = 0.f;
+#pragma unroll
+    for (int u = 0; u < OU; ++u)
+      d = dot16<kBf16>(unit(Cfg::kOffO, half * OU + u), unit(Cfg::kOffDO, half * OU + u), d);
+    halves[half * 128 + rr] = d;
+    tmem_wait_st();
+    fence_proxy_async_smem();   // the copies that follow into these stages come after the reads
+  }
   tc_fence_before();
   __syncthreads();   // Q, dO and the halves of D
   tc_fence_after();
@@ -232,13 +250,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   if (warp == 0) {
     // ===================== TMA producer =====================
     if (lane == 0) {
-      int j = min(n, NS);
+      int j = min(n, Cfg::kFirst);
       for (; j < n; ++j) {
-        if (!mbar_wait(empty(j % NS), (j / NS - 1) & 1, abort_flag, p.status)) break;
+        if (j >= NS && !mbar_wait(empty(j % NS), (j / NS - 1) & 1, abort_flag, p.status)) break;
         load(j);
       }
-      if (*abort_flag)   // let every copy already issued land before the CTA releases its memory
+      if (*abort_flag) {   // let every copy already issued land before the CTA releases its memory
+        drain_wait_b(q_full, 0, p.status);
         for (int i = max(0, j - NS); i < j; ++i) drain_wait_b(full(i % NS), (i / NS) & 1, p.status);
+      }
     }
   } else if (warp == 1) {
     // ===================== MMA issuer (the whole warp, one lane of it the MMAs) =====================
@@ -246,7 +266,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       constexpr uint32_t idesc_s = make_idesc(128, KT, kBf16, false, false);
       constexpr uint32_t idesc_q = make_idesc(128, W, kBf16, false, true);
       auto wait = [&](uint32_t bar, uint32_t parity) { return warp_wait(bar, parity, abort_flag, p.status); };
-      bool ok = true;
 #ifdef FA_WAIT_TEST
       // wait-limit test build: nothing completes this phase before the abort
       // path's own commit, so the wait runs out
@@ -258,14 +277,16 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         tc_fence_after();
         const uint32_t st = sbase + (j % NS) * Cfg::kStageBytes;
         const uint64_t kb = make_sdesc(st, 16, 1024), vb = make_sdesc(st + Cfg::kKChunks * CB, 16, 1024);
-        if (elect_one()) {
+        elected([&] {
           mma_ts_steps<W / 16, true, CB>(tmem, tmem + Cfg::kColQ, kb, idesc_s, 0u);
           tc_commit(s_full);
-        }
-        if (elect_one()) {
+        });
+        if (j > 0 && !wait(dp_free, (j - 1) & 1)) return false;
+        tc_fence_after();
+        elected([&] {
           mma_ts_steps<D / 16, true, CB>(tmem + KT, tmem + Cfg::kColDO, vb, idesc_s, 0u);
           tc_commit(dp_full);
-        }
+        });
         return true;
       };
       if (ok) ok = scores(0);
@@ -274,15 +295,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         if (!(ok = wait(ds_full, j & 1))) break;
         tc_fence_after();
         const uint64_t kb = make_sdesc(sbase + (j % NS) * Cfg::kStageBytes, CB, 1024);
-        if (elect_one()) {
+        elected([&] {
           mma_ts_steps<KT / 16, false, 0>(tmem + Cfg::kColDq, tmem + Cfg::kColDs, kb, idesc_q, j > 0 ? 1u : 0u);
           tc_commit(empty(j % NS));   // (before the one that is waited for at the end: a commit
           tc_commit(dq_done);         // that arrived after the CTA had exited would be a fault)
-        }
+        });
       }
       if (!ok) {
         // every MMA issued so far must finish before the TMEM is released
-        if (elect_one()) tc_commit(drain);
+        elected([&] { tc_commit(drain); });
         drain_wait_b(drain, 0, p.status);
       }
       __syncwarp();
@@ -298,17 +319,19 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     }
     const uint32_t t_s = tmem + lane_off + half * 32;
     const float c = p.scale_log2;
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
+    for (int j = 0; ok && j < n; ++j) {
       ok = __all_sync(0xffffffffu, mbar_wait(s_full, j & 1, abort_flag, p.status));
       if (!ok) break;
       tc_fence_after();
       uint32_t s[32], g[32];
       tmem_ld32(t_s, s);
       tmem_wait_ld();
+      tc_fence_before();   // S is in registers: the next tile's may overwrite it
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_free);
       const int tile_k0 = (tile0 + j) * KT, k0 = tile_k0 + half * 32;
       const bool inside = row_hi > 0 && row_lo >= tile_k0 && row_hi <= tile_k0 + KT;
-      if (k0 < row_lo || k0 + 32 > row_hi) {
+      if (__any_sync(0xffffffffu, k0 < row_lo || k0 + 32 > row_hi)) {
         const uint32_t see = span_bits(row_lo, row_hi, k0);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -327,9 +350,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       tc_fence_after();
       tmem_ld32(t_s + KT, g);
       tmem_wait_ld();
-      tc_fence_before();   // S and dP are in registers: the next tile's may overwrite them
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(s_free);
+      if (lane == 0) mbar_arrive(dp_free);
       // A row whose keys all lie in this tile takes D = sum_j P dP from here, in fp32. From the
       // rounded O it is off by half a step of |dO| |O|, which for rows of few keys, the ones with
       // the largest gradients, counts as much as rounding dS does: dQ's and dK's errors at packed
@@ -385,6 +408,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 #pragma unroll
       for (int cc = 0; cc < W / 64; ++cc) {
         uint32_t o[32];
+        __syncwarp();
         if (n > 0) {
           tmem_ld32(tmem + lane_off + Cfg::kColDq + half * (W / 2) + cc * 32, o);
           tmem_wait_ld();
@@ -562,14 +586,14 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         tc_fence_after();
         const uint32_t st = sbase + Cfg::kOffQ + (g % NS) * Cfg::kStageBytes;
         const uint64_t qb = make_sdesc(st, 16, 1024), ob = make_sdesc(st + Cfg::kKChunks * QB, 16, 1024);
-        if (elect_one()) {
+        elected([&] {
           mma_ss_steps<4 * Cfg::kKChunks, true, CB, true, QB>(tmem + 320, ka, qb, idesc_s, 0u);
           tc_commit(s_full);
-        }
-        if (elect_one()) {
+        });
+        elected([&] {
           mma_ss_steps<4 * Cfg::kVChunks, true, CB, true, QB>(tmem + 384, va, ob, idesc_s, 0u);
           tc_commit(dp_full);
-        }
+        });
         return true;
       };
       if (ok) ok = scores(0);
@@ -579,15 +603,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         tc_fence_after();
         const uint32_t st = sbase + Cfg::kOffQ + (g % NS) * Cfg::kStageBytes;
         const uint64_t qb = make_sdesc(st, QB, 1024), ob = make_sdesc(st + Cfg::kKChunks * QB, QB, 1024);
-        if (elect_one()) {
+        elected([&] {
           mma_ts_steps<4, false, 0>(tmem, tmem + 448, ob, idesc_v, g > 0 ? 1u : 0u);
           mma_ts_steps<4, false, 0>(tmem + 128, tmem + 480, qb, idesc_k, g > 0 ? 1u : 0u);
           tc_commit(empty(g % NS));
           tc_commit(kd_done);
-        }
+        });
       }
       if (!ok) {
-        if (elect_one()) tc_commit(drain);
+        elected([&] { tc_commit(drain); });
         drain_wait_b(drain, 0, p.status);
       }
       __syncwarp();
@@ -606,7 +630,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     for (int g = 0; g < n; ++g) {
       const int st = g % NS;
       uint32_t vis = 0xffffffffu;   // bit e: this lane's key is seen by query column e
-      if (__any_sync(0xffffffffu, sp.x > key0 || sp.y < key0 + 32))
+      const bool masked = __any_sync(0xffffffffu, sp.x > key0 || sp.y < key0 + 32);
+      if (masked)
         vis = transpose_bits(span_bits(sp.x, sp.y, key0), lane);
       if (g + 1 < n) sp = span_of(g + 1);
       ok = __all_sync(0xffffffffu, mbar_wait(full(st), (g / NS) & 1, abort_flag, p.status) &&
@@ -617,7 +642,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       uint32_t s[32];
       tmem_ld32(t_s, s);
       tmem_wait_ld();
-      if (vis != 0xffffffffu) {
+      if (masked) {
 #pragma unroll
         for (int e = 0; e < 32; ++e)
           if (!((vis >> e) & 1u)) s[e] = __float_as_uint(-INFINITY);
@@ -676,6 +701,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       const float f = half == 0 ? p.scale : 1.f;
       Elem* dst = static_cast<Elem*>(v.data) + b * v.sb + h * v.sh + key * v.ss;
       auto load = [&](int col, uint32_t (&o)[32]) {
+        __syncwarp();
         if (n > 0) {
           tmem_ld32(tmem + lane_off + col, o);
           tmem_wait_ld();

@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     const uint64_t pb = make_sdesc(sbase + Cfg::kOffP, 16, 1024);
     auto ready = [](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)); };
     // (votes make what was loaded the same in every lane for the compiler too, and with it the
-    // control flow and the descriptors: elect_one)
+    // control flow and the descriptors: elected)
     bool first_s = false;
     auto next = [&]() {
       const bool more = __all_sync(0xffffffffu, walk.next(p));
@@ -264,11 +264,11 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 #pragma unroll
       for (int m = 0; m < kPairs; ++m) {   // a part a pair
         const uint64_t ca = make_sdesc(sbase + Cfg::kOffC + at_o.slot * 2 * CB, CB, 1024);
-        if (elect_one()) {
+        elected([&] {
           mma_ss_steps<kTile / 16, false, 0, true, Cfg::kP>(o_t + m * NR, ca, pb, idesc_o, more);
           tc_commit(empty(at_o.slot));
           if (m == kPairs - 1) tc_commit(pv_done);
-        }
+        });
         at_o.next();
       }
       ++go;
@@ -311,16 +311,15 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 #pragma unroll
       for (int m = 0; m < kPairs; ++m) {
         const uint64_t cb = make_sdesc(sbase + Cfg::kOffC + at_s.slot * 2 * CB, 16, 1024);
-        if (elect_one())
-          mma_ss_steps<8, true, Cfg::kQB, true, CB>(d, qa + 2 * m * (Cfg::kQB >> 4), cb, idesc_s, m > 0 ? 1u : 0u);
+        elected([&] { mma_ss_steps<8, true, Cfg::kQB, true, CB>(d, qa + 2 * m * (Cfg::kQB >> 4), cb, idesc_s, m > 0 ? 1u : 0u); });
         at_s.next();
       }
       const uint64_t xb = make_sdesc(sbase + Cfg::kOffX + xt.slot * CB, 16, 1024);
-      if (elect_one()) {
+      elected([&] {
         mma_ss_steps<4, true, Cfg::kQB, true, CB>(d, qa + 2 * kPairs * (Cfg::kQB >> 4), xb, idesc_s, 1u);
         tc_commit(x_empty(xt.slot));
         tc_commit(s_full(gs & 1));
-      }
+      });
       xt.next();
       first_of[gs & 1] = begins;
       ++gs;
@@ -329,7 +328,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     while (ok && go < gs) ok = until(0, 0);
     if (!ok) {
       // every MMA issued so far must finish before the TMEM is released
-      if (elect_one()) tc_commit(drain);
+      elected([&] { tc_commit(drain); });
       drain_wait_d(drain, 0, p.status);
     }
     __syncwarp();
@@ -411,6 +410,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         }
         for (int m = 0; m < kPairs; ++m) at.next();
         float x[kHalf], top = -INFINITY;   // scores, and the greatest in the log2 domain
+        __syncwarp();   // (tensor-memory instructions have to find the warp whole)
         if (busy && ok) {
           const int k0 = kv0 + half * kHalf;
           uint32_t raw[kHalf];
@@ -418,7 +418,8 @@ __global__ void __launch_bounds__(kThreadsD, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < kHalf; ++i) x[i] = __uint_as_float(raw[i]);
-          if (k0 < row_lo || k0 + kHalf > row_hi || (p.tree && k0 + kHalf > keys.len - p.Sq)) {
+          if (__any_sync(0xffffffffu, k0 < row_lo || k0 + kHalf > row_hi) ||
+              (p.tree && k0 + kHalf > keys.len - p.Sq)) {
             uint32_t see = span_bits(row_lo, row_hi, k0);
             if (p.tree) see &= static_cast<uint32_t>(tree_bits(tree, keys.len - p.Sq, k0));
 #pragma unroll
@@ -452,6 +453,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
           if (j > 0) {
             if (real && half == 0) row_f[r] = alpha;
             any(false);
+            __syncwarp();
             tc_fence_after();
             for (int m = half * kOwn; m < (half + 1) * kOwn; ++m)
 #pragma unroll
@@ -511,6 +513,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         row_lse[r] = sum.lse2;
       }
       any(false);
+      __syncwarp();
       tc_fence_after();
       const size_t orow = static_cast<size_t>(b) * p.R + row0;                                  // + row
       const size_t prow = (static_cast<size_t>(share_id) * 2 + (head ? 0 : 1)) * p.R + row0;    // + row
@@ -518,6 +521,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         if (whole) p.lse[orow + tid] = row_lse[tid] * kLn2D;
         else p.part_lse2[prow + tid] = row_lse[tid];
       }
+      __syncwarp();
       for (int cc = 0; cc < rows; cc += 16) {
         float f[16];
 #pragma unroll

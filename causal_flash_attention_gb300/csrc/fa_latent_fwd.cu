@@ -174,10 +174,10 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
       auto is_k = [](int u) { return Cfg::kSepP ? u == 0 || u % 2 == 1 : u % 2 == 0; };
       auto tile_of = [&](int u) { return Cfg::kSepP ? (u == 0 ? 0 : is_k(u) ? (u + 1) / 2 : u / 2 - 1) : u / 2; };
       const int n_units = 2 * n_load + (Cfg::kSepP ? 1 : 0);   // (with a K past the last tile, skipped)
-      // At most three units are out at once: each pair of
-      // barriers serves every other tile, and a copy announced on a barrier whose phase still waits
-      // for bytes of the tile two before it would be a second arrival of a phase that expects one.
-      // (The slots alone do not see to that where the last tiles' V follow one another.)
+      // At most three units are out at once: each pair of barriers serves every other tile, and a
+      // copy announced on a barrier whose phase still waits for bytes of the tile two before it would
+      // be a second arrival of a phase that expects one. (The slots alone do not see to that where
+      // the last tiles' V follow one another.)
       int slot = 0, used = 0, held = 0, oldest = 0, jk = 0, jv = 0;   // jk, jv: K and V tiles issued
       for (int u = 0; u < n_units; ++u) {
         const int j = tile_of(u), n = is_k(u) ? KC : VC;
@@ -243,109 +243,99 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
       const uint64_t ring = make_sdesc(sbase + Cfg::kOffRing, 16, 1024);   // K-major
       const uint64_t ring_mn = make_sdesc(sbase + Cfg::kOffRing, CB, 1024);
       constexpr uint64_t kSlot = CB >> 4;
-      // Commits that free slots come before one that a softmax warp waits for before the CTA's end:
-      // a commit that arrived after the CTA had exited would be a fault. (Where a step issues
-      // nothing, slots are freed by a plain arrival.)
-      auto issue_qk = [&](int t, uint32_t freed) {   // S_t = Q_t K^T; freed: the slots' barrier, or 0
+      auto issue_qk = [&](int t) {   // S_t = Q_t K^T
         const uint64_t qa = make_sdesc(sbase + t * Cfg::kKBytes, 16, 1024);
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
           const uint64_t kb = ring + k_slot[c] * kSlot;
-          if (elect_one()) {
+          elected([&] {
             mma_ss_steps<4, true, CB, true, CB>(tmem + t * 128, qa + c * kSlot, kb, idesc_qk, c > 0 ? 1u : 0u);
-            if (c == KC - 1) {
-              if (freed) tc_commit(freed);
-              tc_commit(s_full(t));
-            }
-          }
+            if (c == KC - 1) tc_commit(s_full(t));
+          });
         }
       };
-      auto issue_pv = [&](int t, bool more, uint32_t freed) {   // O_t (+)= P_t V
+      auto issue_pv = [&](int t, bool more) {   // O_t (+)= P_t V
         const uint32_t o_t = tmem + 128 * T + t * 128;
         const uint32_t p_t = Cfg::kSepP ? o_t + D : tmem + t * 128;
         if (VC == 2 && v_slot[VC - 1] == 0) {   // the tile's chunks are not next to each other
           const uint64_t v0 = ring_mn + v_slot[0] * kSlot, v1 = ring_mn;
-          if (elect_one()) {
+          elected([&] {
             mma_ts_steps<8, false, 0>(o_t, p_t, v0, make_idesc(128, 64, kBf16, false, true), more ? 1u : 0u);
             mma_ts_steps<8, false, 0>(o_t + 64, p_t, v1, make_idesc(128, 64, kBf16, false, true), more ? 1u : 0u);
-            if (freed) tc_commit(freed);
             tc_commit(pv_done(t));
-          }
+          });
         } else {
           const uint64_t vb = ring_mn + v_slot[0] * kSlot;
-          if (elect_one()) {
+          elected([&] {
             mma_ts_steps<8, false, 0>(o_t, p_t, vb, idesc_pv, more ? 1u : 0u);
-            if (freed) tc_commit(freed);
             tc_commit(pv_done(t));
-          }
+          });
         }
       };
-      // (a tile that no row of either query tile wants is waited for all the same, so that none is
-      // in flight at the end)
-      auto skip = [&](uint32_t freed) {
-        if (elect_one()) mbar_arrive(freed);
+      // Slots are freed for the loads still to come only: a commit that arrived after the CTA had
+      // exited would be a fault. (A tile that no row of either query tile wants is waited for all
+      // the same, so that none is in flight at the end.)
+      auto commit = [&](uint32_t bar) {
+        elected([&] { tc_commit(bar); });
       };
       if (ok) ok = wait(k_full(0), 0);
       if (ok) {
         tc_fence_after();
         take(k_slot);
-        if (T == 2 && active(0, 0)) issue_qk(0, active(1, 0) ? 0 : k_empty(0));
-        if (active(T - 1, 0)) issue_qk(T - 1, k_empty(0));
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+          if (active(t, 0)) issue_qk(t);
+        if (n_load > 1) commit(k_empty(0));
       }
       for (int j = 0; ok && j < n_load; ++j) {
         const bool last_tile = j + 1 == n_load;
-        const uint32_t v_freed = v_empty(j & 1), k_freed = k_empty((j + 1) & 1);
-        auto next_k = [&]() -> bool {
-          if (!last_tile) take(k_slot);
-          return last_tile || wait(k_full((j + 1) & 1), ((j + 1) >> 1) & 1);
-        };
         if constexpr (Cfg::kSepP) {   // S of the next tile once S has been read, then P V
           const uint32_t n = j - first[0];
-          if (!(ok = next_k())) break;
           if (!last_tile) {
-            if (!(ok = wait(s_free, n & 1))) break;
+            take(k_slot);
+            if (!(ok = wait(k_full((j + 1) & 1), ((j + 1) >> 1) & 1) && wait(s_free, n & 1))) break;
             tc_fence_after();
-            issue_qk(0, k_freed);
+            issue_qk(0);
+            if (j + 2 < n_load) commit(k_empty((j + 1) & 1));
           }
           take_v();
           if (!(ok = wait(v_full(j & 1), (j >> 1) & 1) && wait(p_full(0), n & 1))) break;
           tc_fence_after();
-          issue_pv(0, n > 0, v_freed);
+          issue_pv(0, n > 0);
+          if (!last_tile) commit(v_empty(j & 1));
         } else {   // P_t V, then S_t of the next tile over P_t, for either query tile in turn
           take_v();
           if (!(ok = wait(v_full(j & 1), (j >> 1) & 1))) break;
-          bool k_seen = false;
+          bool k_seen = last_tile;
 #pragma unroll
           for (int t = 0; t < T; ++t) {
             const bool now = active(t, j), then = active(t, j + 1);
-            const int n = j - first[t];   // tiles of this query tile before j
-            // the last user of V_j, and of K_(j+1), frees its slots
-            const bool ends_v = t == T - 1 || !active(T - 1, j), ends_k = t == T - 1 || !active(T - 1, j + 1);
+            const uint32_t n = j - first[t];   // tiles of this query tile before j
             if (now) {
               if (!(ok = wait(p_full(t), n & 1))) break;
               tc_fence_after();
-              issue_pv(t, n > 0, ends_v ? v_freed : 0);
-            } else if (t == T - 1 && !active(0, j)) {
-              skip(v_freed);
+              issue_pv(t, n > 0);
             }
+            // (a commit covers all that was issued before it: V's comes before the next S)
+            if (t == T - 1 && !last_tile) commit(v_empty(j & 1));
             if (!k_seen && (t == T - 1 || then)) {
-              if (!(ok = next_k())) break;
+              take(k_slot);
+              if (!(ok = wait(k_full((j + 1) & 1), ((j + 1) >> 1) & 1))) break;
               k_seen = true;
             }
             if (then) {
               if (now && !(ok = wait(pv_done(t), n & 1))) break;   // P_t V has read P_t
               tc_fence_after();
-              issue_qk(t, ends_k ? k_freed : 0);
-            } else if (t == T - 1 && !last_tile && !active(0, j + 1)) {
-              skip(k_freed);
+              issue_qk(t);
             }
           }
           if (!ok) break;
+          if (j + 2 < n_load) commit(k_empty((j + 1) & 1));
         }
       }
       if (!ok) {
         // every MMA issued so far must finish before the TMEM is released
-        if (elect_one()) tc_commit(drain);
+        elected([&] { tc_commit(drain); });
         drain_wait_l(drain, 0, p.status);
       }
       __syncwarp();
@@ -384,7 +374,8 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
         if (lane == 0) mbar_arrive(s_free);
       }
       const int kv0 = (tile0 + first[t] + j) * kTileN;
-      if (kv0 < row_lo || kv0 + kTileN > row_hi) {
+      // (branches in front of tensor-memory instructions are the warp's, which have to find it whole)
+      if (__any_sync(0xffffffffu, kv0 < row_lo || kv0 + kTileN > row_hi)) {
 #pragma unroll
         for (int w = 0; w < kTileN / 32; ++w) {
           const uint32_t see = span_bits(row_lo, row_hi, kv0 + w * 32);
@@ -470,6 +461,7 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
 #pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t o[32];
+        __syncwarp();
         if (n > 0) {
           tmem_ld32(o_tmem + cc * 32, o);
           tmem_wait_ld();

@@ -407,13 +407,17 @@ __device__ __forceinline__ void mma_ts_product8(uint32_t d_tmem, uint32_t a_tmem
 // A warp that issues products as a whole: waits have one outcome for the warp (warp_wait), so
 // that control flow and descriptors are the same in every lane, and one elected lane (always
 // the same one: a commit covers its thread's own MMAs) executes the MMAs inside a branch
-// on elect_one(). The compiler then keeps the descriptors in uniform registers, where
+// in elected(). The compiler then keeps the descriptors in uniform registers, where
 // tcgen05.mma takes them from; a loop inside `if (lane == 0)` moves them there for every MMA,
 // 45 cycles of issue each, twice that beside a polling warp on the same scheduler.
-__device__ __forceinline__ bool elect_one() {
+// The warp is whole again after it: lanes that ran ahead of the elected one to the next election
+// would elect another.
+template <class F>
+__device__ __forceinline__ void elected(F&& f) {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
+  if (r) f();
+  __syncwarp();
 }
 // mbar_wait by a whole warp.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
