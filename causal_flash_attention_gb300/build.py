@@ -32,7 +32,7 @@ SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_pair.cu", "fa_bwd.cu", "fa_simt.cu"
            "fa_decode.cu", "fa_ragged.cu", "fa_heads.cu", "fa_latent_api.cu", "fa_latent_fwd.cu",
            "fa_latent_bwd.cu", "fa_latent_decode.cu", "fa_latent_append.cu"]
 HEADERS = ["ptx.cuh", "score_mod.cuh", "span_plan.cuh", "fa_internal.h", "fa_decode.h", "fa_ragged.h", "fa_heads.h",
-           "fa_latent.h", "ragged_shares.cuh",
+           "fa_latent.h", "ragged_shares.cuh", "latent_store.cuh",
            os.path.join("..", "..", "include", "fa.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

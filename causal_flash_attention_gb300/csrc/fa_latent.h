@@ -38,7 +38,7 @@ struct LatentFwdParams {
   CUtensorMap tm_k;    // (d, Skv, H, B)
   CUtensorMap tm_kr;   // (64, Skv, 1, B)
   CUtensorMap tm_v;    // (d, Skv, H, B)
-  HeadView out;        // [B][H][Sq][d]
+  CUtensorMap tm_out;  // (d, Sq, H, B), box (32, 32, 1, 1), 64B swizzle
   float* lse;          // [B*H][Sq]
   LatentMask mask;
   int B, H;
@@ -55,7 +55,11 @@ struct LatentBwdParams {
   CUtensorMap tm_k;    // (d, Skv, H, B), as the rest
   CUtensorMap tm_kr;   // (64, Skv, 1, B)
   CUtensorMap tm_v;    // (d, Skv, H, B)
-  HeadView out, dout, dq, dk, dk_rope, dv;
+  CUtensorMap tm_dq;   // as q, dK, dV as k and v: boxes (32, 32, 1, 1), 64B swizzle
+  CUtensorMap tm_dk;
+  CUtensorMap tm_dv;
+  CUtensorMap tm_part; // fp32 (64, Skv, H, B), box (32, 32, 1, 1), 128B swizzle
+  HeadView dk_rope;
   const float* lse;    // [B*H][Sq]
   float* lse2;         // [B*H][Sq_pad]  LSE log2(e), +inf on rows that see nothing
   float* delta;        // [B*H][Sq_pad]  <dO, O>

@@ -53,22 +53,38 @@ int take(std::initializer_list<ViewOf> views, int B, int dtype) {
   return FA_OK;
 }
 
-// 4-D view (d, S, H, B) of a strided 16-bit tensor; box = 64 columns (128 bytes, one
-// swizzle span) x box_rows rows x box_heads heads.
+// 4-D view (d, S, H, B) of a strided 16-bit tensor; box = box_cols columns (one swizzle span, 128
+// bytes of 64) x box_rows rows x box_heads heads.
 bool make_map(CUtensorMap* m, const HeadView& v, int B, int H, int S, int d, int box_rows, bool bf16,
-              int box_heads = 1) {
+              int box_heads = 1, int box_cols = kChunk) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(S), static_cast<cuuint64_t>(H),
                               static_cast<cuuint64_t>(B)};
   auto bytes = [&](long long stride) { return static_cast<cuuint64_t>(stride > 0 ? stride * 2 : d * 2); };
   const cuuint64_t strides[3] = {bytes(v.ss), bytes(v.sh), bytes(v.sb)};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(kChunk), static_cast<cuuint32_t>(box_rows),
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows),
                              static_cast<cuuint32_t>(box_heads), 1};
   const cuuint32_t one[4] = {1, 1, 1, 1};
   return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, v.data, dims, strides,
-             box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_cols == kChunk ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// The same for stores, in a warp's boxes.
+bool make_store_map(CUtensorMap* m, const HeadView& v, int B, int H, int S, int d, bool bf16) {
+  return make_map(m, v, B, H, S, d, 32, bf16, 1, 32);
+}
+// [B][H][S][64] floats, contiguous, in boxes of 32 x 32.
+bool make_part_map(CUtensorMap* m, float* data, int B, int H, int S) {
+  EncodeTiledFn enc = encode_fn();
+  const cuuint64_t row = kRope * 4, dims[4] = {kRope, static_cast<cuuint64_t>(S), static_cast<cuuint64_t>(H),
+                                               static_cast<cuuint64_t>(B)};
+  const cuuint64_t strides[3] = {row, row * dims[1], row * dims[1] * dims[2]};
+  const cuuint32_t box[4] = {32, 32, 1, 1}, one[4] = {1, 1, 1, 1};
+  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, data, dims, strides, box, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int check_mask(const int* begin, const int* end) {
@@ -145,15 +161,16 @@ int fa_fwd_latent(const fa_view* q, const fa_view* k, const fa_view* k_rope, con
   if (rc != FA_OK) return rc;
   LatentFwdParams p;
   std::memset(&p, 0, sizeof(p));
-  HeadView vq, vk, vr, vv;
-  if ((rc = take({{q, H, Sq, &vq}, {k, H, Skv, &vk}, {k_rope, 1, Skv, &vr}, {v, H, Skv, &vv}, {out, H, Sq, &p.out}},
+  HeadView vq, vk, vr, vv, vo;
+  if ((rc = take({{q, H, Sq, &vq}, {k, H, Skv, &vk}, {k_rope, 1, Skv, &vr}, {v, H, Skv, &vv}, {out, H, Sq, &vo}},
                  B, dtype)) != FA_OK)
     return rc;
   if (!lse) return FA_ERR_NULL;
   if (!aligned(lse, 4)) return FA_ERR_ALIGN;
   const bool bf16 = dtype == FA_BF16;
   if (!make_map(&p.tm_q, vq, B, H, Sq, d + kRope, kTileM, bf16) || !make_map(&p.tm_k, vk, B, H, Skv, d, kTileN, bf16) ||
-      !make_map(&p.tm_kr, vr, B, 1, Skv, kRope, kTileN, bf16) || !make_map(&p.tm_v, vv, B, H, Skv, d, kTileN, bf16))
+      !make_map(&p.tm_kr, vr, B, 1, Skv, kRope, kTileN, bf16) || !make_map(&p.tm_v, vv, B, H, Skv, d, kTileN, bf16) ||
+      !make_store_map(&p.tm_out, vo, B, H, Sq, d, bf16))
     return FA_ERR_TMA;
   p.lse = lse;
   p.mask = LatentMask{key_begin, key_end, Sq, Skv};
@@ -180,28 +197,30 @@ int fa_bwd_latent(const fa_view* q, const fa_view* k, const fa_view* k_rope, con
   if (rc != FA_OK) return rc;
   LatentBwdParams p;
   std::memset(&p, 0, sizeof(p));
-  HeadView vq, vk, vr, vv;
-  if ((rc = take({{q, H, Sq, &vq}, {k, H, Skv, &vk}, {k_rope, 1, Skv, &vr}, {v, H, Skv, &vv}, {out, H, Sq, &p.out},
-                  {dout, H, Sq, &p.dout}, {dq, H, Sq, &p.dq}, {dk, H, Skv, &p.dk}, {dk_rope, 1, Skv, &p.dk_rope},
-                  {dv, H, Skv, &p.dv}}, B, dtype)) != FA_OK)
+  HeadView vq, vk, vr, vv, vo, vg, vdq, vdk, vdv;
+  if ((rc = take({{q, H, Sq, &vq}, {k, H, Skv, &vk}, {k_rope, 1, Skv, &vr}, {v, H, Skv, &vv}, {out, H, Sq, &vo},
+                  {dout, H, Sq, &vg}, {dq, H, Sq, &vdq}, {dk, H, Skv, &vdk}, {dk_rope, 1, Skv, &p.dk_rope},
+                  {dv, H, Skv, &vdv}}, B, dtype)) != FA_OK)
     return rc;
   if (!lse) return FA_ERR_NULL;
   if (!aligned(lse, 4)) return FA_ERR_ALIGN;
   const LatentBwdWs w = bwd_ws(B, H, Sq, Skv);
   if (!workspace || workspace_bytes < w.total) return FA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return FA_ERR_ALIGN;
-  const bool bf16 = dtype == FA_BF16;
-  if (!make_map(&p.tm_q, vq, B, H, Sq, d + kRope, 64, bf16) || !make_map(&p.tm_do, p.dout, B, H, Sq, d, 64, bf16) ||
-      !make_map(&p.tm_o, p.out, B, H, Sq, d, 64, bf16) ||
-      !make_map(&p.tm_k, vk, B, H, Skv, d, 64, bf16) || !make_map(&p.tm_kr, vr, B, 1, Skv, kRope, 64, bf16) ||
-      !make_map(&p.tm_v, vv, B, H, Skv, d, 64, bf16))
-    return FA_ERR_TMA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.part = reinterpret_cast<float*>(ws + w.part);
+  const bool bf16 = dtype == FA_BF16;
+  if (!make_map(&p.tm_q, vq, B, H, Sq, d + kRope, 64, bf16) || !make_map(&p.tm_do, vg, B, H, Sq, d, 64, bf16) ||
+      !make_map(&p.tm_o, vo, B, H, Sq, d, 64, bf16) ||
+      !make_map(&p.tm_k, vk, B, H, Skv, d, 64, bf16) || !make_map(&p.tm_kr, vr, B, 1, Skv, kRope, 64, bf16) ||
+      !make_map(&p.tm_v, vv, B, H, Skv, d, 64, bf16) || !make_store_map(&p.tm_dq, vdq, B, H, Sq, d + kRope, bf16) ||
+      !make_store_map(&p.tm_dk, vdk, B, H, Skv, d, bf16) || !make_store_map(&p.tm_dv, vdv, B, H, Skv, d, bf16) ||
+      !make_part_map(&p.tm_part, p.part, B, H, Skv))
+    return FA_ERR_TMA;
   p.lse = lse;
   p.lse2 = reinterpret_cast<float*>(ws + w.lse2);
   p.delta = reinterpret_cast<float*>(ws + w.delta);
   p.ranges = reinterpret_cast<int2*>(ws + w.ranges);
-  p.part = reinterpret_cast<float*>(ws + w.part);
   p.mask = LatentMask{key_begin, key_end, Sq, Skv};
   p.B = B;
   p.H = H;

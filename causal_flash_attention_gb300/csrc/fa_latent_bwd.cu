@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "fa_latent.h"
+#include "latent_store.cuh"
 #include "ptx.cuh"
 #include "score_mod.cuh"
 
@@ -50,20 +51,6 @@ __device__ __forceinline__ float dot16(const uint4& a, const uint4& b, float s) 
     s = fmaf(u.y, v.y, s);
   }
   return s;
-}
-
-// 32 accumulator columns times f, rounded, to 32 consecutive elements of a row.
-template <bool kBf16>
-__device__ __forceinline__ void store32(void* row, const uint32_t (&o)[32], float f) {
-  uint4* dst = static_cast<uint4*>(row);
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = pack2<kBf16>(__uint_as_float(o[8 * v + 2 * e]) * f, __uint_as_float(o[8 * v + 2 * e + 1]) * f);
-    dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
 }
 
 // --------------------------------------------------------------------- dQ --
@@ -104,7 +91,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     latent_dq_kernel(const __grid_constant__ LatentBwdParams p) {
   using Cfg = LatDqCfg<D>;
   constexpr int NS = Cfg::NS, CB = Cfg::CB, W = Cfg::kW, KT = Cfg::kKeys;
-  using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {   // the 128-byte swizzle needs 1024-byte aligned tiles
@@ -404,20 +390,23 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         p.lse2[at] = l2;
         p.delta[at] = delta;
       }
-      Elem* dst = static_cast<Elem*>(p.dq.data) + b * p.dq.sb + h * p.dq.sh + row * p.dq.ss + half * (W / 2);
+      // through the ring's first stages, which every product has read (or none was loaded into)
+      uint8_t* box = smem + (warp - 2) * (W / 64) * kStoreBytes;
 #pragma unroll
       for (int cc = 0; cc < W / 64; ++cc) {
+        const int col = half * (W / 2) + cc * 32;
         uint32_t o[32];
-        __syncwarp();
         if (n > 0) {
-          tmem_ld32(tmem + lane_off + Cfg::kColDq + half * (W / 2) + cc * 32, o);
+          tmem_ld32(tmem + lane_off + Cfg::kColDq + col, o);
           tmem_wait_ld();
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
-        if (row < p.mask.Sq) store32<kBf16>(dst + cc * 32, o, p.scale);
+        if (row - lane < p.mask.Sq)
+          store_box<kBf16>(box + cc * kStoreBytes, &p.tm_dq, o, p.scale, lane, col, row - lane, h, b);
       }
+      if (lane == 0) bulk_wait_all();
     }
   }
   tc_fence_before();
@@ -444,6 +433,8 @@ struct LatDkvCfg {
   static constexpr int kOffV = kKChunks * CB;           // K' first
   static constexpr int kOffQ = kOffV + kVChunks * CB;   // stages: Q, dO, L, D
   static constexpr int kStageBytes = (kKChunks + kVChunks) * QB;
+  static constexpr int kStoreWarp = (2 + D / 32) * kStoreBytes;   // a warp's results on their way out
+  static_assert(8 * kStoreWarp <= NS * kStageBytes && kStoreWarp % 1024 == 0, "results in the stages");
   static constexpr int kOffRow = kOffQ + NS * kStageBytes;
   static constexpr int kOffBar = kOffRow + NS * 2 * kRows * 4;
   // kv_full, full[], empty[], s_full, dp_full, s_free, ds_full, kd_done, drain
@@ -458,7 +449,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     latent_dkv_kernel(const __grid_constant__ LatentBwdParams p) {
   using Cfg = LatDkvCfg<D>;
   constexpr int NS = Cfg::NS, CB = Cfg::CB, QB = Cfg::QB, W = Cfg::kW, R = Cfg::kRows;
-  using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {
@@ -696,12 +686,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(kd_done, (n - 1) & 1, abort_flag, p.status));
     if (ok) {
       tc_fence_after();
-      // warps 2-5 write dK, warps 6-9 dV, each half the shared part
-      const HeadView& v = half == 0 ? p.dk : p.dv;
+      // warps 2-5 write dK, warps 6-9 dV, each half the shared part, through the stages of Q and dO
+      const CUtensorMap* tm = half == 0 ? &p.tm_dk : &p.tm_dv;
       const float f = half == 0 ? p.scale : 1.f;
-      Elem* dst = static_cast<Elem*>(v.data) + b * v.sb + h * v.sh + key * v.ss;
+      uint8_t* box = smem + Cfg::kOffQ + (warp - 2) * Cfg::kStoreWarp;
       auto load = [&](int col, uint32_t (&o)[32]) {
-        __syncwarp();
         if (n > 0) {
           tmem_ld32(tmem + lane_off + col, o);
           tmem_wait_ld();
@@ -710,19 +699,16 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
       };
-      uint32_t o[32];
+      if (key0 < p.mask.Skv) {
+        uint32_t o[32];
+        load(128 + D + half * 32, o);
+        store_box_f32(box, &p.tm_part, o, lane, half * 32, key0, h, b);
 #pragma unroll
-      for (int cc = 0; cc < D / 32; ++cc) {
-        load((half == 0 ? 128 : 0) + cc * 32, o);
-        if (key < p.mask.Skv) store32<kBf16>(dst + cc * 32, o, f);
-      }
-      load(128 + D + half * 32, o);
-      if (key < p.mask.Skv) {
-        float4* part = reinterpret_cast<float4*>(p.part + (static_cast<size_t>(bh) * p.mask.Skv + key) * kRope + half * 32);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          part[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+        for (int cc = 0; cc < D / 32; ++cc) {
+          load((half == 0 ? 128 : 0) + cc * 32, o);
+          store_box<kBf16>(box + (cc + 2) * kStoreBytes, tm, o, f, lane, cc * 32, key0, h, b);
+        }
+        if (lane == 0) bulk_wait_all();
       }
     }
   }

@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "fa_latent.h"
+#include "latent_store.cuh"
 #include "ptx.cuh"
 #include "score_mod.cuh"
 
@@ -62,7 +63,6 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
     latent_fwd_kernel(const __grid_constant__ LatentFwdParams p) {
   using Cfg = LatFwdCfg<D>;
   constexpr int T = Cfg::T, NS = Cfg::kSlots, CB = Cfg::kChunkBytes, KC = Cfg::kKChunks, VC = Cfg::kVChunks;
-  using Elem = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {   // the 128-byte swizzle needs 1024-byte aligned tiles
@@ -451,37 +451,32 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
 
     if (ok && n > 0)
       ok = __all_sync(0xffffffffu, mbar_wait(pv_done(t), (n - 1) & 1, abort_flag, p.status));
+    // (results leave through the query tile's own memory)
+    if (ok && n == 0) ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag, p.status));
     if (ok) {
       tc_fence_after();
       // a row that sees nothing has O = 0, l = 0 (and only its own span says so: a row of NaN
       // or -infinite scores has no sum either)
       const bool none = row_hi == 0;
       const float inv_l = none ? 0.f : 1.f / l;
-      Elem* orow = static_cast<Elem*>(p.out.data) + b * p.out.sb + h * p.out.sh + row * p.out.ss;
+      uint8_t* box = smem + t * Cfg::kKBytes + quarter * (D / 32) * kStoreBytes;
 #pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t o[32];
-        __syncwarp();
         if (n > 0) {
           tmem_ld32(o_tmem + cc * 32, o);
           tmem_wait_ld();
         }
-        if (row < p.mask.Sq) {
-          uint4* dst = reinterpret_cast<uint4*>(orow + cc * 32);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = none ? 0u : pack2<kBf16>(__uint_as_float(o[8 * v + 2 * e]) * inv_l,
-                                              __uint_as_float(o[8 * v + 2 * e + 1]) * inv_l);
-            dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
+        for (int i = 0; i < 32; ++i)
+          if (none) o[i] = 0u;
+        if (row - lane < p.mask.Sq)
+          store_box<kBf16>(box + cc * kStoreBytes, &p.tm_out, o, inv_l, lane, cc * 32, row - lane, h, b);
       }
       if (row < p.mask.Sq)
         p.lse[static_cast<size_t>(bh) * p.mask.Sq + row] =
             none ? -INFINITY : (m_ref + __log2f(l)) * kLn2L;
+      if (lane == 0) bulk_wait_all();
     }
   }
 
