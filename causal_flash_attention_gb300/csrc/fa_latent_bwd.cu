@@ -721,31 +721,38 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 }
 
 // -------------------------------------------------------------------- dKR --
-// dKR_j = scale * the heads' parts, added in head order; 8 elements a thread. Bandwidth-bound.
+// dKR_j = scale * the heads' parts, added in head order; 4 elements a thread. Bound by latency:
+// the parts are in L2, and eight heads' loads go out together (8 elements a thread with two heads'
+// at a time: 7.7 us instead of 4.7 at 2 x 16 heads, 2999 tokens).
+constexpr int kDkrElems = 4;
+
 template <bool kBf16>
 __global__ void __launch_bounds__(256) latent_dkr_kernel(const __grid_constant__ LatentBwdParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long at = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   const long long tokens = static_cast<long long>(p.B) * p.mask.Skv;
-  const long long token = at / (kRope / 8);
-  const int u = static_cast<int>(at % (kRope / 8));
+  const long long token = at / (kRope / kDkrElems);
+  const int e = static_cast<int>(at % (kRope / kDkrElems)) * kDkrElems;
   if (token >= tokens) return;
   const int b = static_cast<int>(token / p.mask.Skv), j = static_cast<int>(token % p.mask.Skv);
   const size_t step = static_cast<size_t>(p.mask.Skv) * kRope;
-  const float* src = p.part + static_cast<size_t>(b) * p.H * step + static_cast<size_t>(j) * kRope + u * 8;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int h = 0; h < p.H; ++h) {
-    const float4 x = reinterpret_cast<const float4*>(src + h * step)[0];
-    const float4 y = reinterpret_cast<const float4*>(src + h * step)[1];
-    acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
-    acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
-  }
-  uint16_t* dst = static_cast<uint16_t*>(p.dk_rope.data) + b * p.dk_rope.sb + j * p.dk_rope.ss + u * 8;
-  uint32_t w[4];
+  const float* src = p.part + static_cast<size_t>(b) * p.H * step + static_cast<size_t>(j) * kRope + e;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kHeads = 8;
+  for (int h = 0; h < p.H; h += kHeads) {
+    float4 x[kHeads];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = pack2<kBf16>(acc[2 * e] * p.scale, acc[2 * e + 1] * p.scale);
-  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < kHeads; ++i)
+      if (h + i < p.H) x[i] = *reinterpret_cast<const float4*>(src + (h + i) * step);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+      if (h + i < p.H) {
+        acc.x += x[i].x; acc.y += x[i].y; acc.z += x[i].z; acc.w += x[i].w;
+      }
+  }
+  uint16_t* dst = static_cast<uint16_t*>(p.dk_rope.data) + b * p.dk_rope.sb + j * p.dk_rope.ss + e;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<kBf16>(acc.x * p.scale, acc.y * p.scale),
+                                              pack2<kBf16>(acc.z * p.scale, acc.w * p.scale));
 }
 
 template <int D, bool kBf16>
@@ -766,7 +773,7 @@ cudaError_t launch_impl(const LatentBwdParams& p0, cudaStream_t stream) {
   e = launch_dependent(dkv, dim3(static_cast<unsigned>(bh * p.n_units)), dim3(kThreadsB),
                        LatDkvCfg<D>::kSmemBytes, stream, p);
   if (e != cudaSuccess) return e;
-  const long long threads = static_cast<long long>(p.B) * p.mask.Skv * (kRope / 8);
+  const long long threads = static_cast<long long>(p.B) * p.mask.Skv * (kRope / kDkrElems);
   return launch_dependent(latent_dkr_kernel<kBf16>, dim3(static_cast<unsigned>((threads + 255) / 256)),
                           dim3(256), 0, stream, p);
 }

@@ -575,7 +575,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __
   // programmatic dependent of the main kernel; a main kernel that follows on the stream may
   // set itself up beside this grid
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kParts = RANK / 128, kRows = kMergeWarps / kParts;   // warps a row, rows a block
   constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
   __shared__ int2 sums[kMergeWarps];
@@ -583,6 +582,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __
   const int r = static_cast<int>(blockIdx.y) * kRows + warp / kParts;
   const int e = warp % kParts * 128 + lane * 4;   // this lane's four elements
   int b, u0, units, total;   // a sequence, its units [u0, u0 + units), all units
+  // The lengths are read before the wait: every block of the main kernel, which let this one start,
+  // has waited for what ran before it, and does not write them.
   auto nothing = [&](int seq) {
     if (r >= p.R) return;
     const size_t row = static_cast<size_t>(seq) * p.R + r;
@@ -602,6 +603,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __
     all = __reduce_add_sync(0xffffffffu, all);
     if (lane == 0) sums[warp] = make_int2(before, all);
     __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     u0 = total = 0;
 #pragma unroll
     for (int w = 0; w < kMergeWarps; ++w) {
@@ -613,6 +615,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __
       return;
     }
   } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int i = blockIdx.x; i < p.B; i += gridDim.x)
       if (seq_keys(p, i).n == 0) nothing(i);
     total = p.starts[0].w;
