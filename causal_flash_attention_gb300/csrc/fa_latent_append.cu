@@ -6,10 +6,10 @@
 //
 // with the rotation, its table of turns and the norm's conventions as in fa_heads.cu.
 //
-// A warp takes units of a token: the latent (8 elements a lane, rank / 256 vectors of them),
-// or a group of four 64-element heads (8 lanes a head), the shared key part being head 0 of
-// the first group's place in the order of work. Bound by the launch for a step's few
-// tokens, by the bytes for prompts.
+// A warp takes units of a token: the latent (8 elements a lane, rank / 256 vectors of them), or
+// eight 64-element heads. Bound by the launch for a step's few tokens; for prompts by the issue of
+// instructions, as which a lane has both elements of a pair and 16 in all (8 elements and the partners
+// by shuffles, one token a block: 9.6 us instead of 6.2 at 3 x 1025 tokens of 16 heads, rank 512).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -25,16 +25,28 @@ namespace {
 constexpr int kWarpsA = 8;
 constexpr unsigned kFullA = 0xffffffffu;
 
-// 8 consecutive elements in fp32.
+// 8 consecutive elements as they are in memory, and in fp32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* src, float (&x)[8]) {
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* src) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) r.v[i] = reinterpret_cast<const uint4*>(src)[i];
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void widen(const Raw8<T>& r, float (&x)[8]) {
   if constexpr (sizeof(T) == 4) {
-    const float4 a = reinterpret_cast<const float4*>(src)[0], b = reinterpret_cast<const float4*>(src)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[4 * i] = __uint_as_float(r.v[i].x); x[4 * i + 1] = __uint_as_float(r.v[i].y);
+      x[4 * i + 2] = __uint_as_float(r.v[i].z); x[4 * i + 3] = __uint_as_float(r.v[i].w);
+    }
   } else {
-    const uint4 v = *reinterpret_cast<const uint4*>(src);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = unpack2<std::is_same<T, __nv_bfloat16>::value>(w[i]);
@@ -56,49 +68,94 @@ __device__ __forceinline__ void store8(T* dst, const float (&x)[8]) {
   }
 }
 
-// A block takes one token, or (blockIdx.y of gridDim.y) a part of its units: unit 0 the
-// latent, unit 1 the shared key part, unit 2 + i query heads 4 i to 4 i + 3.
-template <typename T, int RANK>
+// A block takes kTokens tokens with kWarpsA / kTokens warps each, or (blockIdx.y of gridDim.y) a part
+// of one's units: unit 0 the latent, unit 1 + i eight heads (four lanes a head, 16 elements a lane, those
+// of a pair in one lane), of which the shared key part is the first and query head h number 1 + h. A
+// warp's elements are loaded one unit ahead, the first before the angles are known: they need no length.
+template <typename T, int RANK, int kTokens>
 __global__ void __launch_bounds__(32 * kWarpsA)
     latent_append_kernel(const __grid_constant__ LatentAppendParams p) {
-  __shared__ float2 table[kRope / 2];
+  constexpr int kAngles = kRope / 2, kPer = kWarpsA / kTokens;   // warps a token
+  static_assert(kTokens * kAngles <= 32 * kWarpsA - 32, "a thread an angle, a warp for the rows");
+  __shared__ __align__(16) float2 table[kTokens][kAngles];
+  __shared__ long long cache_rows[kTokens];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (gridDim.x * gridDim.y <= 152) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const unsigned token = blockIdx.x;   // B * Sq < 2^31
+  const unsigned token0 = blockIdx.x * kTokens;   // B * Sq < 2^31
+  const int tokens = static_cast<int>(min(static_cast<unsigned>(kTokens), static_cast<unsigned>(p.B) * p.Sq - token0));
+  const int t = warp / kPer;
+  const unsigned token = token0 + (t < tokens ? t : 0);
   const int b = static_cast<int>(token / p.Sq);
   const int s = static_cast<int>(token - static_cast<unsigned>(b) * p.Sq);
-  // (a length may be any int32, and so far below 0 that 32 bits would wrap around)
-  const long long row = static_cast<long long>(p.seq_lens[b]) - p.Sq + s;
-  if (threadIdx.x < kRope / 2) {
-    const long long position = p.positions ? p.positions[token] : row;
-    const uint64_t turn = static_cast<uint64_t>(position) * p.turns[threadIdx.x];
-    const float x = static_cast<float>(static_cast<int>((turn + 0x80000000u) >> 32)) * 0x1p-31f;
-    float sn, cs;
-    sincospif(x, &sn, &cs);
-    table[threadIdx.x] = make_float2(cs * p.rope_scale, sn * p.rope_scale);
+  const int units = t < tokens ? 1 + (p.H + 8) / 8 : 0, step = static_cast<int>(gridDim.y) * kPer;
+  int u = static_cast<int>(blockIdx.y) * kPer + warp % kPer;
+  constexpr int N = RANK / 256;   // vectors of 8 elements of a lane: of the latent, and two of a head
+  const int e0 = (lane & 3) * 8, e1 = e0 + kRope / 2;   // this lane's elements of a head
+
+  auto load = [&](int unit, Raw8<T> (&x)[2]) {
+    if (unit >= units) return;
+    if (unit == 0) {
+      const T* src = static_cast<const T*>(p.latent.data) + b * p.latent.sb + s * p.latent.ss + lane * 8;
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = load8(src + i * 256);
+      return;
+    }
+    const int h = (unit - 1) * 8 + lane / 4 - 1;   // -1: the shared key part
+    if (h >= p.H) return;
+    const HeadView& v = h < 0 ? p.k_rope : p.q_rope;
+    const T* src = static_cast<const T*>(v.data) + b * v.sb + max(h, 0) * v.sh + s * v.ss;
+    x[0] = load8(src + e0);
+    x[1] = load8(src + e1);
+  };
+  Raw8<T> raw[2] = {}, ahead[2] = {};
+  load(u, raw);
+
+  {
+    // a token's row of its sequence (a length may be any int32, and so far below 0 that 32 bits would
+    // wrap around), its angles, and its row of the cache: -1 if it is not stored
+    const bool angle = threadIdx.x < kTokens * kAngles;
+    const int of = angle ? static_cast<int>(threadIdx.x) / kAngles : static_cast<int>(threadIdx.x) - (32 * kWarpsA - 32);
+    if (of >= 0 && of < tokens) {
+      const unsigned tok = token0 + of;
+      const int seq = static_cast<int>(tok / p.Sq);
+      const long long row = static_cast<long long>(p.seq_lens[seq]) - p.Sq + (tok - static_cast<unsigned>(seq) * p.Sq);
+      if (angle) {
+        const int i = threadIdx.x % kAngles;
+        const long long position = p.positions ? p.positions[tok] : row;
+        const uint64_t turn = static_cast<uint64_t>(position) * p.turns[i];
+        const float f = static_cast<float>(static_cast<int>((turn + 0x80000000u) >> 32)) * 0x1p-31f;
+        float sn, cs;
+        sincospif(f, &sn, &cs);
+        table[of][i] = make_float2(cs * p.rope_scale, sn * p.rope_scale);
+      } else {
+        long long at = -1;
+        if (row >= 0 && row / p.block_size < p.max_blocks) {
+          const int pb = p.block_table[static_cast<size_t>(seq) * p.max_blocks + row / p.block_size];
+          if (pb >= 0 && pb < p.num_blocks) at = static_cast<long long>(pb) * p.block_size + row % p.block_size;
+        }
+        cache_rows[of] = at;
+      }
+    }
   }
   __syncthreads();
-  const int first = static_cast<int>(blockIdx.y) * kWarpsA + warp, step = static_cast<int>(gridDim.y) * kWarpsA;
-  const int units = 2 + (p.H + 3) / 4;
-  long long cache_row = -1;
-  if (first < 2 && row >= 0 && row / p.block_size < p.max_blocks) {
-    const int pb = p.block_table[static_cast<size_t>(b) * p.max_blocks + row / p.block_size];
-    if (pb >= 0 && pb < p.num_blocks) cache_row = static_cast<long long>(pb) * p.block_size + row % p.block_size;
-  }
+  const long long cache_row = cache_rows[t < tokens ? t : 0];
   T* const cache = static_cast<T*>(p.cache) + cache_row * (RANK + kRope);
-  for (int u = first; u < units; u += step) {
+  for (; u < units; u += step) {
+    load(u + step, ahead);
+    float x[2][8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) widen(raw[i], x[i]);
     if (u == 0) {
-      constexpr int N = RANK / 256;
-      const T* src = static_cast<const T*>(p.latent.data) + b * p.latent.sb + s * p.latent.ss;
-      float x[N][8], sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        load8(src + i * 256 + lane * 8, x[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(x[i][e], x[i][e], sum);
-      }
       if (p.weight) {
+        Raw8<T> w[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = load8(static_cast<const T*>(p.weight) + i * 256 + lane * 8);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum = fmaf(x[i][e], x[i][e], sum);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullA, sum, o);
         // the mean plus eps at least the least normal number, as for heads: zeros stay zeros
@@ -107,57 +164,64 @@ __global__ void __launch_bounds__(32 * kWarpsA)
             : "=f"(r) : "f"(sum * (1.f / RANK) + p.eps), "f"(0x1p-126f));
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          float w[8];
-          load8(static_cast<const T*>(p.weight) + i * 256 + lane * 8, w);
+          float f[8];
+          widen(w[i], f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[i][e] = x[i][e] * r * w[e];
+          for (int e = 0; e < 8; ++e) x[i][e] = x[i][e] * r * f[e];
         }
       }
       if (cache_row >= 0) {
 #pragma unroll
         for (int i = 0; i < N; ++i) store8(cache + i * 256 + lane * 8, x[i]);
       }
-      continue;
-    }
-    const int h = u == 1 ? 0 : (u - 2) * 4 + lane / 8;
-    const bool live = u == 1 ? lane < 8 : h < p.H;
-    const HeadView& v = u == 1 ? p.k_rope : p.q_rope;
-    const int e0 = (lane & 7) * 8;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, y[8];
-    if (live) load8(static_cast<const T*>(v.data) + b * v.sb + h * v.sh + s * v.ss + e0, x);
-    if (p.interleaved) {
+    } else {
+      const int h = (u - 1) * 8 + lane / 4 - 1;
+      float y[2][8];
+      if (p.interleaved) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 t = table[e0 / 2 + i];
-        y[2 * i] = t.x * x[2 * i] - t.y * x[2 * i + 1];
-        y[2 * i + 1] = t.y * x[2 * i] + t.x * x[2 * i + 1];
-      }
-    } else {   // the partner is four lanes away
-      const float sign = e0 < kRope / 2 ? -1.f : 1.f;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 t = table[(e0 & (kRope / 2 - 1)) + i];
-        const float o = __shfl_xor_sync(kFullA, x[i], 4);
-        y[i] = t.x * x[i] + sign * t.y * o;
+          for (int k = 0; k < 4; ++k) {
+            const float2 c = table[t][(i == 0 ? e0 : e1) / 2 + k];
+            y[i][2 * k] = c.x * x[i][2 * k] - c.y * x[i][2 * k + 1];
+            y[i][2 * k + 1] = c.y * x[i][2 * k] + c.x * x[i][2 * k + 1];
+          }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 c = table[t][e0 + k];
+          y[0][k] = c.x * x[0][k] - c.y * x[1][k];
+          y[1][k] = c.y * x[0][k] + c.x * x[1][k];
+        }
+      }
+      T* dst = cache + RANK;
+      if (h >= 0) dst = static_cast<T*>(p.q_out.data) + b * p.q_out.sb + h * p.q_out.sh + s * p.q_out.ss;
+      if (h < 0 ? cache_row >= 0 : h < p.H) {
+        store8(dst + e0, y[0]);
+        store8(dst + e1, y[1]);
       }
     }
-    if (u == 1) {
-      if (live && cache_row >= 0) store8(cache + RANK + e0, y);
-    } else if (live) {
-      store8(static_cast<T*>(p.q_out.data) + b * p.q_out.sb + h * p.q_out.sh + s * p.q_out.ss + e0, y);
-    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) raw[i] = ahead[i];
   }
+}
+
+template <typename T, int RANK>
+cudaError_t launch_rank(const LatentAppendParams& p, cudaStream_t stream) {
+  constexpr int kTokens = 4, kSms = 152;
+  const long long tokens = static_cast<long long>(p.B) * p.Sq;
+  const int units = 1 + (p.H + 8) / 8;
+  // with few tokens a warp a unit, with many four tokens a block
+  const int parts = tokens < kSms ? std::min((units + kWarpsA - 1) / kWarpsA, 65535) : 1;
+  const int each = tokens >= kTokens * kSms ? kTokens : 1;
+  const dim3 grid(static_cast<unsigned>((tokens + each - 1) / each), static_cast<unsigned>(parts));
+  return launch_dependent(each == 1 ? latent_append_kernel<T, RANK, 1> : latent_append_kernel<T, RANK, kTokens>, grid,
+                          dim3(32 * kWarpsA), 0, stream, p);
 }
 
 template <typename T>
 cudaError_t launch_type(const LatentAppendParams& p, cudaStream_t stream) {
-  const long long tokens = static_cast<long long>(p.B) * p.Sq;
-  const int units = 2 + (p.H + 3) / 4;
-  // with few tokens a warp a unit
-  const int parts = tokens < 152 ? std::min((units + kWarpsA - 1) / kWarpsA, 65535) : 1;
-  const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(parts));
-  return launch_dependent(p.rank == 512 ? latent_append_kernel<T, 512> : latent_append_kernel<T, 256>, grid,
-                          dim3(32 * kWarpsA), 0, stream, p);
+  return p.rank == 512 ? launch_rank<T, 512>(p, stream) : launch_rank<T, 256>(p, stream);
 }
 
 }  // namespace
