@@ -216,6 +216,13 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         xt.next();
         ++n_x;
         ++n_t;
+        // The next tile's rows on their way to L2 while its slots are still in use (16 sequences of up
+        // to 8192 rows, 128 heads: 46 -> 43.5 us).
+        if (have && n_p + kPairs > NP && pb >= 0 && pb < p.num_blocks) {
+          const int yn = ((seg.tile0 + j) * kTile + lane * p.box_rows) & (p.block_size - 1);
+#pragma unroll
+          for (int cc = 0; cc < Cfg::kChunks; ++cc) tma_prefetch_l2_3d(&p.tm, cc * kChunk, yn, pb);
+        }
       }
       // Aborted: every copy lands before the CTA releases its memory. (A tile given up half-way is
       // arrived for, and so is one that another lane went on to, so that the phases complete.)
