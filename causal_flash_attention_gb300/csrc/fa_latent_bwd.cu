@@ -14,7 +14,8 @@
 //   2. dK, dV:  a CTA per 128 keys of a head walks the query rows, 64 at a time.
 //   3. dKR:     adds up the heads' parts, in head order.
 // Warp roles of 1 and 2: warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 softmax
-// gradient, two warps a tensor-memory lane quarter with half the columns each. P and dS
+// gradient, two warps a tensor-memory lane quarter with half the columns each (four with 16 columns
+// each: 1 and 2% slower), in 1 also warp 10 MMA issuer of dQ. P and dS
 // go back to tensor memory as the A operands of the products, so shared memory holds
 // only what TMA loads.
 #include <algorithm>
@@ -28,7 +29,7 @@
 namespace fa {
 namespace {
 
-constexpr int kThreadsB = 320;
+constexpr int kThreadsQ = 352, kThreadsB = 320;   // of the dQ kernel, of the dK, dV kernel
 constexpr float kLog2eB = 1.4426950408889634f;
 
 __device__ __forceinline__ void drain_wait_b(uint32_t bar, uint32_t parity, int* status) {
@@ -75,8 +76,8 @@ struct LatDqCfg {
   static constexpr int RB = kTileM * 128;               // a chunk of 128 rows
   static constexpr int kOffO = kFirst * kStageBytes, kOffQ = kOffO + kVChunks * RB, kOffDO = kOffQ + kKChunks * RB;
   static_assert(kOffDO + kVChunks * RB <= NS * kStageBytes, "O, Q and dO in the ring");
-  // full[], empty[], s_full, dp_full, s_free, dp_free, ds_full, dq_done, drain, q_full, swap[4]
-  static constexpr int kNumBars = 2 * NS + 12;
+  // full[], empty[], s_full, dp_full, s_free, dp_free, ds_full, dq_done, drain, q_full, swap[4], drain2
+  static constexpr int kNumBars = 2 * NS + 13;
   static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kOffSpan = kOffMisc + 16;        // 4 warps' (begin, end)
   static constexpr int kOffDelta = kOffSpan + 32;       // two buffers of [2][128] halves of D
@@ -87,7 +88,7 @@ struct LatDqCfg {
 };
 
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(kThreadsB, 1)
+__global__ void __launch_bounds__(kThreadsQ, 1)
     latent_dq_kernel(const __grid_constant__ LatentBwdParams p) {
   using Cfg = LatDqCfg<D>;
   constexpr int NS = Cfg::NS, CB = Cfg::CB, W = Cfg::kW, KT = Cfg::kKeys;
@@ -109,6 +110,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   const uint32_t dp_full = s_full + 8, s_free = s_full + 16, dp_free = s_full + 24, ds_full = s_full + 32;
   const uint32_t dq_done = s_full + 40, drain = s_full + 48, q_full = s_full + 56;
   auto swap = [&](int quarter) { return s_full + 64 + 8 * quarter; };
+  const uint32_t drain2 = swap(4);
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(warp_id()), 0);
   const int lane = static_cast<int>(lane_id());
@@ -137,6 +139,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     mbar_init(ds_full, 8);
     mbar_init(dq_done, 1);
     mbar_init(drain, 1);
+    mbar_init(drain2, 1);
     mbar_init(q_full, 1);
     for (int i = 0; i < 4; ++i) mbar_init(swap(i), 2);   // the two warps of a lane quarter
     *abort_flag = 0;
@@ -159,7 +162,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   }
   int row_lo = 0, row_hi = 0;
   float l2 = INFINITY;
-  if (warp >= 2) {
+  const bool soft = warp >= 2 && warp < 10;
+  if (soft) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int2 s = p.mask.span(b, row);
     row_lo = s.x;
@@ -197,7 +201,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   if (warp == 0 && lane == 0)
     for (int j = 0; j < min(n, Cfg::kFirst); ++j) load(j);
   bool ok = true;
-  if (warp >= 2) {
+  if (soft) {
     // this thread's halves of its row of Q and dO into tensor memory, its half of D, and L
     if (row < p.mask.Sq && row_hi > 0) l2 = p.lse[static_cast<size_t>(bh) * p.mask.Sq + row] * kLog2eB;
     // (one outcome for the warp, as for every wait: tensor-memory instructions have to find it whole)
@@ -233,6 +237,14 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   __syncthreads();   // Q, dO and the halves of D
   tc_fence_after();
 
+  // A role that gives up: every MMA it has issued must finish before the tensor memory is released.
+  auto finish = [&](uint32_t bar) {
+    if (!ok) {
+      elected([&] { tc_commit(bar); });
+      drain_wait_b(bar, 0, p.status);
+    }
+    __syncwarp();
+  };
   if (warp == 0) {
     // ===================== TMA producer =====================
     if (lane == 0) {
@@ -247,10 +259,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       }
     }
   } else if (warp == 1) {
-    // ===================== MMA issuer (the whole warp, one lane of it the MMAs) =====================
+    // ===================== MMA issuer of S and dP (the whole warp, one lane of it the MMAs) =====================
     if (n > 0) {
       constexpr uint32_t idesc_s = make_idesc(128, KT, kBf16, false, false);
-      constexpr uint32_t idesc_q = make_idesc(128, W, kBf16, false, true);
       auto wait = [&](uint32_t bar, uint32_t parity) { return warp_wait(bar, parity, abort_flag, p.status); };
 #ifdef FA_WAIT_TEST
       // wait-limit test build: nothing completes this phase before the abort
@@ -275,10 +286,17 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         });
         return true;
       };
-      if (ok) ok = scores(0);
-      for (int j = 0; ok && j < n; ++j) {
-        if (j + 1 < n && !(ok = scores(j + 1))) break;
-        if (!(ok = wait(ds_full, j & 1))) break;
+      for (int j = 0; ok && j < n; ++j) ok = scores(j);
+      finish(drain);
+    }
+  } else if (warp == 10) {
+    // ===================== MMA issuer of dQ =====================
+    // (one issuer for all: 196 us instead of 192 at 4096 tokens, 32 heads; two in the dK, dV kernel, whose
+    // products wait for shared memory: 262 instead of 255)
+    if (n > 0) {
+      constexpr uint32_t idesc_q = make_idesc(128, W, kBf16, false, true);
+      for (int j = 0; ok && j < n; ++j) {   // dQ += dS_j K'_j
+        if (!(ok = warp_wait(ds_full, j & 1, abort_flag, p.status))) break;
         tc_fence_after();
         const uint64_t kb = make_sdesc(sbase + (j % NS) * Cfg::kStageBytes, CB, 1024);
         elected([&] {
@@ -287,12 +305,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           tc_commit(dq_done);         // that arrived after the CTA had exited would be a fault)
         });
       }
-      if (!ok) {
-        // every MMA issued so far must finish before the TMEM is released
-        elected([&] { tc_commit(drain); });
-        drain_wait_b(drain, 0, p.status);
-      }
-      __syncwarp();
+      finish(drain2);
     }
   } else {
     // ===================== softmax gradient, two threads a row =====================
@@ -609,7 +622,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   } else {
     // ===================== softmax gradient, two threads a key =====================
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const int key0 = kv0 + quarter * 32, key = key0 + lane;
+    const int key0 = kv0 + quarter * 32;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem + lane_off + 320 + half * 32;
     const float c = p.scale_log2;
@@ -766,7 +779,7 @@ cudaError_t launch_impl(const LatentBwdParams& p0, cudaStream_t stream) {
   LatentBwdParams p = p0;
   const long long bh = static_cast<long long>(p.B) * p.H;
   p.n_units = p.Sq_pad / kTileM;
-  e = launch_dependent(dq, dim3(static_cast<unsigned>(bh * p.n_units)), dim3(kThreadsB),
+  e = launch_dependent(dq, dim3(static_cast<unsigned>(bh * p.n_units)), dim3(kThreadsQ),
                        LatDqCfg<D>::kSmemBytes, stream, p);
   if (e != cudaSuccess) return e;
   p.n_units = (p.mask.Skv + kTileN - 1) / kTileN;
