@@ -199,6 +199,16 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
           else tma_load_4d(dst, &p.tm_kr, f, 0, y, 0, b);
           slot = slot + 1 == NS ? 0 : slot + 1;
         }
+        // The next tile's on their way to L2, while their slots are in use: at d = 128 the ring holds
+        // less than two tiles and K is waited for in every step (chunk of 1024 over 8192 keys 126 ->
+        // 122 us, 4096 tokens, 32 heads 131 -> 125).
+        if (T == 2 && j + 1 < n_load) {
+          for (int c = 0; c < n; ++c) {
+            if (!is_k(u)) tma_prefetch_l2_4d(&p.tm_v, c * kChunk, y + kTileN, h, b);
+            else if (c < VC) tma_prefetch_l2_4d(&p.tm_k, c * kChunk, y + kTileN, h, b);
+            else tma_prefetch_l2_4d(&p.tm_kr, 0, y + kTileN, 0, b);
+          }
+        }
         used += n;
         ++held;
         if (is_k(u)) ++jk;
