@@ -522,7 +522,8 @@ const char* fa_strerror(int code) {
     case FA_ERR_SHAPE:
       return "invalid shape (B, Hq, Hkv, S >= 1, Hq % Hkv == 0, d in {64, 128}, causal Skv >= Sq; "
              "paged: block_size a power of two from 16 to 1024, Hq / Hkv * Sq <= 128, window >= 0; "
-             "rope_dim a multiple of 16 up to d)";
+             "rope_dim a multiple of 16 up to d; latent: rank 256 or 512, H * Sq <= 1024, positive strides, "
+             "tree masks with Sq <= 64 and no window)";
     case FA_ERR_DTYPE: return "dtype not FA_F32, FA_F16 or FA_BF16, or one this call does not take";
     case FA_ERR_NULL: return "a required pointer is NULL";
     case FA_ERR_ALIGN: return "a pointer or stride is not aligned (tensors and strides 16 bytes, workspace 256, int32 and float "

@@ -18,6 +18,13 @@
 // each: 1 and 2% slower), in 1 also warp 10 MMA issuer of dQ. P and dS
 // go back to tensor memory as the A operands of the products, so shared memory holds
 // only what TMA loads.
+//
+// 4096 tokens, 32 heads, d = 128, bf16, causal: dQ 192 us, 1432 TFLOP/s of products executed (75%
+// of a large product's rate), dK and dV 254 us, 1353 (70%), dKR 7.5. dQ is bound by a tile's chain
+// through the softmax warps (1340 cycles, 1024 of products) and by the filling of a CTA (112 KB in
+// front of the first product, 16% of it); dK and dV by shared memory, from which products 64 rows
+// wide take both operands (1600 cycles a step instead of 1280, 1950 in all): there is no tensor
+// memory left for K' and V beside S^T, dP^T, P^T, dS^T and the sums.
 #include <algorithm>
 #include <type_traits>
 

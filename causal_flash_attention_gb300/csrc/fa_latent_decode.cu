@@ -23,6 +23,13 @@
 // own part of O^T is formed; one barrier a tile tells that it has landed (a wait costs the
 // issuer 100 cycles, three products).
 //
+// Bound by a tile's way through the ring, which holds two tiles beside the queries of 64 rows:
+// landing, S (1325 cycles: M = 64 runs at half rate), softmax, O^T (900) and the next load. One new
+// token of 16 sequences of up to 8192 rows, rank 512: 128 heads 43.5 us with the merge (36.5 + 7), of
+// which a share of 14 tiles takes 25 and a part's 128 KB on their way out 2.4; 16 heads 27.5 (20.8 + 6.7),
+// 67 MB, of which the loop runs at 7 TB/s and the first tiles of all SMs take 3 us to land. (Writing the
+// results 32 columns of all parts at a time: 52 instead of 43.5, registers spilled.)
+//
 // Warp roles (320 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 softmax (lanes
 // 0-15 of the two warps of a tensor-memory quarter w hold rows 16 w .. 16 w + 15, the M = 64
 // layout, each warp 32 of the tile's keys) and O^T (all lanes, each warp half its parts).

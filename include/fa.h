@@ -447,7 +447,9 @@ size_t fa_bwd_latent_workspace_bytes(int B, int H, int Sq, int Skv, int d);
  * lengths are as for fa_fwd_ragged_paged. tree_masks (or NULL): [B][Sq] 64-bit words in device
  * memory for drafted tokens that form a tree. Row s then sees every key before the Sq new
  * tokens, and new token t (at key seq_lens[b] - Sq + t) where bit t of tree_masks[b][s] is
- * set, its own included; bits from Sq on are not looked at.
+ * set, its own included; bits from Sq on are not looked at. A cache row that is not finite and
+ * that some new token of its sequence sees may give NaN to every new token of the sequence, also
+ * to one that does not see it: what a row hides it multiplies by 0.
  *
  * q is a view with positive strides, as for fa_fwd_latent. rank is 256 or 512, H * Sq <= 1024,
  * block_size and max_blocks as for fa_fwd_ragged_paged, with tree_masks Sq <= 64 and no window
