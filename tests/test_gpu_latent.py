@@ -1,5 +1,5 @@
 """Latent attention with expanded keys and values on the GPU, forward and backward, against the
-64-bit definition within derived bounds, and its gradients against differences."""
+64-bit definition within derived bounds (differences: test_gpu_latent_together.py)."""
 import math
 
 import numpy as np

@@ -380,3 +380,47 @@ def test_gradients_against_differences(fa, d):
         want = (loss(y[0]) - loss(y[1])) / (2 * h)
         g = f64(grads[i])
         assert abs((g * way).sum() - want) <= (tol[name + "_tol"] * np.abs(way)).sum() + 1e-5 * np.abs(g * way).sum() + 1e-8
+
+
+@pytest.mark.parametrize("d,interleaved", [(64, False), (128, True)])
+def test_training_step_of_a_layer(fa, d, interleaved):
+    """Queries' and keys' rotated parts turned in place, attention, and both backward calls. The
+    whole gradient along a direction w of the unrotated parts is the attention's along R w, which a
+    difference of the 64-bit loss at the rotated values gives; it is off by the attention's bounds on
+    R w and by one rounding where the gradient is turned back."""
+    heads, n, u = 3, 90, half_step(torch.bfloat16)
+    g = torch.Generator().manual_seed(d)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(DEV)
+    q, kv = r(1, n, heads, d + 64).transpose(1, 2), r(1, n, heads, 2 * d).transpose(1, 2)
+    kr, do, scale = r(1, n, 96)[..., 32:], r(1, n, heads, d).transpose(1, 2), (d + 64) ** -0.5
+    freq, rope_scale = fa.rope_inv_freq(64)
+    turns, spans = fa.rope_turns(freq, DEV), fa.key_spans(1, n, doc_lens=[50, 40], device=DEV)
+    rot = dict(interleaved=interleaved, rope_scale=rope_scale)
+    fa.fa_qk_norm_rope(q[..., d:], kr[:, None], q[..., d:], kr[:, None], turns, **rot)
+    k, v = kv[..., :d], kv[..., d:]
+    out, lse = fa.attention_latent_forward(q, k, kr, v, *spans)
+    dkv = torch.empty(1, n, heads, 2 * d, dtype=torch.bfloat16, device=DEV).transpose(1, 2)
+    dq, _, dkr, _ = fa.attention_latent_backward(q, k, kr, v, out, do, lse, *spans, dk=dkv[..., :d], dv=dkv[..., d:])
+    fa.qk_norm_rope_backward(dq[..., d:], dkr[:, None], None, None, turns, **rot, dq=dq[..., d:], dk=dkr[:, None])
+    torch.cuda.synchronize()
+    assert fa.fa_last_device_status() == 0
+
+    X, DO, sp = [f64(t) for t in (q, k, kr, v)], f64(do), [t.cpu().numpy() for t in spans]
+    tol = ops.latent_attention(*X, *sp, scale, DO, u)
+    loss = lambda y: (ops.latent_attention(*y, *sp, scale)["out"] * DO).sum()
+    pos, f = np.arange(n)[None], f64(torch.as_tensor(freq))
+    turn = lambda z: ops.norm_rope(z, None, f, pos, 0.0, interleaved, rope_scale)
+    rng, h = np.random.default_rng(d), 1e-4
+    ways = [rng.standard_normal(x.shape) for x in X]
+    moved = [w.copy() for w in ways]
+    moved[0][..., d:] = turn(ways[0][..., d:])
+    moved[2] = turn(ways[2][:, None])[:, 0]
+    grads = [f64(t) for t in (dq, dkv[..., :d], dkr, dkv[..., d:])]
+    for i, name in enumerate(("dq", "dk", "dk_rope", "dv")):
+        y = [[a + s * h * moved[i] if j == i else a for j, a in enumerate(X)] for s in (1, -1)]
+        want = (loss(y[0]) - loss(y[1])) / (2 * h)
+        got = (grads[i] * ways[i]).sum()
+        bound = (tol[name + "_tol"] * np.abs(moved[i])).sum() + 1e-5 * abs(got) + 1e-8
+        if i in (0, 2):
+            bound += 1.1 * u * np.abs(grads[i] * ways[i]).sum() + 1e-6
+        assert abs(got - want) <= bound, name
