@@ -22,7 +22,7 @@ int check_sizes(int B, int H, int Sq, int Skv, int d, float scale) {
   // CTAs of any kernel below 2^31, rows and keys within int32 with room for a tile
   const long long bh = static_cast<long long>(B) * H;
   if (bh > (1LL << 30) || Sq > (1 << 30) || Skv > (1 << 30) || bh * ((Sq + 127) / 128) > 0x7fffffffLL ||
-      bh * ((Skv + 127) / 128) > 0x7fffffffLL || static_cast<long long>(B) * Skv * 8 / 256 > 0x7ffffffeLL)
+      bh * ((Skv + 127) / 128) > 0x7fffffffLL || static_cast<long long>(B) * Skv * 16 / 256 > 0x7ffffffeLL)
     return FA_ERR_SHAPE;
   if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_SCALE;
   return FA_OK;
