@@ -19,10 +19,10 @@
 // go back to tensor memory as the A operands of the products, so shared memory holds
 // only what TMA loads.
 //
-// 4096 tokens, 32 heads, d = 128, bf16, causal: dQ 192 us, 1432 TFLOP/s of products executed (75%
-// of a large product's rate), dK and dV 254 us, 1353 (70%), dKR 7.5. dQ is bound by a tile's chain
-// through the softmax warps (1340 cycles, 1024 of products) and by the filling of a CTA (112 KB in
-// front of the first product, 16% of it); dK and dV by shared memory, from which products 64 rows
+// 4096 tokens, 32 heads, d = 128, bf16, causal: dQ 188 us, 1463 TFLOP/s of products executed (76%
+// of a large product's rate), dK and dV 252 us, 1364 (71%), dKR 7.5. dQ is bound by a tile's chain
+// through the softmax warps (1340 cycles, 1024 of products) and by the filling of a CTA (112 KB, a
+// tenth of it); dK and dV by shared memory, from which products 64 rows
 // wide take both operands (1600 cycles a step instead of 1280, 1950 in all): there is no tensor
 // memory left for K' and V beside S^T, dP^T, P^T, dS^T and the sums.
 #include <algorithm>
@@ -83,8 +83,9 @@ struct LatDqCfg {
   static constexpr int RB = kTileM * 128;               // a chunk of 128 rows
   static constexpr int kOffO = kFirst * kStageBytes, kOffQ = kOffO + kVChunks * RB, kOffDO = kOffQ + kKChunks * RB;
   static_assert(kOffDO + kVChunks * RB <= NS * kStageBytes, "O, Q and dO in the ring");
-  // full[], empty[], s_full, dp_full, s_free, dp_free, ds_full, dq_done, drain, q_full, swap[4], drain2
-  static constexpr int kNumBars = 2 * NS + 13;
+  // full[], empty[], s_full, dp_full, s_free, dp_free, ds_full, dq_done, drain, q_full, swap[4], drain2,
+  // do_full, o_full, o_done
+  static constexpr int kNumBars = 2 * NS + 16;
   static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kOffSpan = kOffMisc + 16;        // 4 warps' (begin, end)
   static constexpr int kOffDelta = kOffSpan + 32;       // two buffers of [2][128] halves of D
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   const uint32_t dp_full = s_full + 8, s_free = s_full + 16, dp_free = s_full + 24, ds_full = s_full + 32;
   const uint32_t dq_done = s_full + 40, drain = s_full + 48, q_full = s_full + 56;
   auto swap = [&](int quarter) { return s_full + 64 + 8 * quarter; };
-  const uint32_t drain2 = swap(4);
+  const uint32_t drain2 = swap(4), do_full = swap(5), o_full = swap(6), o_done = swap(7);
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(warp_id()), 0);
   const int lane = static_cast<int>(lane_id());
@@ -141,28 +142,32 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
-    mbar_init(s_free, 8);   // one arrival per compute warp
+    // one arrival per compute warp; the first phase of s_free says that Q is in tensor memory, that of
+    // dp_free that dO is
+    mbar_init(s_free, 8);
     mbar_init(dp_free, 8);
     mbar_init(ds_full, 8);
     mbar_init(dq_done, 1);
     mbar_init(drain, 1);
     mbar_init(drain2, 1);
     mbar_init(q_full, 1);
+    mbar_init(do_full, 1);
+    mbar_init(o_full, 1);
+    mbar_init(o_done, 8);
     for (int i = 0; i < 4; ++i) mbar_init(swap(i), 2);   // the two warps of a lane quarter
     *abort_flag = 0;
     fence_mbar_init();
     // rows past Sq come as zeros
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    mbar_arrive_expect_tx(q_full, (Cfg::kKChunks + 2 * Cfg::kVChunks) * Cfg::RB);
-    for (int r = 0; r < 2; ++r) {
-      const int y = q0 + r * 64, at = r * (Cfg::RB / 2);
-      for (int c = 0; c < Cfg::kKChunks; ++c)
-        tma_load_4d(sbase + Cfg::kOffQ + c * Cfg::RB + at, &p.tm_q, q_full, c * kChunk, y, h, b);
-      for (int c = 0; c < Cfg::kVChunks; ++c) {
-        tma_load_4d(sbase + Cfg::kOffDO + c * Cfg::RB + at, &p.tm_do, q_full, c * kChunk, y, h, b);
-        tma_load_4d(sbase + Cfg::kOffO + c * Cfg::RB + at, &p.tm_o, q_full, c * kChunk, y, h, b);
-      }
-    }
+    auto rows = [&](uint32_t bar, const CUtensorMap* tm, int off, int chunks) {
+      mbar_arrive_expect_tx(bar, chunks * Cfg::RB);
+      for (int c = 0; c < chunks; ++c)
+        for (int r = 0; r < 2; ++r)
+          tma_load_4d(sbase + off + c * Cfg::RB + r * (Cfg::RB / 2), tm, bar, c * kChunk, q0 + r * 64, h, b);
+    };
+    rows(q_full, &p.tm_q, Cfg::kOffQ, Cfg::kKChunks);
+    rows(do_full, &p.tm_do, Cfg::kOffDO, Cfg::kVChunks);
+    rows(o_full, &p.tm_o, Cfg::kOffO, Cfg::kVChunks);
     tma_prefetch_desc(&p.tm_k);
     tma_prefetch_desc(&p.tm_kr);
     tma_prefetch_desc(&p.tm_v);
@@ -209,16 +214,18 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     for (int j = 0; j < min(n, Cfg::kFirst); ++j) load(j);
   bool ok = true;
   if (soft) {
-    // this thread's halves of its row of Q and dO into tensor memory, its half of D, and L
+    // This thread's halves of its row of Q and dO into tensor memory, its half of D, and L: each as
+    // it lands, so that S and dP of the first tile are formed meanwhile.
     if (row < p.mask.Sq && row_hi > 0) l2 = p.lse[static_cast<size_t>(bh) * p.mask.Sq + row] * kLog2eB;
-    // (one outcome for the warp, as for every wait: tensor-memory instructions have to find it whole)
-    ok = warp_wait(q_full, 0, abort_flag, p.status);
     constexpr int QU = W / 16, OU = D / 16;   // 16-byte units of a half row
     auto unit = [&](int off, int u) {   // unit u of this row, chunks of 128 rows with the 128-byte swizzle
       return *reinterpret_cast<const uint4*>(smem + off + (u >> 3) * Cfg::RB + rr * 128 + (((u & 7) ^ (rr & 7)) << 4));
     };
-    auto put = [&](uint32_t col, int off, int first, auto units) {
+    auto put = [&](uint32_t landed, uint32_t there, uint32_t col, int off, int first, auto units) {
       constexpr int N = decltype(units)::value;
+      // (one outcome for the warp, as for every wait: tensor-memory instructions have to find it whole)
+      if (ok) ok = warp_wait(landed, 0, abort_flag, p.status);
+      if (!ok) return;
 #pragma unroll
       for (int i = 0; i < N; i += 4) {
         uint32_t w[16];
@@ -229,20 +236,26 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         }
         tmem_st16(tmem + lane_off + col + (first + i) * 4, w);
       }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(there);
     };
-    put(Cfg::kColQ, Cfg::kOffQ, half * QU, std::integral_constant<int, QU>{});
-    put(Cfg::kColDO, Cfg::kOffDO, half * OU, std::integral_constant<int, OU>{});
+    put(q_full, s_free, Cfg::kColQ, Cfg::kOffQ, half * QU, std::integral_constant<int, QU>{});
+    put(do_full, dp_free, Cfg::kColDO, Cfg::kOffDO, half * OU, std::integral_constant<int, OU>{});
+    if (ok) ok = warp_wait(o_full, 0, abort_flag, p.status);
     float d = 0.f;
+    if (ok) {
 #pragma unroll
-    for (int u = 0; u < OU; ++u)
-      d = dot16<kBf16>(unit(Cfg::kOffO, half * OU + u), unit(Cfg::kOffDO, half * OU + u), d);
+      for (int u = 0; u < OU; ++u)
+        d = dot16<kBf16>(unit(Cfg::kOffO, half * OU + u), unit(Cfg::kOffDO, half * OU + u), d);
+    }
     halves[half * 128 + rr] = d;
-    tmem_wait_st();
     fence_proxy_async_smem();   // the copies that follow into these stages come after the reads
+    __syncwarp();
+    if (lane == 0) mbar_arrive(o_done);
+    asm volatile("bar.sync 1, 256;" ::: "memory");   // the halves of D, among these warps
   }
-  tc_fence_before();
-  __syncthreads();   // Q, dO and the halves of D
-  tc_fence_after();
 
   // A role that gives up: every MMA it has issued must finish before the tensor memory is released.
   auto finish = [&](uint32_t bar) {
@@ -256,12 +269,15 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     // ===================== TMA producer =====================
     if (lane == 0) {
       int j = min(n, Cfg::kFirst);
-      for (; j < n; ++j) {
+      if (j < n) ok = mbar_wait(o_done, 0, abort_flag, p.status);   // the other stages are free
+      for (; ok && j < n; ++j) {
         if (j >= NS && !mbar_wait(empty(j % NS), (j / NS - 1) & 1, abort_flag, p.status)) break;
         load(j);
       }
       if (*abort_flag) {   // let every copy already issued land before the CTA releases its memory
         drain_wait_b(q_full, 0, p.status);
+        drain_wait_b(do_full, 0, p.status);
+        drain_wait_b(o_full, 0, p.status);
         for (int i = max(0, j - NS); i < j; ++i) drain_wait_b(full(i % NS), (i / NS) & 1, p.status);
       }
     }
@@ -277,7 +293,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
 #endif
       auto scores = [&](int j) -> bool {   // S = Q K'_j^T, dP = dO V_j^T
         if (!wait(full(j % NS), (j / NS) & 1)) return false;
-        if (j > 0 && !wait(s_free, (j - 1) & 1)) return false;
+        if (!wait(s_free, j & 1)) return false;
         tc_fence_after();
         const uint32_t st = sbase + (j % NS) * Cfg::kStageBytes;
         const uint64_t kb = make_sdesc(st, 16, 1024), vb = make_sdesc(st + Cfg::kKChunks * CB, 16, 1024);
@@ -285,7 +301,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           mma_ts_steps<W / 16, true, CB>(tmem, tmem + Cfg::kColQ, kb, idesc_s, 0u);
           tc_commit(s_full);
         });
-        if (j > 0 && !wait(dp_free, (j - 1) & 1)) return false;
+        if (!wait(dp_free, j & 1)) return false;
         tc_fence_after();
         elected([&] {
           mma_ts_steps<D / 16, true, CB>(tmem + KT, tmem + Cfg::kColDO, vb, idesc_s, 0u);
