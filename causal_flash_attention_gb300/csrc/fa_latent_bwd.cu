@@ -475,8 +475,9 @@ struct LatDkvCfg {
   static constexpr int kOffBar = kOffRow + NS * 2 * kRows * 4;
   // kv_full, full[], empty[], s_full, dp_full, s_free, ds_full, kd_done, drain
   static constexpr int kNumBars = 1 + 2 * NS + 6;
-  static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // tmem, abort, first, last
-  static constexpr int kSmemBytes = kOffMisc + 16;
+  static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // tmem, abort
+  static constexpr int kOffSteps = kOffMisc + 16;       // first and last step, each warp's
+  static constexpr int kSmemBytes = kOffSteps + kThreadsB / 32 * 8;
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 };
 
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   }
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
-  int* steps = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 8);   // first and last step
+  int2* steps = reinterpret_cast<int2*>(smem + Cfg::kOffSteps);
 
   const uint32_t kv_full = sbase + Cfg::kOffBar;
   auto full = [&](int s) { return kv_full + 8 * (1 + s); };
@@ -523,22 +524,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     mbar_init(kd_done, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
-    steps[0] = 0x7fffffff;
-    steps[1] = -1;
     fence_mbar_init();
-    tma_prefetch_desc(&p.tm_q);
-    tma_prefetch_desc(&p.tm_do);
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the dQ kernel's L, D and ranges
-  if (threadIdx.x == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     mbar_arrive_expect_tx(kv_full, (Cfg::kKChunks + Cfg::kVChunks) * CB);
     for (int r = 0; r < 2; ++r) {   // boxes of 64 rows
       const int y = kv0 + r * 64, at = r * (CB / 2);
@@ -548,8 +535,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       }
       tma_load_4d(sbase + Cfg::kVChunks * CB + at, &p.tm_kr, kv_full, 0, y, 0, b);
     }
+    tma_prefetch_desc(&p.tm_q);
+    tma_prefetch_desc(&p.tm_do);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
   }
   // the steps with a row whose span reaches into the tile, and those between them
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the dQ kernel's L, D and ranges
   {
     const int2* ranges = p.ranges + static_cast<size_t>(b) * n_steps;
     int lo = 0x7fffffff, hi = -1;
@@ -562,14 +556,20 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     }
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0 && hi >= 0) {
-      atomicMin(&steps[0], lo);
-      atomicMax(&steps[1], hi);
-    }
+    if (lane == 0) steps[warp] = make_int2(lo, hi);
   }
-  __syncthreads();
-  const int i0 = steps[1] < 0 ? 0 : steps[0];
-  const int n = steps[1] + 1 - i0;   // 0: nothing sees the tile
+  tc_fence_before();
+  __syncthreads();   // tensor memory, barriers, steps
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int i0 = 0x7fffffff, i1 = -1;
+#pragma unroll
+  for (int w = 0; w < kThreadsB / 32; ++w) {
+    i0 = min(i0, steps[w].x);
+    i1 = max(i1, steps[w].y);
+  }
+  if (i1 < 0) i0 = 0;
+  const int n = i1 + 1 - i0;   // 0: nothing sees the tile
 
   if (warp == 0) {
     // ===================== TMA producer =====================
