@@ -518,8 +518,11 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         if (lane == 0) mbar_arrive(p_full);
       }
       if (dead) break;
-      if (real) halves[half * 64 + r] = l;
+      // The last tile's product has every warp's P, and a warp gives its P after it has read the halves'
+      // maxima: past this wait they may be overwritten, in a segment of one tile too, which has no vote
+      // in between.
       wait(pv_done, g - 1);
+      if (real) halves[half * 64 + r] = l;
       if ((dead = any(!ok))) break;
       if (real && half == 0) {
         const PartSum sum(l + halves[64 + r], m_ref);

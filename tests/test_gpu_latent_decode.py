@@ -80,6 +80,21 @@ def test_decode(fa, lens, H, Sq, rank, dtype, bs, window):
     compare(run(fa, x, window=window), x, window=window)
 
 
+@pytest.mark.parametrize("rank,H,Sq", [(256, 8, 1), (512, 16, 1), (512, 20, 3), (256, 128, 8)])
+def test_segments_of_one_tile(fa, rank, H, Sq):
+    """Short sequences, and a longer one whose tiles go to shares of their own: a row's two halves of
+    the keys exchange maxima and then sums of weights with nothing in between but the tile's product.
+    Maxima that differ by tens between the halves, and the same bits in every call."""
+    lens = [33, 64, 40, 500, 1, 63, 50] + [60] * 20
+    x = make(lens, H, Sq, rank, "bf16", 16, 13, scale_q=6.0)
+    first = run(fa, x)
+    compare(first, x)
+    d = [t.to(DEV) for t in x]
+    got = [fa.decode_latent_paged(*d, SCALE) for _ in range(200)]
+    for out, lse in got:
+        assert torch.equal(out, first["out"]) and torch.equal(lse, first["lse"])
+
+
 @pytest.mark.parametrize("rank,H,scale_q", [(512, 16, 8.0), (256, 64, 8.0), (512, 64, 8.0)])
 def test_large_scores(fa, rank, H, scale_q):
     """Scores of tens: the reference maximum moves from tile to tile."""
