@@ -47,6 +47,12 @@ struct LatentFwdParams {
   int* status;
 };
 
+// fp16 only: what bounds |dS| of 128 keys of a head, for the power of two that dS is scaled by.
+struct LatentNorms {
+  float v;     // greatest norm of their rows of V
+  float ds;    // greatest |dO_i| max_j |V_j| of the query tiles that see one of them: |dS| is at most twice that
+};
+
 // Backward: workspace regions, the dQ kernel's results for the dK, dV kernel among them.
 struct LatentBwdParams {
   CUtensorMap tm_q;    // 4-D (d + 64, Sq, H, B), box (64, 64, 1, 1), 128B swizzle
@@ -60,11 +66,13 @@ struct LatentBwdParams {
   CUtensorMap tm_dv;
   CUtensorMap tm_part; // fp32 (64, Skv, H, B), box (32, 32, 1, 1), 128B swizzle
   HeadView dk_rope;
+  HeadView v;          // (read directly for fp16's norms)
   const float* lse;    // [B*H][Sq]
-  float* lse2;         // [B*H][Sq_pad]  LSE log2(e), +inf on rows that see nothing
+  float* lse2;         // [B*H][Sq_pad]  LSE log2(e) less kShiftP, +inf on rows that see nothing
   float* delta;        // [B*H][Sq_pad]  <dO, O>
   int2* ranges;        // [B][Sq_pad / 64] least and greatest key of 64 rows' spans, (max, 0): none
-  float* part;         // [B*H][Skv][64] each head's unscaled gradient of the shared key part
+  float* part;         // [B*H][Skv][64] each head's unscaled gradient of the shared key part; in fp16, until
+                       // it is written, the first two of each 128 keys hold LatentNorms
   LatentMask mask;
   int B, H, Sq_pad;
   float scale, scale_log2;

@@ -197,8 +197,8 @@ int fa_bwd_latent(const fa_view* q, const fa_view* k, const fa_view* k_rope, con
   if (rc != FA_OK) return rc;
   LatentBwdParams p;
   std::memset(&p, 0, sizeof(p));
-  HeadView vq, vk, vr, vv, vo, vg, vdq, vdk, vdv;
-  if ((rc = take({{q, H, Sq, &vq}, {k, H, Skv, &vk}, {k_rope, 1, Skv, &vr}, {v, H, Skv, &vv}, {out, H, Sq, &vo},
+  HeadView vq, vk, vr, vo, vg, vdq, vdk, vdv;
+  if ((rc = take({{q, H, Sq, &vq}, {k, H, Skv, &vk}, {k_rope, 1, Skv, &vr}, {v, H, Skv, &p.v}, {out, H, Sq, &vo},
                   {dout, H, Sq, &vg}, {dq, H, Sq, &vdq}, {dk, H, Skv, &vdk}, {dk_rope, 1, Skv, &p.dk_rope},
                   {dv, H, Skv, &vdv}}, B, dtype)) != FA_OK)
     return rc;
@@ -213,7 +213,7 @@ int fa_bwd_latent(const fa_view* q, const fa_view* k, const fa_view* k_rope, con
   if (!make_map(&p.tm_q, vq, B, H, Sq, d + kRope, 64, bf16) || !make_map(&p.tm_do, vg, B, H, Sq, d, 64, bf16) ||
       !make_map(&p.tm_o, vo, B, H, Sq, d, 64, bf16) ||
       !make_map(&p.tm_k, vk, B, H, Skv, d, 64, bf16) || !make_map(&p.tm_kr, vr, B, 1, Skv, kRope, 64, bf16) ||
-      !make_map(&p.tm_v, vv, B, H, Skv, d, 64, bf16) || !make_store_map(&p.tm_dq, vdq, B, H, Sq, d + kRope, bf16) ||
+      !make_map(&p.tm_v, p.v, B, H, Skv, d, 64, bf16) || !make_store_map(&p.tm_dq, vdq, B, H, Sq, d + kRope, bf16) ||
       !make_store_map(&p.tm_dk, vdk, B, H, Skv, d, bf16) || !make_store_map(&p.tm_dv, vdv, B, H, Skv, d, bf16) ||
       !make_part_map(&p.tm_part, p.part, B, H, Skv))
     return FA_ERR_TMA;

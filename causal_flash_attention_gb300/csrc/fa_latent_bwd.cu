@@ -13,6 +13,14 @@
 //               it with L and the rows' key ranges for the second.
 //   2. dK, dV:  a CTA per 128 keys of a head walks the query rows, 64 at a time.
 //   3. dKR:     adds up the heads' parts, in head order.
+//
+// P and dS are rounded to the inputs' type as operands of their products. bf16 has fp32's exponents; in
+// fp16 dS is scaled by a power of two first, which the results leave with, since it has the size of
+// dO: at |dO| = 1e-4 over 2048 keys it would be a few of fp16's least steps (dQ's and dK's errors 3 to 5
+// times an output's own rounding), with short rows and |dO| |V| = 3e5 past its largest value. |dS_ij| is at most
+// 2 |dO_i| max_j |V_j| (the norm of O_i is no greater than V's), so one more kernel in front takes the
+// norms of V's rows, 128 keys a block; dQ scales each row by its own bound, dK and dV all rows by the greatest
+// of the query tiles that see one of their keys. P, at most 1, is scaled by 2^kShiftP for dV.
 // Warp roles of 1 and 2: warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 softmax
 // gradient, two warps a tensor-memory lane quarter with half the columns each (four with 16 columns
 // each: 1 and 2% slower), in 1 also warp 10 MMA issuer of dQ. P and dS
@@ -49,6 +57,19 @@ __device__ __forceinline__ void drain_wait_b(uint32_t bar, uint32_t parity, int*
   }
 }
 
+// The shift e for which 2 bound 2^e < 2^15, half of fp16's range; bound >= 0.
+__device__ __forceinline__ int shift_for(float bound) {
+  const int e = 13 - (static_cast<int>(__float_as_uint(bound) >> 23) - 127);
+  return min(max(e, -64), 64);   // (no bound at all, or one that is not finite)
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+template <bool kBf16>
+constexpr int kShiftP = kBf16 ? 0 : 12;   // of P and L as the dK, dV kernel takes them
+__device__ __forceinline__ LatentNorms* norms_of(const LatentBwdParams& p, int bh, int key_tile) {
+  return reinterpret_cast<LatentNorms*>(
+      p.part + (static_cast<size_t>(bh) * p.mask.Skv + static_cast<size_t>(key_tile) * kTileN) * kRope);
+}
+
 template <bool kBf16>
 __device__ __forceinline__ float dot16(const uint4& a, const uint4& b, float s) {
   const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
@@ -59,6 +80,44 @@ __device__ __forceinline__ float dot16(const uint4& a, const uint4& b, float s) 
     s = fmaf(u.y, v.y, s);
   }
   return s;
+}
+
+// --------------------------------------------------------------- V's norms --
+// The greatest norm of 128 rows of V of a head (fp16 only); a row is D / 8 lanes. Reads V once: 24.6 MB
+// at 2 x 16 heads, 2999 tokens.
+constexpr int kThreadsN = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsN) latent_norms_kernel(const __grid_constant__ LatentBwdParams p) {
+  __shared__ uint32_t tops[kThreadsN / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int BH = p.B * p.H;
+  const int tile = static_cast<int>(blockIdx.x) / BH, bh = static_cast<int>(blockIdx.x) % BH;
+  const int b = bh / p.H, h = bh % p.H;
+  constexpr int kLanes = D / 8, kRowsPass = kThreadsN / kLanes, N = kTileN / kRowsPass;
+  const int r0 = tile * kTileN + static_cast<int>(threadIdx.x) / kLanes;
+  const uint16_t* src = static_cast<const uint16_t*>(p.v.data) + b * p.v.sb + h * p.v.sh + threadIdx.x % kLanes * 8;
+  uint4 x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int row = r0 + i * kRowsPass;
+    x[i] = row < p.mask.Skv ? *reinterpret_cast<const uint4*>(src + row * p.v.ss) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  uint32_t top = 0;   // of squares, as bits: not negative
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float s = dot16<false>(x[i], x[i], 0.f);
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    top = max(top, __float_as_uint(s));
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = top;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < kThreadsN / 32; ++w) top = max(top, tops[w]);
+  *norms_of(p, bh, tile) = LatentNorms{sqrtf(__uint_as_float(top)), 0.f};
 }
 
 // --------------------------------------------------------------------- dQ --
@@ -89,7 +148,8 @@ struct LatDqCfg {
   static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kOffSpan = kOffMisc + 16;        // 4 warps' (begin, end)
   static constexpr int kOffDelta = kOffSpan + 32;       // two buffers of [2][128] halves of D
-  static constexpr int kSmemBytes = kOffDelta + 2048;
+  static constexpr int kOffNorm = kOffDelta + 2048;     // fp16: [2][128] halves of |dO|^2, the norm of V
+  static constexpr int kSmemBytes = kOffNorm + 1024 + 16;
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
   static constexpr int kColDq = 128, kColDs = kColDq + kW, kColQ = kColDs + 32, kColDO = kColQ + kW / 2;
   static_assert(kColDO + D / 2 <= 512, "tensor memory");
@@ -110,6 +170,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
   int2* ranges = reinterpret_cast<int2*>(smem + Cfg::kOffSpan);
   float* halves = reinterpret_cast<float*>(smem + Cfg::kOffDelta);
+  float* norms = reinterpret_cast<float*>(smem + Cfg::kOffNorm);
 
   const uint32_t bar0 = sbase + Cfg::kOffBar;
   auto full = [&](int s) { return bar0 + 8 * s; };
@@ -213,6 +274,15 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   if (warp == 0 && lane == 0)
     for (int j = 0; j < min(n, Cfg::kFirst); ++j) load(j);
   bool ok = true;
+  if (!kBf16 && warp == 0) {   // the greatest norm of V's key tiles
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float top = 0.f;
+    for (int t = tile0 * KT / kTileN + lane; t * kTileN < hi; t += 32) top = fmaxf(top, __ldcg(&norms_of(p, bh, t)->v));
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    if (lane == 0) norms[256] = top;
+    __syncwarp();
+    asm volatile("bar.arrive 1, 288;" ::: "memory");
+  }
   if (soft) {
     // This thread's halves of its row of Q and dO into tensor memory, its half of D, and L: each as
     // it lands, so that S and dP of the first tile are formed meanwhile.
@@ -244,19 +314,34 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     put(q_full, s_free, Cfg::kColQ, Cfg::kOffQ, half * QU, std::integral_constant<int, QU>{});
     put(do_full, dp_free, Cfg::kColDO, Cfg::kOffDO, half * OU, std::integral_constant<int, OU>{});
     if (ok) ok = warp_wait(o_full, 0, abort_flag, p.status);
-    float d = 0.f;
+    float d = 0.f, square = 0.f;
     if (ok) {
 #pragma unroll
-      for (int u = 0; u < OU; ++u)
-        d = dot16<kBf16>(unit(Cfg::kOffO, half * OU + u), unit(Cfg::kOffDO, half * OU + u), d);
+      for (int u = 0; u < OU; ++u) {
+        const uint4 g = unit(Cfg::kOffDO, half * OU + u);
+        d = dot16<kBf16>(unit(Cfg::kOffO, half * OU + u), g, d);
+        if constexpr (!kBf16) square = dot16<kBf16>(g, g, square);
+      }
     }
     halves[half * 128 + rr] = d;
+    if constexpr (!kBf16) norms[half * 128 + rr] = row_hi > 0 ? square : 0.f;   // a row that sees nothing has no dS
     fence_proxy_async_smem();   // the copies that follow into these stages come after the reads
     __syncwarp();
     if (lane == 0) mbar_arrive(o_done);
-    asm volatile("bar.sync 1, 256;" ::: "memory");   // the halves of D, among these warps
+    // the halves of D, among these warps; fp16: of |dO|^2, and V's norm from warp 0
+    asm volatile("bar.sync 1, %0;" ::"n"(kBf16 ? 256 : 288) : "memory");
   }
 
+  // The greatest bound of the rows, for dK and dV of the keys that they see. (In warp 0 or 10, which have
+  // the time, the whole kernel is slower: packed documents 53.6 -> 57.5 us, here 54.3.)
+  if (!kBf16 && warp == 2) {
+    float top = 0.f;
+    for (int i = lane; i < kTileM; i += 32) top = fmaxf(top, norms[i] + norms[128 + i]);
+    const uint32_t bound = __reduce_max_sync(0xffffffffu, __float_as_uint(sqrtf(top) * norms[256]));
+    for (int t = tile0 * KT / kTileN + lane; t * kTileN < hi; t += 32)
+      atomicMax(reinterpret_cast<unsigned*>(&norms_of(p, bh, t)->ds), bound);
+    __syncwarp();
+  }
   // A role that gives up: every MMA it has issued must finish before the tensor memory is released.
   auto finish = [&](uint32_t bar) {
     if (!ok) {
@@ -333,6 +418,13 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   } else {
     // ===================== softmax gradient, two threads a row =====================
     float delta = halves[rr] + halves[128 + rr];
+    // fp16: P, and with it dS, is scaled by 2^e, a part of the exponent
+    float up = 1.f, down = 1.f;
+    if constexpr (!kBf16) {
+      const int e = shift_for(sqrtf(norms[rr] + norms[128 + rr]) * norms[256]);
+      up = static_cast<float>(e);
+      down = pow2(-e);
+    }
     int n_swap = 0;   // exchanges of half sums with the other warp of the rows
     if (half == 0 && h == 0 && lane == 0 && (quarter & 1) == 0) {
       const int2 u = ranges[quarter], v = ranges[quarter + 1];
@@ -340,7 +432,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           make_int2(min(u.x, v.x), max(u.y, v.y));
     }
     const uint32_t t_s = tmem + lane_off + half * 32;
-    const float c = p.scale_log2;
+    const float c = p.scale_log2, l2e = kBf16 ? l2 : l2 - up;
     for (int j = 0; ok && j < n; ++j) {
       ok = __all_sync(0xffffffffu, mbar_wait(s_full, j & 1, abort_flag, p.status));
       if (!ok) break;
@@ -359,7 +451,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         for (int i = 0; i < 32; ++i)
           if (!((see >> i) & 1u)) s[i] = __float_as_uint(-INFINITY);
       }
-      const uint64_t c2 = f2_pack(c, c), nl2 = f2_pack(-l2, -l2);
+      const uint64_t c2 = f2_pack(c, c), nl2 = f2_pack(-l2e, -l2e);
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {   // P, in fp32
         float x0, x1;
@@ -395,7 +487,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(swap(quarter), n_swap & 1, abort_flag, p.status));
         if (!ok) break;
         ++n_swap;
-        if (inside) delta = buf[rr] + buf[128 + rr];
+        if (inside) delta = (buf[rr] + buf[128 + rr]) * down;
       }
       const uint64_t nd2 = f2_pack(-delta, -delta);
       uint32_t ds[16];
@@ -423,7 +515,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       tc_fence_after();
       if (half == 0) {
         const size_t at = static_cast<size_t>(bh) * p.Sq_pad + row;
-        p.lse2[at] = l2;
+        p.lse2[at] = l2 - kShiftP<kBf16>;
         p.delta[at] = delta;
       }
       // through the ring's first stages, which every product has read (or none was loaded into)
@@ -440,7 +532,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
         if (row - lane < p.mask.Sq)
-          store_box<kBf16>(box + cc * kStoreBytes, &p.tm_dq, o, p.scale, lane, col, row - lane, h, b);
+          store_box<kBf16>(box + cc * kStoreBytes, &p.tm_dq, o, p.scale * down, lane, col, row - lane, h, b);
       }
       if (lane == 0) bulk_wait_all();
     }
@@ -649,6 +741,14 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem + lane_off + 320 + half * 32;
     const float c = p.scale_log2;
+    float up = 1.f, down = 1.f;   // fp16: dS is scaled, P with it by 2^kShiftP
+    if constexpr (!kBf16) {
+      if (n > 0) {
+        const int e = shift_for(__ldcg(&norms_of(p, bh, kv0 / kTileN)->ds));
+        up = pow2(e - kShiftP<kBf16>);
+        down = pow2(-e);
+      }
+    }
     // the span of query column `lane` of this warp's half of step g
     auto span_of = [&](int g) { return p.mask.span(b, (i0 + g) * R + half * 32 + lane); };
     int2 sp = n > 0 ? span_of(0) : make_int2(0, 0);
@@ -683,8 +783,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         x0 = ex2(x0);
         x1 = ex2(x1);
         pk[e / 2] = pack2<kBf16>(x0, x1);
-        s[e] = __float_as_uint(x0);
-        s[e + 1] = __float_as_uint(x1);
+        s[e] = __float_as_uint(kBf16 ? x0 : x0 * up);
+        s[e + 1] = __float_as_uint(kBf16 ? x1 : x1 * up);
       }
       ok = __all_sync(0xffffffffu, mbar_wait(dp_full, g & 1, abort_flag, p.status));
       if (!ok) break;
@@ -724,7 +824,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       tc_fence_after();
       // warps 2-5 write dK, warps 6-9 dV, each half the shared part, through the stages of Q and dO
       const CUtensorMap* tm = half == 0 ? &p.tm_dk : &p.tm_dv;
-      const float f = half == 0 ? p.scale : 1.f;
+      const float f = half == 0 ? p.scale * down : pow2(-kShiftP<kBf16>);
       uint8_t* box = smem + Cfg::kOffQ + (warp - 2) * Cfg::kStoreWarp;
       auto load = [&](int col, uint32_t (&o)[32]) {
         if (n > 0) {
@@ -738,7 +838,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (key0 < p.mask.Skv) {
         uint32_t o[32];
         load(128 + D + half * 32, o);
-        store_box_f32(box, &p.tm_part, o, lane, half * 32, key0, h, b);
+        store_box_f32(box, &p.tm_part, o, down, lane, half * 32, key0, h, b);
 #pragma unroll
         for (int cc = 0; cc < D / 32; ++cc) {
           load((half == 0 ? 128 : 0) + cc * 32, o);
@@ -801,6 +901,11 @@ cudaError_t launch_impl(const LatentBwdParams& p0, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   LatentBwdParams p = p0;
   const long long bh = static_cast<long long>(p.B) * p.H;
+  if constexpr (!kBf16) {
+    e = launch_dependent(latent_norms_kernel<D>, dim3(static_cast<unsigned>(bh * ((p.mask.Skv + kTileN - 1) / kTileN))),
+                         dim3(kThreadsN), 0, stream, p);
+    if (e != cudaSuccess) return e;
+  }
   p.n_units = p.Sq_pad / kTileM;
   e = launch_dependent(dq, dim3(static_cast<unsigned>(bh * p.n_units)), dim3(kThreadsQ),
                        LatDqCfg<D>::kSmemBytes, stream, p);

@@ -33,13 +33,14 @@ __device__ __forceinline__ void store_box(uint8_t* box, const CUtensorMap* tm, c
   __syncwarp();
 }
 
-// The same in fp32, unscaled: 128-byte rows with the 128-byte swizzle.
-__device__ __forceinline__ void store_box_f32(uint8_t* box, const CUtensorMap* tm, const uint32_t (&o)[32], int lane,
-                                              int col, int row, int h, int b) {
+// The same in fp32: 128-byte rows with the 128-byte swizzle.
+__device__ __forceinline__ void store_box_f32(uint8_t* box, const CUtensorMap* tm, const uint32_t (&o)[32], float f,
+                                              int lane, int col, int row, int h, int b) {
 #pragma unroll
   for (int u = 0; u < 8; ++u)
-    *reinterpret_cast<uint4*>(box + lane * 128 + ((u ^ (lane & 7)) << 4)) =
-        make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+    *reinterpret_cast<float4*>(box + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+        make_float4(__uint_as_float(o[4 * u]) * f, __uint_as_float(o[4 * u + 1]) * f,
+                    __uint_as_float(o[4 * u + 2]) * f, __uint_as_float(o[4 * u + 3]) * f);
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {

@@ -416,7 +416,9 @@ int fa_fwd_latent(const fa_view* q, const fa_view* k, const fa_view* k_rope, con
 /*
  * Backward of fa_fwd_latent: dq, dk, dv, views like q, k, v, and dk_rope like k_rope, summed
  * over the heads. Same bits on every call. Rows that see nothing contribute nothing; keys
- * that no row sees get zeros. Views that are written must not overlap anything.
+ * that no row sees get zeros. Views that are written must not overlap anything. In FA_F16
+ * dout may have any size: what is rounded inside is scaled by powers of two, and only the
+ * gradients themselves have to fit the type.
  * workspace: caller-owned, 256-byte aligned, contents on entry without meaning; calls that
  * may overlap on the GPU need one each.
  */

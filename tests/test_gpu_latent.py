@@ -141,3 +141,62 @@ def test_rows_of_few_keys(fa, d):
     for n in ("dq", "dk", "dk_rope"):
         step = np.linalg.norm(torch.from_numpy(want[n]).half().double().numpy() - want[n])
         assert np.linalg.norm(f64(got[n]) - want[n]) < 1.5 * step, n
+
+
+def rms(x):
+    return np.sqrt((x * x).mean())
+
+
+@pytest.mark.parametrize("d,n,size,large", [(64, 2048, 2.0 ** -13, 1.0), (128, 2048, 2.0 ** -13, 1.0),
+                                            (128, 1024, 2.0 ** -18, 1.0), (64, 300, 2.0 ** 11, 16.0),
+                                            (128, 300, 2.0 ** 11, 16.0)])
+def test_fp16_gradients_of_any_size(fa, d, n, size, large):
+    """Gradients are linear in dout, and so are the bounds for a dout of size one, but for the
+    outputs' own rounding, half of fp16's least step 2^-24 where they are small. At 1e-4 over 2048
+    keys dS is a few such steps itself; with large values and dout short rows' dS are past fp16's
+    largest value, while no gradient is."""
+    x = make(1, 2, n, n, d, "fp16", seed=d + n)
+    x[3] = x[3] * large
+    if large > 1:
+        x[:3] = [t * 0.25 for t in x[:3]]
+    x[4] = (x[4].float().clamp(-2, 2) * size).half()
+    got = run(fa, x)
+    q, k, kr, v, do = (f64(t) for t in x)
+    end = np.arange(1, n + 1)[None]
+    want = ops.latent_attention(q, k, kr, v, np.zeros_like(end), end, (d + 64) ** -0.5, do / size, half_step(torch.float16))
+    for name in ("dq", "dk", "dk_rope", "dv"):
+        ref = want[name] * size
+        assert np.abs(ref).max() < 65504
+        check(name, got[name], ref, want[name + "_tol"] * size + 1.01 * 2.0 ** -25)
+        if large == 1:
+            own = rms(torch.from_numpy(ref).half().double().numpy() - ref)
+            assert rms(f64(got[name]) - ref) < 1.5 * own, name
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp16_gradients_of_rows_that_weigh_differently(fa, d):
+    """Rows whose dout is 2^-20 of the others': dq is each row's own, and so is its bound."""
+    x = make(2, 2, 700, 700, d, "fp16", seed=d)
+    x[1:3] = [t * 8 for t in x[1:3]]         # gradients well above fp16's least steps
+    x[0] = x[0] * 0.125
+    size = torch.where(torch.arange(700) % 3 == 0, 1.0, 2.0 ** -20)[:, None]
+    x[4] = (x[4].float() * size).half()
+    spans = fa.key_spans(2, 700, doc_lens=[[300, 1, 399], [64, 600, 36]], window=500)
+    got = run(fa, x, spans)
+    compare({n: got[n] for n in ("dk", "dk_rope", "dv", "dq")}, x, spans)
+    q, k, kr, v, do = (f64(t) for t in x)
+    size = size.double().numpy()
+    want = ops.latent_attention(q, k, kr, v, *(t.numpy() for t in spans), (d + 64) ** -0.5, do / size,
+                                half_step(torch.float16))
+    check("dq", got["dq"], want["dq"] * size, want["dq_tol"] * size + 1.01 * 2.0 ** -25)
+
+
+@pytest.mark.parametrize("fill", [0xff, 0x7f, 0x00])
+def test_fp16_workspace_contents_have_no_meaning(fa, fill):
+    x = [to_dev(t) for t in make(2, 3, 300, 410, 64, "fp16", seed=3)]
+    out, lse = fa.attention_latent_forward(*x[:4])
+    want = fa.attention_latent_backward(*x[:4], out, x[4], lse)
+    ws = torch.full((fa.fa_bwd_latent_workspace_bytes(2, 3, 300, 410, 64),), fill, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        got = fa.attention_latent_backward(*x[:4], out, x[4], lse, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
