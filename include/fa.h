@@ -451,7 +451,8 @@ size_t fa_bwd_latent_workspace_bytes(int B, int H, int Sq, int Skv, int d);
  * tokens, and new token t (at key seq_lens[b] - Sq + t) where bit t of tree_masks[b][s] is
  * set, its own included; bits from Sq on are not looked at. A cache row that is not finite and
  * that some new token of its sequence sees may give NaN to every new token of the sequence, also
- * to one that does not see it: what a row hides it multiplies by 0.
+ * to one that does not see it: what a row hides it multiplies by 0. A row that none of them sees
+ * may hold anything, a drafted token's that no mask has among them (trees padded to one Sq).
  *
  * q is a view with positive strides, as for fa_fwd_latent. rank is 256 or 512, H * Sq <= 1024,
  * block_size and max_blocks as for fa_fwd_ragged_paged, with tree_masks Sq <= 64 and no window

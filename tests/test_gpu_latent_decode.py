@@ -169,3 +169,22 @@ def test_strided_queries(fa):
     q = x[0].to(DEV).permute(1, 0, 2, 3).contiguous().permute(1, 0, 2, 3)
     out, lse = fa.decode_latent_paged(q, *(t.to(DEV) for t in x[1:]), SCALE)
     assert torch.equal(out, want["out"]) and torch.equal(lse, want["lse"])
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf")])
+@pytest.mark.parametrize("H,rank,Sq", [(16, 512, 8), (40, 256, 8), (3, 512, 64)])
+def test_drafted_tokens_that_nobody_sees(fa, fill, H, rank, Sq):
+    """A batch's trees padded to the same number of tokens, and a token that no mask has: their cache
+    rows may hold anything, as what lies past a sequence may."""
+    lens = [Sq, 70, 300, 64 + Sq - 3]
+    real = [Sq, Sq - 3, 5, 1]                # tokens of each tree; the rest see the prefix only
+    masks = fa.tree_masks([[-1 if s == 0 else (s - 1) // 2 for s in range(Sq)]] * 4)[0]
+    x = make(lens, H, Sq, rank, "bf16", 16, 21)
+    for b, n in enumerate(real):
+        masks[b, n:] = 0
+        masks[b] &= ~4 if b == 1 else -1     # token 2 of a tree: not even its own row sees it
+        for t in [*range(n, Sq)] + [2] * (b == 1):
+            j = lens[b] - Sq + t
+            x[1][x[2][b, j // 16], j % 16] = fill
+    got = run(fa, x, tree_masks=masks)
+    compare(got, x, tree_masks=masks)
