@@ -122,16 +122,6 @@ struct BwdCfg {
   static_assert(kSmemBytesSpan <= 232448, "shared memory of one CTA");
 };
 
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, int* status) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > kDrainLimitCycles) {
-      atomicOr(status, kStatusWaitTimeout);
-      return;
-    }
-  }
-}
-
 template <typename T>
 __device__ __forceinline__ float to_f(T x);
 template <>

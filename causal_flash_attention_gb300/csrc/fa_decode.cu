@@ -67,16 +67,6 @@ struct DecCfg {
   static constexpr int kSmemBytes = kOffMisc + 16 + 1024;   // + alignment slack
 };
 
-__device__ __forceinline__ void drain_wait_d(uint32_t bar, uint32_t parity, int* status) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > kDrainLimitCycles) {
-      atomicOr(status, kStatusWaitTimeout);
-      return;
-    }
-  }
-}
-
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kDecThreads, 1)
     fa_decode_kernel(const __grid_constant__ DecodeParams p) {
@@ -204,8 +194,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       // let every copy already issued land before the CTA releases its memory
       for (int jj = max(0, j - NS); jj < j; ++jj) {
         const uint32_t par = static_cast<uint32_t>(jj / NS) & 1;
-        drain_wait_d(k_full(jj % NS), par, p.status);
-        drain_wait_d(v_full(jj % NS), par, p.status);
+        drain_wait(k_full(jj % NS), par, p.status);
+        drain_wait(v_full(jj % NS), par, p.status);
       }
     }
   } else if (warp == 1) {
@@ -260,7 +250,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       if (!ok) {
         // every MMA issued so far must finish before the TMEM is released
         tc_commit(drain);
-        drain_wait_d(drain, 0, p.status);
+        drain_wait(drain, 0, p.status);
       }
     }
   } else {

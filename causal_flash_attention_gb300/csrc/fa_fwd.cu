@@ -117,17 +117,6 @@ struct FwdBars {
   __device__ uint32_t sfr(int t) const { return s_free + 8 * t; }
 };
 
-// Bounded wait used on the abort path: only the limit can end it.
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, int* status) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > kDrainLimitCycles) {
-      atomicOr(status, kStatusWaitTimeout);
-      return;
-    }
-  }
-}
-
 // kSpan: 0 causal or all keys; 1 key spans; 2 key spans with a cap or a bias
 template <int D, bool kBf16, int T, int kSpan>
 __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, 3 - T)

@@ -64,16 +64,6 @@ struct PairCfg {
   static constexpr int kSmemBytes = kOffMisc + 16 + 1024;   // + alignment slack
 };
 
-__device__ __forceinline__ void drain_wait_pair(uint32_t bar, uint32_t parity, int* status) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > kDrainLimitCycles) {
-      atomicOr(status, kStatusWaitTimeout);
-      return;
-    }
-  }
-}
-
 template <bool kBf16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     fa_fwd_pair_kernel(const __grid_constant__ FwdParams p) {
@@ -201,11 +191,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 mbar_wait_cluster(v_empty(jj % NS), par, abort_flag, p.status);
       }
       if (!clean) {
-        if (q_bytes) drain_wait_pair(q_full, 0, p.status);
+        if (q_bytes) drain_wait(q_full, 0, p.status);
         for (int jj = max(0, j - NS); jj < j; ++jj) {
           const uint32_t par = static_cast<uint32_t>(jj / NS) & 1;
-          drain_wait_pair(k_full(jj % NS), par, p.status);
-          drain_wait_pair(v_full(jj % NS), par, p.status);
+          drain_wait(k_full(jj % NS), par, p.status);
+          drain_wait(v_full(jj % NS), par, p.status);
         }
       }
     }
@@ -292,7 +282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (!ok) {
         // every MMA issued so far must finish before either CTA frees its memory
         tc_commit_pair(drain, 1);
-        drain_wait_pair(drain, 0, p.status);
+        drain_wait(drain, 0, p.status);
       }
     }
   } else {

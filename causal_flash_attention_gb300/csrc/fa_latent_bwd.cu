@@ -47,16 +47,6 @@ namespace {
 constexpr int kThreadsQ = 352, kThreadsB = 320;   // of the dQ kernel, of the dK, dV kernel
 constexpr float kLog2eB = 1.4426950408889634f;
 
-__device__ __forceinline__ void drain_wait_b(uint32_t bar, uint32_t parity, int* status) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > kDrainLimitCycles) {
-      atomicOr(status, kStatusWaitTimeout);
-      return;
-    }
-  }
-}
-
 // The shift e for which 2 bound 2^e < 2^15, half of fp16's range; bound >= 0.
 __device__ __forceinline__ int shift_for(float bound) {
   const int e = 13 - (static_cast<int>(__float_as_uint(bound) >> 23) - 127);
@@ -346,7 +336,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   auto finish = [&](uint32_t bar) {
     if (!ok) {
       elected([&] { tc_commit(bar); });
-      drain_wait_b(bar, 0, p.status);
+      drain_wait(bar, 0, p.status);
     }
     __syncwarp();
   };
@@ -360,10 +350,10 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         load(j);
       }
       if (*abort_flag) {   // let every copy already issued land before the CTA releases its memory
-        drain_wait_b(q_full, 0, p.status);
-        drain_wait_b(do_full, 0, p.status);
-        drain_wait_b(o_full, 0, p.status);
-        for (int i = max(0, j - NS); i < j; ++i) drain_wait_b(full(i % NS), (i / NS) & 1, p.status);
+        drain_wait(q_full, 0, p.status);
+        drain_wait(do_full, 0, p.status);
+        drain_wait(o_full, 0, p.status);
+        for (int i = max(0, j - NS); i < j; ++i) drain_wait(full(i % NS), (i / NS) & 1, p.status);
       }
     }
   } else if (warp == 1) {
@@ -666,7 +656,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   if (warp == 0) {
     // ===================== TMA producer =====================
     if (lane == 0) {
-      if (n == 0) drain_wait_b(kv_full, 0, p.status);
+      if (n == 0) drain_wait(kv_full, 0, p.status);
       int g = 0;
       for (; g < n; ++g) {
         const int st = g % NS;
@@ -682,8 +672,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         bulk_load(sbase + Cfg::kOffRow + st * (2 * R * 4) + R * 4, p.delta + at, R * 4, f);
       }
       if (*abort_flag) {
-        drain_wait_b(kv_full, 0, p.status);
-        for (int j = max(0, g - NS); j < g; ++j) drain_wait_b(full(j % NS), (j / NS) & 1, p.status);
+        drain_wait(kv_full, 0, p.status);
+        for (int j = max(0, g - NS); j < g; ++j) drain_wait(full(j % NS), (j / NS) & 1, p.status);
       }
     }
   } else if (warp == 1) {
@@ -730,7 +720,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       }
       if (!ok) {
         elected([&] { tc_commit(drain); });
-        drain_wait_b(drain, 0, p.status);
+        drain_wait(drain, 0, p.status);
       }
       __syncwarp();
     }

@@ -77,16 +77,6 @@ struct LatDecCfg {
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 };
 
-__device__ __forceinline__ void drain_wait_d(uint32_t bar, uint32_t parity, int* status) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > kDrainLimitCycles) {
-      atomicOr(status, kStatusWaitTimeout);
-      return;
-    }
-  }
-}
-
 // Position in a ring of N slots, and the parity of its use.
 template <int N>
 struct Ring {
@@ -259,7 +249,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         if (!ok) mbar_arrive(full(n_t++ % NT));
         const int most = __reduce_max_sync(lanes, n_t);
         for (; n_t < most; ++n_t) mbar_arrive(full(n_t % NT));
-        for (int i = max(0, most - NT); i < most; ++i) drain_wait_d(full(i % NT), (i / NT) & 1, p.status);
+        for (int i = max(0, most - NT); i < most; ++i) drain_wait(full(i % NT), (i / NT) & 1, p.status);
       }
     }
     __syncwarp();
@@ -364,7 +354,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     if (!ok) {
       // every MMA issued so far must finish before the TMEM is released
       elected([&] { tc_commit(drain); });
-      drain_wait_d(drain, 0, p.status);
+      drain_wait(drain, 0, p.status);
     }
     __syncwarp();
   } else {
@@ -591,7 +581,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       head = false;
     }
     // the last queries asked for land before the CTA releases its memory
-    if (tid == 0 && *abort_flag && share.begin < share.end) drain_wait_d(q_ready, (n_q - 1) & 1, p.status);
+    if (tid == 0 && *abort_flag && share.begin < share.end) drain_wait(q_ready, (n_q - 1) & 1, p.status);
   }
 
   tc_fence_before();

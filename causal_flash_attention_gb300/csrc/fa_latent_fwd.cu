@@ -57,16 +57,6 @@ struct LatFwdCfg {
   static_assert(kSmemBytes <= 232448 && (T == 2 || 2 * (kSmemBytes + 1024) <= 233472), "shared memory");
 };
 
-__device__ __forceinline__ void drain_wait_l(uint32_t bar, uint32_t parity, int* status) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > kDrainLimitCycles) {
-      atomicOr(status, kStatusWaitTimeout);
-      return;
-    }
-  }
-}
-
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPerSm)
     latent_fwd_kernel(const __grid_constant__ LatentFwdParams p) {
@@ -178,7 +168,7 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
   if (warp == 0) {
     // ===================== TMA producer =====================
     if (lane == 0) {
-      if (n_load == 0) drain_wait_l(q_full, 0, p.status);   // no product waits for the queries
+      if (n_load == 0) drain_wait(q_full, 0, p.status);   // no product waits for the queries
       // units of the ring, in order: K or V of a tile
       auto is_k = [](int u) { return Cfg::kSepP ? u == 0 || u % 2 == 1 : u % 2 == 0; };
       auto tile_of = [&](int u) { return Cfg::kSepP ? (u == 0 ? 0 : is_k(u) ? (u + 1) / 2 : u / 2 - 1) : u / 2; };
@@ -225,9 +215,9 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
       }
       if (*abort_flag) {
         // let every copy already issued land before the CTA releases its memory
-        drain_wait_l(q_full, 0, p.status);
-        for (int j = max(0, jk - 2); j < jk; ++j) drain_wait_l(k_full(j & 1), (j >> 1) & 1, p.status);
-        for (int j = max(0, jv - 2); j < jv; ++j) drain_wait_l(v_full(j & 1), (j >> 1) & 1, p.status);
+        drain_wait(q_full, 0, p.status);
+        for (int j = max(0, jk - 2); j < jk; ++j) drain_wait(k_full(j & 1), (j >> 1) & 1, p.status);
+        for (int j = max(0, jv - 2); j < jv; ++j) drain_wait(v_full(j & 1), (j >> 1) & 1, p.status);
       }
     }
   } else if (warp == 1) {
@@ -355,7 +345,7 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
       if (!ok) {
         // every MMA issued so far must finish before the TMEM is released
         elected([&] { tc_commit(drain); });
-        drain_wait_l(drain, 0, p.status);
+        drain_wait(drain, 0, p.status);
       }
       __syncwarp();
     }

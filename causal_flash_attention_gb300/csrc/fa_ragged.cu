@@ -119,8 +119,8 @@ __device__ __forceinline__ void produce(const RaggedParams& p, Segments& seg, ui
     // let every copy already issued land before the CTA releases its memory
     for (int gg = max(0, g - kStages); gg < g; ++gg) {
       const uint32_t par = static_cast<uint32_t>(gg / kStages) & 1;
-      drain_wait_r(k_full(gg % kStages), par, p.status);
-      drain_wait_r(v_full(gg % kStages), par, p.status);
+      drain_wait(k_full(gg % kStages), par, p.status);
+      drain_wait(v_full(gg % kStages), par, p.status);
     }
   }
 }
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) {
         // every MMA issued so far must finish before the TMEM is released
         tc_commit(drain);
-        drain_wait_r(drain, 0, p.status);
+        drain_wait(drain, 0, p.status);
       }
     }
   } else {
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) {
         // every MMA issued so far must finish before the TMEM is released
         tc_commit(drain);
-        drain_wait_r(drain, 0, p.status);
+        drain_wait(drain, 0, p.status);
       }
     }
   } else {

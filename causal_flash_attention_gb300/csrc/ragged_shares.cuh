@@ -15,16 +15,6 @@ namespace {
 
 constexpr int kRaggedThreads = 192;
 
-__device__ __forceinline__ void drain_wait_r(uint32_t bar, uint32_t parity, int* status) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > kDrainLimitCycles) {
-      atomicOr(status, kStatusWaitTimeout);
-      return;
-    }
-  }
-}
-
 // Keys of one sequence that any of its rows sees, and their tiles.
 struct SeqKeys {
   int len, first;     // keys [first, len)
