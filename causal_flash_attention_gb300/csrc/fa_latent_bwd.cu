@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   }
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
+  volatile int* issued = abort_flag + 1;   // tiles that the producer has asked for
   int2* ranges = reinterpret_cast<int2*>(smem + Cfg::kOffSpan);
   float* halves = reinterpret_cast<float*>(smem + Cfg::kOffDelta);
   float* norms = reinterpret_cast<float*>(smem + Cfg::kOffNorm);
@@ -332,29 +333,19 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       atomicMax(reinterpret_cast<unsigned*>(&norms_of(p, bh, t)->ds), bound);
     __syncwarp();
   }
-  // A role that gives up: every MMA it has issued must finish before the tensor memory is released.
-  auto finish = [&](uint32_t bar) {
-    if (!ok) {
-      elected([&] { tc_commit(bar); });
-      drain_wait(bar, 0, p.status);
-    }
-    __syncwarp();
-  };
   if (warp == 0) {
     // ===================== TMA producer =====================
     if (lane == 0) {
       int j = min(n, Cfg::kFirst);
-      if (j < n) ok = mbar_wait(o_done, 0, abort_flag, p.status);   // the other stages are free
+#ifdef FA_WAIT_TEST
+      if (wait_test(kWaitProducer, p.H)) ok = mbar_wait(drain, 0, abort_flag, p.status);
+#endif
+      if (ok && j < n) ok = mbar_wait(o_done, 0, abort_flag, p.status);   // the other stages are free
       for (; ok && j < n; ++j) {
         if (j >= NS && !mbar_wait(empty(j % NS), (j / NS - 1) & 1, abort_flag, p.status)) break;
         load(j);
       }
-      if (*abort_flag) {   // let every copy already issued land before the CTA releases its memory
-        drain_wait(q_full, 0, p.status);
-        drain_wait(do_full, 0, p.status);
-        drain_wait(o_full, 0, p.status);
-        for (int i = max(0, j - NS); i < j; ++i) drain_wait(full(i % NS), (i / NS) & 1, p.status);
-      }
+      *issued = j;
     }
   } else if (warp == 1) {
     // ===================== MMA issuer of S and dP (the whole warp, one lane of it the MMAs) =====================
@@ -364,7 +355,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
 #ifdef FA_WAIT_TEST
       // wait-limit test build: nothing completes this phase before the abort
       // path's own commit, so the wait runs out
-      ok = wait(drain, 0);
+      if (wait_test(kWaitIssuer, p.H)) ok = wait(drain, 0);
 #endif
       auto scores = [&](int j) -> bool {   // S = Q K'_j^T, dP = dO V_j^T
         if (!wait(full(j % NS), (j / NS) & 1)) return false;
@@ -385,7 +376,6 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         return true;
       };
       for (int j = 0; ok && j < n; ++j) ok = scores(j);
-      finish(drain);
     }
   } else if (warp == 10) {
     // ===================== MMA issuer of dQ =====================
@@ -403,7 +393,6 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           tc_commit(dq_done);         // that arrived after the CTA had exited would be a fault)
         });
       }
-      finish(drain2);
     }
   } else {
     // ===================== softmax gradient, two threads a row =====================
@@ -499,6 +488,9 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_full);
     }
+#ifdef FA_WAIT_TEST
+    if (ok && wait_test(kWaitSoftmax, p.H)) ok = warp_wait(drain, 0, abort_flag, p.status);
+#endif
     if (ok && n > 0)
       ok = __all_sync(0xffffffffu, mbar_wait(dq_done, (n - 1) & 1, abort_flag, p.status));
     if (ok) {
@@ -529,6 +521,22 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag) {
+    // A wait ran out, whosever: only now is it known that nothing more is issued. Every copy lands and every
+    // MMA finishes before the CTA releases its memory.
+    if (threadIdx.x == 0) {
+      drain_wait(q_full, 0, p.status);
+      drain_wait(do_full, 0, p.status);
+      drain_wait(o_full, 0, p.status);
+      for (int i = max(0, *issued - NS); i < *issued; ++i) drain_wait(full(i % NS), (i / NS) & 1, p.status);
+    }
+    if (warp == 1 || warp == 10) {
+      const uint32_t bar = warp == 1 ? drain : drain2;
+      elected([&] { tc_commit(bar); });
+      drain_wait(bar, 0, p.status);
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -576,6 +584,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   }
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
+  volatile int* issued = abort_flag + 1;   // tiles that the producer has asked for
   int2* steps = reinterpret_cast<int2*>(smem + Cfg::kOffSteps);
 
   const uint32_t kv_full = sbase + Cfg::kOffBar;
@@ -658,7 +667,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     if (lane == 0) {
       if (n == 0) drain_wait(kv_full, 0, p.status);
       int g = 0;
-      for (; g < n; ++g) {
+      bool ok = true;
+#ifdef FA_WAIT_TEST
+      if (wait_test(kWaitProducer, p.H)) ok = mbar_wait(drain, 0, abort_flag, p.status);
+#endif
+      for (; ok && g < n; ++g) {
         const int st = g % NS;
         if (g >= NS && !mbar_wait(empty(st), (g / NS - 1) & 1, abort_flag, p.status)) break;
         const uint32_t f = full(st), dst = sbase + Cfg::kOffQ + st * Cfg::kStageBytes;
@@ -671,10 +684,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           tma_load_4d(dst + (Cfg::kKChunks + c) * QB, &p.tm_do, f, c * kChunk, y, h, b);
         bulk_load(sbase + Cfg::kOffRow + st * (2 * R * 4) + R * 4, p.delta + at, R * 4, f);
       }
-      if (*abort_flag) {
-        drain_wait(kv_full, 0, p.status);
-        for (int j = max(0, g - NS); j < g; ++j) drain_wait(full(j % NS), (j / NS) & 1, p.status);
-      }
+      *issued = g;
     }
   } else if (warp == 1) {
     // ===================== MMA issuer (the whole warp, one lane of it the MMAs) =====================
@@ -686,7 +696,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       auto wait = [&](uint32_t bar, uint32_t parity) { return warp_wait(bar, parity, abort_flag, p.status); };
       bool ok = wait(kv_full, 0);
 #ifdef FA_WAIT_TEST
-      if (ok) ok = wait(drain, 0);   // runs out, as in the dQ kernel
+      if (ok && wait_test(kWaitIssuer, p.H)) ok = wait(drain, 0);   // runs out, as in the dQ kernel
 #endif
       auto scores = [&](int g) -> bool {   // S^T and dP^T of step g
         if (!wait(full(g % NS), (g / NS) & 1)) return false;
@@ -718,11 +728,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           tc_commit(kd_done);
         });
       }
-      if (!ok) {
-        elected([&] { tc_commit(drain); });
-        drain_wait(drain, 0, p.status);
-      }
-      __syncwarp();
     }
   } else {
     // ===================== softmax gradient, two threads a key =====================
@@ -808,6 +813,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_full);
     }
+#ifdef FA_WAIT_TEST
+    if (ok && wait_test(kWaitSoftmax, p.H)) ok = warp_wait(drain, 0, abort_flag, p.status);
+#endif
     if (ok && n > 0)
       ok = __all_sync(0xffffffffu, mbar_wait(kd_done, (n - 1) & 1, abort_flag, p.status));
     if (ok) {
@@ -840,6 +848,17 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag) {   // as in the dQ kernel
+    if (threadIdx.x == 0) {
+      drain_wait(kv_full, 0, p.status);
+      for (int j = max(0, *issued - NS); j < *issued; ++j) drain_wait(full(j % NS), (j / NS) & 1, p.status);
+    }
+    if (warp == 1) {
+      elected([&] { tc_commit(drain); });
+      drain_wait(drain, 0, p.status);
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

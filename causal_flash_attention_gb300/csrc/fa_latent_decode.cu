@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
   }
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
+  volatile int* issued = abort_flag + 1;   // tiles that the producer has asked for, and segments' queries
   float* row_f = reinterpret_cast<float*>(smem + Cfg::kOffRow);
   float* row_lse = row_f + 64;
   float* halves = row_f + 128;   // [2][64]
@@ -207,7 +208,10 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       };
       bool have = seg.next(p), ok = true;
       int pb = have ? page() : -1;
-      while (have) {
+#ifdef FA_WAIT_TEST
+      if (wait_test(kWaitProducer, p.H)) ok = mbar_wait(drain, 0, abort_flag, p.status);
+#endif
+      while (ok && have) {
         const bool in_range = pb >= 0 && pb < p.num_blocks;
         const int y = in_range ? ((seg.tile0 + j) * kTile + lane * p.box_rows) & (p.block_size - 1) : p.block_size;
         const int z = in_range ? pb : 0;
@@ -242,15 +246,12 @@ __global__ void __launch_bounds__(kThreadsD, 1)
           for (int cc = 0; cc < Cfg::kChunks; ++cc) tma_prefetch_l2_3d(&p.tm, cc * kChunk, yn, pb);
         }
       }
-      // Aborted: every copy lands before the CTA releases its memory. (A tile given up half-way is
-      // arrived for, and so is one that another lane went on to, so that the phases complete.)
-      const uint32_t lanes = (1u << (kTile / p.box_rows)) - 1;
-      if (__any_sync(lanes, *abort_flag)) {
-        if (!ok) mbar_arrive(full(n_t++ % NT));
-        const int most = __reduce_max_sync(lanes, n_t);
-        for (; n_t < most; ++n_t) mbar_arrive(full(n_t % NT));
-        for (int i = max(0, most - NT); i < most; ++i) drain_wait(full(i % NT), (i / NT) & 1, p.status);
-      }
+      // A tile given up half-way is arrived for, and so is one that another lane went on to, so that
+      // the phases complete.
+      if (!ok) mbar_arrive(full(n_t++ % NT));
+      const int most = __reduce_max_sync((1u << (kTile / p.box_rows)) - 1, n_t);
+      for (; n_t < most; ++n_t) mbar_arrive(full(n_t % NT));
+      issued[0] = most;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 #ifdef FA_WAIT_TEST
     // wait-limit test build: nothing completes this phase before the abort
     // path's own commit, so the wait runs out
-    if (have) ok = warp_wait(drain, 0, abort_flag, p.status);
+    if (have && wait_test(kWaitIssuer, p.H)) ok = warp_wait(drain, 0, abort_flag, p.status);
 #endif
     auto issue_o = [&]() {   // O^T (+)= C_go^T P
       tc_fence_after();
@@ -351,12 +352,6 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       have = next();
     }
     while (ok && go < gs) ok = until(0, 0);
-    if (!ok) {
-      // every MMA issued so far must finish before the TMEM is released
-      elected([&] { tc_commit(drain); });
-      drain_wait(drain, 0, p.status);
-    }
-    __syncwarp();
   } else {
     // ===== queries, softmax per tile, O^T =====
     const int quarter = warp & 3;               // TMEM lane quarter of this warp
@@ -384,7 +379,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 
     bool more = seg.next(p);
     if (more) load_q(seg.b);
-    int n_q = 1;        // segments whose queries have been asked for
+    int n_q = more ? 1 : 0;   // segments whose queries have been asked for
     // A wait that fails in one warp must not leave the others in a barrier: the warp goes on
     // without touching anything until the next vote, where all learn of it.
     bool ok = true, dead = false;
@@ -534,6 +529,9 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       // The last tile's product has every warp's P, and a warp gives its P after it has read the halves'
       // maxima: past this wait they may be overwritten, in a segment of one tile too, which has no vote
       // in between.
+#ifdef FA_WAIT_TEST
+      if (wait_test(kWaitSoftmax, p.H)) wait(drain, 0);
+#endif
       wait(pv_done, g - 1);
       if (real) halves[half * 64 + r] = l;
       if ((dead = any(!ok))) break;
@@ -580,12 +578,24 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       any(false);   // the factors have been read
       head = false;
     }
-    // the last queries asked for land before the CTA releases its memory
-    if (tid == 0 && *abort_flag && share.begin < share.end) drain_wait(q_ready, (n_q - 1) & 1, p.status);
+    if (tid == 0) issued[1] = n_q;
   }
 
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag) {
+    // A wait ran out, whosever: only now is it known that nothing more is issued. Every copy lands and every
+    // MMA finishes before the CTA releases its memory.
+    if (threadIdx.x == 0) {
+      for (int i = max(0, issued[0] - NT); i < issued[0]; ++i) drain_wait(full(i % NT), (i / NT) & 1, p.status);
+      if (issued[1] > 0) drain_wait(q_ready, (issued[1] - 1) & 1, p.status);
+    }
+    if (warp == 1) {
+      elected([&] { tc_commit(drain); });
+      drain_wait(drain, 0, p.status);
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
   }
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
+  volatile int* issued = abort_flag + 1;   // K and V tiles that the producer has asked for
   int2* ranges = reinterpret_cast<int2*>(smem + Cfg::kOffSpan);
 
   const uint32_t q_full = sbase + Cfg::kOffBar;
@@ -178,10 +179,13 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
       // be a second arrival of a phase that expects one. (The slots alone do not see to that where
       // the last tiles' V follow one another.)
       int slot = 0, used = 0, held = 0, oldest = 0, jk = 0, jv = 0;   // jk, jv: K and V tiles issued
-      for (int u = 0; u < n_units; ++u) {
+      bool ok = true;
+#ifdef FA_WAIT_TEST
+      if (wait_test(kWaitProducer, p.H)) ok = mbar_wait(drain, 0, abort_flag, p.status);
+#endif
+      for (int u = 0; ok && u < n_units; ++u) {
         const int j = tile_of(u), n = is_k(u) ? KC : VC;
         if (j >= n_load) continue;
-        bool ok = true;
         for (; used + n > NS || held == 3; ++oldest, --held) {
           const int o = tile_of(oldest);
           if (!(ok = mbar_wait(is_k(oldest) ? k_empty(o & 1) : v_empty(o & 1), (o >> 1) & 1, abort_flag, p.status))) break;
@@ -213,12 +217,8 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
         if (is_k(u)) ++jk;
         else ++jv;
       }
-      if (*abort_flag) {
-        // let every copy already issued land before the CTA releases its memory
-        drain_wait(q_full, 0, p.status);
-        for (int j = max(0, jk - 2); j < jk; ++j) drain_wait(k_full(j & 1), (j >> 1) & 1, p.status);
-        for (int j = max(0, jv - 2); j < jv; ++j) drain_wait(v_full(j & 1), (j >> 1) & 1, p.status);
-      }
+      issued[0] = jk;
+      issued[1] = jv;
     }
   } else if (warp == 1) {
     // ===================== MMA issuer (the whole warp, one lane of it the MMAs) =====================
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
 #ifdef FA_WAIT_TEST
       // wait-limit test build: nothing completes this phase before the abort
       // path's own commit, so the wait runs out
-      if (ok) ok = wait(drain, 0);
+      if (ok && wait_test(kWaitIssuer, p.H)) ok = wait(drain, 0);
 #endif
       auto active = [&](int t, int j) { return j >= first[t] && j < last[t]; };
       // the ring's slots of the K tile and the V tile in turn
@@ -342,12 +342,6 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
           if (j + 2 < n_load) commit(k_empty((j + 1) & 1));
         }
       }
-      if (!ok) {
-        // every MMA issued so far must finish before the TMEM is released
-        elected([&] { tc_commit(drain); });
-        drain_wait(drain, 0, p.status);
-      }
-      __syncwarp();
     }
   } else {
     // ===================== softmax / correction / epilogue =====================
@@ -458,6 +452,9 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
       if (lane == 0) mbar_arrive(p_full(t));
     }
 
+#ifdef FA_WAIT_TEST
+    if (ok && wait_test(kWaitSoftmax, p.H)) ok = warp_wait(drain, 0, abort_flag, p.status);
+#endif
     if (ok && n > 0)
       ok = __all_sync(0xffffffffu, mbar_wait(pv_done(t), (n - 1) & 1, abort_flag, p.status));
     // (results leave through the query tile's own memory)
@@ -491,6 +488,20 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
 
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag) {
+    // A wait ran out, whosever: only now is it known that nothing more is issued. Every copy lands and every
+    // MMA finishes before the CTA releases its memory.
+    if (threadIdx.x == 0) {
+      drain_wait(q_full, 0, p.status);
+      for (int j = max(0, issued[0] - 2); j < issued[0]; ++j) drain_wait(k_full(j & 1), (j >> 1) & 1, p.status);
+      for (int j = max(0, issued[1] - 2); j < issued[1]; ++j) drain_wait(v_full(j & 1), (j >> 1) & 1, p.status);
+    }
+    if (warp == 1) {
+      elected([&] { tc_commit(drain); });
+      drain_wait(drain, 0, p.status);
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::kTmemCols);

@@ -26,7 +26,8 @@ enum : int {
 // the library (FA_WAIT_TEST) shortens the first bound only and makes each
 // kernel's MMA issuer start by waiting for a barrier phase that nothing
 // completes, so that its bounded wait runs out and the kernel takes the
-// abort path and reports kStatusWaitTimeout.
+// abort path and reports kStatusWaitTimeout (in the latent kernels the role
+// that wait_test names).
 #ifdef FA_WAIT_LIMIT_CYCLES
 constexpr long long kWaitLimitCycles = FA_WAIT_LIMIT_CYCLES;
 #else
@@ -164,6 +165,12 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, int* s
     }
   }
 }
+
+#ifdef FA_WAIT_TEST
+// Wait-limit test build of the latent kernels: the role whose wait runs out goes by the number of heads.
+enum WaitTest { kWaitProducer = 0, kWaitIssuer = 1, kWaitSoftmax = 2 };
+__device__ __forceinline__ bool wait_test(WaitTest role, int heads) { return heads % 3 == role; }
+#endif
 
 // ------------------------------------------------------------------- TMA --
 __device__ __forceinline__ void tma_prefetch_desc(const void* tmap) {

@@ -314,6 +314,37 @@ def test_wait_that_runs_out(fa, monkeypatch, d, rank, heads):
     assert fa.fa_last_device_status() == 0
 
 
+@pytest.mark.parametrize("role,heads", [("producer", 3), ("issuer", 4), ("softmax", 5), ("softmax", 20)])
+@pytest.mark.parametrize("n,d,rank", [(60, 64, 512), (60, 128, 256), (1000, 64, 256), (1000, 128, 512)])
+def test_wait_that_runs_out_in_any_role(fa, monkeypatch, role, heads, n, d, rank):
+    """The role that gives up goes by the heads in that build. With few tiles the others have issued
+    all their copies and products by then, and are done before it is known."""
+    g = torch.Generator().manual_seed(n + heads)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(DEV)
+    x = (r(2, heads, n, d + 64), r(2, heads, n, d), r(2, n, 64), r(2, heads, n, d))
+    do, q, cache = r(2, heads, n, d), r(3, heads, 2, rank + 64), r(3 * 64, BS, rank + 64)
+    table = torch.randperm(3 * 64, generator=g).to(torch.int32).view(3, 64).to(DEV)
+    lens = torch.tensor([n, 40, n // 2], dtype=torch.int32, device=DEV)
+    out, lse = fa.attention_latent_forward(*x)
+    calls = dict(forward=lambda: fa.attention_latent_forward(*x),
+                 backward=lambda: fa.attention_latent_backward(*x, out, do, lse),
+                 paged=lambda: fa.decode_latent_paged(q, cache, table, lens, 0.1))
+    want = {name: [t.clone() for t in c()] for name, c in calls.items()}
+    torch.cuda.synchronize()
+    with monkeypatch.context() as mp:
+        mp.setattr(fa, "LIB_PATH", fa_build.build(variant="waittest"))
+        mp.setattr(fa, "_lib", None)
+        for name, call in calls.items():
+            for _ in range(3):
+                call()
+            torch.cuda.synchronize()
+            assert fa.fa_last_device_status() == 1, name
+            assert fa.fa_last_device_status() == 0, name
+    for name, call in calls.items():
+        assert same(call(), want[name]), name
+    assert fa.fa_last_device_status() == 0
+
+
 def test_tensors_that_do_not_fit(fa):
     z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device=DEV)
     i32 = z(2, 8, dt=torch.int32)
