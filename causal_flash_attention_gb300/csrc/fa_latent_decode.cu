@@ -440,7 +440,8 @@ __global__ void __launch_bounds__(kThreadsD, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < kHalf; ++i) x[i] = __uint_as_float(raw[i]);
-          if (__any_sync(0xffffffffu, k0 < row_lo || k0 + kHalf > row_hi) ||
+          // (lanes without a row have no say, and their scores no reader)
+          if (__any_sync(0xffffffffu, real && (k0 < row_lo || k0 + kHalf > row_hi)) ||
               (p.tree && k0 + kHalf > keys.len - p.Sq)) {
             uint32_t see = span_bits(row_lo, row_hi, k0);
             if (p.tree) see &= static_cast<uint32_t>(tree_bits(tree, keys.len - p.Sq, k0));
