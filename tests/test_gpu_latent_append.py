@@ -89,6 +89,49 @@ def test_append(fa, lens, H, Sq, rank, dtype, bs, norm, interleaved):
     compare(got, x, f, interleaved, scale)
 
 
+MANY = [
+    # from 608 tokens on a block takes four of them: here 1, 2, 3 or none over, of two sequences or with one
+    # token of each, heads in one unit, in several, and past a multiple of eight
+    (3, 205, 7, 512, "fp16", 16, True, True),        # 615: 3 over
+    (2, 305, 16, 256, "bf16", 64, False, False),     # 610: 2 over
+    (7, 87, 1, 512, "fp32", 32, True, False),        # 609: 1 over
+    (4, 152, 8, 256, "fp32", 16, False, True),       # 608, none
+    (611, 1, 9, 256, "fp16", 16, True, False),       # sequences of one token
+    (1, 1025, 40, 512, "bf16", 256, True, True),
+]
+
+
+@pytest.mark.parametrize("B,Sq,H,rank,dtype,bs,norm,interleaved", MANY)
+def test_append_of_many_tokens(fa, B, Sq, H, rank, dtype, bs, norm, interleaved):
+    """Some of them not stored: before their sequence's start, past the table, in pages outside."""
+    lens = [Sq + (37 * b) % 23 for b in range(B)]
+    lens[B // 2] = Sq - min(Sq, 3)
+    x = make(lens, H, Sq, rank, dtype, bs, norm, B + Sq)
+    x["seq_lens"][-1] += bs
+    x["block_table"][0, 0] = x["cache"].shape[0]
+    f, scale = fa.rope_inv_freq(64, scaling="parts", factor=4.0)
+    compare(run(fa, x, fa.rope_turns(f), interleaved=interleaved, rope_scale=scale), x, f, interleaved, scale)
+    g = torch.Generator().manual_seed(B)
+    pos = torch.randint(-2 ** 31, 2 ** 31, (B, Sq), generator=g).to(torch.int32)
+    compare(run(fa, x, fa.rope_turns(f), interleaved=interleaved, positions=pos), x, f, interleaved, positions=pos)
+
+
+@pytest.mark.parametrize("dtype,rank", [("fp32", 256), ("fp16", 512), ("bf16", 512)])
+def test_many_tokens_at_once_or_a_few_at_a_time(fa, dtype, rank):
+    """The same bits, whichever form a call takes."""
+    B, Sq, H = 3, 250, 11
+    x = make([Sq + 5, Sq, Sq + 40], H, Sq, rank, dtype, 16, True, 5)
+    f, _ = fa.rope_inv_freq(64)
+    want = run(fa, x, fa.rope_turns(f))
+    d = {n: t.to(DEV) for n, t in x.items()}
+    turns, parts = fa.rope_turns(f).to(DEV), []
+    for a, b in ((0, 1), (1, 100), (100, 249), (249, 250)):
+        part = {n: d[n][:, a:b] for n in ("latent", "k_rope")}
+        parts.append(fa.latent_append(**part, q_rope=d["q_rope"][:, :, a:b], cache=d["cache"], turns=turns,
+                                      block_table=d["block_table"], seq_lens=d["seq_lens"] - (Sq - b), weight=d["weight"]))
+    assert torch.equal(torch.cat(parts, 2), want["q_out"]) and torch.equal(d["cache"], want["cache"])
+
+
 def test_positions(fa):
     """Drafted tokens stand at their depth, wherever their rows are; far and negative positions."""
     x = make([20, 1000], 4, 8, 512, "bf16", 16)
