@@ -118,6 +118,21 @@ def test_expanded(fa, B, H, Sq, Skv, d, dtype, mask):
     compare(run(fa, x, spans), x, spans)
 
 
+@pytest.mark.parametrize("B,H,Sq,Skv,d,dtype,mask", [
+    (2, 40, 600, 600, 128, "bf16", None),         # 400 CTAs of the backward kernels
+    (2, 40, 600, 600, 128, "fp16", "gaps"),
+    (4, 24, 500, 500, 64, "bf16", "padded"),
+    (3, 30, 500, 500, 64, "fp16", "documents"),
+    (9, 20, 130, 400, 64, "bf16", None),
+    (200, 2, 70, 70, 128, "bf16", "all"),
+])
+def test_several_waves_of_ctas(fa, B, H, Sq, Skv, d, dtype, mask):
+    """An SM takes one CTA after another: barriers, tensor memory and shared memory are set up anew."""
+    x = make(B, H, Sq, Skv, d, dtype, seed=B + H)
+    spans = spans_of(fa, mask, B, Sq, Skv, B)
+    compare(run(fa, x, spans), x, spans)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_large_scores(fa, d):
     """Scores of tens: the reference maximum moves from tile to tile."""
