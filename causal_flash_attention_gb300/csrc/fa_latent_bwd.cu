@@ -5,10 +5,11 @@
 //   dQ_i = scale sum_j ds_ij K'_j, [dK_j, dKR_j of the head] = scale sum_i ds_ij Q_i,
 //   dV_j = sum_i p_ij dO_i, dKR_j = sum over the heads.
 //
-// Two kernels, each of which recomputes S and dP, instead of one that keeps everything: dK'
-// (192 columns at d = 128) and dV leave no room in tensor memory for a dQ of 192 columns
+// Two kernels, each of which recomputes S and dP, instead of one that keeps everything: at
+// d = 128 dK' (192 columns) and dV leave no room in tensor memory for a dQ of 192 columns
 // beside S and dP, and a dQ kernel of its own needs no sum over key tiles in global
-// memory (so gradients have the same bits on every call). Two products more of seven.
+// memory (so gradients have the same bits on every call). Two products more of seven. d = 64 (128 and 64
+// columns) takes the same two kernels and their layouts; forms of its own were not tried.
 //   1. dQ:      a CTA per 128 query rows walks their key tiles; it also forms D and leaves
 //               it with L and the rows' key ranges for the second.
 //   2. dK, dV:  a CTA per 128 keys of a head walks the query rows, 64 at a time.
@@ -20,19 +21,21 @@
 // times an output's own rounding), with short rows and |dO| |V| = 3e5 past its largest value. |dS_ij| is at most
 // 2 |dO_i| max_j |V_j| (the norm of O_i is no greater than V's), so one more kernel in front takes the
 // norms of V's rows, 128 keys a block; dQ scales each row by its own bound, dK and dV all rows by the greatest
-// of the query tiles that see one of their keys. P, at most 1, is scaled by 2^kShiftP for dV.
+// of the query tiles that see one of their keys. P, at most 1, is scaled by 2^kShiftP for dV. Packed documents of 2999 tokens, 2 x 16 heads: the norms 6 us,
+// dQ 53.6 -> 55.5, dK and dV 66.7 -> 68.
 // Warp roles of 1 and 2: warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 softmax
 // gradient, two warps a tensor-memory lane quarter with half the columns each (four with 16 columns
 // each: 1 and 2% slower), in 1 also warp 10 MMA issuer of dQ. P and dS
 // go back to tensor memory as the A operands of the products, so shared memory holds
 // only what TMA loads.
 //
-// 4096 tokens, 32 heads, d = 128, bf16, causal: dQ 188 us, 1463 TFLOP/s of products executed (76%
-// of a large product's rate), dK and dV 252 us, 1364 (71%), dKR 7.5. dQ is bound by a tile's chain
-// through the softmax warps (1340 cycles, 1024 of products) and by the filling of a CTA (112 KB, a
-// tenth of it); dK and dV by shared memory, from which products 64 rows
-// wide take both operands (1600 cycles a step instead of 1280, 1950 in all): there is no tensor
-// memory left for K' and V beside S^T, dP^T, P^T, dS^T and the sums.
+// 4096 tokens, 32 heads, d = 128, bf16, causal: dQ 183 us, 1502 TFLOP/s of products executed (78%
+// of a large product's rate), dK and dV 253 us, 1358 (71%), dKR 7.6; d = 64: 138, 194 and 6.9. dQ is bound
+// by a tile's chain through the softmax warps (1340 cycles, 1024 of products) and by the filling of a CTA (112
+// KB, a tenth of it); dK and dV by shared memory, from which products 64 rows
+// wide take both operands (1600 cycles a step instead of 1280, 1950 in all): at d = 128 these columns leave no
+// tensor memory for K' and V beside S^T, dP^T, P^T, dS^T and the sums. (With dS^T over dP^T and P^T over S^T V would
+// have room, at the cost of the overlap between steps; at d = 64 128 columns are free. Neither was tried.)
 #include <algorithm>
 #include <type_traits>
 
@@ -175,7 +178,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(warp_id()), 0);
   const int lane = static_cast<int>(lane_id());
   const int BH = p.B * p.H;
-  const int unit = p.n_units - 1 - static_cast<int>(blockIdx.x) / BH;   // heaviest first
+  const int unit = p.n_units - 1 - static_cast<int>(blockIdx.x) / BH;   // last rows first, as in the forward
   const int bh = static_cast<int>(blockIdx.x) % BH;
   const int b = bh / p.H, h = bh % p.H;
   const int q0 = unit * kTileM;

@@ -16,7 +16,8 @@
 // A tile is loaded once and serves both products:
 //   S = Q C^T    rows x 64 keys, M = 64: Q and the tile K-major in shared memory
 //   O^T += C^T P rank x rows, M = 128, rank / 128 products: the tile again, MN-major, and P,
-//                in the type of the cache, as the B operand
+//                in the type of the cache, as the B operand (the product takes no other beside it:
+//                half a step of P |C| in an output; sums, maxima and parts are in fp32)
 // O stands transposed in tensor memory because rows are the short side (rank / 128 * rows
 // columns: 256 at rank 512 with 64 rows; the other way around it would take all 512). The
 // tile goes through a ring of 16 KB pairs of 64-column chunks, each freed as soon as its
@@ -25,10 +26,11 @@
 //
 // Bound by a tile's way through the ring, which holds two tiles beside the queries of 64 rows:
 // landing, S (1325 cycles: M = 64 runs at half rate), softmax, O^T (900) and the next load. One new
-// token of 16 sequences of up to 8192 rows, rank 512: 128 heads 43.5 us with the merge (36.5 + 7), of
-// which a share of 14 tiles takes 25 and a part's 128 KB on their way out 2.4; 16 heads 27.5 (20.8 + 6.7),
+// token of 16 sequences of up to 8192 rows, rank 512: 128 heads 43.1 us with the merge (36 + 7), of
+// which a share of 14 tiles takes 25 and a part's 128 KB on their way out 2.4; 16 heads 27.7 (21 + 6.7),
 // 67 MB, of which the loop runs at 7 TB/s and the first tiles of all SMs take 3 us to land. (Writing the
-// results 32 columns of all parts at a time: 52 instead of 43.5, registers spilled.)
+// results 32 columns of all parts at a time: 52 instead of 43.5, registers spilled.) One long sequence is bound
+// by the merge, below.
 //
 // Warp roles (320 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 softmax (lanes
 // 0-15 of the two warps of a tensor-memory quarter w hold rows 16 w .. 16 w + 15, the M = 64
@@ -608,7 +610,8 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 // warp takes 128 elements of a row. Up to as many sequences as shares, block (b, y) takes
 // sequence b, found by a scan over the lengths as the main kernel's; more sequences than
 // shares, block (c, y) the one whose second part is in share c. Also writes out = 0, LSE =
-// -inf for sequences without keys. Bound by latency (10 KB a row from L2).
+// -inf for sequences without keys. Bound by latency (10 KB a row from L2), and by a row's walk along its
+// parts: one sequence of 8192 rows, 16 heads, leaves 128 of them, 31 of the call's 41 us; of 32768, 152, 41 of 57.
 constexpr int kMergeWarps = 4, kMergeFlight = 12;
 
 template <typename T, int RANK>

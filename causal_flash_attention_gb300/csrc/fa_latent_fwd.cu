@@ -7,6 +7,9 @@
 // under one key range per row. The shared part is loaded beside each head's keys, as a
 // third chunk of the key tile; it is never copied out to the heads in memory.
 //
+// P is rounded to the type of V, whose product takes it as an operand (an output is off by at most half a
+// step of P |V| more); sums and maxima are in fp32.
+//
 // As the forward in fa_fwd.cu: T query tiles of 128 rows per CTA, TMA producer (warp 0),
 // MMA issuer (warp 1), four softmax warps a tile with a thread a row, online softmax with
 // a lazily moved reference maximum, P over S's columns (T = 2) or beside them (T = 1). Two
@@ -16,8 +19,8 @@
 // Bound by a step's chain: 2560 cycles of products for two query tiles of 128 rows by 128 keys,
 // 3900 in all, the rest the handing over between products and softmax and the wait for K (the
 // ring holds less than two tiles beside 96 KB of queries). 4096 tokens, 32 heads, d = 128, bf16,
-// causal: 125 us, 1374 TFLOP/s, 72% of a large product's rate; a chunk of 1024 over 8192 keys, 128
-// CTAs on 152 SMs: 119 us, 1349. Tried and slower at the latter: two issuing warps (151 instead of
+// causal: 126 us, 1364 TFLOP/s, 71% of a large product's rate (d = 64: 84.5, 1220); a chunk of 1024 over 8192
+// keys, 128 CTAs on 152 SMs: 122 us, 1320. Tried and slower at the latter: two issuing warps (151 instead of
 // 134 then), both P V before both S (140), a barrier a chunk of K (128 instead of 122).
 #include <type_traits>
 
@@ -81,7 +84,8 @@ __global__ void __launch_bounds__(LatFwdCfg<D>::kThreads, LatFwdCfg<D>::kCtasPer
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(warp_id()), 0);
   const int lane = static_cast<int>(lane_id());
-  // heaviest tiles first, as under the causal mask
+  // last rows first: the heaviest under the causal mask. (Under other masks the order says nothing about
+  // what a tile costs: padded rows come first, and documents in any order.)
   const int BH = p.B * p.H;
   const int unit = p.n_units - 1 - static_cast<int>(blockIdx.x) / BH;
   const int bh = static_cast<int>(blockIdx.x) % BH;

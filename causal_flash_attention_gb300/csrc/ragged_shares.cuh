@@ -36,7 +36,10 @@ __device__ __forceinline__ SeqKeys seq_keys(const P& p, int b) {
 // costs beside its tiles. Measured at 32 + 8 heads, d = 128, 66137 keys in 16
 // sequences of 8 to 8192 and (second) 65521 + 15 x 1 keys: with no such units one
 // CTA got dozens of one-tile segments, 70.1 and 119 us; 1 unit 60.5 and 69.1; 2
-// units 52.5 and 54.2; 3 units 53.1 and 54.1.
+// units 52.5 and 54.2; 3 units 53.1 and 54.1. The latent decode (64-key tiles, a part of up to 128
+// KB), with 1, 2, 3 and 5 units: 16 sequences of up to 8192 rows, 128 heads 45.0, 43.0, 43.3, 43.3 us, 16 heads
+// 26.9, 27.3, 27.3, 27.2; trees over 3 x 20000 rows 40.2, 37.9, 37.8, 38.2; 60 windows of 512 rows 13.5, 12.9, 13.5,
+// 13.8; 120 sequences of up to 300 rows 17.9, 18.3, 18.9, 19.0; one of 500 rows 9.7, 10.7, 10.7, 10.7.
 constexpr int kSegmentUnits = 2;
 __device__ __forceinline__ int units_of(int tiles) { return tiles > 0 ? tiles + kSegmentUnits : 0; }
 
