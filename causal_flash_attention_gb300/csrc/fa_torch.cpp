@@ -53,12 +53,17 @@ struct Library {
   decltype(&fa_qk_norm_rope_bwd) norm_rope_bwd;
   decltype(&fa_qk_norm_rope_bwd_workspace_bytes) norm_rope_bwd_bytes;
   decltype(&fa_qk_norm_rope_append) append;
-  decltype(&fa_fwd_latent) latent_fwd;
-  decltype(&fa_bwd_latent) latent_bwd;
-  decltype(&fa_bwd_latent_workspace_bytes) latent_bwd_bytes;
-  decltype(&fa_fwd_latent_paged) latent_paged;
-  decltype(&fa_fwd_latent_paged_workspace_bytes) latent_paged_bytes;
-  decltype(&fa_latent_append) latent_append;
+};
+
+// Those of latent attention, found by themselves: a library that has only the ones above serves these.
+struct LatentLibrary {
+  void* handle = nullptr;
+  decltype(&fa_fwd_latent) fwd;
+  decltype(&fa_bwd_latent) bwd;
+  decltype(&fa_bwd_latent_workspace_bytes) bwd_bytes;
+  decltype(&fa_fwd_latent_paged) paged;
+  decltype(&fa_fwd_latent_paged_workspace_bytes) paged_bytes;
+  decltype(&fa_latent_append) append;
 };
 
 template <typename F>
@@ -82,12 +87,23 @@ const Library& library(PyObject* o) {
   find(handle, "fa_qk_norm_rope_bwd", l.norm_rope_bwd);
   find(handle, "fa_qk_norm_rope_bwd_workspace_bytes", l.norm_rope_bwd_bytes);
   find(handle, "fa_qk_norm_rope_append", l.append);
-  find(handle, "fa_fwd_latent", l.latent_fwd);
-  find(handle, "fa_bwd_latent", l.latent_bwd);
-  find(handle, "fa_bwd_latent_workspace_bytes", l.latent_bwd_bytes);
-  find(handle, "fa_fwd_latent_paged", l.latent_paged);
-  find(handle, "fa_fwd_latent_paged_workspace_bytes", l.latent_paged_bytes);
-  find(handle, "fa_latent_append", l.latent_append);
+  l.handle = handle;
+  lib = l;
+  return lib;
+}
+
+const LatentLibrary& latent_library(PyObject* o) {
+  static LatentLibrary lib;   // guarded by the interpreter lock
+  void* handle = PyLong_AsVoidPtr(o);
+  if (handle == lib.handle && handle) return lib;
+  if (!handle) throw BadArgument{"no library handle"};
+  LatentLibrary l;
+  find(handle, "fa_fwd_latent", l.fwd);
+  find(handle, "fa_bwd_latent", l.bwd);
+  find(handle, "fa_bwd_latent_workspace_bytes", l.bwd_bytes);
+  find(handle, "fa_fwd_latent_paged", l.paged);
+  find(handle, "fa_fwd_latent_paged_workspace_bytes", l.paged_bytes);
+  find(handle, "fa_latent_append", l.append);
   l.handle = handle;
   lib = l;
   return lib;
@@ -620,7 +636,7 @@ LatentInputs latent_inputs(const Tensor& q, const Tensor& k, const Tensor& kr, c
 
 // (handle, q, k, k_rope, v, key_begin, key_end, out, lse, scale, stream)
 PyObject* latent_forward(PyObject* const* a) {
-  const Library lib = library(a[0]);
+  const LatentLibrary lib = latent_library(a[0]);
   const Tensor &q = tensor(a[1], "q"), &k = tensor(a[2], "k"), &kr = tensor(a[3], "k_rope"), &v = tensor(a[4], "v");
   const Tensor begin = maybe(a[5], "key_begin"), end = maybe(a[6], "key_end");
   Tensor out = maybe(a[7], "out"), lse = maybe(a[8], "lse");
@@ -632,7 +648,7 @@ PyObject* latent_forward(PyObject* const* a) {
   const fa_view vo = view("out", out, n.dev, n.dt, {n.B, n.H, n.Sq, n.d}, true);
   if (lse.defined()) fit("lse", lse, n.dev, at::kFloat, {n.B, n.H, n.Sq});
   else lse = empty({n.B, n.H, n.Sq}, n.dev, at::kFloat);
-  const int rc = lib.latent_fwd(&n.q, &n.k, &n.kr, &n.v, data<int>(begin), data<int>(end), &vo, data<float>(lse), n.B,
+  const int rc = lib.fwd(&n.q, &n.k, &n.kr, &n.v, data<int>(begin), data<int>(end), &vo, data<float>(lse), n.B,
                                 n.H, n.Sq, n.Skv, n.d, scale, dtype_code(q), at.stream);
   released.end();
   return rc ? PyLong_FromLong(rc) : tensors({out, lse});
@@ -641,7 +657,7 @@ PyObject* latent_forward(PyObject* const* a) {
 // (handle, q, k, k_rope, v, key_begin, key_end, out, dout, lse, dq, dk, dk_rope, dv, workspace,
 //  scale, stream)
 PyObject* latent_backward(PyObject* const* a) {
-  const Library lib = library(a[0]);
+  const LatentLibrary lib = latent_library(a[0]);
   const Tensor &q = tensor(a[1], "q"), &k = tensor(a[2], "k"), &kr = tensor(a[3], "k_rope"), &v = tensor(a[4], "v");
   const Tensor begin = maybe(a[5], "key_begin"), end = maybe(a[6], "key_end");
   const Tensor &out = tensor(a[7], "out"), &dout = tensor(a[8], "dout"), &lse = tensor(a[9], "lse");
@@ -658,11 +674,11 @@ PyObject* latent_backward(PyObject* const* a) {
   if (!dk.defined()) dk = empty_tokens_first(n.B, n.H, n.Skv, n.d, n.dev, n.dt);
   if (!dkr.defined()) dkr = empty({n.B, n.Skv, kRope}, n.dev, n.dt);
   if (!dv.defined()) dv = empty_tokens_first(n.B, n.H, n.Skv, n.d, n.dev, n.dt);
-  if (!ws.defined()) ws = workspace_of(lib.latent_bwd_bytes(n.B, n.H, n.Sq, n.Skv, n.d), n.dev);
+  if (!ws.defined()) ws = workspace_of(lib.bwd_bytes(n.B, n.H, n.Sq, n.Skv, n.d), n.dev);
   const fa_view vdq = view("dq", dq, n.dev, n.dt, {n.B, n.H, n.Sq, n.d + kRope}, true);
   const fa_view vdk = view("dk", dk, n.dev, n.dt, ks, true), vdv = view("dv", dv, n.dev, n.dt, ks, true);
   const fa_view vdkr = flat_view("dk_rope", dkr, n.dev, n.dt, n.B, n.Skv, kRope, true);
-  const int rc = lib.latent_bwd(&n.q, &n.k, &n.kr, &n.v, data<int>(begin), data<int>(end), &vo, &vg, data<float>(lse),
+  const int rc = lib.bwd(&n.q, &n.k, &n.kr, &n.v, data<int>(begin), data<int>(end), &vo, &vg, data<float>(lse),
                                 &vdq, &vdk, &vdkr, &vdv, n.B, n.H, n.Sq, n.Skv, n.d, scale, dtype_code(q),
                                 ws.data_ptr(), workspace_bytes(ws, n.dev), at.stream);
   released.end();
@@ -683,7 +699,7 @@ int latent_cache(CacheDims& c, at::Device dev, at::ScalarType dt, int64_t B, con
 
 // (handle, q, cache, block_table, seq_lens, tree_masks, out, lse, workspace, window, scale, stream)
 PyObject* latent_paged(PyObject* const* a) {
-  const Library lib = library(a[0]);
+  const LatentLibrary lib = latent_library(a[0]);
   const Tensor &q = tensor(a[1], "q"), &cache = tensor(a[2], "cache");
   const Tensor &table = tensor(a[3], "block_table"), &lens = tensor(a[4], "seq_lens");
   const Tensor tree = maybe(a[5], "tree_masks");
@@ -704,8 +720,8 @@ PyObject* latent_paged(PyObject* const* a) {
   else out = empty({B, H, Sq, rank}, dev, dt);
   if (lse.defined()) fit("lse", lse, dev, at::kFloat, {B, H, Sq});
   else lse = empty({B, H, Sq}, dev, at::kFloat);
-  if (!ws.defined()) ws = workspace_of(lib.latent_paged_bytes(B, H, Sq, rank, c.block_size, c.max_blocks), dev);
-  const int rc = lib.latent_paged(&vq, cache.data_ptr(), data<int>(table), data<int>(lens), data<long long>(tree),
+  if (!ws.defined()) ws = workspace_of(lib.paged_bytes(B, H, Sq, rank, c.block_size, c.max_blocks), dev);
+  const int rc = lib.paged(&vq, cache.data_ptr(), data<int>(table), data<int>(lens), data<long long>(tree),
                                   out.data_ptr(), data<float>(lse), B, H, Sq, rank, c.block_size, c.num_blocks,
                                   c.max_blocks, window, scale, dtype_code(q), ws.data_ptr(),
                                   workspace_bytes(ws, dev), at.stream);
@@ -716,7 +732,7 @@ PyObject* latent_paged(PyObject* const* a) {
 // (handle, latent, k_rope, q_rope, q_out, cache, block_table, seq_lens, positions, weight, turns, eps,
 //  interleaved, rope_scale, stream)
 PyObject* latent_append(PyObject* const* a) {
-  const Library lib = library(a[0]);
+  const LatentLibrary lib = latent_library(a[0]);
   const Tensor &latent = tensor(a[1], "latent"), &kr = tensor(a[2], "k_rope"), &qr = tensor(a[3], "q_rope");
   Tensor qo = maybe(a[4], "q_out");
   const Tensor &cache = tensor(a[5], "cache"), &table = tensor(a[6], "block_table"), &lens = tensor(a[7], "seq_lens");
@@ -741,7 +757,7 @@ PyObject* latent_append(PyObject* const* a) {
   Released released;
   if (!qo.defined()) qo = empty({B, H, Sq, kRope}, dev, dt);
   const fa_view vqo = view("q_out", qo, dev, dt, qs, true);
-  const int rc = lib.latent_append(&vl, &vk, &vq, &vqo, cache.data_ptr(), data<int>(table), data<int>(lens),
+  const int rc = lib.append(&vl, &vk, &vq, &vqo, cache.data_ptr(), data<int>(table), data<int>(lens),
                                    data<int>(positions), data<void>(weight), eps, data<unsigned long long>(turns),
                                    interleaved, rope_scale, B, H, Sq, rank, c.block_size, c.num_blocks, c.max_blocks,
                                    dtype_code(latent), at.stream);
