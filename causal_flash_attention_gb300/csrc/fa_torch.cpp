@@ -55,7 +55,8 @@ struct Library {
   decltype(&fa_qk_norm_rope_append) append;
 };
 
-// Those of latent attention, found by themselves: a library that has only the ones above serves these.
+// Those of latent attention, found by themselves on their first use: the calls above also run on the handle of
+// a library that has only theirs, as the binding's own tests give them. (The package loads none without these.)
 struct LatentLibrary {
   void* handle = nullptr;
   decltype(&fa_fwd_latent) fwd;
