@@ -345,6 +345,66 @@ def test_wait_that_runs_out_in_any_role(fa, monkeypatch, role, heads, n, d, rank
     assert fa.fa_last_device_status() == 0
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp16_training_in_graphs_and_threads(fa, d):
+    """fp16's backward has a kernel more in front, and scratch where results come later."""
+    g = torch.Generator().manual_seed(d)
+    r = lambda *s: torch.randn(*s, generator=g).half().to(DEV)
+    sets = [(r(2, 5, 333, d + 64), r(2, 5, 400, d), r(2, 400, 64), r(2, 5, 400, d), r(2, 5, 333, d) * 2.0 ** -9)
+            for _ in range(2)]
+
+    def step(x):
+        out, lse = fa.attention_latent_forward(*x[:4])
+        return [out, lse, *fa.attention_latent_backward(*x[:4], out, x[4], lse)]
+
+    want = [step(x) for x in sets]
+    torch.cuda.synchronize()
+    graph, pad = torch.cuda.CUDAGraph(), torch.empty(1 << 20, device=DEV)
+    with torch.cuda.graph(graph):
+        first = step(sets[0])
+        pad.zero_()
+        second = step(sets[1])
+    wrong = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got = step(sets[i])
+                torch.cuda.current_stream().synchronize()
+                if not same(got, want[i]):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for _ in range(10):
+        graph.replay()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong and same(first, want[0]) and same(second, want[1])
+    assert fa.fa_last_device_status() == 0
+
+
+@pytest.mark.parametrize("heads", [3, 4, 5])
+@pytest.mark.parametrize("n,d", [(60, 128), (1000, 64)])
+def test_wait_that_runs_out_in_fp16(fa, monkeypatch, heads, n, d):
+    g = torch.Generator().manual_seed(n + heads)
+    r = lambda *s: torch.randn(*s, generator=g).half().to(DEV)
+    x, do = (r(2, heads, n, d + 64), r(2, heads, n, d), r(2, n, 64), r(2, heads, n, d)), r(2, heads, n, d)
+    out, lse = fa.attention_latent_forward(*x)
+    call = lambda: fa.attention_latent_backward(*x, out, do, lse)
+    want = call()
+    torch.cuda.synchronize()
+    with monkeypatch.context() as mp:
+        mp.setattr(fa, "LIB_PATH", fa_build.build(variant="waittest"))
+        mp.setattr(fa, "_lib", None)
+        call()
+        torch.cuda.synchronize()
+        assert fa.fa_last_device_status() == 1
+    assert same(call(), want) and fa.fa_last_device_status() == 0
+
+
 def test_tensors_that_do_not_fit(fa):
     z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device=DEV)
     i32 = z(2, 8, dt=torch.int32)
